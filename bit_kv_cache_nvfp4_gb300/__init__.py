@@ -28,13 +28,14 @@ __all__ = [
     "debug_gather_dequant_latent", "sparse_mla_decode_partial", "dcp_mask_topk",
     "merge_partials", "gather_partials", "dcp_sparse_mla_decode", "dcp_local_page_table",
     "dcp_local_slots", "dcp_local_pages", "dcp_compact_topk", "ROW_BYTES", "ROW_BYTES_LATENT", "LATENT", "ROPE", "QK_DIM", "PAGE", "DEV_BAD_SLOT", "DEV_BAD_PAGE",
-    "DEV_TIMEOUT", "HostPipe",
+    "DEV_TIMEOUT", "DEV_NONFINITE", "DEV_BAD_LENGTH", "HostPipe",
+    "append_gqa8", "read_gqa8", "attention_gqa8", "attention_gqa8_workspace",
 ]
 
 ROW_BYTES, LATENT, ROPE, QK_DIM, PAGE, TILE_KEYS = 352, 512, 64, 576, 64, 128
 ROW_BYTES_LATENT = 288
 ROW_BYTES_FP8 = 576
-DEV_BAD_SLOT, DEV_BAD_PAGE, DEV_TIMEOUT = 1, 2, 4
+DEV_BAD_SLOT, DEV_BAD_PAGE, DEV_TIMEOUT, DEV_NONFINITE, DEV_BAD_LENGTH = 1, 2, 4, 8, 16
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported shape or page size",
            3: "device is not compute capability 10.3", 4: "kernel launch failed",
            5: "workspace missing or too small",
@@ -127,6 +128,17 @@ def load_library():
         lib.kv4_host_pipe_step.restype = i32
         lib.kv4_host_pipe_destroy.argtypes = [P]
         lib.kv4_host_pipe_destroy.restype = i32
+        lib.kv4_append_gqa8.argtypes = [P, i64, i64, P, i64, i64, i32, i64, P, P, i64, i32, P, i32,
+                                        i32, i32, P, P, i64, P, P]
+        lib.kv4_append_gqa8.restype = i32
+        lib.kv4_read_gqa8.argtypes = [P, P, i64, P, i64, i32, P, P, i64, i32, i32, i32, i32, P, P,
+                                      P, P]
+        lib.kv4_read_gqa8.restype = i32
+        lib.kv4_attention_gqa8_plan.argtypes = [i32, i32, i64, i32, i32, i32, ctypes.POINTER(sz)]
+        lib.kv4_attention_gqa8_plan.restype = i32
+        lib.kv4_attention_gqa8.argtypes = [P, i64, i64, i32, i64, P, i32, P, P, i64, P, i64, i32,
+                                           P, i32, i32, i32, i32, i32, f32, P, P, P, sz, P, P]
+        lib.kv4_attention_gqa8.restype = i32
         lib.kv4_set_wait_limit.argtypes = [i64, i32]
         lib.kv4_set_wait_limit.restype = i32
         lib.kv4_set_timing_event.argtypes = [P]
@@ -702,3 +714,7 @@ def set_wait_limit(timeout_ns: int = 0, fault_site: int = 0) -> None:
     injected wait on a barrier nothing arrives on (fault_site=1)."""
     _check("kv4_set_wait_limit", load_library().kv4_set_wait_limit(int(timeout_ns),
                                                                    int(fault_site)))
+
+
+from .gqa8 import (append_gqa8, attention_gqa8, attention_gqa8_workspace,  # noqa: E402
+                   read_gqa8)

@@ -6,6 +6,7 @@
 #include "kv4_launch.h"
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstdlib>
 #include <new>
@@ -929,6 +930,199 @@ kv4_status kv4_sparse_mla_decode_noalloc(const void* q_dev, const uint8_t* pool_
 }
 
 size_t kv4_noalloc_scratch_bytes(void) { return kStaticScratchBytes; }
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The 8-bit grouped-query cache.
+// ---------------------------------------------------------------------------
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool aligned128(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 127u) == 0; }
+
+// Sizes that the three entry points share.  Beyond n_tokens * heads * D the
+// grids need one block index per page of the call, n_tokens / 64 + 2 B.
+kv4_status check_gqa8(int64_t n_tokens, int heads, int Hkv, int D, int B, int dtype,
+                      int page_size, int64_t num_pages, int64_t pt_stride) {
+  if (n_tokens < 0 || B < 0 || B > 65535 || Hkv < 1 || heads < 1) return KV4_ERR_INVALID_ARG;
+  if (page_size != KV4_PAGE || (D != 64 && D != 128) || (dtype != KV4_BF16 && dtype != KV4_F16) ||
+      Hkv > 65535)
+    return KV4_ERR_UNSUPPORTED;
+  if (n_tokens > INT32_MAX || n_tokens * heads > (1LL << 40) / D) return KV4_ERR_INVALID_ARG;
+  if (num_pages < 0 || num_pages >= INT32_MAX || pt_stride < 1 || pt_stride > INT32_MAX)
+    return KV4_ERR_INVALID_ARG;
+  if (num_pages > INT64_MAX / (2LL * KV4_PAGE * D) / Hkv) return KV4_ERR_INVALID_ARG;
+  return KV4_OK;
+}
+
+bool strides_ok(const void* p, int64_t token, int64_t head, int heads, int D) {
+  return aligned16(p) && token % 8 == 0 && head % 8 == 0 && token >= 0 && head >= 0 &&
+         (heads == 1 || head >= D);
+}
+
+}  // namespace
+
+extern "C" {
+
+kv4_status kv4_append_gqa8(const void* k_dev, int64_t k_token_stride, int64_t k_head_stride,
+                           const void* v_dev, int64_t v_token_stride, int64_t v_head_stride,
+                           int dtype, int64_t n_tokens, const int32_t* cu_seqlens_dev,
+                           const int32_t* page_table_dev, int64_t pt_stride, int page_size,
+                           const int32_t* seq_lens_dev, int B, int Hkv, int D, uint8_t* pool_dev,
+                           uint8_t* scales_dev, int64_t num_pages, int32_t* dev_err,
+                           kv4_stream_t stream) {
+  const kv4_status shape = check_gqa8(n_tokens, Hkv, Hkv, D, B, dtype, page_size, num_pages, pt_stride);
+  if (shape != KV4_OK) return shape;
+  if (n_tokens == 0 || B == 0) return KV4_OK;
+  if (!k_dev || !v_dev || !cu_seqlens_dev || !page_table_dev || !seq_lens_dev || !pool_dev ||
+      !scales_dev)
+    return KV4_ERR_INVALID_ARG;
+  if (!strides_ok(k_dev, k_token_stride, k_head_stride, Hkv, D) ||
+      !strides_ok(v_dev, v_token_stride, v_head_stride, Hkv, D) || !aligned128(pool_dev) ||
+      !aligned4(cu_seqlens_dev) || !aligned4(page_table_dev) || !aligned4(seq_lens_dev) ||
+      !aligned4(dev_err))
+    return KV4_ERR_INVALID_ARG;
+  int sms = 0;
+  const kv4_status st = device_info(&sms);
+  if (st != KV4_OK) return st;
+  kv4::Gqa8Args a{};
+  a.k = k_dev;
+  a.k_token_stride = k_token_stride;
+  a.k_head_stride = k_head_stride;
+  a.v = v_dev;
+  a.v_token_stride = v_token_stride;
+  a.v_head_stride = v_head_stride;
+  a.f16 = dtype == KV4_F16;
+  a.n_tokens = n_tokens;
+  a.cu = cu_seqlens_dev;
+  a.lens = seq_lens_dev;
+  a.page_table = page_table_dev;
+  a.pt_stride = pt_stride;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.pool = pool_dev;
+  a.scales = scales_dev;
+  a.num_pages = num_pages;
+  a.dev_err = dev_err;
+  return kv4::launch_append_gqa8(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KV4_OK
+             : KV4_ERR_LAUNCH;
+}
+
+kv4_status kv4_read_gqa8(const uint8_t* pool_dev, const uint8_t* scales_dev, int64_t num_pages,
+                         const int32_t* page_table_dev, int64_t pt_stride, int page_size,
+                         const int32_t* starts_dev, const int32_t* cu_seqlens_dev,
+                         int64_t n_tokens, int B, int Hkv, int D, int dtype, void* k_out_dev,
+                         void* v_out_dev, int32_t* dev_err, kv4_stream_t stream) {
+  const kv4_status shape = check_gqa8(n_tokens, Hkv, Hkv, D, B, dtype, page_size, num_pages, pt_stride);
+  if (shape != KV4_OK) return shape;
+  if (n_tokens == 0 || B == 0) return KV4_OK;
+  if (!pool_dev || !scales_dev || !page_table_dev || !starts_dev || !cu_seqlens_dev ||
+      !k_out_dev || !v_out_dev)
+    return KV4_ERR_INVALID_ARG;
+  if (!aligned128(pool_dev) || !aligned16(k_out_dev) || !aligned16(v_out_dev) ||
+      !aligned4(starts_dev) || !aligned4(cu_seqlens_dev) || !aligned4(page_table_dev) ||
+      !aligned4(dev_err))
+    return KV4_ERR_INVALID_ARG;
+  int sms = 0;
+  const kv4_status st = device_info(&sms);
+  if (st != KV4_OK) return st;
+  kv4::Gqa8Args a{};
+  a.k_out = k_out_dev;
+  a.v_out = v_out_dev;
+  a.f16 = dtype == KV4_F16;
+  a.n_tokens = n_tokens;
+  a.cu = cu_seqlens_dev;
+  a.starts = starts_dev;
+  a.page_table = page_table_dev;
+  a.pt_stride = pt_stride;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.pool = const_cast<uint8_t*>(pool_dev);
+  a.scales = const_cast<uint8_t*>(scales_dev);
+  a.num_pages = num_pages;
+  a.dev_err = dev_err;
+  return kv4::launch_read_gqa8(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KV4_OK
+             : KV4_ERR_LAUNCH;
+}
+
+kv4_status kv4_attention_gqa8_plan(int B, int max_new, int64_t n_tokens, int Hq, int Hkv, int D,
+                                   size_t* workspace_bytes) {
+  if (max_new < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0) return KV4_ERR_INVALID_ARG;
+  const kv4_status shape = check_gqa8(n_tokens, Hq, Hkv, D, B, KV4_BF16, KV4_PAGE, 0, 1);
+  if (shape != KV4_OK) return shape;
+  if (Hq / Hkv > 128) return KV4_ERR_UNSUPPORTED;
+  int sms = 0;
+  const kv4_status st = device_info(&sms);
+  if (st != KV4_OK) return st;
+  if (workspace_bytes)
+    *workspace_bytes = kv4::attention_gqa8_workspace(B, max_new, n_tokens, Hq, Hkv, D, sms);
+  return KV4_OK;
+}
+
+kv4_status kv4_attention_gqa8(const void* q_dev, int64_t q_token_stride, int64_t q_head_stride,
+                              int dtype, int64_t n_tokens, const int32_t* cu_seqlens_dev,
+                              int max_new, const uint8_t* pool_dev, const uint8_t* scales_dev,
+                              int64_t num_pages, const int32_t* page_table_dev,
+                              int64_t pt_stride, int page_size, const int32_t* seq_lens_dev,
+                              int B, int Hq, int Hkv, int D, int window, float sm_scale,
+                              void* out_dev, float* lse_dev, void* workspace_dev,
+                              size_t workspace_bytes, int32_t* dev_err, kv4_stream_t stream) {
+  if (max_new < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || window < 0 || !std::isfinite(sm_scale))
+    return KV4_ERR_INVALID_ARG;
+  const kv4_status shape = check_gqa8(n_tokens, Hq, Hkv, D, B, dtype, page_size, num_pages, pt_stride);
+  if (shape != KV4_OK) return shape;
+  if (Hq / Hkv > 128) return KV4_ERR_UNSUPPORTED;
+  if (n_tokens == 0 || B == 0) return KV4_OK;
+  if (max_new == 0) return KV4_ERR_INVALID_ARG;
+  if (!q_dev || !cu_seqlens_dev || !pool_dev || !scales_dev || !page_table_dev || !seq_lens_dev ||
+      !out_dev || !lse_dev)
+    return KV4_ERR_INVALID_ARG;
+  if (!strides_ok(q_dev, q_token_stride, q_head_stride, Hq, D) || !aligned128(pool_dev) ||
+      !aligned16(out_dev) || !aligned4(lse_dev) || !aligned4(cu_seqlens_dev) ||
+      !aligned4(page_table_dev) || !aligned4(seq_lens_dev) || !aligned4(dev_err))
+    return KV4_ERR_INVALID_ARG;
+  int sms = 0;
+  const kv4_status st = device_info(&sms);
+  if (st != KV4_OK) return st;
+  const size_t need = kv4::attention_gqa8_workspace(B, max_new, n_tokens, Hq, Hkv, D, sms);
+  if (need > 0 && (!workspace_dev || workspace_bytes < need || !aligned16(workspace_dev)))
+    return KV4_ERR_WORKSPACE;
+  kv4::Gqa8AttnArgs a{};
+  a.q = q_dev;
+  a.q_token_stride = q_token_stride;
+  a.q_head_stride = q_head_stride;
+  a.f16 = dtype == KV4_F16;
+  a.n_tokens = n_tokens;
+  a.cu = cu_seqlens_dev;
+  a.max_new = max_new;
+  a.pool = pool_dev;
+  a.scales = scales_dev;
+  a.num_pages = num_pages;
+  a.page_table = page_table_dev;
+  a.pt_stride = pt_stride;
+  a.lens = seq_lens_dev;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.window = window;
+  a.sm_scale = sm_scale;
+  a.out = out_dev;
+  a.lse = lse_dev;
+  a.ws = workspace_dev;
+  a.dev_err = dev_err;
+  a.timeout_ns = static_cast<uint64_t>(g_timeout_ns.load());
+  a.fault_site = g_fault_site.load();
+  a.num_sms = sms;
+  return kv4::launch_attention_gqa8(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KV4_OK
+             : KV4_ERR_LAUNCH;
+}
 
 kv4_status kv4_set_wait_limit(int64_t timeout_ns, int fault_site) {
   if (timeout_ns < 0 || fault_site < 0 || fault_site > 1) return KV4_ERR_INVALID_ARG;

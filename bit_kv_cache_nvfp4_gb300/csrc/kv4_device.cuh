@@ -29,6 +29,8 @@ constexpr int kChunkBytes = kTileKeys * 128;   // one 64-column slab of a tile
 constexpr int kDevBadSlot = 1;
 constexpr int kDevBadPage = 2;
 constexpr int kDevTimeout = 4;
+constexpr int kDevNonFinite = 8;
+constexpr int kDevBadLength = 16;
 
 // ---------------------------------------------------------------------------
 // small utilities

@@ -1,0 +1,329 @@
+// kv4_gqa8.cu -- write and read-back of the 8-bit grouped-query cache
+// (kv4_append_gqa8, kv4_read_gqa8).
+//
+// A page holds 64 tokens of one request; the block of a (page, kv head, side)
+// is 64 x D E4M3 codes with one E8M0 exponent byte, value = code * 2^(byte -
+// 127).  The exponent is the least e with amax <= 448 * 2^e, kept in
+// [-48, 48].  E4M3 is itself a floating-point code, so a power-of-two scale
+// costs it no precision (only where in its 15 octaves a block sits), x * 2^-e
+// is exact, and a page whose exponent has to rise when tokens join it keeps
+// its codes exactly but for those that fall into the code's subnormal range.
+//
+// Both kernels give one thread block to one (page of a request, kv head): the
+// block is the unit whose maximum the write needs, and 2 x 64 x D values
+// (32 KB of inputs at D = 128) fit its threads' registers, so the inputs are
+// read once.
+#include "kv4_device.cuh"
+#include "kv4_launch.h"
+
+namespace kv4 {
+namespace {
+
+constexpr int kThreads = 256;
+
+// The page of request `b` that a block of the grid stands for.  Blocks are
+// laid out over page indices g(b) + p with g(b) = cu[b] / 64 + 2 b: a
+// request's n tokens touch at most ceil(n / 64) + 1 <= g(b + 1) - g(b) pages,
+// so no prefix sum over the requests is needed (at most two blocks per
+// request find nothing to do).
+struct PageItem {
+  int b;
+  int64_t row0;        // flat row of the first token at or after position 0 (cu[b] + skipped)
+  int64_t start, end;  // token positions [start, end) of the request, start >= 0
+  int64_t page;        // logical page
+};
+__device__ __forceinline__ int clamp_cu(int32_t v, int64_t n_tokens) {
+  return v < 0 ? 0 : (v > n_tokens ? static_cast<int>(n_tokens) : v);
+}
+
+// starts: first position of each request's range, or null: the range ends at
+// seq_lens (an append).
+__device__ __forceinline__ bool find_page(const Gqa8Args& a, int w, PageItem& it) {
+  int lo = 0, hi = a.B - 1;                       // largest b with g(b) <= w
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    const int g = (clamp_cu(__ldg(a.cu + mid), a.n_tokens) >> 6) + 2 * mid;
+    if (g <= w) lo = mid; else hi = mid - 1;
+  }
+  const int c0 = clamp_cu(__ldg(a.cu + lo), a.n_tokens);
+  const int c1 = clamp_cu(__ldg(a.cu + lo + 1), a.n_tokens);
+  const int p = w - (c0 >> 6) - 2 * lo;
+  const int64_t n = c1 - c0;
+  if (n <= 0 || p < 0) return false;
+  int64_t start = a.starts != nullptr ? static_cast<int64_t>(__ldg(a.starts + lo))
+                                      : static_cast<int64_t>(__ldg(a.lens + lo)) - n;
+  it.b = lo;
+  it.end = start + n;
+  it.row0 = c0;
+  if (start < 0) {                                // tokens before position 0 have no place
+    it.row0 -= start;
+    start = 0;
+  }
+  it.start = start;
+  it.page = (start >> 6) + p;
+  return (it.page << 6) < it.end;
+}
+
+// Physical page, or -1 (flagged) where the table has none.
+__device__ __forceinline__ int64_t physical_page(const Gqa8Args& a, const PageItem& it) {
+  int64_t pg = -1;
+  if (it.page < a.pt_stride) pg = __ldg(a.page_table + it.b * a.pt_stride + it.page);
+  if (pg < 0 || pg >= a.num_pages) {
+    if (threadIdx.x == 0) flag_error(a.dev_err, kDevBadPage);
+    return -1;
+  }
+  return pg;
+}
+
+// 16 values of 16 bits at p as floats.
+template <bool F16>
+__device__ __forceinline__ void widen8(const uint4& v, float* x) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (F16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    } else {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float hi, float lo) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint4 encode16(const float* x, float f) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = f32x2_to_e4m3x2(x[4 * i + 1] * f, x[4 * i] * f) |
+           (f32x2_to_e4m3x2(x[4 * i + 3] * f, x[4 * i + 2] * f) << 16);
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ void decode16(const uint4& c, float* x) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t h = e4m3x2_to_f16x2((w[i] >> (16 * j)) & 0xFFFFu);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      x[4 * i + 2 * j] = f.x;
+      x[4 * i + 2 * j + 1] = f.y;
+    }
+  }
+}
+
+__device__ __forceinline__ float pow2f(int e) {     // e in [-126, 127]
+  return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+}
+// Least e with amax <= 448 * 2^e = 1.75 * 2^(e + 8), from the bits of a finite
+// fp32 amax; [-48, 48].
+__device__ __forceinline__ int block_exponent(uint32_t amax_bits) {
+  const int e = static_cast<int>(amax_bits >> 23) - 127 - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return e < kGqa8ExpMin ? kGqa8ExpMin : (e > kGqa8ExpMax ? kGqa8ExpMax : e);
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads) append_kernel(Gqa8Args a) {
+  constexpr int TPR = D / 16;                      // threads per token row
+  constexpr int RPP = kThreads / TPR;              // rows per pass
+  constexpr int PASSES = kPage / RPP;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  __shared__ uint32_t red[2][kThreads / 32];
+  PageItem it;
+  if (!find_page(a, blockIdx.x, it)) return;
+  const int64_t pg = physical_page(a, it);
+  if (pg < 0) return;
+  const int h = blockIdx.y, tid = threadIdx.x;
+  const int lo = it.start > (it.page << 6) ? static_cast<int>(it.start & 63) : 0;
+  const int hi = it.end - (it.page << 6) < kPage ? static_cast<int>(it.end - (it.page << 6)) : kPage;
+  const int64_t row_of_0 = it.row0 + (it.page << 6) - it.start;     // flat row of the page's row 0
+  uint8_t* scale = a.scales + (pg * a.Hkv + h) * 2;
+  const int col = (tid % TPR) * 16, r0 = tid / TPR;
+  const uint16_t* src[2] = {static_cast<const uint16_t*>(a.k) + h * a.k_head_stride + col,
+                            static_cast<const uint16_t*>(a.v) + h * a.v_head_stride + col};
+  const int64_t ts[2] = {a.k_token_stride, a.v_token_stride};
+  uint4 x[2][PASSES][2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      const int r = r0 + p * RPP;
+      x[s][p][0] = x[s][p][1] = make_uint4(0, 0, 0, 0);
+      if (r >= lo && r < hi) {
+        const uint4* g = reinterpret_cast<const uint4*>(src[s] + (row_of_0 + r) * ts[s]);
+        x[s][p][0] = __ldg(g);
+        x[s][p][1] = __ldg(g + 1);
+      }
+    }
+  // largest finite magnitude of each side, as fp32 bits (which order like the
+  // values); a NaN or an infinity does not count and is flagged
+  uint32_t m[2] = {0, 0};
+  bool odd = false;
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float f[8];
+        widen8<F16>(x[s][p][j], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t u = __float_as_uint(f[i]) & 0x7FFFFFFFu;
+          if (u >= 0x7F800000u) odd = true; else m[s] = max(m[s], u);
+        }
+      }
+  if (odd) flag_error(a.dev_err, kDevNonFinite);
+  m[0] = __reduce_max_sync(0xFFFFFFFFu, m[0]);
+  m[1] = __reduce_max_sync(0xFFFFFFFFu, m[1]);
+  if ((tid & 31) == 0) {
+    red[0][tid >> 5] = m[0];
+    red[1][tid >> 5] = m[1];
+  }
+  int old[2] = {kGqa8ExpMin, kGqa8ExpMin};
+  if (lo > 0) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int e = static_cast<int>(scale[s]) - 127;
+      old[s] = e < kGqa8ExpMin ? kGqa8ExpMin : (e > kGqa8ExpMax ? kGqa8ExpMax : e);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    uint32_t mm = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) mm = max(mm, red[s][i]);
+    const int e = max(block_exponent(mm), old[s]);
+    if (tid == 0) scale[s] = static_cast<uint8_t>(e + 127);
+    uint8_t* blk = a.pool + ((pg * a.Hkv + h) * 2 + s) * (kPage * D) + col;
+    const float f = pow2f(-e);
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      const int r = r0 + p * RPP;
+      if (r >= lo && r < hi) {
+        float v[16];
+        widen8<F16>(x[s][p][0], v);
+        widen8<F16>(x[s][p][1], v + 8);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = v[i] == v[i] ? v[i] : 0.0f;      // NaN -> 0
+        *reinterpret_cast<uint4*>(blk + r * D) = encode16(v, f);
+      } else if (r < lo && e > old[s]) {
+        uint4* c = reinterpret_cast<uint4*>(blk + r * D);
+        float v[16];
+        decode16(*c, v);
+        *c = encode16(v, pow2f(old[s] - e));
+      }
+    }
+  }
+}
+
+// Two floats -> 16-bit pair (first in the low half), round half to even; f16
+// saturates at 65504.
+template <bool F16>
+__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(fminf(fmaxf(lo, -65504.0f), 65504.0f),
+                                        fminf(fmaxf(hi, -65504.0f), 65504.0f));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads) read_kernel(Gqa8Args a) {
+  constexpr int TPR = D / 16, RPP = kThreads / TPR, PASSES = kPage / RPP;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  PageItem it;
+  if (!find_page(a, blockIdx.x, it)) return;
+  const int64_t pg = physical_page(a, it);
+  const int h = blockIdx.y, tid = threadIdx.x;
+  const int lo = it.start > (it.page << 6) ? static_cast<int>(it.start & 63) : 0;
+  const int hi = it.end - (it.page << 6) < kPage ? static_cast<int>(it.end - (it.page << 6)) : kPage;
+  const int64_t row_of_0 = it.row0 + (it.page << 6) - it.start;
+  const int col = (tid % TPR) * 16, r0 = tid / TPR;
+  uint4 c[2][PASSES];
+  float f[2] = {0.0f, 0.0f};
+  if (pg >= 0) {
+    const uint8_t* blk = a.pool + (pg * a.Hkv + h) * 2 * (kPage * D) + col;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int e = static_cast<int>(__ldg(a.scales + (pg * a.Hkv + h) * 2 + s)) - 127;
+      f[s] = pow2f(e < -126 ? -126 : (e > 127 ? 127 : e));
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int r = r0 + p * RPP;
+        c[s][p] = r >= lo && r < hi ? __ldg(reinterpret_cast<const uint4*>(blk + (s * kPage + r) * D))
+                                    : make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      const int r = r0 + p * RPP;
+      if (r < lo || r >= hi) continue;
+      uint4 o[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+      if (pg >= 0) {
+        float v[16];
+        decode16(c[s][p], v);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float* u = v + 8 * j;
+          o[j] = make_uint4(narrow2<F16>(u[0] * f[s], u[1] * f[s]), narrow2<F16>(u[2] * f[s], u[3] * f[s]),
+                            narrow2<F16>(u[4] * f[s], u[5] * f[s]), narrow2<F16>(u[6] * f[s], u[7] * f[s]));
+        }
+      }
+      uint16_t* dst = static_cast<uint16_t*>(s == 0 ? a.k_out : a.v_out) +
+                      ((row_of_0 + r) * a.Hkv + h) * D + col;
+      reinterpret_cast<uint4*>(dst)[0] = o[0];
+      reinterpret_cast<uint4*>(dst)[1] = o[1];
+    }
+}
+
+template <typename K>
+cudaError_t launch_pages(K kernel, const Gqa8Args& a, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.n_tokens / kPage + 2 * static_cast<int64_t>(a.B)),
+                     static_cast<unsigned>(a.Hkv));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+}  // namespace
+
+cudaError_t launch_append_gqa8(const Gqa8Args& a, cudaStream_t stream) {
+  if (a.D == 64)
+    return a.f16 ? launch_pages(append_kernel<64, true>, a, stream)
+                 : launch_pages(append_kernel<64, false>, a, stream);
+  return a.f16 ? launch_pages(append_kernel<128, true>, a, stream)
+               : launch_pages(append_kernel<128, false>, a, stream);
+}
+
+cudaError_t launch_read_gqa8(const Gqa8Args& a, cudaStream_t stream) {
+  if (a.D == 64)
+    return a.f16 ? launch_pages(read_kernel<64, true>, a, stream)
+                 : launch_pages(read_kernel<64, false>, a, stream);
+  return a.f16 ? launch_pages(read_kernel<128, true>, a, stream)
+               : launch_pages(read_kernel<128, false>, a, stream);
+}
+
+}  // namespace kv4

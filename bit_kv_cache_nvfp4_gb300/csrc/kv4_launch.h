@@ -77,6 +77,54 @@ struct GatherArgs {
   int32_t* dev_err;
 };
 
+// The 8-bit grouped-query cache (kv4_append_gqa8, kv4_read_gqa8).
+struct Gqa8Args {
+  const void* k;               // inputs of an append: 16-bit [T, Hkv, D], strided
+  int64_t k_token_stride, k_head_stride;
+  const void* v;
+  int64_t v_token_stride, v_head_stride;
+  void* k_out;                 // outputs of a read: 16-bit [T, Hkv, D]
+  void* v_out;
+  int f16;                     // 16-bit type: 0 bf16, 1 f16
+  int64_t n_tokens;            // T
+  const int32_t* cu;           // int32 [B + 1]: each request's rows of the flat inputs / outputs
+  const int32_t* starts;       // read: first position of each request's range
+  const int32_t* lens;         // append: tokens of each request, the new ones included
+  const int32_t* page_table;
+  int64_t pt_stride;
+  int B, Hkv, D;
+  uint8_t* pool;               // [num_pages, Hkv, 2, 64, D] E4M3
+  uint8_t* scales;             // [num_pages, Hkv, 2] E8M0
+  int64_t num_pages;
+  int32_t* dev_err;
+};
+constexpr int kGqa8ExpMin = -48, kGqa8ExpMax = 48;
+
+struct Gqa8AttnArgs {
+  const void* q;               // 16-bit [T, Hq, D], strided
+  int64_t q_token_stride, q_head_stride;
+  int f16;
+  int64_t n_tokens;
+  const int32_t* cu;
+  int max_new;                 // most new tokens of one request
+  const uint8_t* pool;
+  const uint8_t* scales;
+  int64_t num_pages;
+  const int32_t* page_table;
+  int64_t pt_stride;
+  const int32_t* lens;
+  int B, Hq, Hkv, D;
+  int window;                  // keys a row sees at most (0: all)
+  float sm_scale;
+  void* out;                   // 16-bit [T, Hq, D]
+  float* lse;                  // fp32 [T, Hq]
+  void* ws;
+  int32_t* dev_err;
+  uint64_t timeout_ns;
+  int fault_site;
+  int num_sms;
+};
+
 // Launch of one of the library's kernels with programmatic stream
 // serialization allowed (the kernel may begin while the previous kernel of
 // the stream finishes; it calls grid_dependency_wait() before touching
@@ -125,6 +173,12 @@ cudaError_t launch_merge_partials(const float* o_parts, const float* lse_parts, 
                                   int64_t n_rows, void* out_bf16, float* lse,
                                   cudaStream_t stream);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_append_gqa8(const Gqa8Args& a, cudaStream_t stream);
+cudaError_t launch_read_gqa8(const Gqa8Args& a, cudaStream_t stream);
+cudaError_t launch_attention_gqa8(const Gqa8AttnArgs& a, cudaStream_t stream);
+// Workspace bytes of launch_attention_gqa8 for these sizes on num_sms SMs.
+size_t attention_gqa8_workspace(int B, int max_new, int64_t n_tokens, int Hq, int Hkv, int D,
+                                int num_sms);
 cudaError_t launch_debug_gather(const GatherArgs& a, cudaStream_t stream);
 // The FP8 scratch copy of the rows the keys select: a.rows is uint8
 // [B*Sq*K, 576] (E4M3 of the dequantized NVFP4 values; masked keys 0).

@@ -65,8 +65,12 @@ enum {
   KV4_DEV_BAD_SLOT = 1,      /* write: slot >= num_slots; that row skipped     */
   KV4_DEV_BAD_PAGE = 2,      /* decode: page index >= pt_stride, negative page
                                 entry or slot >= num_slots; that key masked    */
-  KV4_DEV_TIMEOUT = 4        /* a bounded on-chip wait gave up; the outputs of
+  KV4_DEV_TIMEOUT = 4,       /* a bounded on-chip wait gave up; the outputs of
                                 that thread block are not valid               */
+  KV4_DEV_NONFINITE = 8,     /* kv4_append_gqa8: a NaN (stored as 0) or an
+                                infinity (stored saturated) in the inputs     */
+  KV4_DEV_BAD_LENGTH = 16    /* kv4_attention_gqa8: a request with more new
+                                tokens than max_new; its rows are not written */
 };
 
 enum {
@@ -75,6 +79,9 @@ enum {
   KV4_ROW_BYTES_LATENT = 288,  /* latent-only row (the *_latent entry points) */
   KV4_ROW_BYTES_FP8 = 576      /* FP8 comparison row (the *_fp8 entry points)  */
 };
+
+/* 16-bit types of the *_gqa8 entry points. */
+enum { KV4_BF16 = 0, KV4_F16 = 1 };
 
 /* ---------------------------------------------------------------------------
  * kv4_quantize_write -- quantize N new tokens into their cache rows.
@@ -479,6 +486,86 @@ kv4_status kv4_sparse_mla_decode_noalloc(const void* q_dev, const uint8_t* pool_
                                          int force_splits, int32_t* dev_err,
                                          kv4_stream_t stream);
 size_t kv4_noalloc_scratch_bytes(void);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit grouped-query cache (*_gqa8): K and V of models whose query heads
+ * share Hkv key/value heads, in 64-token pages of E4M3 codes with one E8M0
+ * exponent for each page, head and side.  Source: README "4-bit KV cache" (a
+ * quantized paged cache that the attention reads as it is; the FP8 row is its
+ * comparison); the pages' models cache one MLA latent per token, so the block
+ * layout is this project's.
+ *   pool_dev        uint8 [num_pages, Hkv, 2, 64, D]: E4M3 codes, K then V of
+ *                   a page and head; 128-byte aligned
+ *   scales_dev      uint8 [num_pages, Hkv, 2]: value = code * 2^(byte - 127)
+ *   page_table_dev  int32 [B, pt_stride]: physical page of each logical page;
+ *                   page_size must be 64
+ *   seq_lens_dev    int32 [B]: tokens of each request, its new ones included
+ *   cu_seqlens_dev  int32 [B + 1], rising, 0 <= . <= n_tokens: request b's new
+ *                   tokens are rows cu[b] .. cu[b+1]-1 of the flat tensors, at
+ *                   positions seq_lens[b] - n .. seq_lens[b] - 1 (a row whose
+ *                   position is negative is skipped); rows from cu[B] on are
+ *                   neither read nor written
+ *   dtype           KV4_BF16 or KV4_F16, of k, v, q, out and the read-back
+ *   Hkv, D          Hkv >= 1; D = 64 or 128
+ * Sizes: n_tokens * heads * D < 2^40, B <= 65535, num_pages < 2^31 - 1.
+ * Inputs are strided (in elements, multiples of 8; base 16-byte aligned), so
+ * slices of a fused projection's output need no copy; outputs are contiguous.
+ * A page index past the table, a negative entry or one >= num_pages raises
+ * KV4_DEV_BAD_PAGE: the write skips the page, the read gives zeros, the
+ * attention masks its keys.  Nothing else of the device-side data can lead
+ * outside the buffers.
+ *
+ * kv4_append_gqa8 -- quantize the new tokens' K and V into their pages.
+ *   Exponent of a block: the least e with amax <= 448 * 2^e, in [-48, 48],
+ *   over its finite new values; if the request has earlier tokens in the page
+ *   (its first new one is not the page's first row), at least the block's
+ *   exponent so far, and when that rises the earlier codes are re-rounded to
+ *   the new one.  code = E4M3(x * 2^-e), round half to even, saturating; NaN
+ *   gives code 0 and an infinity +-448, both with KV4_DEV_NONFINITE.  Rows
+ *   past the last token are left as they are.  A page that receives tokens
+ *   belongs to one request of the call.
+ * kv4_read_gqa8 -- the values of positions starts[b] .. starts[b] + n - 1 of
+ *   each request (n = cu[b+1] - cu[b]), 16-bit [n_tokens, Hkv, D] each for K
+ *   and V, 16-byte aligned: code * 2^e, rounded once; f16 saturates at 65504.
+ * kv4_attention_gqa8 -- causal attention of the new tokens over the cache
+ *   (which already holds them): row i of request b sees keys j <= its
+ *   position, and with window > 0 only j > position - window.
+ *   q_dev           16-bit [n_tokens, Hq, D], Hq a multiple of Hkv with
+ *                   Hq / Hkv <= 128; head h reads kv head h / (Hq / Hkv)
+ *   max_new         the most new tokens of any request (host value); a request
+ *                   with more raises KV4_DEV_BAD_LENGTH
+ *   out_dev         16-bit [n_tokens, Hq, D]; 0 for a row without a key
+ *   lse_dev         fp32 [n_tokens, Hq], natural log; -inf without a key
+ *   workspace_dev   at least the bytes kv4_attention_gqa8_plan returns for the
+ *                   same sizes, 16-byte aligned, of this call alone while it
+ *                   runs; nothing in it needs a value
+ *   A row of q with a NaN or an infinity gives NaN (when it has a key).  A
+ *   NaN code (0x7F, 0xFF) in a row below seq_lens, which the append never
+ *   writes, may turn any row of the request NaN; what lies past seq_lens, or
+ *   before every row's window, is never used.
+ * ------------------------------------------------------------------------- */
+kv4_status kv4_append_gqa8(const void* k_dev, int64_t k_token_stride, int64_t k_head_stride,
+                           const void* v_dev, int64_t v_token_stride, int64_t v_head_stride,
+                           int dtype, int64_t n_tokens, const int32_t* cu_seqlens_dev,
+                           const int32_t* page_table_dev, int64_t pt_stride, int page_size,
+                           const int32_t* seq_lens_dev, int B, int Hkv, int D, uint8_t* pool_dev,
+                           uint8_t* scales_dev, int64_t num_pages, int32_t* dev_err,
+                           kv4_stream_t stream);
+kv4_status kv4_read_gqa8(const uint8_t* pool_dev, const uint8_t* scales_dev, int64_t num_pages,
+                         const int32_t* page_table_dev, int64_t pt_stride, int page_size,
+                         const int32_t* starts_dev, const int32_t* cu_seqlens_dev,
+                         int64_t n_tokens, int B, int Hkv, int D, int dtype, void* k_out_dev,
+                         void* v_out_dev, int32_t* dev_err, kv4_stream_t stream);
+kv4_status kv4_attention_gqa8_plan(int B, int max_new, int64_t n_tokens, int Hq, int Hkv, int D,
+                                   size_t* workspace_bytes);
+kv4_status kv4_attention_gqa8(const void* q_dev, int64_t q_token_stride, int64_t q_head_stride,
+                              int dtype, int64_t n_tokens, const int32_t* cu_seqlens_dev,
+                              int max_new, const uint8_t* pool_dev, const uint8_t* scales_dev,
+                              int64_t num_pages, const int32_t* page_table_dev,
+                              int64_t pt_stride, int page_size, const int32_t* seq_lens_dev,
+                              int B, int Hq, int Hkv, int D, int window, float sm_scale,
+                              void* out_dev, float* lse_dev, void* workspace_dev,
+                              size_t workspace_bytes, int32_t* dev_err, kv4_stream_t stream);
 
 /* Test hook: the next decode launches use this bounded-wait limit (ns; 0
  * keeps the 1 s default) and, when fault_site == 1, one warp of each block

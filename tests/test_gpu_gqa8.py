@@ -1,0 +1,450 @@
+"""The 8-bit grouped-query cache on the GPU against its 64-bit definition
+(tests/gqa8_ref.py): the append bit for bit, the read-back exactly, the
+attention within bounds derived there."""
+import math
+
+import pytest
+import torch
+
+import bit_kv_cache_nvfp4_gb300 as kv
+import gqa8_ref as ref
+
+pytestmark = pytest.mark.gpu
+BF16, F16 = torch.bfloat16, torch.float16
+
+
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    return torch.device("cuda", torch.cuda.current_device())
+
+
+def ints(x, device):
+    return torch.tensor(x, dtype=torch.int32, device=device)
+
+
+# ---------------------------------------------------------------------------
+# append
+# ---------------------------------------------------------------------------
+def run_append(k, v, cu, c, pool=None, scales=None):
+    pool, scales = c.pool.clone(), c.scales.clone()
+    err = torch.zeros(1, dtype=torch.int32, device=k.device)
+    kv.append_gqa8(k, v, ints(cu, k.device), c.page_table, c.seq_lens, pool, scales, dev_err=err)
+    want_pool, want_scales = c.pool.cpu().clone(), c.scales.cpu().clone()
+    ref.append(k.double().cpu(), v.double().cpu(), cu, c.table, c.lens, want_pool, want_scales)
+    assert torch.equal(scales.cpu(), want_scales)
+    assert torch.equal(pool.cpu(), want_pool)
+    return int(err.item())
+
+
+@pytest.mark.parametrize("d,dtype,hkv", [(128, BF16, 2), (64, F16, 3), (128, F16, 1), (64, BF16, 8)])
+@pytest.mark.parametrize("lens,news", [
+    ([1], [1]), ([64, 65, 63], [64, 65, 63]), ([65, 64, 128, 200], [1, 1, 1, 1]),
+    ([300, 7, 129, 0, 70], [200, 7, 2, 0, 69]), ([5, 0, 90], [9, 2, 90]),
+])
+def test_append_matches_the_definition(d, dtype, hkv, lens, news):
+    device = dev()
+    g = torch.Generator(device=device).manual_seed(len(lens) + d)
+    c = ref.Cache(lens, hkv, d, device, seed=d + hkv)
+    cu = ref.cu_of(news)
+    x = torch.randn(cu[-1] + 3, 2, hkv, d, device=device, generator=g)
+    x = (x * torch.exp2(torch.randint(-9, 9, (cu[-1] + 3, 1, hkv, 1), device=device, generator=g).float())).to(dtype)
+    assert run_append(x[:, 0], x[:, 1], cu, c) == 0
+
+
+def test_append_exponent_limits_and_zero_blocks():
+    """Blocks at and beyond both ends of the exponent's range, all-zero blocks,
+    amax exactly 448 * 2^e and one step above it."""
+    device = dev()
+    rows = [0.0, 448.0, 450.0, 1.75, 1.7578125, 2.0 ** -60, 3e38, 2.0 ** -40 * 448, 1e-38]
+    for i, big in enumerate(rows):
+        c = ref.Cache([40], 1, 64, device, seed=i)
+        x = torch.zeros(40, 1, 64, device=device, dtype=BF16)
+        x[3, 0, 5] = -big
+        x[9, 0, :] = big / 3
+        assert run_append(x, x.flip(0), [0, 40], c) == 0
+
+
+def test_append_keeps_earlier_tokens_of_the_page():
+    """Token by token: the exponent of a page rises with a large token and the
+    earlier codes are re-rounded, also when the write starts at row 1 or 63."""
+    device = dev()
+    c = ref.Cache([1], 2, 64, device, seed=3)
+    pool, scales = c.pool, c.scales
+    table, page = c.page_table, c.table[0][0]
+    want_pool, want_scales = pool.cpu().clone(), scales.cpu().clone()
+    g = torch.Generator(device=device).manual_seed(1)
+    for n in range(1, 65):
+        x = (torch.randn(1, 2, 2, 64, device=device, generator=g) * 2.0 ** ((n * 7) % 23 - 8)).to(BF16)
+        kv.append_gqa8(x[:, 0], x[:, 1], ints([0, 1], device), table, ints([n], device), pool, scales)
+        ref.append(x[:, 0].double().cpu(), x[:, 1].double().cpu(), [0, 1], c.table, [n], want_pool, want_scales)
+        assert torch.equal(scales.cpu()[page], want_scales[page]), n
+        assert torch.equal(pool.cpu()[page], want_pool[page]), n
+
+
+def test_append_flags_and_sanitizes_nonfinite_values():
+    device = dev()
+    c = ref.Cache([70], 1, 64, device, seed=5)
+    x = torch.randn(70, 1, 64, device=device).to(BF16)
+    x[3, 0, 7], x[4, 0, 8], x[69, 0, 1] = math.nan, math.inf, -math.inf
+    y = torch.randn(70, 1, 64, device=device).to(BF16)
+    assert run_append(x, y, [0, 70], c) == kv.DEV_NONFINITE
+
+
+def test_append_skips_bad_pages():
+    device = dev()
+    c = ref.Cache([200, 100], 1, 64, device, seed=6, extra_columns=0)
+    c.table[0][1], c.table[1][0] = c.pool.shape[0], -5
+    c.page_table = ints(c.table, device)
+    c.lens = [300, 100]                     # beyond the table as well
+    c.seq_lens = ints(c.lens, device)
+    x = torch.randn(400, 1, 64, device=device).to(BF16)
+    assert run_append(x, x, [0, 300, 400], c) == kv.DEV_BAD_PAGE
+
+
+# ---------------------------------------------------------------------------
+# read-back
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("d,dtype,hkv", [(128, BF16, 2), (64, F16, 3), (128, F16, 8), (64, BF16, 1)])
+def test_read_is_exact(d, dtype, hkv):
+    device = dev()
+    c = ref.Cache([200, 64, 1, 300, 10], hkv, d, device, seed=d, spread=3)
+    starts, news = [63, 0, 0, 129, 4], [130, 64, 1, 171, 0]
+    cu = ref.cu_of(news)
+    total = cu[-1] + 2
+    k = torch.full((total, hkv, d), 7.0, dtype=dtype, device=device)
+    v = torch.full((total, hkv, d), 8.0, dtype=dtype, device=device)
+    err = torch.zeros(1, dtype=torch.int32, device=device)
+    got = kv.read_gqa8(c.pool, c.scales, c.page_table, ints(starts, device), ints(cu, device), total,
+                       dtype=dtype, k_out=k, v_out=v, dev_err=err)
+    assert got[0] is k and got[1] is v and int(err.item()) == 0
+    for b in range(5):
+        x = ref.values(c.pool, c.scales, c.table[b], starts[b], starts[b] + news[b])
+        rows = slice(cu[b], cu[b + 1])
+        assert torch.equal(k[rows].double(), x[:, 0].transpose(0, 1).to(dtype).double())
+        assert torch.equal(v[rows].double(), x[:, 1].transpose(0, 1).to(dtype).double())
+    assert (k[cu[-1]:] == 7).all() and (v[cu[-1]:] == 8).all()
+
+
+def test_read_saturates_f16_and_zeroes_bad_pages():
+    device = dev()
+    c = ref.Cache([64, 64], 1, 64, device, seed=1)
+    c.pool[c.table[0][0]] = 0x7E                                 # 448
+    c.scales[c.table[0][0]] = 127 + 8                            # 114688
+    table = [c.table[0], [c.pool.shape[0]] + c.table[1][1:]]
+    err = torch.zeros(1, dtype=torch.int32, device=device)
+    k, v = kv.read_gqa8(c.pool, c.scales, ints(table, device), ints([0, 0], device), ints([0, 64, 128], device),
+                        128, dtype=F16, dev_err=err)
+    assert (k[:64] == 65504).all() and (v[:64] == 65504).all()
+    assert (k[64:] == 0).all() and (v[64:] == 0).all() and int(err.item()) == kv.DEV_BAD_PAGE
+
+
+# ---------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------
+def check_attention(c, news, hq, dtype, window=0, sm_scale=None, q=None, max_new=None, seed=0, gain=1.0):
+    device, d = c.pool.device, c.pool.shape[4]
+    cu = ref.cu_of(news)
+    if q is None:
+        g = torch.Generator(device=device).manual_seed(seed)
+        q = (torch.randn(cu[-1], hq, d, device=device, generator=g) * gain).to(dtype)
+    scale = d ** -0.5 if sm_scale is None else sm_scale
+    out = torch.full((q.shape[0], hq, d), 3.0, dtype=dtype, device=device)
+    lse = torch.full((q.shape[0], hq), 3.0, device=device)
+    err = torch.zeros(1, dtype=torch.int32, device=device)
+    kv.attention_gqa8(q, c.pool, c.scales, c.page_table, c.seq_lens, ints(cu, device),
+                      max(news) if max_new is None else max_new, scale, window=window, out=out, lse=lse,
+                      dev_err=err)
+    want = ref.attention(q[:cu[-1]], c.pool, c.scales, c.table, c.lens, cu, scale, window)
+    tol, lse_tol = ref.bounds(*want, dtype, d)
+    n = cu[-1]
+    assert (out[n:] == 3).all() and (lse[n:] == 3).all()         # rows behind the last request
+    off = (out[:n].double() - want[0]).abs()
+    assert out[:n].isfinite().all()
+    worst = float((off / tol).max()) if n else 0.0
+    assert worst <= 1, f"out error {float(off.max()):.3g}, {worst:.3g} of its bound"
+    empty = want[1] == -math.inf
+    assert torch.equal(lse[:n] == -math.inf, empty)
+    off = (lse[:n].double() - want[1]).masked_fill(empty, 0).abs()
+    worst = float((off / lse_tol).max()) if n else 0.0
+    assert worst <= 1, f"lse error {float(off.max()):.3g}, {worst:.3g} of its bound"
+    assert (out[:n][empty] == 0).all()
+    return int(err.item()), out, lse
+
+
+EDGES = [1, 2, 63, 64, 65, 127, 128, 129, 200, 513]
+
+
+@pytest.mark.parametrize("g,hkv,d,dtype", [(1, 2, 128, BF16), (4, 2, 128, BF16), (8, 1, 64, BF16), (7, 3, 64, F16),
+                                           (3, 1, 128, F16), (16, 2, 128, BF16), (12, 1, 64, F16), (33, 1, 128, BF16)])
+def test_attention_single_tokens(g, hkv, d, dtype):
+    c = ref.Cache(EDGES, hkv, d, dev(), seed=g, spread=1)
+    assert check_attention(c, [1] * len(EDGES), g * hkv, dtype, seed=g)[0] == 0
+
+
+@pytest.mark.parametrize("g,hkv,d,dtype", [(8, 1, 128, BF16), (5, 2, 64, F16), (1, 3, 128, F16), (4, 2, 64, BF16)])
+@pytest.mark.parametrize("news", [[2, 3, 4, 1, 0, 4], [9, 1, 30, 64, 65, 2], [130, 257, 1, 200, 33, 64]])
+@pytest.mark.parametrize("window", [0, 1, 50, 100])
+def test_attention_several_tokens(g, hkv, d, dtype, news, window):
+    lens = [max(n, m) for n, m in zip(news, [2, 300, 64, 129, 40, 1000])]
+    c = ref.Cache(lens, hkv, d, dev(), seed=g + window)
+    assert check_attention(c, news, g * hkv, dtype, window=window, seed=g)[0] == 0
+
+
+@pytest.mark.parametrize("news", [[3, 2, 4, 1, 1], [90, 1, 40, 0, 100]])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_attention_rows_without_a_key(news, dtype):
+    """Sequences of length zero, and fewer tokens than rows: 0 and -inf."""
+    c = ref.Cache([2, 0, 1, 1, 0], 2, 128, dev(), seed=2)
+    check_attention(c, news, 8, dtype)
+
+
+@pytest.mark.parametrize("news", [[1, 1, 1], [70, 40, 1]])
+def test_attention_masks_bad_pages(news):
+    c = ref.Cache([300, 400, 130], 2, 128, dev(), seed=4, extra_columns=0)
+    c.table[0][1], c.table[0][4], c.table[1][6] = -1, c.pool.shape[0], 1 << 30
+    c.table[2][:3] = [-7, -7, -7]                                # nothing left of this one
+    c.page_table = ints(c.table, c.pool.device)
+    c.lens[1] = 700                                              # beyond the table
+    c.seq_lens = ints(c.lens, c.pool.device)
+    assert check_attention(c, news, 8, BF16)[0] == kv.DEV_BAD_PAGE
+
+
+@pytest.mark.parametrize("news", [[1, 1], [5, 40]])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_attention_blocks_of_very_different_size(news, dtype):
+    """Page exponents up to 24 octaves apart; the last pages tiny."""
+    c = ref.Cache([700, 1000], 1, 128, dev(), seed=8, spread=12)
+    check_attention(c, news, 4, dtype, sm_scale=2.0 ** -16)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("nats", [8.0, 14.0])
+def test_attention_first_token_draws_most(n, dtype, nats):
+    """One key far above many small ones, whose weights together still count."""
+    device = dev()
+    c = ref.Cache([20000], 1, 64, device, seed=9)
+    page = c.table[0][0]
+    c.pool[page, 0, 0, 0] = 0x38                                 # 1.0
+    c.pool[page, 0, 0, 1:] = 0
+    c.scales[page, 0, 0] = 127
+    g = torch.Generator(device=device).manual_seed(3)
+    q = torch.full((n, 4, 64), nats / 8, device=device) + 0.02 * torch.randn(n, 4, 64, device=device, generator=g)
+    check_attention(c, [n], 4, dtype, q=q.to(dtype))
+
+
+@pytest.mark.parametrize("news", [[1, 1, 1], [2, 33, 1]])
+def test_attention_scales_of_q(news):
+    """Rows of q from 2^-100 to 2^60 and zero rows; negative and zero sm_scale."""
+    device = dev()
+    c = ref.Cache([100, 90, 70], 1, 128, device, seed=10)
+    t = sum(news)
+    g = torch.Generator(device=device).manual_seed(3)
+    q = torch.randn(t, 4, 128, device=device, generator=g)
+    e = torch.tensor([-100.0, 0.0, -20.0, 3.0], device=device)
+    q = (q * torch.exp2(e)[None, :, None]).to(BF16)
+    q[0, 1] = 0
+    for s in (0.125, -0.07, 0.0):
+        check_attention(c, news, 4, BF16, q=q, sm_scale=s)
+    check_attention(c, news, 4, BF16, q=(q.float() * 2.0 ** 60).to(BF16), sm_scale=2.0 ** -63)
+
+
+@pytest.mark.parametrize("news", [[1, 1], [3, 40]])
+def test_attention_nonfinite_queries_stay_in_their_rows(news):
+    device = dev()
+    c = ref.Cache([100, 200], 1, 128, device, seed=11)
+    q = torch.randn(sum(news), 4, 128, device=device).to(BF16)
+    clean = check_attention(c, news, 4, BF16, q=q)[1:]
+    bad = q.clone()
+    bad[0, 1, 5], bad[-1, 2, 0] = math.nan, math.inf
+    out, lse = kv.attention_gqa8(bad, c.pool, c.scales, c.page_table, c.seq_lens, ints(ref.cu_of(news), device),
+                                 max(news), 128 ** -0.5)
+    for t, h in ((0, 1), (q.shape[0] - 1, 2)):
+        assert out[t, h].isnan().all() and lse[t, h].isnan()
+        out[t, h], lse[t, h] = clean[0][t, h], clean[1][t, h]
+    assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
+
+
+def test_attention_strided_queries_and_behind_the_last_request():
+    device = dev()
+    c = ref.Cache([100, 40], 2, 128, device, seed=12)
+    x = torch.randn(9, 3, 4, 128, device=device).to(BF16)
+    check_attention(c, [2, 5], 4, BF16, q=x[:, 1])               # two rows behind the last
+    y = torch.randn(4, 50, 128, device=device).to(BF16).transpose(0, 1)
+    check_attention(c, [40, 10], 4, BF16, q=y)                   # head-major
+
+
+@pytest.mark.parametrize("dtype,n,window", [(BF16, 1, 0), (F16, 3, 0), (BF16, 100, 0), (BF16, 2, 5000)])
+def test_attention_long_contexts(dtype, n, window):
+    c = ref.Cache([30011, 9, 16384], 2, 128, dev(), seed=13)
+    assert check_attention(c, [n, min(n, 9), n], 8, dtype, window=window)[0] == 0
+
+
+def test_attention_many_requests():
+    lens = [(i * 37) % 400 for i in range(300)]
+    c = ref.Cache(lens, 1, 64, dev(), seed=14)
+    check_attention(c, [min(1, n) for n in lens], 4, BF16)
+
+
+def test_attention_mixed_batch():
+    """Prompt chunks and single tokens in one call."""
+    news = [200, 1, 1, 0, 77, 1, 1, 129]
+    lens = [200, 1000, 64, 50, 600, 1, 333, 500]
+    c = ref.Cache(lens, 2, 128, dev(), seed=15)
+    check_attention(c, news, 8, BF16)
+
+
+def test_attention_flags_a_request_beyond_max_new():
+    device = dev()
+    c = ref.Cache([100, 50, 80], 1, 64, device, seed=16)
+    news, cu = [1, 3, 1], ref.cu_of([1, 3, 1])
+    q = torch.randn(5, 2, 64, device=device).to(BF16)
+    err = torch.zeros(1, dtype=torch.int32, device=device)
+    out, lse = (torch.full((5, 2, 64), 3.0, dtype=BF16, device=device), torch.full((5, 2), 3.0, device=device))
+    kv.attention_gqa8(q, c.pool, c.scales, c.page_table, c.seq_lens, ints(cu, device), 1, 0.125, out=out, lse=lse,
+                      dev_err=err)
+    assert int(err.item()) == kv.DEV_BAD_LENGTH
+    whole = check_attention(c, news, 2, BF16, q=q, sm_scale=0.125)
+    for t in (0, 4):
+        assert torch.equal(out[t], whole[1][t]) and torch.equal(lse[t], whole[2][t])
+    assert (out[1:4] == 3).all() and (lse[1:4] == 3).all()
+
+
+# ---------------------------------------------------------------------------
+# together, streams, graphs
+# ---------------------------------------------------------------------------
+def serve(device, steps, d=128, hkv=2, hq=8, dtype=BF16, graph=False):
+    """A prompt chunk of three sessions, then `steps` single tokens each: the
+    attention's outputs and the K, V written."""
+    g = torch.Generator(device=device).manual_seed(77)
+    prompts, B = [100, 63, 1], 3
+    width = 4
+    pool = torch.randint(0, 256, (B * width, hkv, 2, 64, d), dtype=torch.uint8, device=device, generator=g)
+    scales = torch.full((B * width, hkv, 2), 127, dtype=torch.uint8, device=device)
+    table = torch.randperm(B * width, device=device, generator=g).to(torch.int32).view(B, width)
+    cu, lens = ints(ref.cu_of(prompts), device), ints(prompts, device)
+    x = torch.randn(sum(prompts), hq + 2 * hkv, d, device=device, generator=g).to(dtype)
+    kv.append_gqa8(x[:, hq:hq + hkv], x[:, hq + hkv:], cu, table, lens, pool, scales)
+    outs = [kv.attention_gqa8(x[:, :hq], pool, scales, table, lens, cu, max(prompts), d ** -0.5)[0]]
+    cu1 = ints([0, 1, 2, 3], device)
+    tokens = torch.randn(steps, B, hq + 2 * hkv, d, device=device, generator=g).to(dtype)
+    buf = torch.empty_like(tokens[0])
+
+    def step():
+        lens.add_(1)
+        kv.append_gqa8(buf[:, hq:hq + hkv], buf[:, hq + hkv:], cu1, table, lens, pool, scales)
+        return kv.attention_gqa8(buf[:, :hq], pool, scales, table, lens, cu1, 1, d ** -0.5)[0]
+
+    if graph:
+        warm = (lens.clone(), pool.clone(), scales.clone())
+        buf.copy_(tokens[0])
+        step()
+        torch.cuda.synchronize()
+        for t, w in zip((lens, pool, scales), warm):
+            t.copy_(w)
+        captured = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(captured):
+            kept = step()
+    for i in range(steps):
+        buf.copy_(tokens[i])
+        if graph:
+            captured.replay()
+            outs.append(kept.clone())
+        else:
+            outs.append(step())
+    return outs, x, tokens, pool, scales
+
+
+def test_serving_run_against_the_unquantized_attention():
+    """Prompt, then 70 steps (pages fill and new ones begin).  Against
+    attention over the values as they were given: each k, v element is off by
+    at most 2^-4 of itself, or 2^-10 of its page's largest (subnormal codes),
+    twice where its page's exponent rose; |q.k| sums of 128 random signs keep
+    the scores within 0.15 of theirs (6 standard deviations of 128 products
+    each off by 2^-4 / sqrt(3) at most), so out within exp(0.3) - 1 + 2^-3 of
+    the softmax mean of |v| -- and far closer on average."""
+    device = dev()
+    outs, x, tokens, pool, scales = serve(device, 70)
+    hq, hkv, d, prompts = 8, 2, 128, [100, 63, 1]
+    cu = ref.cu_of(prompts)
+    for b in range(3):
+        ks = torch.cat([x[cu[b]:cu[b + 1], hq:hq + hkv], tokens[:, b, hq:hq + hkv]]).double()
+        vs = torch.cat([x[cu[b]:cu[b + 1], hq + hkv:], tokens[:, b, hq + hkv:]]).double()
+        qs = torch.cat([x[cu[b]:cu[b + 1], :hq], tokens[:, b, :hq]]).double()
+        got = torch.cat([outs[0][cu[b]:cu[b + 1]]] + [o[b:b + 1] for o in outs[1:]]).double()
+        n = ks.shape[0]
+        ok = torch.ones(n, n, dtype=torch.bool, device=device).tril()
+        for h in range(hq):
+            s = (qs[:, h] @ ks[:, h // 4].T * d ** -0.5).masked_fill(~ok, -math.inf)
+            p = torch.softmax(s, -1)
+            want, mean = p @ vs[:, h // 4], p @ vs[:, h // 4].abs()
+            assert ((got[:, h] - want).abs() <= 0.48 * mean + 0.01).all()
+            assert float((got[:, h] - want).norm() / want.norm()) < 0.1
+
+
+def test_serving_run_captured_in_a_graph_gives_the_same_bits():
+    device = dev()
+    a, b = serve(device, 70), serve(device, 70, graph=True)
+    for x, y in zip(a[0], b[0]):
+        assert torch.equal(x, y)
+    assert torch.equal(a[3], b[3]) and torch.equal(a[4], b[4])
+
+
+def test_calls_on_two_streams_do_not_share_anything():
+    """Two calls in flight on two streams, each split over the SMs."""
+    device = dev()
+    cs = [ref.Cache([20000], 2, 128, device, seed=s) for s in (20, 21)]
+    q = torch.randn(1, 8, 128, device=device).to(BF16)
+    args = [(q, c.pool, c.scales, c.page_table, c.seq_lens, ints([0, 1], device), 1, 0.09) for c in cs]
+    want = [kv.attention_gqa8(*a) for a in args]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(kv.attention_gqa8(*args[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out, lse in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_two_graphs_replayed_at_once():
+    device = dev()
+    c = ref.Cache([20000, 300], 2, 128, device, seed=22)
+    qs = [torch.randn(2, 8, 128, device=device).to(BF16) for _ in range(2)]
+    args = (c.pool, c.scales, c.page_table, c.seq_lens, ints([0, 1, 2], device), 1, 0.09)
+    want = [kv.attention_gqa8(q, *args) for q in qs]
+    graphs, got = [], []
+    for q in qs:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            got.append(kv.attention_gqa8(q, *args))
+        graphs.append(gr)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for gr, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                gr.replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(got[i][0], want[i][0]) and torch.equal(got[i][1], want[i][1])
+
+
+def test_own_workspace_and_its_refusal():
+    device = dev()
+    c = ref.Cache([20000], 2, 128, device, seed=23)
+    q = torch.randn(1, 8, 128, device=device).to(BF16)
+    args = (q, c.pool, c.scales, c.page_table, c.seq_lens, ints([0, 1], device), 1, 0.09)
+    want = kv.attention_gqa8(*args)
+    n = kv.attention_gqa8_workspace(1, 1, 1, 8, 2, 128)
+    ws = torch.full((max(n, 1),), 255, dtype=torch.uint8, device=device)
+    got = kv.attention_gqa8(*args, workspace=ws)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    if n:
+        with pytest.raises(kv.Kv4Error) as e:
+            kv.attention_gqa8(*args, workspace=ws[:n - 16])
+        assert e.value.status == 5
