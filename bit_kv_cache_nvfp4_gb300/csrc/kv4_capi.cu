@@ -938,6 +938,7 @@ size_t kv4_noalloc_scratch_bytes(void) { return kStaticScratchBytes; }
 // ---------------------------------------------------------------------------
 namespace {
 
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned128(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 127u) == 0; }
 
@@ -952,7 +953,7 @@ kv4_status check_gqa8(int64_t n_tokens, int heads, int Hkv, int D, int B, int dt
   if (n_tokens > INT32_MAX || n_tokens * heads > (1LL << 40) / D) return KV4_ERR_INVALID_ARG;
   if (num_pages < 0 || num_pages >= INT32_MAX || pt_stride < 1 || pt_stride > INT32_MAX)
     return KV4_ERR_INVALID_ARG;
-  if (num_pages > INT64_MAX / (2LL * KV4_PAGE * D) / Hkv) return KV4_ERR_INVALID_ARG;
+  if (num_pages * 2 * Hkv >= INT32_MAX) return KV4_ERR_INVALID_ARG;      // blocks of the pool
   return KV4_OK;
 }
 
@@ -1083,7 +1084,7 @@ kv4_status kv4_attention_gqa8(const void* q_dev, int64_t q_token_stride, int64_t
       !out_dev || !lse_dev)
     return KV4_ERR_INVALID_ARG;
   if (!strides_ok(q_dev, q_token_stride, q_head_stride, Hq, D) || !aligned128(pool_dev) ||
-      !aligned16(out_dev) || !aligned4(lse_dev) || !aligned4(cu_seqlens_dev) ||
+      !aligned16(out_dev) || !aligned4(lse_dev) || !aligned2(scales_dev) || !aligned4(cu_seqlens_dev) ||
       !aligned4(page_table_dev) || !aligned4(seq_lens_dev) || !aligned4(dev_err))
     return KV4_ERR_INVALID_ARG;
   int sms = 0;

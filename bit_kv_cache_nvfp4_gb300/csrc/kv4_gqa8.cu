@@ -13,8 +13,7 @@
 // block is the unit whose maximum the write needs, and 2 x 64 x D values
 // (32 KB of inputs at D = 128) fit its threads' registers, so the inputs are
 // read once.
-#include "kv4_device.cuh"
-#include "kv4_launch.h"
+#include "kv4_gqa8_device.cuh"
 
 namespace kv4 {
 namespace {
@@ -119,9 +118,6 @@ __device__ __forceinline__ void decode16(const uint4& c, float* x) {
   }
 }
 
-__device__ __forceinline__ float pow2f(int e) {     // e in [-126, 127]
-  return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-}
 // Least e with amax <= 448 * 2^e = 1.75 * 2^(e + 8), from the bits of a finite
 // fp32 amax; [-48, 48].
 __device__ __forceinline__ int block_exponent(uint32_t amax_bits) {

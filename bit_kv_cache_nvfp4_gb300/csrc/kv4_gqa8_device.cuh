@@ -1,0 +1,165 @@
+// kv4_gqa8_device.cuh -- helpers of the attention over the 8-bit grouped-query
+// cache: TMA loads of cache pages, the FP8 tensor-core product, and the
+// splitting of 16-bit operands into E4M3 terms.
+#pragma once
+
+#include <cuda.h>
+
+#include "kv4_device.cuh"
+#include "kv4_launch.h"
+
+namespace kv4 {
+
+__device__ __forceinline__ float pow2f(int e) {     // e in [-126, 127]
+  return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+}
+
+// 64 rows of one (page, head, side) -> shared memory, swizzled; box index
+// `block` past the tensor gives zeros.  Completes on the mbarrier.
+__device__ __forceinline__ void tma_load_block(uint32_t dst, const CUtensorMap* map, int block,
+                                               uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(0), "r"(block), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// Instruction descriptor for kind::f8f6f4: D fp32, A and B E4M3, dense.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f8kind(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// f16x2 -> two E4M3 bytes, round half to even, saturating; and back (exact).
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h2) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+  return r;
+}
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+
+// Two values (f16x2, magnitudes up to 448) as NT E4M3 terms each:
+// x = t0 + t1 / 16 + t2 / 256, every term rounded to nearest (4 significant
+// bits).  The differences are exact in f16: after t0 at most 7 of the 11 bits
+// are left, after t1 at most 3.  Two terms hold 8 bits (all of a bf16 value),
+// three hold 11; a value below 2^-6 keeps 2^-10 / 16 (2^-10 / 256) of absolute
+// accuracy.
+template <int NT>
+__device__ __forceinline__ void split_e4m3(uint32_t x, uint32_t (&t)[NT]) {
+  t[0] = e4m3x2_of_f16x2(x);
+#pragma unroll
+  for (int i = 1; i < NT; ++i) {
+    const __half2 r = __hsub2(bits_h2(x), bits_h2(e4m3x2_to_f16x2(t[i - 1])));
+    x = h2_bits(__hmul2(r, __half2half2(__float2half(16.0f))));
+    t[i] = e4m3x2_of_f16x2(x);
+  }
+}
+
+// Largest value over the warp (NaN only where every lane holds one).
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
+  return x;
+}
+
+// ---------------------------------------------------------------------------
+// The work list.  A request's rows are r = i * G + g (new token i, head g of
+// the group); `rows` consecutive ones, of one kv head, are an item, which
+// walks its keys in tiles of 128 (tile t: keys 128 t .. 128 t + 127, two
+// pages).  Items are ordered by request, row group, kv head; each counts for
+// its number of tiles (one where it has none: its rows are still written), and
+// every block takes an equal share of the whole, found from the lengths on the
+// device.  An item of at most kWhole tiles stays with the block that its first
+// tile falls to; longer ones are cut at the shares' borders and merged after.
+// ---------------------------------------------------------------------------
+struct Gqa8Request {
+  int cu0;          // first flat row
+  int n;            // new tokens (0: not of this kernel)
+  int pos0;         // position of the first one (may be negative)
+  int held;         // tokens that the page table can name, of len
+};
+struct Gqa8Span {
+  int klo, khi;     // keys that some row of the item sees
+  int t0, nt;       // first tile, tiles
+};
+__device__ __forceinline__ Gqa8Request gqa8_request(const Gqa8AttnArgs& a, int b, int min_rows,
+                                                    int max_rows, bool report) {
+  Gqa8Request q{0, 0, 0, 0};
+  if (b >= a.B) return q;
+  const int T = static_cast<int>(a.n_tokens);
+  const int c0 = min(max(__ldg(a.cu + b), 0), T), c1 = min(max(__ldg(a.cu + b + 1), 0), T);
+  const int len = max(__ldg(a.lens + b), 0);
+  if (c1 <= c0) return q;
+  if (c1 - c0 > a.max_new) {
+    if (report) flag_error(a.dev_err, kDevBadLength);
+    return q;
+  }
+  const int64_t rows = static_cast<int64_t>(c1 - c0) * (a.Hq / a.Hkv);
+  if (rows < min_rows || rows > max_rows) return q;
+  const int64_t cap = a.pt_stride << 6;
+  q.cu0 = c0;
+  q.n = c1 - c0;
+  q.pos0 = len - q.n;
+  q.held = len < cap ? len : static_cast<int>(cap);
+  if (report && q.held < len) flag_error(a.dev_err, kDevBadPage);
+  return q;
+}
+// Keys of rows [r0, r1) of a request.
+__device__ __forceinline__ Gqa8Span gqa8_span(const Gqa8AttnArgs& a, const Gqa8Request& q, int G,
+                                              int r0, int r1) {
+  Gqa8Span s;
+  const int64_t first = static_cast<int64_t>(q.pos0) + r0 / G, last = static_cast<int64_t>(q.pos0) + (r1 - 1) / G;
+  int64_t lo = a.window > 0 ? first - a.window + 1 : 0;
+  if (lo < 0) lo = 0;
+  int64_t hi = last + 1 < q.held ? last + 1 : q.held;
+  if (hi < lo) hi = lo;
+  s.klo = static_cast<int>(lo);
+  s.khi = static_cast<int>(hi);
+  s.t0 = s.klo >> 7;
+  s.nt = hi > lo ? ((s.khi - 1) >> 7) + 1 - s.t0 : 0;
+  return s;
+}
+__device__ __forceinline__ int64_t gqa8_units(const Gqa8AttnArgs& a, const Gqa8Request& q, int G,
+                                              int rows) {
+  int64_t u = 0;
+  const int R = q.n * G;
+  for (int r0 = 0; r0 < R; r0 += rows)
+    u += max(gqa8_span(a, q, G, r0, min(R, r0 + rows)).nt, 1);
+  return u * a.Hkv;
+}
+
+struct Gqa8Item {
+  int b;                     // request, -1: no more work
+  int h;
+  int cu0, pos0;             // of the request
+  int r0, nrows;
+  int klo, khi;
+  int t_begin, t_end;        // tiles that this block walks
+  int slot;                  // partial slot, or -1: the rows are finished here
+};
+
+// What the merge kernel reads of a block's item that other blocks continue.
+struct Gqa8Tail {
+  int parts;                 // 0: none; else pieces, in this block and the next parts - 1
+  int cu0, h, r0, nrows, pad[3];
+};
+
+}  // namespace kv4

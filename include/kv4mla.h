@@ -496,7 +496,8 @@ size_t kv4_noalloc_scratch_bytes(void);
  * layout is this project's.
  *   pool_dev        uint8 [num_pages, Hkv, 2, 64, D]: E4M3 codes, K then V of
  *                   a page and head; 128-byte aligned
- *   scales_dev      uint8 [num_pages, Hkv, 2]: value = code * 2^(byte - 127)
+ *   scales_dev      uint8 [num_pages, Hkv, 2]: value = code * 2^(byte - 127);
+ *                   2-byte aligned
  *   page_table_dev  int32 [B, pt_stride]: physical page of each logical page;
  *                   page_size must be 64
  *   seq_lens_dev    int32 [B]: tokens of each request, its new ones included
@@ -507,7 +508,7 @@ size_t kv4_noalloc_scratch_bytes(void);
  *                   neither read nor written
  *   dtype           KV4_BF16 or KV4_F16, of k, v, q, out and the read-back
  *   Hkv, D          Hkv >= 1; D = 64 or 128
- * Sizes: n_tokens * heads * D < 2^40, B <= 65535, num_pages < 2^31 - 1.
+ * Sizes: n_tokens * heads * D < 2^40, B <= 65535, 2 Hkv num_pages < 2^31 - 1.
  * Inputs are strided (in elements, multiples of 8; base 16-byte aligned), so
  * slices of a fused projection's output need no copy; outputs are contiguous.
  * A page index past the table, a negative entry or one >= num_pages raises

@@ -448,3 +448,24 @@ def test_own_workspace_and_its_refusal():
         with pytest.raises(kv.Kv4Error) as e:
             kv.attention_gqa8(*args, workspace=ws[:n - 16])
         assert e.value.status == 5
+
+
+def test_attention_reports_a_wait_that_runs_out():
+    """A wait on a barrier that nothing arrives on gives up after its limit:
+    KV4_DEV_TIMEOUT, and the call ends."""
+    device = dev()
+    c = ref.Cache([1000, 30], 1, 128, device, seed=24)
+    for n in (1, 30):
+        q = torch.randn(2 * n, 4, 128, device=device).to(BF16)
+        args = (q, c.pool, c.scales, c.page_table, c.seq_lens, ints([0, n, 2 * n], device), n, 0.09)
+        want = kv.attention_gqa8(*args)
+        err = torch.zeros(1, dtype=torch.int32, device=device)
+        kv.set_wait_limit(2_000_000, 1)
+        try:
+            kv.attention_gqa8(*args, dev_err=err)
+            torch.cuda.synchronize()
+        finally:
+            kv.set_wait_limit()
+        assert int(err.item()) == kv.DEV_TIMEOUT
+        got = kv.attention_gqa8(*args)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
