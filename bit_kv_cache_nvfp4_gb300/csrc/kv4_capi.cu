@@ -1057,6 +1057,7 @@ kv4_status kv4_attention_gqa8_plan(int B, int max_new, int64_t n_tokens, int Hq,
   const kv4_status shape = check_gqa8(n_tokens, Hq, Hkv, D, B, KV4_BF16, KV4_PAGE, 0, 1);
   if (shape != KV4_OK) return shape;
   if (Hq / Hkv > 128) return KV4_ERR_UNSUPPORTED;
+  if (n_tokens * (Hq / Hkv) > INT32_MAX) return KV4_ERR_INVALID_ARG;     // rows of a request
   int sms = 0;
   const kv4_status st = device_info(&sms);
   if (st != KV4_OK) return st;
@@ -1078,6 +1079,7 @@ kv4_status kv4_attention_gqa8(const void* q_dev, int64_t q_token_stride, int64_t
   const kv4_status shape = check_gqa8(n_tokens, Hq, Hkv, D, B, dtype, page_size, num_pages, pt_stride);
   if (shape != KV4_OK) return shape;
   if (Hq / Hkv > 128) return KV4_ERR_UNSUPPORTED;
+  if (n_tokens * (Hq / Hkv) > INT32_MAX) return KV4_ERR_INVALID_ARG;     // rows of a request
   if (n_tokens == 0 || B == 0) return KV4_OK;
   if (max_new == 0) return KV4_ERR_INVALID_ARG;
   if (!q_dev || !cu_seqlens_dev || !pool_dev || !scales_dev || !page_table_dev || !seq_lens_dev ||

@@ -17,8 +17,6 @@
 namespace kv4 {
 namespace {
 
-constexpr int kWhole = 4;      // items of at most so many tiles are never cut
-
 // ---------------------------------------------------------------------------
 // Few rows: single tokens and short drafts
 // ---------------------------------------------------------------------------
@@ -76,8 +74,6 @@ struct FewSmall {
 static_assert(sizeof(FewSmall) <= 4096 && offsetof(FewSmall, red) % 16 == 0 &&
                   offsetof(FewSmall, stash) % 8 == 0,
               "FewSmall");
-constexpr int kMasked = 0x7FFF7FFF;
-constexpr float kLowest = -3e38f;
 
 template <int D, int RP, int NT>
 __global__ void __launch_bounds__(256, FewCfg<D, RP, NT>::kCtas)
@@ -154,12 +150,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
 
   if (warp == 0) {
     // ==== work list and loads ====
-    const int64_t total = static_cast<int64_t>(sm.total);
-    const int blocks = gridDim.x, me = blockIdx.x;
-    const int64_t per = max((total + blocks - 1) / blocks, static_cast<int64_t>(kWhole));
-    const int64_t u0 = me * per, u1 = min(u0 + per, total);
     uint32_t n_items = 0, n_tiles = 0;
-    bool tail = false;
     auto publish = [&](const Gqa8Item& it) {
       const int s = n_items & 3;
       wait(sm.item_empty[s], ((n_items >> 2) & 1) ^ 1);
@@ -171,22 +162,8 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
     };
     auto load = [&](const Gqa8Item& it) {
       for (int t = it.t_begin; t < it.t_end; t += 16) {
-        // lane l: page l of the next 16 tiles
-        const int64_t page = 2 * static_cast<int64_t>(t) + lane;
-        int block = -1, ex = kMasked;
-        if ((page >> 1) < it.t_end && (page << 6) < it.khi && (page << 6) + 64 > it.klo) {
-          const int phys = __ldg(a.page_table + it.b * a.pt_stride + page);
-          if (phys < 0 || phys >= a.num_pages) {
-            flag_error(a.dev_err, kDevBadPage);
-          } else {
-            block = phys * a.Hkv + it.h;
-            const uint32_t e2 = __ldg(reinterpret_cast<const uint16_t*>(a.scales) + block);
-            const int ek = min(max(static_cast<int>(e2 & 0xFF) - 127, -100), 100);
-            const int ev = min(max(static_cast<int>(e2 >> 8) - 127, -100), 100);
-            ex = (ek & 0xFFFF) | (ev << 16);
-          }
-        }
-        if (block < 0) block = a.num_pages * a.Hkv;           // past the tensor: zeros
+        int block, ex;
+        gqa8_pages(a, it, t, lane, block, ex);
         const int nt = min(16, it.t_end - t);
         for (int i = 0; i < nt; ++i, ++n_tiles) {
           const int b0 = __shfl_sync(0xFFFFFFFFu, block, 2 * i), b1 = __shfl_sync(0xFFFFFFFFu, block, 2 * i + 1);
@@ -207,66 +184,11 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
         }
       }
     };
-    int64_t acc = 0;
-    for (int base = 0; base < a.B && acc < u1 && u0 < u1; base += 32) {
-      const Gqa8Request q = gqa8_request(a, base + lane, 1, max_rows, false);
-      const int64_t units = gqa8_units(a, q, G, RP);
-      int64_t end = units;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, end, off);
-        if (lane >= off) end += v;
-      }
-      end += acc;
-      const int64_t chunk_end = __shfl_sync(0xFFFFFFFFu, end, 31);
-      uint32_t todo = __ballot_sync(0xFFFFFFFFu, units > 0 && end > u0 && end - units < u1);
-      for (; todo != 0; todo &= todo - 1) {
-        const int l = __ffs(todo) - 1;
-        Gqa8Request r;
-        r.cu0 = __shfl_sync(0xFFFFFFFFu, q.cu0, l);
-        r.n = __shfl_sync(0xFFFFFFFFu, q.n, l);
-        r.pos0 = __shfl_sync(0xFFFFFFFFu, q.pos0, l);
-        r.held = __shfl_sync(0xFFFFFFFFu, q.held, l);
-        int64_t at = __shfl_sync(0xFFFFFFFFu, end - units, l);
-        const int R = r.n * G;
-        for (int r0 = 0; r0 < R && at < u1; r0 += RP) {
-          const Gqa8Span sp = gqa8_span(a, r, G, r0, min(R, r0 + RP));
-          const int64_t w = max(sp.nt, 1);
-          if (at + w * a.Hkv <= u0) {
-            at += w * a.Hkv;
-            continue;
-          }
-          const int h0 = at < u0 ? static_cast<int>((u0 - at) / w) : 0;
-          int64_t begin = at + h0 * w;
-          for (int h = h0; h < a.Hkv && begin < u1; ++h, begin += w) {
-            int64_t tb = 0, te = sp.nt;
-            int slot = -1;
-            if (w <= kWhole) {
-              if (begin < u0) continue;                       // the block before has it whole
-            } else {
-              tb = max(u0 - begin, static_cast<int64_t>(0));
-              te = min(u1 - begin, w);
-              if (tb > 0) {
-                slot = 2 * me;
-              } else if (te < w) {
-                slot = 2 * me + 1;
-                tail = true;
-                if (lane == 0)
-                  tails[me] = Gqa8Tail{static_cast<int>((begin + w - 1) / per) - me + 1, r.cu0, h, r0, min(RP, R - r0), {}};
-              }
-            }
-            const Gqa8Item it{base + l, h, r.cu0, r.pos0, r0, min(RP, R - r0), sp.klo, sp.khi,
-                              sp.t0 + static_cast<int>(tb), sp.t0 + static_cast<int>(te), slot};
-            publish(it);
-            load(it);
-          }
-          at += w * a.Hkv;
-        }
-      }
-      acc = chunk_end;
-    }
+    gqa8_walk(a, 1, max_rows, RP, static_cast<int64_t>(sm.total), tails, lane, [&](const Gqa8Item& it) {
+      publish(it);
+      load(it);
+    });
     publish(Gqa8Item{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, -1});
-    if (lane == 0 && !tail) tails[me].parts = 0;
     // every load and every product's signal lands before the block's shared
     // memory goes away
     for (uint32_t i = n_tiles > ST ? n_tiles - ST : 0; i < n_tiles; ++i)
@@ -465,11 +387,10 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
         const int ex = sm.exps[st][key >> 6], ex2 = sm.exps[st][(key >> 6) ^ 1];
         const int at = t * kTileKeys + key;               // this thread's key
         const bool live = ex != kMasked && at >= it.klo && at < it.khi;
-        const int ek = static_cast<int16_t>(ex & 0xFFFF), ev = ex == kMasked ? -100 : ex >> 16;
-        const int evm = max(ev, ex2 == kMasked ? -100 : ex2 >> 16);
+        const int ek = static_cast<int16_t>(ex & 0xFFFF), ev = ex == kMasked ? kGqa8ExpMin : ex >> 16;
+        const int evm = max(ev, ex2 == kMasked ? kGqa8ExpMin : ex2 >> 16);
         const float kf = live ? pow2f(ek) : 0.0f;
-        const int dv = ev - evm + 8;
-        const float vf = dv < -126 ? 0.0f : pow2f(dv);
+        const float vf = pow2f(ev - evm + 8);
         const bool edge = (t + 1) * static_cast<int64_t>(kTileKeys) > min(it.khi, pos_first + 1) ||
                           t * kTileKeys < it.klo ||
                           (a.window > 0 && t * static_cast<int64_t>(kTileKeys) <= static_cast<int64_t>(pos_last) - a.window);
@@ -597,12 +518,505 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
 }
 
 // ---------------------------------------------------------------------------
-// The pieces of items that were cut: block (c, r) joins row r of the item that
-// began in block c of the attention kernel, by log-sum-exp over its pieces in
-// their order.
+// Many rows: prompt chunks
+// ---------------------------------------------------------------------------
+// What bounds this case is the tensor core: 4 D flops a pair of row and key.
+// An item is 256 rows of one kv head, two M = 128 tiles that take turns: while
+// the softmax of one works on its scores, the products of the other run.
+//   S[128 rows x 128 keys] = sum_t Q_t . K^T     kind::f8f6f4, NT terms of q
+//   O[128 rows x D] += P . V                     kind::f16, P from TMEM
+// K goes in as its codes, against q split into E4M3 terms (bf16: two, f16:
+// three; all with the same scale, so that they add up in one accumulator).  V
+// is widened to f16 once per tile by two warps (exact), for P in f16 (2^-11)
+// takes one pass where E4M3 terms would take two and twice the instructions
+// in the softmax, which has the least room to spare.
+// A thread is a row: its 128 scores come from TMEM at once, K's block
+// exponents and the scale of q multiply them, V's are added to the exponent of
+// p, so that p is relative to a running reference of score and V exponent
+// together; a row's reference only moves, and its O in TMEM is only rescaled,
+// when that rises by more than 2^6 (p stays below 2^14, f16's top is 2^16).
+template <int D_, int NT_>
+struct ManyCfg {
+  static constexpr int D = D_, NT = NT_, kRows = 256;
+  static constexpr int kK = kTileKeys * D;                // K or V codes of a tile
+  static constexpr int kV16 = kTileKeys * D * 2;
+  static constexpr int kQ = NT * 128 * D;                 // of one of the two row tiles
+  static constexpr int kKStages = NT == 2 ? 3 : 2, kVStages = 2;
+  static constexpr int kSmall = 2048;
+  static constexpr int kSmem = 2 * kQ + kKStages * kK + kVStages * kK + 2 * kV16 + kSmall + 1024;
+};
+static_assert(ManyCfg<128, 3>::kSmem <= 227 * 1024 && ManyCfg<128, 2>::kSmem <= 227 * 1024, "shared memory");
+constexpr int kManyThreads = 384;
+constexpr uint32_t kSoftmaxRegs = 208, kOtherRegs = 88, kLaunchRegs = 168;
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "register shares draw on the launch's");
+
+struct ManySmall {
+  uint64_t k_full[3], k_empty[3], v8_full[2], v8_empty[2], v_full[2], v_empty[2], item_full[2], item_empty[2],
+      ex_full[8], q_full[2], s_full[2], p_full[2], o_full[2], never;
+  unsigned long long total;
+  uint32_t tmem;
+  int dead;
+  int exps[8][2];
+  Gqa8Item items[2];
+};
+static_assert(sizeof(ManySmall) <= 2048, "ManySmall");
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kManyThreads, 1)
+many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const int min_rows,
+            Gqa8Tail* tails, float* ws_lse, float* ws_o) {
+  using C = ManyCfg<D, NT>;
+  constexpr int KS = C::kKStages, VS = C::kVStages;
+  constexpr int kSlab = kTileKeys * 128;                  // 64 f16 columns of V
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* const q_s = smem;
+  uint8_t* const k_s = q_s + 2 * C::kQ;
+  uint8_t* const v8_s = k_s + KS * C::kK;
+  uint8_t* const v_s = v8_s + VS * C::kK;
+  ManySmall& sm = *reinterpret_cast<ManySmall*>(v_s + 2 * C::kV16);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.Hq / a.Hkv;
+  constexpr int kAll = 0x7FFFFFFF;
+
+  if (tid == 0) {
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(smem_addr(&sm.k_full[i]), 1);
+      mbar_init(smem_addr(&sm.k_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sm.v8_full[i]), 1);
+      mbar_init(smem_addr(&sm.v8_empty[i]), 2);
+      mbar_init(smem_addr(&sm.v_full[i]), 2);
+      mbar_init(smem_addr(&sm.v_empty[i]), 1);
+      mbar_init(smem_addr(&sm.item_full[i]), 1);
+      mbar_init(smem_addr(&sm.item_empty[i]), 11);        // the product's lane, 2 + 8 warps
+      mbar_init(smem_addr(&sm.q_full[i]), 4);
+      mbar_init(smem_addr(&sm.s_full[i]), 1);
+      mbar_init(smem_addr(&sm.p_full[i]), 4);
+      mbar_init(smem_addr(&sm.o_full[i]), 1);
+    }
+    for (int i = 0; i < 8; ++i) mbar_init(smem_addr(&sm.ex_full[i]), 1);
+    mbar_init(smem_addr(&sm.never), 1);
+    sm.total = 0;
+    sm.dead = 0;
+    fence_mbar_init();
+    tma_prefetch_map(&map);
+  }
+  if (warp == 1) tmem_alloc(smem_addr(&sm.tmem), 512);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  __syncthreads();
+  {
+    int64_t u = 0;
+    for (int b = tid; b < a.B; b += kManyThreads)
+      u += gqa8_units(a, gqa8_request(a, b, min_rows, kAll, blockIdx.x == 0 && min_rows == 1), G, C::kRows);
+    if (u > 0) atomicAdd(&sm.total, static_cast<unsigned long long>(u));
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = sm.tmem;                          // S/P of the row tiles, then O
+  volatile int* dead = &sm.dead;
+  auto wait = [&](uint64_t& bar, uint32_t parity) {
+    if (mbar_try_wait(smem_addr(&bar), parity)) return;
+    if (*dead) return;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait_suspend(smem_addr(&bar), parity, 20000u)) {
+      if (*dead) return;
+      if (global_timer_ns() - t0 > a.timeout_ns) {
+        *dead = 1;
+        flag_error(a.dev_err, kDevTimeout);
+        return;
+      }
+    }
+  };
+
+  if (warp < 4) {
+    setmaxnreg_dec<kOtherRegs>();
+    if (warp == 0) {
+      // ==== work list and loads ====
+      uint32_t n_items = 0, n_tiles = 0;
+      auto publish = [&](const Gqa8Item& it) {
+        const int s = n_items & 1;
+        wait(sm.item_empty[s], ((n_items >> 1) & 1) ^ 1);
+        if (lane == 0) {
+          sm.items[s] = it;
+          mbar_arrive(smem_addr(&sm.item_full[s]));
+        }
+        ++n_items;
+      };
+      auto load = [&](const Gqa8Item& it) {
+        for (int t = it.t_begin; t < it.t_end; t += 16) {
+          int block, ex;
+          gqa8_pages(a, it, t, lane, block, ex);
+          const int nt = min(16, it.t_end - t);
+          for (int i = 0; i < nt; ++i, ++n_tiles) {
+            const int b0 = __shfl_sync(0xFFFFFFFFu, block, 2 * i), b1 = __shfl_sync(0xFFFFFFFFu, block, 2 * i + 1);
+            const int e0 = __shfl_sync(0xFFFFFFFFu, ex, 2 * i), e1 = __shfl_sync(0xFFFFFFFFu, ex, 2 * i + 1);
+            const int ks = n_tiles % KS, vs = n_tiles % VS;
+            wait(sm.k_empty[ks], ((n_tiles / KS) & 1) ^ 1);
+            if (lane == 0 && !*dead) {
+              // (the softmax of the tile eight before is done: QK of the tile
+              // KS before, which this stage waited for, came after it)
+              sm.exps[n_tiles & 7][0] = e0;
+              sm.exps[n_tiles & 7][1] = e1;
+              mbar_arrive(smem_addr(&sm.ex_full[n_tiles & 7]));
+              const uint32_t bar = smem_addr(&sm.k_full[ks]), dst = smem_addr(k_s + ks * C::kK);
+              mbar_arrive_expect_tx(bar, C::kK);
+              tma_load_block(dst, &map, 2 * b0, bar);
+              tma_load_block(dst + 64 * D, &map, 2 * b1, bar);
+            }
+            __syncwarp();
+            wait(sm.v8_empty[vs], ((n_tiles / VS) & 1) ^ 1);
+            if (lane == 0 && !*dead) {
+              const uint32_t bar = smem_addr(&sm.v8_full[vs]), dst = smem_addr(v8_s + vs * C::kK);
+              mbar_arrive_expect_tx(bar, C::kK);
+              tma_load_block(dst, &map, 2 * b0 + 1, bar);
+              tma_load_block(dst + 64 * D, &map, 2 * b1 + 1, bar);
+            }
+            __syncwarp();
+          }
+        }
+      };
+      gqa8_walk(a, min_rows, kAll, C::kRows, static_cast<int64_t>(sm.total), tails, lane,
+                [&](const Gqa8Item& it) {
+                  publish(it);
+                  load(it);
+                });
+      publish(Gqa8Item{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, -1});
+      // every signal lands before the block's shared memory goes away
+      for (uint32_t i = n_tiles > KS ? n_tiles - KS : 0; i < n_tiles; ++i)
+        wait(sm.k_empty[i % KS], (i / KS) & 1);
+      for (uint32_t i = n_tiles > 2 ? n_tiles - 2 : 0; i < n_tiles; ++i) wait(sm.v_empty[i & 1], (i >> 1) & 1);
+      if (*dead && lane == 0) {
+        for (uint32_t i = n_tiles > KS ? n_tiles - KS : 0; i < n_tiles; ++i)
+          mbar_wait_bounded(smem_addr(&sm.k_full[i % KS]), (i / KS) & 1, 1000000);
+        for (uint32_t i = n_tiles > VS ? n_tiles - VS : 0; i < n_tiles; ++i)
+          mbar_wait_bounded(smem_addr(&sm.v8_full[i % VS]), (i / VS) & 1, 1000000);
+      }
+    } else if (warp == 1) {
+      // ==== products ====
+      if (lane == 0) {
+        constexpr uint32_t kSw = D == 128 ? kSwizzle128 : kSwizzle64;
+        constexpr uint32_t idesc_qk = idesc_e4m3(128, 128, false, false);
+        constexpr uint32_t idesc_pv = idesc_f16(128, D, false, true);
+        uint32_t n_tiles = 0;
+        uint32_t nw[2] = {0, 0}, np[2] = {0, 0};          // items and tiles of each row tile so far
+        auto qk = [&](int qt, uint32_t j) {
+          const uint64_t dk = smem_desc(smem_addr(k_s + (j % KS) * C::kK), 16, 8 * D, kSw);
+          const uint64_t dq = smem_desc(smem_addr(q_s + qt * C::kQ), 16, 8 * D, kSw);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+              mma_f8kind(tmem + qt * 128, dq + ((t * 128 * D) >> 4) + 2 * k, dk + 2 * k, idesc_qk, t + k > 0);
+          mma_commit(smem_addr(&sm.s_full[qt]));
+        };
+        auto pv = [&](int qt, uint32_t j, bool first) {
+          wait(sm.p_full[qt], np[qt] & 1);
+          ++np[qt];
+          tc_fence_after_sync();
+          const uint64_t dv = smem_desc(smem_addr(v_s + (j & 1) * C::kV16), kSlab, 1024, kSwizzle128);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_f16_ts(tmem + 256 + qt * 128, tmem + qt * 128 + 8 * k, dv + ((k * 2048) >> 4), idesc_pv,
+                       !first || k > 0);
+        };
+        for (uint32_t n_items = 0;; ++n_items) {
+          const int s = n_items & 1;
+          wait(sm.item_full[s], (n_items >> 1) & 1);
+          if (*dead) break;
+          const int b = sm.items[s].b, nt = sm.items[s].t_end - sm.items[s].t_begin;
+          const int nq = sm.items[s].nrows > 128 ? 2 : 1;
+          mbar_arrive(smem_addr(&sm.item_empty[s]));
+          if (b < 0) break;
+          if (nt == 0) continue;
+          for (int qt = 0; qt < nq; ++qt) wait(sm.q_full[qt], nw[qt]++ & 1);
+          for (int t = 0; t <= nt; ++t) {
+            const uint32_t j = n_tiles + t;
+            if (t < nt) {
+              wait(sm.k_full[j % KS], (j / KS) & 1);
+              tc_fence_after_sync();
+            }
+            if (t > 0) wait(sm.v_full[(j - 1) & 1], ((j - 1) >> 1) & 1);
+            for (int qt = 0; qt < nq; ++qt) {
+              // P of a row tile lies over its S: the products run in order
+              if (t > 0) pv(qt, j - 1, t == 1);
+              if (t < nt) qk(qt, j);
+              else mma_commit(smem_addr(&sm.o_full[qt]));
+            }
+            if (t > 0) mma_commit(smem_addr(&sm.v_empty[(j - 1) & 1]));
+            if (t < nt) mma_commit(smem_addr(&sm.k_empty[j % KS]));
+          }
+          n_tiles += nt;
+        }
+        if (a.fault_site == 1) wait(sm.never, 0);
+      }
+      __syncwarp();
+    } else {
+      // ==== V to f16 ====
+      uint32_t j = 0;
+      for (uint32_t n_items = 0;; ++n_items) {
+        const int s = n_items & 1;
+        wait(sm.item_full[s], (n_items >> 1) & 1);
+        if (__any_sync(0xFFFFFFFFu, *dead != 0)) break;
+        const int b = sm.items[s].b, t0 = sm.items[s].t_begin, t1 = sm.items[s].t_end;
+        const int klo = sm.items[s].klo, khi = sm.items[s].khi;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
+        if (b < 0) break;
+        for (int t = t0; t < t1; ++t, ++j) {
+          wait(sm.v8_full[j % VS], (j / VS) & 1);
+          wait(sm.v_empty[j & 1], ((j >> 1) & 1) ^ 1);
+          const uint8_t* const src = v8_s + (j % VS) * C::kK;
+          uint8_t* const dst = v_s + (j & 1) * C::kV16;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int row = (warp - 2) * 64 + half * 32 + lane;
+            const int at = t * kTileKeys + row;
+            // a key that no row sees may hold NaN codes, which a weight of
+            // zero would not silence
+            const bool live = at >= klo && at < khi;
+            const int sw8 = D == 128 ? row & 7 : (row >> 1) & 3;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              uint4 w = make_uint4(0, 0, 0, 0);
+              if (live) w = *reinterpret_cast<const uint4*>(src + row * D + ((c ^ sw8) * 16));
+              uint8_t* const o = dst + (c / 4) * kSlab + row * 128;
+              const int i0 = (c % 4) * 2;
+              *reinterpret_cast<uint4*>(o + ((i0 ^ (row & 7)) * 16)) =
+                  make_uint4(e4m3x2_to_f16x2(w.x & 0xFFFFu), e4m3x2_to_f16x2(w.x >> 16),
+                             e4m3x2_to_f16x2(w.y & 0xFFFFu), e4m3x2_to_f16x2(w.y >> 16));
+              *reinterpret_cast<uint4*>(o + (((i0 + 1) ^ (row & 7)) * 16)) =
+                  make_uint4(e4m3x2_to_f16x2(w.z & 0xFFFFu), e4m3x2_to_f16x2(w.z >> 16),
+                             e4m3x2_to_f16x2(w.w & 0xFFFFu), e4m3x2_to_f16x2(w.w >> 16));
+            }
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_addr(&sm.v8_empty[j % VS]));
+            mbar_arrive(smem_addr(&sm.v_full[j & 1]));
+          }
+        }
+      }
+    }
+  } else {
+    // ==== softmax: a thread is a row ====
+    setmaxnreg_inc<kSoftmaxRegs>();
+    const int qt = (warp >> 2) - 1, row = tid & 127;      // of the item: qt * 128 + row
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_tm = tmem + qt * 128 + lanes, o_tm = tmem + 256 + qt * 128 + lanes;
+    uint32_t j = 0, n_mine = 0, n_work = 0;               // tiles of all items, of mine; items of mine
+    for (uint32_t n_items = 0;; ++n_items) {
+      const int s = n_items & 1;
+      wait(sm.item_full[s], (n_items >> 1) & 1);
+      if (__any_sync(0xFFFFFFFFu, *dead != 0)) break;
+      const Gqa8Item it = sm.items[s];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
+      if (it.b < 0) break;
+      const int nt = it.t_end - it.t_begin;
+      if (qt * 128 >= it.nrows) {                         // no second row tile
+        j += nt;
+        continue;
+      }
+      const int r = it.r0 + qt * 128 + row;
+      const bool mine = qt * 128 + row < it.nrows;
+      const int64_t flat = static_cast<int64_t>(it.cu0 + r / G);
+      const int head = it.h * G + r % G;
+      // keys at < hi and >= lo are this row's
+      const int64_t pos = static_cast<int64_t>(it.pos0) + r / G;
+      const int hi = mine ? static_cast<int>(max(min(pos + 1, static_cast<int64_t>(it.khi)), static_cast<int64_t>(0))) : 0;
+      const int lo = a.window > 0 ? static_cast<int>(max(pos - a.window + 1, static_cast<int64_t>(0))) : 0;
+      bool odd = false;
+      float qf = 0.0f;
+      if (nt > 0) {
+        // the row of q as NT E4M3 terms, its scale to the score's
+        uint4 w[D / 8];
+        const uint4* g = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + flat * a.q_token_stride +
+                                                        static_cast<int64_t>(head) * a.q_head_stride);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) w[i] = mine ? __ldg(g + i) : make_uint4(0, 0, 0, 0);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float2 f;
+            if (a.f16) f = __half22float2(bits_h2(u[k]));
+            else f = make_float2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xFFFF0000u));
+            m = max(m, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
+          }
+        }
+        odd = m >= 0x7F800000u;
+        const int e = min(max(static_cast<int>(m >> 23) - 135 + ((m & 0x7FFFFFu) > 0x600000u ? 1 : 0), -118), 118);
+        // a negative sm_scale turns q, so that the scores' factor is positive
+        const float f = (odd ? 0.0f : pow2f(-e)) * (a.sm_scale < 0.0f ? -1.0f : 1.0f);
+        qf = fabsf(a.sm_scale) * 1.4426950408889634f * pow2f(e);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t o[NT][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4& v = w[2 * c + (i >> 1)];
+            const uint32_t u0 = (i & 1) ? v.z : v.x, u1 = (i & 1) ? v.w : v.y;
+            uint32_t t0[NT], t1[NT];
+            float2 f0, f1;
+            if (a.f16) {
+              f0 = __half22float2(bits_h2(u0));
+              f1 = __half22float2(bits_h2(u1));
+            } else {
+              f0 = make_float2(__uint_as_float(u0 << 16), __uint_as_float(u0 & 0xFFFF0000u));
+              f1 = make_float2(__uint_as_float(u1 << 16), __uint_as_float(u1 & 0xFFFF0000u));
+            }
+            if (odd) f0 = f1 = make_float2(0.0f, 0.0f);
+            split_e4m3_same<NT>(h2_bits(__floats2half2_rn(f0.x * f, f0.y * f)), t0);
+            split_e4m3_same<NT>(h2_bits(__floats2half2_rn(f1.x * f, f1.y * f)), t1);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) o[t][i] = t0[t] | (t1[t] << 16);
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            *reinterpret_cast<uint4*>(q_s + qt * C::kQ + t * 128 * D + swizzle<D == 128 ? 3 : 2>(row * D + c * 16)) =
+                make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.q_full[qt]));
+      }
+      float mref = kLowest, l = 0.0f;
+      for (int t = it.t_begin; t < it.t_end; ++t, ++j, ++n_mine) {
+        wait(sm.ex_full[j & 7], (j >> 3) & 1);
+        const int e0 = sm.exps[j & 7][0], e1 = sm.exps[j & 7][1];
+        wait(sm.s_full[qt], n_mine & 1);
+        tc_fence_after_sync();
+        float x[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, reinterpret_cast<uint32_t(&)[32]>(x[32 * c]));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_wait_ld32(reinterpret_cast<uint32_t(&)[32]>(x[32 * c]));
+        // keys of this row in the tile: [c0, c1)
+        const int c0 = lo - t * kTileKeys, c1 = hi - t * kTileKeys;
+        if (__any_sync(0xFFFFFFFFu, c0 > 0 || c1 < kTileKeys) || e0 == kMasked || e1 == kMasked) {
+          const int a0 = max(c0, 0), n = max(min(c1, kTileKeys) - a0, 0);
+#pragma unroll
+          for (int c = 0; c < kTileKeys; ++c) {
+            const bool in = static_cast<unsigned>(c - a0) < static_cast<unsigned>(n) &&
+                            (c < 64 ? e0 : e1) != kMasked;
+            x[c] = in ? x[c] : -INFINITY;
+          }
+        }
+        const int ev0 = e0 == kMasked ? kGqa8ExpMin : e0 >> 16, ev1 = e1 == kMasked ? kGqa8ExpMin : e1 >> 16;
+        // (at least 2^-126, so that a masked -inf stays one where the scale is 0)
+        const float f0 = fmaxf(qf * pow2f(e0 == kMasked ? 0 : static_cast<int16_t>(e0 & 0xFFFF)), 0x1p-126f);
+        const float f1 = fmaxf(qf * pow2f(e1 == kMasked ? 0 : static_cast<int16_t>(e1 & 0xFFFF)), 0x1p-126f);
+        float m0 = x[0], m1 = x[64];
+#pragma unroll
+        for (int c = 1; c < 64; ++c) {
+          m0 = fmaxf(m0, x[c]);
+          m1 = fmaxf(m1, x[64 + c]);
+        }
+        const float top = fmaxf(fmaf(m0, f0, static_cast<float>(ev0)), fmaf(m1, f1, static_cast<float>(ev1)));
+        const bool raise = top > mref + 6.0f;
+        if (__any_sync(0xFFFFFFFFu, raise)) {
+          const float to = fmaxf(top, mref), by = fast_exp2(mref - to);
+          mref = to;
+          l *= by;
+          if (t > it.t_begin) {
+            // s_full came behind the last product into this O
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t v[16];
+              tmem_ld16_sync(o_tm + c, v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * by);
+              tmem_st16(o_tm + c, v);
+            }
+          }
+        }
+        const float b0 = static_cast<float>(ev0) - mref + 8.0f, b1 = static_cast<float>(ev1) - mref + 8.0f;
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t p[32];
+          float sa = 0.0f, sb = 0.0f;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            float y0 = fast_exp2(fmaf(x[half * 64 + 2 * c], half ? f1 : f0, half ? b1 : b0));
+            float y1 = fast_exp2(fmaf(x[half * 64 + 2 * c + 1], half ? f1 : f0, half ? b1 : b0));
+            sa += y0;
+            sb += y1;
+            p[c] = h2_bits(__floats2half2_rn(y0, y1));
+          }
+          sum[half] = sa + sb;
+          tmem_st32(s_tm + 32 * half, p);
+        }
+        l = fmaf(sum[0], pow2f(-ev0), fmaf(sum[1], pow2f(-ev1), l));
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[qt]));
+      }
+      if (nt > 0) {
+        wait(sm.o_full[qt], n_work & 1);
+        ++n_work;
+        tc_fence_after_sync();
+      }
+      const float inv = odd && l > 0.0f ? __uint_as_float(0x7FC00000u) : 1.0f / l;
+      const bool some = l > 0.0f || l != l;
+      const float ls = !some ? -INFINITY : odd ? __uint_as_float(0x7FC00000u) : mref - 8.0f + log2f(l);
+      const int64_t part = static_cast<int64_t>(it.slot) * C::kRows + qt * 128 + row;
+      const int64_t orow = flat * a.Hq + head;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        uint32_t v[16];
+        if (nt > 0) tmem_ld16_sync(o_tm + c, v);
+        float y[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = some && nt > 0 ? __uint_as_float(v[i]) * inv : 0.0f;
+        if (!mine) continue;
+        if (it.slot >= 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(ws_o + part * D + c + 4 * i) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+        } else {
+          uint32_t o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (a.f16) {
+              o[i] = h2_bits(__floats2half2_rn(y[2 * i], y[2 * i + 1]));
+            } else {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+              o[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+          }
+          uint4* const dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + c);
+          dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+          dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      }
+      if (mine) {
+        if (it.slot >= 0) ws_lse[part] = ls;
+        else a.lse[orow] = ls * 0.6931471805599453f;
+      }
+      tc_fence_before_sync();
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// The pieces of items that were cut: block (c, y) joins rows y, y + gridDim.y,
+// .. of the item that began in block c of the attention kernel, by log-sum-exp
+// over its pieces in their order.
 // ---------------------------------------------------------------------------
 template <int D>
-__global__ void __launch_bounds__(512) merge_kernel(const Gqa8AttnArgs a, const int RP,
+__global__ void __launch_bounds__(512) merge_kernel(const Gqa8AttnArgs a, const int rows,
                                                     const Gqa8Tail* tails, const float* ws_lse,
                                                     const float* ws_o) {
   grid_dependency_wait();
@@ -610,123 +1024,57 @@ __global__ void __launch_bounds__(512) merge_kernel(const Gqa8AttnArgs a, const 
   constexpr int kGroups = 512 / D;
   __shared__ float part[kGroups][D];
   __shared__ float top, sum;
-  const int c = blockIdx.x, r = blockIdx.y;
+  const int c = blockIdx.x, tid = threadIdx.x, d = tid % D, g = tid / D;
   const Gqa8Tail t = tails[c];
-  if (t.parts == 0 || r >= t.nrows) return;
-  const int tid = threadIdx.x, d = tid % D, g = tid / D;
-  // piece i is slot 2c + 1 for i = 0, else 2 (c + i)
-  auto row_of = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * RP + r; };
-  if (tid < 32) {
-    float m = -INFINITY;
-    bool odd = false;
-    for (int i = tid; i < t.parts; i += 32) {
-      const float x = ws_lse[row_of(i)];
-      odd |= x != x;
-      m = fmaxf(m, x);
+  if (t.parts == 0) return;
+  const int G = a.Hq / a.Hkv;
+  for (int r = blockIdx.y; r < t.nrows; r += gridDim.y) {
+    // piece i is slot 2c + 1 for i = 0, else 2 (c + i)
+    auto row_of = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * rows + r; };
+    if (tid < 32) {
+      float m = -INFINITY;
+      bool odd = false;
+      for (int i = tid; i < t.parts; i += 32) {
+        const float x = ws_lse[row_of(i)];
+        odd |= x != x;
+        m = fmaxf(m, x);
+      }
+      m = warp_max(m);
+      odd = __any_sync(0xFFFFFFFFu, odd);
+      float s = 0.0f;
+      if (m > -INFINITY)
+        for (int i = tid; i < t.parts; i += 32) s += fast_exp2(ws_lse[row_of(i)] - m);
+      s = warp_sum(s);
+      if (tid == 0) {
+        top = m;
+        sum = odd ? __uint_as_float(0x7FC00000u) : s;
+      }
     }
-    m = warp_max(m);
-    odd = __any_sync(0xFFFFFFFFu, odd);
-    float s = 0.0f;
-    if (m > -INFINITY)
-      for (int i = tid; i < t.parts; i += 32) s += fast_exp2(ws_lse[row_of(i)] - m);
-    s = warp_sum(s);
-    if (tid == 0) {
-      top = m;
-      sum = odd ? __uint_as_float(0x7FC00000u) : s;
-    }
-  }
-  __syncthreads();
-  const float m = top, s = sum;
-  float o = 0.0f;
-  if (s != 0.0f) {
+    __syncthreads();
+    const float m = top, s = sum;
+    float o = 0.0f;
+    if (s != 0.0f) {
 #pragma unroll 4
-    for (int i = g; i < t.parts; i += kGroups) {
-      const float w = fast_exp2(ws_lse[row_of(i)] - m);
-      if (w != 0.0f) o = fmaf(w, ws_o[row_of(i) * D + d], o);
+      for (int i = g; i < t.parts; i += kGroups) {
+        const float w = fast_exp2(ws_lse[row_of(i)] - m);
+        if (w != 0.0f) o = fmaf(w, ws_o[row_of(i) * D + d], o);
+      }
     }
-  }
-  part[g][d] = o;
-  __syncthreads();
-  if (g != 0) return;
+    part[g][d] = o;
+    __syncthreads();
+    if (g == 0) {
 #pragma unroll
-  for (int i = 1; i < kGroups; ++i) o += part[i][d];
-  o = s == 0.0f ? 0.0f : o / s;
-  const int G = a.Hq / a.Hkv, rr = t.r0 + r;
-  const int64_t row = static_cast<int64_t>(t.cu0 + rr / G) * a.Hq + t.h * G + rr % G;
-  if (a.f16) static_cast<__half*>(a.out)[row * D + d] = __float2half_rn(o);
-  else static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(o);
-  if (d == 0) a.lse[row] = s == 0.0f ? -INFINITY : (m + log2f(s)) * 0.6931471805599453f;
-}
-
-// ---------------------------------------------------------------------------
-// Many rows, one warp per row: one key at a time.
-// ---------------------------------------------------------------------------
-template <int D, bool F16>
-__global__ void __launch_bounds__(128) row_kernel(const Gqa8AttnArgs a, const int min_rows) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  constexpr int C = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= a.n_tokens * a.Hq) return;
-  const int64_t t = row / a.Hq;
-  const int h = static_cast<int>(row % a.Hq), hk = h / (a.Hq / a.Hkv);
-  int lo = 0, hi = a.B - 1;                       // largest b with cu[b] <= t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(a.cu + mid) <= t) lo = mid; else hi = mid - 1;
-  }
-  const int c0 = __ldg(a.cu + lo), c1 = __ldg(a.cu + lo + 1);
-  if (t < c0 || t >= c1) return;                  // behind the last request: left as it was
-  if (c1 - c0 > a.max_new || (c1 - c0) * (a.Hq / a.Hkv) < min_rows) return;   // the other kernel's
-  const int64_t pos = static_cast<int64_t>(__ldg(a.lens + lo)) - c1 + t;
-  const int64_t first = a.window > 0 && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
-  float q[C], o[C], m = -INFINITY, l = 0.0f;
-  const uint16_t* qp = static_cast<const uint16_t*>(a.q) + t * a.q_token_stride + h * a.q_head_stride + lane * C;
-#pragma unroll
-  for (int i = 0; i < C; ++i) {
-    q[i] = F16 ? __half2float(reinterpret_cast<const __half*>(qp)[i])
-               : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(qp)[i]);
-    o[i] = 0.0f;
-  }
-  const float c = a.sm_scale * 1.4426950408889634f;
-  const int64_t held = a.pt_stride << 6;          // what the table can name
-  if (pos >= held && lane == 0) flag_error(a.dev_err, kDevBadPage);
-  for (int64_t j = first; j <= pos && j < held; ++j) {
-    const int64_t pg = __ldg(a.page_table + lo * a.pt_stride + (j >> 6));
-    if (pg < 0 || pg >= a.num_pages) {
-      if (lane == 0) flag_error(a.dev_err, kDevBadPage);
-      j |= 63;                                    // the rest of the page is masked too
-      continue;
+      for (int i = 1; i < kGroups; ++i) o += part[i][d];
+      o = s == 0.0f ? 0.0f : o / s;
+      const int rr = t.r0 + r;
+      const int64_t row = static_cast<int64_t>(t.cu0 + rr / G) * a.Hq + t.h * G + rr % G;
+      if (a.f16) static_cast<__half*>(a.out)[row * D + d] = __float2half_rn(o);
+      else static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(o);
+      if (d == 0) a.lse[row] = s == 0.0f ? -INFINITY : (m + log2f(s)) * 0.6931471805599453f;
     }
-    const int64_t blk = (pg * a.Hkv + hk) * 2;
-    const uint8_t* kp = a.pool + blk * (kPage * D) + (j & 63) * D + lane * C;
-    const uint8_t* vp = kp + kPage * D;
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < C; ++i) s = fmaf(q[i], e4m3_to_float(kp[i]), s);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-    s *= c * pow2f(static_cast<int>(__ldg(a.scales + blk)) - 127);
-    const float mn = fmaxf(m, s);
-    const float corr = exp2f(m - mn), p = exp2f(s - mn);
-    const float pv = p * pow2f(static_cast<int>(__ldg(a.scales + blk + 1)) - 127);
-    l = l * corr + p;
-    m = mn;
-#pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = o[i] * corr + pv * e4m3_to_float(vp[i]);
+    __syncthreads();
   }
-  uint16_t* op = static_cast<uint16_t*>(a.out) + row * D + lane * C;
-  const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-#pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const float v = o[i] * inv;
-    if (F16) reinterpret_cast<__half*>(op)[i] = __float2half_rn(v);
-    else reinterpret_cast<__nv_bfloat16*>(op)[i] = __float2bfloat16_rn(v);
-  }
-  if (lane == 0) a.lse[row] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
 }
-
 
 // ---------------------------------------------------------------------------
 // Launch
@@ -768,33 +1116,29 @@ int few_rows(int max_new, int G) {
   const int64_t most = static_cast<int64_t>(max_new) * G, need = most <= 32 ? most : G;
   return need <= 8 ? 8 : need <= 16 ? 16 : need <= 32 ? 32 : 0;
 }
-constexpr int kSlotsPerSm = 4;      // two blocks an SM at most, two slots each
-size_t few_bytes(int rows, int D, int sms) {
-  const size_t slots = static_cast<size_t>(kSlotsPerSm) * sms;
-  return slots / 2 * sizeof(Gqa8Tail) + slots * rows * (D + 1) * sizeof(float);
+// Workspace of one attention kernel: a tail for each of its blocks, then two
+// slots of partial rows for each block.
+size_t part_bytes(int blocks, int rows, int D) {
+  return static_cast<size_t>(blocks) * (sizeof(Gqa8Tail) + 2ull * rows * (D + 1) * sizeof(float));
 }
+struct Parts {
+  Gqa8Tail* tails;
+  float *lse, *o;
+};
+Parts parts_at(void* ws, int blocks, int rows, int D) {
+  Parts p;
+  p.tails = static_cast<Gqa8Tail*>(ws);
+  p.o = reinterpret_cast<float*>(p.tails + blocks);
+  p.lse = p.o + 2ull * blocks * rows * D;
+  return p;
+}
+constexpr int kFewCtas = 2, kManyRows = 256;      // blocks an SM at most
 
-template <int D, int RP, int NT>
-cudaError_t launch_few(const Gqa8AttnArgs& a, const CUtensorMap& map, cudaStream_t stream) {
-  using C = FewCfg<D, RP, NT>;
-  static std::once_flag once[64];
-  static cudaError_t ready[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  std::call_once(once[dev & 63], [&] {
-    ready[dev & 63] = cudaFuncSetAttribute(few_kernel<D, RP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  });
-  if (ready[dev & 63] != cudaSuccess) return ready[dev & 63];
-  const unsigned grid = static_cast<unsigned>(a.num_sms * C::kCtas);
-  const size_t slots = static_cast<size_t>(kSlotsPerSm) * a.num_sms;
-  Gqa8Tail* tails = static_cast<Gqa8Tail*>(a.ws);
-  float* o = reinterpret_cast<float*>(tails + slots / 2);
-  float* lse = o + slots * RP * D;
-  e = launch_pdl(few_kernel<D, RP, NT>, grid, 256, C::kSmem, stream, 1, map, a, RP, tails, lse, o);
-  if (e != cudaSuccess || (a.pt_stride + 1) / 2 <= kWhole) return e;       // nothing is ever cut
+template <int D>
+cudaError_t launch_merge(const Gqa8AttnArgs& a, int blocks, int rows, const Parts& p, cudaStream_t stream) {
+  if ((a.pt_stride + 1) / 2 <= kWhole) return cudaSuccess;                 // nothing is ever cut
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, RP);
+  cfg.gridDim = dim3(blocks, rows < 32 ? rows : 32);
   cfg.blockDim = dim3(512);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -802,8 +1146,54 @@ cudaError_t launch_few(const Gqa8AttnArgs& a, const CUtensorMap& map, cudaStream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, a, RP, static_cast<const Gqa8Tail*>(tails),
-                            static_cast<const float*>(lse), static_cast<const float*>(o));
+  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, a, rows, static_cast<const Gqa8Tail*>(p.tails),
+                            static_cast<const float*>(p.lse), static_cast<const float*>(p.o));
+}
+
+// Once per device and kernel: its shared memory, and, where it splits its
+// registers among its warps, that its launch has as many as the split takes.
+template <auto kKernel>
+cudaError_t prepare_kernel(int smem, int min_regs) {
+  static std::once_flag once[64];
+  static cudaError_t ready[64];
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::call_once(once[dev], [&] {
+    ready[dev] = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaFuncAttributes f;
+    if (ready[dev] == cudaSuccess) ready[dev] = cudaFuncGetAttributes(&f, kKernel);
+    if (ready[dev] == cudaSuccess && f.numRegs < min_regs) ready[dev] = cudaErrorInvalidConfiguration;
+  });
+  return ready[dev];
+}
+
+template <int D, int RP, int NT>
+cudaError_t launch_few(const Gqa8AttnArgs& a, const CUtensorMap& map, void* ws, cudaStream_t stream) {
+  using C = FewCfg<D, RP, NT>;
+  cudaError_t e = prepare_kernel<few_kernel<D, RP, NT>>(C::kSmem, 0);
+  if (e != cudaSuccess) return e;
+  const int blocks = a.num_sms * C::kCtas;
+  const Parts p = parts_at(ws, blocks, RP, D);
+  e = launch_pdl(few_kernel<D, RP, NT>, blocks, 256, C::kSmem, stream, 1, map, a, RP, p.tails, p.lse, p.o);
+  return e != cudaSuccess ? e : launch_merge<D>(a, blocks, RP, p, stream);
+}
+
+template <int D, int NT>
+cudaError_t launch_many(const Gqa8AttnArgs& a, const CUtensorMap& map, int min_rows, void* ws,
+                        cudaStream_t stream) {
+  using C = ManyCfg<D, NT>;
+  cudaError_t e = prepare_kernel<many_kernel<D, NT>>(C::kSmem, kLaunchRegs);
+  if (e != cudaSuccess) return e;
+  const Parts p = parts_at(ws, a.num_sms, kManyRows, D);
+  e = launch_pdl(many_kernel<D, NT>, a.num_sms, kManyThreads, C::kSmem, stream, 1, map, a, min_rows, p.tails,
+                 p.lse, p.o);
+  return e != cudaSuccess ? e : launch_merge<D>(a, a.num_sms, kManyRows, p, stream);
+}
+
+size_t few_bytes(int rows, int D, int sms) {
+  return rows == 0 ? 0 : (part_bytes(kFewCtas * sms, rows, D) + 255) / 256 * 256;
 }
 
 template <int D>
@@ -812,13 +1202,12 @@ cudaError_t launch_d(const Gqa8AttnArgs& a, cudaStream_t stream) {
   if (!pool_map(a, &map)) return cudaErrorInvalidValue;
   const int G = a.Hq / a.Hkv, rows = few_rows(a.max_new, G);
   cudaError_t e = cudaSuccess;
-  if (rows == 8) e = a.f16 ? launch_few<D, 8, 3>(a, map, stream) : launch_few<D, 8, 2>(a, map, stream);
-  else if (rows == 16) e = a.f16 ? launch_few<D, 16, 3>(a, map, stream) : launch_few<D, 16, 2>(a, map, stream);
-  else if (rows == 32) e = a.f16 ? launch_few<D, 32, 3>(a, map, stream) : launch_few<D, 32, 2>(a, map, stream);
+  if (rows == 8) e = a.f16 ? launch_few<D, 8, 3>(a, map, a.ws, stream) : launch_few<D, 8, 2>(a, map, a.ws, stream);
+  else if (rows == 16) e = a.f16 ? launch_few<D, 16, 3>(a, map, a.ws, stream) : launch_few<D, 16, 2>(a, map, a.ws, stream);
+  else if (rows == 32) e = a.f16 ? launch_few<D, 32, 3>(a, map, a.ws, stream) : launch_few<D, 32, 2>(a, map, a.ws, stream);
   if (e != cudaSuccess || static_cast<int64_t>(a.max_new) * G <= rows) return e;
-  const unsigned grid = static_cast<unsigned>((a.n_tokens * a.Hq + 3) / 4);
-  return a.f16 ? launch_pdl(row_kernel<D, true>, grid, 128, 0, stream, 1, a, rows + 1)
-               : launch_pdl(row_kernel<D, false>, grid, 128, 0, stream, 1, a, rows + 1);
+  void* const ws = static_cast<uint8_t*>(a.ws) + few_bytes(rows, D, a.num_sms);
+  return a.f16 ? launch_many<D, 3>(a, map, rows + 1, ws, stream) : launch_many<D, 2>(a, map, rows + 1, ws, stream);
 }
 
 }  // namespace
@@ -829,7 +1218,8 @@ cudaError_t launch_attention_gqa8(const Gqa8AttnArgs& a, cudaStream_t stream) {
 
 size_t attention_gqa8_workspace(int, int max_new, int64_t, int Hq, int Hkv, int D, int num_sms) {
   const int rows = few_rows(max_new, Hq / Hkv);
-  return rows > 0 ? (few_bytes(rows, D, num_sms) + 255) / 256 * 256 : 0;
+  const bool many = static_cast<int64_t>(max_new) * (Hq / Hkv) > rows;
+  return few_bytes(rows, D, num_sms) + (many ? part_bytes(num_sms, kManyRows, D) : 0);
 }
 
 }  // namespace kv4

@@ -68,6 +68,19 @@ __device__ __forceinline__ void split_e4m3(uint32_t x, uint32_t (&t)[NT]) {
   }
 }
 
+// The same without the factors: x = t0 + t1 + .., so that the terms' products
+// add up in one accumulator; with |x|'s largest near 448, elements below 2^-10
+// of it keep 2^-18 of it.
+template <int NT>
+__device__ __forceinline__ void split_e4m3_same(uint32_t x, uint32_t (&t)[NT]) {
+  t[0] = e4m3x2_of_f16x2(x);
+#pragma unroll
+  for (int i = 1; i < NT; ++i) {
+    x = h2_bits(__hsub2(bits_h2(x), bits_h2(e4m3x2_to_f16x2(t[i - 1]))));
+    t[i] = e4m3x2_of_f16x2(x);
+  }
+}
+
 // Largest value over the warp (NaN only where every lane holds one).
 __device__ __forceinline__ float warp_max(float x) {
   float r;
@@ -112,14 +125,14 @@ __device__ __forceinline__ Gqa8Request gqa8_request(const Gqa8AttnArgs& a, int b
     if (report) flag_error(a.dev_err, kDevBadLength);
     return q;
   }
+  const int64_t cap = a.pt_stride << 6;
+  if (report && cap < len) flag_error(a.dev_err, kDevBadPage);
   const int64_t rows = static_cast<int64_t>(c1 - c0) * (a.Hq / a.Hkv);
   if (rows < min_rows || rows > max_rows) return q;
-  const int64_t cap = a.pt_stride << 6;
   q.cu0 = c0;
   q.n = c1 - c0;
   q.pos0 = len - q.n;
   q.held = len < cap ? len : static_cast<int>(cap);
-  if (report && q.held < len) flag_error(a.dev_err, kDevBadPage);
   return q;
 }
 // Keys of rows [r0, r1) of a request.
@@ -161,5 +174,101 @@ struct Gqa8Tail {
   int parts;                 // 0: none; else pieces, in this block and the next parts - 1
   int cu0, h, r0, nrows, pad[3];
 };
+
+constexpr int kWhole = 4;      // items of at most so many tiles are never cut
+constexpr int kMasked = 0x7FFF7FFF;
+constexpr float kLowest = -3e38f;
+
+// The items of this block, in order, to `emit` (whole warp): requests with
+// min_rows .. max_rows rows, `rows` rows an item, `total` tiles in all.  Also
+// leaves this block's tail.
+template <typename Emit>
+__device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, int min_rows, int max_rows, int rows,
+                                          int64_t total, Gqa8Tail* tails, int lane, Emit&& emit) {
+  const int G = a.Hq / a.Hkv, blocks = gridDim.x, me = blockIdx.x;
+  const int64_t per = max((total + blocks - 1) / blocks, static_cast<int64_t>(kWhole));
+  const int64_t u0 = me * per, u1 = min(u0 + per, total);
+  bool tail = false;
+  int64_t acc = 0;
+  for (int base = 0; base < a.B && acc < u1 && u0 < u1; base += 32) {
+    const Gqa8Request q = gqa8_request(a, base + lane, min_rows, max_rows, false);
+    const int64_t units = gqa8_units(a, q, G, rows);
+    int64_t end = units;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, end, off);
+      if (lane >= off) end += v;
+    }
+    end += acc;
+    acc = __shfl_sync(0xFFFFFFFFu, end, 31);
+    uint32_t todo = __ballot_sync(0xFFFFFFFFu, units > 0 && end > u0 && end - units < u1);
+    for (; todo != 0; todo &= todo - 1) {
+      const int l = __ffs(todo) - 1;
+      Gqa8Request r;
+      r.cu0 = __shfl_sync(0xFFFFFFFFu, q.cu0, l);
+      r.n = __shfl_sync(0xFFFFFFFFu, q.n, l);
+      r.pos0 = __shfl_sync(0xFFFFFFFFu, q.pos0, l);
+      r.held = __shfl_sync(0xFFFFFFFFu, q.held, l);
+      int64_t at = __shfl_sync(0xFFFFFFFFu, end - units, l);
+      const int R = r.n * G;
+      for (int r0 = 0; r0 < R && at < u1; r0 += rows) {
+        const int nrows = min(rows, R - r0);
+        const Gqa8Span sp = gqa8_span(a, r, G, r0, r0 + nrows);
+        const int64_t w = max(sp.nt, 1);
+        if (at + w * a.Hkv <= u0) {
+          at += w * a.Hkv;
+          continue;
+        }
+        const int h0 = at < u0 ? static_cast<int>((u0 - at) / w) : 0;
+        int64_t begin = at + h0 * w;
+        for (int h = h0; h < a.Hkv && begin < u1; ++h, begin += w) {
+          int64_t tb = 0, te = sp.nt;
+          int slot = -1;
+          if (w <= kWhole) {
+            if (begin < u0) continue;                       // the block before has it whole
+          } else {
+            tb = max(u0 - begin, static_cast<int64_t>(0));
+            te = min(u1 - begin, w);
+            if (tb > 0) {
+              slot = 2 * me;
+            } else if (te < w) {
+              slot = 2 * me + 1;
+              tail = true;
+              if (lane == 0)
+                tails[me] = Gqa8Tail{static_cast<int>((begin + w - 1) / per) - me + 1, r.cu0, h, r0, nrows, {}};
+            }
+          }
+          emit(Gqa8Item{base + l, h, r.cu0, r.pos0, r0, nrows, sp.klo, sp.khi,
+                        sp.t0 + static_cast<int>(tb), sp.t0 + static_cast<int>(te), slot});
+        }
+        at += w * a.Hkv;
+      }
+    }
+  }
+  if (lane == 0 && !tail) tails[me].parts = 0;
+}
+
+// Page `lane` of the 16 tiles from tile t on: its block of the pool (past the
+// pool where there is none: TMA gives zeros) and its two exponents, kMasked
+// where there is no page.  The append's exponents lie in [-48, 48]; others
+// count as the nearer end, so that sums of p over V exponents stay in range.
+__device__ __forceinline__ void gqa8_pages(const Gqa8AttnArgs& a, const Gqa8Item& it, int t, int lane,
+                                           int& block, int& ex) {
+  const int64_t page = 2 * static_cast<int64_t>(t) + lane;
+  block = static_cast<int>(a.num_pages) * a.Hkv;
+  ex = kMasked;
+  if ((page >> 1) < it.t_end && (page << 6) < it.khi && (page << 6) + 64 > it.klo) {
+    const int phys = __ldg(a.page_table + it.b * a.pt_stride + page);
+    if (phys < 0 || phys >= a.num_pages) {
+      flag_error(a.dev_err, kDevBadPage);
+    } else {
+      block = phys * a.Hkv + it.h;
+      const uint32_t e2 = __ldg(reinterpret_cast<const uint16_t*>(a.scales) + block);
+      const int ek = min(max(static_cast<int>(e2 & 0xFF) - 127, kGqa8ExpMin), kGqa8ExpMax);
+      const int ev = min(max(static_cast<int>(e2 >> 8) - 127, kGqa8ExpMin), kGqa8ExpMax);
+      ex = (ek & 0xFFFF) | static_cast<int>(static_cast<uint32_t>(ev) << 16);
+    }
+  }
+}
 
 }  // namespace kv4
