@@ -13,6 +13,7 @@
 #include <stddef.h>
 
 #include <mutex>
+#include <type_traits>
 
 namespace kv4 {
 namespace {
@@ -57,6 +58,8 @@ struct FewCfg {
   static constexpr int kSmem = kStages * kTile + kFixed + 1024;
   static constexpr uint32_t kTmem = 4 * N <= 64 ? 64 : 4 * N <= 128 ? 128 : 4 * N <= 256 ? 256 : 512;
 };
+
+constexpr int kFewCost = 1;    // of an item, in tiles (its q and its output overlap others' tiles)
 
 struct FewSmall {
   uint64_t full[12], empty[12], item_full[4], item_empty[4], q_full[2], q_empty[2], s_full[2], p_full[2],
@@ -119,12 +122,8 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
   grid_dependency_wait();
   grid_launch_dependents();
   __syncthreads();
-  {
-    int64_t u = 0;
-    for (int b = tid; b < a.B; b += 256)
-      u += gqa8_units(a, gqa8_request(a, b, 1, max_rows, blockIdx.x == 0), G, RP);
-    if (u > 0) atomicAdd(&sm.total, static_cast<unsigned long long>(u));
-  }
+  const Gqa8Kind kind{1, max_rows, RP, kFewCost};
+  gqa8_total(a, kind, blockIdx.x == 0, &sm.total);
   fence_async_smem();
   tc_fence_before_sync();
   __syncthreads();
@@ -184,7 +183,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
         }
       }
     };
-    gqa8_walk(a, 1, max_rows, RP, static_cast<int64_t>(sm.total), tails, lane, [&](const Gqa8Item& it) {
+    gqa8_walk(a, kind, static_cast<int64_t>(sm.total), tails, lane, [&](const Gqa8Item& it) {
       publish(it);
       load(it);
     });
@@ -550,6 +549,8 @@ constexpr int kManyThreads = 384;
 constexpr uint32_t kSoftmaxRegs = 208, kOtherRegs = 88, kLaunchRegs = 168;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "register shares draw on the launch's");
 
+constexpr int kManyCost = 4;   // of an item, in tiles: q in, first scores, last product, output
+
 struct ManySmall {
   uint64_t k_full[3], k_empty[3], v8_full[2], v8_empty[2], v_full[2], v_empty[2], item_full[2], item_empty[2],
       ex_full[8], q_full[2], s_full[2], p_full[2], o_full[2], never;
@@ -607,12 +608,8 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
   grid_dependency_wait();
   grid_launch_dependents();
   __syncthreads();
-  {
-    int64_t u = 0;
-    for (int b = tid; b < a.B; b += kManyThreads)
-      u += gqa8_units(a, gqa8_request(a, b, min_rows, kAll, blockIdx.x == 0 && min_rows == 1), G, C::kRows);
-    if (u > 0) atomicAdd(&sm.total, static_cast<unsigned long long>(u));
-  }
+  const Gqa8Kind kind{min_rows, kAll, C::kRows, kManyCost};
+  gqa8_total(a, kind, blockIdx.x == 0 && min_rows == 1, &sm.total);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -679,11 +676,10 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
           }
         }
       };
-      gqa8_walk(a, min_rows, kAll, C::kRows, static_cast<int64_t>(sm.total), tails, lane,
-                [&](const Gqa8Item& it) {
-                  publish(it);
-                  load(it);
-                });
+      gqa8_walk(a, kind, static_cast<int64_t>(sm.total), tails, lane, [&](const Gqa8Item& it) {
+        publish(it);
+        load(it);
+      });
       publish(Gqa8Item{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, -1});
       // every signal lands before the block's shared memory goes away
       for (uint32_t i = n_tiles > KS ? n_tiles - KS : 0; i < n_tiles; ++i)
@@ -1011,69 +1007,86 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
 }
 
 // ---------------------------------------------------------------------------
-// The pieces of items that were cut: block (c, y) joins rows y, y + gridDim.y,
-// .. of the item that began in block c of the attention kernel, by log-sum-exp
-// over its pieces in their order.
+// The pieces of items that were cut: block (c, y) joins rows of the item that
+// began in block c of the attention kernel, by log-sum-exp over its pieces in
+// their order.  W warps share a row (8 where an item has few rows and a long
+// context many pieces, 1 where it has 256 rows and two or three pieces).
 // ---------------------------------------------------------------------------
-template <int D>
-__global__ void __launch_bounds__(512) merge_kernel(const Gqa8AttnArgs a, const int rows,
+template <int D, int W>
+__global__ void __launch_bounds__(256) merge_kernel(const Gqa8AttnArgs a, const int rows,
                                                     const Gqa8Tail* tails, const float* ws_lse,
                                                     const float* ws_o) {
   grid_dependency_wait();
   grid_launch_dependents();
-  constexpr int kGroups = 512 / D;
-  __shared__ float part[kGroups][D];
-  __shared__ float top, sum;
-  const int c = blockIdx.x, tid = threadIdx.x, d = tid % D, g = tid / D;
+  constexpr int C = D / 32;                               // columns a lane
+  using Vec = std::conditional_t<C == 4, float4, float2>;
+  __shared__ Vec part[8][32];
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Gqa8Tail t = tails[c];
-  if (t.parts == 0) return;
-  const int G = a.Hq / a.Hkv;
-  for (int r = blockIdx.y; r < t.nrows; r += gridDim.y) {
+  const int r = blockIdx.y * (8 / W) + warp / W, wi = warp % W;
+  if (t.parts == 0 || (W == 8 && r >= t.nrows)) return;   // (whole blocks)
+  float o[C], m = -INFINITY, s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < C; ++k) o[k] = 0.0f;
+  bool odd = false;
+  if (r < t.nrows) {
     // piece i is slot 2c + 1 for i = 0, else 2 (c + i)
     auto row_of = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * rows + r; };
-    if (tid < 32) {
-      float m = -INFINITY;
-      bool odd = false;
-      for (int i = tid; i < t.parts; i += 32) {
-        const float x = ws_lse[row_of(i)];
-        odd |= x != x;
-        m = fmaxf(m, x);
-      }
-      m = warp_max(m);
-      odd = __any_sync(0xFFFFFFFFu, odd);
-      float s = 0.0f;
-      if (m > -INFINITY)
-        for (int i = tid; i < t.parts; i += 32) s += fast_exp2(ws_lse[row_of(i)] - m);
-      s = warp_sum(s);
-      if (tid == 0) {
-        top = m;
-        sum = odd ? __uint_as_float(0x7FC00000u) : s;
-      }
+    for (int i = lane; i < t.parts; i += 32) {
+      const float x = __ldg(ws_lse + row_of(i));
+      odd |= x != x;
+      m = fmaxf(m, x);
     }
-    __syncthreads();
-    const float m = top, s = sum;
-    float o = 0.0f;
-    if (s != 0.0f) {
+    m = warp_max(m);
+    odd = __any_sync(0xFFFFFFFFu, odd);
+    if (m > -INFINITY) {
+      for (int i0 = 0; i0 < t.parts; i0 += 32) {
+        const float w = i0 + lane < t.parts ? fast_exp2(__ldg(ws_lse + row_of(i0 + lane)) - m) : 0.0f;
+        s += w;
+        const int n = min(32, t.parts - i0);
 #pragma unroll 4
-      for (int i = g; i < t.parts; i += kGroups) {
-        const float w = fast_exp2(ws_lse[row_of(i)] - m);
-        if (w != 0.0f) o = fmaf(w, ws_o[row_of(i) * D + d], o);
-      }
-    }
-    part[g][d] = o;
-    __syncthreads();
-    if (g == 0) {
+        for (int i = wi; i < n; i += W) {
+          const float wt = __shfl_sync(0xFFFFFFFFu, w, i);
+          const Vec v = __ldg(reinterpret_cast<const Vec*>(ws_o + row_of(i0 + i) * D) + lane);
+          const float* f = reinterpret_cast<const float*>(&v);
 #pragma unroll
-      for (int i = 1; i < kGroups; ++i) o += part[i][d];
-      o = s == 0.0f ? 0.0f : o / s;
-      const int rr = t.r0 + r;
-      const int64_t row = static_cast<int64_t>(t.cu0 + rr / G) * a.Hq + t.h * G + rr % G;
-      if (a.f16) static_cast<__half*>(a.out)[row * D + d] = __float2half_rn(o);
-      else static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(o);
-      if (d == 0) a.lse[row] = s == 0.0f ? -INFINITY : (m + log2f(s)) * 0.6931471805599453f;
+          for (int k = 0; k < C; ++k) o[k] = fmaf(wt, f[k], o[k]);
+        }
+      }
+      s = warp_sum(s);
     }
-    __syncthreads();
+    if (odd) s = __uint_as_float(0x7FC00000u);
   }
+  if constexpr (W > 1) {
+    part[warp][lane] = *reinterpret_cast<const Vec*>(o);
+    __syncthreads();
+    if (wi != 0) return;
+#pragma unroll
+    for (int i = 1; i < W; ++i) {
+      const Vec v = part[warp + i][lane];
+#pragma unroll
+      for (int k = 0; k < C; ++k) o[k] += reinterpret_cast<const float*>(&v)[k];
+    }
+  }
+  if (r >= t.nrows) return;
+  const int G = a.Hq / a.Hkv, rr = t.r0 + r;
+  const int64_t row = static_cast<int64_t>(t.cu0 + rr / G) * a.Hq + t.h * G + rr % G;
+  const float inv = s == 0.0f ? 0.0f : 1.0f / s;
+  uint32_t u[C / 2];
+#pragma unroll
+  for (int k = 0; k < C / 2; ++k) {
+    const float y0 = o[2 * k] * inv, y1 = o[2 * k + 1] * inv;
+    if (a.f16) {
+      u[k] = h2_bits(__floats2half2_rn(y0, y1));
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
+      u[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  uint32_t* const dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * D) + lane * (C / 2);
+  if constexpr (C == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[1]);
+  else *dst = u[0];
+  if (lane == 0) a.lse[row] = s == 0.0f ? -INFINITY : (m + log2f(s)) * 0.6931471805599453f;
 }
 
 // ---------------------------------------------------------------------------
@@ -1134,19 +1147,19 @@ Parts parts_at(void* ws, int blocks, int rows, int D) {
 }
 constexpr int kFewCtas = 2, kManyRows = 256;      // blocks an SM at most
 
-template <int D>
+template <int D, int W>
 cudaError_t launch_merge(const Gqa8AttnArgs& a, int blocks, int rows, const Parts& p, cudaStream_t stream) {
   if ((a.pt_stride + 1) / 2 <= kWhole) return cudaSuccess;                 // nothing is ever cut
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, rows < 32 ? rows : 32);
-  cfg.blockDim = dim3(512);
+  cfg.gridDim = dim3(blocks, rows * W / 8);
+  cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, a, rows, static_cast<const Gqa8Tail*>(p.tails),
+  return cudaLaunchKernelEx(&cfg, merge_kernel<D, W>, a, rows, static_cast<const Gqa8Tail*>(p.tails),
                             static_cast<const float*>(p.lse), static_cast<const float*>(p.o));
 }
 
@@ -1177,7 +1190,7 @@ cudaError_t launch_few(const Gqa8AttnArgs& a, const CUtensorMap& map, void* ws, 
   const int blocks = a.num_sms * C::kCtas;
   const Parts p = parts_at(ws, blocks, RP, D);
   e = launch_pdl(few_kernel<D, RP, NT>, blocks, 256, C::kSmem, stream, 1, map, a, RP, p.tails, p.lse, p.o);
-  return e != cudaSuccess ? e : launch_merge<D>(a, blocks, RP, p, stream);
+  return e != cudaSuccess ? e : launch_merge<D, 8>(a, blocks, RP, p, stream);
 }
 
 template <int D, int NT>
@@ -1189,7 +1202,7 @@ cudaError_t launch_many(const Gqa8AttnArgs& a, const CUtensorMap& map, int min_r
   const Parts p = parts_at(ws, a.num_sms, kManyRows, D);
   e = launch_pdl(many_kernel<D, NT>, a.num_sms, kManyThreads, C::kSmem, stream, 1, map, a, min_rows, p.tails,
                  p.lse, p.o);
-  return e != cudaSuccess ? e : launch_merge<D>(a, a.num_sms, kManyRows, p, stream);
+  return e != cudaSuccess ? e : launch_merge<D, 1>(a, a.num_sms, kManyRows, p, stream);
 }
 
 size_t few_bytes(int rows, int D, int sms) {

@@ -98,10 +98,12 @@ __device__ __forceinline__ float warp_sum(float x) {
 // the group); `rows` consecutive ones, of one kv head, are an item, which
 // walks its keys in tiles of 128 (tile t: keys 128 t .. 128 t + 127, two
 // pages).  Items are ordered by request, row group, kv head; each counts for
-// its number of tiles (one where it has none: its rows are still written), and
-// every block takes an equal share of the whole, found from the lengths on the
-// device.  An item of at most kWhole tiles stays with the block that its first
-// tile falls to; longer ones are cut at the shares' borders and merged after.
+// its tiles and `cost` more (what starting and ending an item takes, in
+// tiles), and every block takes an equal share of the whole, found from the
+// lengths on the device.  An item that a border between two shares falls into
+// is cut there, unless it has few tiles or the cut would leave fewer than
+// kLeast to a side: then the border moves to the item's nearer end.  The
+// pieces of a cut item are joined by a second kernel.
 // ---------------------------------------------------------------------------
 struct Gqa8Request {
   int cu0;          // first flat row
@@ -150,13 +152,51 @@ __device__ __forceinline__ Gqa8Span gqa8_span(const Gqa8AttnArgs& a, const Gqa8R
   s.nt = hi > lo ? ((s.khi - 1) >> 7) + 1 - s.t0 : 0;
   return s;
 }
-__device__ __forceinline__ int64_t gqa8_units(const Gqa8AttnArgs& a, const Gqa8Request& q, int G,
-                                              int rows) {
+struct Gqa8Kind {     // of requests that one of the kernels takes
+  int min_rows, max_rows;
+  int rows;           // of an item
+  int cost;           // of an item beyond its tiles
+};
+constexpr int kWhole = 4, kLeast = 2;
+
+// Units of the requests of a warp's lanes: a lane by itself where it has few
+// row groups, the warp together for the others.
+__device__ __forceinline__ int64_t gqa8_units(const Gqa8AttnArgs& a, const Gqa8Request& q,
+                                              const Gqa8Kind& kind, int G, int lane) {
+  const int R = q.n * G, groups = (R + kind.rows - 1) / kind.rows;
+  auto units = [&](const Gqa8Request& r, int i, int n_rows) {
+    return gqa8_span(a, r, G, i * kind.rows, min(n_rows, (i + 1) * kind.rows)).nt + kind.cost;
+  };
   int64_t u = 0;
-  const int R = q.n * G;
-  for (int r0 = 0; r0 < R; r0 += rows)
-    u += max(gqa8_span(a, q, G, r0, min(R, r0 + rows)).nt, 1);
+  if (groups <= 2)
+    for (int i = 0; i < groups; ++i) u += units(q, i, R);
+  for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, groups > 2); todo != 0; todo &= todo - 1) {
+    const int l = __ffs(todo) - 1;
+    Gqa8Request r;
+    r.cu0 = 0;
+    r.n = __shfl_sync(0xFFFFFFFFu, q.n, l);
+    r.pos0 = __shfl_sync(0xFFFFFFFFu, q.pos0, l);
+    r.held = __shfl_sync(0xFFFFFFFFu, q.held, l);
+    const int gr = __shfl_sync(0xFFFFFFFFu, groups, l);
+    int64_t v = 0;
+    for (int i = lane; i < gr; i += 32) v += units(r, i, r.n * G);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+    if (lane == l) u = v;
+  }
   return u * a.Hkv;
+}
+// Sum over all requests, added to *total by every warp of the block.
+__device__ __forceinline__ void gqa8_total(const Gqa8AttnArgs& a, const Gqa8Kind& kind, bool report,
+                                           unsigned long long* total) {
+  const int lane = threadIdx.x & 31;
+  int64_t u = 0;
+  for (int base = threadIdx.x & ~31; base < a.B; base += blockDim.x)
+    u += gqa8_units(a, gqa8_request(a, base + lane, kind.min_rows, kind.max_rows, report), kind,
+                    a.Hq / a.Hkv, lane);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, off);
+  if (lane == 0 && u > 0) atomicAdd(total, static_cast<unsigned long long>(u));
 }
 
 struct Gqa8Item {
@@ -175,24 +215,35 @@ struct Gqa8Tail {
   int cu0, h, r0, nrows, pad[3];
 };
 
-constexpr int kWhole = 4;      // items of at most so many tiles are never cut
 constexpr int kMasked = 0x7FFF7FFF;
 constexpr float kLowest = -3e38f;
 
-// The items of this block, in order, to `emit` (whole warp): requests with
-// min_rows .. max_rows rows, `rows` rows an item, `total` tiles in all.  Also
-// leaves this block's tail.
+// Where the border at unit u cuts an item of nt tiles that begins at unit
+// `begin`: tiles before the border, 0 .. nt (0 and nt also where it is not in
+// the item at all).
+__device__ __forceinline__ int gqa8_cut(int64_t u, int64_t begin, int nt, int cost) {
+  const int64_t x = u - begin;
+  if (x <= 0) return 0;
+  if (x >= nt + cost) return nt;
+  if (nt <= kWhole) return 2 * x <= nt + cost ? 0 : nt;
+  const int64_t t = x - cost;
+  return t < kLeast ? 0 : t > nt - kLeast ? nt : static_cast<int>(t);
+}
+
+// The items of this block, in order, to `emit` (whole warp), of `total` units.
+// Also leaves this block's tail.
 template <typename Emit>
-__device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, int min_rows, int max_rows, int rows,
-                                          int64_t total, Gqa8Tail* tails, int lane, Emit&& emit) {
+__device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, const Gqa8Kind& kind, int64_t total,
+                                          Gqa8Tail* tails, int lane, Emit&& emit) {
   const int G = a.Hq / a.Hkv, blocks = gridDim.x, me = blockIdx.x;
-  const int64_t per = max((total + blocks - 1) / blocks, static_cast<int64_t>(kWhole));
-  const int64_t u0 = me * per, u1 = min(u0 + per, total);
+  // (a share holds at most one border's surroundings of an item)
+  const int64_t per = max((total + blocks - 1) / blocks, static_cast<int64_t>(kind.cost + kWhole));
+  const int64_t u0 = me * per, u1 = u0 + per;
   bool tail = false;
   int64_t acc = 0;
-  for (int base = 0; base < a.B && acc < u1 && u0 < u1; base += 32) {
-    const Gqa8Request q = gqa8_request(a, base + lane, min_rows, max_rows, false);
-    const int64_t units = gqa8_units(a, q, G, rows);
+  for (int base = 0; base < a.B && acc < u1 && u0 < total; base += 32) {
+    const Gqa8Request q = gqa8_request(a, base + lane, kind.min_rows, kind.max_rows, false);
+    const int64_t units = gqa8_units(a, q, kind, G, lane);
     int64_t end = units;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -209,39 +260,55 @@ __device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, int min_rows, i
       r.n = __shfl_sync(0xFFFFFFFFu, q.n, l);
       r.pos0 = __shfl_sync(0xFFFFFFFFu, q.pos0, l);
       r.held = __shfl_sync(0xFFFFFFFFu, q.held, l);
-      int64_t at = __shfl_sync(0xFFFFFFFFu, end - units, l);
-      const int R = r.n * G;
-      for (int r0 = 0; r0 < R && at < u1; r0 += rows) {
-        const int nrows = min(rows, R - r0);
-        const Gqa8Span sp = gqa8_span(a, r, G, r0, r0 + nrows);
-        const int64_t w = max(sp.nt, 1);
-        if (at + w * a.Hkv <= u0) {
-          at += w * a.Hkv;
-          continue;
+      int64_t first = __shfl_sync(0xFFFFFFFFu, end - units, l);
+      const int R = r.n * G, groups = (R + kind.rows - 1) / kind.rows;
+      for (int g0 = 0; g0 < groups && first < u1; g0 += 32) {
+        // a lane's row group, and where its items begin
+        const int gi = g0 + lane;
+        Gqa8Span sp{0, 0, 0, 0};
+        int64_t w = 0;
+        if (gi < groups) {
+          sp = gqa8_span(a, r, G, gi * kind.rows, min(R, (gi + 1) * kind.rows));
+          w = static_cast<int64_t>(sp.nt + kind.cost) * a.Hkv;
         }
-        const int h0 = at < u0 ? static_cast<int>((u0 - at) / w) : 0;
-        int64_t begin = at + h0 * w;
-        for (int h = h0; h < a.Hkv && begin < u1; ++h, begin += w) {
-          int64_t tb = 0, te = sp.nt;
-          int slot = -1;
-          if (w <= kWhole) {
-            if (begin < u0) continue;                       // the block before has it whole
-          } else {
-            tb = max(u0 - begin, static_cast<int64_t>(0));
-            te = min(u1 - begin, w);
-            if (tb > 0) {
+        int64_t g_end = w;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int64_t v = __shfl_up_sync(0xFFFFFFFFu, g_end, off);
+          if (lane >= off) g_end += v;
+        }
+        g_end += first;
+        uint32_t gtodo = __ballot_sync(0xFFFFFFFFu, w > 0 && g_end > u0 && g_end - w < u1);
+        for (; gtodo != 0; gtodo &= gtodo - 1) {
+          const int gl = __ffs(gtodo) - 1;
+          const int klo = __shfl_sync(0xFFFFFFFFu, sp.klo, gl), khi = __shfl_sync(0xFFFFFFFFu, sp.khi, gl);
+          const int t0 = __shfl_sync(0xFFFFFFFFu, sp.t0, gl), nt = __shfl_sync(0xFFFFFFFFu, sp.nt, gl);
+          const int64_t at = __shfl_sync(0xFFFFFFFFu, g_end - w, gl);
+          const int each = nt + kind.cost, r0 = (g0 + gl) * kind.rows, nrows = min(kind.rows, R - r0);
+          const int h0 = at < u0 ? static_cast<int>((u0 - at) / each) : 0;
+          int64_t begin = at + static_cast<int64_t>(h0) * each;
+          for (int h = h0; h < a.Hkv && begin < u1; ++h, begin += each) {
+            const int tb = gqa8_cut(u0, begin, nt, kind.cost), te = gqa8_cut(u1, begin, nt, kind.cost);
+            int slot = -1;
+            if (nt == 0) {
+              // no tile to cut: the block that its first unit falls to
+              if (begin < u0) continue;
+            } else if (tb == te) {
+              continue;
+            } else if (tb > 0) {
               slot = 2 * me;
-            } else if (te < w) {
+            } else if (te < nt) {
               slot = 2 * me + 1;
               tail = true;
-              if (lane == 0)
-                tails[me] = Gqa8Tail{static_cast<int>((begin + w - 1) / per) - me + 1, r.cu0, h, r0, nrows, {}};
+              // the last block that has some of it
+              int last = static_cast<int>((begin + each - 1) / per);
+              if (gqa8_cut(last * per, begin, nt, kind.cost) == nt) --last;
+              if (lane == 0) tails[me] = Gqa8Tail{last - me + 1, r.cu0, h, r0, nrows, {}};
             }
+            emit(Gqa8Item{base + l, h, r.cu0, r.pos0, r0, nrows, klo, khi, t0 + tb, t0 + te, slot});
           }
-          emit(Gqa8Item{base + l, h, r.cu0, r.pos0, r0, nrows, sp.klo, sp.khi,
-                        sp.t0 + static_cast<int>(tb), sp.t0 + static_cast<int>(te), slot});
         }
-        at += w * a.Hkv;
+        first = __shfl_sync(0xFFFFFFFFu, g_end, 31);
       }
     }
   }
