@@ -111,6 +111,18 @@ __device__ __forceinline__ bool mbar_try_wait_suspend(uint32_t bar, uint32_t par
   return ok != 0;
 }
 
+// One lane of a converged warp (the same one every time).  A whole warp that
+// runs the issue loop and elects a lane around the instructions themselves
+// keeps their operands uniform; in a branch of one lane each operand of each
+// instruction would be moved to a uniform register first.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Wait for the phase with the given parity; gives up after timeout_ns.
 __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
                                                   uint64_t timeout_ns) {

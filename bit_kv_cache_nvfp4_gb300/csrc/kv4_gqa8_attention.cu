@@ -196,71 +196,89 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
       for (uint32_t i = n_tiles > ST ? n_tiles - ST : 0; i < n_tiles; ++i)
         mbar_wait_bounded(smem_addr(&sm.full[i % ST]), (i / ST) & 1, 1000000);
   } else if (warp == 1) {
-    // ==== products ====
-    if (lane == 0) {
-      constexpr uint32_t kSw = D == 128 ? kSwizzle128 : kSwizzle64;
-      constexpr uint32_t idesc_qk = idesc_e4m3(128, N, false, false);
-      constexpr uint32_t idesc_pv = idesc_e4m3(D, N, true, true);
-      uint32_t n_items = 0, n_tiles = 0;
-      // PV of tile j: O^T = V^T . P^T over 128 keys, 32 a step
-      auto pv = [&](uint32_t j) {
-        wait(sm.p_full[j & 1], (j >> 1) & 1);
-        tc_fence_after_sync();
-        const uint64_t dv = smem_desc(smem_addr(smem + (j % ST) * C::kTile) + kTileKeys * D, 16, 8 * D, kSw);
-        const uint64_t dp = smem_desc(smem_addr(p_s + (j & 1) * C::kP), 128, 2048, kSwizzleNone);
+    // ==== products (the whole warp; one lane issues) ====
+    constexpr uint32_t kSw = D == 128 ? kSwizzle128 : kSwizzle64;
+    constexpr uint32_t idesc_qk = idesc_e4m3(128, N, false, false);
+    constexpr uint32_t idesc_pv = idesc_e4m3(D, N, true, true);
+    const uint64_t dk0 = smem_desc(smem_addr(smem), 16, 8 * D, kSw), dq0 = smem_desc(smem_addr(q_s), 16, 8 * D, kSw);
+    const uint64_t dp0 = smem_desc(smem_addr(p_s), 128, 2048, kSwizzleNone);
+    uint32_t n_items = 0, n_tiles = 0;
+    uint32_t st = 0, st_par = 0, st_last = 0;             // stage of the next tile and of the one before
+    // PV of tile j: O^T = V^T . P^T over 128 keys, 32 a step
+    auto pv = [&](uint32_t j) {
+      wait(sm.p_full[j & 1], (j >> 1) & 1);
+      __syncwarp();
+      tc_fence_after_sync();
+      if (elect_one()) {
+        const uint64_t dv = dk0 + ((st_last * C::kTile + kTileKeys * D) >> 4), dp = dp0 + (j & 1) * (C::kP >> 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_f8kind(tmem + 2 * N + (j & 1) * N, dv + ((k * 32 * D) >> 4), dp + ((k * 512) >> 4), idesc_pv,
-                     k > 0);
+          mma_f8kind(tmem + 2 * N + (j & 1) * N, dv + ((k * 32 * D) >> 4), dp + ((k * 512) >> 4), idesc_pv, k > 0);
         mma_commit(smem_addr(&sm.o_full[j & 1]));
-        mma_commit(smem_addr(&sm.empty[j % ST]));
-      };
-      bool pending = false;
-      while (true) {
-        const int s = n_items & 3;
-        if (pending && !mbar_try_wait(smem_addr(&sm.item_full[s]), (n_items >> 2) & 1)) {
-          pv(n_tiles - 1);
+        mma_commit(smem_addr(&sm.empty[st_last]));
+      }
+      __syncwarp();
+    };
+    auto ready = [&](uint64_t& bar, uint32_t parity) {
+      return __any_sync(0xFFFFFFFFu, mbar_try_wait(smem_addr(&bar), parity));
+    };
+    bool pending = false;
+    while (true) {
+      const int s = n_items & 3;
+      if (pending && !ready(sm.item_full[s], (n_items >> 2) & 1)) {
+        pv(n_tiles - 1);
+        pending = false;
+      }
+      wait(sm.item_full[s], (n_items >> 2) & 1);
+      if (__any_sync(0xFFFFFFFFu, *dead != 0)) break;
+      const int b = __shfl_sync(0xFFFFFFFFu, sm.items[s].b, 0);
+      const int nt = __shfl_sync(0xFFFFFFFFu, sm.items[s].t_end - sm.items[s].t_begin, 0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
+      if (b < 0) break;
+      const uint32_t qb = n_items & 1;
+      const uint64_t dq = dq0 + qb * (C::kQ >> 4);
+      for (int t = 0; t < nt; ++t, ++n_tiles) {
+        const uint32_t j = n_tiles;
+        // the next scores first, unless their keys are still on the way
+        if (pending && !ready(sm.full[st], st_par)) {
+          pv(j - 1);
           pending = false;
         }
-        wait(sm.item_full[s], (n_items >> 2) & 1);
-        if (*dead) break;
-        const int b = sm.items[s].b, nt = sm.items[s].t_end - sm.items[s].t_begin;
-        mbar_arrive(smem_addr(&sm.item_empty[s]));
-        if (b < 0) break;
-        const uint32_t qb = n_items & 1;
-        const uint64_t dq = smem_desc(smem_addr(q_s + qb * C::kQ), 16, 8 * D, kSw);
-        for (int t = 0; t < nt; ++t, ++n_tiles) {
-          const uint32_t j = n_tiles;
-          // the next scores first, unless their keys are still on the way
-          if (pending && !mbar_try_wait(smem_addr(&sm.full[j % ST]), (j / ST) & 1)) {
-            pv(j - 1);
-            pending = false;
-          }
-          if (t == 0) wait(sm.q_full[qb], (n_items >> 1) & 1);
-          wait(sm.full[j % ST], (j / ST) & 1);
-          tc_fence_after_sync();
-          const uint64_t dk = smem_desc(smem_addr(smem + (j % ST) * C::kTile), 16, 8 * D, kSw);
+        if (t == 0) wait(sm.q_full[qb], (n_items >> 1) & 1);
+        wait(sm.full[st], st_par);
+        __syncwarp();
+        tc_fence_after_sync();
+        if (elect_one()) {
+          const uint64_t dk = dk0 + st * (C::kTile >> 4);
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)
             mma_f8kind(tmem + (j & 1) * N, dk + 2 * k, dq + 2 * k, idesc_qk, k > 0);
           mma_commit(smem_addr(&sm.s_full[j & 1]));
           if (t == nt - 1) mma_commit(smem_addr(&sm.q_empty[qb]));
-          if (pending) pv(j - 1);
-          pending = true;
         }
-        if (nt == 0) {
-          // (a product left pending here would keep the softmax from its item,
-          // so from the q buffer that the wait after next is for)
-          if (pending) pv(n_tiles - 1);
-          pending = false;
-          wait(sm.q_full[qb], (n_items >> 1) & 1);
-          mbar_arrive(smem_addr(&sm.q_empty[qb]));
+        __syncwarp();
+        if (pending) pv(j - 1);
+        pending = true;
+        st_last = st;
+        if (++st == ST) {
+          st = 0;
+          st_par ^= 1;
         }
-        ++n_items;
       }
-      if (pending) pv(n_tiles - 1);
-      if (a.fault_site == 1) wait(sm.never, 0);
+      if (nt == 0) {
+        // (a product left pending here would keep the softmax from its item,
+        // so from the q buffer that the wait after next is for)
+        if (pending) pv(n_tiles - 1);
+        pending = false;
+        wait(sm.q_full[qb], (n_items >> 1) & 1);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.q_empty[qb]));
+      }
+      ++n_items;
     }
+    if (pending) pv(n_tiles - 1);
+    if (a.fault_site == 1) wait(sm.never, 0);
     __syncwarp();
   } else if (warp < 4) {
     // ==== q of the next item, as NT E4M3 terms ====
@@ -287,39 +305,15 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
           w[1] = __ldg(g + 1);
         }
         float x[16];
-        const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (a.f16) {
-            const float2 f = __half22float2(bits_h2(u[i]));
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-          } else {
-            x[2 * i] = __uint_as_float(u[i] << 16);
-            x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-          }
-          m = max(m, max(__float_as_uint(x[2 * i]) & 0x7FFFFFFFu, __float_as_uint(x[2 * i + 1]) & 0x7FFFFFFFu));
-        }
+        uint32_t m = widen16(w, a.f16, x);
 #pragma unroll
         for (int off = 1; off < TPR; off <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
         const bool odd = m >= 0x7F800000u;                // a NaN or an infinity: NaN in its row
-        // least e with amax <= 448 * 2^e, far enough from the ends of fp32
-        const int e = min(max(static_cast<int>(m >> 23) - 135 + ((m & 0x7FFFFFu) > 0x600000u ? 1 : 0), -118), 118);
-        const float f = odd ? 0.0f : pow2f(-e);
+        const int e = q_exponent(m);
         if (part == 0)
           sm.qf[qb][rr] = odd ? __uint_as_float(0x7FC00000u) : a.sm_scale * 1.4426950408889634f * pow2f(e);
         uint32_t o[NT][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t t0[NT], t1[NT];
-          const float x0 = odd ? 0.0f : x[4 * i] * f, x1 = odd ? 0.0f : x[4 * i + 1] * f;
-          const float x2 = odd ? 0.0f : x[4 * i + 2] * f, x3 = odd ? 0.0f : x[4 * i + 3] * f;
-          split_e4m3<NT>(h2_bits(__floats2half2_rn(x0, x1)), t0);
-          split_e4m3<NT>(h2_bits(__floats2half2_rn(x2, x3)), t1);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) o[t][i] = t0[t] | (t1[t] << 16);
-        }
+        terms16<NT, false>(x, pow2f(-e), odd, o);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const uint32_t off = (t * RP + rr) * D + part * 16;
@@ -529,38 +523,44 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
 // is widened to f16 once per tile by two warps (exact), for P in f16 (2^-11)
 // takes one pass where E4M3 terms would take two and twice the instructions
 // in the softmax, which has the least room to spare.
-// A thread is a row: its 128 scores come from TMEM at once, K's block
-// exponents and the scale of q multiply them, V's are added to the exponent of
-// p, so that p is relative to a running reference of score and V exponent
-// together; a row's reference only moves, and its O in TMEM is only rescaled,
-// when that rises by more than 2^6 (p stays below 2^14, f16's top is 2^16).
+// The chain scores -> softmax -> P -> O, next scores of a row tile is what the
+// other tile's products have to cover, so two threads share a row, one for each
+// page of the tile (64 keys): K's block exponent and the scale of q multiply
+// the scores, V's is added to the exponent of p, so that p is relative to a
+// running reference of score and V exponent together, which the two halves
+// agree on for every tile.  A row's reference only moves, and its O in TMEM is
+// only rescaled, when that rises by more than 2^6 (p stays below 2^14, f16's
+// top is 2^16).
 template <int D_, int NT_>
 struct ManyCfg {
   static constexpr int D = D_, NT = NT_, kRows = 256;
   static constexpr int kK = kTileKeys * D;                // K or V codes of a tile
   static constexpr int kV16 = kTileKeys * D * 2;
   static constexpr int kQ = NT * 128 * D;                 // of one of the two row tiles
-  static constexpr int kKStages = NT == 2 ? 3 : 2, kVStages = 2;
-  static constexpr int kSmall = 2048;
+  static constexpr int kKStages = NT == 2 ? 3 : 2, kVStages = NT == 2 ? 2 : 1;
+  static constexpr int kSmall = 6144;
   static constexpr int kSmem = 2 * kQ + kKStages * kK + kVStages * kK + 2 * kV16 + kSmall + 1024;
 };
 static_assert(ManyCfg<128, 3>::kSmem <= 227 * 1024 && ManyCfg<128, 2>::kSmem <= 227 * 1024, "shared memory");
-constexpr int kManyThreads = 384;
-constexpr uint32_t kSoftmaxRegs = 208, kOtherRegs = 88, kLaunchRegs = 168;
-static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "register shares draw on the launch's");
+constexpr int kManyThreads = 640;
+constexpr uint32_t kSoftmaxRegs = 104, kOtherRegs = 64, kLaunchRegs = 96;
+static_assert(4 * kSoftmaxRegs + kOtherRegs <= 5 * kLaunchRegs, "register shares draw on the launch's");
 
 constexpr int kManyCost = 4;   // of an item, in tiles: q in, first scores, last product, output
 
 struct ManySmall {
   uint64_t k_full[3], k_empty[3], v8_full[2], v8_empty[2], v_full[2], v_empty[2], item_full[2], item_empty[2],
-      ex_full[8], q_full[2], s_full[2], p_full[2], o_full[2], never;
+      ex_full[8], q_full[2], s_full[2], p_full[2][2], o_full[2], never;
   unsigned long long total;
   uint32_t tmem;
   int dead;
   int exps[8][2];
   Gqa8Item items[2];
+  float qf[2][128];           // sm_scale log2(e) 2^eq of a row, NaN where q is not finite
+  float top[2][2][2][128];    // largest score and V exponent of a half row, by row tile and tile parity;
+                              // an item's last sums in the parity its next tile would have
 };
-static_assert(sizeof(ManySmall) <= 2048, "ManySmall");
+static_assert(sizeof(ManySmall) <= 6144, "ManySmall");
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kManyThreads, 1)
@@ -591,10 +591,11 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
       mbar_init(smem_addr(&sm.v_full[i]), 2);
       mbar_init(smem_addr(&sm.v_empty[i]), 1);
       mbar_init(smem_addr(&sm.item_full[i]), 1);
-      mbar_init(smem_addr(&sm.item_empty[i]), 11);        // the product's lane, 2 + 8 warps
-      mbar_init(smem_addr(&sm.q_full[i]), 4);
+      mbar_init(smem_addr(&sm.item_empty[i]), 19);        // the product's lane, 2 + 16 warps
+      mbar_init(smem_addr(&sm.q_full[i]), 8);
       mbar_init(smem_addr(&sm.s_full[i]), 1);
-      mbar_init(smem_addr(&sm.p_full[i]), 4);
+      mbar_init(smem_addr(&sm.p_full[i][0]), 4);
+      mbar_init(smem_addr(&sm.p_full[i][1]), 4);
       mbar_init(smem_addr(&sm.o_full[i]), 1);
     }
     for (int i = 0; i < 8; ++i) mbar_init(smem_addr(&sm.ex_full[i]), 1);
@@ -692,63 +693,91 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
           mbar_wait_bounded(smem_addr(&sm.v8_full[i % VS]), (i / VS) & 1, 1000000);
       }
     } else if (warp == 1) {
-      // ==== products ====
-      if (lane == 0) {
-        constexpr uint32_t kSw = D == 128 ? kSwizzle128 : kSwizzle64;
-        constexpr uint32_t idesc_qk = idesc_e4m3(128, 128, false, false);
-        constexpr uint32_t idesc_pv = idesc_f16(128, D, false, true);
-        uint32_t n_tiles = 0;
-        uint32_t nw[2] = {0, 0}, np[2] = {0, 0};          // items and tiles of each row tile so far
-        auto qk = [&](int qt, uint32_t j) {
-          const uint64_t dk = smem_desc(smem_addr(k_s + (j % KS) * C::kK), 16, 8 * D, kSw);
-          const uint64_t dq = smem_desc(smem_addr(q_s + qt * C::kQ), 16, 8 * D, kSw);
+      // ==== products (the whole warp; one lane issues) ====
+      constexpr uint32_t kSw = D == 128 ? kSwizzle128 : kSwizzle64;
+      constexpr uint32_t idesc_qk = idesc_e4m3(128, 128, false, false);
+      constexpr uint32_t idesc_pv = idesc_f16(128, D, false, true);
+      const uint64_t dk0 = smem_desc(smem_addr(k_s), 16, 8 * D, kSw), dq0 = smem_desc(smem_addr(q_s), 16, 8 * D, kSw);
+      const uint64_t dv0 = smem_desc(smem_addr(v_s), kSlab, 1024, kSwizzle128);
+      uint32_t n_tiles = 0, ks = 0, k_par = 0;            // stage of K and its parity
+      uint32_t w0 = 0, w1 = 0, p0 = 0, p1 = 0;            // parities of the row tiles' q and P
+      auto qk = [&](int qt, uint32_t stage) {
+        if (elect_one()) {
+          const uint64_t dk = dk0 + stage * (C::kK >> 4), dq = dq0 + qt * (C::kQ >> 4);
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
               mma_f8kind(tmem + qt * 128, dq + ((t * 128 * D) >> 4) + 2 * k, dk + 2 * k, idesc_qk, t + k > 0);
           mma_commit(smem_addr(&sm.s_full[qt]));
-        };
-        auto pv = [&](int qt, uint32_t j, bool first) {
-          wait(sm.p_full[qt], np[qt] & 1);
-          ++np[qt];
-          tc_fence_after_sync();
-          const uint64_t dv = smem_desc(smem_addr(v_s + (j & 1) * C::kV16), kSlab, 1024, kSwizzle128);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_f16_ts(tmem + 256 + qt * 128, tmem + qt * 128 + 8 * k, dv + ((k * 2048) >> 4), idesc_pv,
-                       !first || k > 0);
-        };
-        for (uint32_t n_items = 0;; ++n_items) {
-          const int s = n_items & 1;
-          wait(sm.item_full[s], (n_items >> 1) & 1);
-          if (*dead) break;
-          const int b = sm.items[s].b, nt = sm.items[s].t_end - sm.items[s].t_begin;
-          const int nq = sm.items[s].nrows > 128 ? 2 : 1;
-          mbar_arrive(smem_addr(&sm.item_empty[s]));
-          if (b < 0) break;
-          if (nt == 0) continue;
-          for (int qt = 0; qt < nq; ++qt) wait(sm.q_full[qt], nw[qt]++ & 1);
-          for (int t = 0; t <= nt; ++t) {
-            const uint32_t j = n_tiles + t;
-            if (t < nt) {
-              wait(sm.k_full[j % KS], (j / KS) & 1);
-              tc_fence_after_sync();
-            }
-            if (t > 0) wait(sm.v_full[(j - 1) & 1], ((j - 1) >> 1) & 1);
-            for (int qt = 0; qt < nq; ++qt) {
-              // P of a row tile lies over its S: the products run in order
-              if (t > 0) pv(qt, j - 1, t == 1);
-              if (t < nt) qk(qt, j);
-              else mma_commit(smem_addr(&sm.o_full[qt]));
-            }
-            if (t > 0) mma_commit(smem_addr(&sm.v_empty[(j - 1) & 1]));
-            if (t < nt) mma_commit(smem_addr(&sm.k_empty[j % KS]));
-          }
-          n_tiles += nt;
         }
-        if (a.fault_site == 1) wait(sm.never, 0);
+        __syncwarp();
+      };
+      // (each half of P, 64 keys, lies over its own half of S)
+      auto pv = [&](int qt, uint32_t j, bool first, uint32_t& par) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          wait(sm.p_full[qt][half], par);
+          __syncwarp();
+          tc_fence_after_sync();
+          if (elect_one()) {
+            const uint64_t dv = dv0 + (j & 1) * (C::kV16 >> 4);
+#pragma unroll
+            for (int k = 4 * half; k < 4 * half + 4; ++k)
+              mma_f16_ts(tmem + 256 + qt * 128, tmem + qt * 128 + 64 * half + 8 * (k & 3), dv + ((k * 2048) >> 4),
+                         idesc_pv, !first || k > 0);
+          }
+          __syncwarp();
+        }
+        par ^= 1;
+      };
+      for (uint32_t n_items = 0;; ++n_items) {
+        const int s = n_items & 1;
+        wait(sm.item_full[s], (n_items >> 1) & 1);
+        if (__any_sync(0xFFFFFFFFu, *dead != 0)) break;
+        const int b = __shfl_sync(0xFFFFFFFFu, sm.items[s].b, 0);
+        const int nt = __shfl_sync(0xFFFFFFFFu, sm.items[s].t_end - sm.items[s].t_begin, 0);
+        const bool two = __shfl_sync(0xFFFFFFFFu, sm.items[s].nrows, 0) > 128;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
+        if (b < 0) break;
+        if (nt == 0) continue;
+        wait(sm.q_full[0], w0);
+        w0 ^= 1;
+        if (two) {
+          wait(sm.q_full[1], w1);
+          w1 ^= 1;
+        }
+        for (int t = 0; t <= nt; ++t) {
+          const uint32_t j = n_tiles + t;
+          if (t < nt) wait(sm.k_full[ks], k_par);
+          if (t > 0) wait(sm.v_full[(j - 1) & 1], ((j - 1) >> 1) & 1);
+          __syncwarp();
+          tc_fence_after_sync();
+          // P of a row tile lies over its S: the products run in order
+          if (t > 0) pv(0, j - 1, t == 1, p0);
+          if (t < nt) qk(0, ks);
+          if (two) {
+            if (t > 0) pv(1, j - 1, t == 1, p1);
+            if (t < nt) qk(1, ks);
+          }
+          if (elect_one()) {
+            if (t > 0) mma_commit(smem_addr(&sm.v_empty[(j - 1) & 1]));
+            if (t < nt) mma_commit(smem_addr(&sm.k_empty[ks]));
+            if (t == nt) {
+              mma_commit(smem_addr(&sm.o_full[0]));
+              if (two) mma_commit(smem_addr(&sm.o_full[1]));
+            }
+          }
+          __syncwarp();
+          if (t < nt && ++ks == KS) {
+            ks = 0;
+            k_par ^= 1;
+          }
+        }
+        n_tiles += nt;
       }
+      if (a.fault_site == 1) wait(sm.never, 0);
       __syncwarp();
     } else {
       // ==== V to f16 ====
@@ -757,11 +786,23 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
         const int s = n_items & 1;
         wait(sm.item_full[s], (n_items >> 1) & 1);
         if (__any_sync(0xFFFFFFFFu, *dead != 0)) break;
-        const int b = sm.items[s].b, t0 = sm.items[s].t_begin, t1 = sm.items[s].t_end;
-        const int klo = sm.items[s].klo, khi = sm.items[s].khi;
+        const Gqa8Item item = sm.items[s];
+        const int b = item.b, t0 = item.t_begin, t1 = item.t_end;
+        const int klo = item.klo, khi = item.khi;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
         if (b < 0) break;
+        // the item's rows of q into L2, while the one before is worked on
+        {
+          const int cu0 = item.cu0, h = item.h, r0 = item.r0, nrows = item.nrows;
+          for (int rr = tid - 64; rr < nrows; rr += 64) {
+            const uint16_t* row = static_cast<const uint16_t*>(a.q) +
+                                  static_cast<int64_t>(cu0 + (r0 + rr) / G) * a.q_token_stride +
+                                  static_cast<int64_t>(h * G + (r0 + rr) % G) * a.q_head_stride;
+            prefetch_l2_line(row);
+            if (D == 128) prefetch_l2_line(row + 64);
+          }
+        }
         for (int t = t0; t < t1; ++t, ++j) {
           wait(sm.v8_full[j % VS], (j / VS) & 1);
           wait(sm.v_empty[j & 1], ((j >> 1) & 1) ^ 1);
@@ -799,16 +840,20 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
       }
     }
   } else {
-    // ==== softmax: a thread is a row ====
+    // ==== softmax: a thread is half a row, 64 keys of a tile ====
     setmaxnreg_inc<kSoftmaxRegs>();
-    const int qt = (warp >> 2) - 1, row = tid & 127;      // of the item: qt * 128 + row
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_tm = tmem + qt * 128 + lanes, o_tm = tmem + 256 + qt * 128 + lanes;
+    const int qt = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;
+    const int bar = 1 + qt;                               // the row tile's 8 warps
+    const int wrow = (warp & 3) * 32, row = wrow + lane;  // of the row tile
+    const uint32_t lanes = static_cast<uint32_t>(wrow) << 16;
+    const uint32_t s_tm = tmem + qt * 128 + half * 64 + lanes;
+    const uint32_t o_tm = tmem + 256 + qt * 128 + half * (D / 2) + lanes;
+    uint8_t* const q_mine = q_s + qt * C::kQ;
     uint32_t j = 0, n_mine = 0, n_work = 0;               // tiles of all items, of mine; items of mine
     for (uint32_t n_items = 0;; ++n_items) {
       const int s = n_items & 1;
       wait(sm.item_full[s], (n_items >> 1) & 1);
-      if (__any_sync(0xFFFFFFFFu, *dead != 0)) break;
+      if (named_sync_or(bar, 256, *dead != 0)) break;     // (together, for they meet at barriers)
       const Gqa8Item it = sm.items[s];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
@@ -818,113 +863,105 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
         j += nt;
         continue;
       }
-      const int r = it.r0 + qt * 128 + row;
       const bool mine = qt * 128 + row < it.nrows;
-      const int64_t flat = static_cast<int64_t>(it.cu0 + r / G);
-      const int head = it.h * G + r % G;
       // keys at < hi and >= lo are this row's
-      const int64_t pos = static_cast<int64_t>(it.pos0) + r / G;
-      const int hi = mine ? static_cast<int>(max(min(pos + 1, static_cast<int64_t>(it.khi)), static_cast<int64_t>(0))) : 0;
-      const int lo = a.window > 0 ? static_cast<int>(max(pos - a.window + 1, static_cast<int64_t>(0))) : 0;
-      bool odd = false;
-      float qf = 0.0f;
+      int hi = 0, lo = 0;
+      if (mine) {
+        const int64_t pos = static_cast<int64_t>(it.pos0) + (it.r0 + qt * 128 + row) / G;
+        hi = static_cast<int>(max(min(pos + 1, static_cast<int64_t>(it.khi)), static_cast<int64_t>(0)));
+        if (a.window > 0) lo = static_cast<int>(max(pos - a.window + 1, static_cast<int64_t>(0)));
+      }
       if (nt > 0) {
-        // the row of q as NT E4M3 terms, its scale to the score's
-        uint4 w[D / 8];
-        const uint4* g = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + flat * a.q_token_stride +
-                                                        static_cast<int64_t>(head) * a.q_head_stride);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) w[i] = mine ? __ldg(g + i) : make_uint4(0, 0, 0, 0);
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float2 f;
-            if (a.f16) f = __half22float2(bits_h2(u[k]));
-            else f = make_float2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xFFFF0000u));
-            m = max(m, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
+        // 16 of the warp's rows of q (the other half's warp has the others) as
+        // NT E4M3 terms, kTpr threads a row
+        constexpr int kTpr = D / 16, kRpp = 32 / kTpr;
+        const int part = lane % kTpr;
+        const float sign = a.sm_scale < 0.0f ? -1.0f : 1.0f;   // (so that the factor is positive)
+#pragma unroll 2
+        for (int p = 0; p < 16 / kRpp; ++p) {
+          const int rr = wrow + half * 16 + p * kRpp + lane / kTpr;
+          const int gr = it.r0 + qt * 128 + rr;
+          uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+          if (qt * 128 + rr < it.nrows) {
+            const uint4* g = reinterpret_cast<const uint4*>(
+                static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(it.cu0 + gr / G) * a.q_token_stride +
+                static_cast<int64_t>(it.h * G + gr % G) * a.q_head_stride + part * 16);
+            w[0] = __ldg(g);
+            w[1] = __ldg(g + 1);
           }
-        }
-        odd = m >= 0x7F800000u;
-        const int e = min(max(static_cast<int>(m >> 23) - 135 + ((m & 0x7FFFFFu) > 0x600000u ? 1 : 0), -118), 118);
-        // a negative sm_scale turns q, so that the scores' factor is positive
-        const float f = (odd ? 0.0f : pow2f(-e)) * (a.sm_scale < 0.0f ? -1.0f : 1.0f);
-        qf = fabsf(a.sm_scale) * 1.4426950408889634f * pow2f(e);
+          float y[16];
+          uint32_t m = widen16(w, a.f16, y);
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
+          for (int off = 1; off < kTpr; off <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+          const int e = q_exponent(m);
+          const bool odd = m >= 0x7F800000u;              // a NaN or an infinity: NaN in its row
+          if (part == 0)
+            sm.qf[qt][rr] = odd ? __uint_as_float(0x7FC00000u) : fabsf(a.sm_scale) * 1.4426950408889634f * pow2f(e);
           uint32_t o[NT][4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4& v = w[2 * c + (i >> 1)];
-            const uint32_t u0 = (i & 1) ? v.z : v.x, u1 = (i & 1) ? v.w : v.y;
-            uint32_t t0[NT], t1[NT];
-            float2 f0, f1;
-            if (a.f16) {
-              f0 = __half22float2(bits_h2(u0));
-              f1 = __half22float2(bits_h2(u1));
-            } else {
-              f0 = make_float2(__uint_as_float(u0 << 16), __uint_as_float(u0 & 0xFFFF0000u));
-              f1 = make_float2(__uint_as_float(u1 << 16), __uint_as_float(u1 & 0xFFFF0000u));
-            }
-            if (odd) f0 = f1 = make_float2(0.0f, 0.0f);
-            split_e4m3_same<NT>(h2_bits(__floats2half2_rn(f0.x * f, f0.y * f)), t0);
-            split_e4m3_same<NT>(h2_bits(__floats2half2_rn(f1.x * f, f1.y * f)), t1);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) o[t][i] = t0[t] | (t1[t] << 16);
-          }
+          terms16<NT, true>(y, sign * pow2f(-e), odd, o);
 #pragma unroll
           for (int t = 0; t < NT; ++t)
-            *reinterpret_cast<uint4*>(q_s + qt * C::kQ + t * 128 * D + swizzle<D == 128 ? 3 : 2>(row * D + c * 16)) =
+            *reinterpret_cast<uint4*>(q_mine + t * 128 * D + swizzle<D == 128 ? 3 : 2>(rr * D + part * 16)) =
                 make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
         }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.q_full[qt]));
+        named_sync(bar, 256);                             // qf, by both halves' warps
       }
+      float qf = nt > 0 ? sm.qf[qt][row] : 0.0f;
+      const bool odd = qf != qf;
+      if (odd) qf = 0.0f;
       float mref = kLowest, l = 0.0f;
       for (int t = it.t_begin; t < it.t_end; ++t, ++j, ++n_mine) {
         wait(sm.ex_full[j & 7], (j >> 3) & 1);
-        const int e0 = sm.exps[j & 7][0], e1 = sm.exps[j & 7][1];
+        const int ex = sm.exps[j & 7][half];
         wait(sm.s_full[qt], n_mine & 1);
         tc_fence_after_sync();
-        float x[128];
+        float x[64];
+        // the second part is on its way while the first one's maximum is taken
+        tmem_ld32(s_tm, reinterpret_cast<uint32_t(&)[32]>(x[0]));
+        tmem_wait_ld32(reinterpret_cast<uint32_t(&)[32]>(x[0]));
+        tmem_ld32(s_tm + 32, reinterpret_cast<uint32_t(&)[32]>(x[32]));
+        // keys of this row in the page: [c0, c1)
+        const int at = t * kTileKeys + half * 64, c0 = lo - at, c1 = hi - at;
+        const bool edge = __any_sync(0xFFFFFFFFu, c0 > 0 || c1 < 64) || ex == kMasked;
+        const int a0 = max(c0, 0), n = ex == kMasked ? 0 : max(min(c1, 64) - a0, 0);
+        auto mask = [&](int from) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, reinterpret_cast<uint32_t(&)[32]>(x[32 * c]));
+          for (int c = from; c < from + 32; ++c)
+            x[c] = static_cast<unsigned>(c - a0) < static_cast<unsigned>(n) ? x[c] : -INFINITY;
+        };
+        float m[4];
+        if (edge) mask(0);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_wait_ld32(reinterpret_cast<uint32_t(&)[32]>(x[32 * c]));
-        // keys of this row in the tile: [c0, c1)
-        const int c0 = lo - t * kTileKeys, c1 = hi - t * kTileKeys;
-        if (__any_sync(0xFFFFFFFFu, c0 > 0 || c1 < kTileKeys) || e0 == kMasked || e1 == kMasked) {
-          const int a0 = max(c0, 0), n = max(min(c1, kTileKeys) - a0, 0);
+        for (int k = 0; k < 4; ++k) m[k] = fmaxf(x[k], x[4 + k]);
 #pragma unroll
-          for (int c = 0; c < kTileKeys; ++c) {
-            const bool in = static_cast<unsigned>(c - a0) < static_cast<unsigned>(n) &&
-                            (c < 64 ? e0 : e1) != kMasked;
-            x[c] = in ? x[c] : -INFINITY;
-          }
-        }
-        const int ev0 = e0 == kMasked ? kGqa8ExpMin : e0 >> 16, ev1 = e1 == kMasked ? kGqa8ExpMin : e1 >> 16;
+        for (int c = 8; c < 32; c += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m[k] = max3(m[k], x[c + k], x[c + 4 + k]);
+        tmem_wait_ld32(reinterpret_cast<uint32_t(&)[32]>(x[32]));
+        if (edge) mask(32);
+#pragma unroll
+        for (int c = 32; c < 64; c += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m[k] = max3(m[k], x[c + k], x[c + 4 + k]);
+        const int ev = ex == kMasked ? kGqa8ExpMin : ex >> 16;
         // (at least 2^-126, so that a masked -inf stays one where the scale is 0)
-        const float f0 = fmaxf(qf * pow2f(e0 == kMasked ? 0 : static_cast<int16_t>(e0 & 0xFFFF)), 0x1p-126f);
-        const float f1 = fmaxf(qf * pow2f(e1 == kMasked ? 0 : static_cast<int16_t>(e1 & 0xFFFF)), 0x1p-126f);
-        float m0 = x[0], m1 = x[64];
-#pragma unroll
-        for (int c = 1; c < 64; ++c) {
-          m0 = fmaxf(m0, x[c]);
-          m1 = fmaxf(m1, x[64 + c]);
-        }
-        const float top = fmaxf(fmaf(m0, f0, static_cast<float>(ev0)), fmaf(m1, f1, static_cast<float>(ev1)));
-        const bool raise = top > mref + 6.0f;
-        if (__any_sync(0xFFFFFFFFu, raise)) {
+        const float f = fmaxf(qf * pow2f(ex == kMasked ? 0 : static_cast<int16_t>(ex & 0xFFFF)), 0x1p-126f);
+        float top = fmaf(max3(m[0], m[1], fmaxf(m[2], m[3])), f, static_cast<float>(ev));
+        sm.top[qt][j & 1][half][row] = top;
+        named_sync(bar, 256);
+        top = fmaxf(top, sm.top[qt][j & 1][half ^ 1][row]);
+        if (__any_sync(0xFFFFFFFFu, top > mref + 6.0f)) {
           const float to = fmaxf(top, mref), by = fast_exp2(mref - to);
           mref = to;
           l *= by;
           if (t > it.t_begin) {
-            // s_full came behind the last product into this O
+            // s_full came behind the last product into this O; each half takes
+            // its columns
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
+            for (int c = 0; c < D / 2; c += 16) {
               uint32_t v[16];
               tmem_ld16_sync(o_tm + c, v);
 #pragma unroll
@@ -933,68 +970,93 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
             }
           }
         }
-        const float b0 = static_cast<float>(ev0) - mref + 8.0f, b1 = static_cast<float>(ev1) - mref + 8.0f;
-        float sum[2] = {0.0f, 0.0f};
+        const float b = static_cast<float>(ev) - mref + 8.0f;
+        const float2 f2 = make_float2(f, f), b2 = make_float2(b, b);
+        float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t p[32];
-          float sa = 0.0f, sb = 0.0f;
+        for (int q = 0; q < 2; ++q) {
+          uint32_t p[16];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            float y0 = fast_exp2(fmaf(x[half * 64 + 2 * c], half ? f1 : f0, half ? b1 : b0));
-            float y1 = fast_exp2(fmaf(x[half * 64 + 2 * c + 1], half ? f1 : f0, half ? b1 : b0));
-            sa += y0;
-            sb += y1;
-            p[c] = h2_bits(__floats2half2_rn(y0, y1));
+          for (int c = 0; c < 16; ++c) {
+            float2 y = fma2(make_float2(x[q * 32 + 2 * c], x[q * 32 + 2 * c + 1]), f2, b2);
+            y.x = fast_exp2(y.x);
+            y.y = fast_exp2(y.y);
+            acc[c & 1] = add2(acc[c & 1], y);
+            p[c] = h2_bits(__floats2half2_rn(y.x, y.y));
           }
-          sum[half] = sa + sb;
-          tmem_st32(s_tm + 32 * half, p);
+          tmem_st16(s_tm + 16 * q, p);
         }
-        l = fmaf(sum[0], pow2f(-ev0), fmaf(sum[1], pow2f(-ev1), l));
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[qt]));
+        if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[qt][half]));
+        acc[0] = add2(acc[0], acc[1]);
+        l = fmaf(acc[0].x + acc[0].y, pow2f(-ev), l);
       }
+      sm.top[qt][j & 1][half][row] = l;
       if (nt > 0) {
         wait(sm.o_full[qt], n_work & 1);
         ++n_work;
         tc_fence_after_sync();
       }
+      named_sync(bar, 256);
+      l = sm.top[qt][j & 1][0][row] + sm.top[qt][j & 1][1][row];
       const float inv = odd && l > 0.0f ? __uint_as_float(0x7FC00000u) : 1.0f / l;
       const bool some = l > 0.0f || l != l;
-      const float ls = !some ? -INFINITY : odd ? __uint_as_float(0x7FC00000u) : mref - 8.0f + log2f(l);
+      const int r = it.r0 + qt * 128 + row;
       const int64_t part = static_cast<int64_t>(it.slot) * C::kRows + qt * 128 + row;
-      const int64_t orow = flat * a.Hq + head;
+      const int64_t orow = static_cast<int64_t>(it.cu0 + r / G) * a.Hq + it.h * G + r % G;
+      // Out through the rows of q's first two terms, one for each half of the
+      // columns, which no product reads any more, so that the stores to memory
+      // are D contiguous bytes: a half row of 16 bits, a quarter row of fp32.
+      constexpr int kCpr = D / 16;                        // 16-byte chunks of D bytes
+      auto stage = [&](int rr, int c) {
+        return reinterpret_cast<uint4*>(q_mine + half * (128 * D) + swizzle<D == 128 ? 3 : 2>((wrow + rr) * D + c * 16));
+      };
+      auto flush = [&](uint8_t* base, int64_t to, int64_t row_bytes) {
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < kCpr; ++i) {
+          const int rr = (i * 32 + lane) / kCpr, c = lane % kCpr;
+          const int64_t dst = __shfl_sync(0xFFFFFFFFu, to, rr);
+          const uint4 v = *stage(rr, c);
+          if (qt * 128 + wrow + rr < it.nrows) *reinterpret_cast<uint4*>(base + dst * row_bytes + c * 16) = v;
+        }
+        __syncwarp();
+      };
 #pragma unroll 1
-      for (int c = 0; c < D; c += 16) {
+      for (int c0 = 0; c0 < D / 2; c0 += 16) {            // of this half's columns
         uint32_t v[16];
-        if (nt > 0) tmem_ld16_sync(o_tm + c, v);
-        float y[16];
+        if (nt > 0) tmem_ld16_sync(o_tm + c0, v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = some && nt > 0 ? __uint_as_float(v[i]) * inv : 0.0f;
-        if (!mine) continue;
+        for (int c = 0; c < 16; ++c) v[c] = some && nt > 0 ? __float_as_uint(__uint_as_float(v[c]) * inv) : 0u;
         if (it.slot >= 0) {
+          const int at = c0 % (D / 4) / 4;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4*>(ws_o + part * D + c + 4 * i) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          for (int c = 0; c < 4; ++c) *stage(lane, at + c) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+          if ((c0 + 16) % (D / 4) == 0)
+            flush(reinterpret_cast<uint8_t*>(ws_o) + (half * (D / 2) + c0 + 16 - D / 4) * 4, part, 4 * D);
         } else {
-          uint32_t o[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (a.f16) {
-              o[i] = h2_bits(__floats2half2_rn(y[2 * i], y[2 * i + 1]));
-            } else {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-              o[i] = *reinterpret_cast<const uint32_t*>(&h);
+          for (int c = 0; c < 2; ++c) {
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float y0 = __uint_as_float(v[8 * c + 2 * i]), y1 = __uint_as_float(v[8 * c + 2 * i + 1]);
+              if (a.f16) {
+                o[i] = h2_bits(__floats2half2_rn(y0, y1));
+              } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
+                o[i] = *reinterpret_cast<const uint32_t*>(&h);
+              }
             }
+            *stage(lane, c0 / 8 + c) = make_uint4(o[0], o[1], o[2], o[3]);
           }
-          uint4* const dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + c);
-          dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-          dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+          if (c0 + 16 == D / 2) flush(static_cast<uint8_t*>(a.out) + half * D, orow, 2 * D);
         }
       }
-      if (mine) {
+      if (mine && half == 0) {
+        const float ls = !some ? -INFINITY : odd ? __uint_as_float(0x7FC00000u) : mref - 8.0f + log2f(l);
         if (it.slot >= 0) ws_lse[part] = ls;
         else a.lse[orow] = ls * 0.6931471805599453f;
       }

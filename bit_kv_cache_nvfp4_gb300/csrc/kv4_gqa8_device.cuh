@@ -81,6 +81,69 @@ __device__ __forceinline__ void split_e4m3_same(uint32_t x, uint32_t (&t)[NT]) {
   }
 }
 
+// 16 values of q: widened to fp32; returns the bits of the largest magnitude.
+__device__ __forceinline__ uint32_t widen16(const uint4 (&w)[2], int f16, float (&x)[16]) {
+  const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (f16) {
+      const float2 f = __half22float2(bits_h2(u[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    } else {
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+    m = max(m, max(__float_as_uint(x[2 * i]) & 0x7FFFFFFFu, __float_as_uint(x[2 * i + 1]) & 0x7FFFFFFFu));
+  }
+  return m;
+}
+// Least e with amax <= 448 * 2^e, kept where 2^-e and 2^e are normal fp32.
+__device__ __forceinline__ int q_exponent(uint32_t amax_bits) {
+  const int e = static_cast<int>(amax_bits >> 23) - 135 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return min(max(e, -118), 118);
+}
+// 16 values times f (0 where `zero`) as NT terms of 16 bytes.
+template <int NT, bool kSame>
+__device__ __forceinline__ void terms16(const float (&x)[16], float f, bool zero, uint32_t (&o)[NT][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t t[2][NT];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float x0 = zero ? 0.0f : x[4 * i + 2 * k] * f, x1 = zero ? 0.0f : x[4 * i + 2 * k + 1] * f;
+      if constexpr (kSame) split_e4m3_same<NT>(h2_bits(__floats2half2_rn(x0, x1)), t[k]);
+      else split_e4m3<NT>(h2_bits(__floats2half2_rn(x0, x1)), t[k]);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) o[n][i] = t[0][n] | (t[1][n] << 16);
+  }
+}
+
+// Two fp32 operations in one instruction, each rounded as by itself.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Largest value over the warp (NaN only where every lane holds one).
 __device__ __forceinline__ float warp_max(float x) {
   float r;
