@@ -594,8 +594,8 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
       mbar_init(smem_addr(&sm.item_empty[i]), 19);        // the product's lane, 2 + 16 warps
       mbar_init(smem_addr(&sm.q_full[i]), 8);
       mbar_init(smem_addr(&sm.s_full[i]), 1);
-      mbar_init(smem_addr(&sm.p_full[i][0]), 4);
-      mbar_init(smem_addr(&sm.p_full[i][1]), 4);
+      mbar_init(smem_addr(&sm.p_full[i][0]), 8);
+      mbar_init(smem_addr(&sm.p_full[i][1]), 8);
       mbar_init(smem_addr(&sm.o_full[i]), 1);
     }
     for (int i = 0; i < 8; ++i) mbar_init(smem_addr(&sm.ex_full[i]), 1);
@@ -713,19 +713,23 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
         }
         __syncwarp();
       };
-      // (each half of P, 64 keys, lies over its own half of S)
+      // (P of each page lies over its own half of S; it comes in two parts, the
+      // first 32 keys of both pages and the others, so that the first products
+      // overlap the rest of the softmax)
       auto pv = [&](int qt, uint32_t j, bool first, uint32_t& par) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          wait(sm.p_full[qt][half], par);
+        for (int part = 0; part < 2; ++part) {
+          wait(sm.p_full[qt][part], par);
           __syncwarp();
           tc_fence_after_sync();
           if (elect_one()) {
             const uint64_t dv = dv0 + (j & 1) * (C::kV16 >> 4);
 #pragma unroll
-            for (int k = 4 * half; k < 4 * half + 4; ++k)
-              mma_f16_ts(tmem + 256 + qt * 128, tmem + qt * 128 + 64 * half + 8 * (k & 3), dv + ((k * 2048) >> 4),
-                         idesc_pv, !first || k > 0);
+            for (int i = 0; i < 4; ++i) {
+              const int k = 2 * part + (i & 1) + 4 * (i >> 1);       // 16 keys
+              mma_f16_ts(tmem + 256 + qt * 128, tmem + qt * 128 + 64 * (k >> 2) + 8 * (k & 3),
+                         dv + ((k * 2048) >> 4), idesc_pv, !first || part + i > 0);
+            }
           }
           __syncwarp();
         }
@@ -843,7 +847,7 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
     // ==== softmax: a thread is half a row, 64 keys of a tile ====
     setmaxnreg_inc<kSoftmaxRegs>();
     const int qt = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;
-    const int bar = 1 + qt;                               // the row tile's 8 warps
+    const int bar = 1 + qt * 4 + (warp & 3);              // the two warps of 32 rows
     const int wrow = (warp & 3) * 32, row = wrow + lane;  // of the row tile
     const uint32_t lanes = static_cast<uint32_t>(wrow) << 16;
     const uint32_t s_tm = tmem + qt * 128 + half * 64 + lanes;
@@ -853,7 +857,7 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
     for (uint32_t n_items = 0;; ++n_items) {
       const int s = n_items & 1;
       wait(sm.item_full[s], (n_items >> 1) & 1);
-      if (named_sync_or(bar, 256, *dead != 0)) break;     // (together, for they meet at barriers)
+      if (named_sync_or(bar, 64, *dead != 0)) break;     // (together, for they meet at barriers)
       const Gqa8Item it = sm.items[s];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
@@ -907,7 +911,7 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.q_full[qt]));
-        named_sync(bar, 256);                             // qf, by both halves' warps
+        named_sync(bar, 64);                             // qf
       }
       float qf = nt > 0 ? sm.qf[qt][row] : 0.0f;
       const bool odd = qf != qf;
@@ -951,7 +955,7 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
         const float f = fmaxf(qf * pow2f(ex == kMasked ? 0 : static_cast<int16_t>(ex & 0xFFFF)), 0x1p-126f);
         float top = fmaf(max3(m[0], m[1], fmaxf(m[2], m[3])), f, static_cast<float>(ev));
         sm.top[qt][j & 1][half][row] = top;
-        named_sync(bar, 256);
+        named_sync(bar, 64);
         top = fmaxf(top, sm.top[qt][j & 1][half ^ 1][row]);
         if (__any_sync(0xFFFFFFFFu, top > mref + 6.0f)) {
           const float to = fmaxf(top, mref), by = fast_exp2(mref - to);
@@ -985,11 +989,11 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
             p[c] = h2_bits(__floats2half2_rn(y.x, y.y));
           }
           tmem_st16(s_tm + 16 * q, p);
+          tmem_st_wait();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[qt][q]));
         }
-        tmem_st_wait();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[qt][half]));
         acc[0] = add2(acc[0], acc[1]);
         l = fmaf(acc[0].x + acc[0].y, pow2f(-ev), l);
       }
@@ -999,7 +1003,7 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
         ++n_work;
         tc_fence_after_sync();
       }
-      named_sync(bar, 256);
+      named_sync(bar, 64);
       l = sm.top[qt][j & 1][0][row] + sm.top[qt][j & 1][1][row];
       const float inv = odd && l > 0.0f ? __uint_as_float(0x7FC00000u) : 1.0f / l;
       const bool some = l > 0.0f || l != l;
