@@ -36,31 +36,50 @@ __device__ __forceinline__ int clamp_cu(int32_t v, int64_t n_tokens) {
 }
 
 // starts: first position of each request's range, or null: the range ends at
-// seq_lens (an append).
+// seq_lens (an append).  A warp looks for the request among 32 at a time, and
+// reads what it needs of the last 32 in the same round (of 32 requests or
+// fewer: one round of loads).
 __device__ __forceinline__ bool find_page(const Gqa8Args& a, int w, PageItem& it) {
-  int lo = 0, hi = a.B - 1;                       // largest b with g(b) <= w
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    const int g = (clamp_cu(__ldg(a.cu + mid), a.n_tokens) >> 6) + 2 * mid;
-    if (g <= w) lo = mid; else hi = mid - 1;
+  const int lane = threadIdx.x & 31;
+  int base = 0, n = a.B;                          // candidates base .. base + n - 1
+  while (true) {
+    const int step = (n + 31) / 32, b = base + lane * step;
+    const bool in = lane * step < n;
+    int c0 = 0, c1 = 0, at = 0;
+    if (in) {
+      c0 = __ldg(a.cu + b);
+      if (step == 1) {
+        c1 = __ldg(a.cu + b + 1);
+        at = __ldg((a.starts != nullptr ? a.starts : a.lens) + b);
+      }
+    }
+    c0 = clamp_cu(c0, a.n_tokens);
+    // the largest b with g(b) <= w
+    const uint32_t below = __ballot_sync(0xFFFFFFFFu, in && (c0 >> 6) + 2 * b <= w);
+    const int l = 31 - __clz(static_cast<int>(below | 1u));
+    if (step > 1) {
+      n = min(step, n - l * step);
+      base += l * step;
+      continue;
+    }
+    c0 = __shfl_sync(0xFFFFFFFFu, c0, l);
+    c1 = clamp_cu(__shfl_sync(0xFFFFFFFFu, c1, l), a.n_tokens);
+    at = __shfl_sync(0xFFFFFFFFu, at, l);
+    it.b = base + l;
+    const int p = w - (c0 >> 6) - 2 * it.b;
+    const int64_t rows = c1 - c0;
+    if (rows <= 0 || p < 0) return false;
+    int64_t start = a.starts != nullptr ? static_cast<int64_t>(at) : static_cast<int64_t>(at) - rows;
+    it.end = start + rows;
+    it.row0 = c0;
+    if (start < 0) {                              // tokens before position 0 have no place
+      it.row0 -= start;
+      start = 0;
+    }
+    it.start = start;
+    it.page = (start >> 6) + p;
+    return (it.page << 6) < it.end;
   }
-  const int c0 = clamp_cu(__ldg(a.cu + lo), a.n_tokens);
-  const int c1 = clamp_cu(__ldg(a.cu + lo + 1), a.n_tokens);
-  const int p = w - (c0 >> 6) - 2 * lo;
-  const int64_t n = c1 - c0;
-  if (n <= 0 || p < 0) return false;
-  int64_t start = a.starts != nullptr ? static_cast<int64_t>(__ldg(a.starts + lo))
-                                      : static_cast<int64_t>(__ldg(a.lens + lo)) - n;
-  it.b = lo;
-  it.end = start + n;
-  it.row0 = c0;
-  if (start < 0) {                                // tokens before position 0 have no place
-    it.row0 -= start;
-    start = 0;
-  }
-  it.start = start;
-  it.page = (start >> 6) + p;
-  return (it.page << 6) < it.end;
 }
 
 // Physical page, or -1 (flagged) where the table has none.
@@ -68,7 +87,7 @@ __device__ __forceinline__ int64_t physical_page(const Gqa8Args& a, const PageIt
   int64_t pg = -1;
   if (it.page < a.pt_stride) pg = __ldg(a.page_table + it.b * a.pt_stride + it.page);
   if (pg < 0 || pg >= a.num_pages) {
-    if (threadIdx.x == 0) flag_error(a.dev_err, kDevBadPage);
+    if ((threadIdx.x & 31) == 0) flag_error(a.dev_err, kDevBadPage);
     return -1;
   }
   return pg;
@@ -136,12 +155,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Gqa8Args a) {
   PageItem it;
   if (!find_page(a, blockIdx.x, it)) return;
   const int64_t pg = physical_page(a, it);
-  if (pg < 0) return;
   const int h = blockIdx.y, tid = threadIdx.x;
   const int lo = it.start > (it.page << 6) ? static_cast<int>(it.start & 63) : 0;
   const int hi = it.end - (it.page << 6) < kPage ? static_cast<int>(it.end - (it.page << 6)) : kPage;
   const int64_t row_of_0 = it.row0 + (it.page << 6) - it.start;     // flat row of the page's row 0
-  uint8_t* scale = a.scales + (pg * a.Hkv + h) * 2;
   const int col = (tid % TPR) * 16, r0 = tid / TPR;
   const uint16_t* src[2] = {static_cast<const uint16_t*>(a.k) + h * a.k_head_stride + col,
                             static_cast<const uint16_t*>(a.v) + h * a.v_head_stride + col};
@@ -159,6 +176,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Gqa8Args a) {
         x[s][p][1] = __ldg(g + 1);
       }
     }
+  if (pg < 0) return;
+  uint8_t* scale = a.scales + (pg * a.Hkv + h) * 2;
   // largest finite magnitude of each side, as fp32 bits (which order like the
   // values); a NaN or an infinity does not count and is flagged
   uint32_t m[2] = {0, 0};
@@ -219,6 +238,70 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Gqa8Args a) {
         *c = encode16(v, pow2f(old[s] - e));
       }
     }
+  }
+}
+
+// The same with a warp for each (page, head, side): where most pages get a
+// token or two (a decode step), a block a page would leave most of its threads
+// without a row.  The few rows are read twice, the second time from cache.
+template <int D, bool F16>
+__global__ void __launch_bounds__(128) append_rows_kernel(Gqa8Args a) {
+  constexpr int TPR = D / 16, RPP = 32 / TPR;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  PageItem it;
+  if (!find_page(a, blockIdx.x, it)) return;
+  const int64_t pg = physical_page(a, it);
+  const int lane = threadIdx.x & 31, unit = blockIdx.y * 4 + (threadIdx.x >> 5), h = unit >> 1, s = unit & 1;
+  if (h >= a.Hkv) return;
+  const int lo = it.start > (it.page << 6) ? static_cast<int>(it.start & 63) : 0;
+  const int hi = it.end - (it.page << 6) < kPage ? static_cast<int>(it.end - (it.page << 6)) : kPage;
+  const int64_t row_of_0 = it.row0 + (it.page << 6) - it.start;
+  const int col = (lane % TPR) * 16, r0 = lane / TPR;
+  const int64_t ts = s == 0 ? a.k_token_stride : a.v_token_stride;
+  const uint16_t* src = (s == 0 ? static_cast<const uint16_t*>(a.k) + h * a.k_head_stride
+                                : static_cast<const uint16_t*>(a.v) + h * a.v_head_stride) + col;
+  uint32_t m = 0;
+  bool odd = false;
+  auto row_in = [&](int r, float (&v)[16]) {
+    const uint4* g = reinterpret_cast<const uint4*>(src + (row_of_0 + r) * ts);
+    const uint4 x0 = __ldg(g), x1 = __ldg(g + 1);
+    widen8<F16>(x0, v);
+    widen8<F16>(x1, v + 8);
+  };
+  for (int r = lo + r0; r < hi; r += RPP) {
+    float v[16];
+    row_in(r, v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t u = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+      if (u >= 0x7F800000u) odd = true; else m = max(m, u);
+    }
+  }
+  if (pg < 0) return;
+  if (odd) flag_error(a.dev_err, kDevNonFinite);
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  uint8_t* const scale = a.scales + (pg * a.Hkv + h) * 2 + s;
+  int old = kGqa8ExpMin;
+  if (lo > 0) old = min(max(static_cast<int>(*scale) - 127, kGqa8ExpMin), kGqa8ExpMax);
+  const int e = max(block_exponent(m), old);
+  __syncwarp();
+  if (lane == 0) *scale = static_cast<uint8_t>(e + 127);
+  uint8_t* const blk = a.pool + ((pg * a.Hkv + h) * 2 + s) * (kPage * D) + col;
+  if (e > old && lo > 0) {
+    for (int r = r0; r < lo; r += RPP) {
+      uint4* c = reinterpret_cast<uint4*>(blk + r * D);
+      float v[16];
+      decode16(*c, v);
+      *c = encode16(v, pow2f(old - e));
+    }
+  }
+  for (int r = lo + r0; r < hi; r += RPP) {
+    float v[16];
+    row_in(r, v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = v[i] == v[i] ? v[i] : 0.0f;
+    *reinterpret_cast<uint4*>(blk + r * D) = encode16(v, pow2f(-e));
   }
 }
 
@@ -290,11 +373,10 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Gqa8Args a) {
 }
 
 template <typename K>
-cudaError_t launch_pages(K kernel, const Gqa8Args& a, cudaStream_t stream) {
+cudaError_t launch_pages(K kernel, const Gqa8Args& a, unsigned y, unsigned threads, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.n_tokens / kPage + 2 * static_cast<int64_t>(a.B)),
-                     static_cast<unsigned>(a.Hkv));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.n_tokens / kPage + 2 * static_cast<int64_t>(a.B)), y);
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -304,22 +386,27 @@ cudaError_t launch_pages(K kernel, const Gqa8Args& a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+template <int D, bool F16>
+cudaError_t launch_append(const Gqa8Args& a, cudaStream_t stream) {
+  // fewer than 8 tokens a request on average: a warp for each block of codes
+  if (a.n_tokens < 8 * static_cast<int64_t>(a.B))
+    return launch_pages(append_rows_kernel<D, F16>, a, (2 * a.Hkv + 3) / 4, 128, stream);
+  return launch_pages(append_kernel<D, F16>, a, a.Hkv, kThreads, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_append_gqa8(const Gqa8Args& a, cudaStream_t stream) {
-  if (a.D == 64)
-    return a.f16 ? launch_pages(append_kernel<64, true>, a, stream)
-                 : launch_pages(append_kernel<64, false>, a, stream);
-  return a.f16 ? launch_pages(append_kernel<128, true>, a, stream)
-               : launch_pages(append_kernel<128, false>, a, stream);
+  if (a.D == 64) return a.f16 ? launch_append<64, true>(a, stream) : launch_append<64, false>(a, stream);
+  return a.f16 ? launch_append<128, true>(a, stream) : launch_append<128, false>(a, stream);
 }
 
 cudaError_t launch_read_gqa8(const Gqa8Args& a, cudaStream_t stream) {
   if (a.D == 64)
-    return a.f16 ? launch_pages(read_kernel<64, true>, a, stream)
-                 : launch_pages(read_kernel<64, false>, a, stream);
-  return a.f16 ? launch_pages(read_kernel<128, true>, a, stream)
-               : launch_pages(read_kernel<128, false>, a, stream);
+    return a.f16 ? launch_pages(read_kernel<64, true>, a, a.Hkv, kThreads, stream)
+                 : launch_pages(read_kernel<64, false>, a, a.Hkv, kThreads, stream);
+  return a.f16 ? launch_pages(read_kernel<128, true>, a, a.Hkv, kThreads, stream)
+               : launch_pages(read_kernel<128, false>, a, a.Hkv, kThreads, stream);
 }
 
 }  // namespace kv4

@@ -70,6 +70,7 @@ struct FewSmall {
   int exps[12][2];            // per stage and page: K exponent | V exponent << 16; kMasked
   Gqa8Item items[4];
   float qf[2][32];            // sm_scale log2(e) 2^eq of a row, NaN where q is not finite
+  int pos[2][32];             // a row's position, -1 where it is negative
   alignas(16) float red[2][32 * 4];    // read as float4
   alignas(16) float2 stash[2][32];
   float lsum[4][32];
@@ -310,8 +311,10 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
         for (int off = 1; off < TPR; off <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
         const bool odd = m >= 0x7F800000u;                // a NaN or an infinity: NaN in its row
         const int e = q_exponent(m);
-        if (part == 0)
+        if (part == 0) {
+          sm.pos[qb][rr] = max(it.pos0 + (it.r0 + rr) / G, -1);
           sm.qf[qb][rr] = odd ? __uint_as_float(0x7FC00000u) : a.sm_scale * 1.4426950408889634f * pow2f(e);
+        }
         uint32_t o[NT][4];
         terms16<NT, false>(x, pow2f(-e), odd, o);
 #pragma unroll
@@ -414,12 +417,11 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
           }
         }
         if (edge || !live) {
-          const int64_t win = a.window > 0 ? a.window : (1LL << 40);
+          // 0 <= position - key < window
+          const uint32_t win = live ? (a.window > 0 ? a.window : 0x80000000u) : 0u;
 #pragma unroll
-          for (int r = 0; r < RP; ++r) {
-            const int64_t pos = static_cast<int64_t>(it.pos0) + (it.r0 + r) / G;
-            if (!live || at > pos || at <= pos - win) sc[r] = -INFINITY;
-          }
+          for (int r = 0; r < RP; ++r)
+            sc[r] = static_cast<uint32_t>(sm.pos[qb][r] - at) < win ? sc[r] : -INFINITY;
         }
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
@@ -472,35 +474,37 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
       // behind this barrier, which also frees lsum
       named_sync(kBar, 128);
       if (it.t_end > it.t_begin) join(n_tiles - 1);
-      float mine = 0.0f;
-#pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        const float x = warp_sum(l[r]);
-        if (lane == r) mine = x;
+      {
+        int r;
+        const float mine = warp_sums<RP>(l, lane, r);
+        sm.lsum[quarter][r] = mine;
       }
-      if (lane < RP) sm.lsum[quarter][lane] = mine;
       if (lane == 0) mbar_arrive(smem_addr(&sm.q_empty[qb]));
       named_sync(kBar, 128);
       const bool mine_d = D == 128 || lane < 16;          // M = 64: 16 lanes of each warp
       const int d = D == 128 ? key : quarter * 16 + lane;
+      int tok = it.r0 / G, g = it.r0 - tok * G;
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
         if (r >= it.nrows) break;
         const float lt = (sm.lsum[0][r] + sm.lsum[1][r]) + (sm.lsum[2][r] + sm.lsum[3][r]);
-        const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
-        const float ls = lt == 0.0f ? -INFINITY : mref[r] + log2f(lt);
+        const float y = lt == 0.0f ? 0.0f : __fdividef(o[r], lt);
+        const float ls = lt == 0.0f ? -INFINITY : mref[r] + fast_log2(lt);
         if (it.slot >= 0) {
           const int64_t row = static_cast<int64_t>(it.slot) * RP + r;
-          if (mine_d) ws_o[row * D + d] = o[r] * inv;
+          if (mine_d) ws_o[row * D + d] = y;
           if (key == 0) ws_lse[row] = ls;
         } else {
-          const int rr = it.r0 + r;
-          const int64_t row = static_cast<int64_t>(it.cu0 + rr / G) * a.Hq + it.h * G + rr % G;
+          const int64_t row = static_cast<int64_t>(it.cu0 + tok) * a.Hq + it.h * G + g;
           if (mine_d) {
-            if (a.f16) static_cast<__half*>(a.out)[row * D + d] = __float2half_rn(o[r] * inv);
-            else static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(o[r] * inv);
+            if (a.f16) static_cast<__half*>(a.out)[row * D + d] = __float2half_rn(y);
+            else static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(y);
           }
           if (key == 0) a.lse[row] = ls * 0.6931471805599453f;
+        }
+        if (++g == G) {
+          g = 0;
+          ++tok;
         }
       }
     }

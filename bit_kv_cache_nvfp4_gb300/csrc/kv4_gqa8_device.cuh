@@ -150,6 +150,28 @@ __device__ __forceinline__ float warp_max(float x) {
   asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
+// Sums over the warp of R values of each lane (R a power of two, up to 32):
+// every lane gets the sum of value `row`, with R + 3 or so shuffles in place
+// of 5 R.
+template <int R>
+__device__ __forceinline__ float warp_sums(float (&v)[R], int lane, int& row) {
+  int off = 16;
+  row = 0;
+#pragma unroll
+  for (int w = R / 2; w >= 1; w /= 2, off /= 2) {
+    const bool up = (lane & off) != 0;
+    row += up ? w : 0;
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const float give = up ? v[i] : v[i + w], keep = up ? v[i + w] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, off);
+    }
+  }
+  float x = v[0];
+#pragma unroll
+  for (; off > 0; off /= 2) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
+  return x;
+}
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
@@ -221,6 +243,14 @@ struct Gqa8Kind {     // of requests that one of the kernels takes
   int cost;           // of an item beyond its tiles
 };
 constexpr int kWhole = 4, kLeast = 2;
+
+// a / b of non-negative integers; nearly always both fit 32 bits, where the
+// division is several times as fast.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0)
+    return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 
 // Units of the requests of a warp's lanes: a lane by itself where it has few
 // row groups, the warp together for the others.
@@ -299,8 +329,10 @@ template <typename Emit>
 __device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, const Gqa8Kind& kind, int64_t total,
                                           Gqa8Tail* tails, int lane, Emit&& emit) {
   const int G = a.Hq / a.Hkv, blocks = gridDim.x, me = blockIdx.x;
-  // (a share holds at most one border's surroundings of an item)
-  const int64_t per = max((total + blocks - 1) / blocks, static_cast<int64_t>(kind.cost + kWhole));
+  // (no share so small that a long item's pieces would cost more to join than
+  // they save; where no item is ever cut, as small as one item)
+  const int64_t least = (a.pt_stride + 1) / 2 <= kWhole ? 1 : kWhole;
+  const int64_t per = max(quotient(total + blocks - 1, blocks), least);
   const int64_t u0 = me * per, u1 = u0 + per;
   bool tail = false;
   int64_t acc = 0;
@@ -348,7 +380,7 @@ __device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, const Gqa8Kind&
           const int t0 = __shfl_sync(0xFFFFFFFFu, sp.t0, gl), nt = __shfl_sync(0xFFFFFFFFu, sp.nt, gl);
           const int64_t at = __shfl_sync(0xFFFFFFFFu, g_end - w, gl);
           const int each = nt + kind.cost, r0 = (g0 + gl) * kind.rows, nrows = min(kind.rows, R - r0);
-          const int h0 = at < u0 ? static_cast<int>((u0 - at) / each) : 0;
+          const int h0 = at < u0 ? static_cast<int>(quotient(u0 - at, each)) : 0;
           int64_t begin = at + static_cast<int64_t>(h0) * each;
           for (int h = h0; h < a.Hkv && begin < u1; ++h, begin += each) {
             const int tb = gqa8_cut(u0, begin, nt, kind.cost), te = gqa8_cut(u1, begin, nt, kind.cost);
@@ -364,8 +396,8 @@ __device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, const Gqa8Kind&
               slot = 2 * me + 1;
               tail = true;
               // the last block that has some of it
-              int last = static_cast<int>((begin + each - 1) / per);
-              if (gqa8_cut(last * per, begin, nt, kind.cost) == nt) --last;
+              int last = static_cast<int>(quotient(begin + each - 1, per));
+              while (gqa8_cut(last * per, begin, nt, kind.cost) == nt) --last;
               if (lane == 0) tails[me] = Gqa8Tail{last - me + 1, r.cu0, h, r0, nrows, {}};
             }
             emit(Gqa8Item{base + l, h, r.cu0, r.pos0, r0, nrows, klo, khi, t0 + tb, t0 + te, slot});

@@ -469,3 +469,23 @@ def test_attention_reports_a_wait_that_runs_out():
         assert int(err.item()) == kv.DEV_TIMEOUT
         got = kv.attention_gqa8(*args)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("B,news", [(33, (1,)), (40, (0, 3, 70)), (1030, (1, 0, 2)), (1100, (9, 0, 1))])
+def test_append_and_read_many_requests(B, news):
+    """More requests than a warp looks at in one round, in two rounds; some
+    without a token."""
+    device = dev()
+    news = [news[i % len(news)] for i in range(B)]
+    lens = [n + (i * 13) % 90 for i, n in enumerate(news)]
+    c = ref.Cache(lens, 1, 64, device, seed=B)
+    cu = ref.cu_of(news)
+    g = torch.Generator(device=device).manual_seed(B)
+    x = (torch.randn(cu[-1], 2, 1, 64, device=device, generator=g) * 4).to(BF16)
+    assert run_append(x[:, 0], x[:, 1], cu, c) == 0
+    k, v = kv.read_gqa8(c.pool, c.scales, c.page_table, ints([n - m for n, m in zip(lens, news)], device),
+                        ints(cu, device), cu[-1])
+    for b in range(0, B, 7):
+        want = ref.values(c.pool, c.scales, c.table[b], lens[b] - news[b], lens[b])
+        assert torch.equal(k[cu[b]:cu[b + 1]].double(), want[:, 0].transpose(0, 1))
+        assert torch.equal(v[cu[b]:cu[b + 1]].double(), want[:, 1].transpose(0, 1))
