@@ -9,16 +9,17 @@
 // is exact, and a page whose exponent has to rise when tokens join it keeps
 // its codes exactly but for those that fall into the code's subnormal range.
 //
-// Both kernels give one thread block to one (page of a request, kv head): the
-// block is the unit whose maximum the write needs, and 2 x 64 x D values
-// (32 KB of inputs at D = 128) fit its threads' registers, so the inputs are
-// read once.
+// The write gives a thread block to one (page of a request, kv head, side),
+// the unit whose maximum it needs: its 64 x D values (16 KB of inputs at
+// D = 128) stay in the threads' registers between the maximum and the codes, so
+// the inputs are read once.  The read-back gives a block to a page and head.
 #include "kv4_gqa8_device.cuh"
 
 namespace kv4 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;         // of a block of the read-back
+constexpr int kAppendThreads = 128;   // and of the write
 
 // The page of request `b` that a block of the grid stands for.  Blocks are
 // laid out over page indices g(b) + p with g(b) = cu[b] / 64 + 2 b: a
@@ -110,6 +111,31 @@ __device__ __forceinline__ void widen8(const uint4& v, float* x) {
   }
 }
 
+// Largest magnitudes of two pairs of 16-bit values, pair by pair, a NaN where
+// there is one; then that of a pair, as fp32 bits (which order like the
+// values).
+template <bool F16>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t x) {
+  uint32_t r;
+  x &= 0x7FFF7FFFu;
+  if constexpr (F16) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x));
+  else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x));
+  return r;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t largest_bits(uint32_t m) {
+  float lo, hi;
+  if constexpr (F16) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+    lo = f.x;
+    hi = f.y;
+  } else {
+    lo = __uint_as_float(m << 16);
+    hi = __uint_as_float(m & 0xFFFF0000u);
+  }
+  return max(__float_as_uint(lo) & 0x7FFFFFFFu, __float_as_uint(hi) & 0x7FFFFFFFu);
+}
+
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float hi, float lo) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
@@ -145,98 +171,93 @@ __device__ __forceinline__ int block_exponent(uint32_t amax_bits) {
 }
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads) append_kernel(Gqa8Args a) {
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(Gqa8Args a) {
   constexpr int TPR = D / 16;                      // threads per token row
-  constexpr int RPP = kThreads / TPR;              // rows per pass
+  constexpr int RPP = kAppendThreads / TPR;        // rows per pass
   constexpr int PASSES = kPage / RPP;
   grid_dependency_wait();
   grid_launch_dependents();
-  __shared__ uint32_t red[2][kThreads / 32];
+  __shared__ uint32_t red[kAppendThreads / 32];
   PageItem it;
   if (!find_page(a, blockIdx.x, it)) return;
   const int64_t pg = physical_page(a, it);
-  const int h = blockIdx.y, tid = threadIdx.x;
+  const int h = blockIdx.y >> 1, s = blockIdx.y & 1, tid = threadIdx.x;
   const int lo = it.start > (it.page << 6) ? static_cast<int>(it.start & 63) : 0;
   const int hi = it.end - (it.page << 6) < kPage ? static_cast<int>(it.end - (it.page << 6)) : kPage;
   const int64_t row_of_0 = it.row0 + (it.page << 6) - it.start;     // flat row of the page's row 0
   const int col = (tid % TPR) * 16, r0 = tid / TPR;
-  const uint16_t* src[2] = {static_cast<const uint16_t*>(a.k) + h * a.k_head_stride + col,
-                            static_cast<const uint16_t*>(a.v) + h * a.v_head_stride + col};
-  const int64_t ts[2] = {a.k_token_stride, a.v_token_stride};
-  uint4 x[2][PASSES][2];
+  const int64_t ts = s == 0 ? a.k_token_stride : a.v_token_stride;
+  const uint16_t* src = (s == 0 ? static_cast<const uint16_t*>(a.k) + h * a.k_head_stride
+                                : static_cast<const uint16_t*>(a.v) + h * a.v_head_stride) + col;
+  uint4 x[PASSES][2];
 #pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int r = r0 + p * RPP;
-      x[s][p][0] = x[s][p][1] = make_uint4(0, 0, 0, 0);
-      if (r >= lo && r < hi) {
-        const uint4* g = reinterpret_cast<const uint4*>(src[s] + (row_of_0 + r) * ts[s]);
-        x[s][p][0] = __ldg(g);
-        x[s][p][1] = __ldg(g + 1);
-      }
+  for (int p = 0; p < PASSES; ++p) {
+    const int r = r0 + p * RPP;
+    x[p][0] = x[p][1] = make_uint4(0, 0, 0, 0);
+    if (r >= lo && r < hi) {
+      const uint4* g = reinterpret_cast<const uint4*>(src + (row_of_0 + r) * ts);
+      x[p][0] = __ldg(g);
+      x[p][1] = __ldg(g + 1);
     }
+  }
   if (pg < 0) return;
-  uint8_t* scale = a.scales + (pg * a.Hkv + h) * 2;
-  // largest finite magnitude of each side, as fp32 bits (which order like the
-  // values); a NaN or an infinity does not count and is flagged
-  uint32_t m[2] = {0, 0};
-  bool odd = false;
+  uint8_t* const scale = a.scales + (pg * a.Hkv + h) * 2 + s;
+  uint32_t m2 = 0;
 #pragma unroll
-  for (int s = 0; s < 2; ++s)
+  for (int p = 0; p < PASSES; ++p)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      m2 = max_abs2<F16>(max_abs2<F16>(m2, x[p][j].x), x[p][j].y);
+      m2 = max_abs2<F16>(max_abs2<F16>(m2, x[p][j].z), x[p][j].w);
+    }
+  uint32_t m = largest_bits<F16>(m2);
+  // (nearly always none:) a NaN or an infinity does not count and is flagged,
+  // and a NaN gives code 0
+  const bool odd = m >= 0x7F800000u;
+  if (odd) {
+    flag_error(a.dev_err, kDevNonFinite);
+    m = 0;
 #pragma unroll
     for (int p = 0; p < PASSES; ++p)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float f[8];
-        widen8<F16>(x[s][p][j], f);
+        widen8<F16>(x[p][j], f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint32_t u = __float_as_uint(f[i]) & 0x7FFFFFFFu;
-          if (u >= 0x7F800000u) odd = true; else m[s] = max(m[s], u);
+          if (u < 0x7F800000u) m = max(m, u);
         }
       }
-  if (odd) flag_error(a.dev_err, kDevNonFinite);
-  m[0] = __reduce_max_sync(0xFFFFFFFFu, m[0]);
-  m[1] = __reduce_max_sync(0xFFFFFFFFu, m[1]);
-  if ((tid & 31) == 0) {
-    red[0][tid >> 5] = m[0];
-    red[1][tid >> 5] = m[1];
   }
-  int old[2] = {kGqa8ExpMin, kGqa8ExpMin};
-  if (lo > 0) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int e = static_cast<int>(scale[s]) - 127;
-      old[s] = e < kGqa8ExpMin ? kGqa8ExpMin : (e > kGqa8ExpMax ? kGqa8ExpMax : e);
-    }
-  }
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  if ((tid & 31) == 0) red[tid >> 5] = m;
+  int old = kGqa8ExpMin;
+  if (lo > 0) old = min(max(static_cast<int>(*scale) - 127, kGqa8ExpMin), kGqa8ExpMax);
   __syncthreads();
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    uint32_t mm = 0;
+  for (int i = 0; i < kAppendThreads / 32; ++i) m = max(m, red[i]);
+  const int e = max(block_exponent(m), old);
+  if (tid == 0) *scale = static_cast<uint8_t>(e + 127);
+  uint8_t* const blk = a.pool + ((pg * a.Hkv + h) * 2 + s) * (kPage * D) + col;
+  const float f = pow2f(-e);
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) mm = max(mm, red[s][i]);
-    const int e = max(block_exponent(mm), old[s]);
-    if (tid == 0) scale[s] = static_cast<uint8_t>(e + 127);
-    uint8_t* blk = a.pool + ((pg * a.Hkv + h) * 2 + s) * (kPage * D) + col;
-    const float f = pow2f(-e);
+  for (int p = 0; p < PASSES; ++p) {
+    const int r = r0 + p * RPP;
+    if (r >= lo && r < hi) {
+      float v[16];
+      widen8<F16>(x[p][0], v);
+      widen8<F16>(x[p][1], v + 8);
+      if (odd) {
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int r = r0 + p * RPP;
-      if (r >= lo && r < hi) {
-        float v[16];
-        widen8<F16>(x[s][p][0], v);
-        widen8<F16>(x[s][p][1], v + 8);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = v[i] == v[i] ? v[i] : 0.0f;      // NaN -> 0
-        *reinterpret_cast<uint4*>(blk + r * D) = encode16(v, f);
-      } else if (r < lo && e > old[s]) {
-        uint4* c = reinterpret_cast<uint4*>(blk + r * D);
-        float v[16];
-        decode16(*c, v);
-        *c = encode16(v, pow2f(old[s] - e));
+        for (int i = 0; i < 16; ++i) v[i] = v[i] == v[i] ? v[i] : 0.0f;
       }
+      *reinterpret_cast<uint4*>(blk + r * D) = encode16(v, f);
+    } else if (r < lo && e > old) {
+      uint4* c = reinterpret_cast<uint4*>(blk + r * D);
+      float v[16];
+      decode16(*c, v);
+      *c = encode16(v, pow2f(old - e));
     }
   }
 }
@@ -391,7 +412,7 @@ cudaError_t launch_append(const Gqa8Args& a, cudaStream_t stream) {
   // fewer than 8 tokens a request on average: a warp for each block of codes
   if (a.n_tokens < 8 * static_cast<int64_t>(a.B))
     return launch_pages(append_rows_kernel<D, F16>, a, (2 * a.Hkv + 3) / 4, 128, stream);
-  return launch_pages(append_kernel<D, F16>, a, a.Hkv, kThreads, stream);
+  return launch_pages(append_kernel<D, F16>, a, 2 * a.Hkv, kAppendThreads, stream);
 }
 
 }  // namespace
