@@ -1,4 +1,5 @@
-"""Build libkv4mla.so in place with nvcc for sm_103a (GB300).
+"""Build libkv4mla.so in place with nvcc for sm_103a (GB300), and the PyTorch
+side of its *_gqa8 entry points, the extension module _kv4torch, with g++.
 
 Each translation unit under ``csrc/`` is compiled in parallel with
 ``-gencode arch=compute_103a,code=sm_103a -O3 -lineinfo`` (IEEE division and
@@ -19,6 +20,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libkv4mla.so")
+TORCH_PATH = os.path.join(HERE, "_kv4torch.so")
+TORCH_STAMP = os.path.join(BUILD_DIR, "torch_version")   # what _kv4torch.so was built with
+TORCH_SOURCE = "kv4_torch.cpp"
 SOURCES = ["kv4_capi.cu", "kv4_quantize_write.cu", "kv4_sparse_mla_decode.cu", "kv4_dcp.cu",
            "kv4_gqa8.cu", "kv4_gqa8_attention.cu"]
 HEADERS = ["kv4_device.cuh", "kv4_gqa8_device.cuh", "kv4_launch.h"]
@@ -32,13 +36,40 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libkv4mla.so")
 
 
+def _torch_version() -> str:
+    import torch
+    return torch.__version__
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not (os.path.exists(LIB_PATH) and os.path.exists(TORCH_PATH) and os.path.exists(TORCH_STAMP)):
         return True
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
+    with open(TORCH_STAMP) as f:
+        if f.read() != _torch_version():
+            return True
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [TORCH_SOURCE]]
     deps.append(os.path.join(INCLUDE, "kv4mla.h"))
     deps.append(os.path.abspath(__file__))
-    return os.path.getmtime(LIB_PATH) < max(os.path.getmtime(p) for p in deps)
+    built = min(os.path.getmtime(LIB_PATH), os.path.getmtime(TORCH_PATH))
+    return built < max(os.path.getmtime(p) for p in deps)
+
+
+def _torch_object():
+    """(object path, compile command, link flags) of the extension module."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    obj = os.path.join(BUILD_DIR, "kv4_torch.o")
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    compile_cmd = (["g++", "-O2", "-std=c++20", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+                   + [f for d in inc for f in ("-isystem" if d != INCLUDE else "-I", d)]
+                   + ["-c", os.path.join(CSRC, TORCH_SOURCE), "-o", obj])
+    link = ["-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+            "-L", HERE, "-l:libkv4mla.so", "-Wl,-rpath,$ORIGIN"]
+    return obj, compile_cmd, link
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
@@ -59,6 +90,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                             stderr=subprocess.STDOUT, text=True)))
+    torch_obj, torch_cmd, torch_link = _torch_object()
+    if verbose:
+        print(" ".join(torch_cmd), flush=True)
+    procs.append((TORCH_SOURCE, subprocess.Popen(torch_cmd, stdout=subprocess.PIPE,
+                                                 stderr=subprocess.STDOUT, text=True)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -67,11 +103,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         if p.returncode != 0:
             failed.append(src)
     if failed:
-        raise RuntimeError(f"nvcc failed for {failed}")
+        raise RuntimeError(f"compilation failed for {failed}")
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB_PATH)
+    tmp = TORCH_PATH + f".tmp{os.getpid()}"
+    subprocess.run(["g++", "-shared", "-o", tmp, torch_obj] + torch_link, check=True)
+    os.replace(tmp, TORCH_PATH)
+    with open(TORCH_STAMP, "w") as f:
+        f.write(_torch_version())
     return LIB_PATH
 
 
