@@ -123,7 +123,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
   grid_dependency_wait();
   grid_launch_dependents();
   __syncthreads();
-  const Gqa8Kind kind{1, max_rows, RP, kFewCost};
+  const Gqa8Kind kind{1, max_rows, RP, kFewCost, RP, 1};
   gqa8_total(a, kind, blockIdx.x == 0, &sm.total);
   fence_async_smem();
   tc_fence_before_sync();
@@ -519,7 +519,9 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
 // ---------------------------------------------------------------------------
 // What bounds this case is the tensor core: 4 D flops a pair of row and key.
 // An item is 256 rows of one kv head, two M = 128 tiles that take turns: while
-// the softmax of one works on its scores, the products of the other run.
+// the softmax of one works on its scores, the products of the other run.  Of an
+// item with at most 128 rows the two are the same rows over every other tile of
+// keys, joined at its end, so that they take turns all the same.
 //   S[128 rows x 128 keys] = sum_t Q_t . K^T     kind::f8f6f4, NT terms of q
 //   O[128 rows x D] += P . V                     kind::f16, P from TMEM
 // K goes in as its codes, against q split into E4M3 terms (bf16: two, f16:
@@ -542,7 +544,7 @@ struct ManyCfg {
   static constexpr int kV16 = kTileKeys * D * 2;
   static constexpr int kQ = NT * 128 * D;                 // of one of the two row tiles
   static constexpr int kKStages = NT == 2 ? 3 : 2, kVStages = NT == 2 ? 2 : 1;
-  static constexpr int kSmall = 6144;
+  static constexpr int kSmall = 9216;
   static constexpr int kSmem = 2 * kQ + kKStages * kK + kVStages * kK + 2 * kV16 + kSmall + 1024;
 };
 static_assert(ManyCfg<128, 3>::kSmem <= 227 * 1024 && ManyCfg<128, 2>::kSmem <= 227 * 1024, "shared memory");
@@ -550,7 +552,7 @@ constexpr int kManyThreads = 640;
 constexpr uint32_t kSoftmaxRegs = 104, kOtherRegs = 64, kLaunchRegs = 96;
 static_assert(4 * kSoftmaxRegs + kOtherRegs <= 5 * kLaunchRegs, "register shares draw on the launch's");
 
-constexpr int kManyCost = 4;   // of an item, in tiles: q in, first scores, last product, output
+constexpr int kManyCost = 6;   // of an item, in half tiles: q in, first scores, last product, output
 
 struct ManySmall {
   uint64_t k_full[3], k_empty[3], v8_full[2], v8_empty[2], v_full[2], v_empty[2], item_full[2], item_empty[2],
@@ -561,10 +563,10 @@ struct ManySmall {
   int exps[8][2];
   Gqa8Item items[2];
   float qf[2][128];           // sm_scale log2(e) 2^eq of a row, NaN where q is not finite
-  float top[2][2][2][128];    // largest score and V exponent of a half row, by row tile and tile parity;
-                              // an item's last sums in the parity its next tile would have
+  float top[2][2][2][128];    // largest score and V exponent of a half row, by row tile and tile parity
+  float last[2][3][128];      // at an item's end: sums of both halves, reference
 };
-static_assert(sizeof(ManySmall) <= 6144, "ManySmall");
+static_assert(sizeof(ManySmall) <= 9216, "ManySmall");
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kManyThreads, 1)
@@ -613,7 +615,7 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
   grid_dependency_wait();
   grid_launch_dependents();
   __syncthreads();
-  const Gqa8Kind kind{min_rows, kAll, C::kRows, kManyCost};
+  const Gqa8Kind kind{min_rows, kAll, C::kRows, kManyCost, 128, 2};
   gqa8_total(a, kind, blockIdx.x == 0 && min_rows == 1, &sm.total);
   tc_fence_before_sync();
   __syncthreads();
@@ -705,9 +707,9 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
       const uint64_t dv0 = smem_desc(smem_addr(v_s), kSlab, 1024, kSwizzle128);
       uint32_t n_tiles = 0, ks = 0, k_par = 0;            // stage of K and its parity
       uint32_t w0 = 0, w1 = 0, p0 = 0, p1 = 0;            // parities of the row tiles' q and P
-      auto qk = [&](int qt, uint32_t stage) {
+      auto qk = [&](int qt, uint32_t stage, int q) {
         if (elect_one()) {
-          const uint64_t dk = dk0 + stage * (C::kK >> 4), dq = dq0 + qt * (C::kQ >> 4);
+          const uint64_t dk = dk0 + stage * (C::kK >> 4), dq = dq0 + q * (C::kQ >> 4);
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -756,31 +758,59 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
           wait(sm.q_full[1], w1);
           w1 ^= 1;
         }
-        for (int t = 0; t <= nt; ++t) {
-          const uint32_t j = n_tiles + t;
-          if (t < nt) wait(sm.k_full[ks], k_par);
-          if (t > 0) wait(sm.v_full[(j - 1) & 1], ((j - 1) >> 1) & 1);
-          __syncwarp();
-          tc_fence_after_sync();
-          // P of a row tile lies over its S: the products run in order
-          if (t > 0) pv(0, j - 1, t == 1, p0);
-          if (t < nt) qk(0, ks);
-          if (two) {
-            if (t > 0) pv(1, j - 1, t == 1, p1);
-            if (t < nt) qk(1, ks);
-          }
-          if (elect_one()) {
-            if (t > 0) mma_commit(smem_addr(&sm.v_empty[(j - 1) & 1]));
-            if (t < nt) mma_commit(smem_addr(&sm.k_empty[ks]));
-            if (t == nt) {
-              mma_commit(smem_addr(&sm.o_full[0]));
-              if (two) mma_commit(smem_addr(&sm.o_full[1]));
-            }
-          }
-          __syncwarp();
-          if (t < nt && ++ks == KS) {
+        auto next_k = [&] {
+          if (++ks == KS) {
             ks = 0;
             k_par ^= 1;
+          }
+        };
+        // (P of a row tile lies over its S: the products run in order)
+        if (two) {
+          for (int t = 0; t <= nt; ++t) {
+            const uint32_t j = n_tiles + t;
+            if (t < nt) wait(sm.k_full[ks], k_par);
+            if (t > 0) wait(sm.v_full[(j - 1) & 1], ((j - 1) >> 1) & 1);
+            __syncwarp();
+            tc_fence_after_sync();
+            if (t > 0) pv(0, j - 1, t == 1, p0);
+            if (t < nt) qk(0, ks, 0);
+            if (t > 0) pv(1, j - 1, t == 1, p1);
+            if (t < nt) qk(1, ks, 1);
+            if (elect_one()) {
+              if (t > 0) mma_commit(smem_addr(&sm.v_empty[(j - 1) & 1]));
+              if (t < nt) {
+                mma_commit(smem_addr(&sm.k_empty[ks]));
+              } else {
+                mma_commit(smem_addr(&sm.o_full[0]));
+                mma_commit(smem_addr(&sm.o_full[1]));
+              }
+            }
+            __syncwarp();
+            if (t < nt) next_k();
+          }
+        } else {
+          // tile t is row tile t & 1's; its P two tiles on
+          for (int t = 0; t < nt + 2; ++t) {
+            const uint32_t j = n_tiles + t;
+            if (t < nt) wait(sm.k_full[ks], k_par);
+            if (t >= 2) wait(sm.v_full[j & 1], ((j - 2) >> 1) & 1);
+            __syncwarp();
+            tc_fence_after_sync();
+            if (t >= 2) {
+              if (t & 1) pv(1, j - 2, t == 3, p1);
+              else pv(0, j - 2, t == 2, p0);
+              if (elect_one()) {
+                mma_commit(smem_addr(&sm.v_empty[j & 1]));
+                if (t >= nt) mma_commit(smem_addr(&sm.o_full[t & 1]));
+              }
+              __syncwarp();
+            }
+            if (t < nt) {
+              qk(t & 1, ks, 0);
+              if (elect_one()) mma_commit(smem_addr(&sm.k_empty[ks]));
+              __syncwarp();
+              next_k();
+            }
           }
         }
         n_tiles += nt;
@@ -852,6 +882,7 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
     setmaxnreg_inc<kSoftmaxRegs>();
     const int qt = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;
     const int bar = 1 + qt * 4 + (warp & 3);              // the two warps of 32 rows
+    const int bar_rows = 9 + (warp & 3);                  // and those of the other row tile
     const int wrow = (warp & 3) * 32, row = wrow + lane;  // of the row tile
     const uint32_t lanes = static_cast<uint32_t>(wrow) << 16;
     const uint32_t s_tm = tmem + qt * 128 + half * 64 + lanes;
@@ -861,25 +892,23 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
     for (uint32_t n_items = 0;; ++n_items) {
       const int s = n_items & 1;
       wait(sm.item_full[s], (n_items >> 1) & 1);
-      if (named_sync_or(bar, 64, *dead != 0)) break;     // (together, for they meet at barriers)
+      if (named_sync_or(bar_rows, 128, *dead != 0)) break;     // (together, for they meet at barriers)
       const Gqa8Item it = sm.items[s];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
       if (it.b < 0) break;
       const int nt = it.t_end - it.t_begin;
-      if (qt * 128 >= it.nrows) {                         // no second row tile
-        j += nt;
-        continue;
-      }
-      const bool mine = qt * 128 + row < it.nrows;
+      const bool shared = it.nrows <= 128;                // both row tiles are the same rows
+      const int base = shared ? 0 : qt * 128;
+      const bool mine = base + row < it.nrows;
       // keys at < hi and >= lo are this row's
       int hi = 0, lo = 0;
       if (mine) {
-        const int64_t pos = static_cast<int64_t>(it.pos0) + (it.r0 + qt * 128 + row) / G;
+        const int64_t pos = static_cast<int64_t>(it.pos0) + (it.r0 + base + row) / G;
         hi = static_cast<int>(max(min(pos + 1, static_cast<int64_t>(it.khi)), static_cast<int64_t>(0)));
         if (a.window > 0) lo = static_cast<int>(max(pos - a.window + 1, static_cast<int64_t>(0)));
       }
-      if (nt > 0) {
+      if (nt > 0 && !(shared && qt == 1)) {
         // 16 of the warp's rows of q (the other half's warp has the others) as
         // NT E4M3 terms, kTpr threads a row
         constexpr int kTpr = D / 16, kRpp = 32 / kTpr;
@@ -888,9 +917,9 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
 #pragma unroll 2
         for (int p = 0; p < 16 / kRpp; ++p) {
           const int rr = wrow + half * 16 + p * kRpp + lane / kTpr;
-          const int gr = it.r0 + qt * 128 + rr;
+          const int gr = it.r0 + base + rr;
           uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-          if (qt * 128 + rr < it.nrows) {
+          if (base + rr < it.nrows) {
             const uint4* g = reinterpret_cast<const uint4*>(
                 static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(it.cu0 + gr / G) * a.q_token_stride +
                 static_cast<int64_t>(it.h * G + gr % G) * a.q_head_stride + part * 16);
@@ -915,15 +944,19 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.q_full[qt]));
-        named_sync(bar, 64);                             // qf
       }
-      float qf = nt > 0 ? sm.qf[qt][row] : 0.0f;
+      // qf is there for the warps that read it
+      if (shared) named_sync(bar_rows, 128);
+      else named_sync(bar, 64);
+      float qf = nt > 0 ? sm.qf[shared ? 0 : qt][row] : 0.0f;
       const bool odd = qf != qf;
       if (odd) qf = 0.0f;
       float mref = kLowest, l = 0.0f;
-      for (int t = it.t_begin; t < it.t_end; ++t, ++j, ++n_mine) {
-        wait(sm.ex_full[j & 7], (j >> 3) & 1);
-        const int ex = sm.exps[j & 7][half];
+      const int first = it.t_begin + (shared ? qt : 0), step = shared ? 2 : 1;
+      for (int t = first; t < it.t_end; t += step, ++n_mine) {
+        const uint32_t jt = j + (t - it.t_begin);
+        wait(sm.ex_full[jt & 7], (jt >> 3) & 1);
+        const int ex = sm.exps[jt & 7][half];
         wait(sm.s_full[qt], n_mine & 1);
         tc_fence_after_sync();
         float x[64];
@@ -958,14 +991,14 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
         // (at least 2^-126, so that a masked -inf stays one where the scale is 0)
         const float f = fmaxf(qf * pow2f(ex == kMasked ? 0 : static_cast<int16_t>(ex & 0xFFFF)), 0x1p-126f);
         float top = fmaf(max3(m[0], m[1], fmaxf(m[2], m[3])), f, static_cast<float>(ev));
-        sm.top[qt][j & 1][half][row] = top;
+        sm.top[qt][n_mine & 1][half][row] = top;
         named_sync(bar, 64);
-        top = fmaxf(top, sm.top[qt][j & 1][half ^ 1][row]);
+        top = fmaxf(top, sm.top[qt][n_mine & 1][half ^ 1][row]);
         if (__any_sync(0xFFFFFFFFu, top > mref + 6.0f)) {
           const float to = fmaxf(top, mref), by = fast_exp2(mref - to);
           mref = to;
           l *= by;
-          if (t > it.t_begin) {
+          if (t > first) {
             // s_full came behind the last product into this O; each half takes
             // its columns
 #pragma unroll 1
@@ -1001,56 +1034,90 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
         acc[0] = add2(acc[0], acc[1]);
         l = fmaf(acc[0].x + acc[0].y, pow2f(-ev), l);
       }
-      sm.top[qt][j & 1][half][row] = l;
-      if (nt > 0) {
+      j += nt;
+      sm.last[qt][half][row] = l;
+      if (half == 0) sm.last[qt][2][row] = mref;
+      if (first < it.t_end) {
         wait(sm.o_full[qt], n_work & 1);
         ++n_work;
         tc_fence_after_sync();
       }
-      named_sync(bar, 64);
-      l = sm.top[qt][j & 1][0][row] + sm.top[qt][j & 1][1][row];
+      if (shared) named_sync(bar_rows, 128);
+      else named_sync(bar, 64);
+      // out = (O_a w_a + O_b w_b) / (l_a w_a + l_b w_b), b the other row tile of
+      // the same rows; both halves read the same numbers
+      const int ta = shared ? 0 : qt;
+      float wa = 1.0f, wb = 0.0f, lb = 0.0f;
+      mref = sm.last[ta][2][row];
+      l = sm.last[ta][0][row] + sm.last[ta][1][row];
+      if (shared) {
+        lb = sm.last[1][0][row] + sm.last[1][1][row];
+        const float mb = sm.last[1][2][row], to = fmaxf(mref, mb);
+        wa = fast_exp2(mref - to);
+        wb = fast_exp2(mb - to);
+        mref = to;
+      }
+      const bool has_a = nt > 0 && l != 0.0f, has_b = lb != 0.0f;      // (else O may be anything)
+      l = l * wa + lb * wb;
       const float inv = odd && l > 0.0f ? __uint_as_float(0x7FC00000u) : 1.0f / l;
       const bool some = l > 0.0f || l != l;
-      const int r = it.r0 + qt * 128 + row;
-      const int64_t part = static_cast<int64_t>(it.slot) * C::kRows + qt * 128 + row;
+      wa *= inv;
+      wb *= inv;
+      const int r = it.r0 + base + row;
+      const int64_t part = static_cast<int64_t>(it.slot) * C::kRows + base + row;
       const int64_t orow = static_cast<int64_t>(it.cu0 + r / G) * a.Hq + it.h * G + r % G;
-      // Out through the rows of q's first two terms, one for each half of the
-      // columns, which no product reads any more, so that the stores to memory
-      // are D contiguous bytes: a half row of 16 bits, a quarter row of fp32.
-      constexpr int kCpr = D / 16;                        // 16-byte chunks of D bytes
+      // Out through the rows of q's first two terms, which no product reads any
+      // more, so that the stores to memory are up to D contiguous bytes: this
+      // warp's columns of 16 bits, or half of them in fp32.
+      const int cols = shared ? D / 4 : D / 2, col0 = (shared ? 2 * qt + half : half) * cols;
+      const uint32_t oa_tm = tmem + 256 + ta * 128 + lanes + col0, ob_tm = tmem + 256 + 128 + lanes + col0;
       auto stage = [&](int rr, int c) {
         return reinterpret_cast<uint4*>(q_mine + half * (128 * D) + swizzle<D == 128 ? 3 : 2>((wrow + rr) * D + c * 16));
       };
-      auto flush = [&](uint8_t* base, int64_t to, int64_t row_bytes) {
+      // 16-byte chunks of a row: D / 16, half as many where the columns are shared and of 16 bits
+      const int lg = (D == 128 ? 3 : 2) - (shared && it.slot < 0 ? 1 : 0);
+      auto flush = [&](uint8_t* to, int64_t at, int64_t row_bytes) {
         __syncwarp();
 #pragma unroll 4
-        for (int i = 0; i < kCpr; ++i) {
-          const int rr = (i * 32 + lane) / kCpr, c = lane % kCpr;
-          const int64_t dst = __shfl_sync(0xFFFFFFFFu, to, rr);
+        for (int i = lane; i < 32 << lg; i += 32) {
+          const int rr = i >> lg, c = i & ((1 << lg) - 1);
+          const int64_t dst = __shfl_sync(0xFFFFFFFFu, at, rr);
           const uint4 v = *stage(rr, c);
-          if (qt * 128 + wrow + rr < it.nrows) *reinterpret_cast<uint4*>(base + dst * row_bytes + c * 16) = v;
+          if (base + wrow + rr < it.nrows) *reinterpret_cast<uint4*>(to + dst * row_bytes + c * 16) = v;
         }
         __syncwarp();
       };
 #pragma unroll 1
-      for (int c0 = 0; c0 < D / 2; c0 += 16) {            // of this half's columns
+      for (int c0 = 0; c0 < cols; c0 += 16) {             // of this warp's columns
         uint32_t v[16];
-        if (nt > 0) tmem_ld16_sync(o_tm + c0, v);
+        float y[16];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) v[c] = some && nt > 0 ? __float_as_uint(__uint_as_float(v[c]) * inv) : 0u;
+        for (int c = 0; c < 16; ++c) y[c] = 0.0f;
+        if (nt > 0) {
+          tmem_ld16_sync(oa_tm + c0, v);
+          if (has_a)
+#pragma unroll
+            for (int c = 0; c < 16; ++c) y[c] = __uint_as_float(v[c]) * wa;
+        }
+        if (shared && nt > 1) {
+          tmem_ld16_sync(ob_tm + c0, v);
+          if (has_b)
+#pragma unroll
+            for (int c = 0; c < 16; ++c) y[c] = fmaf(__uint_as_float(v[c]), wb, y[c]);
+        }
         if (it.slot >= 0) {
           const int at = c0 % (D / 4) / 4;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) *stage(lane, at + c) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+          for (int c = 0; c < 4; ++c) *stage(lane, at + c) = make_uint4(__float_as_uint(y[4 * c]), __float_as_uint(y[4 * c + 1]), __float_as_uint(y[4 * c + 2]), __float_as_uint(y[4 * c + 3]));
           if ((c0 + 16) % (D / 4) == 0)
-            flush(reinterpret_cast<uint8_t*>(ws_o) + (half * (D / 2) + c0 + 16 - D / 4) * 4, part, 4 * D);
+            flush(reinterpret_cast<uint8_t*>(ws_o) + (col0 + c0 + 16 - D / 4) * 4, part, 4 * D);
         } else {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float y0 = __uint_as_float(v[8 * c + 2 * i]), y1 = __uint_as_float(v[8 * c + 2 * i + 1]);
+              const float y0 = y[8 * c + 2 * i], y1 = y[8 * c + 2 * i + 1];
               if (a.f16) {
                 o[i] = h2_bits(__floats2half2_rn(y0, y1));
               } else {
@@ -1060,15 +1127,17 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
             }
             *stage(lane, c0 / 8 + c) = make_uint4(o[0], o[1], o[2], o[3]);
           }
-          if (c0 + 16 == D / 2) flush(static_cast<uint8_t*>(a.out) + half * D, orow, 2 * D);
+          if (c0 + 16 == cols) flush(static_cast<uint8_t*>(a.out) + col0 * 2, orow, 2 * D);
         }
       }
-      if (mine && half == 0) {
+      if (mine && half == 0 && base == qt * 128) {
         const float ls = !some ? -INFINITY : odd ? __uint_as_float(0x7FC00000u) : mref - 8.0f + log2f(l);
         if (it.slot >= 0) ws_lse[part] = ls;
         else a.lse[orow] = ls * 0.6931471805599453f;
       }
       tc_fence_before_sync();
+      // (both tiles of O, and `last`, are read before a warp goes on)
+      if (shared) named_sync(bar_rows, 128);
     }
   }
   tc_fence_before_sync();

@@ -183,9 +183,9 @@ __device__ __forceinline__ float warp_sum(float x) {
 // the group); `rows` consecutive ones, of one kv head, are an item, which
 // walks its keys in tiles of 128 (tile t: keys 128 t .. 128 t + 127, two
 // pages).  Items are ordered by request, row group, kv head; each counts for
-// its tiles and `cost` more (what starting and ending an item takes, in
-// tiles), and every block takes an equal share of the whole, found from the
-// lengths on the device.  An item that a border between two shares falls into
+// its tiles and `cost` more (what starting and ending an item takes), in units
+// of which a tile has one or more, and every block takes an equal share of the
+// whole, found from the lengths on the device.  An item that a border between two shares falls into
 // is cut there, unless it has few tiles or the cut would leave fewer than
 // kLeast to a side: then the border moves to the item's nearer end.  The
 // pieces of a cut item are joined by a second kernel.
@@ -240,7 +240,10 @@ __device__ __forceinline__ Gqa8Span gqa8_span(const Gqa8AttnArgs& a, const Gqa8R
 struct Gqa8Kind {     // of requests that one of the kernels takes
   int min_rows, max_rows;
   int rows;           // of an item
-  int cost;           // of an item beyond its tiles
+  int cost;           // units of an item beyond its tiles
+  int half;           // items of at most so many rows: a unit a tile
+  int tile;           // others: so many
+  __device__ __forceinline__ int units(int n_rows) const { return n_rows <= half ? 1 : tile; }
 };
 constexpr int kWhole = 4, kLeast = 2;
 
@@ -258,7 +261,8 @@ __device__ __forceinline__ int64_t gqa8_units(const Gqa8AttnArgs& a, const Gqa8R
                                               const Gqa8Kind& kind, int G, int lane) {
   const int R = q.n * G, groups = (R + kind.rows - 1) / kind.rows;
   auto units = [&](const Gqa8Request& r, int i, int n_rows) {
-    return gqa8_span(a, r, G, i * kind.rows, min(n_rows, (i + 1) * kind.rows)).nt + kind.cost;
+    const int r0 = i * kind.rows, r1 = min(n_rows, r0 + kind.rows);
+    return static_cast<int64_t>(gqa8_span(a, r, G, r0, r1).nt) * kind.units(r1 - r0) + kind.cost;
   };
   int64_t u = 0;
   if (groups <= 2)
@@ -311,15 +315,15 @@ struct Gqa8Tail {
 constexpr int kMasked = 0x7FFF7FFF;
 constexpr float kLowest = -3e38f;
 
-// Where the border at unit u cuts an item of nt tiles that begins at unit
-// `begin`: tiles before the border, 0 .. nt (0 and nt also where it is not in
-// the item at all).
-__device__ __forceinline__ int gqa8_cut(int64_t u, int64_t begin, int nt, int cost) {
-  const int64_t x = u - begin;
+// Where the border at unit u cuts an item of nt tiles of `each` units that
+// begins at unit `begin`: tiles before the border, 0 .. nt (0 and nt also where
+// it is not in the item at all).
+__device__ __forceinline__ int gqa8_cut(int64_t u, int64_t begin, int nt, int each, int cost) {
+  const int64_t x = u - begin, all = static_cast<int64_t>(nt) * each + cost;
   if (x <= 0) return 0;
-  if (x >= nt + cost) return nt;
-  if (nt <= kWhole) return 2 * x <= nt + cost ? 0 : nt;
-  const int64_t t = x - cost;
+  if (x >= all) return nt;
+  if (nt <= kWhole) return 2 * x <= all ? 0 : nt;
+  const int64_t t = x <= cost ? 0 : quotient(x - cost, each);
   return t < kLeast ? 0 : t > nt - kLeast ? nt : static_cast<int>(t);
 }
 
@@ -331,7 +335,7 @@ __device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, const Gqa8Kind&
   const int G = a.Hq / a.Hkv, blocks = gridDim.x, me = blockIdx.x;
   // (no share so small that a long item's pieces would cost more to join than
   // they save; where no item is ever cut, as small as one item)
-  const int64_t least = (a.pt_stride + 1) / 2 <= kWhole ? 1 : kWhole;
+  const int64_t least = (a.pt_stride + 1) / 2 <= kWhole ? 1 : kWhole * kind.tile;
   const int64_t per = max(quotient(total + blocks - 1, blocks), least);
   const int64_t u0 = me * per, u1 = u0 + per;
   bool tail = false;
@@ -364,7 +368,8 @@ __device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, const Gqa8Kind&
         int64_t w = 0;
         if (gi < groups) {
           sp = gqa8_span(a, r, G, gi * kind.rows, min(R, (gi + 1) * kind.rows));
-          w = static_cast<int64_t>(sp.nt + kind.cost) * a.Hkv;
+          const int upt = kind.units(min(kind.rows, R - gi * kind.rows));
+          w = (static_cast<int64_t>(sp.nt) * upt + kind.cost) * a.Hkv;
         }
         int64_t g_end = w;
 #pragma unroll
@@ -379,11 +384,12 @@ __device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, const Gqa8Kind&
           const int klo = __shfl_sync(0xFFFFFFFFu, sp.klo, gl), khi = __shfl_sync(0xFFFFFFFFu, sp.khi, gl);
           const int t0 = __shfl_sync(0xFFFFFFFFu, sp.t0, gl), nt = __shfl_sync(0xFFFFFFFFu, sp.nt, gl);
           const int64_t at = __shfl_sync(0xFFFFFFFFu, g_end - w, gl);
-          const int each = nt + kind.cost, r0 = (g0 + gl) * kind.rows, nrows = min(kind.rows, R - r0);
+          const int r0 = (g0 + gl) * kind.rows, nrows = min(kind.rows, R - r0), upt = kind.units(nrows);
+          const int64_t each = static_cast<int64_t>(nt) * upt + kind.cost;
           const int h0 = at < u0 ? static_cast<int>(quotient(u0 - at, each)) : 0;
-          int64_t begin = at + static_cast<int64_t>(h0) * each;
+          int64_t begin = at + h0 * each;
           for (int h = h0; h < a.Hkv && begin < u1; ++h, begin += each) {
-            const int tb = gqa8_cut(u0, begin, nt, kind.cost), te = gqa8_cut(u1, begin, nt, kind.cost);
+            const int tb = gqa8_cut(u0, begin, nt, upt, kind.cost), te = gqa8_cut(u1, begin, nt, upt, kind.cost);
             int slot = -1;
             if (nt == 0) {
               // no tile to cut: the block that its first unit falls to
@@ -397,7 +403,7 @@ __device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, const Gqa8Kind&
               tail = true;
               // the last block that has some of it
               int last = static_cast<int>(quotient(begin + each - 1, per));
-              while (gqa8_cut(last * per, begin, nt, kind.cost) == nt) --last;
+              while (gqa8_cut(last * per, begin, nt, upt, kind.cost) == nt) --last;
               if (lane == 0) tails[me] = Gqa8Tail{last - me + 1, r.cu0, h, r0, nrows, {}};
             }
             emit(Gqa8Item{base + l, h, r.cu0, r.pos0, r0, nrows, klo, khi, t0 + tb, t0 + te, slot});

@@ -281,6 +281,17 @@ def test_attention_long_contexts(dtype, n, window):
     assert check_attention(c, [n, min(n, 9), n], 8, dtype, window=window)[0] == 0
 
 
+@pytest.mark.parametrize("n", [9, 33, 100, 128, 129, 140, 256, 257])
+@pytest.mark.parametrize("d,dtype", [(128, BF16), (64, F16)])
+def test_attention_items_of_every_height(n, d, dtype):
+    """One kv head, so n rows: below and above what an item and each of its two
+    row tiles hold, with one tile of keys, an odd and an even number of them,
+    and cut along the keys."""
+    c = ref.Cache([n, 300, 500, 5000], 1, d, dev(), seed=n, spread=1)
+    check_attention(c, [n, min(n, 300), n, n], 1, dtype, seed=n)
+    check_attention(c, [n, min(n, 300), n, n], 1, dtype, window=200, seed=n)
+
+
 def test_attention_many_requests():
     lens = [(i * 37) % 400 for i in range(300)]
     c = ref.Cache(lens, 1, 64, dev(), seed=14)
