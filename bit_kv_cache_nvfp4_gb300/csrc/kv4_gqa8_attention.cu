@@ -552,7 +552,7 @@ constexpr int kManyThreads = 640;
 constexpr uint32_t kSoftmaxRegs = 104, kOtherRegs = 64, kLaunchRegs = 96;
 static_assert(4 * kSoftmaxRegs + kOtherRegs <= 5 * kLaunchRegs, "register shares draw on the launch's");
 
-constexpr int kManyCost = 6;   // of an item, in half tiles: q in, first scores, last product, output
+constexpr int kManyCost = 10;   // of an item, in half tiles: q in, first scores, last product, output
 
 struct ManySmall {
   uint64_t k_full[3], k_empty[3], v8_full[2], v8_empty[2], v_full[2], v_empty[2], item_full[2], item_empty[2],
