@@ -44,6 +44,7 @@ namespace {
 template <int D_, int RP_, int NT_>
 struct FewCfg {
   static constexpr int D = D_, RP = RP_, NT = NT_;
+  static constexpr bool kF16 = NT == 3;                   // f16 calls take three terms, bf16 ones two
   static constexpr int N = (NT * RP + 15) / 16 * 16;      // MMA columns (N % 16 == 0 at M = 128)
   static constexpr int kTile = 2 * kTileKeys * D;         // K and V of a tile
   static constexpr int kQ = (N * D + 1023) / 1024 * 1024; // one of two
@@ -306,7 +307,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
           w[1] = __ldg(g + 1);
         }
         float x[16];
-        uint32_t m = widen16(w, a.f16, x);
+        uint32_t m = widen16<C::kF16>(w, x);
 #pragma unroll
         for (int off = 1; off < TPR; off <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
         const bool odd = m >= 0x7F800000u;                // a NaN or an infinity: NaN in its row
@@ -497,7 +498,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
         } else {
           const int64_t row = static_cast<int64_t>(it.cu0 + tok) * a.Hq + it.h * G + g;
           if (mine_d) {
-            if (a.f16) static_cast<__half*>(a.out)[row * D + d] = __float2half_rn(y);
+            if constexpr (C::kF16) static_cast<__half*>(a.out)[row * D + d] = __float2half_rn(y);
             else static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(y);
           }
           if (key == 0) a.lse[row] = ls * 0.6931471805599453f;
@@ -540,6 +541,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
 template <int D_, int NT_>
 struct ManyCfg {
   static constexpr int D = D_, NT = NT_, kRows = 256;
+  static constexpr bool kF16 = NT == 3;
   static constexpr int kK = kTileKeys * D;                // K or V codes of a tile
   static constexpr int kV16 = kTileKeys * D * 2;
   static constexpr int kQ = NT * 128 * D;                 // of one of the two row tiles
@@ -914,20 +916,30 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
         constexpr int kTpr = D / 16, kRpp = 32 / kTpr;
         const int part = lane % kTpr;
         const float sign = a.sm_scale < 0.0f ? -1.0f : 1.0f;   // (so that the factor is positive)
-#pragma unroll 2
-        for (int p = 0; p < 16 / kRpp; ++p) {
-          const int rr = wrow + half * 16 + p * kRpp + lane / kTpr;
-          const int gr = it.r0 + base + rr;
-          uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-          if (base + rr < it.nrows) {
+        auto fetch = [&](int p, uint4 (&w)[2]) {
+          const int rr = wrow + half * 16 + p * kRpp + lane / kTpr, gr = it.r0 + base + rr;
+          w[0] = w[1] = make_uint4(0, 0, 0, 0);
+          if (p * kRpp < 16 && base + rr < it.nrows) {
             const uint4* g = reinterpret_cast<const uint4*>(
                 static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(it.cu0 + gr / G) * a.q_token_stride +
                 static_cast<int64_t>(it.h * G + gr % G) * a.q_head_stride + part * 16);
             w[0] = __ldg(g);
             w[1] = __ldg(g + 1);
           }
+        };
+        // (a loop of little code, two fetches ahead: it runs once an item, so
+        // its instructions are as far away as its data)
+        uint4 w[2], w_next[2];
+        fetch(0, w);
+        fetch(1, w_next);
+#pragma unroll 1
+        for (int p = 0; p < 16 / kRpp; ++p) {
+          const int rr = wrow + half * 16 + p * kRpp + lane / kTpr;
           float y[16];
-          uint32_t m = widen16(w, a.f16, y);
+          uint32_t m = widen16<C::kF16>(w, y);
+          w[0] = w_next[0];
+          w[1] = w_next[1];
+          fetch(p + 2, w_next);
 #pragma unroll
           for (int off = 1; off < kTpr; off <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
           const int e = q_exponent(m);
@@ -1074,19 +1086,12 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
       auto stage = [&](int rr, int c) {
         return reinterpret_cast<uint4*>(q_mine + half * (128 * D) + swizzle<D == 128 ? 3 : 2>((wrow + rr) * D + c * 16));
       };
-      // 16-byte chunks of a row: D / 16, half as many where the columns are shared and of 16 bits
-      const int lg = (D == 128 ? 3 : 2) - (shared && it.slot < 0 ? 1 : 0);
-      auto flush = [&](uint8_t* to, int64_t at, int64_t row_bytes) {
-        __syncwarp();
-#pragma unroll 4
-        for (int i = lane; i < 32 << lg; i += 32) {
-          const int rr = i >> lg, c = i & ((1 << lg) - 1);
-          const int64_t dst = __shfl_sync(0xFFFFFFFFu, at, rr);
-          const uint4 v = *stage(rr, c);
-          if (base + wrow + rr < it.nrows) *reinterpret_cast<uint4*>(to + dst * row_bytes + c * 16) = v;
-        }
-        __syncwarp();
-      };
+      // 16-byte chunks of a row: D / 16, half as many where the columns are
+      // shared and of 16 bits
+      const bool cut = it.slot >= 0;
+      const int lg = (D == 128 ? 3 : 2) - (shared && !cut ? 1 : 0);
+      uint8_t* const to = cut ? reinterpret_cast<uint8_t*>(ws_o) : static_cast<uint8_t*>(a.out);
+      const int64_t row_at = cut ? part * (4 * D) : orow * (2 * D);
 #pragma unroll 1
       for (int c0 = 0; c0 < cols; c0 += 16) {             // of this warp's columns
         uint32_t v[16];
@@ -1105,29 +1110,30 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
 #pragma unroll
             for (int c = 0; c < 16; ++c) y[c] = fmaf(__uint_as_float(v[c]), wb, y[c]);
         }
-        if (it.slot >= 0) {
+        if (cut) {
           const int at = c0 % (D / 4) / 4;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) *stage(lane, at + c) = make_uint4(__float_as_uint(y[4 * c]), __float_as_uint(y[4 * c + 1]), __float_as_uint(y[4 * c + 2]), __float_as_uint(y[4 * c + 3]));
-          if ((c0 + 16) % (D / 4) == 0)
-            flush(reinterpret_cast<uint8_t*>(ws_o) + (col0 + c0 + 16 - D / 4) * 4, part, 4 * D);
+          for (int c = 0; c < 4; ++c)
+            *stage(lane, at + c) = make_uint4(__float_as_uint(y[4 * c]), __float_as_uint(y[4 * c + 1]),
+                                              __float_as_uint(y[4 * c + 2]), __float_as_uint(y[4 * c + 3]));
         } else {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float y0 = y[8 * c + 2 * i], y1 = y[8 * c + 2 * i + 1];
-              if (a.f16) {
-                o[i] = h2_bits(__floats2half2_rn(y0, y1));
-              } else {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
-                o[i] = *reinterpret_cast<const uint32_t*>(&h);
-              }
-            }
-            *stage(lane, c0 / 8 + c) = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int c = 0; c < 2; ++c)
+            *stage(lane, c0 / 8 + c) =
+                make_uint4(pack16<C::kF16>(y[8 * c], y[8 * c + 1]), pack16<C::kF16>(y[8 * c + 2], y[8 * c + 3]),
+                           pack16<C::kF16>(y[8 * c + 4], y[8 * c + 5]), pack16<C::kF16>(y[8 * c + 6], y[8 * c + 7]));
+        }
+        if (cut ? (c0 + 16) % (D / 4) == 0 : c0 + 16 == cols) {
+          const int64_t at = row_at + (cut ? (col0 + c0 + 16 - D / 4) * 4 : col0 * 2);
+          __syncwarp();
+#pragma unroll 2
+          for (int i = lane; i < 32 << lg; i += 32) {
+            const int rr = i >> lg, c = i & ((1 << lg) - 1);
+            const int64_t dst = __shfl_sync(0xFFFFFFFFu, at, rr);
+            const uint4 v4 = *stage(rr, c);
+            if (base + wrow + rr < it.nrows) *reinterpret_cast<uint4*>(to + dst + c * 16) = v4;
           }
-          if (c0 + 16 == cols) flush(static_cast<uint8_t*>(a.out) + col0 * 2, orow, 2 * D);
+          __syncwarp();
         }
       }
       if (mine && half == 0 && base == qt * 128) {

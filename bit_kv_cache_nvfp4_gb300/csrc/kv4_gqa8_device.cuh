@@ -82,12 +82,13 @@ __device__ __forceinline__ void split_e4m3_same(uint32_t x, uint32_t (&t)[NT]) {
 }
 
 // 16 values of q: widened to fp32; returns the bits of the largest magnitude.
-__device__ __forceinline__ uint32_t widen16(const uint4 (&w)[2], int f16, float (&x)[16]) {
+template <bool F16>
+__device__ __forceinline__ uint32_t widen16(const uint4 (&w)[2], float (&x)[16]) {
   const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (f16) {
+    if constexpr (F16) {
       const float2 f = __half22float2(bits_h2(u[i]));
       x[2 * i] = f.x;
       x[2 * i + 1] = f.y;
@@ -119,6 +120,14 @@ __device__ __forceinline__ void terms16(const float (&x)[16], float f, bool zero
 #pragma unroll
     for (int n = 0; n < NT; ++n) o[n][i] = t[0][n] | (t[1][n] << 16);
   }
+}
+
+// Two fp32 values -> 16-bit pair (first in the low half), round half to even.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (F16) return h2_bits(__floats2half2_rn(lo, hi));
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Two fp32 operations in one instruction, each rounded as by itself.
