@@ -709,35 +709,37 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
       const uint64_t dv0 = smem_desc(smem_addr(v_s), kSlab, 1024, kSwizzle128);
       uint32_t n_tiles = 0, ks = 0, k_par = 0;            // stage of K and its parity
       uint32_t w0 = 0, w1 = 0, p0 = 0, p1 = 0;            // parities of the row tiles' q and P
-      auto qk = [&](int qt, uint32_t stage, int q) {
-        if (elect_one()) {
-          const uint64_t dk = dk0 + stage * (C::kK >> 4), dq = dq0 + q * (C::kQ >> 4);
+      // The queue of products is a few instructions deep, so what keeps this
+      // warp between two groups of them has to be short: waits come where a group
+      // has just been queued, and a group ends with all its signals.
+      auto qk = [&](int qt, uint32_t stage, int q) {                   // of the elected lane
+        const uint64_t dk = dk0 + stage * (C::kK >> 4), dq = dq0 + q * (C::kQ >> 4);
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-              mma_f8kind(tmem + qt * 128, dq + ((t * 128 * D) >> 4) + 2 * k, dk + 2 * k, idesc_qk, t + k > 0);
-          mma_commit(smem_addr(&sm.s_full[qt]));
-        }
-        __syncwarp();
+          for (int k = 0; k < D / 32; ++k)
+            mma_f8kind(tmem + qt * 128, dq + ((t * 128 * D) >> 4) + 2 * k, dk + 2 * k, idesc_qk, t + k > 0);
+        mma_commit(smem_addr(&sm.s_full[qt]));
       };
-      // (P of each page lies over its own half of S; it comes in two parts, the
-      // first 32 keys of both pages and the others, so that the first products
-      // overlap the rest of the softmax)
-      auto pv = [&](int qt, uint32_t j, bool first, uint32_t& par) {
+      // PV of tile j, then, with the last products, `more` (P of each page lies
+      // over its own half of S; it comes in two parts, the first 32 keys of both
+      // pages and the others, so that the first products overlap the rest of
+      // the softmax)
+      auto pv = [&](int qt, uint32_t j, bool first, uint32_t& par, auto&& more) {
+        const uint64_t dv = dv0 + (j & 1) * (C::kV16 >> 4);
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           wait(sm.p_full[qt][part], par);
           __syncwarp();
           tc_fence_after_sync();
           if (elect_one()) {
-            const uint64_t dv = dv0 + (j & 1) * (C::kV16 >> 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int k = 2 * part + (i & 1) + 4 * (i >> 1);       // 16 keys
               mma_f16_ts(tmem + 256 + qt * 128, tmem + qt * 128 + 64 * (k >> 2) + 8 * (k & 3),
                          dv + ((k * 2048) >> 4), idesc_pv, !first || part + i > 0);
             }
+            if (part == 1) more();
           }
           __syncwarp();
         }
@@ -767,52 +769,77 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
           }
         };
         // (P of a row tile lies over its S: the products run in order)
+        wait(sm.k_full[ks], k_par);
+        __syncwarp();
+        tc_fence_after_sync();
         if (two) {
-          for (int t = 0; t <= nt; ++t) {
+          if (elect_one()) {
+            qk(0, ks, 0);
+            qk(1, ks, 1);
+            mma_commit(smem_addr(&sm.k_empty[ks]));
+          }
+          __syncwarp();
+          for (int t = 0; t < nt; ++t) {
             const uint32_t j = n_tiles + t;
-            if (t < nt) wait(sm.k_full[ks], k_par);
-            if (t > 0) wait(sm.v_full[(j - 1) & 1], ((j - 1) >> 1) & 1);
-            __syncwarp();
-            tc_fence_after_sync();
-            if (t > 0) pv(0, j - 1, t == 1, p0);
-            if (t < nt) qk(0, ks, 0);
-            if (t > 0) pv(1, j - 1, t == 1, p1);
-            if (t < nt) qk(1, ks, 1);
-            if (elect_one()) {
-              if (t > 0) mma_commit(smem_addr(&sm.v_empty[(j - 1) & 1]));
-              if (t < nt) {
-                mma_commit(smem_addr(&sm.k_empty[ks]));
+            const bool next = t + 1 < nt;
+            wait(sm.v_full[j & 1], (j >> 1) & 1);
+            next_k();
+            if (next && (KS < 3 || t == 0)) wait(sm.k_full[ks], k_par);
+            pv(0, j, t == 0, p0, [&] {
+              if (next) qk(0, ks, 0);
+              else mma_commit(smem_addr(&sm.o_full[0]));
+            });
+            const uint32_t ks_now = ks;
+            if (KS >= 3 && t + 2 < nt) {                  // K of the tile after the next
+              const bool wrap = ks + 1 == KS;
+              wait(sm.k_full[wrap ? 0 : ks + 1], wrap ? k_par ^ 1 : k_par);
+            }
+            pv(1, j, t == 0, p1, [&] {
+              if (next) {
+                qk(1, ks_now, 1);
+                mma_commit(smem_addr(&sm.k_empty[ks_now]));
               } else {
-                mma_commit(smem_addr(&sm.o_full[0]));
                 mma_commit(smem_addr(&sm.o_full[1]));
               }
-            }
-            __syncwarp();
-            if (t < nt) next_k();
+              mma_commit(smem_addr(&sm.v_empty[j & 1]));
+            });
           }
         } else {
-          // tile t is row tile t & 1's; its P two tiles on
-          for (int t = 0; t < nt + 2; ++t) {
-            const uint32_t j = n_tiles + t;
-            if (t < nt) wait(sm.k_full[ks], k_par);
-            if (t >= 2) wait(sm.v_full[j & 1], ((j - 2) >> 1) & 1);
+          // tile t is row tile t & 1's
+          if (elect_one()) {
+            qk(0, ks, 0);
+            mma_commit(smem_addr(&sm.k_empty[ks]));
+          }
+          __syncwarp();
+          next_k();
+          if (nt > 1) {
+            wait(sm.k_full[ks], k_par);
             __syncwarp();
             tc_fence_after_sync();
-            if (t >= 2) {
-              if (t & 1) pv(1, j - 2, t == 3, p1);
-              else pv(0, j - 2, t == 2, p0);
-              if (elect_one()) {
-                mma_commit(smem_addr(&sm.v_empty[j & 1]));
-                if (t >= nt) mma_commit(smem_addr(&sm.o_full[t & 1]));
+            if (elect_one()) {
+              qk(1, ks, 0);
+              mma_commit(smem_addr(&sm.k_empty[ks]));
+            }
+            __syncwarp();
+            next_k();
+          }
+          for (int t = 0; t < nt; ++t) {
+            const uint32_t j = n_tiles + t;
+            const bool next = t + 2 < nt;
+            wait(sm.v_full[j & 1], (j >> 1) & 1);
+            if (next) wait(sm.k_full[ks], k_par);
+            auto more = [&](int qt) {
+              if (next) {
+                qk(qt, ks, 0);
+                mma_commit(smem_addr(&sm.k_empty[ks]));
+              } else {
+                mma_commit(smem_addr(&sm.o_full[qt]));
               }
-              __syncwarp();
-            }
-            if (t < nt) {
-              qk(t & 1, ks, 0);
-              if (elect_one()) mma_commit(smem_addr(&sm.k_empty[ks]));
-              __syncwarp();
-              next_k();
-            }
+              mma_commit(smem_addr(&sm.v_empty[j & 1]));
+            };
+            if (t & 1) pv(1, j, t == 1, p1, [&] { more(1); });
+            else pv(0, j, t == 0, p0, [&] { more(0); });
+            if (next) next_k();
           }
         }
         n_tiles += nt;
@@ -972,9 +999,7 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
         wait(sm.s_full[qt], n_mine & 1);
         tc_fence_after_sync();
         float x[64];
-        // the second part is on its way while the first one's maximum is taken
         tmem_ld32(s_tm, reinterpret_cast<uint32_t(&)[32]>(x[0]));
-        tmem_wait_ld32(reinterpret_cast<uint32_t(&)[32]>(x[0]));
         tmem_ld32(s_tm + 32, reinterpret_cast<uint32_t(&)[32]>(x[32]));
         // keys of this row in the page: [c0, c1)
         const int at = t * kTileKeys + half * 64, c0 = lo - at, c1 = hi - at;
@@ -986,17 +1011,16 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
             x[c] = static_cast<unsigned>(c - a0) < static_cast<unsigned>(n) ? x[c] : -INFINITY;
         };
         float m[4];
-        if (edge) mask(0);
+        tmem_wait_ld32(reinterpret_cast<uint32_t(&)[32]>(x[0]));
+        tmem_wait_ld32(reinterpret_cast<uint32_t(&)[32]>(x[32]));
+        if (edge) {
+          mask(0);
+          mask(32);
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) m[k] = fmaxf(x[k], x[4 + k]);
 #pragma unroll
-        for (int c = 8; c < 32; c += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) m[k] = max3(m[k], x[c + k], x[c + 4 + k]);
-        tmem_wait_ld32(reinterpret_cast<uint32_t(&)[32]>(x[32]));
-        if (edge) mask(32);
-#pragma unroll
-        for (int c = 32; c < 64; c += 8)
+        for (int c = 8; c < 64; c += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k) m[k] = max3(m[k], x[c + k], x[c + 4 + k]);
         const int ev = ex == kMasked ? kGqa8ExpMin : ex >> 16;
