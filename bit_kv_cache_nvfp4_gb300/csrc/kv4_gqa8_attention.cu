@@ -347,7 +347,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
       if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
       if (it.b < 0) break;
       wait(sm.q_full[qb], (n_items >> 1) & 1);
-      float o[RP], l[RP], mref[RP];
+      float o[RP], l[RP], mref[RP], mref_mine = kLowest;
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
         o[r] = l[r] = 0.0f;
@@ -432,22 +432,29 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
         if (lane < RP) sm.red[j & 1][lane * 4 + quarter] = mine;
         tc_fence_before_sync();
         named_sync(kBar, 128);
-        const float vs = pow2f(evm - 8);
+        // (all loads before any store: the compiler keeps their order, and a
+        // load behind each column's store would cost its whole latency there)
+        auto top_of = [&](int r) {
+          const float4 m4 = *reinterpret_cast<const float4*>(&sm.red[j & 1][r * 4]);
+          return fmaxf(max3(m4.x, m4.y, m4.z), fmaxf(m4.w, kLowest));
+        };
+        float mt[RP];
+#pragma unroll
+        for (int r = 0; r < RP; ++r) mt[r] = top_of(r);
+        const float mt_mine = top_of(key < RP ? key : 0);
         uint32_t terms[RP / 8 * NT * 2];                  // bytes of the row of P: term, row
 #pragma unroll
         for (int r = 0; r < RP; r += 2) {
           float p[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float4 m4 = *reinterpret_cast<const float4*>(&sm.red[j & 1][(r + i) * 4]);
-            const float mt = fmaxf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), kLowest);
-            const bool up = mt > mref[r + i];
-            const float x = fast_exp2(up ? mref[r + i] - mt : mt - mref[r + i]);
-            const float al = up ? x : 1.0f, be = up ? 1.0f : x;
-            mref[r + i] = up ? mt : mref[r + i];
-            p[i] = fast_exp2(sc[r + i] - mt);
-            l[r + i] = fmaf(l[r + i], al, p[i] * be);
-            if (key == r + i) sm.stash[j & 1][r + i] = make_float2(al, be * vs);
+            // the running reference is the largest so far; of the two factors
+            // one is 1
+            const bool up = mt[r + i] > mref[r + i];
+            const float x = fast_exp2(up ? mref[r + i] - mt[r + i] : mt[r + i] - mref[r + i]);
+            p[i] = fast_exp2(sc[r + i] - mt[r + i]);
+            l[r + i] = up ? fmaf(l[r + i], x, p[i]) : fmaf(p[i], x, l[r + i]);
+            mref[r + i] = up ? mt[r + i] : mref[r + i];
           }
           uint32_t tt[NT];
           split_e4m3<NT>(h2_bits(__floats2half2_rn(p[0] * vf, p[1] * vf)), tt);
@@ -466,6 +473,13 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
           for (int i = 0; i < 4; ++i) w4[i] = (k * 4 + i) < RP * NT / 4 ? terms[(k * 4 + i) < RP * NT / 4 ? k * 4 + i : 0] : 0u;
           *reinterpret_cast<uint4*>(pb + k * 2048) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
         }
+        if (key < RP) {
+          // row `key`'s factors of the running output and of this tile's
+          const bool up = mt_mine > mref_mine;
+          const float x = fast_exp2(up ? mref_mine - mt_mine : mt_mine - mref_mine);
+          sm.stash[j & 1][key] = make_float2(up ? x : 1.0f, (up ? 1.0f : x) * pow2f(evm - 8));
+          mref_mine = up ? mt_mine : mref_mine;
+        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[j & 1]));
@@ -475,10 +489,19 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
       // behind this barrier, which also frees lsum
       named_sync(kBar, 128);
       if (it.t_end > it.t_begin) join(n_tiles - 1);
-      {
+      if constexpr (RP == 24) {
+        float a16[16], a8[8];
+#pragma unroll
+        for (int r = 0; r < 24; ++r) (r < 16 ? a16[r < 16 ? r : 0] : a8[r < 16 ? 0 : r - 16]) = l[r];
         int r;
-        const float mine = warp_sums<RP>(l, lane, r);
-        sm.lsum[quarter][r] = mine;
+        const float s16 = warp_sums<16>(a16, lane, r);
+        sm.lsum[quarter][r] = s16;
+        const float s8 = warp_sums<8>(a8, lane, r);
+        sm.lsum[quarter][16 + r] = s8;
+      } else {
+        int r;
+        const float s = warp_sums<RP>(l, lane, r);
+        sm.lsum[quarter][r] = s;
       }
       if (lane == 0) mbar_arrive(smem_addr(&sm.q_empty[qb]));
       named_sync(kBar, 128);
@@ -1178,11 +1201,12 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
 // ---------------------------------------------------------------------------
 // The pieces of items that were cut: block (c, y) joins rows of the item that
 // began in block c of the attention kernel, by log-sum-exp over its pieces in
-// their order.  W warps share a row (8 where an item has few rows and a long
-// context many pieces, 1 where it has 256 rows and two or three pieces).
+// their order: one kernel for items of few rows, where a long context has many
+// pieces and 8 warps share a row, one for items of 256 rows in two or three
+// pieces, where a warp takes 4 rows at once.
 // ---------------------------------------------------------------------------
-template <int D, int W>
-__global__ void __launch_bounds__(256) merge_kernel(const Gqa8AttnArgs a, const int rows,
+template <int D>
+__global__ void __launch_bounds__(256) merge_few_kernel(const Gqa8AttnArgs a, const int rows,
                                                     const Gqa8Tail* tails, const float* ws_lse,
                                                     const float* ws_o) {
   grid_dependency_wait();
@@ -1192,13 +1216,14 @@ __global__ void __launch_bounds__(256) merge_kernel(const Gqa8AttnArgs a, const 
   __shared__ Vec part[8][32];
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Gqa8Tail t = tails[c];
-  const int r = blockIdx.y * (8 / W) + warp / W, wi = warp % W;
-  if (t.parts == 0 || (W == 8 && r >= t.nrows)) return;   // (whole blocks)
+  constexpr int W = 8;
+  const int r = blockIdx.y, wi = warp;
+  if (t.parts == 0 || r >= t.nrows) return;               // (whole blocks)
   float o[C], m = -INFINITY, s = 0.0f;
 #pragma unroll
   for (int k = 0; k < C; ++k) o[k] = 0.0f;
   bool odd = false;
-  if (r < t.nrows) {
+  {
     // piece i is slot 2c + 1 for i = 0, else 2 (c + i)
     auto row_of = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * rows + r; };
     for (int i = lane; i < t.parts; i += 32) {
@@ -1226,18 +1251,15 @@ __global__ void __launch_bounds__(256) merge_kernel(const Gqa8AttnArgs a, const 
     }
     if (odd) s = __uint_as_float(0x7FC00000u);
   }
-  if constexpr (W > 1) {
-    part[warp][lane] = *reinterpret_cast<const Vec*>(o);
-    __syncthreads();
-    if (wi != 0) return;
+  part[warp][lane] = *reinterpret_cast<const Vec*>(o);
+  __syncthreads();
+  if (wi != 0) return;
 #pragma unroll
-    for (int i = 1; i < W; ++i) {
-      const Vec v = part[warp + i][lane];
+  for (int i = 1; i < W; ++i) {
+    const Vec v = part[i][lane];
 #pragma unroll
-      for (int k = 0; k < C; ++k) o[k] += reinterpret_cast<const float*>(&v)[k];
-    }
+    for (int k = 0; k < C; ++k) o[k] += reinterpret_cast<const float*>(&v)[k];
   }
-  if (r >= t.nrows) return;
   const int G = a.Hq / a.Hkv, rr = t.r0 + r;
   const int64_t row = static_cast<int64_t>(t.cu0 + rr / G) * a.Hq + t.h * G + rr % G;
   const float inv = s == 0.0f ? 0.0f : 1.0f / s;
@@ -1256,6 +1278,77 @@ __global__ void __launch_bounds__(256) merge_kernel(const Gqa8AttnArgs a, const 
   if constexpr (C == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[1]);
   else *dst = u[0];
   if (lane == 0) a.lse[row] = s == 0.0f ? -INFINITY : (m + log2f(s)) * 0.6931471805599453f;
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) merge_many_kernel(const Gqa8AttnArgs a, const int rows,
+                                                         const Gqa8Tail* tails, const float* ws_lse,
+                                                         const float* ws_o) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  constexpr int C = D / 32, R = 4;
+  using Vec = std::conditional_t<C == 4, float4, float2>;
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Gqa8Tail t = tails[c];
+  const int r0 = (blockIdx.y * 8 + warp) * R;
+  if (t.parts == 0 || r0 >= t.nrows) return;
+  auto row_of = [&](int i, int r) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * rows + r; };
+  // lane 8 k + i: row r0 + k, piece i of 8 at a time
+  const int k8 = lane >> 3, i8 = lane & 7, mine = min(r0 + k8, t.nrows - 1);
+  float m = -INFINITY;
+  bool odd = false;
+  for (int i = i8; i < t.parts; i += 8) {
+    const float x = __ldg(ws_lse + row_of(i, mine));
+    odd |= x != x;
+    m = fmaxf(m, x);
+  }
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) {
+    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+    odd |= __shfl_xor_sync(0xFFFFFFFFu, static_cast<int>(odd), off) != 0;
+  }
+  float s = 0.0f, o[R][C];
+#pragma unroll
+  for (int k = 0; k < R; ++k)
+#pragma unroll
+    for (int j = 0; j < C; ++j) o[k][j] = 0.0f;
+  for (int i0 = 0; i0 < t.parts; i0 += 8) {
+    const bool in = i0 + i8 < t.parts && m > -INFINITY;
+    const float w = in ? fast_exp2(__ldg(ws_lse + row_of(i0 + i8, mine)) - m) : 0.0f;
+    s += w;
+    const int n = min(8, t.parts - i0);
+#pragma unroll 2
+    for (int i = 0; i < n; ++i)
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        const float wk = __shfl_sync(0xFFFFFFFFu, w, k * 8 + i);
+        const Vec v = __ldg(reinterpret_cast<const Vec*>(ws_o + row_of(i0 + i, min(r0 + k, t.nrows - 1)) * D) + lane);
+        const float* f = reinterpret_cast<const float*>(&v);
+#pragma unroll
+        for (int j = 0; j < C; ++j) o[k][j] = fmaf(wk, f[j], o[k][j]);
+      }
+  }
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+  if (odd) s = __uint_as_float(0x7FC00000u);
+  const int G = a.Hq / a.Hkv;
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const float sk = __shfl_sync(0xFFFFFFFFu, s, k * 8), mk = __shfl_sync(0xFFFFFFFFu, m, k * 8);
+    if (r0 + k >= t.nrows) break;
+    const int rr = t.r0 + r0 + k;
+    const int64_t row = static_cast<int64_t>(t.cu0 + rr / G) * a.Hq + t.h * G + rr % G;
+    const float inv = sk == 0.0f ? 0.0f : 1.0f / sk;
+    uint32_t u[C / 2];
+#pragma unroll
+    for (int j = 0; j < C / 2; ++j)
+      u[j] = a.f16 ? pack16<true>(o[k][2 * j] * inv, o[k][2 * j + 1] * inv)
+                   : pack16<false>(o[k][2 * j] * inv, o[k][2 * j + 1] * inv);
+    uint32_t* const dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * D) + lane * (C / 2);
+    if constexpr (C == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[1]);
+    else *dst = u[0];
+    if (lane == 0) a.lse[row] = sk == 0.0f ? -INFINITY : (mk + log2f(sk)) * 0.6931471805599453f;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -1291,12 +1384,21 @@ bool pool_map(const Gqa8AttnArgs& a, CUtensorMap* map) {
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of an item and of the largest request that few_kernel takes: the
-// smallest of 8, 16 and 32 that holds every request, or a single token of each
-// where some have more (these go to the other kernel); 0: none of them.
-int few_rows(int max_new, int G) {
-  const int64_t most = static_cast<int64_t>(max_new) * G, need = most <= 32 ? most : G;
-  return need <= 8 ? 8 : need <= 16 ? 16 : need <= 32 ? 32 : 0;
+// Which requests few_kernel takes, by their rows, and how many are an item's.
+// Its work for a tile of keys grows with the rows (about 30 instructions of the
+// softmax warps for each), many_kernel's hardly does below 128; they cross
+// between 40 and 50 (a row group of 24 against 35 rows at D = 64: 29 us and 56
+// of a batch of drafts).  So: the smallest of 8, 16, 24 and 32 that holds every
+// request; up to 48 two groups of 24; where some have more, those that hold a
+// single token of any request.
+struct Few {
+  int rows, most;
+};
+Few few_rows(int max_new, int G) {
+  const int64_t all = static_cast<int64_t>(max_new) * G;
+  const int64_t need = all <= 48 ? all : G;
+  const int rows = need <= 8 ? 8 : need <= 16 ? 16 : need <= 24 ? 24 : need <= 32 ? 32 : need <= 48 ? 24 : 0;
+  return {rows, need <= 32 ? rows : rows == 0 ? 0 : 48};
 }
 // Workspace of one attention kernel: a tail for each of its blocks, then two
 // slots of partial rows for each block.
@@ -1316,11 +1418,12 @@ Parts parts_at(void* ws, int blocks, int rows, int D) {
 }
 constexpr int kFewCtas = 2, kManyRows = 256;      // blocks an SM at most
 
-template <int D, int W>
-cudaError_t launch_merge(const Gqa8AttnArgs& a, int blocks, int rows, const Parts& p, cudaStream_t stream) {
+template <typename K>
+cudaError_t launch_merge(K kernel, const Gqa8AttnArgs& a, int blocks, int y, int rows, const Parts& p,
+                         cudaStream_t stream) {
   if ((a.pt_stride + 1) / 2 <= kWhole) return cudaSuccess;                 // nothing is ever cut
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, rows * W / 8);
+  cfg.gridDim = dim3(blocks, y);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1328,7 +1431,7 @@ cudaError_t launch_merge(const Gqa8AttnArgs& a, int blocks, int rows, const Part
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<D, W>, a, rows, static_cast<const Gqa8Tail*>(p.tails),
+  return cudaLaunchKernelEx(&cfg, kernel, a, rows, static_cast<const Gqa8Tail*>(p.tails),
                             static_cast<const float*>(p.lse), static_cast<const float*>(p.o));
 }
 
@@ -1352,14 +1455,15 @@ cudaError_t prepare_kernel(int smem, int min_regs) {
 }
 
 template <int D, int RP, int NT>
-cudaError_t launch_few(const Gqa8AttnArgs& a, const CUtensorMap& map, void* ws, cudaStream_t stream) {
+cudaError_t launch_few(const Gqa8AttnArgs& a, const CUtensorMap& map, int max_rows, void* ws,
+                       cudaStream_t stream) {
   using C = FewCfg<D, RP, NT>;
   cudaError_t e = prepare_kernel<few_kernel<D, RP, NT>>(C::kSmem, 0);
   if (e != cudaSuccess) return e;
   const int blocks = a.num_sms * C::kCtas;
   const Parts p = parts_at(ws, blocks, RP, D);
-  e = launch_pdl(few_kernel<D, RP, NT>, blocks, 256, C::kSmem, stream, 1, map, a, RP, p.tails, p.lse, p.o);
-  return e != cudaSuccess ? e : launch_merge<D, 8>(a, blocks, RP, p, stream);
+  e = launch_pdl(few_kernel<D, RP, NT>, blocks, 256, C::kSmem, stream, 1, map, a, max_rows, p.tails, p.lse, p.o);
+  return e != cudaSuccess ? e : launch_merge(merge_few_kernel<D>, a, blocks, RP, RP, p, stream);
 }
 
 template <int D, int NT>
@@ -1371,7 +1475,7 @@ cudaError_t launch_many(const Gqa8AttnArgs& a, const CUtensorMap& map, int min_r
   const Parts p = parts_at(ws, a.num_sms, kManyRows, D);
   e = launch_pdl(many_kernel<D, NT>, a.num_sms, kManyThreads, C::kSmem, stream, 1, map, a, min_rows, p.tails,
                  p.lse, p.o);
-  return e != cudaSuccess ? e : launch_merge<D, 1>(a, a.num_sms, kManyRows, p, stream);
+  return e != cudaSuccess ? e : launch_merge(merge_many_kernel<D>, a, a.num_sms, kManyRows / 32, kManyRows, p, stream);
 }
 
 size_t few_bytes(int rows, int D, int sms) {
@@ -1382,14 +1486,22 @@ template <int D>
 cudaError_t launch_d(const Gqa8AttnArgs& a, cudaStream_t stream) {
   CUtensorMap map;
   if (!pool_map(a, &map)) return cudaErrorInvalidValue;
-  const int G = a.Hq / a.Hkv, rows = few_rows(a.max_new, G);
+  const int G = a.Hq / a.Hkv;
+  const Few few = few_rows(a.max_new, G);
+  auto launch = [&](auto rp) {
+    constexpr int RP = decltype(rp)::value;
+    return a.f16 ? launch_few<D, RP, 3>(a, map, few.most, a.ws, stream)
+                 : launch_few<D, RP, 2>(a, map, few.most, a.ws, stream);
+  };
   cudaError_t e = cudaSuccess;
-  if (rows == 8) e = a.f16 ? launch_few<D, 8, 3>(a, map, a.ws, stream) : launch_few<D, 8, 2>(a, map, a.ws, stream);
-  else if (rows == 16) e = a.f16 ? launch_few<D, 16, 3>(a, map, a.ws, stream) : launch_few<D, 16, 2>(a, map, a.ws, stream);
-  else if (rows == 32) e = a.f16 ? launch_few<D, 32, 3>(a, map, a.ws, stream) : launch_few<D, 32, 2>(a, map, a.ws, stream);
-  if (e != cudaSuccess || static_cast<int64_t>(a.max_new) * G <= rows) return e;
-  void* const ws = static_cast<uint8_t*>(a.ws) + few_bytes(rows, D, a.num_sms);
-  return a.f16 ? launch_many<D, 3>(a, map, rows + 1, ws, stream) : launch_many<D, 2>(a, map, rows + 1, ws, stream);
+  if (few.rows == 8) e = launch(std::integral_constant<int, 8>{});
+  else if (few.rows == 16) e = launch(std::integral_constant<int, 16>{});
+  else if (few.rows == 24) e = launch(std::integral_constant<int, 24>{});
+  else if (few.rows == 32) e = launch(std::integral_constant<int, 32>{});
+  if (e != cudaSuccess || static_cast<int64_t>(a.max_new) * G <= few.most) return e;
+  void* const ws = static_cast<uint8_t*>(a.ws) + few_bytes(few.rows, D, a.num_sms);
+  return a.f16 ? launch_many<D, 3>(a, map, few.most + 1, ws, stream)
+               : launch_many<D, 2>(a, map, few.most + 1, ws, stream);
 }
 
 }  // namespace
@@ -1399,9 +1511,9 @@ cudaError_t launch_attention_gqa8(const Gqa8AttnArgs& a, cudaStream_t stream) {
 }
 
 size_t attention_gqa8_workspace(int, int max_new, int64_t, int Hq, int Hkv, int D, int num_sms) {
-  const int rows = few_rows(max_new, Hq / Hkv);
-  const bool many = static_cast<int64_t>(max_new) * (Hq / Hkv) > rows;
-  return few_bytes(rows, D, num_sms) + (many ? part_bytes(num_sms, kManyRows, D) : 0);
+  const Few few = few_rows(max_new, Hq / Hkv);
+  const bool many = static_cast<int64_t>(max_new) * (Hq / Hkv) > few.most;
+  return few_bytes(few.rows, D, num_sms) + (many ? part_bytes(num_sms, kManyRows, D) : 0);
 }
 
 }  // namespace kv4

@@ -183,7 +183,7 @@ def test_attention_single_tokens(g, hkv, d, dtype):
 
 
 @pytest.mark.parametrize("g,hkv,d,dtype", [(8, 1, 128, BF16), (5, 2, 64, F16), (1, 3, 128, F16), (4, 2, 64, BF16)])
-@pytest.mark.parametrize("news", [[2, 3, 4, 1, 0, 4], [9, 1, 30, 64, 65, 2], [130, 257, 1, 200, 33, 64]])
+@pytest.mark.parametrize("news", [[2, 3, 4, 1, 0, 4], [5, 3, 5, 1, 0, 4], [9, 1, 30, 64, 65, 2], [130, 257, 1, 200, 33, 64]])
 @pytest.mark.parametrize("window", [0, 1, 50, 100])
 def test_attention_several_tokens(g, hkv, d, dtype, news, window):
     lens = [max(n, m) for n, m in zip(news, [2, 300, 64, 129, 40, 1000])]
