@@ -38,9 +38,12 @@ namespace {
 // terms) never meets a maximum from far away; each tile's O is a product of
 // its own, joined to the running output in registers.
 //
-// Block: 8 warps.  Warp 0 finds the block's share of the work list and issues
-// the loads, warp 1 the products, warps 2-3 bring q of the next item to E4M3,
-// warps 4-7 are the softmax: a thread holds one key of S^T (and one d of O^T).
+// Block: warp 0 finds the block's share of the work list and issues the loads,
+// warp 1 the products, warps 2-3 bring q of the next item to E4M3, and one or
+// two warpgroups are the softmax: a thread holds one key of S^T (and one d of
+// O^T).  Two blocks share an SM, with one softmax warpgroup each, where they
+// fit; else one block has two warpgroups that take every other tile, each with
+// a running output of its own, joined at the item's end.
 template <int D_, int RP_, int NT_>
 struct FewCfg {
   static constexpr int D = D_, RP = RP_, NT = NT_;
@@ -49,12 +52,15 @@ struct FewCfg {
   static constexpr int kTile = 2 * kTileKeys * D;         // K and V of a tile
   static constexpr int kQ = (N * D + 1023) / 1024 * 1024; // one of two
   static constexpr int kP = N / 16 * 2048;                // one of two
-  static constexpr int kSmall = 4096;                     // barriers, items, factors
+  static constexpr int kSmall = 6144;                     // barriers, items, factors
   static constexpr int kFixed = 2 * kQ + 2 * kP + kSmall;
   // two blocks of an SM where three stages (96 KB) and the rest fit into half
   // of its 228 KB each, else one block with more stages
   static constexpr int kHalf = 113 * 1024 - 1024;
-  static constexpr int kCtas = kFixed + 98304 <= kHalf && RP <= 16 ? 2 : 1;
+  static constexpr int kCtas = kFixed + 98304 <= kHalf && RP == 8 ? 2 : 1;
+  static constexpr int kWgs = kCtas == 2 ? 1 : 2;         // softmax warpgroups
+  static constexpr int kThreads = 128 + 128 * kWgs;
+  static_assert(kWgs == 1 || 2 * kP >= RP * 512, "the joined output goes through P's memory");
   static constexpr int kStages = (kCtas == 2 ? 98304 : 163840) / kTile;
   static constexpr int kSmem = kStages * kTile + kFixed + 1024;
   static constexpr uint32_t kTmem = 4 * N <= 64 ? 64 : 4 * N <= 128 ? 128 : 4 * N <= 256 ? 256 : 512;
@@ -72,20 +78,20 @@ struct FewSmall {
   Gqa8Item items[4];
   float qf[2][32];            // sm_scale log2(e) 2^eq of a row, NaN where q is not finite
   int pos[2][32];             // a row's position, -1 where it is negative
-  alignas(16) float red[2][32 * 4];    // read as float4
-  alignas(16) float2 stash[2][32];
-  float lsum[4][32];
+  alignas(16) float red[4][32 * 4];    // read as float4; by warpgroup and parity of its tiles
+  alignas(16) float2 stash[4][32];
+  float lsum[2][4][32], top[2][32];
 };
-static_assert(sizeof(FewSmall) <= 4096 && offsetof(FewSmall, red) % 16 == 0 &&
+static_assert(sizeof(FewSmall) <= 6144 && offsetof(FewSmall, red) % 16 == 0 &&
                   offsetof(FewSmall, stash) % 8 == 0,
               "FewSmall");
 
 template <int D, int RP, int NT>
-__global__ void __launch_bounds__(256, FewCfg<D, RP, NT>::kCtas)
+__global__ void __launch_bounds__(FewCfg<D, RP, NT>::kThreads, FewCfg<D, RP, NT>::kCtas)
 few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const int max_rows,
            Gqa8Tail* tails, float* ws_lse, float* ws_o) {
   using C = FewCfg<D, RP, NT>;
-  constexpr int N = C::N, ST = C::kStages;
+  constexpr int N = C::N, ST = C::kStages, WGS = C::kWgs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const q_s = smem + ST * C::kTile;
@@ -101,11 +107,11 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_addr(&sm.item_full[i]), 1);
-      mbar_init(smem_addr(&sm.item_empty[i]), 7);      // the product's lane, 2 + 4 warps
+      mbar_init(smem_addr(&sm.item_empty[i]), 3 + 4 * WGS);      // the product's warp, 2, the softmax's
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sm.q_full[i]), 2);
-      mbar_init(smem_addr(&sm.q_empty[i]), 5);         // the last QK, 4 warps
+      mbar_init(smem_addr(&sm.q_empty[i]), 1 + 4 * WGS);         // the last QK, the softmax's warps
       mbar_init(smem_addr(&sm.s_full[i]), 1);
       mbar_init(smem_addr(&sm.p_full[i]), 4);
       mbar_init(smem_addr(&sm.o_full[i]), 1);
@@ -119,7 +125,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
   if (warp == 1) tmem_alloc(smem_addr(&sm.tmem), C::kTmem);
   // columns past NT * RP stay zero in both operands
   if constexpr (N > NT * RP)
-    for (int i = tid; i < (2 * C::kQ + 2 * C::kP) / 16; i += 256)
+    for (int i = tid; i < (2 * C::kQ + 2 * C::kP) / 16; i += C::kThreads)
       reinterpret_cast<uint4*>(q_s)[i] = make_uint4(0, 0, 0, 0);
   grid_dependency_wait();
   grid_launch_dependents();
@@ -331,17 +337,19 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
     }
   } else {
     // ==== softmax ====
-    const int key = tid - 128;                            // of a tile; and d of O^T
+    const int wg = (warp - 4) >> 2;
+    const int key = tid & 127;                            // of a tile; and d of O^T
     const int quarter = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    constexpr int kBar = 1;
-    uint32_t n_tiles = 0;
+    const int bar = 1 + wg;
+    constexpr int kBarAll = 3;
+    uint32_t n_tiles = 0, n_own = 0;                      // tiles of all items, of this warpgroup
     for (uint32_t n_items = 0;; ++n_items) {
       const int s = n_items & 3, qb = n_items & 1;
       wait(sm.item_full[s], (n_items >> 2) & 1);
-      // the four warps stop together: a warp that left alone would leave the
-      // others at their barrier
-      if (named_sync_or(kBar, 128, *dead != 0)) break;
+      // the warps stop together: a warp that left alone would leave the others
+      // at their barrier
+      if (named_sync_or(kBarAll, 128 * WGS, *dead != 0)) break;
       const Gqa8Item it = sm.items[s];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
@@ -355,8 +363,9 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
       }
       // rows' positions: pos0 + (r0 + r) / G
       const int pos_first = it.pos0 + it.r0 / G, pos_last = it.pos0 + (it.r0 + it.nrows - 1) / G;
-      // O of tile j joins the running output
-      auto join = [&](uint32_t j) {
+      // O of tile j, this warpgroup's i-th, joins the running output
+      auto join = [&](uint32_t j, uint32_t i_own) {
+        const float2* const stash = sm.stash[2 * wg + (i_own & 1)];
         wait(sm.o_full[j & 1], (j >> 1) & 1);
         tc_fence_after_sync();
 #pragma unroll
@@ -371,14 +380,17 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
             float x = __uint_as_float(v[NT - 1][i]);
 #pragma unroll
             for (int t = NT - 2; t >= 0; --t) x = fmaf(x, 0.0625f, __uint_as_float(v[t][i]));
-            const float2 f = sm.stash[j & 1][c + i];
+            const float2 f = stash[c + i];
             o[c + i] = fmaf(o[c + i], f.x, x * f.y);
           }
         }
         tc_fence_before_sync();
       };
-      for (int t = it.t_begin; t < it.t_end; ++t, ++n_tiles) {
-        const uint32_t j = n_tiles;
+      // (of two warpgroups, tile j's is the one with its parity, whose S, P and O
+      // memory are)
+      const int first = it.t_begin + (WGS == 2 ? static_cast<int>((n_tiles ^ wg) & 1) : 0);
+      for (int t = first; t < it.t_end; t += WGS, ++n_own) {
+        const uint32_t j = n_tiles + (t - it.t_begin);
         const int st = j % ST;
         wait(sm.full[st], (j / ST) & 1);                  // the exponents, and V where it is cleaned
         const int ex = sm.exps[st][key >> 6], ex2 = sm.exps[st][(key >> 6) ^ 1];
@@ -429,13 +441,15 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
           const float m = warp_max(sc[r]);
           if (lane == r) mine = m;
         }
-        if (lane < RP) sm.red[j & 1][lane * 4 + quarter] = mine;
+        if (lane < RP) sm.red[2 * wg + (n_own & 1)][lane * 4 + quarter] = mine;
         tc_fence_before_sync();
-        named_sync(kBar, 128);
+        named_sync(bar, 128);
+        // (the tile before is done with its O before P of this one is sent)
+        if (WGS == 2 && t > first) join(j - 2, n_own - 1);
         // (all loads before any store: the compiler keeps their order, and a
         // load behind each column's store would cost its whole latency there)
         auto top_of = [&](int r) {
-          const float4 m4 = *reinterpret_cast<const float4*>(&sm.red[j & 1][r * 4]);
+          const float4 m4 = *reinterpret_cast<const float4*>(&sm.red[2 * wg + (n_own & 1)][r * 4]);
           return fmaxf(max3(m4.x, m4.y, m4.z), fmaxf(m4.w, kLowest));
         };
         float mt[RP];
@@ -477,43 +491,65 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
           // row `key`'s factors of the running output and of this tile's
           const bool up = mt_mine > mref_mine;
           const float x = fast_exp2(up ? mref_mine - mt_mine : mt_mine - mref_mine);
-          sm.stash[j & 1][key] = make_float2(up ? x : 1.0f, (up ? 1.0f : x) * pow2f(evm - 8));
+          sm.stash[2 * wg + (n_own & 1)][key] = make_float2(up ? x : 1.0f, (up ? 1.0f : x) * pow2f(evm - 8));
           mref_mine = up ? mt_mine : mref_mine;
         }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[j & 1]));
-        if (t > it.t_begin) join(j - 1);
+        if (WGS == 1 && t > first) join(j - 1, n_own - 1);
       }
       // the factors of the last tile, written by other warps, are visible
-      // behind this barrier, which also frees lsum
-      named_sync(kBar, 128);
-      if (it.t_end > it.t_begin) join(n_tiles - 1);
+      // behind this barrier
+      named_sync(bar, 128);
+      if (first < it.t_end) join(n_tiles + (it.t_end - it.t_begin - 1 - (it.t_end - 1 - first) % WGS), n_own - 1);
+      n_tiles += it.t_end - it.t_begin;
       if constexpr (RP == 24) {
         float a16[16], a8[8];
 #pragma unroll
         for (int r = 0; r < 24; ++r) (r < 16 ? a16[r < 16 ? r : 0] : a8[r < 16 ? 0 : r - 16]) = l[r];
         int r;
         const float s16 = warp_sums<16>(a16, lane, r);
-        sm.lsum[quarter][r] = s16;
+        sm.lsum[wg][quarter][r] = s16;
         const float s8 = warp_sums<8>(a8, lane, r);
-        sm.lsum[quarter][16 + r] = s8;
+        sm.lsum[wg][quarter][16 + r] = s8;
       } else {
         int r;
         const float s = warp_sums<RP>(l, lane, r);
-        sm.lsum[quarter][r] = s;
+        sm.lsum[wg][quarter][r] = s;
       }
+      if (key < RP) sm.top[wg][key] = mref_mine;
       if (lane == 0) mbar_arrive(smem_addr(&sm.q_empty[qb]));
-      named_sync(kBar, 128);
+      named_sync(kBarAll, 128 * WGS);
+      if constexpr (WGS == 2) {
+        // the second warpgroup's output goes to the first relative to the larger
+        // reference of the two, through P's memory, which no product reads now
+        float* const x = reinterpret_cast<float*>(p_s) + key;
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          const float w = fast_exp2(mref[r] - fmaxf(sm.top[0][r], sm.top[1][r]));
+          o[r] *= w;
+          if (wg == 1) x[r * 128] = o[r];
+        }
+        named_sync(kBarAll, 256);
+        if (wg == 1) continue;
+#pragma unroll
+        for (int r = 0; r < RP; ++r) o[r] += x[r * 128];
+      }
       const bool mine_d = D == 128 || lane < 16;          // M = 64: 16 lanes of each warp
       const int d = D == 128 ? key : quarter * 16 + lane;
       int tok = it.r0 / G, g = it.r0 - tok * G;
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
         if (r >= it.nrows) break;
-        const float lt = (sm.lsum[0][r] + sm.lsum[1][r]) + (sm.lsum[2][r] + sm.lsum[3][r]);
+        auto sum_of = [&](int w) { return (sm.lsum[w][0][r] + sm.lsum[w][1][r]) + (sm.lsum[w][2][r] + sm.lsum[w][3][r]); };
+        float lt = sum_of(0), ref = mref[r];
+        if constexpr (WGS == 2) {
+          ref = fmaxf(mref[r], sm.top[1][r]);
+          lt = lt * fast_exp2(mref[r] - ref) + sum_of(1) * fast_exp2(sm.top[1][r] - ref);
+        }
         const float y = lt == 0.0f ? 0.0f : __fdividef(o[r], lt);
-        const float ls = lt == 0.0f ? -INFINITY : mref[r] + fast_log2(lt);
+        const float ls = lt == 0.0f ? -INFINITY : ref + fast_log2(lt);
         if (it.slot >= 0) {
           const int64_t row = static_cast<int64_t>(it.slot) * RP + r;
           if (mine_d) ws_o[row * D + d] = y;
@@ -1384,21 +1420,12 @@ bool pool_map(const Gqa8AttnArgs& a, CUtensorMap* map) {
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Which requests few_kernel takes, by their rows, and how many are an item's.
-// Its work for a tile of keys grows with the rows (about 30 instructions of the
-// softmax warps for each), many_kernel's hardly does below 128; they cross
-// between 40 and 50 (a row group of 24 against 35 rows at D = 64: 29 us and 56
-// of a batch of drafts).  So: the smallest of 8, 16, 24 and 32 that holds every
-// request; up to 48 two groups of 24; where some have more, those that hold a
-// single token of any request.
-struct Few {
-  int rows, most;
-};
-Few few_rows(int max_new, int G) {
-  const int64_t all = static_cast<int64_t>(max_new) * G;
-  const int64_t need = all <= 48 ? all : G;
-  const int rows = need <= 8 ? 8 : need <= 16 ? 16 : need <= 24 ? 24 : need <= 32 ? 32 : need <= 48 ? 24 : 0;
-  return {rows, need <= 32 ? rows : rows == 0 ? 0 : 48};
+// Rows of few_kernel's items, and of the largest request that it takes: the
+// smallest of 8, 16 and 24 that holds every request or, where some have more, a
+// single token of any (the others go to many_kernel); 0: none.
+int few_rows(int max_new, int G) {
+  const int64_t all = static_cast<int64_t>(max_new) * G, need = all <= 24 ? all : G;
+  return need <= 8 ? 8 : need <= 16 ? 16 : need <= 24 ? 24 : 0;
 }
 // Workspace of one attention kernel: a tail for each of its blocks, then two
 // slots of partial rows for each block.
@@ -1462,7 +1489,7 @@ cudaError_t launch_few(const Gqa8AttnArgs& a, const CUtensorMap& map, int max_ro
   if (e != cudaSuccess) return e;
   const int blocks = a.num_sms * C::kCtas;
   const Parts p = parts_at(ws, blocks, RP, D);
-  e = launch_pdl(few_kernel<D, RP, NT>, blocks, 256, C::kSmem, stream, 1, map, a, max_rows, p.tails, p.lse, p.o);
+  e = launch_pdl(few_kernel<D, RP, NT>, blocks, C::kThreads, C::kSmem, stream, 1, map, a, max_rows, p.tails, p.lse, p.o);
   return e != cudaSuccess ? e : launch_merge(merge_few_kernel<D>, a, blocks, RP, RP, p, stream);
 }
 
@@ -1487,21 +1514,20 @@ cudaError_t launch_d(const Gqa8AttnArgs& a, cudaStream_t stream) {
   CUtensorMap map;
   if (!pool_map(a, &map)) return cudaErrorInvalidValue;
   const int G = a.Hq / a.Hkv;
-  const Few few = few_rows(a.max_new, G);
+  const int rows = few_rows(a.max_new, G);
   auto launch = [&](auto rp) {
     constexpr int RP = decltype(rp)::value;
-    return a.f16 ? launch_few<D, RP, 3>(a, map, few.most, a.ws, stream)
-                 : launch_few<D, RP, 2>(a, map, few.most, a.ws, stream);
+    return a.f16 ? launch_few<D, RP, 3>(a, map, rows, a.ws, stream)
+                 : launch_few<D, RP, 2>(a, map, rows, a.ws, stream);
   };
   cudaError_t e = cudaSuccess;
-  if (few.rows == 8) e = launch(std::integral_constant<int, 8>{});
-  else if (few.rows == 16) e = launch(std::integral_constant<int, 16>{});
-  else if (few.rows == 24) e = launch(std::integral_constant<int, 24>{});
-  else if (few.rows == 32) e = launch(std::integral_constant<int, 32>{});
-  if (e != cudaSuccess || static_cast<int64_t>(a.max_new) * G <= few.most) return e;
-  void* const ws = static_cast<uint8_t*>(a.ws) + few_bytes(few.rows, D, a.num_sms);
-  return a.f16 ? launch_many<D, 3>(a, map, few.most + 1, ws, stream)
-               : launch_many<D, 2>(a, map, few.most + 1, ws, stream);
+  if (rows == 8) e = launch(std::integral_constant<int, 8>{});
+  else if (rows == 16) e = launch(std::integral_constant<int, 16>{});
+  else if (rows == 24) e = launch(std::integral_constant<int, 24>{});
+  if (e != cudaSuccess || static_cast<int64_t>(a.max_new) * G <= rows) return e;
+  void* const ws = static_cast<uint8_t*>(a.ws) + few_bytes(rows, D, a.num_sms);
+  return a.f16 ? launch_many<D, 3>(a, map, rows + 1, ws, stream)
+               : launch_many<D, 2>(a, map, rows + 1, ws, stream);
 }
 
 }  // namespace
@@ -1511,9 +1537,9 @@ cudaError_t launch_attention_gqa8(const Gqa8AttnArgs& a, cudaStream_t stream) {
 }
 
 size_t attention_gqa8_workspace(int, int max_new, int64_t, int Hq, int Hkv, int D, int num_sms) {
-  const Few few = few_rows(max_new, Hq / Hkv);
-  const bool many = static_cast<int64_t>(max_new) * (Hq / Hkv) > few.most;
-  return few_bytes(few.rows, D, num_sms) + (many ? part_bytes(num_sms, kManyRows, D) : 0);
+  const int rows = few_rows(max_new, Hq / Hkv);
+  const bool many = static_cast<int64_t>(max_new) * (Hq / Hkv) > rows;
+  return few_bytes(rows, D, num_sms) + (many ? part_bytes(num_sms, kManyRows, D) : 0);
 }
 
 }  // namespace kv4
