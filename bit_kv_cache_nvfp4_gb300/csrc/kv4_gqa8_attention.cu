@@ -54,19 +54,19 @@ struct FewCfg {
   static constexpr int kP = N / 16 * 2048;                // one of two
   static constexpr int kSmall = 6144;                     // barriers, items, factors
   static constexpr int kFixed = 2 * kQ + 2 * kP + kSmall;
-  // two blocks of an SM where three stages (96 KB) and the rest fit into half
-  // of its 228 KB each, else one block with more stages
+  // two blocks of an SM, with half of its 228 KB each, or one with more stages
   static constexpr int kHalf = 113 * 1024 - 1024;
-  static constexpr int kCtas = kFixed + 98304 <= kHalf && RP == 8 ? 2 : 1;
+  static constexpr int kCtas = RP == 8 ? 2 : 1;
   static constexpr int kWgs = kCtas == 2 ? 1 : 2;         // softmax warpgroups
   static constexpr int kThreads = 128 + 128 * kWgs;
+  // what an item takes beyond its tiles, in tiles (1, 3 | 2, 5 | 3, 8 of the two
+  // kinds: decode with 16 heads a group 370, 360, 357 us, with 8 343 all)
+  static constexpr int kCost = kWgs == 2 ? 8 : 3;
   static_assert(kWgs == 1 || 2 * kP >= RP * 512, "the joined output goes through P's memory");
-  static constexpr int kStages = (kCtas == 2 ? 98304 : 163840) / kTile;
+  static constexpr int kStages = (kCtas == 2 ? kHalf - kFixed : 163840) / kTile;
   static constexpr int kSmem = kStages * kTile + kFixed + 1024;
   static constexpr uint32_t kTmem = 4 * N <= 64 ? 64 : 4 * N <= 128 ? 128 : 4 * N <= 256 ? 256 : 512;
 };
-
-constexpr int kFewCost = 1;    // of an item, in tiles (its q and its output overlap others' tiles)
 
 struct FewSmall {
   uint64_t full[12], empty[12], item_full[4], item_empty[4], q_full[2], q_empty[2], s_full[2], p_full[2],
@@ -130,7 +130,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
   grid_dependency_wait();
   grid_launch_dependents();
   __syncthreads();
-  const Gqa8Kind kind{1, max_rows, RP, kFewCost, RP, 1};
+  const Gqa8Kind kind{1, max_rows, RP, C::kCost, RP, 1};
   gqa8_total(a, kind, blockIdx.x == 0, &sm.total);
   fence_async_smem();
   tc_fence_before_sync();
