@@ -1006,6 +1006,7 @@ kv4_status kv4_append_gqa8(const void* k_dev, int64_t k_token_stride, int64_t k_
   a.pool = pool_dev;
   a.scales = scales_dev;
   a.num_pages = num_pages;
+  a.num_sms = sms;
   a.dev_err = dev_err;
   return kv4::launch_append_gqa8(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? KV4_OK
@@ -1045,6 +1046,7 @@ kv4_status kv4_read_gqa8(const uint8_t* pool_dev, const uint8_t* scales_dev, int
   a.pool = const_cast<uint8_t*>(pool_dev);
   a.scales = const_cast<uint8_t*>(scales_dev);
   a.num_pages = num_pages;
+  a.num_sms = sms;
   a.dev_err = dev_err;
   return kv4::launch_read_gqa8(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? KV4_OK

@@ -130,7 +130,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
   grid_dependency_wait();
   grid_launch_dependents();
   __syncthreads();
-  const Gqa8Kind kind{1, max_rows, RP, C::kCost, RP, 1};
+  const Gqa8Kind kind{1, max_rows, RP, C::kCost, RP, C::kCost, 1};
   gqa8_total(a, kind, blockIdx.x == 0, &sm.total);
   fence_async_smem();
   tc_fence_before_sync();
@@ -613,7 +613,10 @@ constexpr int kManyThreads = 640;
 constexpr uint32_t kSoftmaxRegs = 104, kOtherRegs = 64, kLaunchRegs = 96;
 static_assert(4 * kSoftmaxRegs + kOtherRegs <= 5 * kLaunchRegs, "register shares draw on the launch's");
 
-constexpr int kManyCost = 10;   // of an item, in half tiles: q in, first scores, last product, output
+// What an item takes beyond its tiles (q in, first scores, last product, output),
+// in half tiles; of an item of at most 128 rows.  (A whole prompt of 8192: 619
+// us with 6, 541 with 8, 486 with 10, 488 with 12, 493 with 16.)
+constexpr int kManyCost = 10, kSharedCost = 4;
 
 struct ManySmall {
   uint64_t k_full[3], k_empty[3], v8_full[2], v8_empty[2], v_full[2], v_empty[2], item_full[2], item_empty[2],
@@ -676,7 +679,7 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
   grid_dependency_wait();
   grid_launch_dependents();
   __syncthreads();
-  const Gqa8Kind kind{min_rows, kAll, C::kRows, kManyCost, 128, 2};
+  const Gqa8Kind kind{min_rows, kAll, C::kRows, kManyCost, 128, kSharedCost, 2};
   gqa8_total(a, kind, blockIdx.x == 0 && min_rows == 1, &sm.total);
   tc_fence_before_sync();
   __syncthreads();

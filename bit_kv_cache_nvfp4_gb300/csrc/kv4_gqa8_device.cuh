@@ -250,9 +250,11 @@ struct Gqa8Kind {     // of requests that one of the kernels takes
   int min_rows, max_rows;
   int rows;           // of an item
   int cost;           // units of an item beyond its tiles
-  int half;           // items of at most so many rows: a unit a tile
-  int tile;           // others: so many
+  int half;           // items of at most so many rows: a unit a tile,
+  int half_cost;      //   and so many beyond them
+  int tile;           // others: so many a tile
   __device__ __forceinline__ int units(int n_rows) const { return n_rows <= half ? 1 : tile; }
+  __device__ __forceinline__ int beyond(int n_rows) const { return n_rows <= half ? half_cost : cost; }
 };
 constexpr int kWhole = 4, kLeast = 2;
 
@@ -271,7 +273,7 @@ __device__ __forceinline__ int64_t gqa8_units(const Gqa8AttnArgs& a, const Gqa8R
   const int R = q.n * G, groups = (R + kind.rows - 1) / kind.rows;
   auto units = [&](const Gqa8Request& r, int i, int n_rows) {
     const int r0 = i * kind.rows, r1 = min(n_rows, r0 + kind.rows);
-    return static_cast<int64_t>(gqa8_span(a, r, G, r0, r1).nt) * kind.units(r1 - r0) + kind.cost;
+    return static_cast<int64_t>(gqa8_span(a, r, G, r0, r1).nt) * kind.units(r1 - r0) + kind.beyond(r1 - r0);
   };
   int64_t u = 0;
   if (groups <= 2)
@@ -377,8 +379,8 @@ __device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, const Gqa8Kind&
         int64_t w = 0;
         if (gi < groups) {
           sp = gqa8_span(a, r, G, gi * kind.rows, min(R, (gi + 1) * kind.rows));
-          const int upt = kind.units(min(kind.rows, R - gi * kind.rows));
-          w = (static_cast<int64_t>(sp.nt) * upt + kind.cost) * a.Hkv;
+          const int n = min(kind.rows, R - gi * kind.rows);
+          w = (static_cast<int64_t>(sp.nt) * kind.units(n) + kind.beyond(n)) * a.Hkv;
         }
         int64_t g_end = w;
 #pragma unroll
@@ -394,11 +396,12 @@ __device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, const Gqa8Kind&
           const int t0 = __shfl_sync(0xFFFFFFFFu, sp.t0, gl), nt = __shfl_sync(0xFFFFFFFFu, sp.nt, gl);
           const int64_t at = __shfl_sync(0xFFFFFFFFu, g_end - w, gl);
           const int r0 = (g0 + gl) * kind.rows, nrows = min(kind.rows, R - r0), upt = kind.units(nrows);
-          const int64_t each = static_cast<int64_t>(nt) * upt + kind.cost;
+          const int cost = kind.beyond(nrows);
+          const int64_t each = static_cast<int64_t>(nt) * upt + cost;
           const int h0 = at < u0 ? static_cast<int>(quotient(u0 - at, each)) : 0;
           int64_t begin = at + h0 * each;
           for (int h = h0; h < a.Hkv && begin < u1; ++h, begin += each) {
-            const int tb = gqa8_cut(u0, begin, nt, upt, kind.cost), te = gqa8_cut(u1, begin, nt, upt, kind.cost);
+            const int tb = gqa8_cut(u0, begin, nt, upt, cost), te = gqa8_cut(u1, begin, nt, upt, cost);
             int slot = -1;
             if (nt == 0) {
               // no tile to cut: the block that its first unit falls to
@@ -412,7 +415,7 @@ __device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, const Gqa8Kind&
               tail = true;
               // the last block that has some of it
               int last = static_cast<int>(quotient(begin + each - 1, per));
-              while (gqa8_cut(last * per, begin, nt, upt, kind.cost) == nt) --last;
+              while (gqa8_cut(last * per, begin, nt, upt, cost) == nt) --last;
               if (lane == 0) tails[me] = Gqa8Tail{last - me + 1, r.cu0, h, r0, nrows, {}};
             }
             emit(Gqa8Item{base + l, h, r.cu0, r.pos0, r0, nrows, klo, khi, t0 + tb, t0 + te, slot});

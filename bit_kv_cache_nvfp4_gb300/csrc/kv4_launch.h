@@ -93,6 +93,8 @@ struct Gqa8Args {
   const int32_t* page_table;
   int64_t pt_stride;
   int B, Hkv, D;
+  int each;                    // pages a thread block looks after (set by the launch)
+  int num_sms;
   uint8_t* pool;               // [num_pages, Hkv, 2, 64, D] E4M3
   uint8_t* scales;             // [num_pages, Hkv, 2] E8M0
   int64_t num_pages;
