@@ -624,13 +624,13 @@ struct ManySmall {
   unsigned long long total;
   uint32_t tmem;
   int dead;
-  int exps[8][2];
+  alignas(16) float4 exps[8][2];    // per tile and page: 2^eK, eV, 2^-eV, 0 where there is no page
   Gqa8Item items[2];
   float qf[2][128];           // sm_scale log2(e) 2^eq of a row, NaN where q is not finite
   float top[2][2][2][128];    // largest score and V exponent of a half row, by row tile and tile parity
   float last[2][3][128];      // at an item's end: sums of both halves, reference
 };
-static_assert(sizeof(ManySmall) <= 9216, "ManySmall");
+static_assert(sizeof(ManySmall) <= 9216 && offsetof(ManySmall, exps) % 16 == 0, "ManySmall");
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kManyThreads, 1)
@@ -719,16 +719,19 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
           int block, ex;
           gqa8_pages(a, it, t, lane, block, ex);
           const int nt = min(16, it.t_end - t);
+          const bool there = ex != kMasked;
+          const int ev = there ? ex >> 16 : kGqa8ExpMin;
+          const float4 e4 = make_float4(there ? pow2f(static_cast<int16_t>(ex & 0xFFFF)) : 1.0f,
+                                        static_cast<float>(ev), pow2f(-ev), there ? 1.0f : 0.0f);
           for (int i = 0; i < nt; ++i, ++n_tiles) {
             const int b0 = __shfl_sync(0xFFFFFFFFu, block, 2 * i), b1 = __shfl_sync(0xFFFFFFFFu, block, 2 * i + 1);
-            const int e0 = __shfl_sync(0xFFFFFFFFu, ex, 2 * i), e1 = __shfl_sync(0xFFFFFFFFu, ex, 2 * i + 1);
             const int ks = n_tiles % KS, vs = n_tiles % VS;
             wait(sm.k_empty[ks], ((n_tiles / KS) & 1) ^ 1);
+            // (the softmax of the tile eight before is done: QK of the tile KS
+            // before, which this stage waited for, came after it)
+            if ((lane >> 1) == i) sm.exps[n_tiles & 7][lane & 1] = e4;
+            __syncwarp();
             if (lane == 0 && !*dead) {
-              // (the softmax of the tile eight before is done: QK of the tile
-              // KS before, which this stage waited for, came after it)
-              sm.exps[n_tiles & 7][0] = e0;
-              sm.exps[n_tiles & 7][1] = e1;
               mbar_arrive(smem_addr(&sm.ex_full[n_tiles & 7]));
               const uint32_t bar = smem_addr(&sm.k_full[ks]), dst = smem_addr(k_s + ks * C::kK);
               mbar_arrive_expect_tx(bar, C::kK);
@@ -984,9 +987,8 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
       const int s = n_items & 1;
       wait(sm.item_full[s], (n_items >> 1) & 1);
       if (named_sync_or(bar_rows, 128, *dead != 0)) break;     // (together, for they meet at barriers)
+      // (read again at its end, so that the loop over the tiles does not hold it)
       const Gqa8Item it = sm.items[s];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
       if (it.b < 0) break;
       const int nt = it.t_end - it.t_begin;
       const bool shared = it.nrows <= 128;                // both row tiles are the same rows
@@ -1053,31 +1055,33 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
       const bool odd = qf != qf;
       if (odd) qf = 0.0f;
       float mref = kLowest, l = 0.0f;
+      // pages that begin before `full` and not before `open` are every row's whole
+      int full = hi - 63, open = lo;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        full = min(full, __shfl_xor_sync(0xFFFFFFFFu, full, off));
+        open = max(open, __shfl_xor_sync(0xFFFFFFFFu, open, off));
+      }
       const int first = it.t_begin + (shared ? qt : 0), step = shared ? 2 : 1;
       for (int t = first; t < it.t_end; t += step, ++n_mine) {
         const uint32_t jt = j + (t - it.t_begin);
+        const int at = t * kTileKeys + half * 64;
         wait(sm.ex_full[jt & 7], (jt >> 3) & 1);
-        const int ex = sm.exps[jt & 7][half];
+        const float4 ex = sm.exps[jt & 7][half];
         wait(sm.s_full[qt], n_mine & 1);
         tc_fence_after_sync();
         float x[64];
         tmem_ld32(s_tm, reinterpret_cast<uint32_t(&)[32]>(x[0]));
         tmem_ld32(s_tm + 32, reinterpret_cast<uint32_t(&)[32]>(x[32]));
-        // keys of this row in the page: [c0, c1)
-        const int at = t * kTileKeys + half * 64, c0 = lo - at, c1 = hi - at;
-        const bool edge = __any_sync(0xFFFFFFFFu, c0 > 0 || c1 < 64) || ex == kMasked;
-        const int a0 = max(c0, 0), n = ex == kMasked ? 0 : max(min(c1, 64) - a0, 0);
-        auto mask = [&](int from) {
-#pragma unroll
-          for (int c = from; c < from + 32; ++c)
-            x[c] = static_cast<unsigned>(c - a0) < static_cast<unsigned>(n) ? x[c] : -INFINITY;
-        };
         float m[4];
         tmem_wait_ld32(reinterpret_cast<uint32_t(&)[32]>(x[0]));
         tmem_wait_ld32(reinterpret_cast<uint32_t(&)[32]>(x[32]));
-        if (edge) {
-          mask(0);
-          mask(32);
+        if (at >= full || at < open || ex.w == 0.0f) {
+          // keys of this row in the page: [a0, a0 + n)
+          const int a0 = max(lo - at, 0), n = ex.w == 0.0f ? 0 : max(min(hi - at, 64) - a0, 0);
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            x[c] = static_cast<unsigned>(c - a0) < static_cast<unsigned>(n) ? x[c] : -INFINITY;
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) m[k] = fmaxf(x[k], x[4 + k]);
@@ -1085,10 +1089,9 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
         for (int c = 8; c < 64; c += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k) m[k] = max3(m[k], x[c + k], x[c + 4 + k]);
-        const int ev = ex == kMasked ? kGqa8ExpMin : ex >> 16;
         // (at least 2^-126, so that a masked -inf stays one where the scale is 0)
-        const float f = fmaxf(qf * pow2f(ex == kMasked ? 0 : static_cast<int16_t>(ex & 0xFFFF)), 0x1p-126f);
-        float top = fmaf(max3(m[0], m[1], fmaxf(m[2], m[3])), f, static_cast<float>(ev));
+        const float f = fmaxf(qf * ex.x, 0x1p-126f);
+        float top = fmaf(max3(m[0], m[1], fmaxf(m[2], m[3])), f, ex.y);
         sm.top[qt][n_mine & 1][half][row] = top;
         named_sync(bar, 64);
         top = fmaxf(top, sm.top[qt][n_mine & 1][half ^ 1][row]);
@@ -1109,7 +1112,7 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
             }
           }
         }
-        const float b = static_cast<float>(ev) - mref + 8.0f;
+        const float b = ex.y - mref + 8.0f;
         const float2 f2 = make_float2(f, f), b2 = make_float2(b, b);
         float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
@@ -1130,7 +1133,7 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
           if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[qt][q]));
         }
         acc[0] = add2(acc[0], acc[1]);
-        l = fmaf(acc[0].x + acc[0].y, pow2f(-ev), l);
+        l = fmaf(acc[0].x + acc[0].y, ex.z, l);
       }
       j += nt;
       sm.last[qt][half][row] = l;
@@ -1142,6 +1145,9 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
       }
       if (shared) named_sync(bar_rows, 128);
       else named_sync(bar, 64);
+      const Gqa8Item fin = sm.items[s];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
       // out = (O_a w_a + O_b w_b) / (l_a w_a + l_b w_b), b the other row tile of
       // the same rows; both halves read the same numbers
       const int ta = shared ? 0 : qt;
@@ -1161,9 +1167,9 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
       const bool some = l > 0.0f || l != l;
       wa *= inv;
       wb *= inv;
-      const int r = it.r0 + base + row;
-      const int64_t part = static_cast<int64_t>(it.slot) * C::kRows + base + row;
-      const int64_t orow = static_cast<int64_t>(it.cu0 + r / G) * a.Hq + it.h * G + r % G;
+      const int r = fin.r0 + base + row;
+      const int64_t part = static_cast<int64_t>(fin.slot) * C::kRows + base + row;
+      const int64_t orow = static_cast<int64_t>(fin.cu0 + r / G) * a.Hq + fin.h * G + r % G;
       // Out through the rows of q's first two terms, which no product reads any
       // more, so that the stores to memory are up to D contiguous bytes: this
       // warp's columns of 16 bits, or half of them in fp32.
@@ -1174,7 +1180,7 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
       };
       // 16-byte chunks of a row: D / 16, half as many where the columns are
       // shared and of 16 bits
-      const bool cut = it.slot >= 0;
+      const bool cut = fin.slot >= 0;
       const int lg = (D == 128 ? 3 : 2) - (shared && !cut ? 1 : 0);
       uint8_t* const to = cut ? reinterpret_cast<uint8_t*>(ws_o) : static_cast<uint8_t*>(a.out);
       const int64_t row_at = cut ? part * (4 * D) : orow * (2 * D);
@@ -1217,14 +1223,14 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
             const int rr = i >> lg, c = i & ((1 << lg) - 1);
             const int64_t dst = __shfl_sync(0xFFFFFFFFu, at, rr);
             const uint4 v4 = *stage(rr, c);
-            if (base + wrow + rr < it.nrows) *reinterpret_cast<uint4*>(to + dst + c * 16) = v4;
+            if (base + wrow + rr < fin.nrows) *reinterpret_cast<uint4*>(to + dst + c * 16) = v4;
           }
           __syncwarp();
         }
       }
       if (mine && half == 0 && base == qt * 128) {
         const float ls = !some ? -INFINITY : odd ? __uint_as_float(0x7FC00000u) : mref - 8.0f + log2f(l);
-        if (it.slot >= 0) ws_lse[part] = ls;
+        if (fin.slot >= 0) ws_lse[part] = ls;
         else a.lse[orow] = ls * 0.6931471805599453f;
       }
       tc_fence_before_sync();
