@@ -994,8 +994,9 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
       const bool shared = it.nrows <= 128;                // both row tiles are the same rows
       const int base = shared ? 0 : qt * 128;
       const bool mine = base + row < it.nrows;
-      // keys at < hi and >= lo are this row's
-      int hi = 0, lo = 0;
+      // keys at < hi and >= lo are this row's (a row that is not there takes all,
+      // so that its warp needs no mask for it; its numbers go nowhere)
+      int hi = 0x7FFFFFFF, lo = 0;
       if (mine) {
         const int64_t pos = static_cast<int64_t>(it.pos0) + (it.r0 + base + row) / G;
         hi = static_cast<int>(max(min(pos + 1, static_cast<int64_t>(it.khi)), static_cast<int64_t>(0)));
