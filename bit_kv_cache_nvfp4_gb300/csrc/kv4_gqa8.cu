@@ -13,6 +13,9 @@
 // the unit whose maximum it needs: its 64 x D values (16 KB of inputs at
 // D = 128) stay in the threads' registers between the maximum and the codes, so
 // the inputs are read once.  The read-back gives a block to a page and head.
+// Both are bound by HBM in large calls (9 prompts, 171 MB: 27.3 us, 6.3 TB/s; 12
+// prefixes read back, 431 MB: 71 us, 6.0 TB/s) and by three dependent loads
+// (request, page, block) in small ones (one token: 2.6 us).
 #include "kv4_gqa8_device.cuh"
 
 namespace kv4 {

@@ -44,6 +44,10 @@ namespace {
 // O^T).  Two blocks share an SM, with one softmax warpgroup each, where they
 // fit; else one block has two warpgroups that take every other tile, each with
 // a running output of its own, joined at the item's end.
+//
+// Measured (D = 128, bf16): 64 sessions of up to 32768 tokens, 8 heads a group,
+// 2.29 GB of codes: 340 us, 6.7 TB/s, the rate of a copy; 16 heads a group 357
+// us; 2 x 204800 tokens cut over 304 blocks 133 us with the joining kernel.
 template <int D_, int RP_, int NT_>
 struct FewCfg {
   static constexpr int D = D_, RP = RP_, NT = NT_;
@@ -597,6 +601,10 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
 // agree on for every tile.  A row's reference only moves, and its O in TMEM is
 // only rescaled, when that rises by more than 2^6 (p stays below 2^14, f16's
 // top is 2^16).
+//
+// Measured (D = 128, 32 heads over 8, bf16): 2 x 2048 new tokens over 16384 605
+// us, 1.34 PFLOP/s (71 % of the measured bf16 rate; without the softmax the
+// products alone took 500); a prompt of 8192 470 us, 1.17.
 template <int D_, int NT_>
 struct ManyCfg {
   static constexpr int D = D_, NT = NT_, kRows = 256;
