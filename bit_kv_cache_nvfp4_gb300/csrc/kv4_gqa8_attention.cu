@@ -165,7 +165,8 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
     auto publish = [&](const Gqa8Item& it) {
       const int s = n_items & 3;
       wait(sm.item_empty[s], ((n_items >> 2) & 1) ^ 1);
-      if (lane == 0) {
+      // (of a wait that gave up the item before may still be in use)
+      if (lane == 0 && !*dead) {
         sm.items[s] = it;
         mbar_arrive(smem_addr(&sm.item_full[s]));
       }
@@ -181,7 +182,8 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
           const int e0 = __shfl_sync(0xFFFFFFFFu, ex, 2 * i), e1 = __shfl_sync(0xFFFFFFFFu, ex, 2 * i + 1);
           const int s = n_tiles % ST;
           wait(sm.empty[s], ((n_tiles / ST) & 1) ^ 1);
-          if (lane == 0 && !*dead) {
+          if (__any_sync(0xFFFFFFFFu, *dead != 0)) return;   // n_tiles counts the loads that began
+          if (lane == 0) {
             sm.exps[s][0] = e0;
             sm.exps[s][1] = e1;
             const uint32_t bar = smem_addr(&sm.full[s]), dst = smem_addr(smem + s * C::kTile);
@@ -233,6 +235,16 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
     };
     auto ready = [&](uint64_t& bar, uint32_t parity) {
       return __any_sync(0xFFFFFFFFu, mbar_try_wait(smem_addr(&bar), parity));
+    };
+    // In a block that gave up nothing else waits for the products that are
+    // still queued: they end before its memory goes away.
+    auto drain = [&] {
+      if (a.fault_site == 1) wait(sm.never, 0);
+      __syncwarp();
+      if (!__any_sync(0xFFFFFFFFu, *dead != 0)) return;
+      if (elect_one()) mma_commit(smem_addr(&sm.never));
+      __syncwarp();
+      mbar_wait_bounded(smem_addr(&sm.never), 0, 1000000);
     };
     bool pending = false;
     while (true) {
@@ -287,11 +299,11 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.q_empty[qb]));
       }
+      if (a.fault_site == 1) wait(sm.never, 0);
       ++n_items;
     }
     if (pending) pv(n_tiles - 1);
-    if (a.fault_site == 1) wait(sm.never, 0);
-    __syncwarp();
+    drain();
   } else if (warp < 4) {
     // ==== q of the next item, as NT E4M3 terms ====
     constexpr int TPR = D / 16, RPP = 64 / TPR;           // threads a row, rows at once
@@ -716,7 +728,8 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
       auto publish = [&](const Gqa8Item& it) {
         const int s = n_items & 1;
         wait(sm.item_empty[s], ((n_items >> 1) & 1) ^ 1);
-        if (lane == 0) {
+        // (of a wait that gave up the item before may still be in use)
+        if (lane == 0 && !*dead) {
           sm.items[s] = it;
           mbar_arrive(smem_addr(&sm.item_full[s]));
         }
@@ -735,11 +748,12 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
             const int b0 = __shfl_sync(0xFFFFFFFFu, block, 2 * i), b1 = __shfl_sync(0xFFFFFFFFu, block, 2 * i + 1);
             const int ks = n_tiles % KS, vs = n_tiles % VS;
             wait(sm.k_empty[ks], ((n_tiles / KS) & 1) ^ 1);
+            if (__any_sync(0xFFFFFFFFu, *dead != 0)) return;  // n_tiles counts the loads that began
             // (the softmax of the tile eight before is done: QK of the tile KS
             // before, which this stage waited for, came after it)
             if ((lane >> 1) == i) sm.exps[n_tiles & 7][lane & 1] = e4;
             __syncwarp();
-            if (lane == 0 && !*dead) {
+            if (lane == 0) {
               mbar_arrive(smem_addr(&sm.ex_full[n_tiles & 7]));
               const uint32_t bar = smem_addr(&sm.k_full[ks]), dst = smem_addr(k_s + ks * C::kK);
               mbar_arrive_expect_tx(bar, C::kK);
@@ -916,9 +930,17 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
           }
         }
         n_tiles += nt;
+        if (a.fault_site == 1) wait(sm.never, 0);
       }
       if (a.fault_site == 1) wait(sm.never, 0);
+      // in a block that gave up nothing else waits for the products that are
+      // still queued: they end before its memory goes away
       __syncwarp();
+      if (__any_sync(0xFFFFFFFFu, *dead != 0)) {
+        if (elect_one()) mma_commit(smem_addr(&sm.never));
+        __syncwarp();
+        mbar_wait_bounded(smem_addr(&sm.never), 0, 1000000);
+      }
     } else {
       // ==== V to f16 ====
       uint32_t j = 0;

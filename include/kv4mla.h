@@ -568,9 +568,10 @@ kv4_status kv4_attention_gqa8(const void* q_dev, int64_t q_token_stride, int64_t
                               void* out_dev, float* lse_dev, void* workspace_dev,
                               size_t workspace_bytes, int32_t* dev_err, kv4_stream_t stream);
 
-/* Test hook: the next decode launches use this bounded-wait limit (ns; 0
+/* Test hook: the next decode and attention launches use this bounded-wait limit (ns; 0
  * keeps the 1 s default) and, when fault_site == 1, one warp of each block
- * finishes its work and then waits on an mbarrier that nothing arrives on,
+ * finishes its work (kv4_attention_gqa8: its first item, so that the block
+ * gives up the others) and then waits on an mbarrier that nothing arrives on,
  * so that the wait runs out and KV4_DEV_TIMEOUT is reported while the block
  * still exits normally.  fault_site must be 0 or 1.  0, 0 restores the
  * defaults. */

@@ -482,6 +482,33 @@ def test_attention_reports_a_wait_that_runs_out():
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("d,dtype,hq,n", [(128, BF16, 4, 1), (128, F16, 12, 1), (64, BF16, 4, 3), (128, BF16, 4, 40),
+                                          (64, F16, 8, 70)])
+def test_a_wait_that_runs_out_with_work_left(d, dtype, hq, n):
+    """Blocks that give up in the middle of several items: the call ends, no row
+    behind the last request is written, and the next call is whole."""
+    device = dev()
+    B = 700 if n < 8 else 250
+    lens = [n + (i * 53) % 700 for i in range(B)]
+    c = ref.Cache(lens, 2, d, device, seed=25)
+    q = torch.randn(n * B + 5, hq, d, device=device).to(dtype)
+    args = (q, c.pool, c.scales, c.page_table, c.seq_lens, ints(ref.cu_of([n] * B), device), n, 0.09)
+    want = kv.attention_gqa8(*args)
+    err = torch.zeros(1, dtype=torch.int32, device=device)
+    out, lse = (torch.full((n * B + 5, hq, d), 3.0, dtype=dtype, device=device),
+                torch.full((n * B + 5, hq), 3.0, device=device))
+    kv.set_wait_limit(1_000_000, 1)
+    try:
+        kv.attention_gqa8(*args, out=out, lse=lse, dev_err=err)
+        torch.cuda.synchronize()
+    finally:
+        kv.set_wait_limit()
+    assert int(err.item()) == kv.DEV_TIMEOUT
+    assert (out[n * B:] == 3).all() and (lse[n * B:] == 3).all()
+    got = kv.attention_gqa8(*args)
+    assert torch.equal(got[0][:n * B], want[0][:n * B]) and torch.equal(got[1][:n * B], want[1][:n * B])
+
+
 @pytest.mark.parametrize("B,news", [(33, (1,)), (40, (0, 3, 70)), (1030, (1, 0, 2)), (1100, (9, 0, 1))])
 def test_append_and_read_many_requests(B, news):
     """More requests than a warp looks at in one round, in two rounds; some
