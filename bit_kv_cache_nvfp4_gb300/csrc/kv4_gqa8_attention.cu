@@ -161,7 +161,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
 
   if (warp == 0) {
     // ==== work list and loads ====
-    uint32_t n_items = 0, n_tiles = 0;
+    uint32_t n_items = 0, n_tiles = 0, n_loads = 0;       // tiles; loads that lane 0 began
     auto publish = [&](const Gqa8Item& it) {
       const int s = n_items & 3;
       wait(sm.item_empty[s], ((n_items >> 2) & 1) ^ 1);
@@ -182,8 +182,8 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
           const int e0 = __shfl_sync(0xFFFFFFFFu, ex, 2 * i), e1 = __shfl_sync(0xFFFFFFFFu, ex, 2 * i + 1);
           const int s = n_tiles % ST;
           wait(sm.empty[s], ((n_tiles / ST) & 1) ^ 1);
-          if (__any_sync(0xFFFFFFFFu, *dead != 0)) return;   // n_tiles counts the loads that began
-          if (lane == 0) {
+          if (lane == 0 && !*dead) {
+            n_loads = n_tiles + 1;
             sm.exps[s][0] = e0;
             sm.exps[s][1] = e1;
             const uint32_t bar = smem_addr(&sm.full[s]), dst = smem_addr(smem + s * C::kTile);
@@ -207,7 +207,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
     for (uint32_t i = n_tiles > ST ? n_tiles - ST : 0; i < n_tiles; ++i)
       wait(sm.empty[i % ST], (i / ST) & 1);
     if (*dead && lane == 0)
-      for (uint32_t i = n_tiles > ST ? n_tiles - ST : 0; i < n_tiles; ++i)
+      for (uint32_t i = n_loads > ST ? n_loads - ST : 0; i < n_loads; ++i)
         mbar_wait_bounded(smem_addr(&sm.full[i % ST]), (i / ST) & 1, 1000000);
   } else if (warp == 1) {
     // ==== products (the whole warp; one lane issues) ====
@@ -614,9 +614,9 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
 // only rescaled, when that rises by more than 2^6 (p stays below 2^14, f16's
 // top is 2^16).
 //
-// Measured (D = 128, 32 heads over 8, bf16): 2 x 2048 new tokens over 16384 605
-// us, 1.34 PFLOP/s (71 % of the measured bf16 rate; without the softmax the
-// products alone took 500); a prompt of 8192 470 us, 1.17.
+// Measured (D = 128, 32 heads over 8, bf16): 2 x 2048 new tokens over 16384 613
+// us, 1.32 PFLOP/s (70 % of the measured bf16 rate; without the softmax the
+// products alone took 500); a prompt of 8192 472 us, 1.17.
 template <int D_, int NT_>
 struct ManyCfg {
   static constexpr int D = D_, NT = NT_, kRows = 256;
@@ -724,7 +724,7 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
     setmaxnreg_dec<kOtherRegs>();
     if (warp == 0) {
       // ==== work list and loads ====
-      uint32_t n_items = 0, n_tiles = 0;
+      uint32_t n_items = 0, n_tiles = 0, n_loads = 0;     // tiles; loads that lane 0 began
       auto publish = [&](const Gqa8Item& it) {
         const int s = n_items & 1;
         wait(sm.item_empty[s], ((n_items >> 1) & 1) ^ 1);
@@ -748,12 +748,12 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
             const int b0 = __shfl_sync(0xFFFFFFFFu, block, 2 * i), b1 = __shfl_sync(0xFFFFFFFFu, block, 2 * i + 1);
             const int ks = n_tiles % KS, vs = n_tiles % VS;
             wait(sm.k_empty[ks], ((n_tiles / KS) & 1) ^ 1);
-            if (__any_sync(0xFFFFFFFFu, *dead != 0)) return;  // n_tiles counts the loads that began
             // (the softmax of the tile eight before is done: QK of the tile KS
             // before, which this stage waited for, came after it)
             if ((lane >> 1) == i) sm.exps[n_tiles & 7][lane & 1] = e4;
             __syncwarp();
-            if (lane == 0) {
+            if (lane == 0 && !*dead) {
+              n_loads = n_tiles + 1;
               mbar_arrive(smem_addr(&sm.ex_full[n_tiles & 7]));
               const uint32_t bar = smem_addr(&sm.k_full[ks]), dst = smem_addr(k_s + ks * C::kK);
               mbar_arrive_expect_tx(bar, C::kK);
@@ -782,9 +782,9 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
         wait(sm.k_empty[i % KS], (i / KS) & 1);
       for (uint32_t i = n_tiles > 2 ? n_tiles - 2 : 0; i < n_tiles; ++i) wait(sm.v_empty[i & 1], (i >> 1) & 1);
       if (*dead && lane == 0) {
-        for (uint32_t i = n_tiles > KS ? n_tiles - KS : 0; i < n_tiles; ++i)
+        for (uint32_t i = n_loads > KS ? n_loads - KS : 0; i < n_loads; ++i)
           mbar_wait_bounded(smem_addr(&sm.k_full[i % KS]), (i / KS) & 1, 1000000);
-        for (uint32_t i = n_tiles > VS ? n_tiles - VS : 0; i < n_tiles; ++i)
+        for (uint32_t i = n_loads > VS ? n_loads - VS : 0; i < n_loads; ++i)
           mbar_wait_bounded(smem_addr(&sm.v8_full[i % VS]), (i / VS) & 1, 1000000);
       }
     } else if (warp == 1) {
