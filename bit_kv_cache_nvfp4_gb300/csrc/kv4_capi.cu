@@ -948,7 +948,7 @@ kv4_status check_gqa8(int64_t n_tokens, int heads, int Hkv, int D, int B, int dt
                       int page_size, int64_t num_pages, int64_t pt_stride) {
   if (n_tokens < 0 || B < 0 || B > 65535 || Hkv < 1 || heads < 1) return KV4_ERR_INVALID_ARG;
   if (page_size != KV4_PAGE || (D != 64 && D != 128) || (dtype != KV4_BF16 && dtype != KV4_F16) ||
-      Hkv > 65535)
+      Hkv > 32767)                                                        // grid rows: two a head
     return KV4_ERR_UNSUPPORTED;
   if (n_tokens > INT32_MAX || n_tokens * heads > (1LL << 40) / D) return KV4_ERR_INVALID_ARG;
   if (num_pages < 0 || num_pages >= INT32_MAX || pt_stride < 1 || pt_stride > INT32_MAX)
@@ -976,6 +976,7 @@ kv4_status kv4_append_gqa8(const void* k_dev, int64_t k_token_stride, int64_t k_
   const kv4_status shape = check_gqa8(n_tokens, Hkv, Hkv, D, B, dtype, page_size, num_pages, pt_stride);
   if (shape != KV4_OK) return shape;
   if (n_tokens == 0 || B == 0) return KV4_OK;
+  if (num_pages < 1) return KV4_ERR_INVALID_ARG;
   if (!k_dev || !v_dev || !cu_seqlens_dev || !page_table_dev || !seq_lens_dev || !pool_dev ||
       !scales_dev)
     return KV4_ERR_INVALID_ARG;
@@ -1021,6 +1022,7 @@ kv4_status kv4_read_gqa8(const uint8_t* pool_dev, const uint8_t* scales_dev, int
   const kv4_status shape = check_gqa8(n_tokens, Hkv, Hkv, D, B, dtype, page_size, num_pages, pt_stride);
   if (shape != KV4_OK) return shape;
   if (n_tokens == 0 || B == 0) return KV4_OK;
+  if (num_pages < 1) return KV4_ERR_INVALID_ARG;
   if (!pool_dev || !scales_dev || !page_table_dev || !starts_dev || !cu_seqlens_dev ||
       !k_out_dev || !v_out_dev)
     return KV4_ERR_INVALID_ARG;
@@ -1083,7 +1085,7 @@ kv4_status kv4_attention_gqa8(const void* q_dev, int64_t q_token_stride, int64_t
   if (Hq / Hkv > 128) return KV4_ERR_UNSUPPORTED;
   if (n_tokens * (Hq / Hkv) > INT32_MAX) return KV4_ERR_INVALID_ARG;     // rows of a request
   if (n_tokens == 0 || B == 0) return KV4_OK;
-  if (max_new == 0) return KV4_ERR_INVALID_ARG;
+  if (max_new == 0 || num_pages < 1) return KV4_ERR_INVALID_ARG;
   if (!q_dev || !cu_seqlens_dev || !pool_dev || !scales_dev || !page_table_dev || !seq_lens_dev ||
       !out_dev || !lse_dev)
     return KV4_ERR_INVALID_ARG;

@@ -507,10 +507,12 @@ size_t kv4_noalloc_scratch_bytes(void);
  *                   position is negative is skipped); rows from cu[B] on are
  *                   neither read nor written
  *   dtype           KV4_BF16 or KV4_F16, of k, v, q, out and the read-back
- *   Hkv, D          Hkv >= 1; D = 64 or 128
- * Sizes: n_tokens * heads * D < 2^40, B <= 65535, 2 Hkv num_pages < 2^31 - 1.
- * Inputs are strided (in elements, multiples of 8; base 16-byte aligned), so
- * slices of a fused projection's output need no copy; outputs are contiguous.
+ *   Hkv, D          1 <= Hkv <= 32767; D = 64 or 128
+ * Sizes: n_tokens * heads * D <= 2^40, n_tokens * (Hq / Hkv) < 2^31, B <= 65535,
+ * 2 Hkv num_pages < 2^31 - 1; unless n_tokens or B is 0, num_pages >= 1.
+ * Inputs are strided (in elements, multiples of 8, heads at least D apart; base
+ * 16-byte aligned), so slices of a fused projection's output need no copy;
+ * outputs are contiguous, and none overlaps an input.
  * A page index past the table, a negative entry or one >= num_pages raises
  * KV4_DEV_BAD_PAGE: the write skips the page, the read gives zeros, the
  * attention masks its keys.  Nothing else of the device-side data can lead
@@ -524,7 +526,7 @@ size_t kv4_noalloc_scratch_bytes(void);
  *   the new one.  code = E4M3(x * 2^-e), round half to even, saturating; NaN
  *   gives code 0 and an infinity +-448, both with KV4_DEV_NONFINITE.  Rows
  *   past the last token are left as they are.  A page that receives tokens
- *   belongs to one request of the call.
+ *   stands in one place of one request's table.
  * kv4_read_gqa8 -- the values of positions starts[b] .. starts[b] + n - 1 of
  *   each request (n = cu[b+1] - cu[b]), 16-bit [n_tokens, Hkv, D] each for K
  *   and V, 16-byte aligned: code * 2^e, rounded once; f16 saturates at 65504.
@@ -540,6 +542,8 @@ size_t kv4_noalloc_scratch_bytes(void);
  *   workspace_dev   at least the bytes kv4_attention_gqa8_plan returns for the
  *                   same sizes, 16-byte aligned, of this call alone while it
  *                   runs; nothing in it needs a value
+ *   Scale exponents outside [-48, 48], which the append never writes, count as
+ *   the nearer end (the read-back takes them as they are).
  *   A row of q with a NaN or an infinity gives NaN (when it has a key).  A
  *   NaN code (0x7F, 0xFF) in a row below seq_lens, which the append never
  *   writes, may turn any row of the request NaN; what lies past seq_lens, or

@@ -72,6 +72,15 @@ def test_attention_refuses(lib, mem, change, status):
     assert lib.kv4_attention_gqa8(*attention_args(mem[1], **change)) == status
 
 
+@pytest.mark.parametrize("change,status", [(dict(pages=0), BAD), (dict(hkv=32768, ks1=64, vs1=64), UNSUPPORTED)])
+def test_no_pages_and_too_many_heads_are_refused(lib, mem, change, status):
+    rest = {k: v for k, v in change.items() if k not in ("ks1", "vs1")}
+    assert lib.kv4_append_gqa8(*append_args(mem[1], **change)) == status
+    assert lib.kv4_read_gqa8(*read_args(mem[1], **rest)) == status
+    hq = {"hq": rest["hkv"]} if "hkv" in rest else {}
+    assert lib.kv4_attention_gqa8(*attention_args(mem[1], **rest, **hq)) == status
+
+
 def test_misaligned_pointers_are_refused(lib, mem):
     p = mem[1]
     assert lib.kv4_append_gqa8(*append_args(p, pool=p + 64)) == BAD
