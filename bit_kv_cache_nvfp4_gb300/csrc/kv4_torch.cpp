@@ -71,13 +71,14 @@ int dtype_code(at::ScalarType t, const char* name) {
   type_error(std::string(name) + " must be bfloat16 or float16, got " + name_of(t));
 }
 // A [T, heads, D] input: last dimension contiguous, the others any multiple of
-// 16 bytes.
+// 16 bytes.  (The stride of a dimension of one element says nothing: a
+// contiguous tensor may have any.)
 struct Strided {
   const void* p;
   int64_t token, head;
 };
 Strided strided(const at::Tensor& t, const char* name) {
-  Strided s{t.const_data_ptr(), t.stride(0), t.stride(1)};
+  Strided s{t.const_data_ptr(), t.size(0) > 1 ? t.stride(0) : 0, t.size(1) > 1 ? t.stride(1) : 0};
   if (t.stride(2) != 1 || s.token % 8 != 0 || s.head % 8 != 0 || (reinterpret_cast<uintptr_t>(s.p) & 15) != 0)
     value_error(std::string(name) +
                 ": the last dimension must be contiguous, the other strides multiples of 8 elements "
@@ -102,7 +103,7 @@ Cache cache(PyObject* pool_o, PyObject* scales_o, PyObject* table_o) {
   const at::Tensor& scales = plain(scales_o, "scales", at::kByte, 3, c.dev);
   const at::Tensor& table = plain(table_o, "page_table", at::kInt, 2, c.dev);
   c.pages = pool.size(0);
-  if (pool.size(1) < 1 || pool.size(1) > 65535) value_error("the cache needs 1 to 65535 heads");
+  if (pool.size(1) < 1 || pool.size(1) > 65535) value_error("pool: no or too many heads");
   c.hkv = static_cast<int>(pool.size(1));
   c.d = static_cast<int>(std::min<int64_t>(pool.size(4), 1 << 20));
   if (scales.size(0) != c.pages || scales.size(1) != c.hkv || scales.size(2) != 2)

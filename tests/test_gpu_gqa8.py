@@ -527,3 +527,199 @@ def test_append_and_read_many_requests(B, news):
         want = ref.values(c.pool, c.scales, c.table[b], lens[b] - news[b], lens[b])
         assert torch.equal(k[cu[b]:cu[b + 1]].double(), want[:, 0].transpose(0, 1))
         assert torch.equal(v[cu[b]:cu[b + 1]].double(), want[:, 1].transpose(0, 1))
+
+
+# ---------------------------------------------------------------------------
+# what the binding takes and refuses
+# ---------------------------------------------------------------------------
+def test_strides_of_single_elements_do_not_matter():
+    """One token, or one head: a contiguous tensor may have any stride there."""
+    device = dev()
+    c = ref.Cache([100], 1, 64, device, seed=26)
+    x = torch.randn(1, 1, 64, device=device).to(BF16)
+    odd = torch.as_strided(x.clone(), (1, 1, 64), (3, 5, 1))
+    assert odd.is_contiguous()
+    pools = []
+    for t in (x, odd):
+        pool, scales = c.pool.clone(), c.scales.clone()
+        kv.append_gqa8(t, t, ints([0, 1], device), c.page_table, c.seq_lens, pool, scales)
+        pools.append((pool, scales))
+    assert torch.equal(pools[0][0], pools[1][0]) and torch.equal(pools[0][1], pools[1][1])
+    a = [kv.attention_gqa8(t, c.pool, c.scales, c.page_table, c.seq_lens, ints([0, 1], device), 1, 0.125)
+         for t in (x, odd)]
+    assert torch.equal(a[0][0], a[1][0]) and torch.equal(a[0][1], a[1][1])
+
+
+def call_args(device):
+    """A small valid call of each kind, by argument name."""
+    c = ref.Cache([100, 30], 2, 64, device, seed=27)
+    x = torch.randn(5, 2, 64, device=device).to(BF16)
+    cu = ints([0, 3, 5], device)
+    cache = dict(pool=c.pool, scales=c.scales, page_table=c.page_table)
+    return {"append": (kv.append_gqa8, dict(k=x, v=x.clone(), cu_seqlens=cu, seq_lens=c.seq_lens, **cache)),
+            "read": (kv.read_gqa8, dict(starts=ints([3, 0], device), cu_seqlens=cu, total=5, **cache)),
+            "attention": (kv.attention_gqa8, dict(q=x.repeat(1, 2, 1), seq_lens=c.seq_lens, cu_seqlens=cu, max_new=3,
+                                                  sm_scale=0.125, **cache))}
+
+
+def unaligned(t):
+    return torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)[1:].view_as(t).copy_(t)
+
+
+CACHE_REFUSALS = [
+    ("pool", lambda t: t.cpu(), TypeError), ("pool", lambda t: t.view(torch.int8), TypeError),
+    ("pool", lambda t: t[:, :, :1], ValueError), ("pool", lambda t: t[..., :32], ValueError),
+    ("pool", lambda t: t.flatten(3), ValueError), ("pool", lambda t: t.transpose(0, 1), ValueError),
+    ("pool", unaligned, kv.Kv4Error), ("pool", lambda t: t[:0], ValueError),
+    ("scales", lambda t: t[:-1], ValueError), ("scales", lambda t: t.float(), TypeError),
+    ("scales", lambda t: None, TypeError), ("page_table", lambda t: t.long(), TypeError),
+    ("page_table", lambda t: t[:1], ValueError), ("page_table", lambda t: t[0], ValueError),
+    ("page_table", lambda t: t[:, ::2], ValueError), ("page_table", lambda t: t[:, :0], kv.Kv4Error),
+    ("cu_seqlens", lambda t: t[:2], ValueError), ("cu_seqlens", lambda t: t.cpu(), TypeError),
+    ("dev_err", lambda t: torch.zeros(1), TypeError),
+]
+INPUT_REFUSALS = [
+    (lambda t: t.float(), TypeError), (lambda t: t[:, :, :32], ValueError), (lambda t: t[..., ::2], ValueError),
+    (lambda t: t[:, :1], ValueError), (lambda t: unaligned(t), ValueError), (lambda t: t.cpu(), TypeError),
+    (lambda t: torch.empty(5, 1, 64, dtype=BF16, device=t.device).expand(t.shape), kv.Kv4Error),
+    (lambda t: torch.empty(5, t.shape[1], 68, dtype=BF16, device=t.device)[..., :64], ValueError),
+]
+REFUSALS = (
+    [(f, name, change, e) for f in ("append", "read", "attention") for name, change, e in CACHE_REFUSALS]
+    + [("append", name, change, e) for name in ("k", "v") for change, e in INPUT_REFUSALS]
+    + [("attention", "q", change, e) for change, e in INPUT_REFUSALS]
+    + [("append", "v", lambda t: t.half(), TypeError), ("append", "v", lambda t: t[:4], ValueError),
+       ("append", "seq_lens", lambda t: t[:1], ValueError), ("read", "starts", lambda t: t.long(), TypeError),
+       ("read", "total", lambda n: -1, ValueError), ("read", "total", lambda n: 2 ** 31, ValueError),
+       ("read", "total", lambda n: 5.0, TypeError), ("read", "dtype", lambda t: torch.float32, TypeError),
+       ("read", "k_out", lambda t: torch.empty(4, 2, 64, dtype=BF16, device="cuda"), ValueError),
+       ("read", "v_out", lambda t: torch.empty(5, 2, 64, dtype=F16, device="cuda"), TypeError),
+       ("read", "v_out", lambda t: torch.empty(5, 64, 2, dtype=BF16, device="cuda").mT, ValueError),
+       ("attention", "max_new", lambda n: 0, kv.Kv4Error), ("attention", "max_new", lambda n: -1, ValueError),
+       ("attention", "window", lambda n: -1, ValueError), ("attention", "sm_scale", lambda x: "a", TypeError),
+       ("attention", "sm_scale", lambda x: 1e300, kv.Kv4Error), ("attention", "sm_scale", lambda x: math.nan, kv.Kv4Error),
+       ("attention", "out", lambda t: torch.empty(5, 4, 64, dtype=F16, device="cuda"), TypeError),
+       ("attention", "lse", lambda t: torch.empty(4, 5, device="cuda").T, ValueError),
+       ("attention", "workspace", lambda t: torch.empty(1 << 26, dtype=torch.int32, device="cuda"), TypeError)])
+
+
+@pytest.mark.parametrize("i", range(len(REFUSALS)))
+def test_binding_refuses(i):
+    """Nothing is launched, and the next call is as if there had been none."""
+    f, name, change, error = REFUSALS[i]
+    fn, args = call_args(dev())[f]
+    pool = args["pool"].clone()
+    with pytest.raises(error):
+        fn(**{**args, name: change(args.get(name))})
+    assert torch.equal(args["pool"], pool)
+    fn(**args)
+    torch.cuda.synchronize()
+
+
+def test_empty_calls():
+    device = dev()
+    c = ref.Cache([100, 30], 2, 64, device, seed=28)
+    x = torch.empty(0, 2, 64, dtype=BF16, device=device)
+    cu, none = ints([0, 0, 0], device), ints([0], device)
+    pool = c.pool.clone()
+    kv.append_gqa8(x, x, cu, c.page_table, c.seq_lens, c.pool, c.scales)
+    k, v = kv.read_gqa8(c.pool, c.scales, c.page_table, ints([0, 0], device), cu, 0)
+    out, lse = kv.attention_gqa8(x, c.pool, c.scales, c.page_table, c.seq_lens, cu, 0, 0.1)
+    assert k.shape == v.shape == out.shape == (0, 2, 64) and lse.shape == (0, 2)
+    x = torch.ones(3, 2, 64, dtype=BF16, device=device)          # no request at all
+    kv.append_gqa8(x, x, none, c.page_table[:0], c.seq_lens[:0], c.pool, c.scales)
+    out, lse = torch.full((3, 2, 64), 3.0, dtype=BF16, device=device), torch.full((3, 2), 3.0, device=device)
+    kv.attention_gqa8(x, c.pool, c.scales, c.page_table[:0], c.seq_lens[:0], none, 1, 0.1, out=out, lse=lse)
+    assert torch.equal(c.pool, pool) and (out == 3).all() and (lse == 3).all()
+
+
+@pytest.mark.parametrize("cu", [[0, 40, 20, 70], [-9, 5, 2 ** 31 - 1, 3], [70, 0, -2 ** 31, 90], [0, 70, 70, 70]])
+@pytest.mark.parametrize("lens", [[2 ** 31 - 1, -2 ** 31, 5], [3, 2 ** 31 - 1, 2 ** 31 - 40], [90, 20, 60]])
+def test_lengths_and_pages_out_of_range_stay_in_bounds(cu, lens):
+    """Rows, lengths and page numbers that nobody should pass: what lies around
+    the call's tensors is left as it was.  (Every one of them is held to the
+    call's sizes before it makes an address.)"""
+    device = dev()
+    T, hq, hkv, d, pages = 70, 8, 2, 64, 8
+    g = torch.Generator(device=device).manual_seed(3)
+    pool = torch.randint(0, 126, (pages + 2, hkv, 2, 64, d), dtype=torch.uint8, device=device, generator=g)
+    scales = torch.full((pages + 2, hkv, 2), 127, dtype=torch.uint8, device=device)
+    table = ints([[0, 7, 2 ** 31 - 1, 3], [-2 ** 31, 1, 8, 2], [4, 4, 5, -1]], device)
+    guard_pool, guard_scales = pool.clone(), scales.clone()
+    cu_t, lens_t = ints(cu, device), ints(lens, device)
+    x = torch.randn(T, hq + 2 * hkv, d, device=device, generator=g).to(BF16)
+    cache = (pool[1:-1], scales[1:-1])
+    for max_new in (1, 70):
+        out = torch.full((T + 2, hq, d), 3.0, dtype=BF16, device=device)
+        lse = torch.full((T + 2, hq), 3.0, device=device)
+        kv.attention_gqa8(x[:, :hq], *cache, table, lens_t, cu_t, max_new, 0.125, out=out[1:-1], lse=lse[1:-1])
+        for t in (out, lse):
+            assert (t[0] == 3).all() and (t[-1] == 3).all()
+    ko = torch.full((T + 2, hkv, d), 3.0, dtype=BF16, device=device)
+    vo = ko.clone()
+    kv.read_gqa8(*cache, table, lens_t, cu_t, T, k_out=ko[1:-1], v_out=vo[1:-1])
+    for t in (ko, vo):
+        assert (t[0] == 3).all() and (t[-1] == 3).all()
+    kv.append_gqa8(x[:, hq:hq + hkv], x[:, hq + hkv:], cu_t, table, lens_t, *cache)
+    for t, was in ((pool, guard_pool), (scales, guard_scales)):
+        assert torch.equal(t[0], was[0]) and torch.equal(t[-1], was[-1])
+
+
+FIRST_CALLS = """
+import sys
+import torch
+sys.path.insert(0, sys.argv[1])
+import bit_kv_cache_nvfp4_gb300 as kv
+i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+pool = torch.zeros(8, 2, 2, 64, 64, dtype=torch.uint8, device="cuda")
+scales = torch.full((8, 2, 2), 127, dtype=torch.uint8, device="cuda")
+table, lens, cu = i([[0, 1, 2, 3], [4, 5, 6, 7]]), i([200, 1]), i([0, 200, 201])
+x = torch.randn(201, 12, 64, device="cuda").to(torch.bfloat16)
+starts = i([0, 0])
+def calls():
+    kv.append_gqa8(x[:, 8:10], x[:, 10:], cu, table, lens, pool, scales)
+    return (*kv.read_gqa8(pool, scales, table, starts, cu, 201),
+            *kv.attention_gqa8(x[:, :8], pool, scales, table, lens, cu, 200, 0.125))
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    kept = calls()
+g.replay()
+torch.cuda.synchronize()
+kept = [t.clone() for t in kept]
+assert all(torch.equal(a, b) for a, b in zip(kept, calls()))
+"""
+
+
+def test_first_calls_of_a_process_can_be_captured():
+    import pathlib
+    import subprocess
+    import sys
+    dev()
+    root = str(pathlib.Path(__file__).resolve().parents[1])
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS, root], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_calls_from_two_threads():
+    import threading
+    device = dev()
+    c = ref.Cache([3000, 70], 2, 128, device, seed=29)
+    q = torch.randn(41, 8, 128, device=device).to(BF16)
+    args = (q, c.pool, c.scales, c.page_table, c.seq_lens, ints([0, 1, 41], device), 40, 0.09)
+    want = kv.attention_gqa8(*args)
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got[i].append(kv.attention_gqa8(*args))
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for out, lse in got[0] + got[1]:
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
