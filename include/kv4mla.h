@@ -544,6 +544,8 @@ size_t kv4_noalloc_scratch_bytes(void);
  *                   runs; nothing in it needs a value
  *   Scale exponents outside [-48, 48], which the append never writes, count as
  *   the nearer end (the read-back takes them as they are).
+ *   Equal calls give equal bits; a row's last bits may differ with what else
+ *   is in the call, which decides where its keys are cut.
  *   A row of q with a NaN or an infinity gives NaN (when it has a key).  A
  *   NaN code (0x7F, 0xFF) in a row below seq_lens, which the append never
  *   writes, may turn any row of the request NaN; what lies past seq_lens, or

@@ -723,3 +723,89 @@ def test_calls_from_two_threads():
         t.join()
     for out, lse in got[0] + got[1]:
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+# ---------------------------------------------------------------------------
+# offsets beyond 32 bits
+# ---------------------------------------------------------------------------
+def test_pool_beyond_32_bits():
+    """A pool of 6.5 GB, its last pages used: as in a small one."""
+    device, pages = dev(), 200_000
+    lens, news = [300, 65, 1], [40, 1, 1]
+    c = ref.Cache(lens, 2, 128, device, seed=30)
+    n, cu = c.pool.shape[0], ints(ref.cu_of(news), device)
+    pool = torch.empty(pages, 2, 2, 64, 128, dtype=torch.uint8, device=device)
+    scales = torch.empty(pages, 2, 2, dtype=torch.uint8, device=device)
+    pool[pages - n:], scales[pages - n:] = c.pool, c.scales
+    table = torch.where(c.page_table < 0, c.page_table, c.page_table + (pages - n))
+    x = torch.randn(42, 12, 128, device=device).to(BF16)
+    starts = ints([9, 0, 0], device)
+    got = []
+    for p, s, t in ((c.pool, c.scales, c.page_table), (pool, scales, table)):
+        kv.append_gqa8(x[:, 8:10], x[:, 10:], cu, t, c.seq_lens, p, s)
+        got.append((p[-n:], s[-n:], *kv.read_gqa8(p, s, t, starts, cu, 42),
+                    *kv.attention_gqa8(x[:, :8], p, s, t, c.seq_lens, cu, 40, 0.09)))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_input_strides_beyond_32_bits():
+    """Tokens 1.5e9 elements apart."""
+    device = dev()
+    far = torch.empty(2 * 1_500_000_000 + 12 * 128, dtype=BF16, device=device)
+    x = torch.as_strided(far, (3, 12, 128), (1_500_000_000, 128, 1))
+    near = torch.randn(3, 12, 128, device=device).to(BF16)
+    x.copy_(near)
+    c = ref.Cache([80, 3], 2, 128, device, seed=31)
+    cu = ints([0, 2, 3], device)
+    got = []
+    for y in (near, x):
+        pool, scales = c.pool.clone(), c.scales.clone()
+        kv.append_gqa8(y[:, 8:10], y[:, 10:], cu, c.page_table, c.seq_lens, pool, scales)
+        got.append((pool, scales, *kv.attention_gqa8(y[:, :8], pool, scales, c.page_table, c.seq_lens, cu, 2, 0.09)))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_outputs_beyond_32_bits():
+    """2.7e9 elements of out and of the read-back.  The last rows of out within
+    their bounds, not bit for bit as in a call of their own: which of the two
+    warpgroups gets an item's even tiles depends on the tiles before it, and
+    with that the order in which a row's partial sums are added (a + b in fp32
+    is off by up to 2^-24 of itself either way, which the bounds count)."""
+    device = dev()
+    B, hkv, g, d = 65535, 16, 20, 128
+    c = ref.Cache([500], hkv, d, device, seed=32)
+    table = c.page_table[:, :8].expand(B, -1).contiguous()       # every request the same pages
+    lens = torch.randint(1, 500, (B,), dtype=torch.int32, device=device)
+    cu = torch.arange(B + 1, dtype=torch.int32, device=device)
+    q = torch.empty(B, hkv * g, d, dtype=BF16, device=device)
+    q[-9:] = torch.randn(9, hkv * g, d, device=device).to(BF16)
+    q[:-9] = q[-9:-8]
+    out, lse = kv.attention_gqa8(q, c.pool, c.scales, table, lens, cu, 1, 0.09)
+    want = ref.attention(q[-9:], c.pool, c.scales, c.table * 9, lens[-9:].tolist(), list(range(10)), 0.09)
+    tol, lse_tol = ref.bounds(*want, BF16, d)
+    assert ((out[-9:].double() - want[0]).abs() <= tol).all()
+    assert ((lse[-9:].double() - want[1]).abs() <= lse_tol).all()
+    del q, out, lse
+    n = 1_300_000                                                # tokens of a request that repeats its pages
+    row = c.page_table[0, :7].repeat(n // 448 + 1)[None].contiguous()
+    k, v = kv.read_gqa8(c.pool, c.scales, row, ints([0], device), ints([0, n], device), n)
+    last = kv.read_gqa8(c.pool, c.scales, row, ints([n - 100], device), ints([0, 100], device), 100)
+    assert torch.equal(k[-100:], last[0]) and torch.equal(v[-100:], last[1])
+
+
+def test_prompt_of_many_row_groups_and_its_last_rows():
+    """A prompt whose rows fill hundreds of items: its last rows as when they
+    are the only new ones, within the bounds of both."""
+    device = dev()
+    n, hq, d = 20011, 8, 64
+    c = ref.Cache([n], 1, d, device, seed=33)
+    q = torch.randn(n, hq, d, device=device).to(BF16)
+    out, lse = kv.attention_gqa8(q, c.pool, c.scales, c.page_table, c.seq_lens, ints([0, n], device), n, 0.125)
+    for first, count in ((0, 65), (10000, 30), (n - 33, 33)):
+        lens = [first + count]
+        want = ref.attention(q[first:first + count], c.pool, c.scales, c.table, lens, [0, count], 0.125, 0)
+        tol, lse_tol = ref.bounds(*want, BF16, d)
+        assert ((out[first:first + count].double() - want[0]).abs() <= tol).all()
+        assert ((lse[first:first + count].double() - want[1]).abs() <= lse_tol).all()
