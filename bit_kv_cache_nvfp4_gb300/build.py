@@ -67,7 +67,7 @@ def _torch_object():
     compile_cmd = (["g++", "-O2", "-std=c++20", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
                    + [f for d in inc for f in ("-isystem" if d != INCLUDE else "-I", d)]
                    + ["-c", os.path.join(CSRC, TORCH_SOURCE), "-o", obj])
-    link = ["-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+    link = ["-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
             "-L", HERE, "-l:libkv4mla.so", "-Wl,-rpath,$ORIGIN"]
     return obj, compile_cmd, link
 

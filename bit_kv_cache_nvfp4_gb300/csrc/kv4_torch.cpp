@@ -15,7 +15,8 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/pybind.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -147,9 +148,10 @@ int small(PyObject* o, const char* name) {
 kv4_stream_t stream_of(c10::Device dev) {
   return reinterpret_cast<kv4_stream_t>(c10::cuda::getCurrentCUDAStream(dev.index()).stream());
 }
-// An output: the caller's, checked, or a new one.
+// An output: the caller's, checked, or a new one (past the dispatcher, which
+// for a CUDA tensor only leads there).
 at::Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type, c10::Device dev) {
-  if (o == Py_None) return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+  if (o == Py_None) return at::Tensor(at::detail::empty_cuda(shape, type, dev, std::nullopt));
   const at::Tensor& t = plain(o, name, type, static_cast<int>(shape.size()), dev);
   if (t.sizes() != shape) {
     std::string s;
@@ -248,22 +250,26 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const c10::cuda::CUDAGuard guard(c.dev);
     const at::Tensor out = output(a[9], "out", {t, hq, c.d}, q.scalar_type(), c.dev);
     const at::Tensor lse = output(a[10], "lse", {t, hq}, at::kFloat, c.dev);
-    at::Tensor ws;
+    c10::DataPtr own;
+    void* ws = nullptr;
     size_t ws_bytes = 0;
     if (a[11] == Py_None) {
       const kv4_status st = kv4_attention_gqa8_plan(c.B, max_new, t, hq, c.hkv, c.d, &ws_bytes);
       if (st != KV4_OK) return PyLong_FromLong(st);
-      if (ws_bytes > 0)
-        ws = at::empty({static_cast<int64_t>(ws_bytes)}, at::TensorOptions().dtype(at::kByte).device(c.dev));
+      if (ws_bytes > 0) {
+        own = c10::cuda::CUDACachingAllocator::get()->allocate(ws_bytes);
+        ws = own.get();
+      }
     } else {
-      ws = plain(a[11], "workspace", at::kByte, 1, c.dev);
-      ws_bytes = ws.numel();
+      const at::Tensor& given = plain(a[11], "workspace", at::kByte, 1, c.dev);
+      ws = given.mutable_data_ptr();
+      ws_bytes = given.numel();
     }
     return pair_or_status(
         kv4_attention_gqa8(sq.p, sq.token, sq.head, dt, t, cu, max_new, c.pool, c.scales, c.pages, c.table, c.stride,
                            KV4_PAGE, lens, c.B, hq, c.hkv, c.d, window, static_cast<float>(scale),
                            out.mutable_data_ptr(), lse.mutable_data_ptr<float>(),
-                           ws.defined() ? ws.mutable_data_ptr() : nullptr, ws_bytes, err, stream_of(c.dev)),
+                           ws, ws_bytes, err, stream_of(c.dev)),
         out, lse);
   });
 }
