@@ -6,7 +6,7 @@
 // A decode step's write or a short attention takes 3 to 12 us on the GPU; the
 // same checks and the call written in Python over ctypes took 11 to 17 us of a
 // GB300's host core, so such calls waited for their binding.  Written here they
-// take 2 to 5.
+// take 2 to 6.
 //
 // Bad arguments raise TypeError or ValueError before anything is launched.  A
 // nonzero kv4_status is returned as an int, which the Python wrapper
