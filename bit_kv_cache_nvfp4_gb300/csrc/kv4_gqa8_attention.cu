@@ -134,7 +134,11 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
   grid_dependency_wait();
   grid_launch_dependents();
   __syncthreads();
-  const Gqa8Kind kind{1, max_rows, RP, C::kCost, RP, C::kCost, 1};
+  // (a block for each item where they suffice and none is ever cut: all items
+  // weigh the same; 16 requests of 500 tokens over 8 heads 9.3 us, 10.9 with 304
+  // blocks and items by weight, of 1 to 500 tokens 9.7 and 11.0)
+  const bool one_each = (a.pt_stride + 1) / 2 <= kWhole && static_cast<int64_t>(a.B) * a.Hkv <= gridDim.x;
+  const Gqa8Kind kind = one_each ? Gqa8Kind{1, max_rows, RP, 1, 0, 0, 0} : Gqa8Kind{1, max_rows, RP, C::kCost, RP, C::kCost, 1};
   gqa8_total(a, kind, blockIdx.x == 0, &sm.total);
   fence_async_smem();
   tc_fence_before_sync();
@@ -1527,7 +1531,9 @@ cudaError_t launch_few(const Gqa8AttnArgs& a, const CUtensorMap& map, int max_ro
   using C = FewCfg<D, RP, NT>;
   cudaError_t e = prepare_kernel<few_kernel<D, RP, NT>>(C::kSmem, 0);
   if (e != cudaSuccess) return e;
-  const int blocks = a.num_sms * C::kCtas;
+  // (no more blocks than there can be tiles, or items where none is ever cut)
+  const int64_t tiles = (a.pt_stride + 1) / 2, most = a.B * static_cast<int64_t>(a.Hkv) * (tiles <= kWhole ? 1 : tiles);
+  const int blocks = static_cast<int>(std::min<int64_t>(a.num_sms * C::kCtas, most));
   const Parts p = parts_at(ws, blocks, RP, D);
   e = launch_pdl(few_kernel<D, RP, NT>, blocks, C::kThreads, C::kSmem, stream, 1, map, a, max_rows, p.tails, p.lse, p.o);
   return e != cudaSuccess ? e : launch_merge(merge_few_kernel<D>, a, blocks, RP, RP, p, stream);

@@ -306,6 +306,21 @@ def test_attention_mixed_batch():
     check_attention(c, news, 8, BF16)
 
 
+@pytest.mark.parametrize("B", [1, 7, 150, 160, 400])
+@pytest.mark.parametrize("news", [(1,), (1, 0, 2, 1), (1, 40, 0, 1, 9, 200)])
+@pytest.mark.parametrize("d,dtype,g", [(128, BF16, 4), (64, F16, 12)])
+def test_attention_short_tables(B, news, d, dtype, g):
+    """Tables of 8 pages at most, whose items are never cut: a block for each
+    item, or several."""
+    lens = [(i * 89) % 449 for i in range(B)]
+    news = [min(news[i % len(news)], n) for i, n in enumerate(lens)]
+    if sum(news) == 0:
+        lens[0] = news[0] = 1
+    c = ref.Cache(lens, 2, d, dev(), seed=B)
+    assert c.page_table.shape[1] <= 8
+    assert check_attention(c, news, 2 * g, dtype, seed=B)[0] == 0
+
+
 def test_attention_flags_a_request_beyond_max_new():
     device = dev()
     c = ref.Cache([100, 50, 80], 1, 64, device, seed=16)
