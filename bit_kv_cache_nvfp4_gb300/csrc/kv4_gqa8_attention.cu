@@ -30,13 +30,18 @@ namespace {
 //   S^T[128 keys x NT RP] = K . [q_0 | q_1 | ..]^T      (M = 128, N = NT RP)
 //   O^T[D x NT RP] = V^T . [p_0 | p_1 | ..]^T            (M = D, K = 128 keys)
 // s = S_0 + S_1 / 16 + ..., likewise o.  Both accumulate in fp32.  Two terms
-// hold a bf16 q exactly and p to 2^-8 (half a bf16 step); f16 calls take three
-// (q exactly, p to 2^-12).  Block exponents are powers of two: K's is a factor
-// of the score, V's is folded into p (relative to the larger of the tile's two
-// pages), both exact.  p is relative to the maximum of its own tile, so that
-// the codes' 2^-9 granularity (2^-22 of the tile's largest weight with two
-// terms) never meets a maximum from far away; each tile's O is a product of
-// its own, joined to the running output in registers.
+// hold p to 2^-8 (half a bf16 step); f16 calls take three (p to 2^-12).  Block
+// exponents are powers of two: K's is a factor of the score, V's is added to it
+// in the exponent of p,
+//   p_j = 2^(s_j + eV_j - m + 8),   m = max_j (s_j + eV_j) of the row's keys in
+// the tile (s in units of log 2), so that what a weight is rounded by is relative
+// to what its key can add to the row, however far apart the exponents of the
+// tile's pages are, and a page that the row does not see has no part in it.  The
+// terms' 2^-10 granularity is 2^-22 of the tile's largest 2^(s + eV) (two terms;
+// 2^-26 three), and never meets a maximum from far away; each tile's O is a
+// product of its own, joined to the running output in registers.  The softmax's
+// sum takes p 2^-eV, in fp32: eV is in [-48, 48], so the key of the largest score
+// is at least 2^-88 there, and neither it nor a sum can leave the range.
 //
 // Block: warp 0 finds the block's share of the work list and issues the loads,
 // warp 1 the products, warps 2-3 bring q of the next item to E4M3, and one or
@@ -413,13 +418,12 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
         const uint32_t j = n_tiles + (t - it.t_begin);
         const int st = j % ST;
         wait(sm.full[st], (j / ST) & 1);                  // the exponents, and V where it is cleaned
-        const int ex = sm.exps[st][key >> 6], ex2 = sm.exps[st][(key >> 6) ^ 1];
+        const int ex = sm.exps[st][key >> 6];
         const int at = t * kTileKeys + key;               // this thread's key
         const bool live = ex != kMasked && at >= it.klo && at < it.khi;
         const int ek = static_cast<int16_t>(ex & 0xFFFF), ev = ex == kMasked ? kGqa8ExpMin : ex >> 16;
-        const int evm = max(ev, ex2 == kMasked ? kGqa8ExpMin : ex2 >> 16);
         const float kf = live ? pow2f(ek) : 0.0f;
-        const float vf = pow2f(ev - evm + 8);
+        const float evf = static_cast<float>(ev), vinv = pow2f(-ev);
         const bool edge = (t + 1) * static_cast<int64_t>(kTileKeys) > min(it.khi, pos_first + 1) ||
                           t * kTileKeys < it.klo ||
                           (a.window > 0 && t * static_cast<int64_t>(kTileKeys) <= static_cast<int64_t>(pos_last) - a.window);
@@ -446,7 +450,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
             float x = __uint_as_float(v[NT - 1][i]);
 #pragma unroll
             for (int k = NT - 2; k >= 0; --k) x = fmaf(x, 0.0625f, __uint_as_float(v[k][i]));
-            sc[c + i] = x * kf * sm.qf[qb][c + i];
+            sc[c + i] = fmaf(x * kf, sm.qf[qb][c + i], evf);
           }
         }
         if (edge || !live) {
@@ -486,12 +490,13 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
             // one is 1
             const bool up = mt[r + i] > mref[r + i];
             const float x = fast_exp2(up ? mref[r + i] - mt[r + i] : mt[r + i] - mref[r + i]);
-            p[i] = fast_exp2(sc[r + i] - mt[r + i]);
-            l[r + i] = up ? fmaf(l[r + i], x, p[i]) : fmaf(p[i], x, l[r + i]);
+            p[i] = fast_exp2(sc[r + i] - (mt[r + i] - 8.0f));
+            const float w = p[i] * vinv;
+            l[r + i] = up ? fmaf(l[r + i], x, w) : fmaf(w, x, l[r + i]);
             mref[r + i] = up ? mt[r + i] : mref[r + i];
           }
           uint32_t tt[NT];
-          split_e4m3<NT>(h2_bits(__floats2half2_rn(p[0] * vf, p[1] * vf)), tt);
+          split_e4m3<NT>(h2_bits(__floats2half2_rn(p[0], p[1])), tt);
 #pragma unroll
           for (int k = 0; k < NT; ++k) {
             const int byte = k * RP + r;                  // of the key's row
@@ -511,7 +516,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
           // row `key`'s factors of the running output and of this tile's
           const bool up = mt_mine > mref_mine;
           const float x = fast_exp2(up ? mref_mine - mt_mine : mt_mine - mref_mine);
-          sm.stash[2 * wg + (n_own & 1)][key] = make_float2(up ? x : 1.0f, (up ? 1.0f : x) * pow2f(evm - 8));
+          sm.stash[2 * wg + (n_own & 1)][key] = make_float2(up ? x : 1.0f, up ? 1.0f : x);
           mref_mine = up ? mt_mine : mref_mine;
         }
         fence_async_smem();
@@ -569,7 +574,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
           lt = lt * fast_exp2(mref[r] - ref) + sum_of(1) * fast_exp2(sm.top[1][r] - ref);
         }
         const float y = lt == 0.0f ? 0.0f : __fdividef(o[r], lt);
-        const float ls = lt == 0.0f ? -INFINITY : ref + fast_log2(lt);
+        const float ls = lt == 0.0f ? -INFINITY : ref - 8.0f + fast_log2(lt);
         if (it.slot >= 0) {
           const int64_t row = static_cast<int64_t>(it.slot) * RP + r;
           if (mine_d) ws_o[row * D + d] = y;
