@@ -100,10 +100,12 @@ __device__ __forceinline__ uint32_t widen16(const uint4 (&w)[2], float (&x)[16])
   }
   return m;
 }
-// Least e with amax <= 448 * 2^e, kept where 2^-e and 2^e are normal fp32.
+// Least e with amax <= 448 * 2^e of a row of q: 120 for the largest bf16.  From
+// below it is kept at -118, so that 2^-e and 2^e are normal fp32: a row whose
+// largest is under 2^-109 keeps less of itself than other rows do.
 __device__ __forceinline__ int q_exponent(uint32_t amax_bits) {
   const int e = static_cast<int>(amax_bits >> 23) - 135 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return min(max(e, -118), 118);
+  return min(max(e, -118), 120);
 }
 // 16 values times f (0 where `zero`) as NT terms of 16 bytes.
 template <int NT, bool kSame>

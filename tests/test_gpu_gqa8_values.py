@@ -109,3 +109,21 @@ def test_one_page_of_large_values_in_a_long_context(octaves, dtype):
     c.scales[c.table[1][1], :, 1] = 127 + 40 - octaves
     check(c, [1, 1], 16, dtype)
     check(c, [30, 30], 8, dtype)
+
+
+# ---------------------------------------------------------------------------
+# q at the ends of its type
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("news", [[1, 1], [3, 40]])
+@pytest.mark.parametrize("top", [2.0 ** 126, 2.0 ** 127, 3.3e38])
+def test_queries_near_the_largest_bf16(news, top):
+    """With an sm_scale that brings the scores back: the row's exponent has to
+    reach 120 (2^128 / 448)."""
+    device = dev()
+    c = ref.Cache([100, 300], 1, 128, device, seed=3)
+    g = torch.Generator(device=device).manual_seed(5)
+    q = (torch.rand(sum(news), 4, 128, device=device, generator=g) * 2 - 1)
+    q[:, :, 7] = 1.0                                             # every row's largest is `top`
+    q = (q * top).to(BF16)
+    assert q.isfinite().all()
+    check(c, news, 4, BF16, q=q, sm_scale=2.0 ** -126)
