@@ -330,12 +330,13 @@ __global__ void __launch_bounds__(128) append_rows_kernel(Gqa8Args a) {
 }
 
 // Two floats -> 16-bit pair (first in the low half), round half to even; f16
-// saturates at 65504.
+// saturates at 65504 (what rounds to an infinity becomes that), and a NaN stays
+// one.
 template <bool F16>
 __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
   if constexpr (F16) {
-    const __half2 h = __floats2half2_rn(fminf(fmaxf(lo, -65504.0f), 65504.0f),
-                                        fminf(fmaxf(hi, -65504.0f), 65504.0f));
+    const __half2 top = __float2half2_rn(65504.0f);
+    const __half2 h = __hmax2_nan(__hmin2_nan(__floats2half2_rn(lo, hi), top), __hneg2(top));
     return *reinterpret_cast<const uint32_t*>(&h);
   } else {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -365,12 +366,16 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Gqa8Args a) {
     const int64_t row_of_0 = it.row0 + (it.page << 6) - it.start;
     uint4 c[2][PASSES];
     float f[2] = {0.0f, 0.0f};
+    bool twice[2] = {false, false};
     if (pg >= 0) {
       const uint8_t* blk = a.pool + (pg * a.Hkv + h) * 2 * (kPage * D) + col;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const int e = static_cast<int>(__ldg(a.scales + (pg * a.Hkv + h) * 2 + s)) - 127;
-        f[s] = pow2f(e < -126 ? -126 : (e > 127 ? 127 : e));
+        // 2^(byte - 127): fp32's exponent field as it is, but for 2^-127, which is
+        // subnormal, and 2^128, which goes in as 2^127 and a factor of two
+        const uint32_t byte = __ldg(a.scales + (pg * a.Hkv + h) * 2 + s);
+        f[s] = byte == 0 ? 0x1p-127f : __uint_as_float(min(byte, 254u) << 23);
+        twice[s] = byte == 255;
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
           const int r = r0 + p * RPP;
@@ -389,6 +394,10 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Gqa8Args a) {
         if (pg >= 0) {
           float v[16];
           decode16(c[s][p], v);
+          if (twice[s]) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] *= 2.0f;
+          }
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float* u = v + 8 * j;

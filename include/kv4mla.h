@@ -529,7 +529,9 @@ size_t kv4_noalloc_scratch_bytes(void);
  *   stands in one place of one request's table.
  * kv4_read_gqa8 -- the values of positions starts[b] .. starts[b] + n - 1 of
  *   each request (n = cu[b+1] - cu[b]), 16-bit [n_tokens, Hkv, D] each for K
- *   and V, 16-byte aligned: code * 2^e, rounded once; f16 saturates at 65504.
+ *   and V, 16-byte aligned: code * 2^(byte - 127) of any byte, 0 and 255 too,
+ *   rounded once (bf16 beyond its range: an infinity); f16 saturates at 65504;
+ *   a NaN code (0x7F, 0xFF) gives a NaN.
  * kv4_attention_gqa8 -- causal attention of the new tokens over the cache
  *   (which already holds them): row i of request b sees keys j <= its
  *   position, and with window > 0 only j > position - window.

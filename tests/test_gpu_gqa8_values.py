@@ -127,3 +127,28 @@ def test_queries_near_the_largest_bf16(news, top):
     q = (q * top).to(BF16)
     assert q.isfinite().all()
     check(c, news, 4, BF16, q=q, sm_scale=2.0 ** -126)
+
+
+# ---------------------------------------------------------------------------
+# every code at every kind of exponent byte, read back
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_read_of_every_code_and_exponent_byte(d, dtype):
+    """code * 2^(byte - 127) rounded once for all 256 bytes; a NaN code is a NaN
+    in both types, and f16 saturates at 65504."""
+    device = dev()
+    pages = 256
+    pool = torch.arange(256, dtype=torch.int32).repeat(64 * d // 256).view(64, d).to(torch.uint8).to(device)
+    pool = pool[None, None, None].expand(pages, 1, 2, 64, d).contiguous()
+    scales = torch.arange(256, device=device).to(torch.uint8)[:, None, None].expand(pages, 1, 2).contiguous()
+    table = torch.arange(pages, dtype=torch.int32, device=device)[None].contiguous()
+    n = pages * 64
+    got = kv.read_gqa8(pool, scales, table, ints([0], device), ints([0, n], device), n, dtype=dtype)
+    want = ref.values(pool, scales, table[0].tolist(), 0, n)[0]           # [2, n, D]
+    if dtype == F16:
+        want = want.clamp(-65504, 65504)
+    for s in range(2):
+        x, y = got[s][:, 0], want[s].to(dtype)
+        assert torch.equal(x.isnan(), y.isnan())
+        assert torch.equal(x.nan_to_num(nan=0.0), y.nan_to_num(nan=0.0))
