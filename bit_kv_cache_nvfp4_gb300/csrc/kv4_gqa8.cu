@@ -51,10 +51,10 @@ __device__ __forceinline__ bool find_page(const Gqa8Args& a, int w, PageItem& it
     const bool in = lane * step < n;
     int c0 = 0, c1 = 0, at = 0;
     if (in) {
-      c0 = __ldg(a.cu + b);
+      c0 = load(a.cu + b);
       if (step == 1) {
-        c1 = __ldg(a.cu + b + 1);
-        at = __ldg((a.starts != nullptr ? a.starts : a.lens) + b);
+        c1 = load(a.cu + b + 1);
+        at = load((a.starts != nullptr ? a.starts : a.lens) + b);
       }
     }
     c0 = clamp_cu(c0, a.n_tokens);
@@ -86,10 +86,13 @@ __device__ __forceinline__ bool find_page(const Gqa8Args& a, int w, PageItem& it
   }
 }
 
-// Physical page, or -1 (flagged) where the table has none.
-__device__ __forceinline__ int64_t physical_page(const Gqa8Args& a, const PageItem& it) {
-  int64_t pg = -1;
-  if (it.page < a.pt_stride) pg = __ldg(a.page_table + it.b * a.pt_stride + it.page);
+// The table's entry, -1 where it has none; and the physical page of an entry, or
+// -1 (flagged) where there is none.  (Apart, so that what does not depend on the
+// page can be loaded before the entry is looked at: one round of latency less.)
+__device__ __forceinline__ int table_entry(const Gqa8Args& a, const PageItem& it) {
+  return it.page < a.pt_stride ? load(a.page_table + it.b * a.pt_stride + it.page) : -1;
+}
+__device__ __forceinline__ int64_t physical_page(const Gqa8Args& a, int64_t pg) {
   if (pg < 0 || pg >= a.num_pages) {
     if ((threadIdx.x & 31) == 0) flag_error(a.dev_err, kDevBadPage);
     return -1;
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(Gqa8Args a) {
   __shared__ uint32_t red[kAppendThreads / 32];
   PageItem it;
   if (!find_page(a, blockIdx.x, it)) return;
-  const int64_t pg = physical_page(a, it);
+  const int entry = table_entry(a, it);
   const int h = blockIdx.y >> 1, s = blockIdx.y & 1, tid = threadIdx.x;
   const int lo = it.start > (it.page << 6) ? static_cast<int>(it.start & 63) : 0;
   const int hi = it.end - (it.page << 6) < kPage ? static_cast<int>(it.end - (it.page << 6)) : kPage;
@@ -199,10 +202,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(Gqa8Args a) {
     x[p][0] = x[p][1] = make_uint4(0, 0, 0, 0);
     if (r >= lo && r < hi) {
       const uint4* g = reinterpret_cast<const uint4*>(src + (row_of_0 + r) * ts);
-      x[p][0] = __ldg(g);
-      x[p][1] = __ldg(g + 1);
+      x[p][0] = load(g);
+      x[p][1] = load(g + 1);
     }
   }
+  const int64_t pg = physical_page(a, entry);
   if (pg < 0) return;
   uint8_t* const scale = a.scales + (pg * a.Hkv + h) * 2 + s;
   uint32_t m2 = 0;
@@ -275,7 +279,7 @@ __global__ void __launch_bounds__(128) append_rows_kernel(Gqa8Args a) {
   grid_launch_dependents();
   PageItem it;
   if (!find_page(a, blockIdx.x, it)) return;
-  const int64_t pg = physical_page(a, it);
+  const int entry = table_entry(a, it);
   const int lane = threadIdx.x & 31, unit = blockIdx.y * 4 + (threadIdx.x >> 5), h = unit >> 1, s = unit & 1;
   if (h >= a.Hkv) return;
   const int lo = it.start > (it.page << 6) ? static_cast<int>(it.start & 63) : 0;
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(128) append_rows_kernel(Gqa8Args a) {
   bool odd = false;
   auto row_in = [&](int r, float (&v)[16]) {
     const uint4* g = reinterpret_cast<const uint4*>(src + (row_of_0 + r) * ts);
-    const uint4 x0 = __ldg(g), x1 = __ldg(g + 1);
+    const uint4 x0 = load(g), x1 = load(g + 1);
     widen8<F16>(x0, v);
     widen8<F16>(x1, v + 8);
   };
@@ -302,6 +306,7 @@ __global__ void __launch_bounds__(128) append_rows_kernel(Gqa8Args a) {
       if (u >= 0x7F800000u) odd = true; else m = max(m, u);
     }
   }
+  const int64_t pg = physical_page(a, entry);
   if (pg < 0) return;
   if (odd) flag_error(a.dev_err, kDevNonFinite);
   m = __reduce_max_sync(0xFFFFFFFFu, m);
@@ -347,10 +352,11 @@ __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
 // A block reads a.each neighbouring pages of its head: one where there are
 // fewer blocks than the SMs hold, kReadEach where there are several times as
 // many (12 prefixes, 431 MB: 74.5 us with 1, 70.8 with 2; 3 prefixes, 0.9 MB:
-// 3.1 and 4.1).
+// 3.1 and 4.1).  Five blocks an SM (48 registers a thread): with the four that
+// 64 registers leave, the 128 single pages of a decode step take 0.7 us more.
 constexpr int kReadEach = 2;
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads) read_kernel(Gqa8Args a) {
+__global__ void __launch_bounds__(kThreads, 5) read_kernel(Gqa8Args a) {
   constexpr int TPR = D / 16, RPP = kThreads / TPR, PASSES = kPage / RPP;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -360,7 +366,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Gqa8Args a) {
   for (int w = a.each * static_cast<int>(blockIdx.x); w < a.each * (static_cast<int>(blockIdx.x) + 1); ++w) {
     PageItem it;
     if (!find_page(a, w, it)) continue;
-    const int64_t pg = physical_page(a, it);
+    const int64_t pg = physical_page(a, table_entry(a, it));
     const int lo = it.start > (it.page << 6) ? static_cast<int>(it.start & 63) : 0;
     const int hi = it.end - (it.page << 6) < kPage ? static_cast<int>(it.end - (it.page << 6)) : kPage;
     const int64_t row_of_0 = it.row0 + (it.page << 6) - it.start;
@@ -373,13 +379,13 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Gqa8Args a) {
       for (int s = 0; s < 2; ++s) {
         // 2^(byte - 127): fp32's exponent field as it is, but for 2^-127, which is
         // subnormal, and 2^128, which goes in as 2^127 and a factor of two
-        const uint32_t byte = __ldg(a.scales + (pg * a.Hkv + h) * 2 + s);
+        const uint32_t byte = load(a.scales + (pg * a.Hkv + h) * 2 + s);
         f[s] = byte == 0 ? 0x1p-127f : __uint_as_float(min(byte, 254u) << 23);
         twice[s] = byte == 255;
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
           const int r = r0 + p * RPP;
-          c[s][p] = r >= lo && r < hi ? __ldg(reinterpret_cast<const uint4*>(blk + (s * kPage + r) * D))
+          c[s][p] = r >= lo && r < hi ? load(reinterpret_cast<const uint4*>(blk + (s * kPage + r) * D))
                                       : make_uint4(0, 0, 0, 0);
         }
       }

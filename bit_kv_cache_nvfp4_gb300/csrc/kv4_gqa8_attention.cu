@@ -334,8 +334,8 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
           const uint4* g = reinterpret_cast<const uint4*>(
               static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(it.cu0 + r / G) * a.q_token_stride +
               static_cast<int64_t>(it.h * G + r % G) * a.q_head_stride + part * 16);
-          w[0] = __ldg(g);
-          w[1] = __ldg(g + 1);
+          w[0] = load(g);
+          w[1] = load(g + 1);
         }
         float x[16];
         uint32_t m = widen16<C::kF16>(w, x);
@@ -1054,8 +1054,8 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
             const uint4* g = reinterpret_cast<const uint4*>(
                 static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(it.cu0 + gr / G) * a.q_token_stride +
                 static_cast<int64_t>(it.h * G + gr % G) * a.q_head_stride + part * 16);
-            w[0] = __ldg(g);
-            w[1] = __ldg(g + 1);
+            w[0] = load(g);
+            w[1] = load(g + 1);
           }
         };
         // (a loop of little code, two fetches ahead: it runs once an item, so
@@ -1312,7 +1312,7 @@ __global__ void __launch_bounds__(256) merge_few_kernel(const Gqa8AttnArgs a, co
     // piece i is slot 2c + 1 for i = 0, else 2 (c + i)
     auto row_of = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * rows + r; };
     for (int i = lane; i < t.parts; i += 32) {
-      const float x = __ldg(ws_lse + row_of(i));
+      const float x = load(ws_lse + row_of(i));
       odd |= x != x;
       m = fmaxf(m, x);
     }
@@ -1320,13 +1320,13 @@ __global__ void __launch_bounds__(256) merge_few_kernel(const Gqa8AttnArgs a, co
     odd = __any_sync(0xFFFFFFFFu, odd);
     if (m > -INFINITY) {
       for (int i0 = 0; i0 < t.parts; i0 += 32) {
-        const float w = i0 + lane < t.parts ? fast_exp2(__ldg(ws_lse + row_of(i0 + lane)) - m) : 0.0f;
+        const float w = i0 + lane < t.parts ? fast_exp2(load(ws_lse + row_of(i0 + lane)) - m) : 0.0f;
         s += w;
         const int n = min(32, t.parts - i0);
 #pragma unroll 4
         for (int i = wi; i < n; i += W) {
           const float wt = __shfl_sync(0xFFFFFFFFu, w, i);
-          const Vec v = __ldg(reinterpret_cast<const Vec*>(ws_o + row_of(i0 + i) * D) + lane);
+          const Vec v = load(reinterpret_cast<const Vec*>(ws_o + row_of(i0 + i) * D) + lane);
           const float* f = reinterpret_cast<const float*>(&v);
 #pragma unroll
           for (int k = 0; k < C; ++k) o[k] = fmaf(wt, f[k], o[k]);
@@ -1383,7 +1383,7 @@ __global__ void __launch_bounds__(256) merge_many_kernel(const Gqa8AttnArgs a, c
   float m = -INFINITY;
   bool odd = false;
   for (int i = i8; i < t.parts; i += 8) {
-    const float x = __ldg(ws_lse + row_of(i, mine));
+    const float x = load(ws_lse + row_of(i, mine));
     odd |= x != x;
     m = fmaxf(m, x);
   }
@@ -1399,7 +1399,7 @@ __global__ void __launch_bounds__(256) merge_many_kernel(const Gqa8AttnArgs a, c
     for (int j = 0; j < C; ++j) o[k][j] = 0.0f;
   for (int i0 = 0; i0 < t.parts; i0 += 8) {
     const bool in = i0 + i8 < t.parts && m > -INFINITY;
-    const float w = in ? fast_exp2(__ldg(ws_lse + row_of(i0 + i8, mine)) - m) : 0.0f;
+    const float w = in ? fast_exp2(load(ws_lse + row_of(i0 + i8, mine)) - m) : 0.0f;
     s += w;
     const int n = min(8, t.parts - i0);
 #pragma unroll 2
@@ -1407,7 +1407,7 @@ __global__ void __launch_bounds__(256) merge_many_kernel(const Gqa8AttnArgs a, c
 #pragma unroll
       for (int k = 0; k < R; ++k) {
         const float wk = __shfl_sync(0xFFFFFFFFu, w, k * 8 + i);
-        const Vec v = __ldg(reinterpret_cast<const Vec*>(ws_o + row_of(i0 + i, min(r0 + k, t.nrows - 1)) * D) + lane);
+        const Vec v = load(reinterpret_cast<const Vec*>(ws_o + row_of(i0 + i, min(r0 + k, t.nrows - 1)) * D) + lane);
         const float* f = reinterpret_cast<const float*>(&v);
 #pragma unroll
         for (int j = 0; j < C; ++j) o[k][j] = fmaf(wk, f[j], o[k][j]);

@@ -10,6 +10,16 @@
 
 namespace kv4 {
 
+// Every load of the caller's tensors and of the workspace.  The kernels here may
+// begin before the kernel before them has ended (grid_dependency_wait waits for
+// it), and that one may have written any of them, so none is read-only while
+// they run: a plain load, never the read-only path, which may be served from
+// before the wait.
+template <typename T>
+__device__ __forceinline__ T load(const T* p) {
+  return *p;
+}
+
 __device__ __forceinline__ float pow2f(int e) {     // e in [-126, 127]
   return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
@@ -216,8 +226,8 @@ __device__ __forceinline__ Gqa8Request gqa8_request(const Gqa8AttnArgs& a, int b
   Gqa8Request q{0, 0, 0, 0};
   if (b >= a.B) return q;
   const int T = static_cast<int>(a.n_tokens);
-  const int c0 = min(max(__ldg(a.cu + b), 0), T), c1 = min(max(__ldg(a.cu + b + 1), 0), T);
-  const int len = max(__ldg(a.lens + b), 0);
+  const int c0 = min(max(load(a.cu + b), 0), T), c1 = min(max(load(a.cu + b + 1), 0), T);
+  const int len = max(load(a.lens + b), 0);
   if (c1 <= c0) return q;
   if (c1 - c0 > a.max_new) {
     if (report) flag_error(a.dev_err, kDevBadLength);
@@ -440,12 +450,12 @@ __device__ __forceinline__ void gqa8_pages(const Gqa8AttnArgs& a, const Gqa8Item
   block = static_cast<int>(a.num_pages) * a.Hkv;
   ex = kMasked;
   if ((page >> 1) < it.t_end && (page << 6) < it.khi && (page << 6) + 64 > it.klo) {
-    const int phys = __ldg(a.page_table + it.b * a.pt_stride + page);
+    const int phys = load(a.page_table + it.b * a.pt_stride + page);
     if (phys < 0 || phys >= a.num_pages) {
       flag_error(a.dev_err, kDevBadPage);
     } else {
       block = phys * a.Hkv + it.h;
-      const uint32_t e2 = __ldg(reinterpret_cast<const uint16_t*>(a.scales) + block);
+      const uint32_t e2 = load(reinterpret_cast<const uint16_t*>(a.scales) + block);
       const int ek = min(max(static_cast<int>(e2 & 0xFF) - 127, kGqa8ExpMin), kGqa8ExpMax);
       const int ev = min(max(static_cast<int>(e2 >> 8) - 127, kGqa8ExpMin), kGqa8ExpMax);
       ex = (ek & 0xFFFF) | static_cast<int>(static_cast<uint32_t>(ev) << 16);
