@@ -64,7 +64,7 @@ def load_library():
         if _lib is not None:
             return _lib
         from . import build as _build
-        path = _build.build()
+        path = _build.build_library()
         lib = ctypes.CDLL(path)
         P, i32, i64, f32, sz = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
                                 ctypes.c_float, ctypes.c_size_t)

@@ -6,9 +6,14 @@ Each translation unit under ``csrc/`` is compiled in parallel with
 no fast-math, so the cache write stays bit-exact), then linked into a shared
 library next to this file.  Run ``python -m bit_kv_cache_nvfp4_gb300.build``
 or call :func:`build`.
+
+The library needs nvcc alone (:func:`build_library`; where PyTorch is missing,
+running this file builds just that): the extension is built beside it, stale by
+itself, and one that does not build leaves the library in place.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -41,17 +46,24 @@ def _torch_version() -> str:
     return torch.__version__
 
 
+def _newest(sources) -> float:
+    deps = [os.path.join(CSRC, f) for f in sources]
+    deps.append(os.path.join(INCLUDE, "kv4mla.h"))
+    deps.append(os.path.abspath(__file__))
+    return max(os.path.getmtime(p) for p in deps)
+
+
 def _stale() -> bool:
-    if not (os.path.exists(LIB_PATH) and os.path.exists(TORCH_PATH) and os.path.exists(TORCH_STAMP)):
+    return not os.path.exists(LIB_PATH) or os.path.getmtime(LIB_PATH) < _newest(SOURCES + HEADERS)
+
+
+def _torch_stale() -> bool:
+    if not (os.path.exists(TORCH_PATH) and os.path.exists(TORCH_STAMP)):
         return True
     with open(TORCH_STAMP) as f:
         if f.read() != _torch_version():
             return True
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [TORCH_SOURCE]]
-    deps.append(os.path.join(INCLUDE, "kv4mla.h"))
-    deps.append(os.path.abspath(__file__))
-    built = min(os.path.getmtime(LIB_PATH), os.path.getmtime(TORCH_PATH))
-    return built < max(os.path.getmtime(p) for p in deps)
+    return os.path.getmtime(TORCH_PATH) < _newest([TORCH_SOURCE])
 
 
 def _torch_object():
@@ -72,8 +84,27 @@ def _torch_object():
     return obj, compile_cmd, link
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
-    """Compile and link; returns the library path."""
+def _start(cmd, verbose):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
+def _finish(procs, verbose) -> None:
+    """Wait for (source, process) pairs; raise if one failed."""
+    failed = []
+    for src, p in procs:
+        out, _ = p.communicate()
+        if out and (verbose or p.returncode != 0):
+            sys.stdout.write(out)
+        if p.returncode != 0:
+            failed.append(src)
+    if failed:
+        raise RuntimeError(f"compilation failed for {failed}")
+
+
+def build_library(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
+    """Compile and link libkv4mla.so; returns its path."""
     if not force and not _stale():
         return LIB_PATH
     nvcc = _nvcc()
@@ -85,34 +116,48 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     for src in SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
         objs.append(obj)
-        cmd = [nvcc] + flags + ["-c", os.path.join(CSRC, src), "-o", obj]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE,
-                                            stderr=subprocess.STDOUT, text=True)))
-    torch_obj, torch_cmd, torch_link = _torch_object()
-    if verbose:
-        print(" ".join(torch_cmd), flush=True)
-    procs.append((TORCH_SOURCE, subprocess.Popen(torch_cmd, stdout=subprocess.PIPE,
-                                                 stderr=subprocess.STDOUT, text=True)))
-    failed = []
-    for src, p in procs:
-        out, _ = p.communicate()
-        if out and (verbose or p.returncode != 0):
-            sys.stdout.write(out)
-        if p.returncode != 0:
-            failed.append(src)
-    if failed:
-        raise RuntimeError(f"compilation failed for {failed}")
+        procs.append((src, _start([nvcc] + flags + ["-c", os.path.join(CSRC, src), "-o", obj], verbose)))
+    _finish(procs, verbose)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB_PATH)
+    return LIB_PATH
+
+
+def _link_extension(obj, link) -> None:
     tmp = TORCH_PATH + f".tmp{os.getpid()}"
-    subprocess.run(["g++", "-shared", "-o", tmp, torch_obj] + torch_link, check=True)
+    subprocess.run(["g++", "-shared", "-o", tmp, obj] + link, check=True)
     os.replace(tmp, TORCH_PATH)
     with open(TORCH_STAMP, "w") as f:
         f.write(_torch_version())
+
+
+def build_extension(force: bool = False, verbose: bool = False) -> str:
+    """Compile _kv4torch.so and link it to the library, which is there; returns
+    its path."""
+    if force or _torch_stale():
+        os.makedirs(BUILD_DIR, exist_ok=True)
+        obj, cmd, link = _torch_object()
+        _finish([(TORCH_SOURCE, _start(cmd, verbose))], verbose)
+        _link_extension(obj, link)
+    return TORCH_PATH
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
+    """Both, their sources compiled side by side; returns the library's path."""
+    ext = None
+    if importlib.util.find_spec("torch") is not None and (force or _torch_stale()):
+        os.makedirs(BUILD_DIR, exist_ok=True)
+        obj, cmd, link = _torch_object()
+        ext = [(TORCH_SOURCE, _start(cmd, verbose))]
+    try:
+        build_library(force, verbose, extra_flags)
+    finally:
+        if ext is not None:
+            _finish(ext, verbose)
+    if ext is not None:
+        _link_extension(obj, link)
     return LIB_PATH
 
 

@@ -17,24 +17,27 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import threading
 
 import torch
 
 from . import Kv4Error, _check, load_library
 
 _ext = None
+_ext_lock = threading.Lock()
 
 
 def _extension():
     """The module _kv4torch, built if its sources are newer."""
     global _ext
-    if _ext is None:
-        load_library()
-        from . import build as _build
-        spec = importlib.util.spec_from_file_location("_kv4torch", _build.TORCH_PATH)
-        mod = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(mod)
-        _ext = mod
+    load_library()
+    with _ext_lock:
+        if _ext is None:
+            from . import build as _build
+            spec = importlib.util.spec_from_file_location("_kv4torch", _build.build_extension())
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+            _ext = mod
     return _ext
 
 
