@@ -161,6 +161,14 @@ at::Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, at::Scal
   return t;
 }
 
+// A tensor of the caller's that a call writes into: autograd has to learn that
+// what it may have saved of it is gone.  (Inference tensors count nothing.)
+void written(PyObject* o) {
+  if (o == Py_None) return;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject* pair_or_status(kv4_status st, const at::Tensor& a, const at::Tensor& b) {
   if (st != KV4_OK) return PyLong_FromLong(st);
   PyObject* t = PyTuple_New(2);
@@ -200,9 +208,12 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     ragged(c, a[2], a[4], "seq_lens", cu, lens);
     int32_t* const err = err_word(a[7], c.dev);
     const c10::cuda::CUDAGuard guard(c.dev);
-    return PyLong_FromLong(kv4_append_gqa8(sk.p, sk.token, sk.head, sv.p, sv.token, sv.head, dt, k.size(0), cu,
-                                           c.table, c.stride, KV4_PAGE, lens, c.B, c.hkv, c.d, c.pool, c.scales,
-                                           c.pages, err, stream_of(c.dev)));
+    const kv4_status st =
+        kv4_append_gqa8(sk.p, sk.token, sk.head, sv.p, sv.token, sv.head, dt, k.size(0), cu, c.table, c.stride,
+                        KV4_PAGE, lens, c.B, c.hkv, c.d, c.pool, c.scales, c.pages, err, stream_of(c.dev));
+    if (st == KV4_OK)
+      for (const int i : {5, 6, 7}) written(a[i]);
+    return PyLong_FromLong(st);
   });
 }
 
@@ -219,10 +230,12 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::ScalarType type = f16 ? at::kHalf : at::kBFloat16;
     const at::Tensor k = output(a[7], "k_out", {total, c.hkv, c.d}, type, c.dev);
     const at::Tensor v = output(a[8], "v_out", {total, c.hkv, c.d}, type, c.dev);
-    return pair_or_status(
+    const kv4_status st =
         kv4_read_gqa8(c.pool, c.scales, c.pages, c.table, c.stride, KV4_PAGE, starts, cu, total, c.B, c.hkv, c.d,
-                      f16 ? KV4_F16 : KV4_BF16, k.mutable_data_ptr(), v.mutable_data_ptr(), err, stream_of(c.dev)),
-        k, v);
+                      f16 ? KV4_F16 : KV4_BF16, k.mutable_data_ptr(), v.mutable_data_ptr(), err, stream_of(c.dev));
+    if (st == KV4_OK)
+      for (const int i : {7, 8, 9}) written(a[i]);
+    return pair_or_status(st, k, v);
   });
 }
 
@@ -265,12 +278,14 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ws = given.mutable_data_ptr();
       ws_bytes = given.numel();
     }
-    return pair_or_status(
+    const kv4_status st =
         kv4_attention_gqa8(sq.p, sq.token, sq.head, dt, t, cu, max_new, c.pool, c.scales, c.pages, c.table, c.stride,
                            KV4_PAGE, lens, c.B, hq, c.hkv, c.d, window, static_cast<float>(scale),
-                           out.mutable_data_ptr(), lse.mutable_data_ptr<float>(),
-                           ws, ws_bytes, err, stream_of(c.dev)),
-        out, lse);
+                           out.mutable_data_ptr(), lse.mutable_data_ptr<float>(), ws, ws_bytes, err,
+                           stream_of(c.dev));
+    if (st == KV4_OK)
+      for (const int i : {9, 10, 11, 12}) written(a[i]);
+    return pair_or_status(st, out, lse);
   });
 }
 

@@ -9,7 +9,9 @@ masks).  The cache is two tensors:
 
 and a page table int32 [B, stride] as for the other caches of this package.
 Tensors of one call are on one device, which need not be the current one; work
-goes to that device's current stream.  The argument checks and the calls are in
+goes to that device's current stream.  No gradients are computed: the results of
+inputs that require one carry none, and tensors that a call writes into count it
+as a change in place.  The argument checks and the calls are in
 the extension module ``_kv4torch`` (``csrc/kv4_torch.cpp``): these calls are
 short enough for a binding in Python to be what they take.
 """
