@@ -1066,7 +1066,7 @@ kv4_status kv4_attention_gqa8_plan(int B, int max_new, int64_t n_tokens, int Hq,
   const kv4_status st = device_info(&sms);
   if (st != KV4_OK) return st;
   if (workspace_bytes)
-    *workspace_bytes = kv4::attention_gqa8_workspace(B, max_new, n_tokens, Hq, Hkv, D, sms);
+    *workspace_bytes = kv4::attention_gqa8_workspace(max_new, Hq, Hkv, D, sms);
   return KV4_OK;
 }
 
@@ -1096,7 +1096,7 @@ kv4_status kv4_attention_gqa8(const void* q_dev, int64_t q_token_stride, int64_t
   int sms = 0;
   const kv4_status st = device_info(&sms);
   if (st != KV4_OK) return st;
-  const size_t need = kv4::attention_gqa8_workspace(B, max_new, n_tokens, Hq, Hkv, D, sms);
+  const size_t need = kv4::attention_gqa8_workspace(max_new, Hq, Hkv, D, sms);
   if (need > 0 && (!workspace_dev || workspace_bytes < need || !aligned16(workspace_dev)))
     return KV4_ERR_WORKSPACE;
   kv4::Gqa8AttnArgs a{};

@@ -100,7 +100,7 @@ __device__ __forceinline__ int64_t physical_page(const Gqa8Args& a, int64_t pg) 
   return pg;
 }
 
-// 16 values of 16 bits at p as floats.
+// 8 values of 16 bits as floats.
 template <bool F16>
 __device__ __forceinline__ void widen8(const uint4& v, float* x) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};

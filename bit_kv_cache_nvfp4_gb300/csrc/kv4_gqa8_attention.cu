@@ -1587,7 +1587,7 @@ cudaError_t launch_attention_gqa8(const Gqa8AttnArgs& a, cudaStream_t stream) {
   return a.D == 64 ? launch_d<64>(a, stream) : launch_d<128>(a, stream);
 }
 
-size_t attention_gqa8_workspace(int, int max_new, int64_t, int Hq, int Hkv, int D, int num_sms) {
+size_t attention_gqa8_workspace(int max_new, int Hq, int Hkv, int D, int num_sms) {
   const int rows = few_rows(max_new, Hq / Hkv);
   const bool many = static_cast<int64_t>(max_new) * (Hq / Hkv) > rows;
   return few_bytes(rows, D, num_sms) + (many ? part_bytes(num_sms, kManyRows, D) : 0);

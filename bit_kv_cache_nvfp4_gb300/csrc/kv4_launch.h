@@ -179,8 +179,7 @@ cudaError_t launch_append_gqa8(const Gqa8Args& a, cudaStream_t stream);
 cudaError_t launch_read_gqa8(const Gqa8Args& a, cudaStream_t stream);
 cudaError_t launch_attention_gqa8(const Gqa8AttnArgs& a, cudaStream_t stream);
 // Workspace bytes of launch_attention_gqa8 for these sizes on num_sms SMs.
-size_t attention_gqa8_workspace(int B, int max_new, int64_t n_tokens, int Hq, int Hkv, int D,
-                                int num_sms);
+size_t attention_gqa8_workspace(int max_new, int Hq, int Hkv, int D, int num_sms);
 cudaError_t launch_debug_gather(const GatherArgs& a, cudaStream_t stream);
 // The FP8 scratch copy of the rows the keys select: a.rows is uint8
 // [B*Sq*K, 576] (E4M3 of the dequantized NVFP4 values; masked keys 0).
