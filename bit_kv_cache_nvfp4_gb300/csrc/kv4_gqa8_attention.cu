@@ -25,14 +25,15 @@ namespace {
 // codes go from HBM to the tensor core as they are, with no conversion on the
 // way: K and V tiles land in shared memory by TMA in the swizzle that
 // tcgen05.mma reads, and it is the small operands -- q and the softmax weights
-// p -- that are brought to E4M3, as exact sums of NT terms (split_e4m3), the
-// terms side by side as columns of one product:
+// p -- that are brought to E4M3, as sums of NT terms (split_e4m3), the terms side
+// by side as columns of one product:
 //   S^T[128 keys x NT RP] = K . [q_0 | q_1 | ..]^T      (M = 128, N = NT RP)
 //   O^T[D x NT RP] = V^T . [p_0 | p_1 | ..]^T            (M = D, K = 128 keys)
 // s = S_0 + S_1 / 16 + ..., likewise o.  Both accumulate in fp32.  Two terms
-// hold p to 2^-8 (half a bf16 step); f16 calls take three (p to 2^-12).  Block
-// exponents are powers of two: K's is a factor of the score, V's is added to it
-// in the exponent of p,
+// hold p to 2^-8 (half a bf16 step), three, in f16 calls, to f16's 2^-11; and q
+// exactly, but for elements below 2^-14 of their row's largest, which keep 2^-22
+// of that (f16: 2^-26).  Block exponents are powers of two: K's is a factor of
+// the score, V's is added to it in the exponent of p,
 //   p_j = 2^(s_j + eV_j - m + 8),   m = max_j (s_j + eV_j) of the row's keys in
 // the tile (s in units of log 2), so that what a weight is rounded by is relative
 // to what its key can add to the row, however far apart the exponents of the
@@ -51,8 +52,9 @@ namespace {
 // a running output of its own, joined at the item's end.
 //
 // Measured (D = 128, bf16): 64 sessions of up to 32768 tokens, 8 heads a group,
-// 2.29 GB of codes: 340 us, 6.7 TB/s, the rate of a copy; 16 heads a group 357
-// us; 2 x 204800 tokens cut over 304 blocks 133 us with the joining kernel.
+// 2.29 GB of codes: 340 us, 6.7 TB/s, the rate of a copy; 16 heads a group
+// (2.08 GB) 355 us; 2 x 204800 tokens cut over 304 blocks 133 us with the joining
+// kernel.  In f16, with three terms, 394 us for 2.16 GB, 5.5 TB/s.
 template <int D_, int RP_, int NT_>
 struct FewCfg {
   static constexpr int D = D_, RP = RP_, NT = NT_;
@@ -140,8 +142,10 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
   grid_launch_dependents();
   __syncthreads();
   // (a block for each item where they suffice and none is ever cut: all items
-  // weigh the same; 16 requests of 500 tokens over 8 heads 9.3 us, 10.9 with 304
-  // blocks and items by weight, of 1 to 500 tokens 9.7 and 11.0)
+  // weigh the same; in replays of a graph 16 requests of 500 tokens over 8 heads
+  // 9.3 us, 10.9 with 304 blocks and items by weight, of 1 to 500 tokens 9.7 and
+  // 11.0.  The lengths are on the device, so that it is the page table's width, up
+  // to 8 columns, that says none is cut.)
   const bool one_each = (a.pt_stride + 1) / 2 <= kWhole && static_cast<int64_t>(a.B) * a.Hkv <= gridDim.x;
   const Gqa8Kind kind = one_each ? Gqa8Kind{1, max_rows, RP, 1, 0, 0, 0} : Gqa8Kind{1, max_rows, RP, C::kCost, RP, C::kCost, 1};
   gqa8_total(a, kind, blockIdx.x == 0, &sm.total);
@@ -610,7 +614,8 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
 //   S[128 rows x 128 keys] = sum_t Q_t . K^T     kind::f8f6f4, NT terms of q
 //   O[128 rows x D] += P . V                     kind::f16, P from TMEM
 // K goes in as its codes, against q split into E4M3 terms (bf16: two, f16:
-// three; all with the same scale, so that they add up in one accumulator).  V
+// three; all with the same scale, so that they add up in one accumulator, which
+// keeps 2^-18 of a row's largest: split_e4m3_same).  V
 // is widened to f16 once per tile by two warps (exact), for P in f16 (2^-11)
 // takes one pass where E4M3 terms would take two and twice the instructions
 // in the softmax, which has the least room to spare.
@@ -623,9 +628,12 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
 // only rescaled, when that rises by more than 2^6 (p stays below 2^14, f16's
 // top is 2^16).
 //
-// Measured (D = 128, 32 heads over 8, bf16): 2 x 2048 new tokens over 16384 613
-// us, 1.32 PFLOP/s (70 % of the measured bf16 rate; without the softmax the
-// products alone took 500); a prompt of 8192 472 us, 1.17.
+// Measured (D = 128, 32 heads over 8, bf16): 2 x 2048 new tokens over 16384 625
+// us, 1.30 PFLOP/s (69 % of the measured bf16 rate; without the softmax the
+// products alone took 500); a prompt of 8192 474 us, 1.16.  f16, three terms:
+// 808 us for a chunk with 1.27 times the pairs, 1.27 PFLOP/s, and 506 us.  D = 64:
+// 578 and 394 us in bf16, 0.80 and 0.70 PFLOP/s: a tile has the same softmax for
+// half the products.
 template <int D_, int NT_>
 struct ManyCfg {
   static constexpr int D = D_, NT = NT_, kRows = 256;
@@ -1287,8 +1295,11 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
 // The pieces of items that were cut: block (c, y) joins rows of the item that
 // began in block c of the attention kernel, by log-sum-exp over its pieces in
 // their order: one kernel for items of few rows, where a long context has many
-// pieces and 8 warps share a row, one for items of 256 rows in two or three
-// pieces, where a warp takes 4 rows at once.
+// pieces and 8 warps share a row, one for items of up to 256 rows, where a warp
+// takes 4 rows at once and their pieces in turn.  Those of a prompt or a chunk are
+// two or three; but a single short one of few heads over a long context is cut
+// over all blocks (40 rows of one head over 200000 tokens: 97 us, where one row,
+// in the kernels of few rows, takes 28).
 // ---------------------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(256) merge_few_kernel(const Gqa8AttnArgs a, const int rows,

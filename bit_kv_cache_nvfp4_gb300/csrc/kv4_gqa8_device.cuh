@@ -79,8 +79,9 @@ __device__ __forceinline__ void split_e4m3(uint32_t x, uint32_t (&t)[NT]) {
 }
 
 // The same without the factors: x = t0 + t1 + .., so that the terms' products
-// add up in one accumulator; with |x|'s largest near 448, elements below 2^-10
-// of it keep 2^-18 of it.
+// add up in one accumulator; with |x|'s largest near 448, elements below 2^-10 of
+// it (two terms, the 8 bits of a bf16 value) or 2^-7 (three, the 11 of an f16)
+// keep 2^-18 of it.
 template <int NT>
 __device__ __forceinline__ void split_e4m3_same(uint32_t x, uint32_t (&t)[NT]) {
   t[0] = e4m3x2_of_f16x2(x);

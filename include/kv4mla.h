@@ -544,6 +544,13 @@ size_t kv4_noalloc_scratch_bytes(void);
  *   workspace_dev   at least the bytes kv4_attention_gqa8_plan returns for the
  *                   same sizes, 16-byte aligned, of this call alone while it
  *                   runs; nothing in it needs a value
+ *   Precision: scores, the softmax's maximum and sum and the output are held in
+ *   fp32, and the output is rounded once.  Two operands enter their products in
+ *   fewer bits, off by no more than: a key's weight w by 2^-8 (bf16) or 2^-11
+ *   (f16) of itself or, where w 2^e (e the exponent of its V) is below 2^-14 of
+ *   the largest among its 128 keys, 2^-22 of that largest; an element of q by
+ *   2^-18 of its row's largest, and by nothing from 2^-10 (f16: 2^-7) of that on
+ *   (rows whose largest is below 2^-109: by 2^-128).
  *   Scale exponents outside [-48, 48], which the append never writes, count as
  *   the nearer end (the read-back takes them as they are).
  *   Equal calls give equal bits; a row's last bits may differ with what else
