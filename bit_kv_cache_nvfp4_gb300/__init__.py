@@ -30,6 +30,8 @@ __all__ = [
     "dcp_local_slots", "dcp_local_pages", "dcp_compact_topk", "ROW_BYTES", "ROW_BYTES_LATENT", "LATENT", "ROPE", "QK_DIM", "PAGE", "DEV_BAD_SLOT", "DEV_BAD_PAGE",
     "DEV_TIMEOUT", "DEV_NONFINITE", "DEV_BAD_LENGTH", "HostPipe",
     "append_gqa8", "read_gqa8", "attention_gqa8", "attention_gqa8_workspace",
+    "append_gqa4", "read_gqa4", "attention_gqa4", "attention_gqa4_workspace",
+    "rotary", "rotary_frequencies",
 ]
 
 ROW_BYTES, LATENT, ROPE, QK_DIM, PAGE, TILE_KEYS = 352, 512, 64, 576, 64, 128
@@ -139,6 +141,12 @@ def load_library():
         lib.kv4_attention_gqa8.argtypes = [P, i64, i64, i32, i64, P, i32, P, P, i64, P, i64, i32,
                                            P, i32, i32, i32, i32, i32, f32, P, P, P, sz, P, P]
         lib.kv4_attention_gqa8.restype = i32
+        for name in ("append_gqa%d", "read_gqa%d", "attention_gqa%d_plan", "attention_gqa%d"):
+            f4, f8 = getattr(lib, "kv4_" + name % 4), getattr(lib, "kv4_" + name % 8)
+            f4.argtypes, f4.restype = f8.argtypes, i32
+        lib.kv4_rotary.argtypes = ([P, i64, i64, i32, i32, i32, P, i64, i64] * 2 +
+                                   [i32, i64, P, i32, P, i32, i32, f32, P])
+        lib.kv4_rotary.restype = i32
         lib.kv4_set_wait_limit.argtypes = [i64, i32]
         lib.kv4_set_wait_limit.restype = i32
         lib.kv4_set_timing_event.argtypes = [P]
@@ -718,3 +726,6 @@ def set_wait_limit(timeout_ns: int = 0, fault_site: int = 0) -> None:
 
 from .gqa8 import (append_gqa8, attention_gqa8, attention_gqa8_workspace,  # noqa: E402
                    read_gqa8)
+from .gqa4 import (append_gqa4, attention_gqa4, attention_gqa4_workspace,  # noqa: E402
+                   read_gqa4)
+from .rotary import rotary, rotary_frequencies  # noqa: E402

@@ -29,8 +29,8 @@ TORCH_PATH = os.path.join(HERE, "_kv4torch.so")
 TORCH_STAMP = os.path.join(BUILD_DIR, "torch_version")   # what _kv4torch.so was built with
 TORCH_SOURCE = "kv4_torch.cpp"
 SOURCES = ["kv4_capi.cu", "kv4_quantize_write.cu", "kv4_sparse_mla_decode.cu", "kv4_dcp.cu",
-           "kv4_gqa8.cu", "kv4_gqa8_attention.cu"]
-HEADERS = ["kv4_device.cuh", "kv4_gqa8_device.cuh", "kv4_launch.h"]
+           "kv4_gqa8.cu", "kv4_gqa8_attention.cu", "kv4_gqa4.cu", "kv4_gqa4_attention.cu", "kv4_rotary.cu"]
+HEADERS = ["kv4_device.cuh", "kv4_gqa8_device.cuh", "kv4_gqa_pages.cuh", "kv4_gqa_merge.cuh", "kv4_launch.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -934,17 +934,29 @@ size_t kv4_noalloc_scratch_bytes(void) { return kStaticScratchBytes; }
 }  // extern "C"
 
 // ---------------------------------------------------------------------------
-// The 8-bit grouped-query cache.
+// The grouped-query caches: the same calls over 8-bit and over 4-bit pages.
 // ---------------------------------------------------------------------------
 namespace {
 
-bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-bool aligned128(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 127u) == 0; }
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// Sizes that the three entry points share.  Beyond n_tokens * heads * D the
+struct GqaFormat {
+  uintptr_t pool_align, scales_align, attention_scales_align;
+  cudaError_t (*append)(const kv4::Gqa8Args&, cudaStream_t);
+  cudaError_t (*read)(const kv4::Gqa8Args&, cudaStream_t);
+  cudaError_t (*attention)(const kv4::Gqa8AttnArgs&, cudaStream_t);
+  size_t (*workspace)(int max_new, int Hq, int Hkv, int D, int num_sms);
+};
+constexpr GqaFormat kGqa8 = {128, 1, 2, kv4::launch_append_gqa8, kv4::launch_read_gqa8, kv4::launch_attention_gqa8,
+                             kv4::attention_gqa8_workspace};
+// (whole rows of codes and scales move by bulk copies and in vectors)
+constexpr GqaFormat kGqa4 = {16, 16, 16, kv4::launch_append_gqa4, kv4::launch_read_gqa4, kv4::launch_attention_gqa4,
+                             kv4::attention_gqa4_workspace};
+
+// Sizes that the entry points share.  Beyond n_tokens * heads * D the
 // grids need one block index per page of the call, n_tokens / 64 + 2 B.
-kv4_status check_gqa8(int64_t n_tokens, int heads, int Hkv, int D, int B, int dtype,
+kv4_status check_gqa(int64_t n_tokens, int heads, int Hkv, int D, int B, int dtype,
                       int page_size, int64_t num_pages, int64_t pt_stride) {
   if (n_tokens < 0 || B < 0 || B > 65535 || Hkv < 1 || heads < 1) return KV4_ERR_INVALID_ARG;
   if (page_size != KV4_PAGE || (D != 64 && D != 128) || (dtype != KV4_BF16 && dtype != KV4_F16) ||
@@ -962,18 +974,14 @@ bool strides_ok(const void* p, int64_t token, int64_t head, int heads, int D) {
          (heads == 1 || head >= D);
 }
 
-}  // namespace
-
-extern "C" {
-
-kv4_status kv4_append_gqa8(const void* k_dev, int64_t k_token_stride, int64_t k_head_stride,
+kv4_status append_gqa(const GqaFormat& f, const void* k_dev, int64_t k_token_stride, int64_t k_head_stride,
                            const void* v_dev, int64_t v_token_stride, int64_t v_head_stride,
                            int dtype, int64_t n_tokens, const int32_t* cu_seqlens_dev,
                            const int32_t* page_table_dev, int64_t pt_stride, int page_size,
                            const int32_t* seq_lens_dev, int B, int Hkv, int D, uint8_t* pool_dev,
                            uint8_t* scales_dev, int64_t num_pages, int32_t* dev_err,
                            kv4_stream_t stream) {
-  const kv4_status shape = check_gqa8(n_tokens, Hkv, Hkv, D, B, dtype, page_size, num_pages, pt_stride);
+  const kv4_status shape = check_gqa(n_tokens, Hkv, Hkv, D, B, dtype, page_size, num_pages, pt_stride);
   if (shape != KV4_OK) return shape;
   if (n_tokens == 0 || B == 0) return KV4_OK;
   if (num_pages < 1) return KV4_ERR_INVALID_ARG;
@@ -981,9 +989,9 @@ kv4_status kv4_append_gqa8(const void* k_dev, int64_t k_token_stride, int64_t k_
       !scales_dev)
     return KV4_ERR_INVALID_ARG;
   if (!strides_ok(k_dev, k_token_stride, k_head_stride, Hkv, D) ||
-      !strides_ok(v_dev, v_token_stride, v_head_stride, Hkv, D) || !aligned128(pool_dev) ||
-      !aligned4(cu_seqlens_dev) || !aligned4(page_table_dev) || !aligned4(seq_lens_dev) ||
-      !aligned4(dev_err))
+      !strides_ok(v_dev, v_token_stride, v_head_stride, Hkv, D) || !aligned_to(pool_dev, f.pool_align) ||
+      !aligned_to(scales_dev, f.scales_align) || !aligned4(cu_seqlens_dev) || !aligned4(page_table_dev) ||
+      !aligned4(seq_lens_dev) || !aligned4(dev_err))
     return KV4_ERR_INVALID_ARG;
   int sms = 0;
   const kv4_status st = device_info(&sms);
@@ -1009,24 +1017,24 @@ kv4_status kv4_append_gqa8(const void* k_dev, int64_t k_token_stride, int64_t k_
   a.num_pages = num_pages;
   a.num_sms = sms;
   a.dev_err = dev_err;
-  return kv4::launch_append_gqa8(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  return f.append(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? KV4_OK
              : KV4_ERR_LAUNCH;
 }
 
-kv4_status kv4_read_gqa8(const uint8_t* pool_dev, const uint8_t* scales_dev, int64_t num_pages,
+kv4_status read_gqa(const GqaFormat& f, const uint8_t* pool_dev, const uint8_t* scales_dev, int64_t num_pages,
                          const int32_t* page_table_dev, int64_t pt_stride, int page_size,
                          const int32_t* starts_dev, const int32_t* cu_seqlens_dev,
                          int64_t n_tokens, int B, int Hkv, int D, int dtype, void* k_out_dev,
                          void* v_out_dev, int32_t* dev_err, kv4_stream_t stream) {
-  const kv4_status shape = check_gqa8(n_tokens, Hkv, Hkv, D, B, dtype, page_size, num_pages, pt_stride);
+  const kv4_status shape = check_gqa(n_tokens, Hkv, Hkv, D, B, dtype, page_size, num_pages, pt_stride);
   if (shape != KV4_OK) return shape;
   if (n_tokens == 0 || B == 0) return KV4_OK;
   if (num_pages < 1) return KV4_ERR_INVALID_ARG;
   if (!pool_dev || !scales_dev || !page_table_dev || !starts_dev || !cu_seqlens_dev ||
       !k_out_dev || !v_out_dev)
     return KV4_ERR_INVALID_ARG;
-  if (!aligned128(pool_dev) || !aligned16(k_out_dev) || !aligned16(v_out_dev) ||
+  if (!aligned_to(pool_dev, f.pool_align) || !aligned_to(scales_dev, f.scales_align) || !aligned16(k_out_dev) || !aligned16(v_out_dev) ||
       !aligned4(starts_dev) || !aligned4(cu_seqlens_dev) || !aligned4(page_table_dev) ||
       !aligned4(dev_err))
     return KV4_ERR_INVALID_ARG;
@@ -1050,15 +1058,15 @@ kv4_status kv4_read_gqa8(const uint8_t* pool_dev, const uint8_t* scales_dev, int
   a.num_pages = num_pages;
   a.num_sms = sms;
   a.dev_err = dev_err;
-  return kv4::launch_read_gqa8(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  return f.read(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? KV4_OK
              : KV4_ERR_LAUNCH;
 }
 
-kv4_status kv4_attention_gqa8_plan(int B, int max_new, int64_t n_tokens, int Hq, int Hkv, int D,
+kv4_status plan_gqa(const GqaFormat& f, int B, int max_new, int64_t n_tokens, int Hq, int Hkv, int D,
                                    size_t* workspace_bytes) {
   if (max_new < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0) return KV4_ERR_INVALID_ARG;
-  const kv4_status shape = check_gqa8(n_tokens, Hq, Hkv, D, B, KV4_BF16, KV4_PAGE, 0, 1);
+  const kv4_status shape = check_gqa(n_tokens, Hq, Hkv, D, B, KV4_BF16, KV4_PAGE, 0, 1);
   if (shape != KV4_OK) return shape;
   if (Hq / Hkv > 128) return KV4_ERR_UNSUPPORTED;
   if (n_tokens * (Hq / Hkv) > INT32_MAX) return KV4_ERR_INVALID_ARG;     // rows of a request
@@ -1066,11 +1074,11 @@ kv4_status kv4_attention_gqa8_plan(int B, int max_new, int64_t n_tokens, int Hq,
   const kv4_status st = device_info(&sms);
   if (st != KV4_OK) return st;
   if (workspace_bytes)
-    *workspace_bytes = kv4::attention_gqa8_workspace(max_new, Hq, Hkv, D, sms);
+    *workspace_bytes = f.workspace(max_new, Hq, Hkv, D, sms);
   return KV4_OK;
 }
 
-kv4_status kv4_attention_gqa8(const void* q_dev, int64_t q_token_stride, int64_t q_head_stride,
+kv4_status attention_gqa(const GqaFormat& f, const void* q_dev, int64_t q_token_stride, int64_t q_head_stride,
                               int dtype, int64_t n_tokens, const int32_t* cu_seqlens_dev,
                               int max_new, const uint8_t* pool_dev, const uint8_t* scales_dev,
                               int64_t num_pages, const int32_t* page_table_dev,
@@ -1080,7 +1088,7 @@ kv4_status kv4_attention_gqa8(const void* q_dev, int64_t q_token_stride, int64_t
                               size_t workspace_bytes, int32_t* dev_err, kv4_stream_t stream) {
   if (max_new < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || window < 0 || !std::isfinite(sm_scale))
     return KV4_ERR_INVALID_ARG;
-  const kv4_status shape = check_gqa8(n_tokens, Hq, Hkv, D, B, dtype, page_size, num_pages, pt_stride);
+  const kv4_status shape = check_gqa(n_tokens, Hq, Hkv, D, B, dtype, page_size, num_pages, pt_stride);
   if (shape != KV4_OK) return shape;
   if (Hq / Hkv > 128) return KV4_ERR_UNSUPPORTED;
   if (n_tokens * (Hq / Hkv) > INT32_MAX) return KV4_ERR_INVALID_ARG;     // rows of a request
@@ -1089,14 +1097,14 @@ kv4_status kv4_attention_gqa8(const void* q_dev, int64_t q_token_stride, int64_t
   if (!q_dev || !cu_seqlens_dev || !pool_dev || !scales_dev || !page_table_dev || !seq_lens_dev ||
       !out_dev || !lse_dev)
     return KV4_ERR_INVALID_ARG;
-  if (!strides_ok(q_dev, q_token_stride, q_head_stride, Hq, D) || !aligned128(pool_dev) ||
-      !aligned16(out_dev) || !aligned4(lse_dev) || !aligned2(scales_dev) || !aligned4(cu_seqlens_dev) ||
+  if (!strides_ok(q_dev, q_token_stride, q_head_stride, Hq, D) || !aligned_to(pool_dev, f.pool_align) ||
+      !aligned16(out_dev) || !aligned4(lse_dev) || !aligned_to(scales_dev, f.attention_scales_align) || !aligned4(cu_seqlens_dev) ||
       !aligned4(page_table_dev) || !aligned4(seq_lens_dev) || !aligned4(dev_err))
     return KV4_ERR_INVALID_ARG;
   int sms = 0;
   const kv4_status st = device_info(&sms);
   if (st != KV4_OK) return st;
-  const size_t need = kv4::attention_gqa8_workspace(max_new, Hq, Hkv, D, sms);
+  const size_t need = f.workspace(max_new, Hq, Hkv, D, sms);
   if (need > 0 && (!workspace_dev || workspace_bytes < need || !aligned16(workspace_dev)))
     return KV4_ERR_WORKSPACE;
   kv4::Gqa8AttnArgs a{};
@@ -1126,9 +1134,136 @@ kv4_status kv4_attention_gqa8(const void* q_dev, int64_t q_token_stride, int64_t
   a.timeout_ns = static_cast<uint64_t>(g_timeout_ns.load());
   a.fault_site = g_fault_site.load();
   a.num_sms = sms;
-  return kv4::launch_attention_gqa8(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  return f.attention(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? KV4_OK
              : KV4_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" {
+
+kv4_status kv4_append_gqa8(const void* k_dev, int64_t k_token_stride, int64_t k_head_stride,
+                           const void* v_dev, int64_t v_token_stride, int64_t v_head_stride,
+                           int dtype, int64_t n_tokens, const int32_t* cu_seqlens_dev,
+                           const int32_t* page_table_dev, int64_t pt_stride, int page_size,
+                           const int32_t* seq_lens_dev, int B, int Hkv, int D, uint8_t* pool_dev,
+                           uint8_t* scales_dev, int64_t num_pages, int32_t* dev_err,
+                           kv4_stream_t stream) {
+  return append_gqa(kGqa8, k_dev, k_token_stride, k_head_stride, v_dev, v_token_stride, v_head_stride, dtype,
+                    n_tokens, cu_seqlens_dev, page_table_dev, pt_stride, page_size, seq_lens_dev, B, Hkv, D,
+                    pool_dev, scales_dev, num_pages, dev_err, stream);
+}
+kv4_status kv4_read_gqa8(const uint8_t* pool_dev, const uint8_t* scales_dev, int64_t num_pages,
+                         const int32_t* page_table_dev, int64_t pt_stride, int page_size,
+                         const int32_t* starts_dev, const int32_t* cu_seqlens_dev,
+                         int64_t n_tokens, int B, int Hkv, int D, int dtype, void* k_out_dev,
+                         void* v_out_dev, int32_t* dev_err, kv4_stream_t stream) {
+  return read_gqa(kGqa8, pool_dev, scales_dev, num_pages, page_table_dev, pt_stride, page_size, starts_dev,
+                  cu_seqlens_dev, n_tokens, B, Hkv, D, dtype, k_out_dev, v_out_dev, dev_err, stream);
+}
+kv4_status kv4_attention_gqa8_plan(int B, int max_new, int64_t n_tokens, int Hq, int Hkv, int D,
+                                   size_t* workspace_bytes) {
+  return plan_gqa(kGqa8, B, max_new, n_tokens, Hq, Hkv, D, workspace_bytes);
+}
+kv4_status kv4_attention_gqa8(const void* q_dev, int64_t q_token_stride, int64_t q_head_stride,
+                              int dtype, int64_t n_tokens, const int32_t* cu_seqlens_dev,
+                              int max_new, const uint8_t* pool_dev, const uint8_t* scales_dev,
+                              int64_t num_pages, const int32_t* page_table_dev,
+                              int64_t pt_stride, int page_size, const int32_t* seq_lens_dev,
+                              int B, int Hq, int Hkv, int D, int window, float sm_scale,
+                              void* out_dev, float* lse_dev, void* workspace_dev,
+                              size_t workspace_bytes, int32_t* dev_err, kv4_stream_t stream) {
+  return attention_gqa(kGqa8, q_dev, q_token_stride, q_head_stride, dtype, n_tokens, cu_seqlens_dev, max_new,
+                       pool_dev, scales_dev, num_pages, page_table_dev, pt_stride, page_size, seq_lens_dev, B,
+                       Hq, Hkv, D, window, sm_scale, out_dev, lse_dev, workspace_dev, workspace_bytes,
+                       dev_err, stream);
+}
+
+kv4_status kv4_append_gqa4(const void* k_dev, int64_t k_token_stride, int64_t k_head_stride,
+                           const void* v_dev, int64_t v_token_stride, int64_t v_head_stride,
+                           int dtype, int64_t n_tokens, const int32_t* cu_seqlens_dev,
+                           const int32_t* page_table_dev, int64_t pt_stride, int page_size,
+                           const int32_t* seq_lens_dev, int B, int Hkv, int D, uint8_t* pool_dev,
+                           uint8_t* scales_dev, int64_t num_pages, int32_t* dev_err,
+                           kv4_stream_t stream) {
+  return append_gqa(kGqa4, k_dev, k_token_stride, k_head_stride, v_dev, v_token_stride, v_head_stride, dtype,
+                    n_tokens, cu_seqlens_dev, page_table_dev, pt_stride, page_size, seq_lens_dev, B, Hkv, D,
+                    pool_dev, scales_dev, num_pages, dev_err, stream);
+}
+kv4_status kv4_read_gqa4(const uint8_t* pool_dev, const uint8_t* scales_dev, int64_t num_pages,
+                         const int32_t* page_table_dev, int64_t pt_stride, int page_size,
+                         const int32_t* starts_dev, const int32_t* cu_seqlens_dev,
+                         int64_t n_tokens, int B, int Hkv, int D, int dtype, void* k_out_dev,
+                         void* v_out_dev, int32_t* dev_err, kv4_stream_t stream) {
+  return read_gqa(kGqa4, pool_dev, scales_dev, num_pages, page_table_dev, pt_stride, page_size, starts_dev,
+                  cu_seqlens_dev, n_tokens, B, Hkv, D, dtype, k_out_dev, v_out_dev, dev_err, stream);
+}
+kv4_status kv4_attention_gqa4_plan(int B, int max_new, int64_t n_tokens, int Hq, int Hkv, int D,
+                                   size_t* workspace_bytes) {
+  return plan_gqa(kGqa4, B, max_new, n_tokens, Hq, Hkv, D, workspace_bytes);
+}
+kv4_status kv4_attention_gqa4(const void* q_dev, int64_t q_token_stride, int64_t q_head_stride,
+                              int dtype, int64_t n_tokens, const int32_t* cu_seqlens_dev,
+                              int max_new, const uint8_t* pool_dev, const uint8_t* scales_dev,
+                              int64_t num_pages, const int32_t* page_table_dev,
+                              int64_t pt_stride, int page_size, const int32_t* seq_lens_dev,
+                              int B, int Hq, int Hkv, int D, int window, float sm_scale,
+                              void* out_dev, float* lse_dev, void* workspace_dev,
+                              size_t workspace_bytes, int32_t* dev_err, kv4_stream_t stream) {
+  return attention_gqa(kGqa4, q_dev, q_token_stride, q_head_stride, dtype, n_tokens, cu_seqlens_dev, max_new,
+                       pool_dev, scales_dev, num_pages, page_table_dev, pt_stride, page_size, seq_lens_dev, B,
+                       Hq, Hkv, D, window, sm_scale, out_dev, lse_dev, workspace_dev, workspace_bytes,
+                       dev_err, stream);
+}
+
+kv4_status kv4_rotary(const void* q_dev, int64_t q_token_stride, int64_t q_head_stride, int Hq,
+                      int Dq, int q_offset, void* q_out_dev, int64_t q_out_token_stride,
+                      int64_t q_out_head_stride, const void* k_dev, int64_t k_token_stride,
+                      int64_t k_head_stride, int Hk, int Dk, int k_offset, void* k_out_dev,
+                      int64_t k_out_token_stride, int64_t k_out_head_stride, int dtype,
+                      int64_t n_tokens, const void* positions_dev, int position_bits,
+                      const float* inv_freq_dev, int n_pairs, int interleaved, float factor,
+                      kv4_stream_t stream) {
+  if (n_tokens < 0 || Hq < 0 || Hk < 0 || n_pairs < 1 || Hq > 65535 || Hk > 65535 || !std::isfinite(factor))
+    return KV4_ERR_INVALID_ARG;
+  if ((dtype != KV4_BF16 && dtype != KV4_F16) || (position_bits != 32 && position_bits != 64) ||
+      n_pairs > kv4::kRotaryPairs || Hq + Hk > 65535)
+    return KV4_ERR_UNSUPPORTED;
+  kv4::RotaryArgs a{};
+  a.side[0] = {q_dev, q_out_dev, q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride, Hq, Dq, q_offset};
+  a.side[1] = {k_dev, k_out_dev, k_token_stride, k_head_stride, k_out_token_stride, k_out_head_stride, Hk, Dk, k_offset};
+  for (kv4::RotarySide& s : a.side) {
+    if (s.heads == 0) {
+      s = {};
+      continue;
+    }
+    if (s.D < 1 || s.D > 65536 || s.offset < 0 || s.offset > s.D || s.D - s.offset < 2 * n_pairs || n_tokens > INT32_MAX ||
+        s.in_token < 0 || s.in_head < 0 || s.out_token < 0 || s.out_head < 0)
+      return KV4_ERR_INVALID_ARG;
+    // outputs' rows lie apart; one that is its input has its strides
+    if ((s.heads > 1 && s.out_head < s.D) || (n_tokens > 1 && s.out_token < s.D) ||
+        (s.in == s.out && ((n_tokens > 1 && s.in_token != s.out_token) || (s.heads > 1 && s.in_head != s.out_head))))
+      return KV4_ERR_INVALID_ARG;
+  }
+  if (n_tokens == 0 || Hq + Hk == 0) return KV4_OK;
+  for (const kv4::RotarySide& s : a.side)
+    if (s.heads > 0 && (!s.in || !s.out || !aligned_to(s.in, 2) || !aligned_to(s.out, 2))) return KV4_ERR_INVALID_ARG;
+  if (!positions_dev || !inv_freq_dev || !aligned_to(positions_dev, position_bits / 8) || !aligned4(inv_freq_dev))
+    return KV4_ERR_INVALID_ARG;
+  int sms = 0;
+  const kv4_status st = device_info(&sms);
+  if (st != KV4_OK) return st;
+  a.n_tokens = n_tokens;
+  a.positions = positions_dev;
+  a.wide_positions = position_bits == 64;
+  a.inv_freq = inv_freq_dev;
+  a.n = n_pairs;
+  a.interleaved = interleaved != 0;
+  a.f16 = dtype == KV4_F16;
+  a.factor = factor;
+  a.num_sms = sms;
+  return kv4::launch_rotary(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KV4_OK : KV4_ERR_LAUNCH;
 }
 
 kv4_status kv4_set_wait_limit(int64_t timeout_ns, int fault_site) {

@@ -1,0 +1,236 @@
+// kv4_gqa4.cu -- write and read-back of the 4-bit grouped-query cache
+// (kv4_append_gqa4, kv4_read_gqa4).
+//
+// A page holds 64 tokens of one request; the block of a (page, kv head, side)
+// is 64 rows of D / 2 bytes of E2M1 codes and, in a second tensor, 64 rows of
+// D / 16 E4M3 scales, value = code * scale.  A row depends on its token alone:
+//   scale = E4M3(amax / 6),  code = E2M1(x / scale)   of 16 elements
+// both rounded half to even and saturating, so rows that are there stay as
+// they are.
+#include "kv4_gqa_pages.cuh"
+
+namespace kv4 {
+namespace {
+
+constexpr int kThreads = 256;         // of a block of the read-back
+constexpr int kAppendThreads = 128;   // and of the write
+
+__device__ __forceinline__ uint32_t e2m1x2_of_f32(float hi, float lo) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tmov.b32 %0, {b, 0, 0, 0};\n\t}"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+
+// One block: 16 values of 16 bits -> 8 bytes of codes and the scale's byte.
+// x / s is taken as x * fl(1 / s), then rounded to 16 significant bits: x has at
+// most 11 bits, s 4 and a border between two codes 3, so x / s is either a border
+// exactly, which the product meets to 2^-23 and that rounding makes exact again,
+// or at least 2^-11 of itself away from it, which neither can bridge.  The
+// conversion then decides every code as the quotient itself would.  (One division
+// and one reciprocal for 16 elements instead of 17 divisions.)  A NaN counts as
+// 0 and an infinity saturates; neither counts for amax, and `odd` is set.
+template <bool F16>
+__device__ __forceinline__ uint2 quantize16(const uint4& a, const uint4& b, uint32_t& scale, bool& odd) {
+  float x[16];
+  widen8<F16>(a, x);
+  widen8<F16>(b, x + 8);
+  uint32_t m2 = max_abs2<F16>(max_abs2<F16>(max_abs2<F16>(a.x & 0x7FFF7FFFu, a.y), a.z), a.w);
+  m2 = max_abs2<F16>(max_abs2<F16>(max_abs2<F16>(max_abs2<F16>(m2, b.x), b.y), b.z), b.w);
+  uint32_t m = largest_bits<F16>(m2);
+  if (m >= 0x7F800000u) {
+    odd = true;
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t u = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+      if (u < 0x7F800000u) m = max(m, u);
+      if (u > 0x7F800000u) x[i] = 0.0f;
+    }
+  }
+  uint16_t s2;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s2) : "f"(0.0f), "f"(__fdiv_rn(__uint_as_float(m), 6.0f)));
+  scale = s2;
+  const float r = scale != 0 ? __frcp_rn(e4m3_to_float(scale)) : 0.0f;
+  uint32_t o[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float y0 = __uint_as_float((__float_as_uint(x[2 * i] * r) + 0x80u) & 0xFFFFFF00u);
+    const float y1 = __uint_as_float((__float_as_uint(x[2 * i + 1] * r) + 0x80u) & 0xFFFFFF00u);
+    o[i / 4] |= e2m1x2_of_f32(y1, y0) << (8 * (i % 4));
+  }
+  return scale != 0 ? make_uint2(o[0], o[1]) : make_uint2(0, 0);
+}
+
+// Row r of a (page, head, side) block, column block c.
+template <int D>
+__device__ __forceinline__ void store_block(const Gqa8Args& a, int64_t blk, int r, int c, const uint2& codes,
+                                            uint32_t scale) {
+  const int64_t row = blk * kPage + r;
+  *reinterpret_cast<uint2*>(a.pool + row * (D / 2) + c * 8) = codes;
+  a.scales[row * (D / 16) + c] = static_cast<uint8_t>(scale);
+}
+
+// A block for each (page, kv head, side): a thread takes 16 elements of a row, so
+// that a warp reads whole rows and writes 256 contiguous bytes of codes and one
+// sector of scales.
+template <int D, bool F16>
+__global__ void __launch_bounds__(kAppendThreads) append4_kernel(Gqa8Args a) {
+  constexpr int TPR = D / 16, RPP = kAppendThreads / TPR, PASSES = kPage / RPP;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  PageItem it;
+  if (!find_page(a, blockIdx.x, it)) return;
+  const int entry = table_entry(a, it);
+  const int h = blockIdx.y >> 1, s = blockIdx.y & 1, tid = threadIdx.x;
+  const int lo = it.start > (it.page << 6) ? static_cast<int>(it.start & 63) : 0;
+  const int hi = it.end - (it.page << 6) < kPage ? static_cast<int>(it.end - (it.page << 6)) : kPage;
+  const int64_t row_of_0 = it.row0 + (it.page << 6) - it.start;     // flat row of the page's row 0
+  const int c = tid % TPR, r0 = tid / TPR;
+  const int64_t ts = s == 0 ? a.k_token_stride : a.v_token_stride;
+  const uint16_t* src = (s == 0 ? static_cast<const uint16_t*>(a.k) + h * a.k_head_stride
+                                : static_cast<const uint16_t*>(a.v) + h * a.v_head_stride) + c * 16;
+  uint4 x[PASSES][2];
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const int r = r0 + p * RPP;
+    x[p][0] = x[p][1] = make_uint4(0, 0, 0, 0);
+    if (r >= lo && r < hi) {
+      const uint4* g = reinterpret_cast<const uint4*>(src + (row_of_0 + r) * ts);
+      x[p][0] = load(g);
+      x[p][1] = load(g + 1);
+    }
+  }
+  const int64_t pg = physical_page(a, entry);
+  if (pg < 0) return;
+  bool odd = false;
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const int r = r0 + p * RPP;
+    uint32_t scale;
+    const uint2 codes = quantize16<F16>(x[p][0], x[p][1], scale, odd);
+    if (r >= lo && r < hi) store_block<D>(a, (pg * a.Hkv + h) * 2 + s, r, c, codes, scale);
+  }
+  if (odd) flag_error(a.dev_err, kDevNonFinite);
+}
+
+// The same with a warp's threads on the blocks of one token, all heads and both
+// sides: where most pages get a token or two (a decode step), a block a page
+// would leave most of its threads without a row.
+template <int D, bool F16>
+__global__ void __launch_bounds__(kAppendThreads) append4_rows_kernel(Gqa8Args a) {
+  constexpr int TPR = D / 16;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int t = blockIdx.x;
+  int b, entry = -1;
+  int64_t pos;
+  if (!find_token(a, t, b, pos)) return;
+  if ((pos >> 6) < a.pt_stride) entry = load(a.page_table + b * a.pt_stride + (pos >> 6));
+  const int64_t pg = physical_page(a, entry);
+  if (pg < 0) return;
+  bool odd = false;
+  for (int u = blockIdx.y * kAppendThreads + threadIdx.x; u < 2 * a.Hkv * TPR; u += gridDim.y * kAppendThreads) {
+    const int c = u % TPR, hs = u / TPR, s = hs >= a.Hkv ? 1 : 0, h = hs - s * a.Hkv;
+    const uint16_t* src = s == 0 ? static_cast<const uint16_t*>(a.k) + t * a.k_token_stride + h * a.k_head_stride
+                                 : static_cast<const uint16_t*>(a.v) + t * a.v_token_stride + h * a.v_head_stride;
+    const uint4* g = reinterpret_cast<const uint4*>(src + c * 16);
+    uint32_t scale;
+    const uint2 codes = quantize16<F16>(load(g), load(g + 1), scale, odd);
+    store_block<D>(a, (pg * a.Hkv + h) * 2 + s, static_cast<int>(pos & 63), c, codes, scale);
+  }
+  if (odd) flag_error(a.dev_err, kDevNonFinite);
+}
+
+// 16 codes times a scale, as 16 values of 16 bits: exact in both types (at most 6
+// significant bits, magnitudes from 2^-10 to 2688; a NaN scale gives NaNs).
+template <bool F16>
+__device__ __forceinline__ void values16(const uint2& codes, uint32_t scale, uint4 (&o)[2]) {
+  const uint32_t s2 = e4m3x2_to_f16x2(scale | (scale << 8));
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    uint32_t h[4];
+    e2m1x8_to_f16x8(w == 0 ? codes.x : codes.y, h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[i] = f16x2_mul(h[i], s2);
+      if constexpr (!F16) {
+        const float2 f = __half22float2(bits_h2(h[i]));
+        h[i] = pack16<false>(f.x, f.y);
+      }
+    }
+    o[w] = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads) read4_kernel(Gqa8Args a) {
+  constexpr int TPR = D / 16, RPP = kThreads / TPR, PASSES = kPage / RPP;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int h = blockIdx.y, tid = threadIdx.x;
+  const int c = tid % TPR, r0 = tid / TPR;
+  PageItem it;
+  if (!find_page(a, blockIdx.x, it)) return;
+  const int64_t pg = physical_page(a, table_entry(a, it));
+  const int lo = it.start > (it.page << 6) ? static_cast<int>(it.start & 63) : 0;
+  const int hi = it.end - (it.page << 6) < kPage ? static_cast<int>(it.end - (it.page << 6)) : kPage;
+  const int64_t row_of_0 = it.row0 + (it.page << 6) - it.start;
+  uint2 codes[2][PASSES];
+  uint32_t scale[2][PASSES];
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      const int r = r0 + p * RPP;
+      codes[s][p] = make_uint2(0, 0);
+      scale[s][p] = 0;
+      if (pg >= 0 && r >= lo && r < hi) {
+        const int64_t row = ((pg * a.Hkv + h) * 2 + s) * kPage + r;
+        codes[s][p] = load(reinterpret_cast<const uint2*>(a.pool + row * (D / 2) + c * 8));
+        scale[s][p] = load(a.scales + row * (D / 16) + c);
+      }
+    }
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      const int r = r0 + p * RPP;
+      if (r < lo || r >= hi) continue;
+      uint4 o[2];
+      values16<F16>(codes[s][p], scale[s][p], o);
+      uint16_t* dst = static_cast<uint16_t*>(s == 0 ? a.k_out : a.v_out) + ((row_of_0 + r) * a.Hkv + h) * D + c * 16;
+      reinterpret_cast<uint4*>(dst)[0] = o[0];
+      reinterpret_cast<uint4*>(dst)[1] = o[1];
+    }
+}
+
+template <int D, bool F16>
+cudaError_t launch_append(const Gqa8Args& a, cudaStream_t stream) {
+  // fewer than 8 tokens a request on average: a block for each token
+  if (a.n_tokens < 8 * static_cast<int64_t>(a.B)) {
+    const int units = 2 * a.Hkv * (D / 16);
+    return launch_grid(append4_rows_kernel<D, F16>, a,
+                       dim3(static_cast<unsigned>(a.n_tokens), (units + kAppendThreads - 1) / kAppendThreads),
+                       kAppendThreads, stream);
+  }
+  return launch_pages(append4_kernel<D, F16>, a, 1, 2 * a.Hkv, kAppendThreads, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_append_gqa4(const Gqa8Args& a, cudaStream_t stream) {
+  if (a.D == 64) return a.f16 ? launch_append<64, true>(a, stream) : launch_append<64, false>(a, stream);
+  return a.f16 ? launch_append<128, true>(a, stream) : launch_append<128, false>(a, stream);
+}
+
+cudaError_t launch_read_gqa4(const Gqa8Args& a, cudaStream_t stream) {
+  if (a.D == 64)
+    return a.f16 ? launch_pages(read4_kernel<64, true>, a, 1, a.Hkv, kThreads, stream)
+                 : launch_pages(read4_kernel<64, false>, a, 1, a.Hkv, kThreads, stream);
+  return a.f16 ? launch_pages(read4_kernel<128, true>, a, 1, a.Hkv, kThreads, stream)
+               : launch_pages(read4_kernel<128, false>, a, 1, a.Hkv, kThreads, stream);
+}
+
+}  // namespace kv4

@@ -7,13 +7,9 @@
 // and sum and the output are held in fp32:
 //   s_j = sm_scale q.k_j,  o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),
 //   lse = m + log sum_j exp(s_j - m);  a row without a key: 0 and -inf.
-#include "kv4_gqa8_device.cuh"
+#include "kv4_gqa_merge.cuh"
 
-#include <math.h>
 #include <stddef.h>
-
-#include <mutex>
-#include <type_traits>
 
 namespace kv4 {
 namespace {
@@ -1292,162 +1288,6 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
 }
 
 // ---------------------------------------------------------------------------
-// The pieces of items that were cut: block (c, y) joins rows of the item that
-// began in block c of the attention kernel, by log-sum-exp over its pieces in
-// their order: one kernel for items of few rows, where a long context has many
-// pieces and 8 warps share a row, one for items of up to 256 rows, where a warp
-// takes 4 rows at once and their pieces in turn.  Those of a prompt or a chunk are
-// two or three; but a single short one of few heads over a long context is cut
-// over all blocks (40 rows of one head over 200000 tokens: 97 us, where one row,
-// in the kernels of few rows, takes 28).
-// ---------------------------------------------------------------------------
-template <int D>
-__global__ void __launch_bounds__(256) merge_few_kernel(const Gqa8AttnArgs a, const int rows,
-                                                    const Gqa8Tail* tails, const float* ws_lse,
-                                                    const float* ws_o) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  constexpr int C = D / 32;                               // columns a lane
-  using Vec = std::conditional_t<C == 4, float4, float2>;
-  __shared__ Vec part[8][32];
-  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Gqa8Tail t = tails[c];
-  constexpr int W = 8;
-  const int r = blockIdx.y, wi = warp;
-  if (t.parts == 0 || r >= t.nrows) return;               // (whole blocks)
-  float o[C], m = -INFINITY, s = 0.0f;
-#pragma unroll
-  for (int k = 0; k < C; ++k) o[k] = 0.0f;
-  bool odd = false;
-  {
-    // piece i is slot 2c + 1 for i = 0, else 2 (c + i)
-    auto row_of = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * rows + r; };
-    for (int i = lane; i < t.parts; i += 32) {
-      const float x = load(ws_lse + row_of(i));
-      odd |= x != x;
-      m = fmaxf(m, x);
-    }
-    m = warp_max(m);
-    odd = __any_sync(0xFFFFFFFFu, odd);
-    if (m > -INFINITY) {
-      for (int i0 = 0; i0 < t.parts; i0 += 32) {
-        const float w = i0 + lane < t.parts ? fast_exp2(load(ws_lse + row_of(i0 + lane)) - m) : 0.0f;
-        s += w;
-        const int n = min(32, t.parts - i0);
-#pragma unroll 4
-        for (int i = wi; i < n; i += W) {
-          const float wt = __shfl_sync(0xFFFFFFFFu, w, i);
-          const Vec v = load(reinterpret_cast<const Vec*>(ws_o + row_of(i0 + i) * D) + lane);
-          const float* f = reinterpret_cast<const float*>(&v);
-#pragma unroll
-          for (int k = 0; k < C; ++k) o[k] = fmaf(wt, f[k], o[k]);
-        }
-      }
-      s = warp_sum(s);
-    }
-    if (odd) s = __uint_as_float(0x7FC00000u);
-  }
-  part[warp][lane] = *reinterpret_cast<const Vec*>(o);
-  __syncthreads();
-  if (wi != 0) return;
-#pragma unroll
-  for (int i = 1; i < W; ++i) {
-    const Vec v = part[i][lane];
-#pragma unroll
-    for (int k = 0; k < C; ++k) o[k] += reinterpret_cast<const float*>(&v)[k];
-  }
-  const int G = a.Hq / a.Hkv, rr = t.r0 + r;
-  const int64_t row = static_cast<int64_t>(t.cu0 + rr / G) * a.Hq + t.h * G + rr % G;
-  const float inv = s == 0.0f ? 0.0f : 1.0f / s;
-  uint32_t u[C / 2];
-#pragma unroll
-  for (int k = 0; k < C / 2; ++k) {
-    const float y0 = o[2 * k] * inv, y1 = o[2 * k + 1] * inv;
-    if (a.f16) {
-      u[k] = h2_bits(__floats2half2_rn(y0, y1));
-    } else {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
-      u[k] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  }
-  uint32_t* const dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * D) + lane * (C / 2);
-  if constexpr (C == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[1]);
-  else *dst = u[0];
-  if (lane == 0) a.lse[row] = s == 0.0f ? -INFINITY : (m + log2f(s)) * 0.6931471805599453f;
-}
-
-template <int D>
-__global__ void __launch_bounds__(256) merge_many_kernel(const Gqa8AttnArgs a, const int rows,
-                                                         const Gqa8Tail* tails, const float* ws_lse,
-                                                         const float* ws_o) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  constexpr int C = D / 32, R = 4;
-  using Vec = std::conditional_t<C == 4, float4, float2>;
-  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Gqa8Tail t = tails[c];
-  const int r0 = (blockIdx.y * 8 + warp) * R;
-  if (t.parts == 0 || r0 >= t.nrows) return;
-  auto row_of = [&](int i, int r) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * rows + r; };
-  // lane 8 k + i: row r0 + k, piece i of 8 at a time
-  const int k8 = lane >> 3, i8 = lane & 7, mine = min(r0 + k8, t.nrows - 1);
-  float m = -INFINITY;
-  bool odd = false;
-  for (int i = i8; i < t.parts; i += 8) {
-    const float x = load(ws_lse + row_of(i, mine));
-    odd |= x != x;
-    m = fmaxf(m, x);
-  }
-#pragma unroll
-  for (int off = 4; off > 0; off >>= 1) {
-    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
-    odd |= __shfl_xor_sync(0xFFFFFFFFu, static_cast<int>(odd), off) != 0;
-  }
-  float s = 0.0f, o[R][C];
-#pragma unroll
-  for (int k = 0; k < R; ++k)
-#pragma unroll
-    for (int j = 0; j < C; ++j) o[k][j] = 0.0f;
-  for (int i0 = 0; i0 < t.parts; i0 += 8) {
-    const bool in = i0 + i8 < t.parts && m > -INFINITY;
-    const float w = in ? fast_exp2(load(ws_lse + row_of(i0 + i8, mine)) - m) : 0.0f;
-    s += w;
-    const int n = min(8, t.parts - i0);
-#pragma unroll 2
-    for (int i = 0; i < n; ++i)
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        const float wk = __shfl_sync(0xFFFFFFFFu, w, k * 8 + i);
-        const Vec v = load(reinterpret_cast<const Vec*>(ws_o + row_of(i0 + i, min(r0 + k, t.nrows - 1)) * D) + lane);
-        const float* f = reinterpret_cast<const float*>(&v);
-#pragma unroll
-        for (int j = 0; j < C; ++j) o[k][j] = fmaf(wk, f[j], o[k][j]);
-      }
-  }
-#pragma unroll
-  for (int off = 4; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-  if (odd) s = __uint_as_float(0x7FC00000u);
-  const int G = a.Hq / a.Hkv;
-#pragma unroll
-  for (int k = 0; k < R; ++k) {
-    const float sk = __shfl_sync(0xFFFFFFFFu, s, k * 8), mk = __shfl_sync(0xFFFFFFFFu, m, k * 8);
-    if (r0 + k >= t.nrows) break;
-    const int rr = t.r0 + r0 + k;
-    const int64_t row = static_cast<int64_t>(t.cu0 + rr / G) * a.Hq + t.h * G + rr % G;
-    const float inv = sk == 0.0f ? 0.0f : 1.0f / sk;
-    uint32_t u[C / 2];
-#pragma unroll
-    for (int j = 0; j < C / 2; ++j)
-      u[j] = a.f16 ? pack16<true>(o[k][2 * j] * inv, o[k][2 * j + 1] * inv)
-                   : pack16<false>(o[k][2 * j] * inv, o[k][2 * j + 1] * inv);
-    uint32_t* const dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * D) + lane * (C / 2);
-    if constexpr (C == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[1]);
-    else *dst = u[0];
-    if (lane == 0) a.lse[row] = sk == 0.0f ? -INFINITY : (mk + log2f(sk)) * 0.6931471805599453f;
-  }
-}
-
-// ---------------------------------------------------------------------------
 // Launch
 // ---------------------------------------------------------------------------
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1487,59 +1327,7 @@ int few_rows(int max_new, int G) {
   const int64_t all = static_cast<int64_t>(max_new) * G, need = all <= 24 ? all : G;
   return need <= 8 ? 8 : need <= 16 ? 16 : need <= 24 ? 24 : 0;
 }
-// Workspace of one attention kernel: a tail for each of its blocks, then two
-// slots of partial rows for each block.
-size_t part_bytes(int blocks, int rows, int D) {
-  return static_cast<size_t>(blocks) * (sizeof(Gqa8Tail) + 2ull * rows * (D + 1) * sizeof(float));
-}
-struct Parts {
-  Gqa8Tail* tails;
-  float *lse, *o;
-};
-Parts parts_at(void* ws, int blocks, int rows, int D) {
-  Parts p;
-  p.tails = static_cast<Gqa8Tail*>(ws);
-  p.o = reinterpret_cast<float*>(p.tails + blocks);
-  p.lse = p.o + 2ull * blocks * rows * D;
-  return p;
-}
 constexpr int kFewCtas = 2, kManyRows = 256;      // blocks an SM at most
-
-template <typename K>
-cudaError_t launch_merge(K kernel, const Gqa8AttnArgs& a, int blocks, int y, int rows, const Parts& p,
-                         cudaStream_t stream) {
-  if ((a.pt_stride + 1) / 2 <= kWhole) return cudaSuccess;                 // nothing is ever cut
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, y);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, rows, static_cast<const Gqa8Tail*>(p.tails),
-                            static_cast<const float*>(p.lse), static_cast<const float*>(p.o));
-}
-
-// Once per device and kernel: its shared memory, and, where it splits its
-// registers among its warps, that its launch has as many as the split takes.
-template <auto kKernel>
-cudaError_t prepare_kernel(int smem, int min_regs) {
-  static std::once_flag once[64];
-  static cudaError_t ready[64];
-  int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  std::call_once(once[dev], [&] {
-    ready[dev] = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    cudaFuncAttributes f;
-    if (ready[dev] == cudaSuccess) ready[dev] = cudaFuncGetAttributes(&f, kKernel);
-    if (ready[dev] == cudaSuccess && f.numRegs < min_regs) ready[dev] = cudaErrorInvalidConfiguration;
-  });
-  return ready[dev];
-}
 
 template <int D, int RP, int NT>
 cudaError_t launch_few(const Gqa8AttnArgs& a, const CUtensorMap& map, int max_rows, void* ws,

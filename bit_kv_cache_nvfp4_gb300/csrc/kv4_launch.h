@@ -77,7 +77,8 @@ struct GatherArgs {
   int32_t* dev_err;
 };
 
-// The 8-bit grouped-query cache (kv4_append_gqa8, kv4_read_gqa8).
+// The grouped-query caches (kv4_append_gqa8, kv4_read_gqa8, kv4_append_gqa4,
+// kv4_read_gqa4).
 struct Gqa8Args {
   const void* k;               // inputs of an append: 16-bit [T, Hkv, D], strided
   int64_t k_token_stride, k_head_stride;
@@ -95,8 +96,8 @@ struct Gqa8Args {
   int B, Hkv, D;
   int each;                    // pages a thread block looks after (set by the launch)
   int num_sms;
-  uint8_t* pool;               // [num_pages, Hkv, 2, 64, D] E4M3
-  uint8_t* scales;             // [num_pages, Hkv, 2] E8M0
+  uint8_t* pool;               // [num_pages, Hkv, 2, 64, D] E4M3 (4-bit cache: [.., 64, D / 2] E2M1)
+  uint8_t* scales;             // [num_pages, Hkv, 2] E8M0 (4-bit cache: [.., 64, D / 16] E4M3)
   int64_t num_pages;
   int32_t* dev_err;
 };
@@ -124,6 +125,28 @@ struct Gqa8AttnArgs {
   int32_t* dev_err;
   uint64_t timeout_ns;
   int fault_site;
+  int num_sms;
+};
+
+// Rotary positions (kv4_rotary).
+struct RotarySide {
+  const void* in;              // 16-bit [T, heads, D], strided
+  void* out;                   // the same, or `in` itself with its strides
+  int64_t in_token, in_head, out_token, out_head;
+  int heads, D;                // (no heads: not there)
+  int offset;                  // first element that turns
+};
+constexpr int kRotaryPairs = 512;
+struct RotaryArgs {
+  RotarySide side[2];          // q, k
+  int64_t n_tokens;
+  const void* positions;       // int32 or int64 [T]
+  int wide_positions;
+  const float* inv_freq;       // fp32 [n]
+  int n;                       // pairs of a head, 1 .. kRotaryPairs
+  int interleaved, f16;
+  float factor;
+  int heads, heads_at_once, tokens;      // of a thread block (set by the launch)
   int num_sms;
 };
 
@@ -180,6 +203,11 @@ cudaError_t launch_read_gqa8(const Gqa8Args& a, cudaStream_t stream);
 cudaError_t launch_attention_gqa8(const Gqa8AttnArgs& a, cudaStream_t stream);
 // Workspace bytes of launch_attention_gqa8 for these sizes on num_sms SMs.
 size_t attention_gqa8_workspace(int max_new, int Hq, int Hkv, int D, int num_sms);
+cudaError_t launch_append_gqa4(const Gqa8Args& a, cudaStream_t stream);
+cudaError_t launch_read_gqa4(const Gqa8Args& a, cudaStream_t stream);
+cudaError_t launch_attention_gqa4(const Gqa8AttnArgs& a, cudaStream_t stream);
+size_t attention_gqa4_workspace(int max_new, int Hq, int Hkv, int D, int num_sms);
+cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t stream);
 cudaError_t launch_debug_gather(const GatherArgs& a, cudaStream_t stream);
 // The FP8 scratch copy of the rows the keys select: a.rows is uint8
 // [B*Sq*K, 576] (E4M3 of the dequantized NVFP4 values; masked keys 0).

@@ -1,4 +1,4 @@
-// kv4_torch.cpp -- the PyTorch side of the *_gqa8 entry points: a Python
+// kv4_torch.cpp -- the PyTorch side of the *_gqa8, *_gqa4 and rotary entry points: a Python
 // extension module (_kv4torch) that checks tensors, allocates outputs and
 // workspace, and calls the C ABI on the tensors' device and its current
 // stream.
@@ -10,7 +10,7 @@
 //
 // Bad arguments raise TypeError or ValueError before anything is launched.  A
 // nonzero kv4_status is returned as an int, which the Python wrapper
-// (gqa8.py) turns into Kv4Error.
+// (gqa8.py, gqa4.py, rotary.py) turns into Kv4Error.
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/pybind.h>
@@ -94,21 +94,27 @@ struct Cache {
   int64_t pages, stride;
   int B, hkv, d;
 };
+// The cache of 8-bit pages, [.., 64, D] with an exponent a block, or of 4-bit ones,
+// [.., 64, D / 2] with a scale for each 16 elements.
+template <int BITS>
 Cache cache(PyObject* pool_o, PyObject* scales_o, PyObject* table_o) {
+  constexpr bool k4 = BITS == 4;
   Cache c;
   const at::Tensor& pool = cuda_tensor(pool_o, "pool");
   if (pool.dim() != 5 || pool.size(2) != 2 || pool.size(3) != KV4_PAGE)
-    value_error("pool must be [num_pages, Hkv, 2, 64, D]");
+    value_error(k4 ? "pool must be [num_pages, Hkv, 2, 64, D / 2]" : "pool must be [num_pages, Hkv, 2, 64, D]");
   c.dev = pool.device();
   plain(pool_o, "pool", at::kByte, 5, c.dev);
-  const at::Tensor& scales = plain(scales_o, "scales", at::kByte, 3, c.dev);
+  const at::Tensor& scales = plain(scales_o, "scales", at::kByte, k4 ? 5 : 3, c.dev);
   const at::Tensor& table = plain(table_o, "page_table", at::kInt, 2, c.dev);
   c.pages = pool.size(0);
   if (pool.size(1) < 1 || pool.size(1) > 65535) value_error("pool: no or too many heads");
   c.hkv = static_cast<int>(pool.size(1));
-  c.d = static_cast<int>(std::min<int64_t>(pool.size(4), 1 << 20));
-  if (scales.size(0) != c.pages || scales.size(1) != c.hkv || scales.size(2) != 2)
-    value_error("scales must be [" + std::to_string(c.pages) + ", " + std::to_string(c.hkv) + ", 2]");
+  c.d = static_cast<int>(std::min<int64_t>(pool.size(4), 1 << 20)) * (k4 ? 2 : 1);
+  if (scales.size(0) != c.pages || scales.size(1) != c.hkv || scales.size(2) != 2 ||
+      (k4 && (scales.size(3) != KV4_PAGE || scales.size(4) != c.d / 16)))
+    value_error("scales must be [" + std::to_string(c.pages) + ", " + std::to_string(c.hkv) + ", 2" +
+                (k4 ? ", 64, " + std::to_string(c.d / 16) : "") + "]");
   c.pool = pool.mutable_data_ptr<uint8_t>();
   c.scales = scales.mutable_data_ptr<uint8_t>();
   c.table = table.const_data_ptr<int32_t>();
@@ -192,9 +198,10 @@ PyObject* guarded(const char* name, Py_ssize_t n, F&& f) {
 }
 
 // k, v, cu_seqlens, page_table, seq_lens, pool, scales, dev_err
+template <int BITS>
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded<8>("append", n, [&]() -> PyObject* {
-    const Cache c = cache(a[5], a[6], a[3]);
+    const Cache c = cache<BITS>(a[5], a[6], a[3]);
     const at::Tensor &k = cuda_tensor(a[0], "k"), &v = cuda_tensor(a[1], "v");
     const int dt = dtype_code(k.scalar_type(), "k");
     if (v.scalar_type() != k.scalar_type())
@@ -209,7 +216,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t* const err = err_word(a[7], c.dev);
     const c10::cuda::CUDAGuard guard(c.dev);
     const kv4_status st =
-        kv4_append_gqa8(sk.p, sk.token, sk.head, sv.p, sv.token, sv.head, dt, k.size(0), cu, c.table, c.stride,
+        (BITS == 8 ? kv4_append_gqa8 : kv4_append_gqa4)(sk.p, sk.token, sk.head, sv.p, sv.token, sv.head, dt, k.size(0), cu, c.table, c.stride,
                         KV4_PAGE, lens, c.B, c.hkv, c.d, c.pool, c.scales, c.pages, err, stream_of(c.dev));
     if (st == KV4_OK)
       for (const int i : {5, 6, 7}) written(a[i]);
@@ -218,9 +225,10 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // pool, scales, page_table, starts, cu_seqlens, total, f16, k_out, v_out, dev_err
+template <int BITS>
 PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded<10>("read", n, [&]() -> PyObject* {
-    const Cache c = cache(a[0], a[1], a[2]);
+    const Cache c = cache<BITS>(a[0], a[1], a[2]);
     const int32_t *cu, *starts;
     ragged(c, a[4], a[3], "starts", cu, starts);
     const int64_t total = small(a[5], "total");
@@ -231,7 +239,7 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor k = output(a[7], "k_out", {total, c.hkv, c.d}, type, c.dev);
     const at::Tensor v = output(a[8], "v_out", {total, c.hkv, c.d}, type, c.dev);
     const kv4_status st =
-        kv4_read_gqa8(c.pool, c.scales, c.pages, c.table, c.stride, KV4_PAGE, starts, cu, total, c.B, c.hkv, c.d,
+        (BITS == 8 ? kv4_read_gqa8 : kv4_read_gqa4)(c.pool, c.scales, c.pages, c.table, c.stride, KV4_PAGE, starts, cu, total, c.B, c.hkv, c.d,
                       f16 ? KV4_F16 : KV4_BF16, k.mutable_data_ptr(), v.mutable_data_ptr(), err, stream_of(c.dev));
     if (st == KV4_OK)
       for (const int i : {7, 8, 9}) written(a[i]);
@@ -240,9 +248,10 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // q, pool, scales, page_table, seq_lens, cu_seqlens, max_new, sm_scale, window, out, lse, workspace, dev_err
+template <int BITS>
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded<13>("attention", n, [&]() -> PyObject* {
-    const Cache c = cache(a[1], a[2], a[3]);
+    const Cache c = cache<BITS>(a[1], a[2], a[3]);
     const at::Tensor& q = cuda_tensor(a[0], "q");
     const int dt = dtype_code(q.scalar_type(), "q");
     if (q.dim() != 3 || q.size(2) != c.d || q.size(1) < 1 || q.size(1) % c.hkv != 0 || q.size(1) > (1 << 30))
@@ -267,7 +276,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* ws = nullptr;
     size_t ws_bytes = 0;
     if (a[11] == Py_None) {
-      const kv4_status st = kv4_attention_gqa8_plan(c.B, max_new, t, hq, c.hkv, c.d, &ws_bytes);
+      const kv4_status st = (BITS == 8 ? kv4_attention_gqa8_plan : kv4_attention_gqa4_plan)(c.B, max_new, t, hq, c.hkv, c.d, &ws_bytes);
       if (st != KV4_OK) return PyLong_FromLong(st);
       if (ws_bytes > 0) {
         own = c10::cuda::CUDACachingAllocator::get()->allocate(ws_bytes);
@@ -279,7 +288,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ws_bytes = given.numel();
     }
     const kv4_status st =
-        kv4_attention_gqa8(sq.p, sq.token, sq.head, dt, t, cu, max_new, c.pool, c.scales, c.pages, c.table, c.stride,
+        (BITS == 8 ? kv4_attention_gqa8 : kv4_attention_gqa4)(sq.p, sq.token, sq.head, dt, t, cu, max_new, c.pool, c.scales, c.pages, c.table, c.stride,
                            KV4_PAGE, lens, c.B, hq, c.hkv, c.d, window, static_cast<float>(scale),
                            out.mutable_data_ptr(), lse.mutable_data_ptr<float>(), ws, ws_bytes, err,
                            stream_of(c.dev));
@@ -289,14 +298,129 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// One side of a rotary call, q or k: nothing (None), or [T, heads, D] with contiguous
+// heads; the output is the caller's (which may be the input itself) or a new one.
+struct Side {
+  const void* in = nullptr;
+  void* out = nullptr;
+  int64_t in_token = 0, in_head = 0, out_token = 0, out_head = 0, tokens = 0;
+  int heads = 0, d = 0;
+  at::Tensor result;
+};
+// Bytes from the first element to past the last one.
+int64_t span_of(const at::Tensor& t) {
+  int64_t n = 1;
+  for (int64_t i = 0; i < t.dim(); ++i) n += (t.size(i) - 1) * t.stride(i);
+  return n * t.element_size();
+}
+Side side_of(PyObject* in_o, PyObject* out_o, const char* name, const at::Tensor& first) {
+  Side s;
+  const std::string out_name = std::string(name) + "_out";
+  if (in_o == Py_None) {
+    if (out_o != Py_None) value_error(out_name + " without " + name);
+    return s;
+  }
+  const at::Tensor& t = cuda_tensor(in_o, name);
+  if (t.scalar_type() != first.scalar_type())
+    type_error(std::string(name) + " must be " + name_of(first.scalar_type()) + ", got " + name_of(t.scalar_type()));
+  if (t.dim() != 3 || t.size(0) != first.size(0)) value_error(std::string(name) + " must be [" + std::to_string(first.size(0)) + ", heads, D]");
+  same_device(t, name, first.device());
+  auto strides = [](const at::Tensor& x, const std::string& what, int64_t& token, int64_t& head) {
+    if (x.size(2) > 1 && x.stride(2) != 1) value_error(what + ": the last dimension must be contiguous");
+    token = x.size(0) > 1 ? x.stride(0) : 0;
+    head = x.size(1) > 1 ? x.stride(1) : 0;
+  };
+  if (t.size(1) > 65535 || t.size(2) > 65536) value_error(std::string(name) + ": too many heads or elements");
+  s.tokens = t.size(0);
+  s.heads = static_cast<int>(t.size(1));
+  s.d = static_cast<int>(t.size(2));
+  strides(t, name, s.in_token, s.in_head);
+  s.in = t.const_data_ptr();
+  if (out_o == Py_None) {
+    s.result = at::Tensor(at::detail::empty_cuda(t.sizes(), t.scalar_type(), t.device(), std::nullopt));
+  } else {
+    const at::Tensor& o = cuda_tensor(out_o, out_name.c_str());
+    if (o.scalar_type() != t.scalar_type())
+      type_error(out_name + " must be " + name_of(t.scalar_type()) + ", got " + name_of(o.scalar_type()));
+    if (o.sizes() != t.sizes()) value_error(out_name + " must have the shape of " + name);
+    same_device(o, out_name.c_str(), t.device());
+    s.result = o;
+  }
+  strides(s.result, out_name, s.out_token, s.out_head);
+  s.out = s.result.mutable_data_ptr();
+  const char *a = static_cast<const char*>(s.in), *b = static_cast<const char*>(s.out);
+  if (t.numel() > 0 && !(a == b && s.in_token == s.out_token && s.in_head == s.out_head) && a < b + span_of(s.result) &&
+      b < a + span_of(t))
+    value_error(out_name + " must be " + name + " itself or lie apart from it");
+  return s;
+}
+
+// q, k, positions, inv_freq, interleaved, q_offset, k_offset, factor, q_out, k_out
+PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded<10>("rotary", n, [&]() -> PyObject* {
+    const at::Tensor& first = cuda_tensor(a[0] == Py_None ? a[1] : a[0], a[0] == Py_None ? "k" : "q");
+    const int dt = dtype_code(first.scalar_type(), a[0] == Py_None ? "k" : "q");
+    if (first.dim() != 3) value_error("q and k must be [T, heads, D]");
+    const c10::Device dev = first.device();
+    const at::Tensor& pos = cuda_tensor(a[2], "positions");
+    if (pos.scalar_type() != at::kInt && pos.scalar_type() != at::kLong)
+      type_error("positions must be torch.int32 or torch.int64, got " + name_of(pos.scalar_type()));
+    if (pos.dim() != 1 || pos.size(0) != first.size(0) || !pos.is_contiguous())
+      value_error("positions must be [" + std::to_string(first.size(0)) + "], contiguous");
+    if (pos.device() != dev) value_error("positions is on " + pos.device().str() + ", the inputs on " + dev.str());
+    const at::Tensor& freq = cuda_tensor(a[3], "inv_freq");
+    if (freq.scalar_type() != at::kFloat) type_error("inv_freq must be torch.float32, got " + name_of(freq.scalar_type()));
+    if (freq.dim() != 1 || !freq.is_contiguous()) value_error("inv_freq must have one dimension, contiguous");
+    if (freq.device() != dev) value_error("inv_freq is on " + freq.device().str() + ", the inputs on " + dev.str());
+    const int near = PyObject_IsTrue(a[4]);
+    const int q_at = small(a[5], "q_offset"), k_at = small(a[6], "k_offset");
+    const double factor = PyFloat_AsDouble(a[7]);
+    if (factor == -1.0 && PyErr_Occurred()) {
+      PyErr_Clear();
+      type_error("factor must be a number");
+    }
+    const c10::cuda::CUDAGuard guard(dev);
+    const Side q = side_of(a[0], a[8], "q", first), k = side_of(a[1], a[9], "k", first);
+    auto room = [&](const Side& s, const char* name, int at) {
+      if (s.heads > 0 && (at > s.d || s.d - at < 2 * freq.size(0)))
+        value_error(std::string(name) + ": " + std::to_string(2 * freq.size(0)) + " elements from " + std::to_string(at) +
+                    " on do not fit a head of " + std::to_string(s.d));
+    };
+    room(q, "q", q_at);
+    room(k, "k", k_at);
+    const kv4_status st =
+        kv4_rotary(q.in, q.in_token, q.in_head, q.heads, q.d, q_at, q.out, q.out_token, q.out_head, k.in, k.in_token,
+                   k.in_head, k.heads, k.d, k_at, k.out, k.out_token, k.out_head, dt, first.size(0),
+                   pos.const_data_ptr(), pos.scalar_type() == at::kLong ? 64 : 32, freq.const_data_ptr<float>(),
+                   static_cast<int>(std::min<int64_t>(freq.size(0), 1 << 20)), near, static_cast<float>(factor),
+                   stream_of(dev));
+    if (st != KV4_OK) return PyLong_FromLong(st);
+    written(a[8]);
+    written(a[9]);
+    PyObject* t = PyTuple_New(2);
+    if (t == nullptr) return nullptr;
+    auto item = [](PyObject* given, PyObject* in, const at::Tensor& made) -> PyObject* {
+      if (in == Py_None || given != Py_None) return Py_NewRef(in == Py_None ? Py_None : given);
+      return THPVariable_Wrap(made);
+    };
+    PyTuple_SET_ITEM(t, 0, item(a[8], a[0], q.result));
+    PyTuple_SET_ITEM(t, 1, item(a[9], a[1], k.result));
+    return t;
+  });
+}
+
 PyCFunction fast(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f));
 }
-PyMethodDef methods[] = {{"append", fast(append), METH_FASTCALL, "kv4_append_gqa8"},
-                         {"read", fast(read), METH_FASTCALL, "kv4_read_gqa8"},
-                         {"attention", fast(attention), METH_FASTCALL, "kv4_attention_gqa8"},
+PyMethodDef methods[] = {{"append", fast(append<8>), METH_FASTCALL, "kv4_append_gqa8"},
+                         {"read", fast(read<8>), METH_FASTCALL, "kv4_read_gqa8"},
+                         {"attention", fast(attention<8>), METH_FASTCALL, "kv4_attention_gqa8"},
+                         {"append4", fast(append<4>), METH_FASTCALL, "kv4_append_gqa4"},
+                         {"read4", fast(read<4>), METH_FASTCALL, "kv4_read_gqa4"},
+                         {"attention4", fast(attention<4>), METH_FASTCALL, "kv4_attention_gqa4"},
+                         {"rotary", fast(rotary), METH_FASTCALL, "kv4_rotary"},
                          {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kv4torch", "PyTorch side of the *_gqa8 entry points.", -1, methods,
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kv4torch", "PyTorch side of the *_gqa8, *_gqa4 and rotary entry points.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -67,10 +67,11 @@ enum {
                                 entry or slot >= num_slots; that key masked    */
   KV4_DEV_TIMEOUT = 4,       /* a bounded on-chip wait gave up; the outputs of
                                 that thread block are not valid               */
-  KV4_DEV_NONFINITE = 8,     /* kv4_append_gqa8: a NaN (stored as 0) or an
-                                infinity (stored saturated) in the inputs     */
-  KV4_DEV_BAD_LENGTH = 16    /* kv4_attention_gqa8: a request with more new
-                                tokens than max_new; its rows are not written */
+  KV4_DEV_NONFINITE = 8,     /* kv4_append_gqa8, _gqa4: a NaN (stored as 0) or
+                                an infinity (stored saturated) in the inputs  */
+  KV4_DEV_BAD_LENGTH = 16    /* kv4_attention_gqa8, _gqa4: a request with more
+                                new tokens than max_new; its rows are not
+                                written                                       */
 };
 
 enum {
@@ -80,7 +81,7 @@ enum {
   KV4_ROW_BYTES_FP8 = 576      /* FP8 comparison row (the *_fp8 entry points)  */
 };
 
-/* 16-bit types of the *_gqa8 entry points. */
+/* 16-bit types of the *_gqa8, *_gqa4 and rotary entry points. */
 enum { KV4_BF16 = 0, KV4_F16 = 1 };
 
 /* ---------------------------------------------------------------------------
@@ -583,9 +584,93 @@ kv4_status kv4_attention_gqa8(const void* q_dev, int64_t q_token_stride, int64_t
                               void* out_dev, float* lse_dev, void* workspace_dev,
                               size_t workspace_bytes, int32_t* dev_err, kv4_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The 4-bit grouped-query cache (*_gqa4): the 8-bit cache's calls over pages of
+ * NVFP4 rows.  Source: README "4-bit KV cache" (E2M1 values with one E4M3 scale
+ * per 16); the pages' models cache one MLA latent per token, so the block layout
+ * is this project's.  Arguments, sizes, strides, the page table, ragged batches
+ * and errors are those of the *_gqa8 calls, except:
+ *   pool_dev        uint8 [num_pages, Hkv, 2, 64, D / 2]: E2M1 codes, K then V of
+ *                   a page and head, a byte holding element 2j in its low half
+ *                   and 2j + 1 in its high half; 16-byte aligned
+ *   scales_dev      uint8 [num_pages, Hkv, 2, 64, D / 16]: E4M3, one for each 16
+ *                   elements of a row, value = code * scale; 16-byte aligned
+ * kv4_append_gqa4 -- per 16 elements of a token's head: scale = E4M3(amax / 6)
+ *   (IEEE fp32 division, round half to even, saturating at 448), code =
+ *   E2M1(x / scale) (round half to even, saturating at 6, sign of x kept); a
+ *   scale of 0 gives codes of 0.  A NaN counts as 0 and an infinity saturates,
+ *   neither counts for amax, both raise KV4_DEV_NONFINITE.  Rows depend on their
+ *   tokens alone: no other row of a page changes.
+ * kv4_read_gqa4 -- code * scale, exact in both 16-bit types; a NaN scale byte
+ *   (0x7F, 0xFF) gives NaNs.
+ * kv4_attention_gqa4 -- K and V enter their products exactly.  Two operands
+ *   enter in fewer bits: an element of q keeps its 8 or 11 bits unless it is below
+ *   2^-22 of its row's largest, and is then off by at most 2^-32 of that largest; a
+ *   weight is off by 2^-11 of itself or, below 2^-20 of the largest that its row
+ *   has met so far, by 2^-32 of that.  Scores, sums and outputs are held in fp32.
+ *   Equal calls give equal bits.  A row of q with a NaN or an infinity gives NaN
+ *   (when it has a key), and so may scores beyond fp32's range.  A NaN scale in a
+ *   row below seq_lens, which the append never writes, may turn any row of the
+ *   request NaN; what lies past seq_lens, or before every row's window, is never
+ *   used.
+ * ------------------------------------------------------------------------- */
+kv4_status kv4_append_gqa4(const void* k_dev, int64_t k_token_stride, int64_t k_head_stride,
+                           const void* v_dev, int64_t v_token_stride, int64_t v_head_stride,
+                           int dtype, int64_t n_tokens, const int32_t* cu_seqlens_dev,
+                           const int32_t* page_table_dev, int64_t pt_stride, int page_size,
+                           const int32_t* seq_lens_dev, int B, int Hkv, int D, uint8_t* pool_dev,
+                           uint8_t* scales_dev, int64_t num_pages, int32_t* dev_err,
+                           kv4_stream_t stream);
+kv4_status kv4_read_gqa4(const uint8_t* pool_dev, const uint8_t* scales_dev, int64_t num_pages,
+                         const int32_t* page_table_dev, int64_t pt_stride, int page_size,
+                         const int32_t* starts_dev, const int32_t* cu_seqlens_dev,
+                         int64_t n_tokens, int B, int Hkv, int D, int dtype, void* k_out_dev,
+                         void* v_out_dev, int32_t* dev_err, kv4_stream_t stream);
+kv4_status kv4_attention_gqa4_plan(int B, int max_new, int64_t n_tokens, int Hq, int Hkv, int D,
+                                   size_t* workspace_bytes);
+kv4_status kv4_attention_gqa4(const void* q_dev, int64_t q_token_stride, int64_t q_head_stride,
+                              int dtype, int64_t n_tokens, const int32_t* cu_seqlens_dev,
+                              int max_new, const uint8_t* pool_dev, const uint8_t* scales_dev,
+                              int64_t num_pages, const int32_t* page_table_dev,
+                              int64_t pt_stride, int page_size, const int32_t* seq_lens_dev,
+                              int B, int Hq, int Hkv, int D, int window, float sm_scale,
+                              void* out_dev, float* lse_dev, void* workspace_dev,
+                              size_t workspace_bytes, int32_t* dev_err, kv4_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * kv4_rotary -- rotary positions of queries and keys, in one call.
+ * The pages' models turn the rope part of q and of the cached key before the
+ * cache write and the attention; the pages give no layout, so both common ones
+ * are here.
+ *   q_dev, k_dev    16-bit [n_tokens, Hq, Dq] and [n_tokens, Hk, Dk], strided (in
+ *                   elements; heads' elements contiguous); Hq or Hk may be 0, and
+ *                   that side's pointers are then not looked at.  Hq + Hk <=
+ *                   65535, D <= 65536
+ *   q_out_dev, ..   the same shapes, rows at least D elements apart; an output is
+ *                   its input, with the same strides, or overlaps no input
+ *   positions_dev   int32 or int64 [n_tokens] (position_bits 32 or 64),
+ *                   magnitudes up to 2^31
+ *   inv_freq_dev    fp32 [n_pairs], 1 <= n_pairs <= 512, magnitudes up to 4:
+ *                   radians a position
+ * Pair i of a head is elements (offset + 2i, offset + 2i + 1) where interleaved is
+ * nonzero and (offset + i, offset + n_pairs + i) where it is 0; with the angle
+ * a = position * inv_freq[i] (held to 2^-31 of a turn)
+ *   (x, y) -> factor * (x cos a - y sin a, x sin a + y cos a)
+ * in fp32, rounded once.  Elements outside offset .. offset + 2 n_pairs - 1 are
+ * copied as they are.
+ * ------------------------------------------------------------------------- */
+kv4_status kv4_rotary(const void* q_dev, int64_t q_token_stride, int64_t q_head_stride, int Hq,
+                      int Dq, int q_offset, void* q_out_dev, int64_t q_out_token_stride,
+                      int64_t q_out_head_stride, const void* k_dev, int64_t k_token_stride,
+                      int64_t k_head_stride, int Hk, int Dk, int k_offset, void* k_out_dev,
+                      int64_t k_out_token_stride, int64_t k_out_head_stride, int dtype,
+                      int64_t n_tokens, const void* positions_dev, int position_bits,
+                      const float* inv_freq_dev, int n_pairs, int interleaved, float factor,
+                      kv4_stream_t stream);
+
 /* Test hook: the next decode and attention launches use this bounded-wait limit (ns; 0
  * keeps the 1 s default) and, when fault_site == 1, one warp of each block
- * finishes its work (kv4_attention_gqa8: its first item, so that the block
+ * finishes its work (kv4_attention_gqa8, _gqa4: its first item, so that the block
  * gives up the others) and then waits on an mbarrier that nothing arrives on,
  * so that the wait runs out and KV4_DEV_TIMEOUT is reported while the block
  * still exits normally.  fault_site must be 0 or 1.  0, 0 restores the
