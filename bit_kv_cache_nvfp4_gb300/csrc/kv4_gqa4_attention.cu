@@ -36,38 +36,56 @@ namespace {
 // power of two for each row, see the header for what it can lose), p is rounded
 // to 2^-11.
 //
-// Block: warp 0 finds the block's share of the work list and copies chunks of 2304
-// bytes of K and of V into a ring; each other warp takes every W-th chunk, with a
-// softmax and an output of its own, and they join at the item's end.  The running
+// Block: warp 0 finds the block's share of the work list and copies whole pages
+// into a ring, K and V by one copy and their scales by another (a copy for each
+// side of each half page, 4608 bytes by four of them, left the ring empty: 448 us
+// for the decode step below); each other warp takes every W-th 16 KB of elements, a
+// chunk, with a softmax and an output of its own, and they join at the item's end.  The running
 // reference of a row moves, and its output is rescaled, when the maximum rises by
 // more than 2^6 (p stays below 2^14).
 template <int D_, int RP_>
 struct FewCfg {
   static constexpr int D = D_, RP = RP_, NT = RP / 8;
   static constexpr int kKeys = 4096 / D;                  // of a chunk
-  static constexpr int kCodes = kKeys * D / 2, kScales = kKeys * D / 16;
-  static constexpr int kStage = 2 * (kCodes + kScales);
+  static constexpr int kEach = kPage / kKeys;             // chunks of a page
+  static constexpr int kCodes = kPage * D / 2, kScales = kPage * D / 16;   // of a page's side
+  static constexpr int kStage = 2 * (kCodes + kScales);   // K, V, scales of K, of V
   static constexpr int kCtas = RP == 8 ? 2 : 1;
   static constexpr int kWarps = RP == 8 ? 7 : 11;         // that compute
   static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int kJoin = kWarps * RP * D * 4;
   static constexpr int kSmall = 3072;
   static constexpr int kRoom = kCtas == 2 ? 112 * 1024 : 227 * 1024;
-  static constexpr int kStages = (kRoom - kJoin - kSmall) / kStage < 32 ? (kRoom - kJoin - kSmall) / kStage : 32;
+  // Chunk c of a block lies in stage c / kEach mod kStages and is warp c mod
+  // kWarps's.  A warp that waits for the f-th fill of a stage must have seen the one
+  // before: copies end in any order, and a barrier tells only odd rounds from even
+  // ones.  So a part of a stage is always the same warp's.
+  static constexpr int kStep = kWarps % kEach == 0 ? kWarps / kEach : kWarps;
+  static constexpr int kStages = (kRoom - kJoin - kSmall) / kStage / kStep * kStep;
+  static_assert(kStages > 0 && kStages * kEach % kWarps == 0, "a part of a stage has one warp");
   static constexpr int kSmem = kStages * kStage + kJoin + kSmall;
   static constexpr int kCost = 3;                         // what an item takes beyond its tiles, in tiles
 };
 
 struct FewSmall {
-  uint64_t full[32], empty[32], item_full[4], item_empty[4], never;
+  uint64_t full[48], empty[48], item_full[4], item_empty[4], never;
   unsigned long long total;
   int dead;
-  int gone[32];               // of a stage: its page is not there
+  int gone[48];               // of a stage: its page is not there
   Gqa8Item items[4];
-  float top[11][16], sum[11][16];
+  float top[12][16], sum[12][16];
 };
-static_assert(sizeof(FewSmall) <= 3072, "FewSmall");
+static_assert(sizeof(FewSmall) <= 3072 && FewCfg<64, 16>::kStages <= 48 && FewCfg<128, 16>::kWarps <= 12, "FewSmall");
 
+// c = A B, c += A B.
+__device__ __forceinline__ void mma_16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -90,10 +108,10 @@ __device__ __forceinline__ uint32_t pair_even(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t pair_odd(uint32_t a, uint32_t b) {
   return ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
 }
-__device__ __forceinline__ void scaled8(uint32_t w, uint32_t s2, uint32_t (&h)[4]) {
+__device__ __forceinline__ void scaled8(uint32_t w, __half2 s, uint32_t (&h)[4]) {
   e2m1x8_to_f16x8(w, h);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = f16x2_mul(h[i], s2);
+  for (int i = 0; i < 4; ++i) h[i] = h2_bits(__hmul2(bits_h2(h[i]), s));
 }
 
 template <int D, int RP, bool F16>
@@ -110,7 +128,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(smem_addr(&sm.full[i]), 1);
-      mbar_init(smem_addr(&sm.empty[i]), 1);
+      mbar_init(smem_addr(&sm.empty[i]), C::kEach);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_addr(&sm.item_full[i]), 1);
@@ -146,24 +164,26 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
       }
     }
   };
-  // an item's chunks: of its first key on, up to its last
-  struct Chunks {
+  // an item's pages: of its first key on, up to its last
+  struct Pages {
     int first, n;
   };
-  auto chunks_of = [](const Gqa8Item& it) {
+  auto pages_of = [](const Gqa8Item& it) {
     const int64_t lo = max(static_cast<int64_t>(it.klo), static_cast<int64_t>(it.t_begin) * kTileKeys);
     const int64_t hi = min(static_cast<int64_t>(it.khi), static_cast<int64_t>(it.t_end) * kTileKeys);
-    Chunks c{static_cast<int>(lo / CK), 0};
-    if (hi > lo) c.n = static_cast<int>((hi - 1) / CK) + 1 - c.first;
-    return c;
+    Pages p{static_cast<int>(lo / kPage), 0};
+    if (hi > lo) p.n = static_cast<int>((hi - 1) / kPage) + 1 - p.first;
+    return p;
   };
 
   if (warp == 0) {
     // ==== work list and loads ====
-    uint32_t n_items = 0, n_chunks = 0, n_loads = 0;      // chunks; up to which copies began
+    uint32_t n_items = 0, n_pages = 0, n_loads = 0;       // pages; up to which lane 0 began copies
+    uint32_t stage = 0, empty_par = 1;                    // of the next page
     auto publish = [&](const Gqa8Item& it) {
       const int s = n_items & 3;
       wait(sm.item_empty[s], ((n_items >> 2) & 1) ^ 1);
+      __syncwarp();                                       // (no lane still looks for the round before)
       // (of a wait that gave up the item before may still be in use)
       if (lane == 0 && !*dead) {
         sm.items[s] = it;
@@ -171,42 +191,40 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
       }
       ++n_items;
     };
-    // lanes 0 .. 3 copy codes of K, of V, scales of K, of V
-    uint8_t* const base = lane & 2 ? const_cast<uint8_t*>(a.scales) : const_cast<uint8_t*>(a.pool);
-    const int row_bytes = lane & 2 ? D / 16 : D / 2;
-    const uint32_t bytes = lane & 2 ? C::kScales : C::kCodes;
-    const uint32_t dst0 = smem_addr(smem) + (lane & 2 ? 2 * C::kCodes : 0) + (lane & 1) * bytes;
     auto load_item = [&](const Gqa8Item& it) {
-      const Chunks c = chunks_of(it);
-      constexpr int kEach = kPage / CK;                   // chunks of a page
-      int page = 0, page0 = -32;
-      for (int i = 0; i < c.n; ++i, ++n_chunks) {
-        const int chunk = c.first + i, p = chunk / kEach;
-        if (p >= page0 + 32 || i == 0) {
-          page0 = p;
-          const int64_t at = static_cast<int64_t>(p) + lane;
-          page = at * kPage < it.khi && at < a.pt_stride ? load(a.page_table + it.b * a.pt_stride + at) : 0;
-          if (page < 0 || page >= a.num_pages) {
-            page = -1;
-            flag_error(a.dev_err, kDevBadPage);
+      const Pages c = pages_of(it);
+      int block = -1;                                     // (2 Hkv num_pages < 2^31)
+      for (int i = 0; i < c.n; ++i, ++n_pages) {
+        if ((i & 31) == 0) {
+          // a lane's page: its K and V, or -1 where the table has none
+          const int64_t at = static_cast<int64_t>(c.first) + i + lane;
+          block = -1;
+          if (at * kPage < it.khi) {
+            const int phys = load(a.page_table + it.b * a.pt_stride + at);
+            if (phys < 0 || phys >= a.num_pages) flag_error(a.dev_err, kDevBadPage);
+            else block = phys * a.Hkv + it.h;
           }
         }
-        const int phys = __shfl_sync(0xFFFFFFFFu, page, p - page0);
-        const int s = n_chunks % ST;
-        wait(sm.empty[s], ((n_chunks / ST) & 1) ^ 1);
-        const bool go = !__any_sync(0xFFFFFFFFu, *dead != 0);
-        if (lane == 0 && go) {
-          sm.gone[s] = phys < 0;
-          if (phys >= 0) mbar_arrive_expect_tx(smem_addr(&sm.full[s]), C::kStage);
-          else mbar_arrive(smem_addr(&sm.full[s]));
+        const int64_t blk = __shfl_sync(0xFFFFFFFFu, block, i & 31);
+        wait(sm.empty[stage], empty_par);
+        __syncwarp();
+        if (lane == 0 && !*dead) {
+          n_loads = n_pages + 1;
+          sm.gone[stage] = blk < 0;
+          const uint32_t bar = smem_addr(&sm.full[stage]), dst = smem_addr(smem) + stage * C::kStage;
+          if (blk >= 0) {
+            mbar_arrive_expect_tx(bar, C::kStage);
+            bulk_copy_g2s(dst, a.pool + blk * (2 * C::kCodes), 2 * C::kCodes, bar);
+            bulk_copy_g2s(dst + 2 * C::kCodes, a.scales + blk * (2 * C::kScales), 2 * C::kScales, bar);
+          } else {
+            mbar_arrive(bar);
+          }
         }
         __syncwarp();
-        if (go) n_loads = n_chunks + 1;
-        if (go && phys >= 0 && lane < 4) {
-          const int64_t row = ((static_cast<int64_t>(phys) * a.Hkv + it.h) * 2 + (lane & 1)) * kPage + chunk % kEach * CK;
-          bulk_copy_g2s(dst0 + s * C::kStage, base + row * row_bytes, bytes, smem_addr(&sm.full[s]));
+        if (++stage == ST) {
+          stage = 0;
+          empty_par ^= 1;
         }
-        __syncwarp();
       }
     };
     gqa8_walk(a, kind, static_cast<int64_t>(sm.total), tails, lane, [&](const Gqa8Item& it) {
@@ -215,7 +233,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
     });
     publish(Gqa8Item{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, -1});
     // every copy lands before the block's shared memory goes away
-    for (uint32_t i = n_chunks > ST ? n_chunks - ST : 0; i < n_chunks; ++i)
+    for (uint32_t i = n_pages > ST ? n_pages - ST : 0; i < n_pages; ++i)
       wait(sm.empty[i % ST], (i / ST) & 1);
     if (*dead && lane == 0)
       for (uint32_t i = n_loads > ST ? n_loads - ST : 0; i < n_loads; ++i)
@@ -227,7 +245,12 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
     // that a thread's four keys of V are t, t + 4, t + 8, t + 12, whose rows lie in
     // all banks
     const int key_r = (r8 >> 1) + (r8 & 1) * 4;
-    uint32_t n_chunks = 0;
+    // this warp's next chunk of the ring (of kEach * ST), and its rounds' parity
+    uint32_t slot = w, par = 0, turn = 0;                 // turn: chunks of the block so far, mod W
+    const uint8_t* const k_l = smem + key_r * (D / 2) + t4 * (D / 8);
+    const uint8_t* const ks_l = smem + 2 * C::kCodes + key_r * (D / 16) + t4 * (D / 64);
+    const uint8_t* const v_l = smem + C::kCodes + t4 * (D / 2) + r8 * (D / 16);
+    const uint8_t* const vs_l = smem + 2 * C::kCodes + C::kScales + t4 * (D / 16) + r8 * (D / 16) / 8;
     for (uint32_t n_items = 0;; ++n_items) {
       const int si = n_items & 3;
       wait(sm.item_full[si], (n_items >> 2) & 1);
@@ -238,7 +261,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[si]));
       if (it.b < 0) break;
-      const Chunks c = chunks_of(it);
+      const Pages c = pages_of(it);
 
       // q: row n of 8 is threads 4n .. 4n + 3's, D / 4 elements each
       uint32_t q[MD][NT][2];
@@ -279,13 +302,15 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
         }
       }
       const int pos_first = it.pos0 + it.r0 / G, pos_last = it.pos0 + (it.r0 + it.nrows - 1) / G;
-      float o[MD][NT][4], l[NT][2], mref[NT][2];
+      // p = 2^(s qf + ref), ref = 8 - (the reference); scores above `limit` raise it
+      float o[MD][NT][4], l[NT][2], ref[NT][2], limit[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           l[nt][i] = 0.0f;
-          mref[nt][i] = kLowest;
+          ref[nt][i] = -kLowest;
+          limit[nt][i] = -INFINITY;
         }
 #pragma unroll
         for (int i = 0; i < MD; ++i)
@@ -293,56 +318,62 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
           for (int k = 0; k < 4; ++k) o[i][nt][k] = 0.0f;
       }
 
-      // chunk i of the item is the block's chunk n_chunks + i: warp (that mod W)'s
-      for (int i = (w + W - static_cast<int>(n_chunks % W)) % W; i < c.n; i += W) {
-        const uint32_t n = n_chunks + i;
-        const int st = n % ST;
-        wait(sm.full[st], (n / ST) & 1);
-        const int64_t base = static_cast<int64_t>(c.first + i) * CK;
-        const uint8_t* const k_s = smem + st * C::kStage;
-        const uint8_t* const v_s = k_s + C::kCodes;
-        const uint8_t* const ks_s = k_s + 2 * C::kCodes;
-        const uint8_t* const vs_s = ks_s + C::kScales;
+      // chunks before `open` or from `full` on have keys that some row does not see
+      const int64_t last_whole = min(static_cast<int64_t>(it.khi), static_cast<int64_t>(pos_first) + 1) - CK;
+      const int full = static_cast<int>(max(last_whole, static_cast<int64_t>(-1)));
+      const int open = a.window > 0 ? max(it.klo, static_cast<int>(max(static_cast<int64_t>(pos_last) - a.window + 1, static_cast<int64_t>(0)))) : it.klo;
+      // chunk i of the item: warp ((i + the block's chunks before it) mod W)'s
+      for (int i = static_cast<int>((w + W - turn) % W); i < c.n * C::kEach; i += W) {
+        const uint32_t st = slot / C::kEach, part = slot % C::kEach;
+        wait(sm.full[st], par);
+        __syncwarp();
+        slot += W;
+        if (slot >= ST * C::kEach) {
+          slot -= ST * C::kEach;
+          par ^= 1;
+        }
+        const int base = c.first * kPage + i * CK;        // (below khi)
         if (!sm.gone[st]) {
-          const bool edge = base + CK > min(it.khi, pos_first + 1) || base < it.klo ||
-                            (a.window > 0 && base <= static_cast<int64_t>(pos_last) - a.window);
+          const bool edge = base > full || base < open;
+          const uint32_t at = st * C::kStage + part * (CK * D / 2), at_s = st * C::kStage + part * (CK * D / 16);
           float s[MK][NT][4];
+          alignas(16) uint32_t kw[MK][2][D / 32];         // codes of keys r and r + 8
+          uint32_t ks[MK][2];                             // scales of their blocks
+#pragma unroll
+          for (int mk = 0; mk < MK; ++mk)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int row = mk * 16 + 8 * j;
+              if constexpr (D == 128) {
+                *reinterpret_cast<uint4*>(kw[mk][j]) = *reinterpret_cast<const uint4*>(k_l + at + row * 64);
+                ks[mk][j] = *reinterpret_cast<const uint16_t*>(ks_l + at_s + row * 8);
+              } else {
+                *reinterpret_cast<uint2*>(kw[mk][j]) = *reinterpret_cast<const uint2*>(k_l + at + row * 32);
+                ks[mk][j] = ks_l[at_s + row * 4];
+              }
+            }
 #pragma unroll
           for (int mk = 0; mk < MK; ++mk) {
+            ks[mk][0] = e4m3x2_to_f16x2(ks[mk][0]);
+            ks[mk][1] = e4m3x2_to_f16x2(ks[mk][1]);
+          }
+          // (the key tiles in turns: each is a chain of products)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+          for (int x = 0; x < D / 32; ++x)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) s[mk][nt][k] = 0.0f;
-            const int row0 = mk * 16 + key_r;
-            uint32_t w0[D / 32], w1[D / 32], s0, s1;      // codes of keys r and r + 8, scales of their blocks
-            if constexpr (D == 128) {
-              *reinterpret_cast<uint4*>(w0) = *reinterpret_cast<const uint4*>(k_s + row0 * 64 + t4 * 16);
-              *reinterpret_cast<uint4*>(w1) = *reinterpret_cast<const uint4*>(k_s + (row0 + 8) * 64 + t4 * 16);
-              s0 = *reinterpret_cast<const uint16_t*>(ks_s + row0 * 8 + t4 * 2);
-              s1 = *reinterpret_cast<const uint16_t*>(ks_s + (row0 + 8) * 8 + t4 * 2);
-            } else {
-              *reinterpret_cast<uint2*>(w0) = *reinterpret_cast<const uint2*>(k_s + row0 * 32 + t4 * 8);
-              *reinterpret_cast<uint2*>(w1) = *reinterpret_cast<const uint2*>(k_s + (row0 + 8) * 32 + t4 * 8);
-              s0 = ks_s[row0 * 4 + t4];
-              s1 = ks_s[(row0 + 8) * 4 + t4];
-            }
-            s0 = e4m3x2_to_f16x2(s0);
-            s1 = e4m3x2_to_f16x2(s1);
-#pragma unroll
-            for (int x = 0; x < D / 32; ++x) {
+            for (int mk = 0; mk < MK; ++mk) {
               // (two words a block of 16)
-              const uint32_t f0 = __byte_perm(s0, 0, x / 2 == 0 ? 0x1010 : 0x3232);
-              const uint32_t f1 = __byte_perm(s1, 0, x / 2 == 0 ? 0x1010 : 0x3232);
               uint32_t h0[4], h1[4];
-              scaled8(w0[x], f0, h0);
-              scaled8(w1[x], f1, h1);
+              auto scale = [&](uint32_t two) { return x < 2 ? __low2half2(bits_h2(two)) : __high2half2(bits_h2(two)); };
+              scaled8(kw[mk][0][x], scale(ks[mk][0]), h0);
+              scaled8(kw[mk][1][x], scale(ks[mk][1]), h1);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                mma_16816(s[mk][nt], h0[0], h1[0], h0[1], h1[1], q[2 * x][nt][0], q[2 * x][nt][1]);
+                if (x == 0) mma_16816_first(s[mk][nt], h0[0], h1[0], h0[1], h1[1], q[0][nt][0], q[0][nt][1]);
+                else mma_16816(s[mk][nt], h0[0], h1[0], h0[1], h1[1], q[2 * x][nt][0], q[2 * x][nt][1]);
                 mma_16816(s[mk][nt], h0[2], h1[2], h0[3], h1[3], q[2 * x + 1][nt][0], q[2 * x + 1][nt][1]);
               }
             }
-          }
           if (edge) {
             // 0 <= position - key < window, of the keys that are there
             const uint32_t win = a.window > 0 ? a.window : 0x80000000u;
@@ -350,33 +381,36 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
             for (int mk = 0; mk < MK; ++mk)
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const int key = static_cast<int>(base) + mk * 16 + key_r + (k & 2) * 4;
+                const int key = base + mk * 16 + key_r + (k & 2) * 4;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                   if (!(static_cast<uint32_t>(pos[nt][k & 1] - key) < win && key < it.khi)) s[mk][nt][k] = -INFINITY;
               }
           }
+          // Each thread looks at its own scores; only where one rises too far is
+          // a maximum taken over the row's threads.
           float mx[NT][2];
           bool rise = false;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              float m = fmaxf(s[0][nt][k], s[0][nt][k + 2]);
+              mx[nt][k] = fmaxf(s[0][nt][k], s[0][nt][k + 2]);
 #pragma unroll
-              for (int mk = 1; mk < MK; ++mk) m = max3(m, s[mk][nt][k], s[mk][nt][k + 2]);
-#pragma unroll
-              for (int off = 4; off < 32; off *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
-              mx[nt][k] = m * qf[nt][k];
-              rise |= mx[nt][k] > mref[nt][k] + 6.0f;
+              for (int mk = 1; mk < MK; ++mk) mx[nt][k] = max3(mx[nt][k], s[mk][nt][k], s[mk][nt][k + 2]);
+              rise |= mx[nt][k] > limit[nt][k];
             }
           if (__any_sync(0xFFFFFFFFu, rise)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const float to = fmaxf(mref[nt][k], mx[nt][k]), by = fast_exp2(mref[nt][k] - to);
-                mref[nt][k] = to;
+                float m = mx[nt][k];
+#pragma unroll
+                for (int off = 4; off < 32; off *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+                const float to = fminf(ref[nt][k], 8.0f - m * qf[nt][k]), by = fast_exp2(to - ref[nt][k]);
+                ref[nt][k] = to;
+                limit[nt][k] = to == -kLowest ? -INFINITY : (14.0f - to) / qf[nt][k];
                 l[nt][k] *= by;
 #pragma unroll
                 for (int x = 0; x < MD; ++x) {
@@ -388,13 +422,12 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
           uint32_t p[MK][NT][2];                          // P^T: keys 2t, 2t + 1 and 8 more, row lane / 4
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const float b0 = 8.0f - mref[nt][0], b1 = 8.0f - mref[nt][1];
 #pragma unroll
             for (int mk = 0; mk < MK; ++mk)
 #pragma unroll
               for (int k = 0; k < 4; k += 2) {
-                const float p0 = fast_exp2(fmaf(s[mk][nt][k], qf[nt][0], b0));
-                const float p1 = fast_exp2(fmaf(s[mk][nt][k + 1], qf[nt][1], b1));
+                const float p0 = fast_exp2(fmaf(s[mk][nt][k], qf[nt][0], ref[nt][0]));
+                const float p1 = fast_exp2(fmaf(s[mk][nt][k + 1], qf[nt][1], ref[nt][1]));
                 l[nt][0] += p0;
                 l[nt][1] += p1;
                 p[mk][nt][k / 2] = transpose8x8(h2_bits(__floats2half2_rn(p0, p1)));
@@ -402,22 +435,19 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
           }
 #pragma unroll
           for (int mk = 0; mk < MK; ++mk) {
-            uint32_t v[4][D / 64], sc[4];
+            alignas(8) uint32_t v[4][D / 64];
+            uint32_t sc[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const int row = mk * 16 + t4 + 4 * k;
-              if constexpr (D == 128) {
-                *reinterpret_cast<uint2*>(v[k]) = *reinterpret_cast<const uint2*>(v_s + row * 64 + r8 * 8);
-                sc[k] = vs_s[row * 8 + r8];
-              } else {
-                v[k][0] = *reinterpret_cast<const uint32_t*>(v_s + row * 32 + r8 * 4);
-                sc[k] = vs_s[row * 4 + (r8 >> 1)];
-              }
+              const int row = mk * 16 + 4 * k;
+              if constexpr (D == 128) *reinterpret_cast<uint2*>(v[k]) = *reinterpret_cast<const uint2*>(v_l + at + row * 64);
+              else v[k][0] = *reinterpret_cast<const uint32_t*>(v_l + at + row * 32);
+              sc[k] = vs_l[at_s + row * (D / 16)];
               // a key that no row sees may hold a NaN scale, which a weight of zero
               // would not silence
-              if (edge) sc[k] = base + row >= it.klo && base + row < it.khi ? sc[k] : 0u;
+              if (edge) sc[k] = base + row + t4 >= it.klo && base + row + t4 < it.khi ? sc[k] : 0u;
             }
-            const uint32_t s01 = e4m3x2_to_f16x2(sc[0] | (sc[1] << 8)), s23 = e4m3x2_to_f16x2(sc[2] | (sc[3] << 8));
+            const __half2 s01 = bits_h2(e4m3x2_to_f16x2(sc[0] + sc[1] * 256)), s23 = bits_h2(e4m3x2_to_f16x2(sc[2] + sc[3] * 256));
 #pragma unroll
             for (int x = 0; x < D / 64; ++x) {
               uint32_t e01[4], o01[4], e23[4], o23[4];
@@ -436,7 +466,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.empty[st]));
       }
-      n_chunks += c.n;
+      turn = (turn + c.n * C::kEach) % W;
 
       // ---- the warps' outputs, joined relative to the largest reference ----
       // (behind this barrier all have read what the item before left here)
@@ -450,7 +480,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
           for (int off = 4; off < 32; off *= 2) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
           const int row = nt * 8 + 2 * t4 + k;
           if (r8 == 0) {
-            sm.top[w][row] = mref[nt][k];
+            sm.top[w][row] = -ref[nt][k];
             sm.sum[w][row] = odd_col[nt][k] && x > 0.0f ? __uint_as_float(0x7FC00000u) : x;
           }
           // d = 2 MD lane / 4 + 2 i and the next
@@ -477,7 +507,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
           y[3] = fmaf(v.w, f, y[3]);
         }
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        const float ls = sum == 0.0f ? -INFINITY : top - 8.0f + log2f(sum);
+        const float ls = sum == 0.0f ? -INFINITY : top + log2f(sum);
         if (it.slot >= 0) {
           const int64_t at = static_cast<int64_t>(it.slot) * RP + row;
           *reinterpret_cast<float4*>(ws_o + at * D + d) = make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
@@ -496,92 +526,701 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
   __syncthreads();
 }
 
-// The plain kernel: a block for each row, a key for each warp at a time, D / 32
-// elements a lane.
+// ---------------------------------------------------------------------------
+// Many rows: prompt chunks
+// ---------------------------------------------------------------------------
+// What bounds this case is the tensor core: 4 D flops a pair of row and key.
+// An item is 256 rows of one kv head, two M = 128 tiles that take turns: while
+// the softmax of one works on its scores, the products of the other run.  Of an
+// item with at most 128 rows the two are the same rows over every other tile of
+// keys, joined at its end, so that they take turns all the same.
+//   S[128 rows x 128 keys] = Q . K^T     kind::f16, both from shared memory
+//   O[128 rows x D] += P . V             kind::f16, P from TMEM
+// K and V are widened to f16 once per tile by two warps (exact: code * scale has 6
+// significant bits), from codes that bulk copies bring, a side of a page at a time;
+// q is exact in f16 but for elements below 2^-22 of its row's largest.  The chain
+// scores -> softmax -> P -> O, next scores of a row tile is what the other tile's
+// products have to cover, so two threads share a row, one for each page of the
+// tile (64 keys).  A row's reference only moves, and its O in TMEM is only
+// rescaled, when the maximum rises by more than 2^6 (p stays below 2^14, f16's top
+// is 2^16).
+template <int D_>
+struct ManyCfg {
+  static constexpr int D = D_, kRows = 256;
+  static constexpr int kTile = kTileKeys * D * 2;         // of K, of V, or of 128 rows of q in f16
+  static constexpr int kCodes = kPage * D / 2, kScales = kPage * D / 16, kSide = kCodes + kScales;
+  static constexpr int kSmall = 9216;
+  static constexpr int kRoom = 227 * 1024 - 1024 - 6 * kTile - kSmall;
+  static constexpr int kRaw = kRoom / kSide < 16 ? kRoom / kSide : 16;     // sides of pages on their way
+  static constexpr int kSmem = 6 * kTile + kRaw * kSide + kSmall + 1024;
+};
+static_assert(ManyCfg<128>::kRaw >= 4, "a tile's sides are in the ring together");
+constexpr int kManyThreads = 640;
+constexpr uint32_t kSoftmaxRegs = 104, kOtherRegs = 64, kLaunchRegs = 96;
+static_assert(4 * kSoftmaxRegs + kOtherRegs <= 5 * kLaunchRegs, "register shares draw on the launch's");
+
+// What an item takes beyond its tiles (q in, first scores, last product, output),
+// in half tiles; of an item of at most 128 rows.
+constexpr int kManyCost = 10, kSharedCost = 4;
+
+struct ManySmall {
+  uint64_t raw_full[16], raw_empty[16], k_full[2], k_empty[2], v_full[2], v_empty[2], item_full[2], item_empty[2],
+      gone_full[8], q_full[2], s_full[2], p_full[2][2], o_full[2], never;
+  unsigned long long total;
+  uint32_t tmem;
+  int dead;
+  int gone[8][2];             // per tile and page: not there
+  Gqa8Item items[2];
+  float qf[2][128];           // sm_scale log2(e) 2^eq of a row, NaN where q is not finite
+  float top[2][2][2][128];    // largest score of a half row, by row tile and tile parity
+  float last[2][3][128];      // at an item's end: sums of both halves, reference
+};
+static_assert(sizeof(ManySmall) <= 9216, "ManySmall");
+
 template <int D, bool F16>
-__global__ void __launch_bounds__(128) row_kernel(const Gqa8AttnArgs a, const int min_rows) {
-  constexpr int E = D / 32;
+__global__ void __launch_bounds__(kManyThreads, 1)
+many4_kernel(const Gqa8AttnArgs a, const int min_rows,
+            Gqa8Tail* tails, float* ws_lse, float* ws_o) {
+  using C = ManyCfg<D>;
+  constexpr int NR = C::kRaw;
+  constexpr int kSlab = kTileKeys * 128;                  // 64 f16 columns of an operand
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* const q_s = smem;
+  uint8_t* const k_s = q_s + 2 * C::kTile;
+  uint8_t* const v_s = k_s + 2 * C::kTile;
+  uint8_t* const raw_s = v_s + 2 * C::kTile;
+  ManySmall& sm = *reinterpret_cast<ManySmall*>(raw_s + NR * C::kSide);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.Hq / a.Hkv;
+  constexpr int kAll = 0x7FFFFFFF;
+
+  if (tid == 0) {
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(smem_addr(&sm.raw_full[i]), 1);
+      mbar_init(smem_addr(&sm.raw_empty[i]), 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sm.k_full[i]), 2);
+      mbar_init(smem_addr(&sm.k_empty[i]), 1);
+      mbar_init(smem_addr(&sm.v_full[i]), 2);
+      mbar_init(smem_addr(&sm.v_empty[i]), 1);
+      mbar_init(smem_addr(&sm.item_full[i]), 1);
+      mbar_init(smem_addr(&sm.item_empty[i]), 19);        // the product's lane, 2 + 16 warps
+      mbar_init(smem_addr(&sm.q_full[i]), 8);
+      mbar_init(smem_addr(&sm.s_full[i]), 1);
+      mbar_init(smem_addr(&sm.p_full[i][0]), 8);
+      mbar_init(smem_addr(&sm.p_full[i][1]), 8);
+      mbar_init(smem_addr(&sm.o_full[i]), 1);
+    }
+    for (int i = 0; i < 8; ++i) mbar_init(smem_addr(&sm.gone_full[i]), 1);
+    mbar_init(smem_addr(&sm.never), 1);
+    sm.total = 0;
+    sm.dead = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(smem_addr(&sm.tmem), 512);
   grid_dependency_wait();
   grid_launch_dependents();
-  __shared__ float part_o[4][D], part_m[4], part_l[4];
-  const int t = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = a.Hq / a.Hkv, hk = h / G;
-  int b = 0;
-  for (; b < a.B; ++b)
-    if (load(a.cu + b) <= t && t < load(a.cu + b + 1)) break;
-  if (b == a.B) return;
-  const Gqa8Request r = gqa8_request(a, b, min_rows, 0x7FFFFFFF, min_rows == 1 && h == 0 && t == min(max(load(a.cu + b), 0), static_cast<int>(a.n_tokens)));
-  if (r.n == 0) return;
-  const int pos = r.pos0 + (t - r.cu0);
-  const int lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0, hi = min(pos + 1, r.held);
-  const uint16_t* q = static_cast<const uint16_t*>(a.q) + t * a.q_token_stride + h * a.q_head_stride + lane * E;
-  float x[E], o[E];
-  bool odd = false;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    x[e] = F16 ? __half2float(__ushort_as_half(load(q + e))) : __uint_as_float(static_cast<uint32_t>(load(q + e)) << 16);
-    odd |= !isfinite(x[e]);
-    o[e] = 0.0f;
-  }
-  odd = __any_sync(0xFFFFFFFFu, odd);
-  float m = -INFINITY, l = 0.0f;
-  for (int64_t j = lo + warp; j < hi; j += 4) {
-    const int pg = load(a.page_table + b * a.pt_stride + (j >> 6));
-    if (pg < 0 || pg >= a.num_pages) {
-      if (lane == 0) flag_error(a.dev_err, kDevBadPage);
-      continue;
-    }
-    auto values = [&](int side, float (&v)[E]) {
-      const int64_t row = ((static_cast<int64_t>(pg) * a.Hkv + hk) * 2 + side) * kPage + (j & 63);
-      const float s = e4m3_to_float(load(a.scales + row * (D / 16) + lane * E / 16));
-      uint32_t w = 0;
-      for (int i = 0; i < E / 2; ++i) w |= static_cast<uint32_t>(load(a.pool + row * (D / 2) + lane * (E / 2) + i)) << (8 * i);
-      uint32_t f[4];
-      e2m1x8_to_f16x8(w, f);
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) {
-        const float2 p = __half22float2(bits_h2(f[i]));
-        v[2 * i] = p.x * s;
-        v[2 * i + 1] = p.y * s;
-      }
-    };
-    float k[E], v[E];
-    values(0, k);
-    values(1, v);
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(x[e], k[e], s);
-    s = warp_sum(s) * a.sm_scale;
-    const float to = fmaxf(m, s), by = expf(m - to), p = expf(s - to);
-    m = to;
-    l = l * by + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * by + p * v[e];
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) part_o[warp][lane * E + e] = o[e];
-  if (lane == 0) {
-    part_m[warp] = m;
-    part_l[warp] = l;
-  }
   __syncthreads();
-  const float top = fmaxf(fmaxf(part_m[0], part_m[1]), fmaxf(part_m[2], part_m[3]));
-  float sum = 0.0f, w[4];
-  for (int i = 0; i < 4; ++i) {
-    w[i] = part_l[i] > 0.0f ? expf(part_m[i] - top) : 0.0f;
-    sum += part_l[i] * w[i];
+  const Gqa8Kind kind{min_rows, kAll, C::kRows, kManyCost, 128, kSharedCost, 2};
+  gqa8_total(a, kind, blockIdx.x == 0 && min_rows == 1, &sm.total);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = sm.tmem;                          // S/P of the row tiles, then O
+  volatile int* dead = &sm.dead;
+  auto wait = [&](uint64_t& bar, uint32_t parity) {
+    if (mbar_try_wait(smem_addr(&bar), parity)) return;
+    if (*dead) return;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait_suspend(smem_addr(&bar), parity, 20000u)) {
+      if (*dead) return;
+      if (global_timer_ns() - t0 > a.timeout_ns) {
+        *dead = 1;
+        flag_error(a.dev_err, kDevTimeout);
+        return;
+      }
+    }
+  };
+
+  if (warp < 4) {
+    setmaxnreg_dec<kOtherRegs>();
+    if (warp == 0) {
+      // ==== work list and loads ====
+      uint32_t n_items = 0, n_tiles = 0;
+      uint32_t n_sides = 0, n_loads = 0;                  // sides of pages; up to which lane 0 began copies
+      uint32_t st = 0, st_par = 1;                        // of the next side
+      auto publish = [&](const Gqa8Item& it) {
+        const int s = n_items & 1;
+        wait(sm.item_empty[s], ((n_items >> 1) & 1) ^ 1);
+        __syncwarp();                                     // (no lane still looks for the round before)
+        // (of a wait that gave up the item before may still be in use)
+        if (lane == 0 && !*dead) {
+          sm.items[s] = it;
+          mbar_arrive(smem_addr(&sm.item_full[s]));
+        }
+        ++n_items;
+      };
+      auto load_item = [&](const Gqa8Item& it) {
+        for (int t = it.t_begin; t < it.t_end; t += 16) {
+          // page `lane` of 16 tiles: its K and V, or -1 where no key of it is seen
+          // or the table has none
+          const int64_t page = 2 * static_cast<int64_t>(t) + lane;
+          int block = -1;
+          if ((page >> 1) < it.t_end && (page << 6) < it.khi && (page << 6) + 64 > it.klo) {
+            const int phys = load(a.page_table + it.b * a.pt_stride + page);
+            if (phys < 0 || phys >= a.num_pages) flag_error(a.dev_err, kDevBadPage);
+            else block = phys * a.Hkv + it.h;             // (2 Hkv num_pages < 2^31)
+          }
+          const int nt = min(16, it.t_end - t);
+          for (int i = 0; i < nt; ++i, ++n_tiles) {
+            const int b[2] = {__shfl_sync(0xFFFFFFFFu, block, 2 * i), __shfl_sync(0xFFFFFFFFu, block, 2 * i + 1)};
+#pragma unroll
+            for (int side = 0; side < 4; ++side) {        // K of both pages, then V
+              wait(sm.raw_empty[st], st_par);
+              __syncwarp();
+              if (lane == 0 && !*dead) {
+                n_loads = n_sides + 1;
+                if (side == 0) {
+                  // (the softmax of the tile eight before is done: the widening
+                  // warps, whose side this stage waited for, are at most two tiles
+                  // ahead of the products, and those two ahead of it)
+                  sm.gone[n_tiles & 7][0] = b[0] < 0;
+                  sm.gone[n_tiles & 7][1] = b[1] < 0;
+                  mbar_arrive(smem_addr(&sm.gone_full[n_tiles & 7]));
+                }
+                const uint32_t bar = smem_addr(&sm.raw_full[st]), dst = smem_addr(raw_s) + st * C::kSide;
+                const int64_t blk = 2 * static_cast<int64_t>(b[side & 1]) + (side >> 1);
+                if (blk >= 0) {
+                  mbar_arrive_expect_tx(bar, C::kSide);
+                  bulk_copy_g2s(dst, a.pool + blk * C::kCodes, C::kCodes, bar);
+                  bulk_copy_g2s(dst + C::kCodes, a.scales + blk * C::kScales, C::kScales, bar);
+                } else {
+                  mbar_arrive(bar);
+                }
+              }
+              __syncwarp();
+              ++n_sides;
+              if (++st == NR) {
+                st = 0;
+                st_par ^= 1;
+              }
+            }
+          }
+        }
+      };
+      gqa8_walk(a, kind, static_cast<int64_t>(sm.total), tails, lane, [&](const Gqa8Item& it) {
+        publish(it);
+        load_item(it);
+      });
+      publish(Gqa8Item{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, -1});
+      // every copy and every signal lands before the block's shared memory goes away
+      for (uint32_t i = n_sides > NR ? n_sides - NR : 0; i < n_sides; ++i)
+        wait(sm.raw_empty[i % NR], (i / NR) & 1);
+      for (uint32_t i = n_tiles > 2 ? n_tiles - 2 : 0; i < n_tiles; ++i) {
+        wait(sm.k_empty[i & 1], (i >> 1) & 1);
+        wait(sm.v_empty[i & 1], (i >> 1) & 1);
+      }
+      if (*dead && lane == 0)
+        for (uint32_t i = n_loads > NR ? n_loads - NR : 0; i < n_loads; ++i)
+          mbar_wait_bounded(smem_addr(&sm.raw_full[i % NR]), (i / NR) & 1, 1000000);
+    } else if (warp == 1) {
+      // ==== products (the whole warp; one lane issues) ====
+      constexpr uint32_t idesc_qk = idesc_f16(128, 128, false, false);
+      constexpr uint32_t idesc_pv = idesc_f16(128, D, false, true);
+      const uint64_t dk0 = smem_desc(smem_addr(k_s), 16, 1024, kSwizzle128), dq0 = smem_desc(smem_addr(q_s), 16, 1024, kSwizzle128);
+      const uint64_t dv0 = smem_desc(smem_addr(v_s), kSlab, 1024, kSwizzle128);
+      uint32_t n_tiles = 0, ks = 0, k_par = 0;            // stage of K and its parity
+      uint32_t w0 = 0, w1 = 0, p0 = 0, p1 = 0;            // parities of the row tiles' q and P
+      // The queue of products is a few instructions deep, so what keeps this
+      // warp between two groups of them has to be short: waits come where a group
+      // has just been queued, and a group ends with all its signals.
+      auto qk = [&](int qt, uint32_t stage, int q) {                   // of the elected lane
+        const uint64_t dk = dk0 + stage * (C::kTile >> 4), dq = dq0 + q * (C::kTile >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t at = (k / 4 * kSlab + k % 4 * 32) >> 4;
+          mma_f16kind(tmem + qt * 128, dq + at, dk + at, idesc_qk, k > 0);
+        }
+        mma_commit(smem_addr(&sm.s_full[qt]));
+      };
+      // PV of tile j, then, with the last products, `more` (P of each page lies
+      // over its own half of S; it comes in two parts, the first 32 keys of both
+      // pages and the others, so that the first products overlap the rest of
+      // the softmax)
+      auto pv = [&](int qt, uint32_t j, bool first, uint32_t& par, auto&& more) {
+        const uint64_t dv = dv0 + (j & 1) * (C::kTile >> 4);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          wait(sm.p_full[qt][part], par);
+          __syncwarp();
+          tc_fence_after_sync();
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int k = 2 * part + (i & 1) + 4 * (i >> 1);       // 16 keys
+              mma_f16_ts(tmem + 256 + qt * 128, tmem + qt * 128 + 64 * (k >> 2) + 8 * (k & 3),
+                         dv + ((k * 2048) >> 4), idesc_pv, !first || part + i > 0);
+            }
+            if (part == 1) more();
+          }
+          __syncwarp();
+        }
+        par ^= 1;
+      };
+      for (uint32_t n_items = 0;; ++n_items) {
+        const int s = n_items & 1;
+        wait(sm.item_full[s], (n_items >> 1) & 1);
+        if (__any_sync(0xFFFFFFFFu, *dead != 0)) break;
+        const int b = __shfl_sync(0xFFFFFFFFu, sm.items[s].b, 0);
+        const int nt = __shfl_sync(0xFFFFFFFFu, sm.items[s].t_end - sm.items[s].t_begin, 0);
+        const bool two = __shfl_sync(0xFFFFFFFFu, sm.items[s].nrows, 0) > 128;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
+        if (b < 0) break;
+        if (nt == 0) continue;
+        wait(sm.q_full[0], w0);
+        w0 ^= 1;
+        if (two) {
+          wait(sm.q_full[1], w1);
+          w1 ^= 1;
+        }
+        auto next_k = [&] {
+          ks ^= 1;
+          if (ks == 0) k_par ^= 1;
+        };
+        // (P of a row tile lies over its S: the products run in order)
+        wait(sm.k_full[ks], k_par);
+        __syncwarp();
+        tc_fence_after_sync();
+        if (two) {
+          if (elect_one()) {
+            qk(0, ks, 0);
+            qk(1, ks, 1);
+            mma_commit(smem_addr(&sm.k_empty[ks]));
+          }
+          __syncwarp();
+          for (int t = 0; t < nt; ++t) {
+            const uint32_t j = n_tiles + t;
+            const bool next = t + 1 < nt;
+            wait(sm.v_full[j & 1], (j >> 1) & 1);
+            next_k();
+            if (next) wait(sm.k_full[ks], k_par);
+            pv(0, j, t == 0, p0, [&] {
+              if (next) qk(0, ks, 0);
+              else mma_commit(smem_addr(&sm.o_full[0]));
+            });
+            pv(1, j, t == 0, p1, [&] {
+              if (next) {
+                qk(1, ks, 1);
+                mma_commit(smem_addr(&sm.k_empty[ks]));
+              } else {
+                mma_commit(smem_addr(&sm.o_full[1]));
+              }
+              mma_commit(smem_addr(&sm.v_empty[j & 1]));
+            });
+          }
+        } else {
+          // tile t is row tile t & 1's
+          if (elect_one()) {
+            qk(0, ks, 0);
+            mma_commit(smem_addr(&sm.k_empty[ks]));
+          }
+          __syncwarp();
+          next_k();
+          if (nt > 1) {
+            wait(sm.k_full[ks], k_par);
+            __syncwarp();
+            tc_fence_after_sync();
+            if (elect_one()) {
+              qk(1, ks, 0);
+              mma_commit(smem_addr(&sm.k_empty[ks]));
+            }
+            __syncwarp();
+            next_k();
+          }
+          for (int t = 0; t < nt; ++t) {
+            const uint32_t j = n_tiles + t;
+            const bool next = t + 2 < nt;
+            wait(sm.v_full[j & 1], (j >> 1) & 1);
+            if (next) wait(sm.k_full[ks], k_par);
+            auto more = [&](int qt) {
+              if (next) {
+                qk(qt, ks, 0);
+                mma_commit(smem_addr(&sm.k_empty[ks]));
+              } else {
+                mma_commit(smem_addr(&sm.o_full[qt]));
+              }
+              mma_commit(smem_addr(&sm.v_empty[j & 1]));
+            };
+            if (t & 1) pv(1, j, t == 1, p1, [&] { more(1); });
+            else pv(0, j, t == 0, p0, [&] { more(0); });
+            if (next) next_k();
+          }
+        }
+        n_tiles += nt;
+        if (a.fault_site == 1) wait(sm.never, 0);
+      }
+      if (a.fault_site == 1) wait(sm.never, 0);
+      // in a block that gave up nothing else waits for the products that are
+      // still queued: they end before its memory goes away
+      __syncwarp();
+      if (__any_sync(0xFFFFFFFFu, *dead != 0)) {
+        if (elect_one()) mma_commit(smem_addr(&sm.never));
+        __syncwarp();
+        mbar_wait_bounded(smem_addr(&sm.never), 0, 1000000);
+      }
+    } else {
+      // ==== K and V to f16: a thread is a key of a page ====
+      uint32_t j = 0, st = 0, st_par = 0;
+      for (uint32_t n_items = 0;; ++n_items) {
+        const int s = n_items & 1;
+        wait(sm.item_full[s], (n_items >> 1) & 1);
+        if (__any_sync(0xFFFFFFFFu, *dead != 0)) break;
+        const Gqa8Item item = sm.items[s];
+        const int b = item.b, t0 = item.t_begin, t1 = item.t_end;
+        const int klo = item.klo, khi = item.khi;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
+        if (b < 0) break;
+        // the item's rows of q into L2, while the one before is worked on
+        {
+          const int cu0 = item.cu0, h = item.h, r0 = item.r0, nrows = item.nrows;
+          for (int rr = tid - 64; rr < nrows; rr += 64) {
+            const uint16_t* row = static_cast<const uint16_t*>(a.q) +
+                                  static_cast<int64_t>(cu0 + (r0 + rr) / G) * a.q_token_stride +
+                                  static_cast<int64_t>(h * G + (r0 + rr) % G) * a.q_head_stride;
+            prefetch_l2_line(row);
+            if (D == 128) prefetch_l2_line(row + 64);
+          }
+        }
+        const int key = tid - 64;                         // of a page
+        for (int t = t0; t < t1; ++t, ++j) {
+#pragma unroll 1
+          for (int side = 0; side < 4; ++side) {          // K of both pages, then V
+            if (side == 0) wait(sm.k_empty[j & 1], ((j >> 1) & 1) ^ 1);
+            if (side == 2) wait(sm.v_empty[j & 1], ((j >> 1) & 1) ^ 1);
+            wait(sm.raw_full[st], st_par);
+            __syncwarp();
+            const int64_t at = static_cast<int64_t>(t) * kTileKeys + (side & 1) * kPage + key;
+            // a key that no row sees may hold a NaN scale, which a weight of zero
+            // would not silence
+            const bool live = at >= klo && at < khi && !sm.gone[j & 7][side & 1];
+            const uint8_t* const src = raw_s + st * C::kSide;
+            uint8_t* const dst = (side < 2 ? k_s : v_s) + (j & 1) * C::kTile + ((side & 1) * kPage + key) * 128;
+            uint64_t sc = 0;                              // the row's scales
+            if (live) {
+              if constexpr (D == 128) sc = *reinterpret_cast<const uint64_t*>(src + C::kCodes + key * 8);
+              else sc = *reinterpret_cast<const uint32_t*>(src + C::kCodes + key * 4);
+            }
+            // (32 elements at a time, a thread's pieces in an order of its own so
+            // that 8 rows' pieces lie in different banks)
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              const int p = D == 128 ? (c + (key >> 1)) & 3 : (c + (key >> 2)) & 1;
+              uint4 w = make_uint4(0, 0, 0, 0);
+              if (live) w = *reinterpret_cast<const uint4*>(src + key * (D / 2) + p * 16);
+              const __half2 s2 = bits_h2(e4m3x2_to_f16x2(static_cast<uint32_t>(sc >> (p * 16)) & 0xFFFFu));
+              uint8_t* const o = dst + (p / 2) * kSlab;
+              const int u0 = p % 2 * 4;
+              auto put = [&](int u, uint32_t x, __half2 f) {
+                uint32_t h[4];
+                scaled8(x, f, h);
+                *reinterpret_cast<uint4*>(o + ((u0 + u) ^ (key & 7)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+              };
+              put(0, w.x, __low2half2(s2));
+              put(1, w.y, __low2half2(s2));
+              put(2, w.z, __high2half2(s2));
+              put(3, w.w, __high2half2(s2));
+            }
+            if (side & 1) fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(smem_addr(&sm.raw_empty[st]));
+              if (side & 1) mbar_arrive(smem_addr(side == 1 ? &sm.k_full[j & 1] : &sm.v_full[j & 1]));
+            }
+            if (++st == NR) {
+              st = 0;
+              st_par ^= 1;
+            }
+          }
+        }
+      }
+    }
+  } else {
+    // ==== softmax: a thread is half a row, 64 keys of a tile ====
+    setmaxnreg_inc<kSoftmaxRegs>();
+    const int qt = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;
+    const int bar = 1 + qt * 4 + (warp & 3);              // the two warps of 32 rows
+    const int bar_rows = 9 + (warp & 3);                  // and those of the other row tile
+    const int wrow = (warp & 3) * 32, row = wrow + lane;  // of the row tile
+    const uint32_t lanes = static_cast<uint32_t>(wrow) << 16;
+    const uint32_t s_tm = tmem + qt * 128 + half * 64 + lanes;
+    const uint32_t o_tm = tmem + 256 + qt * 128 + half * (D / 2) + lanes;
+    uint8_t* const q_mine = q_s + qt * C::kTile;
+    uint32_t j = 0, n_mine = 0, n_work = 0;               // tiles of all items, of mine; items of mine
+    for (uint32_t n_items = 0;; ++n_items) {
+      const int s = n_items & 1;
+      wait(sm.item_full[s], (n_items >> 1) & 1);
+      if (named_sync_or(bar_rows, 128, *dead != 0)) break;     // (together, for they meet at barriers)
+      // (read again at its end, so that the loop over the tiles does not hold it)
+      const Gqa8Item it = sm.items[s];
+      if (it.b < 0) break;
+      const int nt = it.t_end - it.t_begin;
+      const bool shared = it.nrows <= 128;                // both row tiles are the same rows
+      const int base = shared ? 0 : qt * 128;
+      const bool mine = base + row < it.nrows;
+      // keys at < hi and >= lo are this row's (a row that is not there takes all,
+      // so that its warp needs no mask for it; its numbers go nowhere)
+      int hi = 0x7FFFFFFF, lo = 0;
+      if (mine) {
+        const int64_t pos = static_cast<int64_t>(it.pos0) + (it.r0 + base + row) / G;
+        hi = static_cast<int>(max(min(pos + 1, static_cast<int64_t>(it.khi)), static_cast<int64_t>(0)));
+        if (a.window > 0) lo = static_cast<int>(max(pos - a.window + 1, static_cast<int64_t>(0)));
+      }
+      if (nt > 0 && !(shared && qt == 1)) {
+        // 16 of the warp's rows of q (the other half's warp has the others) as f16,
+        // kTpr threads a row
+        constexpr int kTpr = D / 16, kRpp = 32 / kTpr;
+        const int part = lane % kTpr;
+        const float sign = a.sm_scale < 0.0f ? -1.0f : 1.0f;   // (so that the factor is positive)
+        auto fetch = [&](int p, uint4 (&w)[2]) {
+          const int rr = wrow + half * 16 + p * kRpp + lane / kTpr, gr = it.r0 + base + rr;
+          w[0] = w[1] = make_uint4(0, 0, 0, 0);
+          if (p * kRpp < 16 && base + rr < it.nrows) {
+            const uint4* g = reinterpret_cast<const uint4*>(
+                static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(it.cu0 + gr / G) * a.q_token_stride +
+                static_cast<int64_t>(it.h * G + gr % G) * a.q_head_stride + part * 16);
+            w[0] = load(g);
+            w[1] = load(g + 1);
+          }
+        };
+        // (a loop of little code, two fetches ahead: it runs once an item, so
+        // its instructions are as far away as its data)
+        uint4 w[2], w_next[2];
+        fetch(0, w);
+        fetch(1, w_next);
+#pragma unroll 1
+        for (int p = 0; p < 16 / kRpp; ++p) {
+          const int rr = wrow + half * 16 + p * kRpp + lane / kTpr;
+          float y[16];
+          uint32_t m = widen16<F16>(w, y);
+          w[0] = w_next[0];
+          w[1] = w_next[1];
+          fetch(p + 2, w_next);
+#pragma unroll
+          for (int off = 1; off < kTpr; off <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+          const int e = q_exponent(m);
+          const bool odd = m >= 0x7F800000u;              // a NaN or an infinity: NaN in its row
+          if (part == 0)
+            sm.qf[qt][rr] = odd ? __uint_as_float(0x7FC00000u) : fabsf(a.sm_scale) * 1.4426950408889634f * pow2f(e);
+          const float f = sign * pow2f(-e);
+          uint32_t o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = odd ? 0u : h2_bits(__floats2half2_rn(y[2 * i] * f, y[2 * i + 1] * f));
+          uint8_t* const to = q_mine + (part / 4) * kSlab + rr * 128;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<uint4*>(to + ((part % 4 * 2 + i) ^ (rr & 7)) * 16) =
+                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.q_full[qt]));
+      }
+      // qf is there for the warps that read it
+      if (shared) named_sync(bar_rows, 128);
+      else named_sync(bar, 64);
+      const float qf = nt > 0 ? sm.qf[shared ? 0 : qt][row] : 0.0f;
+      const bool odd = qf != qf;
+      // (at least 2^-126, so that a masked -inf stays one where the scale is 0)
+      const float f = odd ? 0x1p-126f : fmaxf(qf, 0x1p-126f);
+      float mref = kLowest, l = 0.0f;
+      // pages that begin before `full` and not before `open` are every row's whole
+      int full = hi - 63, open = lo;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        full = min(full, __shfl_xor_sync(0xFFFFFFFFu, full, off));
+        open = max(open, __shfl_xor_sync(0xFFFFFFFFu, open, off));
+      }
+      const int first = it.t_begin + (shared ? qt : 0), step = shared ? 2 : 1;
+      for (int t = first; t < it.t_end; t += step, ++n_mine) {
+        const uint32_t jt = j + (t - it.t_begin);
+        const int at = t * kTileKeys + half * 64;
+        wait(sm.gone_full[jt & 7], (jt >> 3) & 1);
+        const bool gone = sm.gone[jt & 7][half] != 0;
+        wait(sm.s_full[qt], n_mine & 1);
+        tc_fence_after_sync();
+        float x[64];
+        tmem_ld32(s_tm, reinterpret_cast<uint32_t(&)[32]>(x[0]));
+        tmem_ld32(s_tm + 32, reinterpret_cast<uint32_t(&)[32]>(x[32]));
+        float m[4];
+        tmem_wait_ld32(reinterpret_cast<uint32_t(&)[32]>(x[0]));
+        tmem_wait_ld32(reinterpret_cast<uint32_t(&)[32]>(x[32]));
+        if (at >= full || at < open || gone) {
+          // keys of this row in the page: [a0, a0 + n)
+          const int a0 = max(lo - at, 0), n = gone ? 0 : max(min(hi - at, 64) - a0, 0);
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            x[c] = static_cast<unsigned>(c - a0) < static_cast<unsigned>(n) ? x[c] : -INFINITY;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = fmaxf(x[k], x[4 + k]);
+#pragma unroll
+        for (int c = 8; c < 64; c += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m[k] = max3(m[k], x[c + k], x[c + 4 + k]);
+        float top = max3(m[0], m[1], fmaxf(m[2], m[3])) * f;
+        sm.top[qt][n_mine & 1][half][row] = top;
+        named_sync(bar, 64);
+        top = fmaxf(top, sm.top[qt][n_mine & 1][half ^ 1][row]);
+        if (__any_sync(0xFFFFFFFFu, top > mref + 6.0f)) {
+          const float to = fmaxf(top, mref), by = fast_exp2(mref - to);
+          mref = to;
+          l *= by;
+          if (t > first) {
+            // s_full came behind the last product into this O; each half takes
+            // its columns
+#pragma unroll 1
+            for (int c = 0; c < D / 2; c += 16) {
+              uint32_t v[16];
+              tmem_ld16_sync(o_tm + c, v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * by);
+              tmem_st16(o_tm + c, v);
+            }
+          }
+        }
+        const float b = 8.0f - mref;
+        const float2 f2 = make_float2(f, f), b2 = make_float2(b, b);
+        float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t p[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float2 y = fma2(make_float2(x[q * 32 + 2 * c], x[q * 32 + 2 * c + 1]), f2, b2);
+            y.x = fast_exp2(y.x);
+            y.y = fast_exp2(y.y);
+            acc[c & 1] = add2(acc[c & 1], y);
+            p[c] = h2_bits(__floats2half2_rn(y.x, y.y));
+          }
+          tmem_st16(s_tm + 16 * q, p);
+          tmem_st_wait();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[qt][q]));
+        }
+        acc[0] = add2(acc[0], acc[1]);
+        l += acc[0].x + acc[0].y;
+      }
+      j += nt;
+      sm.last[qt][half][row] = l;
+      if (half == 0) sm.last[qt][2][row] = mref;
+      if (first < it.t_end) {
+        wait(sm.o_full[qt], n_work & 1);
+        ++n_work;
+        tc_fence_after_sync();
+      }
+      if (shared) named_sync(bar_rows, 128);
+      else named_sync(bar, 64);
+      const Gqa8Item fin = sm.items[s];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
+      // out = (O_a w_a + O_b w_b) / (l_a w_a + l_b w_b), b the other row tile of
+      // the same rows; both halves read the same numbers
+      const int ta = shared ? 0 : qt;
+      float wa = 1.0f, wb = 0.0f, lb = 0.0f;
+      mref = sm.last[ta][2][row];
+      l = sm.last[ta][0][row] + sm.last[ta][1][row];
+      if (shared) {
+        lb = sm.last[1][0][row] + sm.last[1][1][row];
+        const float mb = sm.last[1][2][row], to = fmaxf(mref, mb);
+        wa = fast_exp2(mref - to);
+        wb = fast_exp2(mb - to);
+        mref = to;
+      }
+      const bool has_a = nt > 0 && l != 0.0f, has_b = lb != 0.0f;      // (else O may be anything)
+      l = l * wa + lb * wb;
+      const float inv = odd && l > 0.0f ? __uint_as_float(0x7FC00000u) : 1.0f / l;
+      const bool some = l > 0.0f || l != l;
+      wa *= inv;
+      wb *= inv;
+      const int r = fin.r0 + base + row;
+      const int64_t part = static_cast<int64_t>(fin.slot) * C::kRows + base + row;
+      const int64_t orow = static_cast<int64_t>(fin.cu0 + r / G) * a.Hq + fin.h * G + r % G;
+      // Out through the rows of q's first two terms, which no product reads any
+      // more, so that the stores to memory are up to D contiguous bytes: this
+      // warp's columns of 16 bits, or half of them in fp32.
+      const int cols = shared ? D / 4 : D / 2, col0 = (shared ? 2 * qt + half : half) * cols;
+      const uint32_t oa_tm = tmem + 256 + ta * 128 + lanes + col0, ob_tm = tmem + 256 + 128 + lanes + col0;
+      auto stage = [&](int rr, int c) {
+        return reinterpret_cast<uint4*>(q_mine + half * (128 * D) + swizzle<D == 128 ? 3 : 2>((wrow + rr) * D + c * 16));
+      };
+      // 16-byte chunks of a row: D / 16, half as many where the columns are
+      // shared and of 16 bits
+      const bool cut = fin.slot >= 0;
+      const int lg = (D == 128 ? 3 : 2) - (shared && !cut ? 1 : 0);
+      uint8_t* const to = cut ? reinterpret_cast<uint8_t*>(ws_o) : static_cast<uint8_t*>(a.out);
+      const int64_t row_at = cut ? part * (4 * D) : orow * (2 * D);
+#pragma unroll 1
+      for (int c0 = 0; c0 < cols; c0 += 16) {             // of this warp's columns
+        uint32_t v[16];
+        float y[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) y[c] = 0.0f;
+        if (nt > 0) {
+          tmem_ld16_sync(oa_tm + c0, v);
+          if (has_a)
+#pragma unroll
+            for (int c = 0; c < 16; ++c) y[c] = __uint_as_float(v[c]) * wa;
+        }
+        if (shared && nt > 1) {
+          tmem_ld16_sync(ob_tm + c0, v);
+          if (has_b)
+#pragma unroll
+            for (int c = 0; c < 16; ++c) y[c] = fmaf(__uint_as_float(v[c]), wb, y[c]);
+        }
+        if (cut) {
+          const int at = c0 % (D / 4) / 4;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *stage(lane, at + c) = make_uint4(__float_as_uint(y[4 * c]), __float_as_uint(y[4 * c + 1]),
+                                              __float_as_uint(y[4 * c + 2]), __float_as_uint(y[4 * c + 3]));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            *stage(lane, c0 / 8 + c) =
+                make_uint4(pack16<F16>(y[8 * c], y[8 * c + 1]), pack16<F16>(y[8 * c + 2], y[8 * c + 3]),
+                           pack16<F16>(y[8 * c + 4], y[8 * c + 5]), pack16<F16>(y[8 * c + 6], y[8 * c + 7]));
+        }
+        if (cut ? (c0 + 16) % (D / 4) == 0 : c0 + 16 == cols) {
+          const int64_t at = row_at + (cut ? (col0 + c0 + 16 - D / 4) * 4 : col0 * 2);
+          __syncwarp();
+#pragma unroll 2
+          for (int i = lane; i < 32 << lg; i += 32) {
+            const int rr = i >> lg, c = i & ((1 << lg) - 1);
+            const int64_t dst = __shfl_sync(0xFFFFFFFFu, at, rr);
+            const uint4 v4 = *stage(rr, c);
+            if (base + wrow + rr < fin.nrows) *reinterpret_cast<uint4*>(to + dst + c * 16) = v4;
+          }
+          __syncwarp();
+        }
+      }
+      if (mine && half == 0 && base == qt * 128) {
+        const float ls = !some ? -INFINITY : odd ? __uint_as_float(0x7FC00000u) : mref - 8.0f + log2f(l);
+        if (fin.slot >= 0) ws_lse[part] = ls;
+        else a.lse[orow] = ls * 0.6931471805599453f;
+      }
+      tc_fence_before_sync();
+      // (both tiles of O, and `last`, are read before a warp goes on)
+      if (shared) named_sync(bar_rows, 128);
+    }
   }
-  const bool nan = odd && hi > lo;
-  const int64_t row = static_cast<int64_t>(t) * a.Hq + h;
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float y = 0.0f;
-    for (int i = 0; i < 4; ++i) y += part_o[i][d] * w[i];
-    y = nan ? __uint_as_float(0x7FC00000u) : sum > 0.0f ? y / sum : 0.0f;
-    if constexpr (F16) static_cast<__half*>(a.out)[row * D + d] = __float2half_rn(y);
-    else static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(y);
-  }
-  if (threadIdx.x == 0)
-    a.lse[row] = nan ? __uint_as_float(0x7FC00000u) : sum > 0.0f ? top + logf(sum) : -INFINITY;
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -613,14 +1252,24 @@ cudaError_t launch_few(const Gqa8AttnArgs& a, int max_rows, void* ws, cudaStream
 }
 
 template <int D, bool F16>
+cudaError_t launch_many(const Gqa8AttnArgs& a, int min_rows, void* ws, cudaStream_t stream) {
+  using C = ManyCfg<D>;
+  cudaError_t e = prepare_kernel<many4_kernel<D, F16>>(C::kSmem, kLaunchRegs);
+  if (e != cudaSuccess) return e;
+  const Parts p = parts_at(ws, a.num_sms, C::kRows, D);
+  e = launch_pdl(many4_kernel<D, F16>, a.num_sms, kManyThreads, C::kSmem, stream, 1, a, min_rows, p.tails, p.lse, p.o);
+  return e != cudaSuccess ? e : launch_merge(merge_many_kernel<D>, a, a.num_sms, C::kRows / 32, C::kRows, p, stream);
+}
+
+template <int D, bool F16>
 cudaError_t launch_d(const Gqa8AttnArgs& a, cudaStream_t stream) {
   const int G = a.Hq / a.Hkv, rows = few_rows(a.max_new, G);
   cudaError_t e = cudaSuccess;
   if (rows == 8) e = launch_few<D, 8, F16>(a, rows, a.ws, stream);
   else if (rows == 16) e = launch_few<D, 16, F16>(a, rows, a.ws, stream);
   if (e != cudaSuccess || static_cast<int64_t>(a.max_new) * G <= rows) return e;
-  row_kernel<D, F16><<<dim3(static_cast<unsigned>(a.n_tokens), a.Hq), 128, 0, stream>>>(a, rows + 1);
-  return cudaGetLastError();
+  void* const ws = static_cast<uint8_t*>(a.ws) + few_bytes(rows, D, a.num_sms);
+  return launch_many<D, F16>(a, rows + 1, ws, stream);
 }
 
 }  // namespace
@@ -631,7 +1280,9 @@ cudaError_t launch_attention_gqa4(const Gqa8AttnArgs& a, cudaStream_t stream) {
 }
 
 size_t attention_gqa4_workspace(int max_new, int Hq, int Hkv, int D, int num_sms) {
-  return few_bytes(few_rows(max_new, Hq / Hkv), D, num_sms);
+  const int rows = few_rows(max_new, Hq / Hkv);
+  const bool many = static_cast<int64_t>(max_new) * (Hq / Hkv) > rows;
+  return few_bytes(rows, D, num_sms) + (many ? part_bytes(num_sms, ManyCfg<128>::kRows, D) : 0);
 }
 
 }  // namespace kv4
