@@ -536,7 +536,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
 // keys, joined at its end, so that they take turns all the same.
 //   S[128 rows x 128 keys] = Q . K^T     kind::f16, both from shared memory
 //   O[128 rows x D] += P . V             kind::f16, P from TMEM
-// K and V are widened to f16 once per tile by two warps (exact: code * scale has 6
+// K and V are widened to f16 once per tile by four warps (exact: code * scale has 6
 // significant bits), from codes that bulk copies bring, a side of a page at a time;
 // q is exact in f16 but for elements below 2^-22 of its row's largest.  The chain
 // scores -> softmax -> P -> O, next scores of a row tile is what the other tile's
@@ -555,9 +555,9 @@ struct ManyCfg {
   static constexpr int kSmem = 6 * kTile + kRaw * kSide + kSmall + 1024;
 };
 static_assert(ManyCfg<128>::kRaw >= 4, "a tile's sides are in the ring together");
-constexpr int kManyThreads = 640;
-constexpr uint32_t kSoftmaxRegs = 104, kOtherRegs = 64, kLaunchRegs = 96;
-static_assert(4 * kSoftmaxRegs + kOtherRegs <= 5 * kLaunchRegs, "register shares draw on the launch's");
+constexpr int kManyThreads = 768;
+constexpr uint32_t kSoftmaxRegs = 96, kOtherRegs = 48, kLaunchRegs = 80;
+static_assert(4 * kSoftmaxRegs + 2 * kOtherRegs <= 6 * kLaunchRegs, "register shares draw on the launch's");
 
 // What an item takes beyond its tiles (q in, first scores, last product, output),
 // in half tiles; of an item of at most 128 rows.
@@ -598,15 +598,15 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
   if (tid == 0) {
     for (int i = 0; i < NR; ++i) {
       mbar_init(smem_addr(&sm.raw_full[i]), 1);
-      mbar_init(smem_addr(&sm.raw_empty[i]), 2);
+      mbar_init(smem_addr(&sm.raw_empty[i]), 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_addr(&sm.k_full[i]), 2);
+      mbar_init(smem_addr(&sm.k_full[i]), 4);
       mbar_init(smem_addr(&sm.k_empty[i]), 1);
-      mbar_init(smem_addr(&sm.v_full[i]), 2);
+      mbar_init(smem_addr(&sm.v_full[i]), 4);
       mbar_init(smem_addr(&sm.v_empty[i]), 1);
       mbar_init(smem_addr(&sm.item_full[i]), 1);
-      mbar_init(smem_addr(&sm.item_empty[i]), 19);        // the product's lane, 2 + 16 warps
+      mbar_init(smem_addr(&sm.item_empty[i]), 21);        // the product's lane, 4 + 16 warps
       mbar_init(smem_addr(&sm.q_full[i]), 8);
       mbar_init(smem_addr(&sm.s_full[i]), 1);
       mbar_init(smem_addr(&sm.p_full[i][0]), 8);
@@ -644,7 +644,7 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
     }
   };
 
-  if (warp < 4) {
+  if (warp < 8) {
     setmaxnreg_dec<kOtherRegs>();
     if (warp == 0) {
       // ==== work list and loads ====
@@ -871,23 +871,20 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
         __syncwarp();
         mbar_wait_bounded(smem_addr(&sm.never), 0, 1000000);
       }
-    } else {
-      // ==== K and V to f16: a thread is a key of a page ====
+    } else if (warp >= 4) {
+      // ==== K and V to f16: a thread is half a key of a page ====
+      const int key = tid & 63, hf = (tid >> 6) & 1;
       uint32_t j = 0, st = 0, st_par = 0;
       for (uint32_t n_items = 0;; ++n_items) {
         const int s = n_items & 1;
         wait(sm.item_full[s], (n_items >> 1) & 1);
         if (__any_sync(0xFFFFFFFFu, *dead != 0)) break;
-        const Gqa8Item item = sm.items[s];
-        const int b = item.b, t0 = item.t_begin, t1 = item.t_end;
-        const int klo = item.klo, khi = item.khi;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
-        if (b < 0) break;
+        const int b = sm.items[s].b, t0 = sm.items[s].t_begin, t1 = sm.items[s].t_end;
+        const int klo = sm.items[s].klo, khi = sm.items[s].khi;
         // the item's rows of q into L2, while the one before is worked on
-        {
-          const int cu0 = item.cu0, h = item.h, r0 = item.r0, nrows = item.nrows;
-          for (int rr = tid - 64; rr < nrows; rr += 64) {
+        if (b >= 0) {
+          const int cu0 = sm.items[s].cu0, h = sm.items[s].h, r0 = sm.items[s].r0, nrows = sm.items[s].nrows;
+          for (int rr = tid - 128; rr < nrows; rr += 128) {
             const uint16_t* row = static_cast<const uint16_t*>(a.q) +
                                   static_cast<int64_t>(cu0 + (r0 + rr) / G) * a.q_token_stride +
                                   static_cast<int64_t>(h * G + (r0 + rr) % G) * a.q_head_stride;
@@ -895,7 +892,9 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
             if (D == 128) prefetch_l2_line(row + 64);
           }
         }
-        const int key = tid - 64;                         // of a page
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
+        if (b < 0) break;
         for (int t = t0; t < t1; ++t, ++j) {
 #pragma unroll 1
           for (int side = 0; side < 4; ++side) {          // K of both pages, then V
@@ -909,36 +908,41 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
             const bool live = at >= klo && at < khi && !sm.gone[j & 7][side & 1];
             const uint8_t* const src = raw_s + st * C::kSide;
             uint8_t* const dst = (side < 2 ? k_s : v_s) + (j & 1) * C::kTile + ((side & 1) * kPage + key) * 128;
-            uint64_t sc = 0;                              // the row's scales
-            if (live) {
-              if constexpr (D == 128) sc = *reinterpret_cast<const uint64_t*>(src + C::kCodes + key * 8);
-              else sc = *reinterpret_cast<const uint32_t*>(src + C::kCodes + key * 4);
-            }
-            // (32 elements at a time, a thread's pieces in an order of its own so
-            // that 8 rows' pieces lie in different banks)
+            // Pieces of 32 elements, in an order of the thread's own so that the
+            // pieces of 8 keys lie in different banks.
+            constexpr int kPieces = D / 64;
+            uint4 w[kPieces];
+            uint32_t sc[kPieces];
+            int p[kPieces];
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              const int p = D == 128 ? (c + (key >> 1)) & 3 : (c + (key >> 2)) & 1;
-              uint4 w = make_uint4(0, 0, 0, 0);
-              if (live) w = *reinterpret_cast<const uint4*>(src + key * (D / 2) + p * 16);
-              const __half2 s2 = bits_h2(e4m3x2_to_f16x2(static_cast<uint32_t>(sc >> (p * 16)) & 0xFFFFu));
-              uint8_t* const o = dst + (p / 2) * kSlab;
-              const int u0 = p % 2 * 4;
+            for (int c = 0; c < kPieces; ++c) {
+              p[c] = D == 128 ? (hf + (key >> 1) + 2 * c) & 3 : (hf + (key >> 2)) & 1;
+              w[c] = *reinterpret_cast<const uint4*>(src + key * (D / 2) + p[c] * 16);
+              sc[c] = *reinterpret_cast<const uint16_t*>(src + C::kCodes + key * (D / 16) + p[c] * 2);
+              if (!live) sc[c] = 0;
+            }
+            // (the stage goes back before its codes are worked on)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sm.raw_empty[st]));
+#pragma unroll
+            for (int c = 0; c < kPieces; ++c) {
+              const __half2 s2 = bits_h2(e4m3x2_to_f16x2(sc[c]));
+              uint8_t* const o = dst + (p[c] / 2) * kSlab;
+              const int u0 = (p[c] % 2 * 4) ^ (key & 7);
               auto put = [&](int u, uint32_t x, __half2 f) {
                 uint32_t h[4];
                 scaled8(x, f, h);
-                *reinterpret_cast<uint4*>(o + ((u0 + u) ^ (key & 7)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(o + (u0 ^ u) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
               };
-              put(0, w.x, __low2half2(s2));
-              put(1, w.y, __low2half2(s2));
-              put(2, w.z, __high2half2(s2));
-              put(3, w.w, __high2half2(s2));
+              put(0, w[c].x, __low2half2(s2));
+              put(1, w[c].y, __low2half2(s2));
+              put(2, w[c].z, __high2half2(s2));
+              put(3, w[c].w, __high2half2(s2));
             }
-            if (side & 1) fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(smem_addr(&sm.raw_empty[st]));
-              if (side & 1) mbar_arrive(smem_addr(side == 1 ? &sm.k_full[j & 1] : &sm.v_full[j & 1]));
+            if (side & 1) {
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_addr(side == 1 ? &sm.k_full[j & 1] : &sm.v_full[j & 1]));
             }
             if (++st == NR) {
               st = 0;
@@ -951,7 +955,7 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
   } else {
     // ==== softmax: a thread is half a row, 64 keys of a tile ====
     setmaxnreg_inc<kSoftmaxRegs>();
-    const int qt = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;
+    const int qt = (warp - 8) >> 3, half = ((warp - 8) >> 2) & 1;
     const int bar = 1 + qt * 4 + (warp & 3);              // the two warps of 32 rows
     const int bar_rows = 9 + (warp & 3);                  // and those of the other row tile
     const int wrow = (warp & 3) * 32, row = wrow + lane;  // of the row tile
