@@ -556,7 +556,7 @@ struct ManyCfg {
 };
 static_assert(ManyCfg<128>::kRaw >= 4, "a tile's sides are in the ring together");
 constexpr int kManyThreads = 768;
-constexpr uint32_t kSoftmaxRegs = 96, kOtherRegs = 48, kLaunchRegs = 80;
+constexpr uint32_t kSoftmaxRegs = 88, kOtherRegs = 64, kLaunchRegs = 80;
 static_assert(4 * kSoftmaxRegs + 2 * kOtherRegs <= 6 * kLaunchRegs, "register shares draw on the launch's");
 
 // What an item takes beyond its tiles (q in, first scores, last product, output),
@@ -872,8 +872,18 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
         mbar_wait_bounded(smem_addr(&sm.never), 0, 1000000);
       }
     } else if (warp >= 4) {
-      // ==== K and V to f16: a thread is half a key of a page ====
+      // ==== K and V to f16: a thread is half a key of each page ====
       const int key = tid & 63, hf = (tid >> 6) & 1;
+      // Pieces of 32 elements, which of a row being the thread's own so that the
+      // pieces of 8 keys lie in different banks: where they come from and go to.
+      constexpr int kPieces = D / 64;
+      uint32_t from[kPieces], to[kPieces];
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c) {
+        const int p = D == 128 ? (hf + (key >> 1) + 2 * c) & 3 : (hf + (key >> 2)) & 1;
+        from[c] = key * (D / 2) + p * 16;
+        to[c] = p / 2 * kSlab + key * 128 + ((p % 2 * 4) ^ (key & 7)) * 16;
+      }
       uint32_t j = 0, st = 0, st_par = 0;
       for (uint32_t n_items = 0;; ++n_items) {
         const int s = n_items & 1;
@@ -896,58 +906,57 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
         if (lane == 0) mbar_arrive(smem_addr(&sm.item_empty[s]));
         if (b < 0) break;
         for (int t = t0; t < t1; ++t, ++j) {
+          uint8_t* const tile = k_s + (j & 1) * C::kTile;
+          // keys of the tile that some row sees: [lo, hi)
+          const int lo = klo - t * kTileKeys, hi = khi - t * kTileKeys;
 #pragma unroll 1
-          for (int side = 0; side < 4; ++side) {          // K of both pages, then V
-            if (side == 0) wait(sm.k_empty[j & 1], ((j >> 1) & 1) ^ 1);
-            if (side == 2) wait(sm.v_empty[j & 1], ((j >> 1) & 1) ^ 1);
-            wait(sm.raw_full[st], st_par);
-            __syncwarp();
-            const int64_t at = static_cast<int64_t>(t) * kTileKeys + (side & 1) * kPage + key;
-            // a key that no row sees may hold a NaN scale, which a weight of zero
-            // would not silence
-            const bool live = at >= klo && at < khi && !sm.gone[j & 7][side & 1];
-            const uint8_t* const src = raw_s + st * C::kSide;
-            uint8_t* const dst = (side < 2 ? k_s : v_s) + (j & 1) * C::kTile + ((side & 1) * kPage + key) * 128;
-            // Pieces of 32 elements, in an order of the thread's own so that the
-            // pieces of 8 keys lie in different banks.
-            constexpr int kPieces = D / 64;
-            uint4 w[kPieces];
-            uint32_t sc[kPieces];
-            int p[kPieces];
+          for (int side = 0; side < 2; ++side) {          // K, V
+            wait(side == 0 ? sm.k_empty[j & 1] : sm.v_empty[j & 1], ((j >> 1) & 1) ^ 1);
 #pragma unroll
-            for (int c = 0; c < kPieces; ++c) {
-              p[c] = D == 128 ? (hf + (key >> 1) + 2 * c) & 3 : (hf + (key >> 2)) & 1;
-              w[c] = *reinterpret_cast<const uint4*>(src + key * (D / 2) + p[c] * 16);
-              sc[c] = *reinterpret_cast<const uint16_t*>(src + C::kCodes + key * (D / 16) + p[c] * 2);
-              if (!live) sc[c] = 0;
-            }
-            // (the stage goes back before its codes are worked on)
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sm.raw_empty[st]));
-#pragma unroll
-            for (int c = 0; c < kPieces; ++c) {
-              const __half2 s2 = bits_h2(e4m3x2_to_f16x2(sc[c]));
-              uint8_t* const o = dst + (p[c] / 2) * kSlab;
-              const int u0 = (p[c] % 2 * 4) ^ (key & 7);
-              auto put = [&](int u, uint32_t x, __half2 f) {
-                uint32_t h[4];
-                scaled8(x, f, h);
-                *reinterpret_cast<uint4*>(o + (u0 ^ u) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
-              };
-              put(0, w[c].x, __low2half2(s2));
-              put(1, w[c].y, __low2half2(s2));
-              put(2, w[c].z, __high2half2(s2));
-              put(3, w[c].w, __high2half2(s2));
-            }
-            if (side & 1) {
-              fence_async_smem();
+            for (int pg = 0; pg < 2; ++pg) {
+              wait(sm.raw_full[st], st_par);
               __syncwarp();
-              if (lane == 0) mbar_arrive(smem_addr(side == 1 ? &sm.k_full[j & 1] : &sm.v_full[j & 1]));
+              const uint8_t* const src = raw_s + st * C::kSide;
+              uint4 w[kPieces];
+              uint32_t sc[kPieces];
+#pragma unroll
+              for (int c = 0; c < kPieces; ++c) {
+                w[c] = *reinterpret_cast<const uint4*>(src + from[c]);
+                sc[c] = *reinterpret_cast<const uint16_t*>(src + C::kCodes + from[c] / 8);
+              }
+              const bool gone = sm.gone[j & 7][pg] != 0;
+              // (the stage goes back before its codes are worked on)
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_addr(&sm.raw_empty[st]));
+              if (++st == NR) {
+                st = 0;
+                st_par ^= 1;
+              }
+              if (gone || pg * kPage < lo || pg * kPage + kPage > hi) {
+                // a key that no row sees may hold a NaN scale, which a weight of
+                // zero would not silence
+                const bool live = !gone && pg * kPage + key >= lo && pg * kPage + key < hi;
+#pragma unroll
+                for (int c = 0; c < kPieces; ++c) sc[c] = live ? sc[c] : 0u;
+              }
+              uint8_t* const o = tile + side * (2 * C::kTile) + pg * (kPage * 128);
+#pragma unroll
+              for (int c = 0; c < kPieces; ++c) {
+                const __half2 s2 = bits_h2(e4m3x2_to_f16x2(sc[c]));
+                auto put = [&](int u, uint32_t x, __half2 f) {
+                  uint32_t h[4];
+                  scaled8(x, f, h);
+                  *reinterpret_cast<uint4*>(o + (to[c] ^ (u * 16))) = make_uint4(h[0], h[1], h[2], h[3]);
+                };
+                put(0, w[c].x, __low2half2(s2));
+                put(1, w[c].y, __low2half2(s2));
+                put(2, w[c].z, __high2half2(s2));
+                put(3, w[c].w, __high2half2(s2));
+              }
             }
-            if (++st == NR) {
-              st = 0;
-              st_par ^= 1;
-            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(side == 0 ? &sm.k_full[j & 1] : &sm.v_full[j & 1]));
           }
         }
       }
