@@ -7,6 +7,8 @@
 // and sum and the output are held in fp32:
 //   s_j = sm_scale q.k_j,  o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),
 //   lse = m + log sum_j exp(s_j - m);  a row without a key: 0 and -inf.
+#include <algorithm>
+
 #include "kv4_gqa_merge.cuh"
 
 namespace kv4 {
@@ -46,24 +48,27 @@ namespace {
 template <int D_, int RP_>
 struct FewCfg {
   static constexpr int D = D_, RP = RP_, NT = RP / 8;
-  static constexpr int kKeys = 4096 / D;                  // of a chunk
+  static constexpr int kKeys = D == 64 && RP <= 16 ? 64 : 32;              // of a chunk
   static constexpr int kEach = kPage / kKeys;             // chunks of a page
   static constexpr int kCodes = kPage * D / 2, kScales = kPage * D / 16;   // of a page's side
   static constexpr int kStage = 2 * (kCodes + kScales);   // K, V, scales of K, of V
+  // q as operands in registers, or in shared memory where the outputs of more rows
+  // take the registers
+  static constexpr bool kSharedQ = RP > 16;
   static constexpr int kCtas = RP == 8 ? 2 : 1;
-  static constexpr int kWarps = RP == 8 ? 7 : 11;         // that compute
+  static constexpr int kWarps = RP == 16 ? 11 : 7;        // that compute
   static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kJoin = kWarps * RP * D * 4;
-  static constexpr int kSmall = 3072;
-  static constexpr int kRoom = kCtas == 2 ? 112 * 1024 : 227 * 1024;
+  static constexpr int kJoin = kWarps * RP * (D + 2) * 4; // outputs, references, sums
+  static constexpr int kQ = kSharedQ ? RP * (D * 2 + 4) : 0;
+  static constexpr int kSmall = 2048;
+  static constexpr int kRoom = (kCtas == 2 ? 112 * 1024 : 227 * 1024) - kJoin - kQ - kSmall;
   // Chunk c of a block lies in stage c / kEach mod kStages and is warp c mod
   // kWarps's.  A warp that waits for the f-th fill of a stage must have seen the one
   // before: copies end in any order, and a barrier tells only odd rounds from even
   // ones.  So a part of a stage is always the same warp's.
-  static constexpr int kStep = kWarps % kEach == 0 ? kWarps / kEach : kWarps;
-  static constexpr int kStages = (kRoom - kJoin - kSmall) / kStage / kStep * kStep;
-  static_assert(kStages > 0 && kStages * kEach % kWarps == 0, "a part of a stage has one warp");
-  static constexpr int kSmem = kStages * kStage + kJoin + kSmall;
+  static constexpr int kStages = kRoom / kStage / kWarps * kWarps;
+  static_assert(kStages > 0 && kStages <= 48 && kStages * kEach % kWarps == 0, "a part of a stage has one warp");
+  static constexpr int kSmem = kStages * kStage + kJoin + kQ + kSmall;
   static constexpr int kCost = 3;                         // what an item takes beyond its tiles, in tiles
 };
 
@@ -73,9 +78,8 @@ struct FewSmall {
   int dead;
   int gone[48];               // of a stage: its page is not there
   Gqa8Item items[4];
-  float top[12][16], sum[12][16];
 };
-static_assert(sizeof(FewSmall) <= 3072 && FewCfg<64, 16>::kStages <= 48 && FewCfg<128, 16>::kWarps <= 12, "FewSmall");
+static_assert(sizeof(FewSmall) <= 2048, "FewSmall");
 
 // c = A B, c += A B.
 __device__ __forceinline__ void mma_16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -114,14 +118,23 @@ __device__ __forceinline__ void scaled8(uint32_t w, __half2 s, uint32_t (&h)[4])
   for (int i = 0; i < 4; ++i) h[i] = h2_bits(__hmul2(bits_h2(h[i]), s));
 }
 
-template <int D, int RP, bool F16>
+// 16 values of q, as widen16, by the call's type.
+__device__ __forceinline__ uint32_t widen_q(bool f16, const uint4 (&w)[2], float (&x)[16]) {
+  return f16 ? widen16<true>(w, x) : widen16<false>(w, x);
+}
+
+template <int D, int RP>
 __global__ void __launch_bounds__(FewCfg<D, RP>::kThreads, FewCfg<D, RP>::kCtas)
 few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws_lse, float* ws_o) {
   using C = FewCfg<D, RP>;
   constexpr int NT = C::NT, ST = C::kStages, W = C::kWarps, CK = C::kKeys, MK = CK / 16, MD = D / 16;
   extern __shared__ __align__(128) uint8_t smem[];
   float* const join = reinterpret_cast<float*>(smem + ST * C::kStage);
-  FewSmall& sm = *reinterpret_cast<FewSmall*>(smem + ST * C::kStage + C::kJoin);
+  float* const tops = join + W * RP * D;
+  float* const sums = tops + W * RP;
+  uint2* const q_s = reinterpret_cast<uint2*>(smem + ST * C::kStage + C::kJoin);
+  float* const qf_s = reinterpret_cast<float*>(q_s + (C::kSharedQ ? RP * D / 4 : 0));
+  FewSmall& sm = *reinterpret_cast<FewSmall*>(smem + ST * C::kStage + C::kJoin + C::kQ);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.Hq / a.Hkv;
 
@@ -263,54 +276,94 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
       if (it.b < 0) break;
       const Pages c = pages_of(it);
 
-      // q: row n of 8 is threads 4n .. 4n + 3's, D / 4 elements each
-      uint32_t q[MD][NT][2];
+      // q: row n of 8 is threads 4n .. 4n + 3's, D / 4 elements each.  Its factor is
+      // at least 2^-126, so that a masked -inf stays one where the scale is 0; a row
+      // with a NaN or an infinity becomes NaN at the end.
+      constexpr int QN = C::kSharedQ ? 1 : NT, QD = C::kSharedQ ? 1 : MD;
+      uint32_t q[QD][QN][2];
       float qf[NT][2];
-      int pos[NT][2];
-      bool odd_col[NT][2];
+      const float sign = a.sm_scale < 0.0f ? -1.0f : 1.0f, unit = fabsf(a.sm_scale) * 1.4426950408889634f;
+      auto row_of = [&](int rr) {
+        const int r = it.r0 + min(rr, it.nrows - 1);
+        return static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(it.cu0 + r / G) * a.q_token_stride +
+               static_cast<int64_t>(it.h * G + r % G) * a.q_head_stride;
+      };
+      constexpr float kNan = __builtin_nanf("");
+      if constexpr (C::kSharedQ) {
+        // 16 elements a thread, a row by D / 16 of them
+        constexpr int kTpr = D / 16;
+        for (int rr = (tid - 32) / kTpr; rr < RP; rr += 32 * W / kTpr) {
+          const int part = (tid - 32) % kTpr;
+          float x[16];
+          const uint4* g = reinterpret_cast<const uint4*>(row_of(rr) + part * 16);
+          const uint4 two[2] = {load(g), load(g + 1)};
+          uint32_t m = widen_q(a.f16, two, x);
+          const uint32_t group = kTpr == 8 ? 0xFFu << (lane & 24) : 0xFu << (lane & 28);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int rr = nt * 8 + r8, r = it.r0 + min(rr, it.nrows - 1);
-        float x[D / 4];
-        uint32_t m = 0;
-        const uint4* g = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(it.cu0 + r / G) * a.q_token_stride +
-            static_cast<int64_t>(it.h * G + r % G) * a.q_head_stride + t4 * (D / 4));
+          for (int off = 1; off < kTpr; off *= 2) m = max(m, __shfl_xor_sync(group, m, off));
+          const bool odd = m >= 0x7F800000u;
+          const int e = q_exponent(m);
+          const float f = sign * pow2f(-e);
+          if (part == 0) qf_s[rr] = odd ? kNan : fmaxf(unit * pow2f(e), 0x1p-126f);
+          // element i of thread t's D / 4: product i / 4, half (i % 4) / 2
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          const uint4 two[2] = {load(g + 2 * i), load(g + 2 * i + 1)};
-          m = max(m, widen16<F16>(two, reinterpret_cast<float(&)[16]>(x[16 * i])));
+          for (int i = 0; i < 4; ++i) {
+            const int el = part * 16 + 4 * i, t = el / (D / 4), j = el % (D / 4) / 4;
+            q_s[(j * NT + rr / 8) * 32 + rr % 8 * 4 + t] =
+                odd ? make_uint2(0, 0) : make_uint2(h2_bits(__floats2half2_rn(x[4 * i] * f, x[4 * i + 1] * f)),
+                                                    h2_bits(__floats2half2_rn(x[4 * i + 2] * f, x[4 * i + 3] * f)));
+          }
         }
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        const bool odd = m >= 0x7F800000u;                // a NaN or an infinity: NaN in its row
-        const int e = q_exponent(m);
-        const float f = (a.sm_scale < 0.0f ? -1.0f : 1.0f) * pow2f(-e);
+        named_sync(1, 32 * W);
 #pragma unroll
-        for (int j = 0; j < MD; ++j)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            q[j][nt][i] = odd ? 0u : h2_bits(__floats2half2_rn(x[4 * j + 2 * i] * f, x[4 * j + 2 * i + 1] * f));
-        // (at least 2^-126, so that a masked -inf stays one where the scale is 0)
-        const float mine = fmaxf(fabsf(a.sm_scale) * 1.4426950408889634f * pow2f(e), 0x1p-126f);
+          for (int i = 0; i < 2; ++i) qf[nt][i] = qf_s[nt * 8 + 2 * t4 + i];
+      } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int col = 2 * t4 + i;                     // of the 8: its row's threads hold the factor
-          qf[nt][i] = __shfl_sync(0xFFFFFFFFu, mine, col * 4);
-          odd_col[nt][i] = __shfl_sync(0xFFFFFFFFu, static_cast<int>(odd), col * 4) != 0;
-          pos[nt][i] = it.pos0 + (it.r0 + min(nt * 8 + col, it.nrows - 1)) / G;
+        for (int nt = 0; nt < NT; ++nt) {
+          float x[D / 4];
+          uint32_t m = 0;
+          const uint4* g = reinterpret_cast<const uint4*>(row_of(nt * 8 + r8) + t4 * (D / 4));
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) {
+            const uint4 two[2] = {load(g + 2 * i), load(g + 2 * i + 1)};
+            m = max(m, widen_q(a.f16, two, reinterpret_cast<float(&)[16]>(x[16 * i])));
+          }
+          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+          const bool odd = m >= 0x7F800000u;
+          const int e = q_exponent(m);
+          const float f = sign * pow2f(-e);
+#pragma unroll
+          for (int j = 0; j < MD; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              q[j][nt][i] = odd ? 0u : h2_bits(__floats2half2_rn(x[4 * j + 2 * i] * f, x[4 * j + 2 * i + 1] * f));
+          const float mine = odd ? kNan : fmaxf(unit * pow2f(e), 0x1p-126f);
+          // (the columns' factors are their rows' threads')
+#pragma unroll
+          for (int i = 0; i < 2; ++i) qf[nt][i] = __shfl_sync(0xFFFFFFFFu, mine, (2 * t4 + i) * 4);
         }
       }
+      uint32_t odd_rows = 0;                              // bit 2 nt + i
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (qf[nt][i] != qf[nt][i]) {
+            odd_rows |= 1u << (2 * nt + i);
+            qf[nt][i] = 0x1p-126f;
+          }
       const int pos_first = it.pos0 + it.r0 / G, pos_last = it.pos0 + (it.r0 + it.nrows - 1) / G;
-      // p = 2^(s qf + ref), ref = 8 - (the reference); scores above `limit` raise it
-      float o[MD][NT][4], l[NT][2], ref[NT][2], limit[NT][2];
+      // p = 2^(s qf + ref), ref = 8 - (the reference)
+      float o[MD][NT][4], l[NT][2], ref[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           l[nt][i] = 0.0f;
           ref[nt][i] = -kLowest;
-          limit[nt][i] = -INFINITY;
         }
 #pragma unroll
         for (int i = 0; i < MD; ++i)
@@ -369,48 +422,59 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
               scaled8(kw[mk][1][x], scale(ks[mk][1]), h1);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                if (x == 0) mma_16816_first(s[mk][nt], h0[0], h1[0], h0[1], h1[1], q[0][nt][0], q[0][nt][1]);
-                else mma_16816(s[mk][nt], h0[0], h1[0], h0[1], h1[1], q[2 * x][nt][0], q[2 * x][nt][1]);
-                mma_16816(s[mk][nt], h0[2], h1[2], h0[3], h1[3], q[2 * x + 1][nt][0], q[2 * x + 1][nt][1]);
+                uint2 b0, b1;
+                if constexpr (C::kSharedQ) {
+                  b0 = q_s[(2 * x * NT + nt) * 32 + lane];
+                  b1 = q_s[((2 * x + 1) * NT + nt) * 32 + lane];
+                } else {
+                  b0 = make_uint2(q[2 * x][nt][0], q[2 * x][nt][1]);
+                  b1 = make_uint2(q[2 * x + 1][nt][0], q[2 * x + 1][nt][1]);
+                }
+                if (x == 0) mma_16816_first(s[mk][nt], h0[0], h1[0], h0[1], h1[1], b0.x, b0.y);
+                else mma_16816(s[mk][nt], h0[0], h1[0], h0[1], h1[1], b0.x, b0.y);
+                mma_16816(s[mk][nt], h0[2], h1[2], h0[3], h1[3], b1.x, b1.y);
               }
             }
           if (edge) {
             // 0 <= position - key < window, of the keys that are there
             const uint32_t win = a.window > 0 ? a.window : 0x80000000u;
 #pragma unroll
-            for (int mk = 0; mk < MK; ++mk)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int key = base + mk * 16 + key_r + (k & 2) * 4;
+              for (int i = 0; i < 2; ++i) {
+                const int pos = it.pos0 + (it.r0 + min(nt * 8 + 2 * t4 + i, it.nrows - 1)) / G;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  if (!(static_cast<uint32_t>(pos[nt][k & 1] - key) < win && key < it.khi)) s[mk][nt][k] = -INFINITY;
+                for (int mk = 0; mk < MK; ++mk)
+#pragma unroll
+                  for (int k = i; k < 4; k += 2) {
+                    const int key = base + mk * 16 + key_r + (k & 2) * 4;
+                    if (!(static_cast<uint32_t>(pos - key) < win && key < it.khi)) s[mk][nt][k] = -INFINITY;
+                  }
               }
           }
           // Each thread looks at its own scores; only where one rises too far is
           // a maximum taken over the row's threads.
-          float mx[NT][2];
+          auto top_of = [&](int nt, int k) {
+            float m = fmaxf(s[0][nt][k], s[0][nt][k + 2]);
+#pragma unroll
+            for (int mk = 1; mk < MK; ++mk) m = max3(m, s[mk][nt][k], s[mk][nt][k + 2]);
+            return m;
+          };
           bool rise = false;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              mx[nt][k] = fmaxf(s[0][nt][k], s[0][nt][k + 2]);
-#pragma unroll
-              for (int mk = 1; mk < MK; ++mk) mx[nt][k] = max3(mx[nt][k], s[mk][nt][k], s[mk][nt][k + 2]);
-              rise |= mx[nt][k] > limit[nt][k];
-            }
+            for (int k = 0; k < 2; ++k) rise |= fmaf(top_of(nt, k), qf[nt][k], ref[nt][k]) > 14.0f;
           if (__any_sync(0xFFFFFFFFu, rise)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                float m = mx[nt][k];
+                float m = top_of(nt, k);
 #pragma unroll
                 for (int off = 4; off < 32; off *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
                 const float to = fminf(ref[nt][k], 8.0f - m * qf[nt][k]), by = fast_exp2(to - ref[nt][k]);
                 ref[nt][k] = to;
-                limit[nt][k] = to == -kLowest ? -INFINITY : (14.0f - to) / qf[nt][k];
                 l[nt][k] *= by;
 #pragma unroll
                 for (int x = 0; x < MD; ++x) {
@@ -480,8 +544,8 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
           for (int off = 4; off < 32; off *= 2) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
           const int row = nt * 8 + 2 * t4 + k;
           if (r8 == 0) {
-            sm.top[w][row] = -ref[nt][k];
-            sm.sum[w][row] = odd_col[nt][k] && x > 0.0f ? __uint_as_float(0x7FC00000u) : x;
+            tops[w * RP + row] = -ref[nt][k];
+            sums[w * RP + row] = (odd_rows >> (2 * nt + k) & 1u) != 0 && x > 0.0f ? kNan : x;
           }
           // d = 2 MD lane / 4 + 2 i and the next
 #pragma unroll
@@ -494,12 +558,12 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
         const int row = u / (D / 4), d = u % (D / 4) * 4;
         float top = kLowest;
 #pragma unroll
-        for (int i = 0; i < W; ++i) top = fmaxf(top, sm.top[i][row]);
+        for (int i = 0; i < W; ++i) top = fmaxf(top, tops[i * RP + row]);
         float y[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          const float f = fast_exp2(sm.top[i][row] - top);
-          sum = fmaf(sm.sum[i][row], f, sum);
+          const float f = fast_exp2(tops[i * RP + row] - top);
+          sum = fmaf(sums[i * RP + row], f, sum);
           const float4 v = *reinterpret_cast<const float4*>(join + (i * RP + row) * D + d);
           y[0] = fmaf(v.x, f, y[0]);
           y[1] = fmaf(v.y, f, y[1]);
@@ -516,7 +580,8 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
           const int r = it.r0 + row;
           const int64_t at = static_cast<int64_t>(it.cu0 + r / G) * a.Hq + it.h * G + r % G;
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + d) =
-              make_uint2(pack16<F16>(y[0] * inv, y[1] * inv), pack16<F16>(y[2] * inv, y[3] * inv));
+              a.f16 ? make_uint2(pack16<true>(y[0] * inv, y[1] * inv), pack16<true>(y[2] * inv, y[3] * inv))
+                    : make_uint2(pack16<false>(y[0] * inv, y[1] * inv), pack16<false>(y[2] * inv, y[3] * inv));
           if (d == 0) a.lse[at] = ls * 0.6931471805599453f;
         }
       }
@@ -1239,28 +1304,31 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
 // ---------------------------------------------------------------------------
 // Launch
 // ---------------------------------------------------------------------------
-// Rows of few4_kernel's items, and of the largest request that it takes: 8 or 16,
-// the smaller that holds every request or, where some have more, a single token of
-// any; 0: none.
-int few_rows(int max_new, int G) {
-  const int64_t all = static_cast<int64_t>(max_new) * G, need = all <= 16 ? all : G;
-  return need <= 8 ? 8 : need <= 16 ? 16 : 0;
+// Rows of few4_kernel's items, and of the largest request that it takes: the
+// smallest of its heights that holds every request or, where some have more than
+// it can, a single token of any; 0: none.  (Its outputs are in registers: 32 rows
+// of 128 or 48 of 64.)
+int few_rows(int max_new, int G, int D) {
+  const int64_t all = static_cast<int64_t>(max_new) * G, most = D == 64 ? 48 : 32, need = all <= most ? all : G;
+  for (const int rows : {8, 16, 24, 32, 40, 48})
+    if (need <= rows && rows <= most) return rows;
+  return 0;
 }
 constexpr int kFewCtas = 2;                               // blocks an SM at most
 size_t few_bytes(int rows, int D, int sms) {
   return rows == 0 ? 0 : (part_bytes(kFewCtas * sms, rows, D) + 255) / 256 * 256;
 }
 
-template <int D, int RP, bool F16>
-cudaError_t launch_few(const Gqa8AttnArgs& a, int max_rows, void* ws, cudaStream_t stream) {
+template <int D, int RP>
+cudaError_t launch_few(const Gqa8AttnArgs& a, void* ws, cudaStream_t stream) {
   using C = FewCfg<D, RP>;
-  cudaError_t e = prepare_kernel<few4_kernel<D, RP, F16>>(C::kSmem, 0);
+  cudaError_t e = prepare_kernel<few4_kernel<D, RP>>(C::kSmem, 0);
   if (e != cudaSuccess) return e;
   // (no more blocks than there can be tiles, or items where none is ever cut)
   const int64_t tiles = (a.pt_stride + 1) / 2, most = a.B * static_cast<int64_t>(a.Hkv) * (tiles <= kWhole ? 1 : tiles);
   const int blocks = static_cast<int>(std::min<int64_t>(a.num_sms * C::kCtas, most));
   const Parts p = parts_at(ws, blocks, RP, D);
-  e = launch_pdl(few4_kernel<D, RP, F16>, blocks, C::kThreads, C::kSmem, stream, 1, a, max_rows, p.tails, p.lse, p.o);
+  e = launch_pdl(few4_kernel<D, RP>, blocks, C::kThreads, C::kSmem, stream, 1, a, RP, p.tails, p.lse, p.o);
   return e != cudaSuccess ? e : launch_merge(merge_few_kernel<D>, a, blocks, RP, RP, p, stream);
 }
 
@@ -1274,26 +1342,33 @@ cudaError_t launch_many(const Gqa8AttnArgs& a, int min_rows, void* ws, cudaStrea
   return e != cudaSuccess ? e : launch_merge(merge_many_kernel<D>, a, a.num_sms, C::kRows / 32, C::kRows, p, stream);
 }
 
-template <int D, bool F16>
+template <int D>
 cudaError_t launch_d(const Gqa8AttnArgs& a, cudaStream_t stream) {
-  const int G = a.Hq / a.Hkv, rows = few_rows(a.max_new, G);
+  const int G = a.Hq / a.Hkv, rows = few_rows(a.max_new, G, D);
   cudaError_t e = cudaSuccess;
-  if (rows == 8) e = launch_few<D, 8, F16>(a, rows, a.ws, stream);
-  else if (rows == 16) e = launch_few<D, 16, F16>(a, rows, a.ws, stream);
+  switch (rows) {
+    case 8: e = launch_few<D, 8>(a, a.ws, stream); break;
+    case 16: e = launch_few<D, 16>(a, a.ws, stream); break;
+    case 24: e = launch_few<D, 24>(a, a.ws, stream); break;
+    case 32: e = launch_few<D, 32>(a, a.ws, stream); break;
+  }
+  if constexpr (D == 64) {
+    if (rows == 40) e = launch_few<D, 40>(a, a.ws, stream);
+    else if (rows == 48) e = launch_few<D, 48>(a, a.ws, stream);
+  }
   if (e != cudaSuccess || static_cast<int64_t>(a.max_new) * G <= rows) return e;
   void* const ws = static_cast<uint8_t*>(a.ws) + few_bytes(rows, D, a.num_sms);
-  return launch_many<D, F16>(a, rows + 1, ws, stream);
+  return a.f16 ? launch_many<D, true>(a, rows + 1, ws, stream) : launch_many<D, false>(a, rows + 1, ws, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_attention_gqa4(const Gqa8AttnArgs& a, cudaStream_t stream) {
-  if (a.D == 64) return a.f16 ? launch_d<64, true>(a, stream) : launch_d<64, false>(a, stream);
-  return a.f16 ? launch_d<128, true>(a, stream) : launch_d<128, false>(a, stream);
+  return a.D == 64 ? launch_d<64>(a, stream) : launch_d<128>(a, stream);
 }
 
 size_t attention_gqa4_workspace(int max_new, int Hq, int Hkv, int D, int num_sms) {
-  const int rows = few_rows(max_new, Hq / Hkv);
+  const int rows = few_rows(max_new, Hq / Hkv, D);
   const bool many = static_cast<int64_t>(max_new) * (Hq / Hkv) > rows;
   return few_bytes(rows, D, num_sms) + (many ? part_bytes(num_sms, ManyCfg<128>::kRows, D) : 0);
 }
