@@ -62,21 +62,22 @@ struct FewCfg {
   static constexpr int kQ = kSharedQ ? RP * (D * 2 + 4) : 0;
   static constexpr int kSmall = 2048;
   static constexpr int kRoom = (kCtas == 2 ? 112 * 1024 : 227 * 1024) - kJoin - kQ - kSmall;
-  // Chunk c of a block lies in stage c / kEach mod kStages and is warp c mod
-  // kWarps's.  A warp that waits for the f-th fill of a stage must have seen the one
-  // before: copies end in any order, and a barrier tells only odd rounds from even
-  // ones.  So a part of a stage is always the same warp's.
-  static constexpr int kStages = kRoom / kStage / kWarps * kWarps;
-  static_assert(kStages > 0 && kStages <= 48 && kStages * kEach % kWarps == 0, "a part of a stage has one warp");
+  static constexpr int kStages = kRoom / kStage < 40 ? kRoom / kStage : 40;
   static constexpr int kSmem = kStages * kStage + kJoin + kQ + kSmall;
   static constexpr int kCost = 3;                         // what an item takes beyond its tiles, in tiles
 };
 
 struct FewSmall {
-  uint64_t full[48], empty[48], item_full[4], item_empty[4], never;
+  uint64_t full[40], empty[40], item_full[4], item_empty[4], never;
   unsigned long long total;
   int dead;
-  int gone[48];               // of a stage: its page is not there
+  // The page of the block that a stage is for (its number, from 0), twice, plus 1
+  // where the table has none.  Pages go round the ring in order and their copies end
+  // in any order, and a warp does not wait for every page of a stage, only for
+  // those with a chunk of its own: a barrier tells odd rounds from even ones, so a
+  // warp that waits for a round must know that the one before has ended.  It has
+  // once the stage is for the page that the warp looks for.
+  volatile uint32_t page[40];
   Gqa8Item items[4];
 };
 static_assert(sizeof(FewSmall) <= 2048, "FewSmall");
@@ -148,6 +149,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
       mbar_init(smem_addr(&sm.item_empty[i]), W);
     }
     mbar_init(smem_addr(&sm.never), 1);
+    for (int i = 0; i < ST; ++i) sm.page[i] = 0xFFFFFFFFu;
     sm.total = 0;
     sm.dead = 0;
     fence_mbar_init();
@@ -156,11 +158,17 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
   grid_launch_dependents();
   __syncthreads();
   // (a block for each item where they suffice and none is ever cut: all items
-  // weigh the same)
+  // weigh the same, and nothing has to be added up)
   const bool one_each = (a.pt_stride + 1) / 2 <= kWhole && static_cast<int64_t>(a.B) * a.Hkv <= gridDim.x;
   const Gqa8Kind kind = one_each ? Gqa8Kind{1, max_rows, RP, 1, 0, 0, 0} : Gqa8Kind{1, max_rows, RP, C::kCost, RP, C::kCost, 1};
-  gqa8_total(a, kind, blockIdx.x == 0, &sm.total);
-  __syncthreads();
+  int64_t total = static_cast<int64_t>(a.B) * a.Hkv;
+  if (!one_each) {
+    gqa8_total(a, kind, blockIdx.x == 0, &sm.total);
+    __syncthreads();
+    total = static_cast<int64_t>(sm.total);
+  } else if (blockIdx.x == 0 && warp == W) {
+    for (int base = 0; base < a.B; base += 32) gqa8_request(a, base + lane, 1, max_rows, true);
+  }
   volatile int* dead = &sm.dead;
   // A wait that gives up ends every later one of the block at once: the roles
   // then run to their ends without new loads, and the outputs are not valid.
@@ -223,7 +231,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
         __syncwarp();
         if (lane == 0 && !*dead) {
           n_loads = n_pages + 1;
-          sm.gone[stage] = blk < 0;
+          sm.page[stage] = 2 * n_pages + (blk < 0);
           const uint32_t bar = smem_addr(&sm.full[stage]), dst = smem_addr(smem) + stage * C::kStage;
           if (blk >= 0) {
             mbar_arrive_expect_tx(bar, C::kStage);
@@ -240,7 +248,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
         }
       }
     };
-    gqa8_walk(a, kind, static_cast<int64_t>(sm.total), tails, lane, [&](const Gqa8Item& it) {
+    gqa8_walk(a, kind, total, tails, lane, [&](const Gqa8Item& it) {
       publish(it);
       load_item(it);
     });
@@ -258,8 +266,9 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
     // that a thread's four keys of V are t, t + 4, t + 8, t + 12, whose rows lie in
     // all banks
     const int key_r = (r8 >> 1) + (r8 & 1) * 4;
-    // this warp's next chunk of the ring (of kEach * ST), and its rounds' parity
-    uint32_t slot = w, par = 0, turn = 0;                 // turn: chunks of the block so far, mod W
+    // this warp's next chunk of the ring (of kEach * ST), its rounds' parity and its
+    // page's number in the block
+    uint32_t slot = w, par = 0, turn = 0, chunk = w;      // turn: chunks of the block so far, mod W
     const uint8_t* const k_l = smem + key_r * (D / 2) + t4 * (D / 8);
     const uint8_t* const ks_l = smem + 2 * C::kCodes + key_r * (D / 16) + t4 * (D / 64);
     const uint8_t* const v_l = smem + C::kCodes + t4 * (D / 2) + r8 * (D / 16);
@@ -378,15 +387,26 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
       // chunk i of the item: warp ((i + the block's chunks before it) mod W)'s
       for (int i = static_cast<int>((w + W - turn) % W); i < c.n * C::kEach; i += W) {
         const uint32_t st = slot / C::kEach, part = slot % C::kEach;
+        const uint32_t number = chunk / C::kEach;
+        uint32_t there = sm.page[st];
+        if (there / 2 != number) {
+          const uint64_t since = global_timer_ns();
+          while ((there = sm.page[st]) / 2 != number && !*dead)
+            if (global_timer_ns() - since > a.timeout_ns) {
+              *dead = 1;
+              flag_error(a.dev_err, kDevTimeout);
+            }
+        }
         wait(sm.full[st], par);
         __syncwarp();
+        chunk += W;
         slot += W;
         if (slot >= ST * C::kEach) {
           slot -= ST * C::kEach;
           par ^= 1;
         }
         const int base = c.first * kPage + i * CK;        // (below khi)
-        if (!sm.gone[st]) {
+        if (there % 2 == 0) {
           const bool edge = base > full || base < open;
           const uint32_t at = st * C::kStage + part * (CK * D / 2), at_s = st * C::kStage + part * (CK * D / 16);
           float s[MK][NT][4];
@@ -1228,13 +1248,14 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
       const int r = fin.r0 + base + row;
       const int64_t part = static_cast<int64_t>(fin.slot) * C::kRows + base + row;
       const int64_t orow = static_cast<int64_t>(fin.cu0 + r / G) * a.Hq + fin.h * G + r % G;
-      // Out through the rows of q's first two terms, which no product reads any
-      // more, so that the stores to memory are up to D contiguous bytes: this
-      // warp's columns of 16 bits, or half of them in fp32.
+      // Out through the rows of q that these warps brought in (each half its own slab
+      // or half of the rows: another 32 rows' warps may be at the next item's q), which
+      // no product reads any more, so that the stores to memory are up to D contiguous
+      // bytes: this warp's columns of 16 bits, or half of them in fp32.
       const int cols = shared ? D / 4 : D / 2, col0 = (shared ? 2 * qt + half : half) * cols;
       const uint32_t oa_tm = tmem + 256 + ta * 128 + lanes + col0, ob_tm = tmem + 256 + 128 + lanes + col0;
       auto stage = [&](int rr, int c) {
-        return reinterpret_cast<uint4*>(q_mine + half * (128 * D) + swizzle<D == 128 ? 3 : 2>((wrow + rr) * D + c * 16));
+        return reinterpret_cast<uint4*>(q_mine + swizzle<3>((wrow + rr) * 128 + half * (D == 128 ? kSlab : 64) + c * 16));
       };
       // 16-byte chunks of a row: D / 16, half as many where the columns are
       // shared and of 16 bits
