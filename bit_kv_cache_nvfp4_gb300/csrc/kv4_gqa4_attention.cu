@@ -79,6 +79,7 @@ struct FewSmall {
   // once the stage is for the page that the warp looks for.
   volatile uint32_t page[40];
   Gqa8Item items[4];
+  int blocks[32];             // of the pages that are loaded next
 };
 static_assert(sizeof(FewSmall) <= 2048, "FewSmall");
 
@@ -200,7 +201,6 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
   if (warp == 0) {
     // ==== work list and loads ====
     uint32_t n_items = 0, n_pages = 0, n_loads = 0;       // pages; up to which lane 0 began copies
-    uint32_t stage = 0, empty_par = 1;                    // of the next page
     auto publish = [&](const Gqa8Item& it) {
       const int s = n_items & 3;
       wait(sm.item_empty[s], ((n_items >> 2) & 1) ^ 1);
@@ -214,38 +214,42 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
     };
     auto load_item = [&](const Gqa8Item& it) {
       const Pages c = pages_of(it);
-      int block = -1;                                     // (2 Hkv num_pages < 2^31)
-      for (int i = 0; i < c.n; ++i, ++n_pages) {
-        if ((i & 31) == 0) {
-          // a lane's page: its K and V, or -1 where the table has none
-          const int64_t at = static_cast<int64_t>(c.first) + i + lane;
-          block = -1;
-          if (at * kPage < it.khi) {
-            const int phys = load(a.page_table + it.b * a.pt_stride + at);
-            if (phys < 0 || phys >= a.num_pages) flag_error(a.dev_err, kDevBadPage);
-            else block = phys * a.Hkv + it.h;
+      for (int i = 0; i < c.n; i += 32) {
+        // a lane's page: its K and V, or -1 where the table has none
+        const int64_t at = static_cast<int64_t>(c.first) + i + lane;
+        int block = -1;                                   // (2 Hkv num_pages < 2^31)
+        if (at * kPage < it.khi) {
+          const int phys = load(a.page_table + it.b * a.pt_stride + at);
+          if (phys < 0 || phys >= a.num_pages) flag_error(a.dev_err, kDevBadPage);
+          else block = phys * a.Hkv + it.h;
+        }
+        sm.blocks[lane] = block;
+        __syncwarp();
+        const int n = min(32, c.n - i);
+        if (lane == 0) {
+          uint32_t stage = n_pages % ST, empty_par = (n_pages / ST & 1) ^ 1;
+          for (int k = 0; k < n; ++k) {
+            const int blk = sm.blocks[k];
+            wait(sm.empty[stage], empty_par);
+            if (*dead) break;
+            sm.page[stage] = 2 * (n_pages + k) + (blk < 0);
+            n_loads = n_pages + k + 1;
+            const uint32_t bar = smem_addr(&sm.full[stage]), dst = smem_addr(smem) + stage * C::kStage;
+            if (blk >= 0) {
+              mbar_arrive_expect_tx(bar, C::kStage);
+              bulk_copy_g2s(dst, a.pool + static_cast<int64_t>(blk) * (2 * C::kCodes), 2 * C::kCodes, bar);
+              bulk_copy_g2s(dst + 2 * C::kCodes, a.scales + static_cast<int64_t>(blk) * (2 * C::kScales), 2 * C::kScales, bar);
+            } else {
+              mbar_arrive(bar);
+            }
+            if (++stage == ST) {
+              stage = 0;
+              empty_par ^= 1;
+            }
           }
         }
-        const int64_t blk = __shfl_sync(0xFFFFFFFFu, block, i & 31);
-        wait(sm.empty[stage], empty_par);
         __syncwarp();
-        if (lane == 0 && !*dead) {
-          n_loads = n_pages + 1;
-          sm.page[stage] = 2 * n_pages + (blk < 0);
-          const uint32_t bar = smem_addr(&sm.full[stage]), dst = smem_addr(smem) + stage * C::kStage;
-          if (blk >= 0) {
-            mbar_arrive_expect_tx(bar, C::kStage);
-            bulk_copy_g2s(dst, a.pool + blk * (2 * C::kCodes), 2 * C::kCodes, bar);
-            bulk_copy_g2s(dst + 2 * C::kCodes, a.scales + blk * (2 * C::kScales), 2 * C::kScales, bar);
-          } else {
-            mbar_arrive(bar);
-          }
-        }
-        __syncwarp();
-        if (++stage == ST) {
-          stage = 0;
-          empty_par ^= 1;
-        }
+        n_pages += n;
       }
     };
     gqa8_walk(a, kind, total, tails, lane, [&](const Gqa8Item& it) {
