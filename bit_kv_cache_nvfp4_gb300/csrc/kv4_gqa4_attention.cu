@@ -478,6 +478,21 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
           }
           // Each thread looks at its own scores; only where one rises too far is
           // a maximum taken over the row's threads.
+          struct Vs {
+            alignas(8) uint32_t v[4][D / 64];
+            uint32_t sc[4];
+          };
+          auto load_v = [&](int mk, Vs& z) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int row = mk * 16 + 4 * k;
+              if constexpr (D == 128) *reinterpret_cast<uint2*>(z.v[k]) = *reinterpret_cast<const uint2*>(v_l + at + row * 64);
+              else z.v[k][0] = *reinterpret_cast<const uint32_t*>(v_l + at + row * 32);
+              z.sc[k] = vs_l[at_s + row * (D / 16)];
+            }
+          };
+          Vs vs[2];
+          load_v(0, vs[0]);
           auto top_of = [&](int nt, int k) {
             float m = fmaxf(s[0][nt][k], s[0][nt][k + 2]);
 #pragma unroll
@@ -523,17 +538,17 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
           }
 #pragma unroll
           for (int mk = 0; mk < MK; ++mk) {
-            alignas(8) uint32_t v[4][D / 64];
-            uint32_t sc[4];
+            if (mk + 1 < MK) load_v(mk + 1, vs[(mk + 1) & 1]);
+            auto& v = vs[mk & 1].v;
+            auto& sc = vs[mk & 1].sc;
+            // a key that no row sees may hold a NaN scale, which a weight of zero
+            // would not silence
+            if (edge) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int row = mk * 16 + 4 * k;
-              if constexpr (D == 128) *reinterpret_cast<uint2*>(v[k]) = *reinterpret_cast<const uint2*>(v_l + at + row * 64);
-              else v[k][0] = *reinterpret_cast<const uint32_t*>(v_l + at + row * 32);
-              sc[k] = vs_l[at_s + row * (D / 16)];
-              // a key that no row sees may hold a NaN scale, which a weight of zero
-              // would not silence
-              if (edge) sc[k] = base + row + t4 >= it.klo && base + row + t4 < it.khi ? sc[k] : 0u;
+              for (int k = 0; k < 4; ++k) {
+                const int row = base + mk * 16 + 4 * k + t4;
+                sc[k] = row >= it.klo && row < it.khi ? sc[k] : 0u;
+              }
             }
             const __half2 s01 = bits_h2(e4m3x2_to_f16x2(sc[0] + sc[1] * 256)), s23 = bits_h2(e4m3x2_to_f16x2(sc[2] + sc[3] * 256));
 #pragma unroll
