@@ -15,30 +15,43 @@ namespace {
 constexpr int kThreads = 256;         // of a block of the read-back
 constexpr int kAppendThreads = 128;   // and of the write
 
-__device__ __forceinline__ uint32_t e2m1x2_of_f32(float hi, float lo) {
+// Eight values -> eight E2M1 codes, the first in the lowest bits.
+__device__ __forceinline__ uint32_t e2m1x8_of_f32(const float* y) {
   uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tmov.b32 %0, {b, 0, 0, 0};\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return r;
+}
+// The larger magnitude of each pair (under any sign), a NaN where there is one.
+template <bool F16>
+__device__ __forceinline__ uint32_t max_magnitude2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (F16) asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
 // One block: 16 values of 16 bits -> 8 bytes of codes and the scale's byte.
-// x / s is taken as x * fl(1 / s), then rounded to 16 significant bits: x has at
-// most 11 bits, s 4 and a border between two codes 3, so x / s is either a border
-// exactly, which the product meets to 2^-23 and that rounding makes exact again,
-// or at least 2^-11 of itself away from it, which neither can bridge.  The
-// conversion then decides every code as the quotient itself would.  (One division
-// and one reciprocal for 16 elements instead of 17 divisions.)  A NaN counts as
-// 0 and an infinity saturates; neither counts for amax, and `odd` is set.
+// x / s is taken as x * fl(1 / s), rounded to a multiple of 2^-14 by adding and
+// taking off 768 (the product of the first addition is exact): x has at most 11
+// bits, s 4 and a border between two codes 3, so x / s is either a border exactly,
+// which the product is within 2^-21 of and that rounding makes exact again, or at
+// least 2^-13 away from it (borders lie at 2^-2 and above), which neither can
+// bridge.  The conversion then decides every code as the quotient itself would.
+// (One division and one reciprocal for 16 elements instead of 17 divisions.)  A NaN
+// counts as 0 and an infinity saturates; neither counts for amax, and `odd` is set.
 template <bool F16>
 __device__ __forceinline__ uint2 quantize16(const uint4& a, const uint4& b, uint32_t& scale, bool& odd) {
   float x[16];
   widen8<F16>(a, x);
   widen8<F16>(b, x + 8);
-  uint32_t m2 = max_abs2<F16>(max_abs2<F16>(max_abs2<F16>(a.x & 0x7FFF7FFFu, a.y), a.z), a.w);
-  m2 = max_abs2<F16>(max_abs2<F16>(max_abs2<F16>(max_abs2<F16>(m2, b.x), b.y), b.z), b.w);
-  uint32_t m = largest_bits<F16>(m2);
+  const uint32_t m0 = max_magnitude2<F16>(max_magnitude2<F16>(a.x, a.y), max_magnitude2<F16>(a.z, a.w));
+  const uint32_t m1 = max_magnitude2<F16>(max_magnitude2<F16>(b.x, b.y), max_magnitude2<F16>(b.z, b.w));
+  uint32_t m = largest_bits<F16>(max_magnitude2<F16>(m0, m1));
   if (m >= 0x7F800000u) {
     odd = true;
     m = 0;
@@ -53,14 +66,10 @@ __device__ __forceinline__ uint2 quantize16(const uint4& a, const uint4& b, uint
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s2) : "f"(0.0f), "f"(__fdiv_rn(__uint_as_float(m), 6.0f)));
   scale = s2;
   const float r = scale != 0 ? __frcp_rn(e4m3_to_float(scale)) : 0.0f;
-  uint32_t o[2] = {0, 0};
+  float y[16];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float y0 = __uint_as_float((__float_as_uint(x[2 * i] * r) + 0x80u) & 0xFFFFFF00u);
-    const float y1 = __uint_as_float((__float_as_uint(x[2 * i + 1] * r) + 0x80u) & 0xFFFFFF00u);
-    o[i / 4] |= e2m1x2_of_f32(y1, y0) << (8 * (i % 4));
-  }
-  return scale != 0 ? make_uint2(o[0], o[1]) : make_uint2(0, 0);
+  for (int i = 0; i < 16; ++i) y[i] = copysignf(__fadd_rn(__fmaf_rn(x[i], r, 768.0f), -768.0f), x[i]);
+  return scale != 0 ? make_uint2(e2m1x8_of_f32(y), e2m1x8_of_f32(y + 8)) : make_uint2(0, 0);
 }
 
 // Row r of a (page, head, side) block, column block c.

@@ -24,7 +24,7 @@
 namespace kv4 {
 namespace {
 
-constexpr int kBlock = 256;
+constexpr int kBlock = 256, kTable = 2048;                // threads; angles of a block
 
 // inv_freq / 2 pi modulo 1, in units of 2^-64: m * 2^(E - 150) times the fraction
 // 1 / 2 pi = 0x0.28BE60DB9391054A.. of a turn.
@@ -37,146 +37,195 @@ __device__ __forceinline__ uint64_t turn_fraction(float inv_freq) {
   return (u >> 31) ? 0 - f : f;
 }
 
+// V elements in 32-bit words (one alone in the low half).
 template <int V>
-struct alignas(2 * V) Vec {
-  uint16_t x[V];
+struct Vec {
+  static constexpr int kWords = (V + 1) / 2;
+  uint32_t w[kWords];
 };
 template <int V>
 __device__ __forceinline__ Vec<V> load_vec(const uint16_t* p) {
   Vec<V> v;
-  if constexpr (V == 8) *reinterpret_cast<uint4*>(v.x) = load(reinterpret_cast<const uint4*>(p));
-  else if constexpr (V == 4) *reinterpret_cast<uint2*>(v.x) = load(reinterpret_cast<const uint2*>(p));
-  else if constexpr (V == 2) *reinterpret_cast<uint32_t*>(v.x) = load(reinterpret_cast<const uint32_t*>(p));
-  else v.x[0] = load(p);
+  if constexpr (V == 8) {
+    const uint4 u = load(reinterpret_cast<const uint4*>(p));
+    v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
+  } else if constexpr (V == 4) {
+    const uint2 u = load(reinterpret_cast<const uint2*>(p));
+    v.w[0] = u.x, v.w[1] = u.y;
+  } else if constexpr (V == 2) {
+    v.w[0] = load(reinterpret_cast<const uint32_t*>(p));
+  } else {
+    v.w[0] = load(p);
+  }
   return v;
 }
 template <int V>
 __device__ __forceinline__ void store_vec(uint16_t* p, const Vec<V>& v) {
-  if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v.x);
-  else if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(v.x);
-  else if constexpr (V == 2) *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(v.x);
-  else *p = v.x[0];
+  if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+  else if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(v.w[0], v.w[1]);
+  else if constexpr (V == 2) *reinterpret_cast<uint32_t*>(p) = v.w[0];
+  else *p = static_cast<uint16_t>(v.w[0]);
 }
 template <bool F16>
-__device__ __forceinline__ float wide(uint16_t x) {
-  if constexpr (F16) return __half2float(__ushort_as_half(x));
-  return __uint_as_float(static_cast<uint32_t>(x) << 16);
+__device__ __forceinline__ float2 wide2(uint32_t w) {
+  if constexpr (F16) return __half22float2(bits_h2(w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
-template <bool F16>
-__device__ __forceinline__ uint16_t narrow(float x) {
-  if constexpr (F16) return __half_as_ushort(__float2half_rn(x));
-  return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+// The pairs (u.x, v.x), (u.y, v.y), turned.
+__device__ __forceinline__ void turn2(const float2& u, const float2& v, const float* c, const float* z, float2& p,
+                                      float2& q) {
+  p = make_float2(u.x * c[0] - v.x * z[0], u.y * c[1] - v.y * z[1]);
+  q = make_float2(u.x * z[0] + v.x * c[0], u.y * z[1] + v.y * c[1]);
 }
 
-// Threads: vector i of the turned part (n / V of a head), head slot, token slot.
+// Threads: vector i of the turned part (n / V of a head), head slot, token slot; a
+// thread goes through its tokens and, of each, its heads, with the next row's
+// elements on their way.
 template <int V, bool NEAR, bool F16>
 __global__ void __launch_bounds__(2 * kBlock) rotary_kernel(const RotaryArgs a) {
-  __shared__ alignas(16) float cosine[kBlock * 8], sine[kBlock * 8];
+  constexpr int W = Vec<V>::kWords;
+  __shared__ alignas(16) float cosine[kTable], sine[kTable];
   grid_dependency_wait();
   grid_launch_dependents();
   const int R = a.n / V, tid = threadIdx.x;
-  const int i = tid % R, slot = tid / R, hs = slot % a.heads_at_once, ts = slot / a.heads_at_once;
+  const int slot = tid / R, i = tid - slot * R, ts = slot / a.heads_at_once, hs = slot - ts * a.heads_at_once;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens;
-  const int64_t t = t0 + ts;
-  const int heads = a.side[0].heads + a.side[1].heads;
-  const bool in = t < a.n_tokens && ts < a.tokens;
-  const int h_end = min(heads, static_cast<int>(blockIdx.y + 1) * a.heads);
-  int h = blockIdx.y * a.heads + hs;
-  auto at = [&](int head, bool out) -> uint16_t* {
-    const int k = head >= a.side[0].heads;
+  const int tokens = static_cast<int>(min(static_cast<int64_t>(a.tokens), a.n_tokens - t0));
+  const int q_heads = a.side[0].heads, h0 = blockIdx.y * a.heads + hs;
+  const int h_end = min(q_heads + a.side[1].heads, static_cast<int>(blockIdx.y + 1) * a.heads);
+  auto row_in = [&](int tk, int h) {
+    const int k = h >= q_heads;
     const RotarySide& s = a.side[k];
-    const int64_t j = head - k * a.side[0].heads;
-    return (out ? static_cast<uint16_t*>(s.out) + t * s.out_token + j * s.out_head
-                : static_cast<uint16_t*>(const_cast<void*>(s.in)) + t * s.in_token + j * s.in_head) + s.offset;
+    return static_cast<const uint16_t*>(s.in) + (t0 + tk) * s.in_token + (h - k * q_heads) * s.in_head + s.offset;
+  };
+  auto row_out = [&](int tk, int h) {
+    const int k = h >= q_heads;
+    const RotarySide& s = a.side[k];
+    return static_cast<uint16_t*>(s.out) + (t0 + tk) * s.out_token + (h - k * q_heads) * s.out_head + s.offset;
   };
   const int first = NEAR ? 2 * i * V : i * V, second = NEAR ? first + V : first + a.n;
   Vec<V> x, y;
-  if (in && h < h_end) {
-    const uint16_t* const p = at(h, false);
+  int tk = ts, h = h0;
+  bool in = tk < tokens && ts < a.tokens_at_once && h < h_end;
+  if (in) {
+    const uint16_t* const p = row_in(tk, h);
     x = load_vec<V>(p + first);
     y = load_vec<V>(p + second);
   }
-  for (int k = tid; k < a.tokens * a.n; k += blockDim.x) {
-    const int64_t tk = t0 + k / a.n;
-    if (tk < a.n_tokens) {
-      const int64_t pos = a.wide_positions ? load(static_cast<const int64_t*>(a.positions) + tk)
-                                           : load(static_cast<const int32_t*>(a.positions) + tk);
-      const uint64_t turn = static_cast<uint64_t>(pos) * turn_fraction(load(a.inv_freq + k % a.n));
-      float s, c;
-      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s, &c);
-      cosine[k] = c * a.factor;
-      sine[k] = s * a.factor;
-    }
+  for (int k = tid; k < tokens * a.n; k += blockDim.x) {
+    const int kt = k / a.n;
+    const int64_t pos = a.wide_positions ? load(static_cast<const int64_t*>(a.positions) + t0 + kt)
+                                         : load(static_cast<const int32_t*>(a.positions) + t0 + kt);
+    const uint64_t turn = static_cast<uint64_t>(pos) * turn_fraction(load(a.inv_freq + (k - kt * a.n)));
+    float s, c;
+    sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s, &c);
+    cosine[k] = c * a.factor;
+    sine[k] = s * a.factor;
   }
   __syncthreads();
-  if (in && h < h_end) {
-    alignas(16) float c[V], z[V];
-    const int k0 = ts * a.n + i * V;
-    if constexpr (V % 4 == 0) {
+  alignas(16) float c[V > 1 ? V : 2], z[V > 1 ? V : 2];
+  int have = -1;                                          // token whose angles are in c and z
+  while (in) {
+    if (have != tk) {
+      have = tk;
+      const int k0 = tk * a.n + i * V;
+      if constexpr (V % 4 == 0) {
 #pragma unroll
-      for (int j = 0; j < V; j += 4) {
-        *reinterpret_cast<float4*>(c + j) = *reinterpret_cast<const float4*>(cosine + k0 + j);
-        *reinterpret_cast<float4*>(z + j) = *reinterpret_cast<const float4*>(sine + k0 + j);
+        for (int j = 0; j < V; j += 4) {
+          *reinterpret_cast<float4*>(c + j) = *reinterpret_cast<const float4*>(cosine + k0 + j);
+          *reinterpret_cast<float4*>(z + j) = *reinterpret_cast<const float4*>(sine + k0 + j);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          c[j] = cosine[k0 + j];
+          z[j] = sine[k0 + j];
+        }
+        if constexpr (V == 1) c[1] = z[1] = 0.0f;
+      }
+    }
+    uint16_t* const o = row_out(tk, h);
+    h += a.heads_at_once;
+    if (h >= h_end) {
+      h = h0;
+      tk += a.tokens_at_once;
+    }
+    in = tk < tokens;
+    Vec<V> nx, ny;
+    if (in) {
+      const uint16_t* const p = row_in(tk, h);
+      nx = load_vec<V>(p + first);
+      ny = load_vec<V>(p + second);
+    }
+    if constexpr (!NEAR || V == 1) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        float2 p, q;
+        turn2(wide2<F16>(x.w[j]), wide2<F16>(y.w[j]), c + 2 * j, z + 2 * j, p, q);
+        x.w[j] = pack16<F16>(p.x, p.y);
+        y.w[j] = pack16<F16>(q.x, q.y);
       }
     } else {
+      // a word is a pair
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        c[j] = cosine[k0 + j];
-        z[j] = sine[k0 + j];
+      for (int j = 0; j < 2 * W; ++j) {
+        uint32_t& w = j < W ? x.w[j % W] : y.w[j % W];
+        const float2 u = wide2<F16>(w);
+        w = pack16<F16>(u.x * c[j] - u.y * z[j], u.x * z[j] + u.y * c[j]);
       }
     }
-    while (true) {
-      // (the next head's row first)
-      const int next = h + a.heads_at_once;
-      Vec<V> nx, ny;
-      if (next < h_end) {
-        const uint16_t* const p = at(next, false);
-        nx = load_vec<V>(p + first);
-        ny = load_vec<V>(p + second);
-      }
-      Vec<V> ox, oy;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        // pair j: elements j of both vectors, or 2j and 2j + 1 of the two in a row
-        constexpr bool kNear = NEAR;
-        const int e0 = 2 * j, e1 = 2 * j + 1;
-        const float u = wide<F16>(kNear ? (e0 < V ? x.x[e0 % V] : y.x[e0 % V]) : x.x[j]);
-        const float v = wide<F16>(kNear ? (e1 < V ? x.x[e1 % V] : y.x[e1 % V]) : y.x[j]);
-        const uint16_t p0 = narrow<F16>(u * c[j] - v * z[j]), p1 = narrow<F16>(u * z[j] + v * c[j]);
-        if constexpr (kNear) {
-          (e0 < V ? ox : oy).x[e0 % V] = p0;
-          (e1 < V ? ox : oy).x[e1 % V] = p1;
-        } else {
-          ox.x[j] = p0;
-          oy.x[j] = p1;
-        }
-      }
-      uint16_t* const o = at(h, true);
-      store_vec<V>(o + first, ox);
-      store_vec<V>(o + second, oy);
-      if (next >= h_end) break;
-      h = next;
-      x = nx;
-      y = ny;
-    }
+    store_vec<V>(o + first, x);
+    store_vec<V>(o + second, y);
+    x = nx;
+    y = ny;
   }
   // the elements that do not turn, where the outputs are not the inputs
-#pragma unroll
+#pragma unroll 1
   for (int k = 0; k < 2; ++k) {
     const RotarySide& s = a.side[k];
     const int rest = (s.D - 2 * a.n) / V;                 // vectors of a head
     if (rest == 0 || s.out == s.in) continue;
-    const int h0 = max(static_cast<int>(blockIdx.y) * a.heads - k * a.side[0].heads, 0);
-    const int h1 = min(h_end - k * a.side[0].heads, s.heads);
-    const int per = (h1 - h0) * rest;                     // of a token
-    for (int u = tid; u < per * a.tokens; u += blockDim.x) {
-      const int64_t tk = t0 + u / per;
-      if (tk >= a.n_tokens) break;
-      const int w = u % per, j = h0 + w / rest;
-      int e = w % rest * V;
+    const int ha = max(static_cast<int>(blockIdx.y) * a.heads - k * q_heads, 0);
+    const int per = (min(h_end - k * q_heads, s.heads) - ha) * rest;       // of a token
+    auto place = [&](int u, const uint16_t*& in_p, uint16_t*& out_p) {
+      const int j = u / rest;
+      int e = (u - j * rest) * V;
       if (e >= s.offset) e += 2 * a.n;
-      store_vec<V>(static_cast<uint16_t*>(s.out) + tk * s.out_token + j * s.out_head + e,
-                   load_vec<V>(static_cast<const uint16_t*>(s.in) + tk * s.in_token + j * s.in_head + e));
+      in_p = static_cast<const uint16_t*>(s.in) + t0 * s.in_token + (ha + j) * s.in_head + e;
+      out_p = static_cast<uint16_t*>(s.out) + t0 * s.out_token + (ha + j) * s.out_head + e;
+    };
+    // four loads on their way: of neighbouring tokens, or of one token's vectors
+    Vec<V> v[4];
+    if (tokens >= 4) {
+      for (int u = tid; u < per; u += blockDim.x) {
+        const uint16_t* in_p;
+        uint16_t* out_p;
+        place(u, in_p, out_p);
+        for (int kt = 0; kt < tokens; kt += 4, in_p += 4 * s.in_token, out_p += 4 * s.out_token) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            if (kt + m < tokens) v[m] = load_vec<V>(in_p + m * s.in_token);
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            if (kt + m < tokens) store_vec<V>(out_p + m * s.out_token, v[m]);
+        }
+      }
+    } else {
+      for (int kt = 0; kt < tokens; ++kt)
+        for (int u = tid; u < per; u += 4 * blockDim.x) {
+          uint16_t* out_p[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const int um = u + m * blockDim.x;
+            if (um >= per) continue;
+            const uint16_t* in_p;
+            place(um, in_p, out_p[m]);
+            v[m] = load_vec<V>(in_p + kt * s.in_token);
+          }
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            if (u + m * static_cast<int>(blockDim.x) < per) store_vec<V>(out_p[m] + kt * s.out_token, v[m]);
+        }
     }
   }
 }
@@ -216,15 +265,22 @@ cudaError_t launch_rotary(const RotaryArgs& args, cudaStream_t stream) {
   const int V = vector_width(a), R = a.n / V, heads = a.side[0].heads + a.side[1].heads;
   // (n <= kRotaryPairs, so that R threads are a block at most)
   a.heads_at_once = std::max(1, std::min(heads, kBlock / R));
+  a.tokens_at_once = a.heads_at_once < heads ? 1 : std::max(1, kBlock / (R * heads));
   a.heads = heads;
+  a.tokens = a.tokens_at_once;
   const int64_t sms = a.num_sms;
-  // all heads of a token by one block, unless the blocks would not fill the SMs
-  if (a.n_tokens < 4 * sms) a.heads = a.heads_at_once;
-  a.tokens = a.heads_at_once < heads ? 1 : std::max(1, std::min(kBlock / (R * heads), 16));
-  while (a.tokens > 1 && a.n_tokens < 2 * sms * a.tokens) --a.tokens;
+  if (a.n_tokens < 4 * sms) {
+    // (all heads of a token by one block, unless the blocks would not fill the SMs)
+    a.heads = a.heads_at_once;
+    while (a.tokens_at_once > 1 && a.n_tokens < 2 * sms * a.tokens_at_once) --a.tokens_at_once;
+    a.tokens = a.tokens_at_once;
+  } else {
+    // several tokens after one another, so that all threads have angles to compute
+    while (a.tokens * a.n < kBlock && a.n_tokens >= 16 * sms * a.tokens) a.tokens += a.tokens_at_once;
+  }
   const dim3 grid(static_cast<unsigned>((a.n_tokens + a.tokens - 1) / a.tokens),
                   static_cast<unsigned>((heads + a.heads - 1) / a.heads));
-  const unsigned threads = (static_cast<unsigned>(R * a.heads_at_once * a.tokens) + 31) / 32 * 32;
+  const unsigned threads = (static_cast<unsigned>(R * a.heads_at_once * a.tokens_at_once) + 31) / 32 * 32;
   auto launch = [&](auto v) {
     constexpr int W = decltype(v)::value;
     return a.f16 ? launch_v<W, true>(a, grid, threads, stream) : launch_v<W, false>(a, grid, threads, stream);
