@@ -42,8 +42,8 @@ __device__ __forceinline__ uint32_t max_magnitude2(uint32_t a, uint32_t b) {
 // which the product is within 2^-21 of and that rounding makes exact again, or at
 // least 2^-13 away from it (borders lie at 2^-2 and above), which neither can
 // bridge.  The conversion then decides every code as the quotient itself would.
-// (One division and one reciprocal for 16 elements instead of 17 divisions.)  A NaN
-// counts as 0 and an infinity saturates; neither counts for amax, and `odd` is set.
+// amax / 6 becomes the scale in the same way: amax * fl(1 / 6) is rounded to 16
+// significant bits, and then decides as the quotient would.  A NaN and an infinity saturates; neither counts for amax, and `odd` is set.
 template <bool F16>
 __device__ __forceinline__ uint2 quantize16(const uint4& a, const uint4& b, uint32_t& scale, bool& odd) {
   float x[16];
@@ -62,10 +62,11 @@ __device__ __forceinline__ uint2 quantize16(const uint4& a, const uint4& b, uint
       if (u > 0x7F800000u) x[i] = 0.0f;
     }
   }
+  const float sixth = __uint_as_float((__float_as_uint(__uint_as_float(m) * (1.0f / 6.0f)) + 0x80u) & 0xFFFFFF00u);
   uint16_t s2;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s2) : "f"(0.0f), "f"(__fdiv_rn(__uint_as_float(m), 6.0f)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s2) : "f"(0.0f), "f"(sixth));
   scale = s2;
-  const float r = scale != 0 ? __frcp_rn(e4m3_to_float(scale)) : 0.0f;
+  const float r = __fdividef(1.0f, fmaxf(e4m3_to_float(scale), 0x1p-9f));
   float y[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) y[i] = copysignf(__fadd_rn(__fmaf_rn(x[i], r, 768.0f), -768.0f), x[i]);
@@ -132,50 +133,56 @@ __global__ void __launch_bounds__(kAppendThreads) append4_rows_kernel(Gqa8Args a
   constexpr int TPR = D / 16;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int t = blockIdx.x;
+  // (the inputs' place is known before the page's: their loads go first)
+  const int t = blockIdx.x, u = blockIdx.y * kAppendThreads + threadIdx.x;
+  const int c = u % TPR, hs = u / TPR, s = hs >= a.Hkv ? 1 : 0, h = hs - s * a.Hkv;
+  const bool mine = hs < 2 * a.Hkv;
+  uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+  if (mine) {
+    const uint16_t* src = s == 0 ? static_cast<const uint16_t*>(a.k) + t * a.k_token_stride + h * a.k_head_stride
+                                 : static_cast<const uint16_t*>(a.v) + t * a.v_token_stride + h * a.v_head_stride;
+    const uint4* g = reinterpret_cast<const uint4*>(src + c * 16);
+    x0 = load(g);
+    x1 = load(g + 1);
+  }
   int b, entry = -1;
   int64_t pos;
   if (!find_token(a, t, b, pos)) return;
   if ((pos >> 6) < a.pt_stride) entry = load(a.page_table + b * a.pt_stride + (pos >> 6));
   const int64_t pg = physical_page(a, entry);
-  if (pg < 0) return;
+  if (pg < 0 || !mine) return;
   bool odd = false;
-  for (int u = blockIdx.y * kAppendThreads + threadIdx.x; u < 2 * a.Hkv * TPR; u += gridDim.y * kAppendThreads) {
-    const int c = u % TPR, hs = u / TPR, s = hs >= a.Hkv ? 1 : 0, h = hs - s * a.Hkv;
-    const uint16_t* src = s == 0 ? static_cast<const uint16_t*>(a.k) + t * a.k_token_stride + h * a.k_head_stride
-                                 : static_cast<const uint16_t*>(a.v) + t * a.v_token_stride + h * a.v_head_stride;
-    const uint4* g = reinterpret_cast<const uint4*>(src + c * 16);
-    uint32_t scale;
-    const uint2 codes = quantize16<F16>(load(g), load(g + 1), scale, odd);
-    store_block<D>(a, (pg * a.Hkv + h) * 2 + s, static_cast<int>(pos & 63), c, codes, scale);
-  }
+  uint32_t scale;
+  const uint2 codes = quantize16<F16>(x0, x1, scale, odd);
+  store_block<D>(a, (pg * a.Hkv + h) * 2 + s, static_cast<int>(pos & 63), c, codes, scale);
   if (odd) flag_error(a.dev_err, kDevNonFinite);
 }
 
-// 16 codes times a scale, as 16 values of 16 bits: exact in both types (at most 6
+// 8 codes times a scale, as 8 values of 16 bits: exact in both types (at most 6
 // significant bits, magnitudes from 2^-10 to 2688; a NaN scale gives NaNs).
 template <bool F16>
-__device__ __forceinline__ void values16(const uint2& codes, uint32_t scale, uint4 (&o)[2]) {
-  const uint32_t s2 = e4m3x2_to_f16x2(scale | (scale << 8));
+__device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t scale) {
+  const __half2 s = bits_h2(e4m3x2_to_f16x2(scale));
+  uint32_t h[4];
+  e2m1x8_to_f16x8(codes, h);
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    uint32_t h[4];
-    e2m1x8_to_f16x8(w == 0 ? codes.x : codes.y, h);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[i] = f16x2_mul(h[i], s2);
-      if constexpr (!F16) {
-        const float2 f = __half22float2(bits_h2(h[i]));
-        h[i] = pack16<false>(f.x, f.y);
-      }
+  for (int i = 0; i < 4; ++i) {
+    const __half2 v = __hmul2(bits_h2(h[i]), __low2half2(s));
+    h[i] = h2_bits(v);
+    if constexpr (!F16) {
+      const float2 f = __half22float2(v);
+      h[i] = pack16<false>(f.x, f.y);
     }
-    o[w] = make_uint4(h[0], h[1], h[2], h[3]);
   }
+  return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
+// A block for each page and head; a thread takes 8 elements of a row, so that a
+// warp writes 512 contiguous bytes at once (with 16, of which each store takes every
+// other half sector: 70.4 us for 12 prefixes).
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads) read4_kernel(Gqa8Args a) {
-  constexpr int TPR = D / 16, RPP = kThreads / TPR, PASSES = kPage / RPP;
+  constexpr int TPR = D / 8, RPP = kThreads / TPR, PASSES = kPage / RPP;
   grid_dependency_wait();
   grid_launch_dependents();
   const int h = blockIdx.y, tid = threadIdx.x;
@@ -186,19 +193,17 @@ __global__ void __launch_bounds__(kThreads) read4_kernel(Gqa8Args a) {
   const int lo = it.start > (it.page << 6) ? static_cast<int>(it.start & 63) : 0;
   const int hi = it.end - (it.page << 6) < kPage ? static_cast<int>(it.end - (it.page << 6)) : kPage;
   const int64_t row_of_0 = it.row0 + (it.page << 6) - it.start;
-  uint2 codes[2][PASSES];
-  uint32_t scale[2][PASSES];
+  uint32_t codes[2][PASSES], scale[2][PASSES];
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
       const int r = r0 + p * RPP;
-      codes[s][p] = make_uint2(0, 0);
-      scale[s][p] = 0;
+      codes[s][p] = scale[s][p] = 0;
       if (pg >= 0 && r >= lo && r < hi) {
         const int64_t row = ((pg * a.Hkv + h) * 2 + s) * kPage + r;
-        codes[s][p] = load(reinterpret_cast<const uint2*>(a.pool + row * (D / 2) + c * 8));
-        scale[s][p] = load(a.scales + row * (D / 16) + c);
+        codes[s][p] = load(reinterpret_cast<const uint32_t*>(a.pool + row * (D / 2)) + c);
+        scale[s][p] = load(a.scales + row * (D / 16) + c / 2);
       }
     }
 #pragma unroll
@@ -207,11 +212,8 @@ __global__ void __launch_bounds__(kThreads) read4_kernel(Gqa8Args a) {
     for (int p = 0; p < PASSES; ++p) {
       const int r = r0 + p * RPP;
       if (r < lo || r >= hi) continue;
-      uint4 o[2];
-      values16<F16>(codes[s][p], scale[s][p], o);
-      uint16_t* dst = static_cast<uint16_t*>(s == 0 ? a.k_out : a.v_out) + ((row_of_0 + r) * a.Hkv + h) * D + c * 16;
-      reinterpret_cast<uint4*>(dst)[0] = o[0];
-      reinterpret_cast<uint4*>(dst)[1] = o[1];
+      uint16_t* dst = static_cast<uint16_t*>(s == 0 ? a.k_out : a.v_out) + ((row_of_0 + r) * a.Hkv + h) * D;
+      reinterpret_cast<uint4*>(dst)[c] = values8<F16>(codes[s][p], scale[s][p]);
     }
 }
 

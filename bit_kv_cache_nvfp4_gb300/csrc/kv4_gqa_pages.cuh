@@ -74,6 +74,16 @@ __device__ __forceinline__ bool find_page(const Gqa8Args& a, int w, PageItem& it
 __device__ __forceinline__ bool find_token(const Gqa8Args& a, int t, int& b, int64_t& pos) {
   const int lane = threadIdx.x & 31;
   int base = 0, n = a.B;
+  if (n > 32 && t < n) {
+    // (a token each, as in a decode step: request t's)
+    const int c0 = clamp_cu(load(a.cu + t), a.n_tokens), c1 = clamp_cu(load(a.cu + t + 1), a.n_tokens);
+    const int len = load(a.lens + t);
+    if (c0 <= t && t < c1) {
+      b = t;
+      pos = static_cast<int64_t>(len) - (c1 - t);
+      return pos >= 0;
+    }
+  }
   while (true) {
     const int step = (n + 31) / 32, at = base + lane * step;
     const bool in = lane * step < n;

@@ -82,7 +82,7 @@ __device__ __forceinline__ void turn2(const float2& u, const float2& v, const fl
 // thread goes through its tokens and, of each, its heads, with the next row's
 // elements on their way.
 template <int V, bool NEAR, bool F16>
-__global__ void __launch_bounds__(2 * kBlock) rotary_kernel(const RotaryArgs a) {
+__global__ void __launch_bounds__(V == 1 ? 2 * kBlock : kBlock) rotary_kernel(const RotaryArgs a) {
   constexpr int W = Vec<V>::kWords;
   __shared__ alignas(16) float cosine[kTable], sine[kTable];
   grid_dependency_wait();
