@@ -146,7 +146,7 @@ struct RotaryArgs {
   int n;                       // pairs of a head, 1 .. kRotaryPairs
   int interleaved, f16;
   float factor;
-  int heads, heads_at_once, tokens, tokens_at_once;      // of a thread block (set by the launch)
+  int heads, tokens, slots;    // of a thread block (set by the launch)
   int num_sms;
 };
 

@@ -78,9 +78,8 @@ __device__ __forceinline__ void turn2(const float2& u, const float2& v, const fl
   q = make_float2(u.x * z[0] + v.x * c[0], u.y * z[1] + v.y * c[1]);
 }
 
-// Threads: vector i of the turned part (n / V of a head), head slot, token slot; a
-// thread goes through its tokens and, of each, its heads, with the next row's
-// elements on their way.
+// Threads: vector i of the turned part (n / V of a head) and a slot; the slots take
+// the block's rows (token, head) in turns, with the next row's elements on their way.
 template <int V, bool NEAR, bool F16>
 __global__ void __launch_bounds__(V == 1 ? 2 * kBlock : kBlock) rotary_kernel(const RotaryArgs a) {
   constexpr int W = Vec<V>::kWords;
@@ -88,11 +87,12 @@ __global__ void __launch_bounds__(V == 1 ? 2 * kBlock : kBlock) rotary_kernel(co
   grid_dependency_wait();
   grid_launch_dependents();
   const int R = a.n / V, tid = threadIdx.x;
-  const int slot = tid / R, i = tid - slot * R, ts = slot / a.heads_at_once, hs = slot - ts * a.heads_at_once;
+  const int slot = tid / R, i = tid - slot * R;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens;
   const int tokens = static_cast<int>(min(static_cast<int64_t>(a.tokens), a.n_tokens - t0));
-  const int q_heads = a.side[0].heads, h0 = blockIdx.y * a.heads + hs;
-  const int h_end = min(q_heads + a.side[1].heads, static_cast<int>(blockIdx.y + 1) * a.heads);
+  const int q_heads = a.side[0].heads, h0 = blockIdx.y * a.heads;
+  const int h_end = min(q_heads + a.side[1].heads, h0 + a.heads), heads = h_end - h0;
+  const int step_tk = a.slots / heads, step_h = a.slots - step_tk * heads;
   auto row_in = [&](int tk, int h) {
     const int k = h >= q_heads;
     const RotarySide& s = a.side[k];
@@ -105,8 +105,8 @@ __global__ void __launch_bounds__(V == 1 ? 2 * kBlock : kBlock) rotary_kernel(co
   };
   const int first = NEAR ? 2 * i * V : i * V, second = NEAR ? first + V : first + a.n;
   Vec<V> x, y;
-  int tk = ts, h = h0;
-  bool in = tk < tokens && ts < a.tokens_at_once && h < h_end;
+  int tk = slot / heads, h = h0 + slot - tk * heads;
+  bool in = tk < tokens && slot < a.slots;
   if (in) {
     const uint16_t* const p = row_in(tk, h);
     x = load_vec<V>(p + first);
@@ -145,10 +145,11 @@ __global__ void __launch_bounds__(V == 1 ? 2 * kBlock : kBlock) rotary_kernel(co
       }
     }
     uint16_t* const o = row_out(tk, h);
-    h += a.heads_at_once;
+    h += step_h;
+    tk += step_tk;
     if (h >= h_end) {
-      h = h0;
-      tk += a.tokens_at_once;
+      h -= heads;
+      ++tk;
     }
     in = tk < tokens;
     Vec<V> nx, ny;
@@ -264,23 +265,23 @@ cudaError_t launch_rotary(const RotaryArgs& args, cudaStream_t stream) {
   RotaryArgs a = args;
   const int V = vector_width(a), R = a.n / V, heads = a.side[0].heads + a.side[1].heads;
   // (n <= kRotaryPairs, so that R threads are a block at most)
-  a.heads_at_once = std::max(1, std::min(heads, kBlock / R));
-  a.tokens_at_once = a.heads_at_once < heads ? 1 : std::max(1, kBlock / (R * heads));
+  a.slots = std::max(1, kBlock / R);
   a.heads = heads;
-  a.tokens = a.tokens_at_once;
+  a.tokens = 1;
   const int64_t sms = a.num_sms;
+  // No more than 2048 angles (kTable) a block: tokens * n <= kBlock + n.
   if (a.n_tokens < 4 * sms) {
     // (all heads of a token by one block, unless the blocks would not fill the SMs)
-    a.heads = a.heads_at_once;
-    while (a.tokens_at_once > 1 && a.n_tokens < 2 * sms * a.tokens_at_once) --a.tokens_at_once;
-    a.tokens = a.tokens_at_once;
+    a.heads = std::min(heads, a.slots);
+    while (a.tokens * a.heads < a.slots && a.tokens * a.n < kBlock && a.n_tokens >= 2 * sms * (a.tokens + 1)) ++a.tokens;
   } else {
     // several tokens after one another, so that all threads have angles to compute
-    while (a.tokens * a.n < kBlock && a.n_tokens >= 16 * sms * a.tokens) a.tokens += a.tokens_at_once;
+    while (a.tokens * a.n < kBlock && a.n_tokens >= 16 * sms * a.tokens) ++a.tokens;
   }
+  a.slots = std::min(a.slots, a.tokens * a.heads);
   const dim3 grid(static_cast<unsigned>((a.n_tokens + a.tokens - 1) / a.tokens),
                   static_cast<unsigned>((heads + a.heads - 1) / a.heads));
-  const unsigned threads = (static_cast<unsigned>(R * a.heads_at_once * a.tokens_at_once) + 31) / 32 * 32;
+  const unsigned threads = (static_cast<unsigned>(R * a.slots) + 31) / 32 * 32;
   auto launch = [&](auto v) {
     constexpr int W = decltype(v)::value;
     return a.f16 ? launch_v<W, true>(a, grid, threads, stream) : launch_v<W, false>(a, grid, threads, stream);
