@@ -271,8 +271,9 @@ cudaError_t launch_rotary(const RotaryArgs& args, cudaStream_t stream) {
   const int64_t sms = a.num_sms;
   // No more than 2048 angles (kTable) a block: tokens * n <= kBlock + n.
   if (a.n_tokens < 4 * sms) {
-    // (all heads of a token by one block, unless the blocks would not fill the SMs)
-    a.heads = std::min(heads, a.slots);
+    // few tokens: their heads over more blocks, each with the angles for itself
+    const int share = static_cast<int>(heads * a.n_tokens / (8 * sms));
+    a.heads = std::min({heads, a.slots, std::max(8, share)});
     while (a.tokens * a.heads < a.slots && a.tokens * a.n < kBlock && a.n_tokens >= 2 * sms * (a.tokens + 1)) ++a.tokens;
   } else {
     // several tokens after one another, so that all threads have angles to compute
@@ -281,7 +282,12 @@ cudaError_t launch_rotary(const RotaryArgs& args, cudaStream_t stream) {
   a.slots = std::min(a.slots, a.tokens * a.heads);
   const dim3 grid(static_cast<unsigned>((a.n_tokens + a.tokens - 1) / a.tokens),
                   static_cast<unsigned>((heads + a.heads - 1) / a.heads));
-  const unsigned threads = (static_cast<unsigned>(R * a.slots) + 31) / 32 * 32;
+  // (threads beyond the slots' have their part in the angles and the copies)
+  int rest = 0;
+  for (const RotarySide& s : a.side)
+    if (s.heads > 0 && s.out != s.in) rest = std::max(rest, (s.D - 2 * a.n) / V);
+  const int copies = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(rest) * a.heads / 4, kBlock));
+  const unsigned threads = (static_cast<unsigned>(std::max(R * a.slots, copies)) + 31) / 32 * 32;
   auto launch = [&](auto v) {
     constexpr int W = decltype(v)::value;
     return a.f16 ? launch_v<W, true>(a, grid, threads, stream) : launch_v<W, false>(a, grid, threads, stream);
