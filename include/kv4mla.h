@@ -654,7 +654,7 @@ kv4_status kv4_attention_gqa4(const void* q_dev, int64_t q_token_stride, int64_t
  *                   radians a position
  * Pair i of a head is elements (offset + 2i, offset + 2i + 1) where interleaved is
  * nonzero and (offset + i, offset + n_pairs + i) where it is 0; with the angle
- * a = position * inv_freq[i] (held to 2^-31 of a turn)
+ * a = position * inv_freq[i] (held to 2^-29 of a turn)
  *   (x, y) -> factor * (x cos a - y sin a, x sin a + y cos a)
  * in fp32, rounded once.  Elements outside offset .. offset + 2 n_pairs - 1 are
  * copied as they are.

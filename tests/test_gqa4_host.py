@@ -1,0 +1,145 @@
+"""The 4-bit grouped-query and rotary entry points without a GPU: what they refuse,
+frequencies, and the reference's own pieces."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import bit_kv_cache_nvfp4_gb300 as kv
+import gqa4_ref as ref
+from test_gqa8_host import (BAD, SHARED, UNSUPPORTED, append_args, attention_args, lib, mem,  # noqa: F401
+                            read_args)
+
+ALIGNED = [("pool", 8), ("scales", 8)]
+
+
+@pytest.mark.parametrize("change,status", SHARED + [
+    (dict(k=None), BAD), (dict(v=None), BAD), (dict(lens=None), BAD), (dict(ks0=132), BAD), (dict(vs1=4), BAD),
+    (dict(ks1=32), BAD), (dict(ks0=-128), BAD), (dict(pages=0), BAD)])
+def test_append_refuses(lib, mem, change, status):  # noqa: F811
+    assert lib.kv4_append_gqa4(*append_args(mem[1], **change)) == status
+
+
+@pytest.mark.parametrize("change,status", SHARED + [(dict(starts=None), BAD), (dict(k=None), BAD), (dict(v=None), BAD)])
+def test_read_refuses(lib, mem, change, status):  # noqa: F811
+    assert lib.kv4_read_gqa4(*read_args(mem[1], **change)) == status
+
+
+@pytest.mark.parametrize("change,status", SHARED + [
+    (dict(q=None), BAD), (dict(lens=None), BAD), (dict(out=None), BAD), (dict(lse=None), BAD), (dict(hq=7), BAD),
+    (dict(hq=1), BAD), (dict(hq=2 * 129), UNSUPPORTED), (dict(window=-1), BAD), (dict(max_new=0), BAD),
+    (dict(max_new=-1), BAD), (dict(scale=math.inf), BAD), (dict(scale=math.nan), BAD), (dict(qs0=513), BAD)])
+def test_attention_refuses(lib, mem, change, status):  # noqa: F811
+    assert lib.kv4_attention_gqa4(*attention_args(mem[1], **change)) == status
+
+
+@pytest.mark.parametrize("name,off", ALIGNED)
+def test_alignment(lib, mem, name, off):  # noqa: F811
+    """Codes and scales move in 16-byte pieces."""
+    change = {name: mem[1] + off}
+    assert lib.kv4_append_gqa4(*append_args(mem[1], **change)) == BAD
+    assert lib.kv4_read_gqa4(*read_args(mem[1], **change)) == BAD
+    assert lib.kv4_attention_gqa4(*attention_args(mem[1], **change)) == BAD
+
+
+def test_empty_calls_need_no_device(lib, mem):  # noqa: F811
+    for args in (dict(T=0), dict(B=0)):
+        assert lib.kv4_append_gqa4(*append_args(mem[1], **args)) == 0
+        assert lib.kv4_read_gqa4(*read_args(mem[1], **args)) == 0
+        assert lib.kv4_attention_gqa4(*attention_args(mem[1], **args)) == 0
+
+
+# ---------------------------------------------------------------------------
+# rotary
+# ---------------------------------------------------------------------------
+def rotary_args(p, **kw):
+    a = dict(q=p, qs0=256, qs1=64, hq=4, dq=64, qo=0, qout=p, qos0=256, qos1=64, k=p, ks0=64, ks1=64, hk=1, dk=64, ko=0,
+             kout=p, kos0=64, kos1=64, dtype=0, T=3, pos=p, bits=32, freq=p, n=32, near=0, factor=1.0, stream=None)
+    a.update(kw)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(q=None), BAD), (dict(qout=None), BAD), (dict(k=None), BAD), (dict(kout=None), BAD), (dict(pos=None), BAD),
+    (dict(freq=None), BAD), (dict(T=-1), BAD), (dict(T=2 ** 31), BAD), (dict(hq=-1), BAD), (dict(hq=65536), BAD),
+    (dict(hq=65535, qos1=64, qs1=64), UNSUPPORTED), (dict(n=0), BAD), (dict(n=33), BAD), (dict(n=513, dq=2000), UNSUPPORTED),
+    (dict(qo=1), BAD), (dict(qo=-1), BAD), (dict(ko=2 ** 31 - 1), BAD), (dict(dq=0), BAD), (dict(dk=65537), BAD),
+    (dict(dtype=2), UNSUPPORTED), (dict(bits=16), UNSUPPORTED), (dict(factor=math.inf), BAD), (dict(factor=math.nan), BAD),
+    (dict(qs0=-1), BAD), (dict(qos1=63), BAD), (dict(kos0=63), BAD), (dict(qos0=512), BAD), (dict(qs1=128), BAD)])
+def test_rotary_refuses(lib, mem, change, status):  # noqa: F811
+    assert lib.kv4_rotary(*rotary_args(mem[1], **change)) == status
+
+
+def test_rotary_alignment(lib, mem):  # noqa: F811
+    for change in (dict(q=mem[1] + 1), dict(kout=mem[1] + 3), dict(pos=mem[1] + 2), dict(pos=mem[1] + 4, bits=64),
+                   dict(freq=mem[1] + 2)):
+        assert lib.kv4_rotary(*rotary_args(mem[1], **change)) == BAD
+
+
+def test_rotary_of_nothing(lib, mem):  # noqa: F811
+    none = dict(q=None, qout=None, hq=0, k=None, kout=None, hk=0)
+    assert lib.kv4_rotary(*rotary_args(mem[1], **none)) == 0
+    assert lib.kv4_rotary(*rotary_args(mem[1], T=0)) == 0
+
+
+def test_frequencies():
+    f = kv.rotary_frequencies(64)
+    i = torch.arange(32, dtype=torch.float64)
+    want = 10000.0 ** (-i / 32)
+    assert f.dtype == torch.float32 and torch.equal(f, want.float())
+    assert torch.equal(kv.rotary_frequencies(64, scaling="linear", stretch=8.0), (want / 8).float())
+    base = kv.rotary_frequencies(64, scaling="base", stretch=8.0)
+    assert base[0] == 1 and abs(float(base[-1]) / float(want[-1] / 8) - 1) < 1e-6
+    ramp = kv.rotary_frequencies(64, scaling="ramp", stretch=8.0, original_length=4096, slow=1.0, fast=32.0).double()
+    turns = 4096 * want / (2 * math.pi)
+    r = ramp / want
+    assert ((r - 1).abs()[turns > 32] < 1e-6).all() and ((r * 8 - 1).abs()[turns < 1] < 1e-6).all()
+    between = (turns > 1) & (turns < 32)
+    assert between.any() and (r[between] > 1 / 8).all() and (r[between] < 1).all()
+    assert (r[1:] <= r[:-1] * (1 + 2.0 ** -22)).all()            # (rounded to fp32: 2^-24 of each)
+    assert torch.equal(kv.rotary_frequencies(2), torch.ones(1))
+
+
+@pytest.mark.parametrize("args", [dict(dim=0), dict(dim=7), dict(dim=8, base=0.0), dict(dim=8, stretch=-1.0),
+                                  dict(dim=2, scaling="base", stretch=2.0), dict(dim=8, scaling="ramp", slow=4.0, fast=4.0),
+                                  dict(dim=8, scaling="other"), dict(dim=8, base=math.inf), dict(dim=8, stretch=math.nan)])
+def test_frequencies_refuse(args):
+    with pytest.raises(ValueError):
+        kv.rotary_frequencies(**args)
+
+
+# ---------------------------------------------------------------------------
+# the reference
+# ---------------------------------------------------------------------------
+def test_reference_codes_by_hand():
+    """A block of amax 6: scale 1 and codes of the values themselves, ties to even;
+    one of amax 12: scale 2; a block of zeros."""
+    x = torch.tensor([6, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, -0.25, -0.26, 0.5, 1, 1.5, 2, 3, -4], dtype=torch.float64)
+    codes, scale = ref.quantize(torch.cat([x, 2 * x, 0 * x]))
+    assert scale.tolist() == [0x38, 0x40, 0]
+    half = torch.stack([codes[:8] & 15, codes[:8] >> 4], -1).flatten().tolist()
+    assert half == [7, 0, 2, 2, 4, 4, 6, 6, 8, 9, 1, 2, 3, 4, 5, 14]
+    assert torch.equal(codes[:8], codes[8:16]) and (codes[16:] == 0).all()
+
+
+def test_reference_round_trip():
+    """Every code of every positive scale comes back."""
+    s = torch.arange(1, 127, dtype=torch.uint8)
+    code = torch.arange(16, dtype=torch.uint8)
+    x = ref.dequantize((code[0::2] | code[1::2] << 4).expand(126, 8), s[:, None])
+    codes, scales = ref.quantize(x)
+    assert torch.equal(scales[:, 0], s)
+    assert torch.equal(ref.dequantize(codes, scales), x)
+
+
+def test_bounds_see_a_lost_page():
+    """Of the reference itself: without the values of one page of a request whose
+    query asks for it, a row is many times its bound off."""
+    c = ref.Cache([300], 1, 64, "cpu", seed=1)
+    q = torch.randn(1, 1, 64) * 0.1
+    want = ref.attention(q, c.pool, c.scales, c.table, c.lens, [0, 1], 0.125)
+    tol, _ = ref.bounds(*want, torch.bfloat16, 64)
+    c.scales[c.table[0][2], :, 1] = 0
+    lost = ref.attention(q, c.pool, c.scales, c.table, c.lens, [0, 1], 0.125)[0]
+    assert float(((lost - want[0]).abs() / tol).max()) > 20
