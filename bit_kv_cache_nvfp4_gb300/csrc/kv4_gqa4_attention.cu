@@ -910,10 +910,15 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
             const bool next = t + 1 < nt;
             wait(sm.v_full[j & 1], (j >> 1) & 1);
             next_k();
-            if (next) wait(sm.k_full[ks], k_par);
+            // (the wait for K of the next tile comes behind the products of this)
             pv(0, j, t == 0, p0, [&] {
-              if (next) qk(0, ks, 0);
-              else mma_commit(smem_addr(&sm.o_full[0]));
+              if (next) {
+                wait(sm.k_full[ks], k_par);
+                tc_fence_after_sync();
+                qk(0, ks, 0);
+              } else {
+                mma_commit(smem_addr(&sm.o_full[0]));
+              }
             });
             pv(1, j, t == 0, p1, [&] {
               if (next) {
@@ -948,15 +953,16 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
             const uint32_t j = n_tiles + t;
             const bool next = t + 2 < nt;
             wait(sm.v_full[j & 1], (j >> 1) & 1);
-            if (next) wait(sm.k_full[ks], k_par);
             auto more = [&](int qt) {
+              mma_commit(smem_addr(&sm.v_empty[j & 1]));
               if (next) {
+                wait(sm.k_full[ks], k_par);
+                tc_fence_after_sync();
                 qk(qt, ks, 0);
                 mma_commit(smem_addr(&sm.k_empty[ks]));
               } else {
                 mma_commit(smem_addr(&sm.o_full[qt]));
               }
-              mma_commit(smem_addr(&sm.v_empty[j & 1]));
             };
             if (t & 1) pv(1, j, t == 1, p1, [&] { more(1); });
             else pv(0, j, t == 0, p0, [&] { more(0); });
@@ -1015,49 +1021,52 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
           const int lo = klo - t * kTileKeys, hi = khi - t * kTileKeys;
 #pragma unroll 1
           for (int side = 0; side < 2; ++side) {          // K, V
-            wait(side == 0 ? sm.k_empty[j & 1] : sm.v_empty[j & 1], ((j >> 1) & 1) ^ 1);
+            uint4 w[2][kPieces];
+            uint32_t sc[2][kPieces];
+            const uint32_t st1 = st + 1 == NR ? 0 : st + 1, par1 = st + 1 == NR ? st_par ^ 1 : st_par;
 #pragma unroll
             for (int pg = 0; pg < 2; ++pg) {
-              wait(sm.raw_full[st], st_par);
-              __syncwarp();
-              const uint8_t* const src = raw_s + st * C::kSide;
-              uint4 w[kPieces];
-              uint32_t sc[kPieces];
+              wait(sm.raw_full[pg == 0 ? st : st1], pg == 0 ? st_par : par1);
+              const uint8_t* const src = raw_s + (pg == 0 ? st : st1) * C::kSide;
 #pragma unroll
               for (int c = 0; c < kPieces; ++c) {
-                w[c] = *reinterpret_cast<const uint4*>(src + from[c]);
-                sc[c] = *reinterpret_cast<const uint16_t*>(src + C::kCodes + from[c] / 8);
+                w[pg][c] = *reinterpret_cast<const uint4*>(src + from[c]);
+                sc[pg][c] = *reinterpret_cast<const uint16_t*>(src + C::kCodes + from[c] / 8);
               }
               const bool gone = sm.gone[j & 7][pg] != 0;
-              // (the stage goes back before its codes are worked on)
-              __syncwarp();
-              if (lane == 0) mbar_arrive(smem_addr(&sm.raw_empty[st]));
-              if (++st == NR) {
-                st = 0;
-                st_par ^= 1;
-              }
               if (gone || pg * kPage < lo || pg * kPage + kPage > hi) {
                 // a key that no row sees may hold a NaN scale, which a weight of
                 // zero would not silence
                 const bool live = !gone && pg * kPage + key >= lo && pg * kPage + key < hi;
 #pragma unroll
-                for (int c = 0; c < kPieces; ++c) sc[c] = live ? sc[c] : 0u;
+                for (int c = 0; c < kPieces; ++c) sc[pg][c] = live ? sc[pg][c] : 0u;
               }
-              uint8_t* const o = tile + side * (2 * C::kTile) + pg * (kPage * 128);
+            }
+            // (the stages go back before their codes are worked on)
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(smem_addr(&sm.raw_empty[st]));
+              mbar_arrive(smem_addr(&sm.raw_empty[st1]));
+            }
+            st = st1 + 1 == NR ? 0 : st1 + 1;
+            st_par = st1 + 1 == NR ? par1 ^ 1 : par1;
+            wait(side == 0 ? sm.k_empty[j & 1] : sm.v_empty[j & 1], ((j >> 1) & 1) ^ 1);
+            uint8_t* const o = tile + side * (2 * C::kTile);
+#pragma unroll
+            for (int pg = 0; pg < 2; ++pg)
 #pragma unroll
               for (int c = 0; c < kPieces; ++c) {
-                const __half2 s2 = bits_h2(e4m3x2_to_f16x2(sc[c]));
+                const __half2 s2 = bits_h2(e4m3x2_to_f16x2(sc[pg][c]));
                 auto put = [&](int u, uint32_t x, __half2 f) {
                   uint32_t h[4];
                   scaled8(x, f, h);
-                  *reinterpret_cast<uint4*>(o + (to[c] ^ (u * 16))) = make_uint4(h[0], h[1], h[2], h[3]);
+                  *reinterpret_cast<uint4*>(o + pg * (kPage * 128) + (to[c] ^ (u * 16))) = make_uint4(h[0], h[1], h[2], h[3]);
                 };
-                put(0, w[c].x, __low2half2(s2));
-                put(1, w[c].y, __low2half2(s2));
-                put(2, w[c].z, __high2half2(s2));
-                put(3, w[c].w, __high2half2(s2));
+                put(0, w[pg][c].x, __low2half2(s2));
+                put(1, w[pg][c].y, __low2half2(s2));
+                put(2, w[pg][c].z, __high2half2(s2));
+                put(3, w[pg][c].w, __high2half2(s2));
               }
-            }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(side == 0 ? &sm.k_full[j & 1] : &sm.v_full[j & 1]));
