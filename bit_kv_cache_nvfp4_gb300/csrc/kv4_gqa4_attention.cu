@@ -660,8 +660,8 @@ struct ManyCfg {
 };
 static_assert(ManyCfg<128>::kRaw >= 4, "a tile's sides are in the ring together");
 constexpr int kManyThreads = 768;
-constexpr uint32_t kSoftmaxRegs = 88, kOtherRegs = 64, kLaunchRegs = 80;
-static_assert(4 * kSoftmaxRegs + 2 * kOtherRegs <= 6 * kLaunchRegs, "register shares draw on the launch's");
+constexpr uint32_t kSoftmaxRegs = 96, kIssueRegs = 40, kWidenRegs = 56, kLaunchRegs = 80;
+static_assert(4 * kSoftmaxRegs + kIssueRegs + kWidenRegs <= 6 * kLaunchRegs, "register shares draw on the launch's");
 
 // What an item takes beyond its tiles (q in, first scores, last product, output),
 // in half tiles; of an item of at most 128 rows.
@@ -748,8 +748,8 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
     }
   };
 
-  if (warp < 8) {
-    setmaxnreg_dec<kOtherRegs>();
+  if (warp < 4) {
+    setmaxnreg_dec<kIssueRegs>();
     if (warp == 0) {
       // ==== work list and loads ====
       uint32_t n_items = 0, n_tiles = 0;
@@ -981,7 +981,10 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
         __syncwarp();
         mbar_wait_bounded(smem_addr(&sm.never), 0, 1000000);
       }
-    } else if (warp >= 4) {
+    }
+  } else if (warp < 8) {
+    setmaxnreg_dec<kWidenRegs>();
+    {
       // ==== K and V to f16: a thread is half a key of each page ====
       const int key = tid & 63, hf = (tid >> 6) & 1;
       // Pieces of 32 elements, which of a row being the thread's own so that the
