@@ -64,7 +64,9 @@ struct FewCfg {
   static constexpr int kRoom = (kCtas == 2 ? 112 * 1024 : 227 * 1024) - kJoin - kQ - kSmall;
   static constexpr int kStages = kRoom / kStage < 40 ? kRoom / kStage : 40;
   static constexpr int kSmem = kStages * kStage + kJoin + kQ + kSmall;
-  static constexpr int kCost = 3;                         // what an item takes beyond its tiles, in tiles
+  // what an item takes beyond its tiles, in tiles (2, 3, 5 of them: the decode step
+  // below 247, 244, 238 us, drafts of 35 rows 47.7, 41.6, 43.6)
+  static constexpr int kCost = RP == 8 ? 5 : 3;
 };
 
 struct FewSmall {
@@ -158,17 +160,13 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
   grid_dependency_wait();
   grid_launch_dependents();
   __syncthreads();
-  // (a block for each item where they suffice and none is ever cut: all items
-  // weigh the same, and nothing has to be added up)
+  // Where none is ever cut and they suffice, a block for each request and kv head:
+  // nothing has to be added up.
   const bool one_each = (a.pt_stride + 1) / 2 <= kWhole && static_cast<int64_t>(a.B) * a.Hkv <= gridDim.x;
-  const Gqa8Kind kind = one_each ? Gqa8Kind{1, max_rows, RP, 1, 0, 0, 0} : Gqa8Kind{1, max_rows, RP, C::kCost, RP, C::kCost, 1};
-  int64_t total = static_cast<int64_t>(a.B) * a.Hkv;
+  const Gqa8Kind kind{1, max_rows, RP, C::kCost, RP, C::kCost, 1};
   if (!one_each) {
     gqa8_total(a, kind, blockIdx.x == 0, &sm.total);
     __syncthreads();
-    total = static_cast<int64_t>(sm.total);
-  } else if (blockIdx.x == 0 && warp == W) {
-    for (int base = 0; base < a.B; base += 32) gqa8_request(a, base + lane, 1, max_rows, true);
   }
   volatile int* dead = &sm.dead;
   // A wait that gives up ends every later one of the block at once: the roles
@@ -252,10 +250,18 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
         n_pages += n;
       }
     };
-    gqa8_walk(a, kind, total, tails, lane, [&](const Gqa8Item& it) {
+    auto take = [&](const Gqa8Item& it) {
       publish(it);
       load_item(it);
-    });
+    };
+    if (one_each) {
+      const int b = blockIdx.x / a.Hkv, h = blockIdx.x - b * a.Hkv;
+      const Gqa8Request r = gqa8_request(a, b, 1, max_rows, h == 0 && lane == 0);
+      const Gqa8Span sp = gqa8_span(a, r, G, 0, max(r.n * G, 1));
+      if (r.n > 0) take(Gqa8Item{b, h, r.cu0, r.pos0, 0, r.n * G, sp.klo, sp.khi, sp.t0, sp.t0 + sp.nt, -1});
+    } else {
+      gqa8_walk(a, kind, static_cast<int64_t>(sm.total), tails, lane, take);
+    }
     publish(Gqa8Item{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, -1});
     // every copy lands before the block's shared memory goes away
     for (uint32_t i = n_pages > ST ? n_pages - ST : 0; i < n_pages; ++i)
@@ -395,11 +401,13 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
         uint32_t there = sm.page[st];
         if (there / 2 != number) {
           const uint64_t since = global_timer_ns();
-          while ((there = sm.page[st]) / 2 != number && !*dead)
+          while ((there = sm.page[st]) / 2 != number && !*dead) {
+            __nanosleep(40);
             if (global_timer_ns() - since > a.timeout_ns) {
               *dead = 1;
               flag_error(a.dev_err, kDevTimeout);
             }
+          }
         }
         wait(sm.full[st], par);
         __syncwarp();
@@ -658,7 +666,7 @@ struct ManyCfg {
   static constexpr int kRaw = kRoom / kSide < 16 ? kRoom / kSide : 16;     // sides of pages on their way
   static constexpr int kSmem = 6 * kTile + kRaw * kSide + kSmall + 1024;
 };
-static_assert(ManyCfg<128>::kRaw >= 4, "a tile's sides are in the ring together");
+static_assert(ManyCfg<128>::kRaw >= 4 && ManyCfg<64>::kRaw <= 16, "a tile's sides are in the ring together, four tiles' at most");
 constexpr int kManyThreads = 768;
 constexpr uint32_t kSoftmaxRegs = 96, kIssueRegs = 40, kWidenRegs = 56, kLaunchRegs = 80;
 static_assert(4 * kSoftmaxRegs + kIssueRegs + kWidenRegs <= 6 * kLaunchRegs, "register shares draw on the launch's");
@@ -787,9 +795,9 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
               if (lane == 0 && !*dead) {
                 n_loads = n_sides + 1;
                 if (side == 0) {
-                  // (the softmax of the tile eight before is done: the widening
-                  // warps, whose side this stage waited for, are at most two tiles
-                  // ahead of the products, and those two ahead of it)
+                  // (the softmax of the tile eight before is done: this stage was, up
+                  // to four tiles ago, one of the widening warps', which then had V of
+                  // the tile before, so the products of the tile seven before were over)
                   sm.gone[n_tiles & 7][0] = b[0] < 0;
                   sm.gone[n_tiles & 7][1] = b[1] < 0;
                   mbar_arrive(smem_addr(&sm.gone_full[n_tiles & 7]));
