@@ -58,7 +58,8 @@ struct FewCfg {
   static constexpr int kCtas = RP == 8 ? 2 : 1;
   static constexpr int kWarps = RP == 16 ? 11 : 7;        // that compute
   static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kJoin = kWarps * RP * (D + 2) * 4; // outputs, references, sums
+  static constexpr int kRowFloats = D + 4;                // of an output that is joined: four rows apart, all banks
+  static constexpr int kJoin = kWarps * RP * (kRowFloats + 2) * 4;         // outputs, references, sums
   static constexpr int kQ = kSharedQ ? RP * (D * 2 + 4) : 0;
   static constexpr int kSmall = 2048;
   static constexpr int kRoom = (kCtas == 2 ? 112 * 1024 : 227 * 1024) - kJoin - kQ - kSmall;
@@ -134,7 +135,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
   constexpr int NT = C::NT, ST = C::kStages, W = C::kWarps, CK = C::kKeys, MK = CK / 16, MD = D / 16;
   extern __shared__ __align__(128) uint8_t smem[];
   float* const join = reinterpret_cast<float*>(smem + ST * C::kStage);
-  float* const tops = join + W * RP * D;
+  float* const tops = join + W * RP * C::kRowFloats;
   float* const sums = tops + W * RP;
   uint2* const q_s = reinterpret_cast<uint2*>(smem + ST * C::kStage + C::kJoin);
   float* const qf_s = reinterpret_cast<float*>(q_s + (C::kSharedQ ? RP * D / 4 : 0));
@@ -594,15 +595,17 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
             tops[w * RP + row] = -ref[nt][k];
             sums[w * RP + row] = (odd_rows >> (2 * nt + k) & 1u) != 0 && x > 0.0f ? kNan : x;
           }
-          // d = 2 MD lane / 4 + 2 i and the next
+          // elements lane / 4 * D / 8 + 2 i and the next, at 16 i + lane / 4 * 2 of the row,
+          // where a half warp's lie in all banks
+          float* const to = join + (w * RP + row) * C::kRowFloats + r8 * 2;
 #pragma unroll
-          for (int i = 0; i < MD; ++i)
-            *reinterpret_cast<float2*>(join + (w * RP + row) * D + r8 * (D / 8) + 2 * i) =
-                make_float2(o[i][nt][k], o[i][nt][k + 2]);
+          for (int i = 0; i < MD; ++i) *reinterpret_cast<float2*>(to + 16 * i) = make_float2(o[i][nt][k], o[i][nt][k + 2]);
         }
       named_sync(1, 32 * W);
       for (int u = tid - 32; u < it.nrows * (D / 4); u += 32 * W) {
-        const int row = u / (D / 4), d = u % (D / 4) * 4;
+        const int row = u / (D / 4), at4 = u % (D / 4);
+        // two pairs of elements, D / 8 apart
+        const int d = at4 % 4 * 2 * (D / 8) + at4 / 4 * 2;
         float top = kLowest;
 #pragma unroll
         for (int i = 0; i < W; ++i) top = fmaxf(top, tops[i * RP + row]);
@@ -611,7 +614,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
         for (int i = 0; i < W; ++i) {
           const float f = fast_exp2(tops[i * RP + row] - top);
           sum = fmaf(sums[i * RP + row], f, sum);
-          const float4 v = *reinterpret_cast<const float4*>(join + (i * RP + row) * D + d);
+          const float4 v = *reinterpret_cast<const float4*>(join + (i * RP + row) * C::kRowFloats + at4 * 4);
           y[0] = fmaf(v.x, f, y[0]);
           y[1] = fmaf(v.y, f, y[1]);
           y[2] = fmaf(v.z, f, y[2]);
@@ -621,15 +624,16 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
         const float ls = sum == 0.0f ? -INFINITY : top + log2f(sum);
         if (it.slot >= 0) {
           const int64_t at = static_cast<int64_t>(it.slot) * RP + row;
-          *reinterpret_cast<float4*>(ws_o + at * D + d) = make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-          if (d == 0) ws_lse[at] = ls;
+          *reinterpret_cast<float2*>(ws_o + at * D + d) = make_float2(y[0] * inv, y[1] * inv);
+          *reinterpret_cast<float2*>(ws_o + at * D + d + D / 8) = make_float2(y[2] * inv, y[3] * inv);
+          if (at4 == 0) ws_lse[at] = ls;
         } else {
           const int r = it.r0 + row;
           const int64_t at = static_cast<int64_t>(it.cu0 + r / G) * a.Hq + it.h * G + r % G;
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + d) =
-              a.f16 ? make_uint2(pack16<true>(y[0] * inv, y[1] * inv), pack16<true>(y[2] * inv, y[3] * inv))
-                    : make_uint2(pack16<false>(y[0] * inv, y[1] * inv), pack16<false>(y[2] * inv, y[3] * inv));
-          if (d == 0) a.lse[at] = ls * 0.6931471805599453f;
+          uint16_t* const to = static_cast<uint16_t*>(a.out) + at * D + d;
+          *reinterpret_cast<uint32_t*>(to) = a.f16 ? pack16<true>(y[0] * inv, y[1] * inv) : pack16<false>(y[0] * inv, y[1] * inv);
+          *reinterpret_cast<uint32_t*>(to + D / 8) = a.f16 ? pack16<true>(y[2] * inv, y[3] * inv) : pack16<false>(y[2] * inv, y[3] * inv);
+          if (at4 == 0) a.lse[at] = ls * 0.6931471805599453f;
         }
       }
       if (a.fault_site == 1 && w == 0) wait(sm.never, 0);
