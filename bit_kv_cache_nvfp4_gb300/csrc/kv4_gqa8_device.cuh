@@ -1,6 +1,6 @@
-// kv4_gqa8_device.cuh -- helpers of the attention over the 8-bit grouped-query
-// cache: TMA loads of cache pages, the FP8 tensor-core product, and the
-// splitting of 16-bit operands into E4M3 terms.
+// kv4_gqa8_device.cuh -- helpers of the attention over the grouped-query caches:
+// the work list of ragged batches, and, for the 8-bit one, TMA loads of cache pages,
+// the FP8 tensor-core product and the splitting of 16-bit operands into E4M3 terms.
 #pragma once
 
 #include <cuda.h>

@@ -94,7 +94,7 @@ struct Gqa8Args {
   const int32_t* page_table;
   int64_t pt_stride;
   int B, Hkv, D;
-  int each;                    // pages a thread block looks after (set by the launch)
+  int each;                    // pages (4-bit read-back: heads) of a thread block (set by the launch)
   int num_sms;
   uint8_t* pool;               // [num_pages, Hkv, 2, 64, D] E4M3 (4-bit cache: [.., 64, D / 2] E2M1)
   uint8_t* scales;             // [num_pages, Hkv, 2] E8M0 (4-bit cache: [.., 64, D / 16] E4M3)
