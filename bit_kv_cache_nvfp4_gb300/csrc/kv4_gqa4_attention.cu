@@ -94,7 +94,6 @@ struct FewSmall {
   // once the stage is for the page that the warp looks for.
   volatile uint32_t page[40];
   Gqa8Item items[4];
-  int blocks[32];             // of the pages that are loaded next
 };
 static_assert(sizeof(FewSmall) <= 2048, "FewSmall");
 
@@ -211,7 +210,8 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
 
   if (warp == 0) {
     // ==== work list and loads ====
-    uint32_t n_items = 0, n_pages = 0, n_loads = 0;       // pages; up to which lane 0 began copies
+    uint32_t n_items = 0, n_pages = 0, n_loads = 0;       // pages; up to which copies began
+    uint32_t stage = 0, empty_par = 1;                    // of the next page
     auto publish = [&](const Gqa8Item& it) {
       const int s = n_items & 3;
       wait(sm.item_empty[s], ((n_items >> 2) & 1) ^ 1);
@@ -234,32 +234,34 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
           if (phys < 0 || phys >= a.num_pages) flag_error(a.dev_err, kDevBadPage);
           else block = phys * a.Hkv + it.h;
         }
-        sm.blocks[lane] = block;
-        __syncwarp();
+        // (the whole warp walks the pages, so that what the copies take but the page
+        // itself stays uniform; whether the block gave up is looked at only where a
+        // stage is not free yet)
         const int n = min(32, c.n - i);
-        if (lane == 0) {
-          uint32_t stage = n_pages % ST, empty_par = (n_pages / ST & 1) ^ 1;
-          for (int k = 0; k < n; ++k) {
-            const int blk = sm.blocks[k];
+        for (int k = 0; k < n; ++k) {
+          const int64_t blk = __shfl_sync(0xFFFFFFFFu, block, k);
+          if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_addr(&sm.empty[stage]), empty_par))) {
             wait(sm.empty[stage], empty_par);
-            if (*dead) break;
-            sm.page[stage] = 2 * (n_pages + k) + (blk < 0);
-            n_loads = n_pages + k + 1;
+            if (__any_sync(0xFFFFFFFFu, *dead != 0)) break;
+          }
+          if (elect_one()) {
             const uint32_t bar = smem_addr(&sm.full[stage]), dst = smem_addr(smem) + stage * C::kStage;
+            sm.page[stage] = 2 * (n_pages + k) + (blk < 0);
             if (blk >= 0) {
               mbar_arrive_expect_tx(bar, C::kStage);
-              bulk_copy_g2s(dst, a.pool + static_cast<int64_t>(blk) * (2 * C::kCodes), 2 * C::kCodes, bar);
-              bulk_copy_g2s(dst + 2 * C::kCodes, a.scales + static_cast<int64_t>(blk) * (2 * C::kScales), 2 * C::kScales, bar);
+              bulk_copy_g2s(dst, a.pool + blk * (2 * C::kCodes), 2 * C::kCodes, bar);
+              bulk_copy_g2s(dst + 2 * C::kCodes, a.scales + blk * (2 * C::kScales), 2 * C::kScales, bar);
             } else {
               mbar_arrive(bar);
             }
-            if (++stage == ST) {
-              stage = 0;
-              empty_par ^= 1;
-            }
+          }
+          __syncwarp();
+          n_loads = n_pages + k + 1;
+          if (++stage == ST) {
+            stage = 0;
+            empty_par ^= 1;
           }
         }
-        __syncwarp();
         n_pages += n;
       }
     };
@@ -785,7 +787,7 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
     if (warp == 0) {
       // ==== work list and loads ====
       uint32_t n_items = 0, n_tiles = 0;
-      uint32_t n_sides = 0, n_loads = 0;                  // sides of pages; up to which lane 0 began copies
+      uint32_t n_sides = 0, n_loads = 0;                  // sides of pages; up to which copies began
       uint32_t st = 0, st_par = 1;                        // of the next side
       auto publish = [&](const Gqa8Item& it) {
         const int s = n_items & 1;
@@ -814,10 +816,14 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
             const int b[2] = {__shfl_sync(0xFFFFFFFFu, block, 2 * i), __shfl_sync(0xFFFFFFFFu, block, 2 * i + 1)};
 #pragma unroll
             for (int side = 0; side < 4; ++side) {        // K of both pages, then V
-              wait(sm.raw_empty[st], st_par);
-              __syncwarp();
-              if (lane == 0 && !*dead) {
-                n_loads = n_sides + 1;
+              // (the whole warp, so that what the copies take but the page itself stays
+              // uniform; whether the block gave up is looked at only where a stage is
+              // not free yet)
+              if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_addr(&sm.raw_empty[st]), st_par))) {
+                wait(sm.raw_empty[st], st_par);
+                if (__any_sync(0xFFFFFFFFu, *dead != 0)) return;
+              }
+              if (elect_one()) {
                 if (side == 0) {
                   // (the softmax of the tile eight before is done: this stage was, up
                   // to four tiles ago, one of the widening warps', which then had V of
@@ -837,7 +843,7 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
                 }
               }
               __syncwarp();
-              ++n_sides;
+              n_loads = ++n_sides;
               if (++st == NR) {
                 st = 0;
                 st_par ^= 1;
