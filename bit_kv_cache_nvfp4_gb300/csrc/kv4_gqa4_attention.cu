@@ -98,6 +98,22 @@ struct FewSmall {
 };
 static_assert(sizeof(FewSmall) <= 2048, "FewSmall");
 
+// This block's items.  Of 32 requests or fewer one warp adds up the work, and walks
+// what it has in registers; of more the block has added it up (sm_total).  In ints where
+// that cannot overflow: half the instructions of a chain that a short call waits for.
+template <typename Emit>
+__device__ __forceinline__ void walk_work(const Gqa8AttnArgs& a, const Gqa8Kind& kind, unsigned long long sm_total,
+                                          bool report, Gqa8Tail* tails, int lane, Emit&& emit) {
+  auto walk = [&](auto zero) {
+    using I = decltype(zero);
+    Gqa8Request q{};
+    I units = 0, total = static_cast<I>(sm_total);
+    if (a.B <= 32) total = gqa8_warp_total<I>(a, kind, report, lane, q, units);
+    gqa8_walk<I>(a, kind, total, tails, lane, emit, a.B <= 32, q, units);
+  };
+  if (a.narrow) walk(int{0});
+  else walk(int64_t{0});
+}
 // c = A B, c += A B.
 __device__ __forceinline__ void mma_16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                 uint32_t b0, uint32_t b1) {
@@ -177,7 +193,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
   // nothing has to be added up.
   const bool one_each = (a.pt_stride + 1) / 2 <= kWhole && static_cast<int64_t>(a.B) * a.Hkv <= gridDim.x;
   const Gqa8Kind kind{1, max_rows, RP, C::kCost, RP, C::kCost, 1};
-  if (!one_each) {
+  if (!one_each && a.B > 32) {
     gqa8_total(a, kind, blockIdx.x == 0, &sm.total);
     __syncthreads();
   }
@@ -276,7 +292,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
       const Gqa8Span sp = gqa8_span(a, r, G, 0, max(r.n * G, 1));
       if (r.n > 0) take(Gqa8Item{b, h, r.cu0, r.pos0, 0, r.n * G, sp.klo, sp.khi, sp.t0, sp.t0 + sp.nt, -1});
     } else {
-      gqa8_walk(a, kind, static_cast<int64_t>(sm.total), tails, lane, take);
+      walk_work(a, kind, sm.total, blockIdx.x == 0, tails, lane, take);
     }
     publish(Gqa8Item{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, -1});
     // every copy lands before the block's shared memory goes away
@@ -763,7 +779,7 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
   grid_launch_dependents();
   __syncthreads();
   const Gqa8Kind kind{min_rows, kAll, C::kRows, kManyCost, 128, kSharedCost, 2};
-  gqa8_total(a, kind, blockIdx.x == 0 && min_rows == 1, &sm.total);
+  if (a.B > 32) gqa8_total(a, kind, blockIdx.x == 0 && min_rows == 1, &sm.total);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -853,7 +869,7 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
           }
         }
       };
-      gqa8_walk(a, kind, static_cast<int64_t>(sm.total), tails, lane, [&](const Gqa8Item& it) {
+      walk_work(a, kind, sm.total, blockIdx.x == 0 && min_rows == 1, tails, lane, [&](const Gqa8Item& it) {
         publish(it);
         load_item(it);
       });
@@ -1410,9 +1426,19 @@ size_t few_bytes(int rows, int D, int sms) {
   return rows == 0 ? 0 : (part_bytes(kFewCtas * sms, rows, D) + 255) / 256 * 256;
 }
 
+// Whether the units of a call's items, of so many rows, fit an int whatever the
+// lengths on the device are.
+bool narrow(const Gqa8AttnArgs& a, int rows, int units_a_tile, int cost) {
+  const double tall = static_cast<double>(std::min<int64_t>(a.max_new, a.n_tokens)) * (a.Hq / a.Hkv) / rows + 1;
+  const double tiles = static_cast<double>(a.pt_stride) / 2 + 1;
+  return a.B * tall * a.Hkv * (tiles * units_a_tile + cost) < (1 << 30);
+}
+
 template <int D, int RP>
-cudaError_t launch_few(const Gqa8AttnArgs& a, void* ws, cudaStream_t stream) {
+cudaError_t launch_few(const Gqa8AttnArgs& args, void* ws, cudaStream_t stream) {
   using C = FewCfg<D, RP>;
+  Gqa8AttnArgs a = args;
+  a.narrow = narrow(a, RP, 1, C::kCost);
   cudaError_t e = prepare_kernel<few4_kernel<D, RP>>(C::kSmem, 0);
   if (e != cudaSuccess) return e;
   // (no more blocks than there can be tiles, or items where none is ever cut)
@@ -1424,8 +1450,10 @@ cudaError_t launch_few(const Gqa8AttnArgs& a, void* ws, cudaStream_t stream) {
 }
 
 template <int D, bool F16>
-cudaError_t launch_many(const Gqa8AttnArgs& a, int min_rows, void* ws, cudaStream_t stream) {
+cudaError_t launch_many(const Gqa8AttnArgs& args, int min_rows, void* ws, cudaStream_t stream) {
   using C = ManyCfg<D>;
+  Gqa8AttnArgs a = args;
+  a.narrow = narrow(a, C::kRows, 2, kManyCost);
   cudaError_t e = prepare_kernel<many4_kernel<D, F16>>(C::kSmem, kLaunchRegs);
   if (e != cudaSuccess) return e;
   const Parts p = parts_at(ws, a.num_sms, C::kRows, D);

@@ -278,17 +278,22 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
   return a / b;
 }
+__device__ __forceinline__ int quotient(int a, int b) {
+  return static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
 
 // Units of the requests of a warp's lanes: a lane by itself where it has few
-// row groups, the warp together for the others.
-__device__ __forceinline__ int64_t gqa8_units(const Gqa8AttnArgs& a, const Gqa8Request& q,
+// row groups, the warp together for the others.  (I: int64_t, or int where no sum of
+// units, whatever the lengths, can leave it.)
+template <typename I = int64_t>
+__device__ __forceinline__ I gqa8_units(const Gqa8AttnArgs& a, const Gqa8Request& q,
                                               const Gqa8Kind& kind, int G, int lane) {
   const int R = q.n * G, groups = (R + kind.rows - 1) / kind.rows;
   auto units = [&](const Gqa8Request& r, int i, int n_rows) {
     const int r0 = i * kind.rows, r1 = min(n_rows, r0 + kind.rows);
-    return static_cast<int64_t>(gqa8_span(a, r, G, r0, r1).nt) * kind.units(r1 - r0) + kind.beyond(r1 - r0);
+    return static_cast<I>(gqa8_span(a, r, G, r0, r1).nt) * kind.units(r1 - r0) + kind.beyond(r1 - r0);
   };
-  int64_t u = 0;
+  I u = 0;
   if (groups <= 2)
     for (int i = 0; i < groups; ++i) u += units(q, i, R);
   for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, groups > 2); todo != 0; todo &= todo - 1) {
@@ -299,7 +304,7 @@ __device__ __forceinline__ int64_t gqa8_units(const Gqa8AttnArgs& a, const Gqa8R
     r.pos0 = __shfl_sync(0xFFFFFFFFu, q.pos0, l);
     r.held = __shfl_sync(0xFFFFFFFFu, q.held, l);
     const int gr = __shfl_sync(0xFFFFFFFFu, groups, l);
-    int64_t v = 0;
+    I v = 0;
     for (int i = lane; i < gr; i += 32) v += units(r, i, r.n * G);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
@@ -308,16 +313,29 @@ __device__ __forceinline__ int64_t gqa8_units(const Gqa8AttnArgs& a, const Gqa8R
   return u * a.Hkv;
 }
 // Sum over all requests, added to *total by every warp of the block.
+template <typename I = int64_t>
 __device__ __forceinline__ void gqa8_total(const Gqa8AttnArgs& a, const Gqa8Kind& kind, bool report,
                                            unsigned long long* total) {
   const int lane = threadIdx.x & 31;
-  int64_t u = 0;
+  I u = 0;
   for (int base = threadIdx.x & ~31; base < a.B; base += blockDim.x)
-    u += gqa8_units(a, gqa8_request(a, base + lane, kind.min_rows, kind.max_rows, report), kind,
+    u += gqa8_units<I>(a, gqa8_request(a, base + lane, kind.min_rows, kind.max_rows, report), kind,
                     a.Hq / a.Hkv, lane);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, off);
   if (lane == 0 && u > 0) atomicAdd(total, static_cast<unsigned long long>(u));
+}
+
+// The same by one warp, for 32 requests or fewer: theirs, and their units.
+template <typename I>
+__device__ __forceinline__ I gqa8_warp_total(const Gqa8AttnArgs& a, const Gqa8Kind& kind, bool report, int lane,
+                                             Gqa8Request& q, I& units) {
+  q = gqa8_request(a, lane, kind.min_rows, kind.max_rows, report);
+  units = gqa8_units<I>(a, q, kind, a.Hq / a.Hkv, lane);
+  I u = units;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, off);
+  return u;
 }
 
 struct Gqa8Item {
@@ -342,35 +360,42 @@ constexpr float kLowest = -3e38f;
 // Where the border at unit u cuts an item of nt tiles of `each` units that
 // begins at unit `begin`: tiles before the border, 0 .. nt (0 and nt also where
 // it is not in the item at all).
-__device__ __forceinline__ int gqa8_cut(int64_t u, int64_t begin, int nt, int each, int cost) {
-  const int64_t x = u - begin, all = static_cast<int64_t>(nt) * each + cost;
+template <typename I>
+__device__ __forceinline__ int gqa8_cut(I u, I begin, int nt, int each, int cost) {
+  const I x = u - begin, all = static_cast<I>(nt) * each + cost;
   if (x <= 0) return 0;
   if (x >= all) return nt;
   if (nt <= kWhole) return 2 * x <= all ? 0 : nt;
-  const int64_t t = x <= cost ? 0 : quotient(x - cost, each);
+  const I t = x <= cost ? I{0} : quotient(x - cost, static_cast<I>(each));
   return t < kLeast ? 0 : t > nt - kLeast ? nt : static_cast<int>(t);
 }
 
 // The items of this block, in order, to `emit` (whole warp), of `total` units.
-// Also leaves this block's tail.
-template <typename Emit>
-__device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, const Gqa8Kind& kind, int64_t total,
-                                          Gqa8Tail* tails, int lane, Emit&& emit) {
+// Also leaves this block's tail.  known: the caller has the first 32 requests and
+// their units.
+template <typename I = int64_t, typename Emit>
+__device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, const Gqa8Kind& kind, I total,
+                                          Gqa8Tail* tails, int lane, Emit&& emit,
+                                          bool known = false, Gqa8Request q0 = {}, I units0 = 0) {
   const int G = a.Hq / a.Hkv, blocks = gridDim.x, me = blockIdx.x;
   // (no share so small that a long item's pieces would cost more to join than
   // they save; where no item is ever cut, as small as one item)
-  const int64_t least = (a.pt_stride + 1) / 2 <= kWhole ? 1 : kWhole * kind.tile;
-  const int64_t per = max(quotient(total + blocks - 1, blocks), least);
-  const int64_t u0 = me * per, u1 = u0 + per;
+  const I least = static_cast<I>((a.pt_stride + 1) / 2 <= kWhole ? 1 : kWhole * kind.tile);
+  const I per = max(quotient(total + blocks - 1, static_cast<I>(blocks)), least);
+  const I u0 = me * per, u1 = u0 + per;
   bool tail = false;
-  int64_t acc = 0;
+  I acc = 0;
   for (int base = 0; base < a.B && acc < u1 && u0 < total; base += 32) {
-    const Gqa8Request q = gqa8_request(a, base + lane, kind.min_rows, kind.max_rows, false);
-    const int64_t units = gqa8_units(a, q, kind, G, lane);
-    int64_t end = units;
+    Gqa8Request q = q0;
+    I units = units0;
+    if (!known || base > 0) {
+      q = gqa8_request(a, base + lane, kind.min_rows, kind.max_rows, false);
+      units = gqa8_units<I>(a, q, kind, G, lane);
+    }
+    I end = units;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, end, off);
+      const I v = __shfl_up_sync(0xFFFFFFFFu, end, off);
       if (lane >= off) end += v;
     }
     end += acc;
@@ -383,22 +408,22 @@ __device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, const Gqa8Kind&
       r.n = __shfl_sync(0xFFFFFFFFu, q.n, l);
       r.pos0 = __shfl_sync(0xFFFFFFFFu, q.pos0, l);
       r.held = __shfl_sync(0xFFFFFFFFu, q.held, l);
-      int64_t first = __shfl_sync(0xFFFFFFFFu, end - units, l);
+      I first = __shfl_sync(0xFFFFFFFFu, end - units, l);
       const int R = r.n * G, groups = (R + kind.rows - 1) / kind.rows;
       for (int g0 = 0; g0 < groups && first < u1; g0 += 32) {
         // a lane's row group, and where its items begin
         const int gi = g0 + lane;
         Gqa8Span sp{0, 0, 0, 0};
-        int64_t w = 0;
+        I w = 0;
         if (gi < groups) {
           sp = gqa8_span(a, r, G, gi * kind.rows, min(R, (gi + 1) * kind.rows));
           const int n = min(kind.rows, R - gi * kind.rows);
-          w = (static_cast<int64_t>(sp.nt) * kind.units(n) + kind.beyond(n)) * a.Hkv;
+          w = (static_cast<I>(sp.nt) * kind.units(n) + kind.beyond(n)) * a.Hkv;
         }
-        int64_t g_end = w;
+        I g_end = w;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-          const int64_t v = __shfl_up_sync(0xFFFFFFFFu, g_end, off);
+          const I v = __shfl_up_sync(0xFFFFFFFFu, g_end, off);
           if (lane >= off) g_end += v;
         }
         g_end += first;
@@ -407,12 +432,12 @@ __device__ __forceinline__ void gqa8_walk(const Gqa8AttnArgs& a, const Gqa8Kind&
           const int gl = __ffs(gtodo) - 1;
           const int klo = __shfl_sync(0xFFFFFFFFu, sp.klo, gl), khi = __shfl_sync(0xFFFFFFFFu, sp.khi, gl);
           const int t0 = __shfl_sync(0xFFFFFFFFu, sp.t0, gl), nt = __shfl_sync(0xFFFFFFFFu, sp.nt, gl);
-          const int64_t at = __shfl_sync(0xFFFFFFFFu, g_end - w, gl);
+          const I at = __shfl_sync(0xFFFFFFFFu, g_end - w, gl);
           const int r0 = (g0 + gl) * kind.rows, nrows = min(kind.rows, R - r0), upt = kind.units(nrows);
           const int cost = kind.beyond(nrows);
-          const int64_t each = static_cast<int64_t>(nt) * upt + cost;
+          const I each = static_cast<I>(nt) * upt + cost;
           const int h0 = at < u0 ? static_cast<int>(quotient(u0 - at, each)) : 0;
-          int64_t begin = at + h0 * each;
+          I begin = at + h0 * each;
           for (int h = h0; h < a.Hkv && begin < u1; ++h, begin += each) {
             const int tb = gqa8_cut(u0, begin, nt, upt, cost), te = gqa8_cut(u1, begin, nt, upt, cost);
             int slot = -1;
