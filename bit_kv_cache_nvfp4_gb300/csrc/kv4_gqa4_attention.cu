@@ -684,7 +684,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
 //   S[128 rows x 128 keys] = Q . K^T     kind::f16, both from shared memory
 //   O[128 rows x D] += P . V             kind::f16, P from TMEM
 // K and V are widened to f16 once per tile by four warps (exact: code * scale has 6
-// significant bits), from codes that bulk copies bring, a side of a page at a time;
+// significant bits), from codes that bulk copies bring, a side of a tile at a time;
 // q is exact in f16 but for elements below 2^-22 of its row's largest.  The chain
 // scores -> softmax -> P -> O, next scores of a row tile is what the other tile's
 // products have to cover, so two threads share a row, one for each page of the
@@ -702,13 +702,14 @@ template <int D_>
 struct ManyCfg {
   static constexpr int D = D_, kRows = 256;
   static constexpr int kTile = kTileKeys * D * 2;         // of K, of V, or of 128 rows of q in f16
-  static constexpr int kCodes = kPage * D / 2, kScales = kPage * D / 16, kSide = kCodes + kScales;
-  static constexpr int kSmall = 9216;
+  static constexpr int kCodes = kPage * D / 2, kScales = kPage * D / 16;   // of a page's side
+  static constexpr int kSide = 2 * (kCodes + kScales);    // of a tile's: codes of both pages, then scales
+  static constexpr int kSmall = 6144;
   static constexpr int kRoom = 227 * 1024 - 1024 - 6 * kTile - kSmall;
-  static constexpr int kRaw = kRoom / kSide < 16 ? kRoom / kSide : 16;     // sides of pages on their way
+  static constexpr int kRaw = kRoom / kSide < 8 ? kRoom / kSide : 8;       // sides of tiles on their way
   static constexpr int kSmem = 6 * kTile + kRaw * kSide + kSmall + 1024;
 };
-static_assert(ManyCfg<128>::kRaw >= 4 && ManyCfg<64>::kRaw <= 16, "a tile's sides are in the ring together, four tiles' at most");
+static_assert(ManyCfg<128>::kRaw >= 3 && ManyCfg<64>::kRaw <= 8, "more than a tile is on its way, four tiles at most");
 constexpr int kManyThreads = 768;
 constexpr uint32_t kSoftmaxRegs = 96, kIssueRegs = 40, kWidenRegs = 56, kLaunchRegs = 80;
 static_assert(4 * kSoftmaxRegs + kIssueRegs + kWidenRegs <= 6 * kLaunchRegs, "register shares draw on the launch's");
@@ -719,7 +720,7 @@ static_assert(4 * kSoftmaxRegs + kIssueRegs + kWidenRegs <= 6 * kLaunchRegs, "re
 constexpr int kManyCost = 10, kSharedCost = 4;
 
 struct ManySmall {
-  uint64_t raw_full[16], raw_empty[16], k_full[2], k_empty[2], v_full[2], v_empty[2], item_full[2], item_empty[2],
+  uint64_t raw_full[8], raw_empty[8], k_full[2], k_empty[2], v_full[2], v_empty[2], item_full[2], item_empty[2],
       gone_full[8], q_full[2], s_full[2], p_full[2][2], o_full[2], never;
   unsigned long long total;
   uint32_t tmem;
@@ -727,10 +728,11 @@ struct ManySmall {
   int gone[8][2];             // per tile and page: not there
   Gqa8Item items[2];
   float qf[2][128];           // sm_scale log2(e) 2^eq of a row, NaN where q is not finite
-  float top[2][2][2][128];    // largest score of a half row, by row tile and tile parity
-  float last[2][3][128];      // at an item's end: sums of both halves, reference
+  float top[2][2][2][128];    // largest score of a half row, by row tile and tile parity;
+                              //   at an item's end sums of both halves and reference (last)
+  __device__ float& last(int qt, int k, int row) { return top[qt][k >> 1][k & 1][row]; }
 };
-static_assert(sizeof(ManySmall) <= 9216, "ManySmall");
+static_assert(sizeof(ManySmall) <= 6144, "ManySmall");
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kManyThreads, 1)
@@ -804,7 +806,7 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
     if (warp == 0) {
       // ==== work list and loads ====
       uint32_t n_items = 0, n_tiles = 0;
-      uint32_t n_sides = 0, n_loads = 0;                  // sides of pages; up to which copies began
+      uint32_t n_sides = 0, n_loads = 0;                  // sides of tiles; up to which copies began
       uint32_t st = 0, st_par = 1;                        // of the next side
       auto publish = [&](const Gqa8Item& it) {
         const int s = n_items & 1;
@@ -832,7 +834,7 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
           for (int i = 0; i < nt; ++i, ++n_tiles) {
             const int b[2] = {__shfl_sync(0xFFFFFFFFu, block, 2 * i), __shfl_sync(0xFFFFFFFFu, block, 2 * i + 1)};
 #pragma unroll
-            for (int side = 0; side < 4; ++side) {        // K of both pages, then V
+            for (int side = 0; side < 2; ++side) {        // K, V
               // (the whole warp, so that what the copies take but the page itself stays
               // uniform; whether the block gave up is looked at only where a stage is
               // not free yet)
@@ -850,14 +852,16 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
                   mbar_arrive(smem_addr(&sm.gone_full[n_tiles & 7]));
                 }
                 const uint32_t bar = smem_addr(&sm.raw_full[st]), dst = smem_addr(raw_s) + st * C::kSide;
-                const int64_t blk = 2 * static_cast<int64_t>(b[side & 1]) + (side >> 1);
-                if (blk >= 0) {
-                  mbar_arrive_expect_tx(bar, C::kSide);
-                  bulk_copy_g2s(dst, a.pool + blk * C::kCodes, C::kCodes, bar);
-                  bulk_copy_g2s(dst + C::kCodes, a.scales + blk * C::kScales, C::kScales, bar);
-                } else {
-                  mbar_arrive(bar);
-                }
+                const uint32_t there = (b[0] >= 0) + (b[1] >= 0);
+                if (there > 0) mbar_arrive_expect_tx(bar, there * (C::kCodes + C::kScales));
+                else mbar_arrive(bar);
+#pragma unroll
+                for (int pg = 0; pg < 2; ++pg)
+                  if (b[pg] >= 0) {
+                    const int64_t blk = 2 * static_cast<int64_t>(b[pg]) + side;
+                    bulk_copy_g2s(dst + pg * C::kCodes, a.pool + blk * C::kCodes, C::kCodes, bar);
+                    bulk_copy_g2s(dst + 2 * C::kCodes + pg * C::kScales, a.scales + blk * C::kScales, C::kScales, bar);
+                  }
               }
               __syncwarp();
               n_loads = ++n_sides;
@@ -1081,15 +1085,14 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
           for (int side = 0; side < 2; ++side) {          // K, V
             uint4 w[2][kPieces];
             uint32_t sc[2][kPieces];
-            const uint32_t st1 = st + 1 == NR ? 0 : st + 1, par1 = st + 1 == NR ? st_par ^ 1 : st_par;
+            wait(sm.raw_full[st], st_par);
+            const uint8_t* const src = raw_s + st * C::kSide;
 #pragma unroll
             for (int pg = 0; pg < 2; ++pg) {
-              wait(sm.raw_full[pg == 0 ? st : st1], pg == 0 ? st_par : par1);
-              const uint8_t* const src = raw_s + (pg == 0 ? st : st1) * C::kSide;
 #pragma unroll
               for (int c = 0; c < kPieces; ++c) {
-                w[pg][c] = *reinterpret_cast<const uint4*>(src + from[c]);
-                sc[pg][c] = *reinterpret_cast<const uint16_t*>(src + C::kCodes + from[c] / 8);
+                w[pg][c] = *reinterpret_cast<const uint4*>(src + pg * C::kCodes + from[c]);
+                sc[pg][c] = *reinterpret_cast<const uint16_t*>(src + 2 * C::kCodes + pg * C::kScales + from[c] / 8);
               }
               const bool gone = sm.gone[j & 7][pg] != 0;
               if (gone || pg * kPage < lo || pg * kPage + kPage > hi) {
@@ -1100,14 +1103,13 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
                 for (int c = 0; c < kPieces; ++c) sc[pg][c] = live ? sc[pg][c] : 0u;
               }
             }
-            // (the stages go back before their codes are worked on)
+            // (the stage goes back before its codes are worked on)
             __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(smem_addr(&sm.raw_empty[st]));
-              mbar_arrive(smem_addr(&sm.raw_empty[st1]));
+            if (lane == 0) mbar_arrive(smem_addr(&sm.raw_empty[st]));
+            if (++st == NR) {
+              st = 0;
+              st_par ^= 1;
             }
-            st = st1 + 1 == NR ? 0 : st1 + 1;
-            st_par = st1 + 1 == NR ? par1 ^ 1 : par1;
             wait(side == 0 ? sm.k_empty[j & 1] : sm.v_empty[j & 1], ((j >> 1) & 1) ^ 1);
             uint8_t* const o = tile + side * (2 * C::kTile);
 #pragma unroll
@@ -1300,8 +1302,9 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
         l += acc[0].x + acc[0].y;
       }
       j += nt;
-      sm.last[qt][half][row] = l;
-      if (half == 0) sm.last[qt][2][row] = mref;
+      named_sync(bar, 64);                                // (`last` lies where the other half reads `top`)
+      sm.last(qt, half, row) = l;
+      if (half == 0) sm.last(qt, 2, row) = mref;
       if (first < it.t_end) {
         wait(sm.o_full[qt], n_work & 1);
         ++n_work;
@@ -1316,11 +1319,11 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
       // the same rows; both halves read the same numbers
       const int ta = shared ? 0 : qt;
       float wa = 1.0f, wb = 0.0f, lb = 0.0f;
-      mref = sm.last[ta][2][row];
-      l = sm.last[ta][0][row] + sm.last[ta][1][row];
+      mref = sm.last(ta, 2, row);
+      l = sm.last(ta, 0, row) + sm.last(ta, 1, row);
       if (shared) {
-        lb = sm.last[1][0][row] + sm.last[1][1][row];
-        const float mb = sm.last[1][2][row], to = fmaxf(mref, mb);
+        lb = sm.last(1, 0, row) + sm.last(1, 1, row);
+        const float mb = sm.last(1, 2, row), to = fmaxf(mref, mb);
         wa = fast_exp2(mref - to);
         wb = fast_exp2(mb - to);
         mref = to;
