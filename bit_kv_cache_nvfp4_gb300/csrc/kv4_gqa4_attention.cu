@@ -99,20 +99,17 @@ struct FewSmall {
 static_assert(sizeof(FewSmall) <= 2048, "FewSmall");
 
 // This block's items.  Of 32 requests or fewer one warp adds up the work, and walks
-// what it has in registers; of more the block has added it up (sm_total).  In ints where
-// that cannot overflow: half the instructions of a chain that a short call waits for.
-template <typename Emit>
+// what it has in registers; of more the block has added it up (sm_total).  I: int where
+// no sum of units can leave it, half the instructions of a chain that a short call waits
+// for (8 requests of 3000 tokens 15.8 us against 16.2, in replays).  Not both in one
+// kernel: its code comes from memory at a first call, 5 us more than for one of them.
+template <typename I, typename Emit>
 __device__ __forceinline__ void walk_work(const Gqa8AttnArgs& a, const Gqa8Kind& kind, unsigned long long sm_total,
                                           bool report, Gqa8Tail* tails, int lane, Emit&& emit) {
-  auto walk = [&](auto zero) {
-    using I = decltype(zero);
-    Gqa8Request q{};
-    I units = 0, total = static_cast<I>(sm_total);
-    if (a.B <= 32) total = gqa8_warp_total<I>(a, kind, report, lane, q, units);
-    gqa8_walk<I>(a, kind, total, tails, lane, emit, a.B <= 32, q, units);
-  };
-  if (a.narrow) walk(int{0});
-  else walk(int64_t{0});
+  Gqa8Request q{};
+  I units = 0, total = static_cast<I>(sm_total);
+  if (a.B <= 32) total = gqa8_warp_total<I>(a, kind, report, lane, q, units);
+  gqa8_walk<I>(a, kind, total, tails, lane, emit, a.B <= 32, q, units);
 }
 // c = A B, c += A B.
 __device__ __forceinline__ void mma_16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -156,7 +153,7 @@ __device__ __forceinline__ uint32_t widen_q(bool f16, const uint4 (&w)[2], float
   return f16 ? widen16<true>(w, x) : widen16<false>(w, x);
 }
 
-template <int D, int RP>
+template <int D, int RP, typename I>
 __global__ void __launch_bounds__(FewCfg<D, RP>::kThreads, FewCfg<D, RP>::kCtas)
 few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws_lse, float* ws_o) {
   using C = FewCfg<D, RP>;
@@ -292,7 +289,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
       const Gqa8Span sp = gqa8_span(a, r, G, 0, max(r.n * G, 1));
       if (r.n > 0) take(Gqa8Item{b, h, r.cu0, r.pos0, 0, r.n * G, sp.klo, sp.khi, sp.t0, sp.t0 + sp.nt, -1});
     } else {
-      walk_work(a, kind, sm.total, blockIdx.x == 0, tails, lane, take);
+      walk_work<I>(a, kind, sm.total, blockIdx.x == 0, tails, lane, take);
     }
     publish(Gqa8Item{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, -1});
     // every copy lands before the block's shared memory goes away
@@ -692,12 +689,12 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
 // rescaled, when the maximum rises by more than 2^6 (p stays below 2^14, f16's top
 // is 2^16).
 //
-// Measured (32 heads over 8, D = 128, bf16): 2 x 2048 new tokens over up to 16384 632 us,
-// 1.28 PFLOP/s, 68 % of the measured bf16 rate; without the widening, on whatever the
-// tiles hold, 563.  What it costs is the time of its chain (codes, f16, fence, products)
+// Measured (32 heads over 8, D = 128, bf16): 2 x 2048 new tokens over up to 16384 622 us,
+// 1.30 PFLOP/s, 69 % of the measured bf16 rate; without the widening, on whatever the
+// tiles hold, 563 (of 632 then).  What it costs is the time of its chain (codes, f16, fence, products)
 // rather than its instructions: two warps took 1040 us, four 814, a page's pieces at
 // fixed places 698, both pages together 674, and the softmax with 96 registers in place
-// of 88 645.  A prompt of 8192 489 us, 1.12 PFLOP/s.
+// of 88 645.  A prompt of 8192 481 us, 1.14 PFLOP/s.
 template <int D_>
 struct ManyCfg {
   static constexpr int D = D_, kRows = 256;
@@ -711,7 +708,9 @@ struct ManyCfg {
 };
 static_assert(ManyCfg<128>::kRaw >= 3 && ManyCfg<64>::kRaw <= 8, "more than a tile is on its way, four tiles at most");
 constexpr int kManyThreads = 768;
-constexpr uint32_t kSoftmaxRegs = 96, kIssueRegs = 40, kWidenRegs = 56, kLaunchRegs = 80;
+// (One head's 64 rows: 109 us with 40 and 56 registers, 107 with 48 and 48, 103 so; with
+// 88 for the softmax chunks take 5 % more.)
+constexpr uint32_t kSoftmaxRegs = 96, kIssueRegs = 32, kWidenRegs = 64, kLaunchRegs = 80;
 static_assert(4 * kSoftmaxRegs + kIssueRegs + kWidenRegs <= 6 * kLaunchRegs, "register shares draw on the launch's");
 
 // What an item takes beyond its tiles (q in, first scores, last product, output),
@@ -734,7 +733,7 @@ struct ManySmall {
 };
 static_assert(sizeof(ManySmall) <= 6144, "ManySmall");
 
-template <int D, bool F16>
+template <int D, bool F16, typename I>
 __global__ void __launch_bounds__(kManyThreads, 1)
 many4_kernel(const Gqa8AttnArgs a, const int min_rows,
             Gqa8Tail* tails, float* ws_lse, float* ws_o) {
@@ -873,7 +872,7 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
           }
         }
       };
-      walk_work(a, kind, sm.total, blockIdx.x == 0 && min_rows == 1, tails, lane, [&](const Gqa8Item& it) {
+      walk_work<I>(a, kind, sm.total, blockIdx.x == 0 && min_rows == 1, tails, lane, [&](const Gqa8Item& it) {
         publish(it);
         load_item(it);
       });
@@ -1437,31 +1436,38 @@ bool narrow(const Gqa8AttnArgs& a, int rows, int units_a_tile, int cost) {
   return a.B * tall * a.Hkv * (tiles * units_a_tile + cost) < (1 << 30);
 }
 
-template <int D, int RP>
-cudaError_t launch_few(const Gqa8AttnArgs& args, void* ws, cudaStream_t stream) {
+template <int D, int RP, typename I>
+cudaError_t launch_few(const Gqa8AttnArgs& a, void* ws, cudaStream_t stream) {
   using C = FewCfg<D, RP>;
-  Gqa8AttnArgs a = args;
-  a.narrow = narrow(a, RP, 1, C::kCost);
-  cudaError_t e = prepare_kernel<few4_kernel<D, RP>>(C::kSmem, 0);
+  cudaError_t e = prepare_kernel<few4_kernel<D, RP, I>>(C::kSmem, 0);
   if (e != cudaSuccess) return e;
   // (no more blocks than there can be tiles, or items where none is ever cut)
   const int64_t tiles = (a.pt_stride + 1) / 2, most = a.B * static_cast<int64_t>(a.Hkv) * (tiles <= kWhole ? 1 : tiles);
   const int blocks = static_cast<int>(std::min<int64_t>(a.num_sms * C::kCtas, most));
   const Parts p = parts_at(ws, blocks, RP, D);
-  e = launch_pdl(few4_kernel<D, RP>, blocks, C::kThreads, C::kSmem, stream, 1, a, RP, p.tails, p.lse, p.o);
+  e = launch_pdl(few4_kernel<D, RP, I>, blocks, C::kThreads, C::kSmem, stream, 1, a, RP, p.tails, p.lse, p.o);
   return e != cudaSuccess ? e : launch_merge(merge_few_kernel<D>, a, blocks, RP, RP, p, stream);
 }
+template <int D, int RP>
+cudaError_t launch_few(const Gqa8AttnArgs& a, cudaStream_t stream) {
+  return narrow(a, RP, 1, FewCfg<D, RP>::kCost) ? launch_few<D, RP, int>(a, a.ws, stream)
+                                                : launch_few<D, RP, int64_t>(a, a.ws, stream);
+}
 
-template <int D, bool F16>
-cudaError_t launch_many(const Gqa8AttnArgs& args, int min_rows, void* ws, cudaStream_t stream) {
+template <int D, bool F16, typename I>
+cudaError_t launch_many(const Gqa8AttnArgs& a, int min_rows, void* ws, cudaStream_t stream) {
   using C = ManyCfg<D>;
-  Gqa8AttnArgs a = args;
-  a.narrow = narrow(a, C::kRows, 2, kManyCost);
-  cudaError_t e = prepare_kernel<many4_kernel<D, F16>>(C::kSmem, kLaunchRegs);
+  cudaError_t e = prepare_kernel<many4_kernel<D, F16, I>>(C::kSmem, kLaunchRegs);
   if (e != cudaSuccess) return e;
   const Parts p = parts_at(ws, a.num_sms, C::kRows, D);
-  e = launch_pdl(many4_kernel<D, F16>, a.num_sms, kManyThreads, C::kSmem, stream, 1, a, min_rows, p.tails, p.lse, p.o);
+  e = launch_pdl(many4_kernel<D, F16, I>, a.num_sms, kManyThreads, C::kSmem, stream, 1, a, min_rows, p.tails, p.lse,
+                 p.o);
   return e != cudaSuccess ? e : launch_merge(merge_many_kernel<D>, a, a.num_sms, C::kRows / 32, C::kRows, p, stream);
+}
+template <int D, bool F16>
+cudaError_t launch_many(const Gqa8AttnArgs& a, int min_rows, void* ws, cudaStream_t stream) {
+  return narrow(a, ManyCfg<D>::kRows, 2, kManyCost) ? launch_many<D, F16, int>(a, min_rows, ws, stream)
+                                                    : launch_many<D, F16, int64_t>(a, min_rows, ws, stream);
 }
 
 template <int D>
@@ -1469,14 +1475,14 @@ cudaError_t launch_d(const Gqa8AttnArgs& a, cudaStream_t stream) {
   const int G = a.Hq / a.Hkv, rows = few_rows(a.max_new, G, D);
   cudaError_t e = cudaSuccess;
   switch (rows) {
-    case 8: e = launch_few<D, 8>(a, a.ws, stream); break;
-    case 16: e = launch_few<D, 16>(a, a.ws, stream); break;
-    case 24: e = launch_few<D, 24>(a, a.ws, stream); break;
-    case 32: e = launch_few<D, 32>(a, a.ws, stream); break;
+    case 8: e = launch_few<D, 8>(a, stream); break;
+    case 16: e = launch_few<D, 16>(a, stream); break;
+    case 24: e = launch_few<D, 24>(a, stream); break;
+    case 32: e = launch_few<D, 32>(a, stream); break;
   }
   if constexpr (D == 64) {
-    if (rows == 40) e = launch_few<D, 40>(a, a.ws, stream);
-    else if (rows == 48) e = launch_few<D, 48>(a, a.ws, stream);
+    if (rows == 40) e = launch_few<D, 40>(a, stream);
+    else if (rows == 48) e = launch_few<D, 48>(a, stream);
   }
   if (e != cudaSuccess || static_cast<int64_t>(a.max_new) * G <= rows) return e;
   void* const ws = static_cast<uint8_t*>(a.ws) + few_bytes(rows, D, a.num_sms);

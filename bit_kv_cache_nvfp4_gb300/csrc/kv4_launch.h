@@ -126,7 +126,6 @@ struct Gqa8AttnArgs {
   uint64_t timeout_ns;
   int fault_site;
   int num_sms;
-  int narrow;                  // units of work, whatever the lengths, fit an int (4-bit cache)
 };
 
 // Rotary positions (kv4_rotary).

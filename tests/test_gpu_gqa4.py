@@ -417,6 +417,19 @@ def test_attention_flags_a_request_beyond_max_new(wide):
     assert (out[1:4] == 3).all() and (lse[1:4] == 3).all()
 
 
+@pytest.mark.parametrize("B,columns,d", [(64, 1 << 19, 128), (32, 1 << 20, 64)])
+def test_attention_by_tables_with_room_for_more_than_an_int_of_work(B, columns, d):
+    """The tables could name 2^30 units of work and more, though the requests are
+    short: single tokens, drafts and a prompt's chunk."""
+    news = [300, 1, 0, 9, 2, 64] + [1] * (B - 6)
+    lens = [333, 70, 40, 9, 129, 64] + [1 + 37 * i % 500 for i in range(B - 6)]
+    c = ref.Cache(lens, 8, d, dev(), seed=B)
+    wide = torch.full((B, columns), -1, dtype=torch.int32, device=c.pool.device)
+    wide[:, :c.page_table.shape[1]] = c.page_table
+    c.page_table = wide
+    assert check_attention(c, news, 32, BF16, seed=B)[0] == 0
+
+
 # ---------------------------------------------------------------------------
 # every tile counts
 # ---------------------------------------------------------------------------
