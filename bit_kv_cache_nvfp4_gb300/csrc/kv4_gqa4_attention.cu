@@ -689,12 +689,12 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
 // rescaled, when the maximum rises by more than 2^6 (p stays below 2^14, f16's top
 // is 2^16).
 //
-// Measured (32 heads over 8, D = 128, bf16): 2 x 2048 new tokens over up to 16384 622 us,
-// 1.30 PFLOP/s, 69 % of the measured bf16 rate; without the widening, on whatever the
+// Measured (32 heads over 8, D = 128, bf16): 2 x 2048 new tokens over up to 16384 607 us,
+// 1.34 PFLOP/s, 71 % of the measured bf16 rate; without the widening, on whatever the
 // tiles hold, 563 (of 632 then).  What it costs is the time of its chain (codes, f16, fence, products)
 // rather than its instructions: two warps took 1040 us, four 814, a page's pieces at
 // fixed places 698, both pages together 674, and the softmax with 96 registers in place
-// of 88 645.  A prompt of 8192 481 us, 1.14 PFLOP/s.
+// of 88 645.  A prompt of 8192 475 us, 1.16 PFLOP/s.
 template <int D_>
 struct ManyCfg {
   static constexpr int D = D_, kRows = 256;
@@ -891,19 +891,21 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
       // ==== products (the whole warp; one lane issues) ====
       constexpr uint32_t idesc_qk = idesc_f16(128, 128, false, false);
       constexpr uint32_t idesc_pv = idesc_f16(128, D, false, true);
-      const uint64_t dk0 = smem_desc(smem_addr(k_s), 16, 1024, kSwizzle128), dq0 = smem_desc(smem_addr(q_s), 16, 1024, kSwizzle128);
-      const uint64_t dv0 = smem_desc(smem_addr(v_s), kSlab, 1024, kSwizzle128);
+      // (descriptors: addresses are in the lower words, which never carry)
+      const uint32_t dk0 = smem_desc(smem_addr(k_s), 16, 1024, kSwizzle128), dq0 = smem_desc(smem_addr(q_s), 16, 1024, kSwizzle128);
+      const uint32_t dv0 = smem_desc(smem_addr(v_s), kSlab, 1024, kSwizzle128);
+      auto desc = [](uint32_t lower) { return (smem_desc(0, 0, 1024, kSwizzle128) & ~0xFFFFFFFFull) | lower; };
       uint32_t n_tiles = 0, ks = 0, k_par = 0;            // stage of K and its parity
       uint32_t w0 = 0, w1 = 0, p0 = 0, p1 = 0;            // parities of the row tiles' q and P
       // The queue of products is a few instructions deep, so what keeps this
       // warp between two groups of them has to be short: waits come where a group
       // has just been queued, and a group ends with all its signals.
       auto qk = [&](int qt, uint32_t stage, int q) {                   // of the elected lane
-        const uint64_t dk = dk0 + stage * (C::kTile >> 4), dq = dq0 + q * (C::kTile >> 4);
+        const uint32_t dk = dk0 + stage * (C::kTile >> 4), dq = dq0 + q * (C::kTile >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t at = (k / 4 * kSlab + k % 4 * 32) >> 4;
-          mma_f16kind(tmem + qt * 128, dq + at, dk + at, idesc_qk, k > 0);
+          mma_f16kind(tmem + qt * 128, desc(dq + at), desc(dk + at), idesc_qk, k > 0);
         }
         mma_commit(smem_addr(&sm.s_full[qt]));
       };
@@ -912,7 +914,7 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
       // pages and the others, so that the first products overlap the rest of
       // the softmax)
       auto pv = [&](int qt, uint32_t j, bool first, uint32_t& par, auto&& more) {
-        const uint64_t dv = dv0 + (j & 1) * (C::kTile >> 4);
+        const uint32_t dv = dv0 + (j & 1) * (C::kTile >> 4);
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           wait(sm.p_full[qt][part], par);
@@ -923,7 +925,7 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
             for (int i = 0; i < 4; ++i) {
               const int k = 2 * part + (i & 1) + 4 * (i >> 1);       // 16 keys
               mma_f16_ts(tmem + 256 + qt * 128, tmem + qt * 128 + 64 * (k >> 2) + 8 * (k & 3),
-                         dv + ((k * 2048) >> 4), idesc_pv, !first || part + i > 0);
+                         desc(dv + ((k * 2048) >> 4)), idesc_pv, !first || part + i > 0);
             }
             if (part == 1) more();
           }
