@@ -53,7 +53,7 @@ namespace {
 // scales are 8, at 2.4 a clock and SM, half of what the ALU pipe gives (two blocks of
 // seven warps a SM; with six 268 us; joining in place, for a ring of 12 pages in place
 // of 9, 250 against 244; codes of V loaded behind the softmax 243 against 240).  2 x
-// 204800 tokens cut over 304 blocks 89 us with the joining kernel, 333 tokens of one
+// 204800 tokens cut over 304 blocks 88 us with the joining kernel, 333 tokens of one
 // session 5.7 us.  D = 64, the same sessions: 154 us, 4.3 TB/s (214 before the copies'
 // operands were uniform).  Taller items have an SM's registers for one block: drafts of 35 rows
 // (D = 64, f16, 24 requests with a window of 4096) 35 us, where the prompt kernel took
