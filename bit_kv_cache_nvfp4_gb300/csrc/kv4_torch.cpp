@@ -307,11 +307,29 @@ struct Side {
   int heads = 0, d = 0;
   at::Tensor result;
 };
-// Bytes from the first element to past the last one.
-int64_t span_of(const at::Tensor& t) {
-  int64_t n = 1;
-  for (int64_t i = 0; i < t.dim(); ++i) n += (t.size(i) - 1) * t.stride(i);
-  return n * t.element_size();
+// Rows of a side's input or output, strides in elements of 16 bits.
+struct Rows {
+  const char* p;
+  int64_t token, head, tokens;
+  int heads, d;
+  int64_t row() const { return 2 * ((heads - 1) * head + d); }
+  int64_t span() const { return 2 * (tokens - 1) * token + row(); }
+};
+Rows in_of(const Side& s) { return {static_cast<const char*>(s.in), s.in_token, s.in_head, s.tokens, s.heads, s.d}; }
+Rows out_of(const Side& s) { return {static_cast<const char*>(s.out), s.out_token, s.out_head, s.tokens, s.heads, s.d}; }
+// Whether no element is both a's and b's: apart as a whole, or in every token (slices of a
+// fused projection's rows), or in every head (of a projection [T, heads, parts, D]).
+bool lie_apart(const Rows& a, const Rows& b) {
+  if (a.tokens == 0 || a.heads == 0 || b.heads == 0) return true;
+  if (a.p + a.span() <= b.p || b.p + b.span() <= a.p) return true;
+  auto within = [&](int64_t period, int64_t of_a, int64_t of_b) {
+    const int64_t at = ((b.p - a.p) % period + period) % period;
+    return of_a <= at && at + of_b <= period;
+  };
+  if (a.tokens > 1 && a.token > 0 && a.token == b.token && within(2 * a.token, a.row(), b.row())) return true;
+  const int64_t head = a.heads > 1 ? a.head : b.head;
+  return head > 0 && (a.heads == 1 || b.heads == 1 || a.head == b.head) && a.token % head == 0 && b.token % head == 0 &&
+         within(2 * head, 2 * a.d, 2 * b.d);
 }
 Side side_of(PyObject* in_o, PyObject* out_o, const char* name, const at::Tensor& first) {
   Side s;
@@ -348,9 +366,8 @@ Side side_of(PyObject* in_o, PyObject* out_o, const char* name, const at::Tensor
   }
   strides(s.result, out_name, s.out_token, s.out_head);
   s.out = s.result.mutable_data_ptr();
-  const char *a = static_cast<const char*>(s.in), *b = static_cast<const char*>(s.out);
-  if (t.numel() > 0 && !(a == b && s.in_token == s.out_token && s.in_head == s.out_head) && a < b + span_of(s.result) &&
-      b < a + span_of(t))
+  const bool same = s.in == s.out && s.in_token == s.out_token && s.in_head == s.out_head;
+  if (t.numel() > 0 && !same && !lie_apart(in_of(s), out_of(s)))
     value_error(out_name + " must be " + name + " itself or lie apart from it");
   return s;
 }
@@ -381,6 +398,12 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const c10::cuda::CUDAGuard guard(dev);
     const Side q = side_of(a[0], a[8], "q", first), k = side_of(a[1], a[9], "k", first);
+    if (a[0] != Py_None && a[1] != Py_None) {
+      if (a[8] != Py_None && !lie_apart(out_of(q), in_of(k))) value_error("q_out must lie apart from k");
+      if (a[9] != Py_None && !lie_apart(out_of(k), in_of(q))) value_error("k_out must lie apart from q");
+      if (a[8] != Py_None && a[9] != Py_None && !lie_apart(out_of(q), out_of(k)))
+        value_error("q_out and k_out must lie apart");
+    }
     auto room = [&](const Side& s, const char* name, int at) {
       if (s.heads > 0 && (at > s.d || s.d - at < 2 * freq.size(0)))
         value_error(std::string(name) + ": " + std::to_string(2 * freq.size(0)) + " elements from " + std::to_string(at) +

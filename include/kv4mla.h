@@ -647,14 +647,16 @@ kv4_status kv4_attention_gqa4(const void* q_dev, int64_t q_token_stride, int64_t
  *                   that side's pointers are then not looked at.  Hq + Hk <=
  *                   65535, D <= 65536
  *   q_out_dev, ..   the same shapes, rows at least D elements apart; an output is
- *                   its input, with the same strides, or overlaps no input
+ *                   its input, with the same strides, or overlaps no input, and
+ *                   overlaps not the other output
  *   positions_dev   int32 or int64 [n_tokens] (position_bits 32 or 64),
  *                   magnitudes up to 2^31
  *   inv_freq_dev    fp32 [n_pairs], 1 <= n_pairs <= 512, magnitudes up to 4:
  *                   radians a position
  * Pair i of a head is elements (offset + 2i, offset + 2i + 1) where interleaved is
  * nonzero and (offset + i, offset + n_pairs + i) where it is 0; with the angle
- * a = position * inv_freq[i] (held to 2^-29 of a turn)
+ * a = position * inv_freq[i] (reduced to less than a turn in integers, to 2^-29 of
+ * one, then rounded to fp32)
  *   (x, y) -> factor * (x cos a - y sin a, x sin a + y cos a)
  * in fp32, rounded once.  Elements outside offset .. offset + 2 n_pairs - 1 are
  * copied as they are.

@@ -201,6 +201,42 @@ def test_refusals():
     torch.cuda.synchronize()
 
 
+def test_outputs_that_share_elements_with_the_other_side_are_refused():
+    device = dev()
+    freq = kv.rotary_frequencies(64, device=device)
+    for t in (1, 7):
+        pos = torch.arange(t, device=device) + 9
+        x = torch.randn(t, 4, 64, device=device).to(BF16)
+        y, z = x.clone(), torch.empty(t, 9, 64, dtype=BF16, device=device)
+        for q, k, out in ((x, x, dict(q_out=x)), (x, x, dict(k_out=x)), (x, y, dict(q_out=y)), (x, y, dict(k_out=x)),
+                          (x, y, dict(q_out=z[:, :4], k_out=z[:, 3:7])), (x, y, dict(q_out=z[:, 5:], k_out=z[:, 3:7])),
+                          (x, y, dict(q_out=z[:, ::2][:, :4], k_out=z[:, 2:6])),
+                          (x, y[:, :1], dict(q_out=z[:, :4], k_out=z[:, 3:4])),
+                          (x[..., :32], y[..., :32], dict(q_out=z[:, :4, :32], k_out=z[:, :4, 31:63]))):
+            freq_of = freq[:q.shape[2] // 2]
+            with pytest.raises(ValueError, match="apart"):
+                kv.rotary(q, k, pos, freq_of, **out)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("t", [1, 7, 300])
+@pytest.mark.parametrize("near", [False, True])
+def test_slices_of_one_tensor_turn_in_place(t, near):
+    """By tokens [T, q heads | k heads | v heads, D], by heads [T, heads, q | k | v, D], and
+    tokens behind one another."""
+    device = dev()
+    freq, pos = kv.rotary_frequencies(64, device=device), torch.arange(t, device=device) * 3 + 1
+    rows = torch.randn(t, 9, 64, device=device).to(BF16)
+    heads = torch.randn(t, 4, 3, 64, device=device).to(BF16)
+    whole = torch.randn(2 * t, 4, 64, device=device).to(BF16)
+    for q, k in ((rows[:, :6], rows[:, 6:8]), (rows[:, 8:], rows[:, 2:5]), (heads[:, :, 0], heads[:, :, 1]),
+                 (heads[:, :, 2], heads[:, :1, 1]), (whole[:t], whole[t:])):
+        want = kv.rotary(q, k, pos, freq, interleaved=near)
+        assert all(not torch.equal(a, b) for a, b in zip(want, (q, k)))
+        kv.rotary(q, k, pos, freq, interleaved=near, q_out=q, k_out=k)
+        assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
 def test_empty_calls():
     device = dev()
     freq, pos = torch.ones(4, device=device), torch.zeros(0, dtype=torch.int64, device=device)
