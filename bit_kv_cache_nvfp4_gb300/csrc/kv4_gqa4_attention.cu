@@ -1448,7 +1448,7 @@ cudaError_t launch_few(const Gqa8AttnArgs& a, void* ws, cudaStream_t stream) {
   const int blocks = static_cast<int>(std::min<int64_t>(a.num_sms * C::kCtas, most));
   const Parts p = parts_at(ws, blocks, RP, D);
   e = launch_pdl(few4_kernel<D, RP, I>, blocks, C::kThreads, C::kSmem, stream, 1, a, RP, p.tails, p.lse, p.o);
-  return e != cudaSuccess ? e : launch_merge(merge_few_kernel<D>, a, blocks, RP, RP, p, stream);
+  return e != cudaSuccess ? e : launch_merge_few<D>(a, blocks, RP, p, stream);
 }
 template <int D, int RP>
 cudaError_t launch_few(const Gqa8AttnArgs& a, cudaStream_t stream) {
@@ -1464,7 +1464,7 @@ cudaError_t launch_many(const Gqa8AttnArgs& a, int min_rows, void* ws, cudaStrea
   const Parts p = parts_at(ws, a.num_sms, C::kRows, D);
   e = launch_pdl(many4_kernel<D, F16, I>, a.num_sms, kManyThreads, C::kSmem, stream, 1, a, min_rows, p.tails, p.lse,
                  p.o);
-  return e != cudaSuccess ? e : launch_merge(merge_many_kernel<D>, a, a.num_sms, C::kRows / 32, C::kRows, p, stream);
+  return e != cudaSuccess ? e : launch_merge_many<D>(a, a.num_sms, C::kRows, p, stream);
 }
 template <int D, bool F16>
 cudaError_t launch_many(const Gqa8AttnArgs& a, int min_rows, void* ws, cudaStream_t stream) {

@@ -1340,7 +1340,7 @@ cudaError_t launch_few(const Gqa8AttnArgs& a, const CUtensorMap& map, int max_ro
   const int blocks = static_cast<int>(std::min<int64_t>(a.num_sms * C::kCtas, most));
   const Parts p = parts_at(ws, blocks, RP, D);
   e = launch_pdl(few_kernel<D, RP, NT>, blocks, C::kThreads, C::kSmem, stream, 1, map, a, max_rows, p.tails, p.lse, p.o);
-  return e != cudaSuccess ? e : launch_merge(merge_few_kernel<D>, a, blocks, RP, RP, p, stream);
+  return e != cudaSuccess ? e : launch_merge_few<D>(a, blocks, RP, p, stream);
 }
 
 template <int D, int NT>
@@ -1352,7 +1352,7 @@ cudaError_t launch_many(const Gqa8AttnArgs& a, const CUtensorMap& map, int min_r
   const Parts p = parts_at(ws, a.num_sms, kManyRows, D);
   e = launch_pdl(many_kernel<D, NT>, a.num_sms, kManyThreads, C::kSmem, stream, 1, map, a, min_rows, p.tails,
                  p.lse, p.o);
-  return e != cudaSuccess ? e : launch_merge(merge_many_kernel<D>, a, a.num_sms, kManyRows / 32, kManyRows, p, stream);
+  return e != cudaSuccess ? e : launch_merge_many<D>(a, a.num_sms, kManyRows, p, stream);
 }
 
 size_t few_bytes(int rows, int D, int sms) {

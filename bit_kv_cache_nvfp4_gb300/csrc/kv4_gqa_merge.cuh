@@ -23,29 +23,77 @@ namespace {
 // over all blocks (40 rows of one head over 200000 tokens: 97 us, where one row,
 // in the kernels of few rows, takes 28).
 // ---------------------------------------------------------------------------
+// Block (c, y) takes `each` rows, 8 or 1.  Up to 8 pieces a warp takes in one go, a row
+// by itself; more of them the 8 warps share, row after row.  (So 8 rows a block where
+// requests and heads are many, whose items are cut in two or three; and 1 where few of
+// them are cut over all blocks.)
 template <int D>
-__global__ void __launch_bounds__(256) merge_few_kernel(const Gqa8AttnArgs a, const int rows,
+__global__ void __launch_bounds__(256) merge_few_kernel(const Gqa8AttnArgs a, const int rows, const int each,
                                                     const Gqa8Tail* tails, const float* ws_lse,
                                                     const float* ws_o) {
   grid_dependency_wait();
   grid_launch_dependents();
-  constexpr int C = D / 32;                               // columns a lane
+  constexpr int C = D / 32, W = 8;                        // columns a lane; warps
   using Vec = std::conditional_t<C == 4, float4, float2>;
-  __shared__ Vec part[8][32];
+  __shared__ Vec part[W][32];
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Gqa8Tail t = tails[c];
-  constexpr int W = 8;
-  const int r = blockIdx.y, wi = warp;
-  if (t.parts == 0 || r >= t.nrows) return;               // (whole blocks)
-  float o[C], m = -INFINITY, s = 0.0f;
+  const int r_begin = blockIdx.y * each, r_end = min(t.nrows, r_begin + each);
+  if (t.parts == 0 || r_begin >= r_end) return;           // (whole blocks)
+  // piece i of row r is slot 2c + 1 for i = 0, else 2 (c + i)
+  auto row_of = [&](int i, int r) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * rows + r; };
+  auto finish = [&](int r, float m, float s, const float (&o)[C]) {
+    const int G = a.Hq / a.Hkv, rr = t.r0 + r;
+    const int64_t row = static_cast<int64_t>(t.cu0 + rr / G) * a.Hq + t.h * G + rr % G;
+    const float inv = s == 0.0f ? 0.0f : 1.0f / s;
+    uint32_t u[C / 2];
 #pragma unroll
-  for (int k = 0; k < C; ++k) o[k] = 0.0f;
-  bool odd = false;
-  {
-    // piece i is slot 2c + 1 for i = 0, else 2 (c + i)
-    auto row_of = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * rows + r; };
+    for (int k = 0; k < C / 2; ++k) {
+      const float y0 = o[2 * k] * inv, y1 = o[2 * k + 1] * inv;
+      u[k] = a.f16 ? pack16<true>(y0, y1) : pack16<false>(y0, y1);
+    }
+    uint32_t* const dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * D) + lane * (C / 2);
+    if constexpr (C == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[1]);
+    else *dst = u[0];
+    if (lane == 0) a.lse[row] = s == 0.0f ? -INFINITY : (m + log2f(s)) * 0.6931471805599453f;
+  };
+  if (t.parts <= W) {
+    const int r = r_begin + warp;
+    if (r >= r_end) return;
+    const float x = lane < t.parts ? load(ws_lse + row_of(lane, r)) : -INFINITY;
+    Vec v[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (i < t.parts) v[i] = load(reinterpret_cast<const Vec*>(ws_o + row_of(i, r) * D) + lane);
+    const float m = warp_max(x);
+    const bool odd = __any_sync(0xFFFFFFFFu, x != x);
+    float o[C];
+#pragma unroll
+    for (int k = 0; k < C; ++k) o[k] = 0.0f;
+    float s = 0.0f;
+    if (m > -INFINITY) {
+      const float w = lane < t.parts ? fast_exp2(x - m) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (i < t.parts) {
+          const float wt = __shfl_sync(0xFFFFFFFFu, w, i);
+          const float* f = reinterpret_cast<const float*>(&v[i]);
+#pragma unroll
+          for (int k = 0; k < C; ++k) o[k] += __fmul_rn(wt, f[k]);
+        }
+      s = warp_sum(w);
+    }
+    finish(r, m, odd ? __uint_as_float(0x7FC00000u) : s, o);
+    return;
+  }
+#pragma unroll 1
+  for (int r = r_begin; r < r_end; ++r) {
+    float o[C], m = -INFINITY, s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < C; ++k) o[k] = 0.0f;
+    bool odd = false;
     for (int i = lane; i < t.parts; i += 32) {
-      const float x = load(ws_lse + row_of(i));
+      const float x = load(ws_lse + row_of(i, r));
       odd |= x != x;
       m = fmaxf(m, x);
     }
@@ -53,13 +101,13 @@ __global__ void __launch_bounds__(256) merge_few_kernel(const Gqa8AttnArgs a, co
     odd = __any_sync(0xFFFFFFFFu, odd);
     if (m > -INFINITY) {
       for (int i0 = 0; i0 < t.parts; i0 += 32) {
-        const float w = i0 + lane < t.parts ? fast_exp2(load(ws_lse + row_of(i0 + lane)) - m) : 0.0f;
+        const float w = i0 + lane < t.parts ? fast_exp2(load(ws_lse + row_of(i0 + lane, r)) - m) : 0.0f;
         s += w;
         const int n = min(32, t.parts - i0);
 #pragma unroll 4
-        for (int i = wi; i < n; i += W) {
+        for (int i = warp; i < n; i += W) {
           const float wt = __shfl_sync(0xFFFFFFFFu, w, i);
-          const Vec v = load(reinterpret_cast<const Vec*>(ws_o + row_of(i0 + i) * D) + lane);
+          const Vec v = load(reinterpret_cast<const Vec*>(ws_o + row_of(i0 + i, r) * D) + lane);
           const float* f = reinterpret_cast<const float*>(&v);
 #pragma unroll
           for (int k = 0; k < C; ++k) o[k] = fmaf(wt, f[k], o[k]);
@@ -67,35 +115,19 @@ __global__ void __launch_bounds__(256) merge_few_kernel(const Gqa8AttnArgs a, co
       }
       s = warp_sum(s);
     }
-    if (odd) s = __uint_as_float(0x7FC00000u);
-  }
-  part[warp][lane] = *reinterpret_cast<const Vec*>(o);
-  __syncthreads();
-  if (wi != 0) return;
+    part[warp][lane] = *reinterpret_cast<const Vec*>(o);
+    __syncthreads();
+    if (warp == 0) {
 #pragma unroll
-  for (int i = 1; i < W; ++i) {
-    const Vec v = part[i][lane];
+      for (int i = 1; i < W; ++i) {
+        const Vec v = part[i][lane];
 #pragma unroll
-    for (int k = 0; k < C; ++k) o[k] += reinterpret_cast<const float*>(&v)[k];
-  }
-  const int G = a.Hq / a.Hkv, rr = t.r0 + r;
-  const int64_t row = static_cast<int64_t>(t.cu0 + rr / G) * a.Hq + t.h * G + rr % G;
-  const float inv = s == 0.0f ? 0.0f : 1.0f / s;
-  uint32_t u[C / 2];
-#pragma unroll
-  for (int k = 0; k < C / 2; ++k) {
-    const float y0 = o[2 * k] * inv, y1 = o[2 * k + 1] * inv;
-    if (a.f16) {
-      u[k] = h2_bits(__floats2half2_rn(y0, y1));
-    } else {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
-      u[k] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int k = 0; k < C; ++k) o[k] += reinterpret_cast<const float*>(&v)[k];
+      }
+      finish(r, m, odd ? __uint_as_float(0x7FC00000u) : s, o);
     }
+    __syncthreads();
   }
-  uint32_t* const dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * D) + lane * (C / 2);
-  if constexpr (C == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[1]);
-  else *dst = u[0];
-  if (lane == 0) a.lse[row] = s == 0.0f ? -INFINITY : (m + log2f(s)) * 0.6931471805599453f;
 }
 
 template <int D>
@@ -185,12 +217,12 @@ inline Parts parts_at(void* ws, int blocks, int rows, int D) {
   p.lse = p.o + 2ull * blocks * rows * D;
   return p;
 }
-template <typename K>
-cudaError_t launch_merge(K kernel, const Gqa8AttnArgs& a, int blocks, int y, int rows, const Parts& p,
-                         cudaStream_t stream) {
+template <typename... Args>
+cudaError_t launch_merge(void (*kernel)(Gqa8AttnArgs, Args...), const Gqa8AttnArgs& a, dim3 grid, cudaStream_t stream,
+                         Args... args) {
   if ((a.pt_stride + 1) / 2 <= kWhole) return cudaSuccess;                 // nothing is ever cut
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, y);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -198,8 +230,19 @@ cudaError_t launch_merge(K kernel, const Gqa8AttnArgs& a, int blocks, int y, int
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, rows, static_cast<const Gqa8Tail*>(p.tails),
-                            static_cast<const float*>(p.lse), static_cast<const float*>(p.o));
+  return cudaLaunchKernelEx(&cfg, kernel, a, args...);
+}
+template <int D>
+cudaError_t launch_merge_few(const Gqa8AttnArgs& a, int blocks, int rows, const Parts& p, cudaStream_t stream) {
+  // (of fewer items an average one may have more than 8 pieces)
+  const int each = static_cast<int64_t>(a.B) * a.Hkv * 8 >= blocks ? 8 : 1;
+  return launch_merge<int, int, const Gqa8Tail*, const float*, const float*>(
+      merge_few_kernel<D>, a, dim3(blocks, (rows + each - 1) / each), stream, rows, each, p.tails, p.lse, p.o);
+}
+template <int D>
+cudaError_t launch_merge_many(const Gqa8AttnArgs& a, int blocks, int rows, const Parts& p, cudaStream_t stream) {
+  return launch_merge<int, const Gqa8Tail*, const float*, const float*>(
+      merge_many_kernel<D>, a, dim3(blocks, (rows + 31) / 32), stream, rows, p.tails, p.lse, p.o);
 }
 
 // Once per device and kernel: its shared memory, and, where it splits its
