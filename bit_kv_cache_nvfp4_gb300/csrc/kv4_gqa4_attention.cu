@@ -48,16 +48,16 @@ namespace {
 // scores, and only where one has risen the row's threads meet.
 //
 // Measured (D = 128, bf16): 64 sessions of up to 32768 tokens, 8 heads a group, 1.29 GB
-// of rows: 228 us, 5.7 TB/s, 84 % of the measured copy rate; the loads alone take 197.
+// of rows: 223 us, 5.8 TB/s, 85 % of the measured copy rate; the loads alone take 197.
 // What is left is instructions: 18 a key and warp, of which the conversions and their
 // scales are 8, at 2.4 a clock and SM, half of what the ALU pipe gives (two blocks of
 // seven warps a SM; with six 268 us; joining in place, for a ring of 12 pages in place
 // of 9, 250 against 244; codes of V loaded behind the softmax 243 against 240).  2 x
 // 204800 tokens cut over 304 blocks 88 us with the joining kernel, 333 tokens of one
-// session 5.7 us.  D = 64, the same sessions: 154 us, 4.3 TB/s (214 before the copies'
+// session 5.7 us.  D = 64, the same sessions: 150 us, 4.4 TB/s (214 before the copies'
 // operands were uniform).  Taller items have an SM's registers for one block: drafts of 35 rows
-// (D = 64, f16, 24 requests with a window of 4096) 35 us, where the prompt kernel took
-// 66; half of that is the fixed part of the call.
+// (D = 64, f16, 24 requests with a window of 4096) 29 us, where the prompt kernel took
+// 66; a third of that is the fixed part of the call.
 template <int D_, int RP_>
 struct FewCfg {
   static constexpr int D = D_, RP = RP_, NT = RP / 8;
@@ -689,12 +689,12 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
 // rescaled, when the maximum rises by more than 2^6 (p stays below 2^14, f16's top
 // is 2^16).
 //
-// Measured (32 heads over 8, D = 128, bf16): 2 x 2048 new tokens over up to 16384 607 us,
+// Measured (32 heads over 8, D = 128, bf16): 2 x 2048 new tokens over up to 16384 605 us,
 // 1.34 PFLOP/s, 71 % of the measured bf16 rate; without the widening, on whatever the
 // tiles hold, 563 (of 632 then).  What it costs is the time of its chain (codes, f16, fence, products)
 // rather than its instructions: two warps took 1040 us, four 814, a page's pieces at
 // fixed places 698, both pages together 674, and the softmax with 96 registers in place
-// of 88 645.  A prompt of 8192 475 us, 1.16 PFLOP/s.
+// of 88 645.  A prompt of 8192 477 us, 1.15 PFLOP/s.
 template <int D_>
 struct ManyCfg {
   static constexpr int D = D_, kRows = 256;

@@ -26,7 +26,8 @@ namespace {
 // Block (c, y) takes `each` rows, 8 or 1.  Up to 8 pieces a warp takes in one go, a row
 // by itself; more of them the 8 warps share, row after row.  (So 8 rows a block where
 // requests and heads are many, whose items are cut in two or three; and 1 where few of
-// them are cut over all blocks.)
+// them are cut over all blocks.  A block for every row: drafts of 35 rows 34.6 us for 28.8,
+// 64 sessions' decode step 227 for 223, of the 4-bit cache.)
 template <int D>
 __global__ void __launch_bounds__(256) merge_few_kernel(const Gqa8AttnArgs a, const int rows, const int each,
                                                     const Gqa8Tail* tails, const float* ws_lse,
