@@ -48,7 +48,7 @@ namespace {
 // scores, and only where one has risen the row's threads meet.
 //
 // Measured (D = 128, bf16): 64 sessions of up to 32768 tokens, 8 heads a group, 1.29 GB
-// of rows: 223 us, 5.8 TB/s, 85 % of the measured copy rate; the loads alone take 197.
+// of rows: 222 us, 5.8 TB/s, 86 % of the measured copy rate; the loads alone take 197.
 // What is left is instructions: 18 a key and warp, of which the conversions and their
 // scales are 8, at 2.4 a clock and SM, half of what the ALU pipe gives (two blocks of
 // seven warps a SM; with six 268 us; joining in place, for a ring of 12 pages in place
@@ -689,7 +689,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
 // rescaled, when the maximum rises by more than 2^6 (p stays below 2^14, f16's top
 // is 2^16).
 //
-// Measured (32 heads over 8, D = 128, bf16): 2 x 2048 new tokens over up to 16384 605 us,
+// Measured (32 heads over 8, D = 128, bf16): 2 x 2048 new tokens over up to 16384 606 us,
 // 1.34 PFLOP/s, 71 % of the measured bf16 rate; without the widening, on whatever the
 // tiles hold, 563 (of 632 then).  What it costs is the time of its chain (codes, f16, fence, products)
 // rather than its instructions: two warps took 1040 us, four 814, a page's pieces at

@@ -48,7 +48,7 @@ namespace {
 // a running output of its own, joined at the item's end.
 //
 // Measured (D = 128, bf16): 64 sessions of up to 32768 tokens, 8 heads a group,
-// 2.29 GB of codes: 340 us, 6.7 TB/s, the rate of a copy; 16 heads a group
+// 2.29 GB of codes: 336 us, 6.8 TB/s, the rate of a copy; 16 heads a group
 // (2.08 GB) 355 us; 2 x 204800 tokens cut over 304 blocks 133 us with the joining
 // kernel.  In f16, with three terms, 394 us for 2.16 GB, 5.5 TB/s.
 template <int D_, int RP_, int NT_>
