@@ -1033,14 +1033,12 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
         if (a.fault_site == 1) wait(sm.never, 0);
       }
       if (a.fault_site == 1) wait(sm.never, 0);
-      // in a block that gave up nothing else waits for the products that are
-      // still queued: they end before its memory goes away
+      // in a block that gave up, which any role may still do, nothing else waits for
+      // the products that are queued: they end before its memory goes away
       __syncwarp();
-      if (__any_sync(0xFFFFFFFFu, *dead != 0)) {
-        if (elect_one()) mma_commit(smem_addr(&sm.never));
-        __syncwarp();
-        mbar_wait_bounded(smem_addr(&sm.never), 0, 1000000);
-      }
+      if (elect_one()) mma_commit(smem_addr(&sm.never));
+      __syncwarp();
+      mbar_wait_bounded(smem_addr(&sm.never), 0, 1000000);
     }
   } else if (warp < 8) {
     setmaxnreg_dec<kWidenRegs>();

@@ -245,12 +245,11 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
     auto ready = [&](uint64_t& bar, uint32_t parity) {
       return __any_sync(0xFFFFFFFFu, mbar_try_wait(smem_addr(&bar), parity));
     };
-    // In a block that gave up nothing else waits for the products that are
-    // still queued: they end before its memory goes away.
+    // In a block that gave up, which any role may still do, nothing else waits for the
+    // products that are queued: they end before its memory goes away.
     auto drain = [&] {
       if (a.fault_site == 1) wait(sm.never, 0);
       __syncwarp();
-      if (!__any_sync(0xFFFFFFFFu, *dead != 0)) return;
       if (elect_one()) mma_commit(smem_addr(&sm.never));
       __syncwarp();
       mbar_wait_bounded(smem_addr(&sm.never), 0, 1000000);
@@ -946,14 +945,12 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
         if (a.fault_site == 1) wait(sm.never, 0);
       }
       if (a.fault_site == 1) wait(sm.never, 0);
-      // in a block that gave up nothing else waits for the products that are
-      // still queued: they end before its memory goes away
+      // in a block that gave up, which any role may still do, nothing else waits for
+      // the products that are queued: they end before its memory goes away
       __syncwarp();
-      if (__any_sync(0xFFFFFFFFu, *dead != 0)) {
-        if (elect_one()) mma_commit(smem_addr(&sm.never));
-        __syncwarp();
-        mbar_wait_bounded(smem_addr(&sm.never), 0, 1000000);
-      }
+      if (elect_one()) mma_commit(smem_addr(&sm.never));
+      __syncwarp();
+      mbar_wait_bounded(smem_addr(&sm.never), 0, 1000000);
     } else {
       // ==== V to f16 ====
       uint32_t j = 0;

@@ -21,3 +21,14 @@ def test_kernels_that_begin_early_read_nothing_as_read_only(name):
     for body in kernels:
         before = body[:body.index("grid_dependency_wait()")]
         assert not re.search(r"\bload\(|\ba\.(cu|lens|scales|page_table|dev_err)\b", before)
+
+
+@pytest.mark.parametrize("name,kernels", [("kv4_gqa8_attention.cu", 2), ("kv4_gqa4_attention.cu", 1)])
+def test_queued_products_end_before_a_block_does(name, kernels):
+    """Whoever gives up a wait may do so behind the last product's issue, so the issuing
+    warp waits for what it queued whether or not the block has given up by then."""
+    code = re.sub(r"//[^\n]*", "", (CSRC / name).read_text())
+    drains = re.findall(r"([^\n]*)\n *__syncwarp\(\);\n *if \(elect_one\(\)\) mma_commit\(smem_addr\(&sm\.never\)\);"
+                        r"\n *__syncwarp\(\);\n *mbar_wait_bounded\(smem_addr\(&sm\.never\)", code)
+    assert len(drains) == kernels == code.count("mma_commit(smem_addr(&sm.never))")
+    assert not any("dead" in line for line in drains)
