@@ -195,20 +195,23 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
     __syncthreads();
   }
   volatile int* dead = &sm.dead;
-  // A wait that gives up ends every later one of the block at once: the roles
-  // then run to their ends without new loads, and the outputs are not valid.
+  // A wait that gives up (false) ends every later one of the block at once: the roles
+  // then run to their ends, and the outputs are not valid.  A warp that gave up a page
+  // frees no stage any more, so that a free stage never has a copy on its way, and the
+  // loading warp begins none behind the first stage that it does not get.
   auto wait = [&](uint64_t& bar, uint32_t parity) {
-    if (mbar_try_wait(smem_addr(&bar), parity)) return;
-    if (*dead) return;
+    if (mbar_try_wait(smem_addr(&bar), parity)) return true;
+    if (*dead) return false;
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait_suspend(smem_addr(&bar), parity, 20000u)) {
-      if (*dead) return;
+      if (*dead) return false;
       if (global_timer_ns() - t0 > a.timeout_ns) {
         *dead = 1;
         flag_error(a.dev_err, kDevTimeout);
-        return;
+        return false;
       }
     }
+    return true;
   };
   // an item's pages: of its first key on, up to its last
   struct Pages {
@@ -224,8 +227,9 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
 
   if (warp == 0) {
     // ==== work list and loads ====
-    uint32_t n_items = 0, n_pages = 0, n_loads = 0;       // pages; up to which copies began
+    uint32_t n_items = 0, n_pages = 0;                    // pages whose copies began
     uint32_t stage = 0, empty_par = 1;                    // of the next page
+    bool stopped = false;                                 // no more copies
     auto publish = [&](const Gqa8Item& it) {
       const int s = n_items & 3;
       wait(sm.item_empty[s], ((n_items >> 2) & 1) ^ 1);
@@ -239,7 +243,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
     };
     auto load_item = [&](const Gqa8Item& it) {
       const Pages c = pages_of(it);
-      for (int i = 0; i < c.n; i += 32) {
+      for (int i = 0; i < c.n && !stopped; i += 32) {
         // a lane's page: its K and V, or -1 where the table has none
         const int64_t at = static_cast<int64_t>(c.first) + i + lane;
         int block = -1;                                   // (2 Hkv num_pages < 2^31)
@@ -256,11 +260,12 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
           const int64_t blk = __shfl_sync(0xFFFFFFFFu, block, k);
           if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_addr(&sm.empty[stage]), empty_par))) {
             wait(sm.empty[stage], empty_par);
-            if (__any_sync(0xFFFFFFFFu, *dead != 0)) break;
+            stopped = __any_sync(0xFFFFFFFFu, *dead != 0);
+            if (stopped) break;
           }
           if (elect_one()) {
             const uint32_t bar = smem_addr(&sm.full[stage]), dst = smem_addr(smem) + stage * C::kStage;
-            sm.page[stage] = 2 * (n_pages + k) + (blk < 0);
+            sm.page[stage] = 2 * n_pages + (blk < 0);
             if (blk >= 0) {
               mbar_arrive_expect_tx(bar, C::kStage);
               bulk_copy_g2s(dst, a.pool + blk * (2 * C::kCodes), 2 * C::kCodes, bar);
@@ -270,13 +275,12 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
             }
           }
           __syncwarp();
-          n_loads = n_pages + k + 1;
+          ++n_pages;
           if (++stage == ST) {
             stage = 0;
             empty_par ^= 1;
           }
         }
-        n_pages += n;
       }
     };
     auto take = [&](const Gqa8Item& it) {
@@ -296,7 +300,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
     for (uint32_t i = n_pages > ST ? n_pages - ST : 0; i < n_pages; ++i)
       wait(sm.empty[i % ST], (i / ST) & 1);
     if (*dead && lane == 0)
-      for (uint32_t i = n_loads > ST ? n_loads - ST : 0; i < n_loads; ++i)
+      for (uint32_t i = n_pages > ST ? n_pages - ST : 0; i < n_pages; ++i)
         mbar_wait_bounded(smem_addr(&sm.full[i % ST]), (i / ST) & 1, 1000000);
   } else {
     // ==== scores, softmax, output ====
@@ -428,7 +432,7 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
         const uint32_t st = slot / C::kEach, part = slot % C::kEach;
         const uint32_t number = chunk / C::kEach;
         uint32_t there = sm.page[st];
-        if (there / 2 != number) {
+        if (!__all_sync(0xFFFFFFFFu, there / 2 == number && mbar_try_wait(smem_addr(&sm.full[st]), par))) {
           const uint64_t since = global_timer_ns();
           while ((there = sm.page[st]) / 2 != number && !*dead) {
             __nanosleep(40);
@@ -437,9 +441,9 @@ few4_kernel(const Gqa8AttnArgs a, const int max_rows, Gqa8Tail* tails, float* ws
               flag_error(a.dev_err, kDevTimeout);
             }
           }
+          // (a page that was given up frees no stage, and its block is at its last item)
+          if (!__all_sync(0xFFFFFFFFu, there / 2 == number && wait(sm.full[st], par))) break;
         }
-        wait(sm.full[st], par);
-        __syncwarp();
         chunk += W;
         slot += W;
         if (slot >= ST * C::kEach) {
@@ -786,18 +790,21 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
   tc_fence_after_sync();
   const uint32_t tmem = sm.tmem;                          // S/P of the row tiles, then O
   volatile int* dead = &sm.dead;
+  // As in few4_kernel: false where it gave up, and a warp that gave up a side of a tile
+  // frees no stage any more.
   auto wait = [&](uint64_t& bar, uint32_t parity) {
-    if (mbar_try_wait(smem_addr(&bar), parity)) return;
-    if (*dead) return;
+    if (mbar_try_wait(smem_addr(&bar), parity)) return true;
+    if (*dead) return false;
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait_suspend(smem_addr(&bar), parity, 20000u)) {
-      if (*dead) return;
+      if (*dead) return false;
       if (global_timer_ns() - t0 > a.timeout_ns) {
         *dead = 1;
         flag_error(a.dev_err, kDevTimeout);
-        return;
+        return false;
       }
     }
+    return true;
   };
 
   if (warp < 4) {
@@ -805,8 +812,9 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
     if (warp == 0) {
       // ==== work list and loads ====
       uint32_t n_items = 0, n_tiles = 0;
-      uint32_t n_sides = 0, n_loads = 0;                  // sides of tiles; up to which copies began
+      uint32_t n_sides = 0;                               // sides of tiles whose copies began
       uint32_t st = 0, st_par = 1;                        // of the next side
+      bool stopped = false;                               // no more copies
       auto publish = [&](const Gqa8Item& it) {
         const int s = n_items & 1;
         wait(sm.item_empty[s], ((n_items >> 1) & 1) ^ 1);
@@ -819,7 +827,7 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
         ++n_items;
       };
       auto load_item = [&](const Gqa8Item& it) {
-        for (int t = it.t_begin; t < it.t_end; t += 16) {
+        for (int t = it.t_begin; t < it.t_end && !stopped; t += 16) {
           // page `lane` of 16 tiles: its K and V, or -1 where no key of it is seen
           // or the table has none
           const int64_t page = 2 * static_cast<int64_t>(t) + lane;
@@ -839,7 +847,8 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
               // not free yet)
               if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_addr(&sm.raw_empty[st]), st_par))) {
                 wait(sm.raw_empty[st], st_par);
-                if (__any_sync(0xFFFFFFFFu, *dead != 0)) return;
+                stopped = __any_sync(0xFFFFFFFFu, *dead != 0);
+                if (stopped) return;
               }
               if (elect_one()) {
                 if (side == 0) {
@@ -863,7 +872,7 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
                   }
               }
               __syncwarp();
-              n_loads = ++n_sides;
+              ++n_sides;
               if (++st == NR) {
                 st = 0;
                 st_par ^= 1;
@@ -885,7 +894,7 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
         wait(sm.v_empty[i & 1], (i >> 1) & 1);
       }
       if (*dead && lane == 0)
-        for (uint32_t i = n_loads > NR ? n_loads - NR : 0; i < n_loads; ++i)
+        for (uint32_t i = n_sides > NR ? n_sides - NR : 0; i < n_sides; ++i)
           mbar_wait_bounded(smem_addr(&sm.raw_full[i % NR]), (i / NR) & 1, 1000000);
     } else if (warp == 1) {
       // ==== products (the whole warp; one lane issues) ====
@@ -1084,7 +1093,11 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
           for (int side = 0; side < 2; ++side) {          // K, V
             uint4 w[2][kPieces];
             uint32_t sc[2][kPieces];
-            wait(sm.raw_full[st], st_par);
+            // (a side that was given up frees no stage, and its block is at its last item)
+            if (!__all_sync(0xFFFFFFFFu, wait(sm.raw_full[st], st_par))) {
+              t = t1;
+              break;
+            }
             const uint8_t* const src = raw_s + st * C::kSide;
 #pragma unroll
             for (int pg = 0; pg < 2; ++pg) {

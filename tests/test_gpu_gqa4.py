@@ -666,6 +666,44 @@ def test_a_wait_that_runs_out(d, dtype, hq, n):
     assert torch.equal(got[0][:n * B], want[0][:n * B]) and torch.equal(got[1][:n * B], want[1][:n * B])
 
 
+@pytest.mark.parametrize("limit", [1, 1500, 4000, 12000])
+@pytest.mark.parametrize("d,dtype,hq,n,B,length", [
+    (128, BF16, 16, 1, 150, 3000), (128, F16, 4, 1, 3, 60000), (64, BF16, 16, 1, 150, 5000), (64, F16, 10, 5, 60, 3000),
+    (64, BF16, 48, 2, 60, 3000), (128, BF16, 8, 70, 40, 3000), (64, F16, 4, 300, 30, 3000)])
+def test_waits_that_give_up_with_copies_on_their_way(d, dtype, hq, n, B, length, limit):
+    """A limit as short as a copy's own time: any wait of a block may be the one that
+    gives up, on whatever is on its way (or none, where the hardware's own suspension of a
+    waiting thread outlasts them all: a short call may still be whole, but not without
+    saying so otherwise).  The call ends, what it does not own stays as it is, and the next
+    call is whole."""
+    device = dev()
+    lens = [max(n, length - 37 * (i % 40)) for i in range(B)]
+    c = ref.Cache(lens, 2, d, device, seed=26)
+    q = torch.randn(n * B + 3, hq, d, device=device).to(dtype)
+    args = (q, c.pool, c.scales, c.page_table, c.seq_lens, ints(ref.cu_of([n] * B), device), n, 0.09)
+    size = kv.attention_gqa4_workspace(B, n, n * B + 3, hq, 2, d)
+    ws = torch.full((size + 4096,), 7, dtype=torch.uint8, device=device)
+    want = kv.attention_gqa4(*args, workspace=ws[:size])
+    held = c.pool.clone(), c.scales.clone(), q.clone()
+    out, lse = (torch.full((n * B + 3, hq, d), 3.0, dtype=dtype, device=device),
+                torch.full((n * B + 3, hq), 3.0, device=device))
+    kv.set_wait_limit(limit)
+    try:
+        for _ in range(5):
+            err = torch.zeros(1, dtype=torch.int32, device=device)
+            kv.attention_gqa4(*args, out=out, lse=lse, workspace=ws[:size], dev_err=err)
+            torch.cuda.synchronize()
+            assert int(err.item()) in (0, kv.DEV_TIMEOUT)
+            if int(err.item()) == 0:
+                assert torch.equal(out[:n * B], want[0][:n * B]) and torch.equal(lse[:n * B], want[1][:n * B])
+    finally:
+        kv.set_wait_limit()
+    assert (out[n * B:] == 3).all() and (lse[n * B:] == 3).all() and (ws[size:] == 7).all()
+    assert all(torch.equal(x, y) for x, y in zip(held, (c.pool, c.scales, q)))
+    got = kv.attention_gqa4(*args, workspace=ws[:size])
+    assert torch.equal(got[0][:n * B], want[0][:n * B]) and torch.equal(got[1][:n * B], want[1][:n * B])
+
+
 # ---------------------------------------------------------------------------
 # what the binding takes and refuses
 # ---------------------------------------------------------------------------
