@@ -10,6 +10,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <new>
+#include <utility>
 
 namespace {
 
@@ -974,6 +975,32 @@ bool strides_ok(const void* p, int64_t token, int64_t head, int heads, int D) {
          (heads == 1 || head >= D);
 }
 
+// Whether rows of D elements, one for each of n x m pairs at i * a + j * b, share none.
+bool rows_apart(int64_t n, int64_t a, int64_t m, int64_t b, int64_t D) {
+  if ((n > 1 && a < D) || (m > 1 && b < D)) return false;
+  if (n <= 1 || m <= 1) return true;
+  // the rows of one dimension between two of the other's
+  if ((a - D) / b >= m - 1 || (b - D) / a >= n - 1) return true;
+  // else two rows meet where i steps of the one stride end less than D from j of the
+  // other's, 1 <= i < n, 1 <= j < m
+  if (n > m) {
+    std::swap(n, m);
+    std::swap(a, b);
+  }
+  int64_t j = 0, over = 0;                                 // i a = j b + over
+  for (int64_t i = 1; i < n; ++i) {
+    j += a / b;
+    over += a % b;
+    if (over >= b) {
+      over -= b;
+      ++j;
+    }
+    if (j >= m) break;                                     // (and from here on)
+    if ((j >= 1 && over < D) || (j + 1 < m && b - over < D)) return false;
+  }
+  return true;
+}
+
 kv4_status append_gqa(const GqaFormat& f, const void* k_dev, int64_t k_token_stride, int64_t k_head_stride,
                            const void* v_dev, int64_t v_token_stride, int64_t v_head_stride,
                            int dtype, int64_t n_tokens, const int32_t* cu_seqlens_dev,
@@ -1242,7 +1269,7 @@ kv4_status kv4_rotary(const void* q_dev, int64_t q_token_stride, int64_t q_head_
         s.in_token < 0 || s.in_head < 0 || s.out_token < 0 || s.out_head < 0)
       return KV4_ERR_INVALID_ARG;
     // outputs' rows lie apart; one that is its input has its strides
-    if ((s.heads > 1 && s.out_head < s.D) || (n_tokens > 1 && s.out_token < s.D) ||
+    if (!rows_apart(n_tokens, s.out_token, s.heads, s.out_head, s.D) ||
         (s.in == s.out && ((n_tokens > 1 && s.in_token != s.out_token) || (s.heads > 1 && s.in_head != s.out_head))))
       return KV4_ERR_INVALID_ARG;
   }

@@ -35,7 +35,7 @@ def rotary(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tens
     else halves (i, n + i).  Turned elements are multiplied by `factor` (a stretched
     context's attention factor, for instance), the others copied.  Returns (q, k),
     new tensors unless q_out or k_out is given, which may be the input itself and else
-    shares no element with q, k or the other output.  No gradients are computed; that of
+    shares no element with q, k or the other output; its own rows share none either.  No gradients are computed; that of
     a rotation is the rotation by -positions of the outputs' gradients."""
     r = (_ext or _load()).rotary(q, k, positions, inv_freq, interleaved, q_offset, k_offset, factor, q_out, k_out)
     if type(r) is int:

@@ -646,8 +646,8 @@ kv4_status kv4_attention_gqa4(const void* q_dev, int64_t q_token_stride, int64_t
  *                   elements; heads' elements contiguous); Hq or Hk may be 0, and
  *                   that side's pointers are then not looked at.  Hq + Hk <=
  *                   65535, D <= 65536
- *   q_out_dev, ..   the same shapes, rows at least D elements apart; an output is
- *                   its input, with the same strides, or overlaps no input, and
+ *   q_out_dev, ..   the same shapes, no two rows with an element in common; an output
+ *                   is its input, with the same strides, or overlaps no input, and
  *                   overlaps not the other output
  *   positions_dev   int32 or int64 [n_tokens] (position_bits 32 or 64),
  *                   magnitudes up to 2^31

@@ -237,6 +237,31 @@ def test_slices_of_one_tensor_turn_in_place(t, near):
         assert torch.equal(q, want[0]) and torch.equal(k, want[1])
 
 
+def test_outputs_whose_own_rows_meet_are_refused():
+    """Sliding windows, out of place and in place; nothing is written.  Rows that lie
+    between one another's, tokens inside heads among them, are fine."""
+    device = dev()
+    freq, pos = kv.rotary_frequencies(64, device=device), torch.arange(6, device=device) + 3
+    x = torch.randn(6, 3, 64, device=device).to(BF16)
+    want = kv.rotary(x, None, pos, freq)[0]
+    flat = torch.randn(6000, device=device).to(BF16)
+    kept = flat.clone()
+    for strides in ((64, 64, 1), (128, 64, 1), (64, 128, 1), (128, 192, 1), (129, 65, 1), (330, 192, 1)):
+        slide = flat.as_strided((6, 3, 64), strides)
+        for q in (x, slide):
+            with pytest.raises(kv.Kv4Error):
+                kv.rotary(q, None, pos, freq, q_out=slide)
+    torch.cuda.synchronize()
+    assert torch.equal(flat, kept)
+    for strides in ((192, 64, 1), (64, 384, 1), (64, 400, 1), (250, 70, 1), (512, 192, 1), (320, 192, 1), (384, 704, 1)):
+        out = flat.as_strided((6, 3, 64), strides)
+        kv.rotary(x, None, pos, freq, q_out=out)
+        assert torch.equal(out, want)
+        out.copy_(x)
+        kv.rotary(out, None, pos, freq, q_out=out)
+        assert torch.equal(out, want)
+
+
 def test_empty_calls():
     device = dev()
     freq, pos = torch.ones(4, device=device), torch.zeros(0, dtype=torch.int64, device=device)

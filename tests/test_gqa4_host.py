@@ -71,6 +71,35 @@ def test_rotary_refuses(lib, mem, change, status):  # noqa: F811
     assert lib.kv4_rotary(*rotary_args(mem[1], **change)) == status
 
 
+def rows_meet(t, token, h, head, d):
+    """Whether two of the rows [i * token + j * head, + d) share an element, by looking."""
+    at = sorted(i * token + j * head for i in range(t) for j in range(h))
+    return any(y - x < d for x, y in zip(at, at[1:]))
+
+
+def test_rotary_refuses_outputs_whose_rows_meet(lib, mem):  # noqa: F811
+    """All strides of small outputs, out of place and in place: a step that is at least a
+    row long is not enough, and rows of one dimension may lie between the other's."""
+    refused = accepted = 0
+    for t in range(1, 6):
+        for h in range(1, 5):
+            for token in range(1, 27):
+                for head in range(1, 19):
+                    meet = rows_meet(t, token, h, head, 4)
+                    refused, accepted = refused + meet, accepted + (not meet)
+                    if not meet and torch.cuda.is_available():
+                        continue                                  # (it would be launched)
+                    one = dict(T=t, n=2, k=None, kout=None, hk=0, hq=h, dq=4, qos0=token, qos1=head)
+                    for args in (dict(one, qs0=64, qs1=8, qout=mem[1] + 64), dict(one, qs0=token, qs1=head)):
+                        assert (lib.kv4_rotary(*rotary_args(mem[1], **args)) == BAD) == meet, (t, token, h, head)
+    assert refused > 1000 and accepted > 1000
+    # sizes at which a product of steps and strides would leave 64 bits
+    for t, token, h, head, meet in ((2 ** 31 - 1, 2 ** 62, 65535, 2 ** 62, True), (2 ** 31 - 1, 64, 65535, 64, True),
+                                    (2 ** 31 - 1, 64, 65535, 2 ** 31 * 64 - 128, True), (2 ** 20, 2 ** 61 + 1, 3, 2 ** 62, True)):
+        args = dict(T=t, n=2, k=None, kout=None, hk=0, hq=h, dq=4, qos0=token, qos1=head, qs0=0, qs1=0, qout=mem[1] + 64)
+        assert (lib.kv4_rotary(*rotary_args(mem[1], **args)) == BAD) == meet
+
+
 def test_rotary_alignment(lib, mem):  # noqa: F811
     for change in (dict(q=mem[1] + 1), dict(kout=mem[1] + 3), dict(pos=mem[1] + 2), dict(pos=mem[1] + 4, bits=64),
                    dict(freq=mem[1] + 2)):
