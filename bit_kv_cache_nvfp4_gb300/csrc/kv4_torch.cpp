@@ -390,6 +390,10 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (freq.dim() != 1 || !freq.is_contiguous()) value_error("inv_freq must have one dimension, contiguous");
     if (freq.device() != dev) value_error("inv_freq is on " + freq.device().str() + ", the inputs on " + dev.str());
     const int near = PyObject_IsTrue(a[4]);
+    if (near < 0) {
+      PyErr_Clear();
+      type_error("interleaved must be a truth value");
+    }
     const int q_at = small(a[5], "q_offset"), k_at = small(a[6], "k_offset");
     const double factor = PyFloat_AsDouble(a[7]);
     if (factor == -1.0 && PyErr_Occurred()) {

@@ -262,6 +262,18 @@ def test_outputs_whose_own_rows_meet_are_refused():
         assert torch.equal(out, want)
 
 
+def test_interleaved_without_a_truth_value_is_refused():
+    """Before anything is written, in place."""
+    device = dev()
+    good, _ = refusals(device)
+    q, k = good["q"].clone(), good["k"].clone()
+    for value in (torch.ones(2), torch.ones(2, device=device)):
+        with pytest.raises(TypeError, match="interleaved"):
+            kv.rotary(**{**good, "q": q, "k": k, "interleaved": value, "q_out": q, "k_out": k})
+    torch.cuda.synchronize()
+    assert torch.equal(q, good["q"]) and torch.equal(k, good["k"])
+
+
 def test_empty_calls():
     device = dev()
     freq, pos = torch.ones(4, device=device), torch.zeros(0, dtype=torch.int64, device=device)
