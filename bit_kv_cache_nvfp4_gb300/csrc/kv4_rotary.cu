@@ -34,7 +34,7 @@ constexpr int kBlock = 256, kTable = 2048;                // threads; angles of 
 // 1 / 2 pi = 0x0.28BE60DB9391054A.. of a turn.
 __device__ __forceinline__ uint64_t turn_fraction(float inv_freq) {
   const uint32_t u = __float_as_uint(inv_freq), e = (u >> 23) & 255u;
-  if (e == 0 || e == 255) return 0;                       // 0 and subnormals: no turn at all
+  if (e == 0 || e == 255) return 0;                       // 0 and subnormals: no turn; not finite: see below
   const uint64_t m = static_cast<uint64_t>((u & 0x7FFFFFu) | 0x800000u) << 40;
   const uint64_t p = __umul64hi(m, 0x28BE60DB9391054Aull);                 // m / 2 pi, of 2^(e - 126)
   const uint64_t f = e <= 126 ? (e >= 63 ? p >> (126 - e) : 0) : (e < 190 ? p << (e - 126) : 0);
@@ -120,9 +120,11 @@ __global__ void __launch_bounds__(V == 1 ? 2 * kBlock : kBlock) rotary_kernel(co
     const int kt = k / a.n;
     const int64_t pos = a.wide_positions ? load(static_cast<const int64_t*>(a.positions) + t0 + kt)
                                          : load(static_cast<const int32_t*>(a.positions) + t0 + kt);
-    const uint64_t turn = static_cast<uint64_t>(pos) * turn_fraction(load(a.inv_freq + (k - kt * a.n)));
+    const float freq = load(a.inv_freq + (k - kt * a.n));
+    const uint64_t turn = static_cast<uint64_t>(pos) * turn_fraction(freq);
     float s, c;
-    sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s, &c);
+    // (freq - freq: 0, or NaN of a frequency that is not finite)
+    sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f + (freq - freq), &s, &c);
     cosine[k] = c * a.factor;
     sine[k] = s * a.factor;
   }

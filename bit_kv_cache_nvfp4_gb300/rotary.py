@@ -30,12 +30,14 @@ def rotary(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tens
     """q and k with their rotary positions (kv4_rotary).
 
     q, k bf16 or f16 [T, heads, D], strided, either may be None; positions int32
-    or int64 [T]; inv_freq fp32 [n] in radians a position.  2 n elements of each
-    head turn, from the offset on: neighbours (2i, 2i + 1) where `interleaved`,
-    else halves (i, n + i).  Turned elements are multiplied by `factor` (a stretched
-    context's attention factor, for instance), the others copied.  Returns (q, k),
-    new tensors unless q_out or k_out is given, which may be the input itself and else
-    shares no element with q, k or the other output; its own rows share none either.  No gradients are computed; that of
+    or int64 [T], magnitudes up to 2^31; inv_freq fp32 [n] in radians a position, n up
+    to 512, magnitudes up to 4 (beyond, and at farther positions, angles lose bits;
+    one that is not finite makes its pair NaN).  2 n elements of each head turn, from
+    the offset on: neighbours (2i, 2i + 1) where `interleaved`, else halves (i, n + i).
+    Turned elements are multiplied by `factor` (a stretched context's attention factor,
+    for instance), the others copied.  Returns (q, k), new tensors unless q_out or k_out
+    is given, which may be the input itself and else shares no element with q, k or the
+    other output; its own rows share none either.  No gradients are computed; that of
     a rotation is the rotation by -positions of the outputs' gradients."""
     r = (_ext or _load()).rotary(q, k, positions, inv_freq, interleaved, q_offset, k_offset, factor, q_out, k_out)
     if type(r) is int:

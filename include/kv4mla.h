@@ -652,7 +652,7 @@ kv4_status kv4_attention_gqa4(const void* q_dev, int64_t q_token_stride, int64_t
  *   positions_dev   int32 or int64 [n_tokens] (position_bits 32 or 64),
  *                   magnitudes up to 2^31
  *   inv_freq_dev    fp32 [n_pairs], 1 <= n_pairs <= 512, magnitudes up to 4:
- *                   radians a position
+ *                   radians a position; one that is not finite makes its pair NaN
  * Pair i of a head is elements (offset + 2i, offset + 2i + 1) where interleaved is
  * nonzero and (offset + i, offset + n_pairs + i) where it is 0; with the angle
  * a = position * inv_freq[i] (reduced to less than a turn in integers, to 2^-29 of

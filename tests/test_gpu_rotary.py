@@ -274,6 +274,28 @@ def test_interleaved_without_a_truth_value_is_refused():
     assert torch.equal(q, good["q"]) and torch.equal(k, good["k"])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("near", [False, True])
+@pytest.mark.parametrize("n", [16, 5])
+def test_frequencies_that_are_not_finite_give_nan_in_their_pairs(n, near, dtype):
+    """At position 0 too (0 * inf is NaN); the other pairs and what does not turn are as
+    without them."""
+    device = dev()
+    x = torch.randn(40, 3, 40, device=device).to(dtype)
+    pos = torch.arange(40, device=device) * 7
+    freq = kv.rotary_frequencies(2 * n, device=device)
+    want = kv.rotary(x, None, pos, freq, interleaved=near, q_offset=3)[0]
+    bad = {0: math.nan, 2: math.inf, n - 1: -math.inf}
+    odd = freq.clone()
+    for i, value in bad.items():
+        odd[i] = value
+        first = 3 + (2 * i if near else i)
+        want[..., first] = want[..., first + (1 if near else n)] = math.nan
+    got = kv.rotary(x, None, pos, odd, interleaved=near, q_offset=3)[0]
+    assert torch.equal(got.isnan(), want.isnan()) and int(got.isnan().sum()) == 40 * 3 * 6
+    assert torch.equal(got.nan_to_num(), want.nan_to_num())
+
+
 def test_empty_calls():
     device = dev()
     freq, pos = torch.ones(4, device=device), torch.zeros(0, dtype=torch.int64, device=device)
