@@ -1042,12 +1042,6 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
         if (a.fault_site == 1) wait(sm.never, 0);
       }
       if (a.fault_site == 1) wait(sm.never, 0);
-      // in a block that gave up, which any role may still do, nothing else waits for
-      // the products that are queued: they end before its memory goes away
-      __syncwarp();
-      if (elect_one()) mma_commit(smem_addr(&sm.never));
-      __syncwarp();
-      mbar_wait_bounded(smem_addr(&sm.never), 0, 1000000);
     }
   } else if (warp < 8) {
     setmaxnreg_dec<kWidenRegs>();
@@ -1420,7 +1414,17 @@ many4_kernel(const Gqa8AttnArgs a, const int min_rows,
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) {
+    // In a block that gave up, which any role may have done up to here, nothing has
+    // waited for the products that are queued: they end before its memory goes away.
+    if (__any_sync(0xFFFFFFFFu, *dead != 0)) {
+      if (elect_one()) mma_commit(smem_addr(&sm.never));
+      __syncwarp();
+      mbar_wait_bounded(smem_addr(&sm.never), 0, 1000000);
+      __syncwarp();
+    }
+    tmem_dealloc(tmem, 512);
+  }
 }
 
 // ---------------------------------------------------------------------------

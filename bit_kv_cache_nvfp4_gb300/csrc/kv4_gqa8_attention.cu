@@ -245,15 +245,6 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
     auto ready = [&](uint64_t& bar, uint32_t parity) {
       return __any_sync(0xFFFFFFFFu, mbar_try_wait(smem_addr(&bar), parity));
     };
-    // In a block that gave up, which any role may still do, nothing else waits for the
-    // products that are queued: they end before its memory goes away.
-    auto drain = [&] {
-      if (a.fault_site == 1) wait(sm.never, 0);
-      __syncwarp();
-      if (elect_one()) mma_commit(smem_addr(&sm.never));
-      __syncwarp();
-      mbar_wait_bounded(smem_addr(&sm.never), 0, 1000000);
-    };
     bool pending = false;
     while (true) {
       const int s = n_items & 3;
@@ -311,7 +302,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
       ++n_items;
     }
     if (pending) pv(n_tiles - 1);
-    drain();
+    if (a.fault_site == 1) wait(sm.never, 0);
   } else if (warp < 4) {
     // ==== q of the next item, as NT E4M3 terms ====
     constexpr int TPR = D / 16, RPP = 64 / TPR;           // threads a row, rows at once
@@ -595,7 +586,17 @@ few_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const 
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, C::kTmem);
+  if (warp == 1) {
+    // In a block that gave up, which any role may have done up to here, nothing has
+    // waited for the products that are queued: they end before its memory goes away.
+    if (__any_sync(0xFFFFFFFFu, *dead != 0)) {
+      if (elect_one()) mma_commit(smem_addr(&sm.never));
+      __syncwarp();
+      mbar_wait_bounded(smem_addr(&sm.never), 0, 1000000);
+      __syncwarp();
+    }
+    tmem_dealloc(tmem, C::kTmem);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -945,12 +946,6 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
         if (a.fault_site == 1) wait(sm.never, 0);
       }
       if (a.fault_site == 1) wait(sm.never, 0);
-      // in a block that gave up, which any role may still do, nothing else waits for
-      // the products that are queued: they end before its memory goes away
-      __syncwarp();
-      if (elect_one()) mma_commit(smem_addr(&sm.never));
-      __syncwarp();
-      mbar_wait_bounded(smem_addr(&sm.never), 0, 1000000);
     } else {
       // ==== V to f16 ====
       uint32_t j = 0;
@@ -1281,7 +1276,17 @@ many_kernel(const __grid_constant__ CUtensorMap map, const Gqa8AttnArgs a, const
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) {
+    // In a block that gave up, which any role may have done up to here, nothing has
+    // waited for the products that are queued: they end before its memory goes away.
+    if (__any_sync(0xFFFFFFFFu, *dead != 0)) {
+      if (elect_one()) mma_commit(smem_addr(&sm.never));
+      __syncwarp();
+      mbar_wait_bounded(smem_addr(&sm.never), 0, 1000000);
+      __syncwarp();
+    }
+    tmem_dealloc(tmem, 512);
+  }
 }
 
 // ---------------------------------------------------------------------------

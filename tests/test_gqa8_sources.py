@@ -25,10 +25,10 @@ def test_kernels_that_begin_early_read_nothing_as_read_only(name):
 
 @pytest.mark.parametrize("name,kernels", [("kv4_gqa8_attention.cu", 2), ("kv4_gqa4_attention.cu", 1)])
 def test_queued_products_end_before_a_block_does(name, kernels):
-    """Whoever gives up a wait may do so behind the last product's issue, so the issuing
-    warp waits for what it queued whether or not the block has given up by then."""
+    """Whoever gives up a wait may do so behind the last product's issue, so whether a
+    block has given up is looked at behind the barrier that all its waits come before."""
     code = re.sub(r"//[^\n]*", "", (CSRC / name).read_text())
-    drains = re.findall(r"([^\n]*)\n *__syncwarp\(\);\n *if \(elect_one\(\)\) mma_commit\(smem_addr\(&sm\.never\)\);"
-                        r"\n *__syncwarp\(\);\n *mbar_wait_bounded\(smem_addr\(&sm\.never\)", code)
-    assert len(drains) == kernels == code.count("mma_commit(smem_addr(&sm.never))")
-    assert not any("dead" in line for line in drains)
+    ends = re.findall(r"__syncthreads\(\);\s*if \(warp == 1\) \{\s*if \(__any_sync\(0xFFFFFFFFu, \*dead != 0\)\) \{\s*"
+                      r"if \(elect_one\(\)\) mma_commit\(smem_addr\(&sm\.never\)\);\s*__syncwarp\(\);\s*"
+                      r"mbar_wait_bounded\(smem_addr\(&sm\.never\)[^}]*\}\s*tmem_dealloc", code)
+    assert len(ends) == kernels == code.count("mma_commit(smem_addr(&sm.never))") == code.count("tmem_dealloc(")
