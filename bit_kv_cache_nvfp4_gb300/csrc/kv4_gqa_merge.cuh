@@ -17,118 +17,109 @@ namespace {
 // The pieces of items that were cut: block (c, y) joins rows of the item that
 // began in block c of the attention kernel, by log-sum-exp over its pieces in
 // their order: one kernel for items of few rows, where a long context has many
-// pieces and 8 warps share a row, one for items of up to 256 rows, where a warp
-// takes 4 rows at once and their pieces in turn.  Those of a prompt or a chunk are
+// pieces, one for items of up to 256 rows, where a warp takes 4 rows at once and
+// their pieces in turn.  Those of a prompt or a chunk are
 // two or three; but a single short one of few heads over a long context is cut
 // over all blocks (40 rows of one head over 200000 tokens: 97 us, where one row,
 // in the kernels of few rows, takes 28).
 // ---------------------------------------------------------------------------
-// Block (c, y) takes `each` rows, 8 or 1.  Up to 8 pieces a warp takes in one go, a row
-// by itself; more of them the 8 warps share, row after row.  (So 8 rows a block where
-// requests and heads are many, whose items are cut in two or three; and 1 where few of
-// them are cut over all blocks.  A block for every row: drafts of 35 rows 34.6 us for 28.8,
-// 64 sessions' decode step 227 for 223, of the 4-bit cache.)
-template <int D>
-__global__ void __launch_bounds__(256) merge_few_kernel(const Gqa8AttnArgs a, const int rows, const int each,
-                                                    const Gqa8Tail* tails, const float* ws_lse,
-                                                    const float* ws_o) {
+// Block (c, y) takes EACH rows: 8, a warp each, 8 pieces at a time with the next 8 on
+// their way, where requests and heads are many, whose items are cut in two or three; or 1,
+// whose pieces its 8 warps share, where few items are cut over all blocks.  Both add up
+// pieces 0, 8, 16, .., pieces 1, 9, .. and so on by themselves, and then those sums.  (A
+// block for every row: drafts of 35 rows 34.6 us for 28.8, 64 sessions' decode step 227 for
+// 223, of the 4-bit cache.  Among many requests one may be cut over all blocks as well, which
+// only the device knows: 63 padded slots and a session of 200000 tokens, 8 heads a group,
+// take 76 us from the 8-bit cache, 75 with a block for every row, 90 with a block's 8 warps
+// on its 8 rows in turns.  Two blocks an SM are enough, and leave the registers for 16
+// pieces: 200 of them, one K/V head's, in 5 us less than with three.)
+template <int D, int EACH>
+__global__ void __launch_bounds__(256, 2) merge_few_kernel(const Gqa8AttnArgs a, const int rows,
+                                                        const Gqa8Tail* tails, const float* ws_lse,
+                                                        const float* ws_o) {
   grid_dependency_wait();
   grid_launch_dependents();
-  constexpr int C = D / 32, W = 8;                        // columns a lane; warps
+  constexpr int C = D / 32, W = 8;                        // columns a lane; warps, and sums of a row
   using Vec = std::conditional_t<C == 4, float4, float2>;
-  __shared__ Vec part[W][32];
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Gqa8Tail t = tails[c];
-  const int r_begin = blockIdx.y * each, r_end = min(t.nrows, r_begin + each);
-  if (t.parts == 0 || r_begin >= r_end) return;           // (whole blocks)
-  // piece i of row r is slot 2c + 1 for i = 0, else 2 (c + i)
-  auto row_of = [&](int i, int r) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * rows + r; };
-  auto finish = [&](int r, float m, float s, const float (&o)[C]) {
-    const int G = a.Hq / a.Hkv, rr = t.r0 + r;
-    const int64_t row = static_cast<int64_t>(t.cu0 + rr / G) * a.Hq + t.h * G + rr % G;
-    const float inv = s == 0.0f ? 0.0f : 1.0f / s;
-    uint32_t u[C / 2];
+  const int r = blockIdx.y * EACH + (EACH == 1 ? 0 : warp);
+  if (t.parts == 0 || r >= t.nrows) return;               // (whole blocks of one row)
+  // piece i is slot 2c + 1 for i = 0, else 2 (c + i)
+  auto row_of = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * rows + r; };
+  auto piece = [&](int i) { return load(reinterpret_cast<const Vec*>(ws_o + row_of(i) * D) + lane); };
+  float x = lane < t.parts ? load(ws_lse + row_of(lane)) : -INFINITY;
+  // (the first 8 pieces on their way with it)
+  Vec v[W];
+  if constexpr (EACH > 1)
 #pragma unroll
-    for (int k = 0; k < C / 2; ++k) {
-      const float y0 = o[2 * k] * inv, y1 = o[2 * k + 1] * inv;
-      u[k] = a.f16 ? pack16<true>(y0, y1) : pack16<false>(y0, y1);
-    }
-    uint32_t* const dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * D) + lane * (C / 2);
-    if constexpr (C == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[1]);
-    else *dst = u[0];
-    if (lane == 0) a.lse[row] = s == 0.0f ? -INFINITY : (m + log2f(s)) * 0.6931471805599453f;
-  };
-  if (t.parts <= W) {
-    const int r = r_begin + warp;
-    if (r >= r_end) return;
-    const float x = lane < t.parts ? load(ws_lse + row_of(lane, r)) : -INFINITY;
-    Vec v[W];
+    for (int j = 0; j < W; ++j)
+      if (j < t.parts) v[j] = piece(j);
+  float m = x, s = 0.0f, o[W][C];                         // (of one row a block o[0] alone, the warp's)
 #pragma unroll
-    for (int i = 0; i < W; ++i)
-      if (i < t.parts) v[i] = load(reinterpret_cast<const Vec*>(ws_o + row_of(i, r) * D) + lane);
-    const float m = warp_max(x);
-    const bool odd = __any_sync(0xFFFFFFFFu, x != x);
-    float o[C];
+  for (int j = 0; j < W; ++j)
 #pragma unroll
-    for (int k = 0; k < C; ++k) o[k] = 0.0f;
-    float s = 0.0f;
-    if (m > -INFINITY) {
-      const float w = lane < t.parts ? fast_exp2(x - m) : 0.0f;
-#pragma unroll
-      for (int i = 0; i < W; ++i)
-        if (i < t.parts) {
-          const float wt = __shfl_sync(0xFFFFFFFFu, w, i);
-          const float* f = reinterpret_cast<const float*>(&v[i]);
-#pragma unroll
-          for (int k = 0; k < C; ++k) o[k] += __fmul_rn(wt, f[k]);
-        }
-      s = warp_sum(w);
-    }
-    finish(r, m, odd ? __uint_as_float(0x7FC00000u) : s, o);
-    return;
+    for (int k = 0; k < C; ++k) o[j][k] = 0.0f;
+  bool odd = x != x;
+  for (int i = 32 + lane; i < t.parts; i += 32) {
+    const float y = load(ws_lse + row_of(i));
+    odd |= y != y;
+    m = fmaxf(m, y);
   }
+  m = warp_max(m);
+  odd = __any_sync(0xFFFFFFFFu, odd);
 #pragma unroll 1
-  for (int r = r_begin; r < r_end; ++r) {
-    float o[C], m = -INFINITY, s = 0.0f;
+  for (int i0 = 0; i0 < t.parts; i0 += 32) {
+    if (i0 > 0) x = i0 + lane < t.parts ? load(ws_lse + row_of(i0 + lane)) : -INFINITY;
+    const float w = m > -INFINITY ? fast_exp2(x - m) : 0.0f;
+    s += w;
+    const int n = min(32, t.parts - i0);
+    auto add = [&](int i, const Vec& y, float (&to)[C]) {
+      const float wt = __shfl_sync(0xFFFFFFFFu, w, i);
+      const float* f = reinterpret_cast<const float*>(&y);
 #pragma unroll
-    for (int k = 0; k < C; ++k) o[k] = 0.0f;
-    bool odd = false;
-    for (int i = lane; i < t.parts; i += 32) {
-      const float x = load(ws_lse + row_of(i, r));
-      odd |= x != x;
-      m = fmaxf(m, x);
-    }
-    m = warp_max(m);
-    odd = __any_sync(0xFFFFFFFFu, odd);
-    if (m > -INFINITY) {
-      for (int i0 = 0; i0 < t.parts; i0 += 32) {
-        const float w = i0 + lane < t.parts ? fast_exp2(load(ws_lse + row_of(i0 + lane, r)) - m) : 0.0f;
-        s += w;
-        const int n = min(32, t.parts - i0);
+      for (int k = 0; k < C; ++k) to[k] = fmaf(wt, f[k], to[k]);
+    };
+    if constexpr (EACH == 1) {
 #pragma unroll 4
-        for (int i = warp; i < n; i += W) {
-          const float wt = __shfl_sync(0xFFFFFFFFu, w, i);
-          const Vec v = load(reinterpret_cast<const Vec*>(ws_o + row_of(i0 + i, r) * D) + lane);
-          const float* f = reinterpret_cast<const float*>(&v);
+      for (int i = warp; i < n; i += W) add(i, piece(i0 + i), o[0]);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < n; i += W)
 #pragma unroll
-          for (int k = 0; k < C; ++k) o[k] = fmaf(wt, f[k], o[k]);
+        for (int j = 0; j < W; ++j) {
+          if (i + j < n) add(i + j, v[j], o[j]);
+          if (i0 + i + j + W < t.parts) v[j] = piece(i0 + i + j + W);
         }
-      }
-      s = warp_sum(s);
     }
-    part[warp][lane] = *reinterpret_cast<const Vec*>(o);
-    __syncthreads();
-    if (warp == 0) {
-#pragma unroll
-      for (int i = 1; i < W; ++i) {
-        const Vec v = part[i][lane];
-#pragma unroll
-        for (int k = 0; k < C; ++k) o[k] += reinterpret_cast<const float*>(&v)[k];
-      }
-      finish(r, m, odd ? __uint_as_float(0x7FC00000u) : s, o);
-    }
-    __syncthreads();
   }
+  s = warp_sum(s);
+  if (odd) s = __uint_as_float(0x7FC00000u);
+  if constexpr (EACH == 1) {
+    __shared__ Vec part[W][32];
+    part[warp][lane] = *reinterpret_cast<const Vec*>(o[0]);
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int j = 1; j < W; ++j) *reinterpret_cast<Vec*>(o[j]) = part[j][lane];
+  }
+#pragma unroll
+  for (int j = 1; j < W; ++j)
+#pragma unroll
+    for (int k = 0; k < C; ++k) o[0][k] += o[j][k];
+  const int G = a.Hq / a.Hkv, rr = t.r0 + r;
+  const int64_t row = static_cast<int64_t>(t.cu0 + rr / G) * a.Hq + t.h * G + rr % G;
+  const float inv = s == 0.0f ? 0.0f : 1.0f / s;
+  uint32_t u[C / 2];
+#pragma unroll
+  for (int k = 0; k < C / 2; ++k) {
+    const float y0 = o[0][2 * k] * inv, y1 = o[0][2 * k + 1] * inv;
+    u[k] = a.f16 ? pack16<true>(y0, y1) : pack16<false>(y0, y1);
+  }
+  uint32_t* const dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * D) + lane * (C / 2);
+  if constexpr (C == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[1]);
+  else *dst = u[0];
+  if (lane == 0) a.lse[row] = s == 0.0f ? -INFINITY : (m + log2f(s)) * 0.6931471805599453f;
 }
 
 template <int D>
@@ -236,9 +227,11 @@ cudaError_t launch_merge(void (*kernel)(Gqa8AttnArgs, Args...), const Gqa8AttnAr
 template <int D>
 cudaError_t launch_merge_few(const Gqa8AttnArgs& a, int blocks, int rows, const Parts& p, cudaStream_t stream) {
   // (of fewer items an average one may have more than 8 pieces)
-  const int each = static_cast<int64_t>(a.B) * a.Hkv * 8 >= blocks ? 8 : 1;
-  return launch_merge<int, int, const Gqa8Tail*, const float*, const float*>(
-      merge_few_kernel<D>, a, dim3(blocks, (rows + each - 1) / each), stream, rows, each, p.tails, p.lse, p.o);
+  if (static_cast<int64_t>(a.B) * a.Hkv * 8 >= blocks)
+    return launch_merge<int, const Gqa8Tail*, const float*, const float*>(
+        merge_few_kernel<D, 8>, a, dim3(blocks, (rows + 7) / 8), stream, rows, p.tails, p.lse, p.o);
+  return launch_merge<int, const Gqa8Tail*, const float*, const float*>(
+      merge_few_kernel<D, 1>, a, dim3(blocks, rows), stream, rows, p.tails, p.lse, p.o);
 }
 template <int D>
 cudaError_t launch_merge_many(const Gqa8AttnArgs& a, int blocks, int rows, const Parts& p, cudaStream_t stream) {
