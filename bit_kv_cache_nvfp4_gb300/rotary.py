@@ -57,7 +57,12 @@ def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str | None = No
                 stretch, the fastest kept
       "ramp"    those of fewer than `slow` turns over original_length divided by
                 stretch, those of more than `fast` kept, linear in the turns
-                between"""
+                between
+      "index_ramp"  the same ends, linear in the pair's index between: from the
+                index at which a frequency makes `fast` turns, rounded down, to
+                that of `slow` turns, rounded up.  In between it is several times
+                the other (4.3 at a stretch of 40): take the one that a model was
+                trained with"""
     if dim < 2 or dim % 2:
         raise ValueError(f"dim must be even and at least 2, got {dim}")
     if not (base > 0 and math.isfinite(base)) or not (stretch > 0 and math.isfinite(stretch)):
@@ -75,6 +80,15 @@ def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str | None = No
             raise ValueError("fast must be above slow")
         keep = ((original_length * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
         f = f * (keep + (1 - keep) / stretch)
+    elif scaling == "index_ramp":
+        if not (fast > slow > 0 and base > 1 and original_length > 0):
+            raise ValueError("fast must be above slow, slow and original_length above 0, base above 1")
+        # base^(-2 at / dim) * original_length = 2 pi turns
+        low, high = (dim * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base)) for turns in (fast, slow))
+        low, high = max(math.floor(low), 0), min(math.ceil(high), dim - 1)
+        # (a step where both are one index)
+        keep = 1 - ((torch.arange(dim // 2, dtype=torch.float64) - low) / max(high - low, 1e-3)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / stretch)
     elif scaling not in (None, "base"):
-        raise ValueError(f'scaling must be None, "linear", "base" or "ramp", got {scaling!r}')
+        raise ValueError(f'scaling must be None, "linear", "base", "ramp" or "index_ramp", got {scaling!r}')
     return f.float().to(device if device is not None else "cpu")

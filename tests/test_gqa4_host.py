@@ -130,12 +130,43 @@ def test_frequencies():
     assert torch.equal(kv.rotary_frequencies(2), torch.ones(1))
 
 
+def test_frequencies_of_a_ramp_by_index():
+    """64 turned elements over 4096 tokens: 32 turns are at pair 10.47, 1 turn at 22.52,
+    so pairs up to 10 are kept, those from 23 on divided, pair 16 six thirteenths between."""
+    want = [10000.0 ** (-i / 32) for i in range(32)]
+    assert math.floor(64 * math.log(4096 / (64 * math.pi)) / (2 * math.log(1e4))) == 10
+    assert math.ceil(64 * math.log(4096 / (2 * math.pi)) / (2 * math.log(1e4))) == 23
+    for i in range(32):
+        keep = min(max((23 - i) / 13, 0.0), 1.0)
+        want[i] *= keep + (1 - keep) / 40
+    args = dict(stretch=40.0, original_length=4096, slow=1.0, fast=32.0)
+    got = kv.rotary_frequencies(64, scaling="index_ramp", **args)
+    assert got.dtype == torch.float32
+    # (each rounded once: half a step of fp32)
+    assert (got.double() / torch.tensor(want, dtype=torch.float64) - 1).abs().max() <= 2.0 ** -24 * (1 + 2.0 ** -20)
+    by_turns = kv.rotary_frequencies(64, scaling="ramp", **args)
+    ratio = (by_turns / got).tolist()
+    assert all(abs(r - 1) < 1e-6 for r in ratio[:10] + ratio[24:]) and abs(ratio[11] - 0.93) < 0.01 and min(ratio) < 0.24
+    # a step, where both ends are one index, and ends beyond the pairs
+    step = kv.rotary_frequencies(64, scaling="index_ramp", stretch=4.0, original_length=2 * math.pi * 1.5, slow=1.0, fast=1.2)
+    assert step[0] == 1 and abs(float(step[2]) / 10000.0 ** (-2 / 32) - 0.25) < 1e-6
+    short = kv.rotary_frequencies(8, scaling="index_ramp", stretch=4.0, original_length=3)
+    assert torch.allclose(short.double(), 10000.0 ** (-torch.arange(4, dtype=torch.float64) / 4) / 4 * torch.tensor([4.0, 1, 1, 1]), rtol=1e-6)
+
+
 @pytest.mark.parametrize("args", [dict(dim=0), dict(dim=7), dict(dim=8, base=0.0), dict(dim=8, stretch=-1.0),
                                   dict(dim=2, scaling="base", stretch=2.0), dict(dim=8, scaling="ramp", slow=4.0, fast=4.0),
                                   dict(dim=8, scaling="other"), dict(dim=8, base=math.inf), dict(dim=8, stretch=math.nan)])
 def test_frequencies_refuse(args):
     with pytest.raises(ValueError):
         kv.rotary_frequencies(**args)
+
+
+@pytest.mark.parametrize("args", [dict(slow=2.0, fast=2.0), dict(slow=0.0), dict(slow=-1.0), dict(base=1.0), dict(base=0.5),
+                                  dict(original_length=0), dict(original_length=math.nan), dict(fast=math.nan)])
+def test_frequencies_of_a_ramp_by_index_refuse(args):
+    with pytest.raises(ValueError):
+        kv.rotary_frequencies(64, scaling="index_ramp", stretch=8.0, **args)
 
 
 # ---------------------------------------------------------------------------
