@@ -42,14 +42,15 @@ __device__ __forceinline__ uint32_t max_magnitude2(uint32_t a, uint32_t b) {
 }
 
 // One block: 16 values of 16 bits -> 8 bytes of codes and the scale's byte.
-// x / s is taken as x * fl(1 / s), rounded to a multiple of 2^-14 by adding and
-// taking off 768 (the product of the first addition is exact): x has at most 11
+// x / s is taken as x * r, r = 1 / s to 2 ulp, rounded to a multiple of 2^-14 by adding
+// and taking off 768 (the product of the first addition is exact): x has at most 11
 // bits, s 4 and a border between two codes 3, so x / s is either a border exactly,
-// which the product is within 2^-21 of and that rounding makes exact again, or at
-// least 2^-13 away from it (borders lie at 2^-2 and above), which neither can
-// bridge.  The conversion then decides every code as the quotient itself would.
-// amax / 6 becomes the scale in the same way: amax * fl(1 / 6) is rounded to 16
-// significant bits, and then decides as the quotient would.  A NaN and an infinity saturates; neither counts for amax, and `odd` is set.
+// which the product is within 2^-19 of (borders are 5 at most, r is within 2^-22 of
+// itself) and that rounding makes exact again, or at least 2^-13 away from it (borders
+// lie at 2^-2 and above), which neither can bridge.  The conversion then decides every
+// code as the quotient itself would.  amax / 6 becomes the scale in the same way: amax *
+// fl(1 / 6) is rounded to 16 significant bits, and then decides as the quotient would.
+// A NaN counts as 0 and an infinity saturates; neither counts for amax, and `odd` is set.
 template <bool F16>
 __device__ __forceinline__ uint2 quantize16(const uint4& a, const uint4& b, uint32_t& scale, bool& odd) {
   float x[16];

@@ -52,9 +52,10 @@ namespace {
 // What is left is instructions: 18 a key and warp, of which the conversions and their
 // scales are 8, at 2.4 a clock and SM, half of what the ALU pipe gives (two blocks of
 // seven warps a SM; with six 268 us; joining in place, for a ring of 12 pages in place
-// of 9, 250 against 244; codes of V loaded behind the softmax 243 against 240).  2 x
-// 204800 tokens cut over 304 blocks 88 us with the joining kernel, 333 tokens of one
-// session 5.7 us.  D = 64, the same sessions: 150 us, 4.4 TB/s (214 before the copies'
+// of the 9 that it had then, 250 against 244, and of its 8 now, between whose outputs lie
+// four floats, a ninth changes nothing; codes of V loaded behind the softmax 243 against
+// 240).  2 x 204800 tokens cut over 304 blocks 88 us with the joining kernel, 333 tokens of
+// one session 5.7 us.  D = 64, the same sessions: 150 us, 4.4 TB/s (214 before the copies'
 // operands were uniform).  Taller items have an SM's registers for one block: drafts of 35 rows
 // (D = 64, f16, 24 requests with a window of 4096) 29 us, where the prompt kernel took
 // 66; a third of that is the fixed part of the call.
@@ -97,6 +98,7 @@ struct FewSmall {
   Gqa8Item items[4];
 };
 static_assert(sizeof(FewSmall) <= 2048, "FewSmall");
+static_assert(FewCfg<128, 8>::kStages == 8, "the ring that the decode step's figures are of");
 
 // This block's items.  Of 32 requests or fewer one warp adds up the work, and walks
 // what it has in registers; of more the block has added it up (sm_total).  I: int where

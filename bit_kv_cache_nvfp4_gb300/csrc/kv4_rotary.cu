@@ -10,7 +10,8 @@
 // it is rounded, in turns and in integers: F = inv_freq / 2 pi as a 64-bit
 // fraction of a turn (to 2^-63 for frequencies up to 1), and position *
 // F modulo 2^64 drops the whole turns by itself.  Its top 32 bits are the angle in
-// units of pi / 2^31, good to 2^-32 of a turn, for sincospi.
+// units of pi / 2^31, good to 2^-32 of a turn at positions up to 2^31 (to 2^-29 at
+// frequencies of 4), which fp32 rounds for sincospi: off by 2^-26 of a turn at most.
 //
 // Bound by HBM in large calls: 16381 tokens of 40 heads of 128, 336 MB, in 60 us whole and
 // 61 with a quarter of each head copied, 5.5 TB/s, where a copy of the same tensors takes
