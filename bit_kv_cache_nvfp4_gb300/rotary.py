@@ -81,8 +81,8 @@ def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str | None = No
         keep = ((original_length * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
         f = f * (keep + (1 - keep) / stretch)
     elif scaling == "index_ramp":
-        if not (fast > slow > 0 and base > 1 and original_length > 0):
-            raise ValueError("fast must be above slow, slow and original_length above 0, base above 1")
+        if not (math.inf > fast > slow > 0 and base > 1 and math.inf > original_length > 0):
+            raise ValueError("fast must be above slow, slow and original_length above 0, base above 1, all finite")
         # base^(-2 at / dim) * original_length = 2 pi turns
         low, high = (dim * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base)) for turns in (fast, slow))
         low, high = max(math.floor(low), 0), min(math.ceil(high), dim - 1)

@@ -163,7 +163,8 @@ def test_frequencies_refuse(args):
 
 
 @pytest.mark.parametrize("args", [dict(slow=2.0, fast=2.0), dict(slow=0.0), dict(slow=-1.0), dict(base=1.0), dict(base=0.5),
-                                  dict(original_length=0), dict(original_length=math.nan), dict(fast=math.nan)])
+                                  dict(original_length=0), dict(original_length=math.nan), dict(original_length=math.inf),
+                                  dict(fast=math.nan), dict(fast=math.inf)])
 def test_frequencies_of_a_ramp_by_index_refuse(args):
     with pytest.raises(ValueError):
         kv.rotary_frequencies(64, scaling="index_ramp", stretch=8.0, **args)
